@@ -31,6 +31,7 @@
  *   - Supported head counts: 16 and 32 (one CTA per SM) and 48..128 in steps
  *     of 16 (a two-CTA cluster per worker); both work in 64-token tiles.
  *     kv_lora_rank is 512 and qk_rope_head_dim is 64; nothing else is built.
+ *     (The prompt side, further down, takes any head count.)
  *   - The natural log is used for every LSE.
  */
 #ifndef MLA_DECODE_H_
@@ -477,6 +478,176 @@ int mla_decode_run_fp8(const int32_t* plan_host, const int32_t* plan_dev, const 
  * batch < 0, num_slots < 1 or a bad kv_scale; nothing is launched then. */
 int mla_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slots, const void* rows, int32_t batch,
                       float kv_scale, void* workspace, void* stream);
+
+/* ---- the prompt side ------------------------------------------------------
+ * What stands before the decode: rotary positions, a row's way into the cache,
+ * and a prompt's attention in the EXPANDED form (per-head keys and values made
+ * from the latents), which takes 192 + 128 multiply-adds a head and pair
+ * instead of the absorbed form's 576 + 512 ("MLA and torch.compile: v0.3's two
+ * sources", section "MLA: starting from a 439-line commit": prefill takes the
+ * ordinary path, decode the absorbing one).  All activations and weights are
+ * bf16; strides are in elements, non-negative multiples of 8. */
+
+/* mla_rope_frequencies -- host only.  The rotary frequencies of the 64-wide
+ * part, as the 64-bit fractions of a turn per position that the calls below
+ * take: freqs[i] = 2^64 f_i / (2 pi), i = 0..31, with inv_i = theta^(-i/32) and
+ *   scaling 0 (none)    f_i = inv_i
+ *   scaling 1 (linear)  f_i = inv_i / factor
+ *   scaling 2 (YaRN)    f_i = inv_i ((1 - r_i) + r_i / factor),
+ *                       r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *                       lo = max(floor(p(beta_fast)), 0),
+ *                       hi = min(ceil(p(beta_slow)), 63),
+ *                       p(beta) = 32 ln(original_positions / (2 pi beta)) / ln theta
+ *   theta               finite, > 1;  factor finite, >= 1 (scaling 1 and 2);
+ *                       original_positions >= 1, beta_fast >= beta_slow > 0,
+ *                       beta_fast finite (scaling 2).  Unused values are not
+ *                       looked at.
+ *   freqs               host uint64[32], written.
+ * The position times freqs[i] modulo 2^64 is the angle as a fraction of a
+ * turn, exactly: no position loses precision.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (another scaling). */
+int mla_rope_frequencies(double theta, int32_t scaling, double factor, int32_t original_positions, double beta_fast,
+                         double beta_slow, uint64_t* freqs);
+
+/* mla_rope_query -- asynchronous on `stream`.
+ *
+ * Rotates the rotary part of every head's query by its token's position:
+ * with x = the last 64 of the head's nope_dim + 64 values,
+ *   (x0, x1) -> amplitude (x0 cos - x1 sin, x1 cos + x0 sin)
+ * over pairs (2i, 2i + 1) (interleaved 1) or (i, i + 32) (interleaved 0), in
+ * fp32 with one rounding.
+ *   q          device bf16: head h of token t at q + t*q_token_stride +
+ *              h*q_head_stride, nope_dim values and then the 64 rotary ones.
+ *   positions  device int32 [tokens]; any value (a negative one turns back).
+ *   nope_dim   a multiple of 8 (0 .. 65536).
+ *   freqs      host uint64[32] from mla_rope_frequencies (read now; a captured
+ *              graph keeps them).   amplitude  finite factor on cos and sin
+ *              (1, or YaRN's ratio of attention scalings).
+ *   q_rope     device bf16, written: (t, h) at q_rope + t*rope_token_stride +
+ *              h*rope_head_stride.  [tokens, heads, 64] dense is what
+ *              mla_decode_run takes; q + nope_dim with q's strides rotates in
+ *              place.  Any other overlap with q is not allowed.
+ *   q_nope     NULL, or device bf16 [tokens, heads, nope_dim] dense: the rest
+ *              of each head is copied there (what mla_absorb_query takes).
+ * Errors: MLA_ERR_INVALID_ARG for null or non-16-byte-aligned pointers
+ * (positions: 4), tokens < 0, num_heads < 1, bad strides (q_rope's rows
+ * overlapping included); MLA_ERR_UNSUPPORTED for another nope_dim or more than
+ * 2^31 - 1 blocks of work.  Nothing is launched then, nor for tokens == 0. */
+int mla_rope_query(const void* q, int64_t q_token_stride, int64_t q_head_stride, const int32_t* positions,
+                   int32_t tokens, int32_t num_heads, int32_t nope_dim, const uint64_t* freqs, float amplitude,
+                   int32_t interleaved, void* q_rope, int64_t rope_token_stride, int64_t rope_head_stride,
+                   void* q_nope, void* stream);
+
+/* mla_rope_append_kv -- asynchronous on `stream`.
+ *
+ * mla_append_kv for rows as the projection leaves them: the latent is
+ * normalised (y = x / sqrt(mean x^2 + eps) * norm_weight over its 512 values;
+ * norm_weight NULL: unchanged), the rope key rotated as in mla_rope_query, and
+ * the row written to its slot; fp32 arithmetic, one rounding.
+ *   kv_cache     device bf16 [num_slots, 576], written in place.
+ *   slots        device int32 [tokens], distinct (two rows to one slot: any
+ *                part of either may win).
+ *   rows         device bf16, token t at rows + t*row_stride: 512 latent
+ *                values, then 64 of the rope key; row_stride >= 576 (not
+ *                looked at for one token).
+ *   norm_weight  device bf16 [512] or NULL;  eps finite, >= 0.
+ *   workspace    NULL, or a decode workspace: a slot outside [0, num_slots) is
+ *                skipped and recorded there as MLA_ERR_INDEX_OOB.
+ *   positions, freqs, amplitude, interleaved: as for mla_rope_query.
+ * Errors: MLA_ERR_INVALID_ARG for bad pointers (rows, cache, weight and
+ * workspace 16-byte aligned; slots and positions 4), sizes, strides or scalars;
+ * nothing is launched then, nor for tokens == 0. */
+int mla_rope_append_kv(void* kv_cache, int64_t num_slots, const int32_t* slots, const void* rows, int64_t row_stride,
+                       const int32_t* positions, int32_t tokens, const void* norm_weight, float eps,
+                       const uint64_t* freqs, float amplitude, int32_t interleaved, void* workspace, void* stream);
+
+/* mla_rope_append_kv_fp8 -- the same into an FP8 cache (uint8 [num_slots, 576]
+ * E4M3 codes): the fp32 values are divided by kv_scale (finite, > 0) and
+ * rounded once, as in mla_append_kv_fp8. */
+int mla_rope_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slots, const void* rows,
+                           int64_t row_stride, const int32_t* positions, int32_t tokens, const void* norm_weight,
+                           float eps, const uint64_t* freqs, float amplitude, int32_t interleaved, float kv_scale,
+                           void* workspace, void* stream);
+
+/* mla_expand_kv -- asynchronous on `stream`.
+ *
+ * Per-head keys and values of cached rows: with c_t = the latent of row
+ * kv_indices[t],
+ *   k_nope[t, h, n] = sum_r c_t[r] w_kc[h, n, r]      (fp32 sums, bf16 result)
+ *   v[t, h, n]      = sum_r c_t[r] w_vc[h, r, n]
+ *   k_rope[t, :]    = the row's rope key (shared by all heads, copied)
+ * -- what mla_prefill_run takes.  The weights are those of mla_absorb_query
+ * and mla_project_output.
+ *   kv_cache    device bf16 [num_slots, 576].
+ *   kv_indices  device int32 [tokens]; repeats are allowed.  An index outside
+ *               [0, num_slots) reads row 0 and records MLA_ERR_INDEX_OOB in the
+ *               workspace status, when there is one.
+ *   w_kc        device bf16 [num_heads, 128, 512];  w_vc  [num_heads, 512, 128].
+ *   k_nope, v   device bf16 [tokens, num_heads, 128];  k_rope  [tokens, 64].
+ *   workspace   NULL, or a decode workspace (its status word).
+ * Errors: MLA_ERR_INVALID_ARG for null or misaligned pointers (16 bytes;
+ * kv_indices 4), tokens < 0, num_heads < 1, num_slots < 1; nothing is launched
+ * then, nor for tokens == 0. */
+int mla_expand_kv(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, int32_t tokens,
+                  const void* w_kc, const void* w_vc, int32_t num_heads, void* k_nope, void* k_rope, void* v,
+                  void* workspace, void* stream);
+
+/* mla_expand_kv_fp8 -- the same from an FP8 cache: a value is its E4M3 code
+ * times kv_scale (finite, > 0), applied to the fp32 sums. */
+int mla_expand_kv_fp8(const void* kv_cache, int64_t num_slots, float kv_scale, const int32_t* kv_indices,
+                      int32_t tokens, const void* w_kc, const void* w_vc, int32_t num_heads, void* k_nope,
+                      void* k_rope, void* v, void* workspace, void* stream);
+
+/* mla_prefill_plan -- host only, no device work, deterministic.
+ *
+ * The work plan of one batch of the expanded attention: tiles of query rows,
+ * heaviest first, and, where few rows meet long keys, the cut of their keys
+ * into pieces that mla_prefill_run joins.
+ *   q_indptr, kv_indptr  host int32 [batch + 1], each from 0, non-decreasing:
+ *              request b's queries are rows q_indptr[b] .. q_indptr[b+1] and
+ *              its keys kv_indptr[b] .. kv_indptr[b+1] of the packed arrays.
+ *   causal     1: with L_q queries and L_k keys, query i sees keys
+ *              j <= i + L_k - L_q (the ends aligned: a chunk that continues a
+ *              cached context; with L_k < L_q the first rows see nothing);
+ *              0: every key of its request.
+ *   num_sms, plan, plan_words, plan_words_needed, workspace_bytes: as for
+ *   mla_decode_plan.
+ * Errors: those of mla_decode_plan; any num_heads of 1 .. 65535 is supported;
+ * MLA_ERR_UNSUPPORTED for 2^30 - 1 or more queries or keys. */
+int mla_prefill_plan(const int32_t* q_indptr, const int32_t* kv_indptr, int32_t batch, int32_t num_heads,
+                     int32_t causal, int32_t num_sms, int32_t* plan, size_t plan_words, size_t* plan_words_needed,
+                     size_t* workspace_bytes);
+
+/* mla_prefill_run -- asynchronous on `stream`.
+ *
+ *   s_ij = sm_scale (q_i . [k_nope_j, k_rope_j]);   lse_i = ln sum_j exp(s_ij);
+ *   out_i = sum_j softmax(s_i)_j v_j                 over the keys row i sees.
+ * A row that sees no key gets out = 0 and lse = -inf.  Values of keys that a
+ * row does not see never reach it, whatever they are.
+ *   plan_host, plan_dev  the words of mla_prefill_plan, on both sides
+ *              (plan_dev 16-byte aligned).
+ *   q          device bf16: head h of row i at q + i*q_token_stride +
+ *              h*q_head_stride, 128 values and then the 64 rotary ones.
+ *   k_nope, v  device bf16, 128 values of (row, head) each, with strides (the
+ *              halves of one [rows, heads, 256] projection will do).
+ *   k_rope     device bf16, 64 values of a row, shared by the heads.
+ *              k_nope, k_rope and v are not looked at when there are no keys.
+ *   Strides are at least the width of what lies there (192, 128, 64), where
+ *   there is more than one row or head, and below 2^38.
+ *   out        device bf16 [q rows, heads, 128] dense; the weights of the
+ *              values are rounded to bf16, sums are fp32.
+ *   lse        device fp32 [q rows, heads] or NULL.
+ *   workspace  device, at least the plan's workspace_bytes, 16-byte aligned,
+ *              zero-filled before first use (status word as for mla_decode_run;
+ *              calls sharing one must not overlap on the GPU).
+ * Safe to capture in a CUDA graph.  Errors as for mla_decode_run; with no
+ * query row nothing is launched.  A plan_dev that does not lie inside the
+ * arrays of plan_host is skipped item by item with MLA_ERR_PLAN_MISMATCH. */
+int mla_prefill_run(const int32_t* plan_host, const int32_t* plan_dev, const void* q, int64_t q_token_stride,
+                    int64_t q_head_stride, const void* k_nope, int64_t k_token_stride, int64_t k_head_stride,
+                    const void* k_rope, int64_t k_rope_stride, const void* v, int64_t v_token_stride,
+                    int64_t v_head_stride, float sm_scale, void* out, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream);
 
 /* mla_check_errors -- synchronises `stream`, reads the workspace status word,
  * clears it, and returns it (MLA_OK when the kernels found nothing wrong), or

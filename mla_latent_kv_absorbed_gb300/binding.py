@@ -28,7 +28,8 @@ EXPORTS = ("mla_status_string", "mla_abi_version", "mla_decode_plan", "mla_decod
            "mla_append_kv", "mla_step_staging_bytes", "mla_decode_step_host", "mla_decode_run_multi_query",
            "mla_merge_two_states", "mla_decode_fp8_workspace_bytes", "mla_decode_run_fp8", "mla_append_kv_fp8",
            "mla_decode_graph_sizes", "mla_decode_run_graph", "mla_noalloc_check_errors", "mla_decode_run_tree",
-           "mla_probe_wait_limit")
+           "mla_probe_wait_limit", "mla_rope_frequencies", "mla_rope_query", "mla_rope_append_kv",
+           "mla_rope_append_kv_fp8", "mla_expand_kv", "mla_expand_kv_fp8", "mla_prefill_plan", "mla_prefill_run")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 if not os.path.exists(LIB_PATH):
@@ -98,6 +99,25 @@ _lib.mla_decode_run_graph.argtypes = [_vp, ctypes.c_size_t, ctypes.c_int32, ctyp
 _lib.mla_project_output.restype = ctypes.c_int
 _lib.mla_project_output.argtypes = [_vp, _vp, _vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                     _vp, _vp]
+_i32, _i64, _f32, _f64, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
+_lib.mla_rope_frequencies.restype = ctypes.c_int
+_lib.mla_rope_frequencies.argtypes = [_f64, _i32, _f64, _i32, _f64, _f64, _vp]
+_lib.mla_rope_query.restype = ctypes.c_int
+_lib.mla_rope_query.argtypes = [_vp, _i64, _i64, _vp, _i32, _i32, _i32, _vp, _f32, _i32, _vp, _i64, _i64, _vp, _vp]
+_lib.mla_rope_append_kv.restype = ctypes.c_int
+_lib.mla_rope_append_kv.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _f32, _vp, _f32, _i32, _vp, _vp]
+_lib.mla_rope_append_kv_fp8.restype = ctypes.c_int
+_lib.mla_rope_append_kv_fp8.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _f32, _vp, _f32, _i32, _f32, _vp,
+                                        _vp]
+_lib.mla_expand_kv.restype = ctypes.c_int
+_lib.mla_expand_kv.argtypes = [_vp, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp]
+_lib.mla_expand_kv_fp8.restype = ctypes.c_int
+_lib.mla_expand_kv_fp8.argtypes = [_vp, _i64, _f32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp]
+_lib.mla_prefill_plan.restype = ctypes.c_int
+_lib.mla_prefill_plan.argtypes = [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _sz, _c_szp, _c_szp]
+_lib.mla_prefill_run.restype = ctypes.c_int
+_lib.mla_prefill_run.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _f32, _vp,
+                                 _vp, _vp, _sz, _vp]
 
 
 class MLAError(RuntimeError):
@@ -405,6 +425,212 @@ def decode_step_host(q_nope, q_rope, kv_indptr, kv_indices, kv_cache, sm_scale, 
         raise MLAError(st, "mla_decode_step_host")
 
 
+# ---- the prompt side: rotary positions, latent expansion, expanded attention ----
+
+def _need(where, name, t, dtype, shape, dense=True) -> None:
+    """The ABI passes no lengths and no types: a tensor of another type, shape (None: any size), layout or
+    device is refused here, before any launch.  dense: contiguous; else only the last dimension is."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{where}: {name} is {t.dtype}, {dtype} is wanted")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, {tuple('*' if w is None else w for w in shape)} "
+                         "is wanted")
+    if t.numel() and not (t.is_contiguous() if dense else (t.stride(-1) == 1 or t.shape[-1] == 1)):
+        raise ValueError(f"{where}: {name} is not laid out {'densely' if dense else 'with its last dimension together'}")
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} is not on a CUDA device")
+
+
+def _one_device(where, *tensors) -> None:
+    """Every tensor on the current device: the launch goes there."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"{where}: a tensor is on cuda:{t.get_device()}, the current device is cuda:{cur}")
+
+
+_ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
+
+
+def rope_frequencies(theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_positions: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0) -> np.ndarray:
+    """Rotary frequencies of the 64-wide part as 64-bit fractions of a turn per position: uint64 numpy [32].
+    scaling: "none", "linear" (positions interpolated by factor) or "yarn"."""
+    freqs = np.zeros(32, dtype=np.uint64)
+    if scaling not in _ROPE_SCALING:
+        raise MLAError(2, f"mla_rope_frequencies: scaling {scaling!r}")
+    st = _lib.mla_rope_frequencies(float(theta), _ROPE_SCALING[scaling], float(factor), int(original_positions),
+                                   float(beta_fast), float(beta_slow), freqs.ctypes.data)
+    if st != MLA_OK:
+        raise MLAError(st, "mla_rope_frequencies")
+    return freqs
+
+
+def _freqs_ptr(where, freqs):
+    if not isinstance(freqs, np.ndarray) or freqs.dtype != np.uint64 or freqs.shape != (32,) or \
+            not freqs.flags.c_contiguous:
+        raise ValueError(f"{where}: freqs is the uint64 array of rope_frequencies")
+    return freqs.ctypes.data
+
+
+def rope_query(q, positions, freqs, q_rope, q_nope=None, amplitude: float = 1.0, interleaved: bool = True,
+               stream=None) -> None:
+    """Rotate the last 64 values of every head: q bf16 [T, H, nope + 64] (any strides that are multiples of 8),
+    positions int32 [T] -> q_rope bf16 [T, H, 64] (a dense tensor, or q[..., nope:] itself to rotate in place);
+    q_nope: optional dense bf16 [T, H, nope] that receives the rest of each head."""
+    import torch
+    w = "mla_rope_query"
+    T, H, D = q.shape if q.dim() == 3 else (-1, -1, -1)
+    nope = D - 64
+    _need(w, "q", q, torch.bfloat16, (None, None, None), dense=False)
+    if nope < 0:
+        raise ValueError(f"{w}: q has {D} values a head, at least the 64 rotary ones are wanted")
+    _need(w, "positions", positions, torch.int32, (T,))
+    _need(w, "q_rope", q_rope, torch.bfloat16, (T, H, 64), dense=False)
+    if q_nope is not None:
+        _need(w, "q_nope", q_nope, torch.bfloat16, (T, H, nope))
+    _one_device(w, q, positions, q_rope, q_nope)
+    if T == 0 or H == 0:
+        return
+    st = _lib.mla_rope_query(q.data_ptr(), q.stride(0), q.stride(1), positions.data_ptr(), T, H, nope,
+                             _freqs_ptr(w, freqs), float(amplitude), int(bool(interleaved)), q_rope.data_ptr(),
+                             q_rope.stride(0), q_rope.stride(1), _ptr(q_nope), _stream_handle(stream))
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
+def _rope_append(w, cache_dtype, kv_cache, slots, rows, positions, freqs, norm_weight, workspace):
+    import torch
+    T = rows.shape[0] if rows.dim() == 2 else -1
+    _need(w, "kv_cache", kv_cache, cache_dtype, (None, 576))
+    _need(w, "rows", rows, torch.bfloat16, (None, 576), dense=False)
+    _need(w, "slots", slots, torch.int32, (T,))
+    _need(w, "positions", positions, torch.int32, (T,))
+    if norm_weight is not None:
+        _need(w, "norm_weight", norm_weight, torch.bfloat16, (512,))
+    _one_device(w, kv_cache, rows, slots, positions, norm_weight, workspace)
+    return T, _freqs_ptr(w, freqs)
+
+
+def rope_append_kv(kv_cache, slots, rows, positions, freqs, norm_weight=None, eps: float = 1e-6,
+                   amplitude: float = 1.0, interleaved: bool = True, workspace=None, stream=None) -> None:
+    """kv_cache[slots[t]] = [rms_norm(rows[t, :512]) * norm_weight, rotated rows[t, 512:]]: bf16 [num_slots, 576]
+    <- bf16 [T, 576] (rows may be a slice of a wider projection); norm_weight bf16 [512] or None (no norm)."""
+    import torch
+    w = "mla_rope_append_kv"
+    T, fr = _rope_append(w, torch.bfloat16, kv_cache, slots, rows, positions, freqs, norm_weight, workspace)
+    st = _lib.mla_rope_append_kv(kv_cache.data_ptr(), kv_cache.shape[0], slots.data_ptr(), rows.data_ptr(),
+                                 rows.stride(0), positions.data_ptr(), T, _ptr(norm_weight), float(eps), fr,
+                                 float(amplitude), int(bool(interleaved)), _ptr(workspace), _stream_handle(stream))
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
+def rope_append_kv_fp8(kv_cache, slots, rows, positions, freqs, kv_scale, norm_weight=None, eps: float = 1e-6,
+                       amplitude: float = 1.0, interleaved: bool = True, workspace=None, stream=None) -> None:
+    """rope_append_kv into an FP8 cache: uint8 [num_slots, 576] E4M3 codes of the values / kv_scale."""
+    import torch
+    w = "mla_rope_append_kv_fp8"
+    T, fr = _rope_append(w, torch.uint8, kv_cache, slots, rows, positions, freqs, norm_weight, workspace)
+    st = _lib.mla_rope_append_kv_fp8(kv_cache.data_ptr(), kv_cache.shape[0], slots.data_ptr(), rows.data_ptr(),
+                                     rows.stride(0), positions.data_ptr(), T, _ptr(norm_weight), float(eps), fr,
+                                     float(amplitude), int(bool(interleaved)), float(kv_scale), _ptr(workspace),
+                                     _stream_handle(stream))
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
+def _expand(w, cache_dtype, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace):
+    import torch
+    T = kv_indices.shape[0] if kv_indices.dim() == 1 else -1
+    H = w_kc.shape[0] if w_kc.dim() == 3 else -1
+    bf = torch.bfloat16
+    _need(w, "kv_cache", kv_cache, cache_dtype, (None, 576))
+    _need(w, "kv_indices", kv_indices, torch.int32, (None,))
+    _need(w, "w_kc", w_kc, bf, (None, 128, 512))
+    _need(w, "w_vc", w_vc, bf, (H, 512, 128))
+    _need(w, "k_nope", k_nope, bf, (T, H, 128))
+    _need(w, "k_rope", k_rope, bf, (T, 64))
+    _need(w, "v", v, bf, (T, H, 128))
+    _one_device(w, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace)
+    return T, H
+
+
+def expand_kv(kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace=None, stream=None) -> None:
+    """Per-head keys and values of the cached rows kv_indices int32 [T]: k_nope[t,h,:] = c_t . w_kc[h]^T and
+    v[t,h,:] = c_t . w_vc[h] (bf16 [T,H,128]), k_rope[t,:] the rows' rope keys (bf16 [T,64])."""
+    import torch
+    T, H = _expand("mla_expand_kv", torch.bfloat16, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace)
+    st = _lib.mla_expand_kv(kv_cache.data_ptr(), kv_cache.shape[0], kv_indices.data_ptr(), T, w_kc.data_ptr(),
+                            w_vc.data_ptr(), H, k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), _ptr(workspace),
+                            _stream_handle(stream))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_expand_kv")
+
+
+def expand_kv_fp8(kv_cache, kv_scale, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace=None,
+                  stream=None) -> None:
+    """expand_kv from an FP8 cache: uint8 [num_slots, 576] E4M3 codes (value = code x kv_scale)."""
+    import torch
+    w = "mla_expand_kv_fp8"
+    T, H = _expand(w, torch.uint8, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace)
+    st = _lib.mla_expand_kv_fp8(kv_cache.data_ptr(), kv_cache.shape[0], float(kv_scale), kv_indices.data_ptr(), T,
+                                w_kc.data_ptr(), w_vc.data_ptr(), H, k_nope.data_ptr(), k_rope.data_ptr(),
+                                v.data_ptr(), _ptr(workspace), _stream_handle(stream))
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
+def prefill_plan(q_indptr_host, kv_indptr_host, num_heads: int, causal: bool = True, num_sms: int = 0):
+    """Host plan of the expanded attention.  Returns (plan words as int32 numpy array, workspace bytes)."""
+    qp = np.ascontiguousarray(np.asarray(q_indptr_host), dtype=np.int32)
+    kp = np.ascontiguousarray(np.asarray(kv_indptr_host), dtype=np.int32)
+    if qp.ndim != 1 or qp.shape != kp.shape or qp.shape[0] < 1:
+        raise ValueError("mla_prefill_plan: q_indptr and kv_indptr must both hold batch + 1 entries")
+    need, ws = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    plan = np.zeros(0, dtype=np.int32)
+    for _ in range(2):                               # the sizes, then the words
+        st = _lib.mla_prefill_plan(qp.ctypes.data, kp.ctypes.data, qp.shape[0] - 1, int(num_heads), int(bool(causal)),
+                                   int(num_sms), plan.ctypes.data if plan.size else None, plan.size,
+                                   ctypes.byref(need), ctypes.byref(ws))
+        if st != MLA_OK:
+            raise MLAError(st, "mla_prefill_plan")
+        if not plan.size:
+            plan = np.zeros(need.value, dtype=np.int32)
+    return plan, int(ws.value)
+
+
+_P_HEADS, _P_Q, _P_KV = 3, 5, 6                      # prefill plan header words
+
+
+def prefill_run(plan_host, plan_dev, q, k_nope, k_rope, v, sm_scale: float, out, lse, workspace, stream=None) -> None:
+    """Attention over expanded keys: q bf16 [Tq,H,192], k_nope and v bf16 [Tk,H,128], k_rope bf16 [Tk,64] (strides
+    that are multiples of 8), out bf16 [Tq,H,128], lse fp32 [Tq,H] or None, workspace uint8 (zero-filled once)."""
+    import torch
+    w, bf = "mla_prefill_run", torch.bfloat16
+    if not isinstance(plan_host, np.ndarray) or plan_host.dtype != np.int32 or plan_host.shape[0] < 16:
+        raise ValueError(f"{w}: plan_host is the int32 array of prefill_plan")
+    H, nq, nk = int(plan_host[_P_HEADS]), int(plan_host[_P_Q]), int(plan_host[_P_KV])
+    _need(w, "plan_dev", plan_dev, torch.int32, (plan_host.shape[0],))
+    _need(w, "q", q, bf, (nq, H, 192), dense=False)
+    _need(w, "k_nope", k_nope, bf, (nk, H, 128), dense=False)
+    _need(w, "k_rope", k_rope, bf, (nk, 64), dense=False)
+    _need(w, "v", v, bf, (nk, H, 128), dense=False)
+    _need(w, "out", out, bf, (nq, H, 128))
+    if lse is not None:
+        _need(w, "lse", lse, torch.float32, (nq, H))
+    _need(w, "workspace", workspace, torch.uint8, (None,))
+    _one_device(w, plan_dev, q, k_nope, k_rope, v, out, lse, workspace)
+    st = _lib.mla_prefill_run(plan_host.ctypes.data, plan_dev.data_ptr(), q.data_ptr(), q.stride(0), q.stride(1),
+                              k_nope.data_ptr(), k_nope.stride(0), k_nope.stride(1), k_rope.data_ptr(),
+                              k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1), float(sm_scale),
+                              out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
+                              _stream_handle(stream))
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
 def check_errors(workspace, stream=None) -> int:
     """Synchronise, read and clear the device status; returns the status code."""
     return int(_lib.mla_check_errors(_ptr(workspace), _stream_handle(stream)))
@@ -448,6 +674,23 @@ class Decoder:
     @property
     def has_merge(self) -> bool:
         return int(self.plan_host[10]) > 0
+
+    def check(self, stream=None) -> int:
+        return check_errors(self.workspace, stream)
+
+
+class Prefiller:
+    """Convenience holder: plan a batch's prompt attention once, then run it on device tensors."""
+
+    def __init__(self, q_indptr_host, kv_indptr_host, num_heads: int, causal: bool = True, device="cuda",
+                 num_sms: int = 0):
+        import torch
+        self.plan_host, self.workspace_bytes = prefill_plan(q_indptr_host, kv_indptr_host, num_heads, causal, num_sms)
+        self.plan_dev = torch.from_numpy(self.plan_host).to(device)
+        self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=device)
+
+    def run(self, q, k_nope, k_rope, v, sm_scale, out, lse=None, stream=None):
+        prefill_run(self.plan_host, self.plan_dev, q, k_nope, k_rope, v, sm_scale, out, lse, self.workspace, stream)
 
     def check(self, stream=None) -> int:
         return check_errors(self.workspace, stream)

@@ -1,0 +1,170 @@
+// Host plan of the expanded attention: which query rows and keys one work item
+// of the kernel takes, and in what order items are launched.
+//
+//   * an item is up to 256 query rows of one request (two tiles of 128) and
+//     the keys they see, for every head; causal items end at the last key of
+//     their last row, so no tile without a visible key is visited;
+//   * items are launched heaviest first (blocks start in launch order as SMs
+//     fall free, so the short ones fill the end), for a group of heads at a
+//     time: the group's keys and values stay in L2 while all its rows pass;
+//   * where whole items would leave SMs idle (few rows over long keys), an
+//     item's keys are cut into pieces of whole tiles whose partial outputs a
+//     second kernel joins.  The cut is the one, among a few equal shares of
+//     the mean load, whose greedy schedule ends first.
+// The plan is deterministic: equal inputs give identical words.
+#include <algorithm>
+#include <cstdint>
+#include <functional>
+#include <queue>
+#include <vector>
+
+#include "mla_prompt.h"
+
+namespace mla {
+namespace {
+
+struct Tile {
+  int b, q0, nq, k0, nk, off;
+};
+struct Piece {
+  int tile, t0, n;           // key tiles [t0, t0 + n) of the tile
+  long long cost;
+};
+
+constexpr long long kItemCost = 30;      // an item's prologue and epilogue, in tenths of a key tile
+constexpr long long kPieceCost = 15;     // a partial output written and read again
+constexpr long long kL2Bytes = 64ll << 20;
+
+inline int key_tiles(int nk) { return (nk + kPfKeys - 1) / kPfKeys; }
+// A key tile against two row tiles costs 10, against one 7.
+inline long long tile_cost(int nq) { return nq > kPfRows / 2 ? 10 : 7; }
+
+void cut(const std::vector<Tile>& tiles, long long cap, std::vector<Piece>& pieces) {
+  pieces.clear();
+  for (size_t i = 0; i < tiles.size(); ++i) {
+    const int nt = key_tiles(tiles[i].nk);
+    const long long c = tile_cost(tiles[i].nq);
+    int parts = 1;
+    if (cap > 0 && nt > 1) {
+      const long long most = std::max<long long>(4, cap / c);             // key tiles of a piece
+      parts = static_cast<int>((nt + most - 1) / most);
+    }
+    for (int k = 0; k < parts; ++k) {
+      const int a = static_cast<int>(static_cast<long long>(nt) * k / parts);
+      const int e = static_cast<int>(static_cast<long long>(nt) * (k + 1) / parts);
+      pieces.push_back({static_cast<int>(i), a, e - a, c * (e - a) + kItemCost + (parts > 1 ? kPieceCost : 0)});
+    }
+  }
+  std::stable_sort(pieces.begin(), pieces.end(), [](const Piece& x, const Piece& y) { return x.cost > y.cost; });
+}
+
+// End of the greedy schedule of the pieces, `heads` times each, on `sms`.
+long long makespan(const std::vector<Piece>& pieces, int heads, int sms) {
+  std::priority_queue<long long, std::vector<long long>, std::greater<long long>> free_at;
+  for (int i = 0; i < sms; ++i) free_at.push(0);
+  long long end = 0;
+  for (const Piece& p : pieces)
+    for (int h = 0; h < heads; ++h) {
+      const long long t = free_at.top() + p.cost;
+      free_at.pop();
+      free_at.push(t);
+      end = std::max(end, t);
+    }
+  return end;
+}
+
+}  // namespace
+
+int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int causal, int num_sms,
+                       std::vector<int32_t>& words) {
+  std::vector<Tile> tiles;
+  for (int b = 0; b < B; ++b) {
+    const int lq = qp[b + 1] - qp[b], lk = kp[b + 1] - kp[b];
+    for (int r = 0; r < lq; r += kPfRows) {
+      const int nq = std::min(kPfRows, lq - r);
+      // row r + i sees keys j <= r + i + lk - lq
+      const long long off = causal ? static_cast<long long>(r) + lk - lq : kPfNoLimit;
+      const long long seen = std::min<long long>(lk, std::max<long long>(0, off + nq));
+      tiles.push_back({b, qp[b] + r, nq, kp[b], static_cast<int>(seen), static_cast<int>(off)});
+    }
+  }
+  std::vector<Piece> best, trial;
+  cut(tiles, 0, best);
+  long long total = 0, most = 0;
+  for (const Piece& p : best) {
+    total += p.cost * H;
+    most = std::max(most, p.cost);
+  }
+  const long long mean = (total + num_sms - 1) / num_sms;
+  // the schedule of many items, none of them long, cannot be improved by cutting
+  if (!tiles.empty() && !(static_cast<long long>(best.size()) * H >= 8ll * num_sms && most <= mean / 2)) {
+    long long end = makespan(best, H, num_sms);
+    for (int share = 1; share <= 6; ++share) {
+      const long long cap = std::max<long long>(1, mean / share - kItemCost - kPieceCost);
+      cut(tiles, cap, trial);
+      if (trial.size() == tiles.size() || trial.size() > 65535) continue;
+      const long long e = makespan(trial, H, num_sms) + 2 * kItemCost;    // the joining kernel
+      if (e < end) {
+        end = e;
+        best.swap(trial);
+      }
+    }
+  }
+  // partial slots, in tile order, and the merge entries
+  std::vector<int> parts(tiles.size(), 0), first(tiles.size(), 0), next(tiles.size(), 0);
+  for (const Piece& p : best) ++parts[p.tile];
+  int partials = 0, merges = 0;
+  for (size_t i = 0; i < tiles.size(); ++i)
+    if (parts[i] > 1) {
+      first[i] = partials;
+      partials += parts[i];
+      ++merges;
+    }
+  const long long n_words = kPfHeaderWords + static_cast<long long>(kPfItemWords) * best.size() +
+                            static_cast<long long>(kPfMergeWords) * merges;
+  const long long blocks = static_cast<long long>(best.size()) * H;
+  if (n_words > 0x7FFFFFFFll || blocks > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
+  const long long per_head = std::max<long long>(1, static_cast<long long>(kp[B]) * 2 * kNope * 2);
+  long long group = std::max<long long>(kL2Bytes / per_head,
+                                        best.empty() ? 1 : (2ll * num_sms + best.size() - 1) / best.size());
+  group = std::min<long long>(H, std::max<long long>(1, group));
+  words.assign(static_cast<size_t>(n_words), 0);
+  words[kPMagic] = kPfMagic;
+  words[kPVersion] = kPfVersion;
+  words[kPBatch] = B;
+  words[kPHeads] = H;
+  words[kPCausal] = causal ? 1 : 0;
+  words[kPQTokens] = qp[B];
+  words[kPKvTokens] = kp[B];
+  words[kPItems] = static_cast<int32_t>(best.size());
+  words[kPPartials] = partials;
+  words[kPMerges] = merges;
+  words[kPHeadGroup] = static_cast<int32_t>(group);
+  words[kPTotalWords] = static_cast<int32_t>(n_words);
+  words[kPNumSms] = num_sms;
+  int32_t* w = words.data() + kPfHeaderWords;
+  for (const Piece& p : best) {
+    const Tile& t = tiles[p.tile];
+    const int k = p.t0 * kPfKeys;
+    const int nk = std::min(t.nk - k, p.n * kPfKeys);
+    w[0] = t.b;
+    w[1] = t.q0;
+    w[2] = t.nq;
+    w[3] = t.k0 + k;
+    w[4] = nk;
+    w[5] = causal ? t.off - k : kPfNoLimit;
+    w[6] = parts[p.tile] > 1 ? first[p.tile] + next[p.tile]++ : -1;
+    w += kPfItemWords;
+  }
+  for (size_t i = 0; i < tiles.size(); ++i)
+    if (parts[i] > 1) {
+      w[0] = tiles[i].q0;
+      w[1] = tiles[i].nq;
+      w[2] = first[i];
+      w[3] = first[i] + parts[i];
+      w += kPfMergeWords;
+    }
+  return MLA_OK;
+}
+
+}  // namespace mla
