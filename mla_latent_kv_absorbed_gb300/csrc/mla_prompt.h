@@ -102,12 +102,16 @@ struct PrefillParams {
   int* status;
   int n_items, n_merges, heads, head_group, partials;
   int q_tokens, kv_tokens;
-  float scale_log2;           // sm_scale * log2(e)
+  float scale_log2;           // |sm_scale| * log2(e), > 0
+  int negate;                 // sm_scale < 0: the scores are those of -q
 };
 
 int launch_rope_query(const RopeQueryParams& p, const RopeFreqs& f, cudaStream_t stream);
 int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, cudaStream_t stream);
 int launch_expand(const ExpandParams& p, bool fp8, cudaStream_t stream);
-int launch_prefill(const PrefillParams& p, cudaStream_t stream);
+// tm_q over q as [rows, heads, 192] (box 128 rows x 64), tm_k and tm_v over
+// [keys, heads, 128] (boxes of 128 and 64 keys x 64), tm_kr over [keys, 64].
+int launch_prefill(const PrefillParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_kr,
+                   const CUtensorMap& tm_v, cudaStream_t stream);
 
 }  // namespace mla

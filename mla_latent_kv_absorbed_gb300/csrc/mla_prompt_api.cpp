@@ -23,6 +23,45 @@ inline bool stride_ok(int64_t s, int64_t n = 1, int64_t width = 0) {
   return s >= 0 && s < (1ll << 38) && s % 8 == 0 && (n <= 1 || s >= width);
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<EncodeTiledFn>(p);
+    return nullptr;
+  }();
+  return fn;
+}
+
+// bf16 [rows, heads, width] with strides in elements (heads 0: [rows, width]),
+// boxes of `box_rows` rows of one head x 64 values, 128-byte swizzle; reads
+// past the last row give zeros.  The stride of a dimension of one is not used.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride,
+              int width, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t rs = static_cast<cuuint64_t>(rows > 1 ? row_stride : width) * 2;
+  const cuuint64_t hs = static_cast<cuuint64_t>(heads > 1 ? head_stride : width) * 2;
+  const int rank = heads > 0 ? 3 : 2;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {hs, rs};
+  cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)}, step[3] = {1, 1, 1};
+  if (rank == 2) {
+    dims[1] = dims[2];
+    strides[0] = rs;
+    box[1] = box[2];
+  }
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool rope_args(const uint64_t* freqs, float amplitude, int32_t interleaved, RopeFreqs* f) {
   if (!freqs || !std::isfinite(amplitude) || (interleaved != 0 && interleaved != 1)) return false;
   std::memcpy(f->f, freqs, sizeof f->f);
@@ -276,8 +315,21 @@ int mla_prefill_run(const int32_t* plan_host, const int32_t* plan_dev, const voi
   p.partials = plan_host[kPPartials];
   p.q_tokens = plan_host[kPQTokens];
   p.kv_tokens = plan_host[kPKvTokens];
-  p.scale_log2 = sm_scale * 1.4426950408889634f;
-  return launch_prefill(p, reinterpret_cast<cudaStream_t>(stream));
+  // the kernel takes maxima of the products before it scales them: a positive
+  // scale (0 becomes one that leaves every finite score at 0 in fp32)
+  p.scale_log2 = std::fmax(std::fabs(sm_scale) * 1.4426950408889634f, 1e-30f);
+  p.negate = sm_scale < 0.f;
+  if (!std::isfinite(p.scale_log2)) return MLA_ERR_INVALID_ARG;
+  CUtensorMap tm_q, tm_k, tm_kr, tm_v;
+  if (!make_map(&tm_q, q, nq, q_token_stride, H, q_head_stride, kQk, 128)) return MLA_ERR_CUDA;
+  if (nk == 0) {
+    tm_k = tm_kr = tm_v = tm_q;                 // nothing is loaded through them
+  } else if (!make_map(&tm_k, k_nope, nk, k_token_stride, H, k_head_stride, kNope, 128) ||
+             !make_map(&tm_kr, k_rope, nk, k_rope_stride, 0, 0, kRope, 128) ||
+             !make_map(&tm_v, v, nk, v_token_stride, H, v_head_stride, kNope, 64)) {
+    return MLA_ERR_CUDA;
+  }
+  return launch_prefill(p, tm_q, tm_k, tm_kr, tm_v, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

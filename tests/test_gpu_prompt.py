@@ -408,6 +408,19 @@ def test_prefill_of_peaked_scores(scale):
     assert np.abs(lse.cpu().numpy() - ref_lse).max() <= LSE_ATOL + off
 
 
+@pytest.mark.parametrize("sm", [-SM, 0.0, -0.5, 1e-20])
+def test_prefill_of_any_scale(sm):
+    # a negative scale turns the order of the scores around; zero weighs every key alike
+    torch, B = _t()
+    qp, kp = _indptr([150]), _indptr([200])
+    (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(6, 150, 200, 2)
+    ref, ref_lse, mag = P.prefill_attention(xq, xk, xr, xv, qp, kp, sm)
+    out, lse = _attend(B.Prefiller(qp, kp, 2), q, k, kr, v, sm=sm)
+    # 192 products at |sm| up to 0.5: at most 7 times the score error of SM's
+    _within(_f64(out), ref, _attention_bound(ref, mag) + 2.0 ** -8 * mag, "out")
+    assert np.abs(lse.cpu().numpy() - ref_lse).max() <= 4 * LSE_ATOL
+
+
 def test_prefill_strides():
     # q out of a wider projection; keys and values as the halves of one [T, H, 256] projection; heads outermost
     torch, B = _t()
