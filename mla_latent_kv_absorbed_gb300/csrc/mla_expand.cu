@@ -2,70 +2,351 @@
 // and values,
 //   k[t, h, n] = sum_r c_t[r] w_kc[h, n, r],   v[t, h, n] = sum_r c_t[r] w_vc[h, r, n],
 // and the rope key that all heads share.  c_t is the 512-wide latent of the
-// row (an FP8 row's code values times kv_scale); sums in fp32, one rounding.
+// row (an FP8 row's code values, kv_scale applied to the sums); fp32 sums, one
+// rounding.
+//
+// One matrix product [tokens, 512] x [512, 256 heads] whose left side is
+// gathered.  A CTA keeps the whole depth of 128 rows in shared memory (128
+// KB), so a row is gathered - and an FP8 row widened - once for all the column
+// tiles that the CTA walks, by plain loads of four warps, and only weights
+// stream.  A column tile is NT columns: the keys, or the values, of NT / 128
+// heads; w_kc is K-major as it lies, w_vc N-major.
+//   warp 0      TMA producer of the weights, 64-deep chunks in a ring
+//   warp 1      TMEM allocator, MMA issuer: M = 128, N = NT, two accumulators
+//   warps 4-7   epilogue: a TMEM lane is a row; 32-byte stores
+//   warps 8-11  rows: gather, swizzle (128-byte atoms), rope keys
+// Bound: the tensor core at many rows (512 MACs an output byte pair), the
+// weights' bytes at few.
 #include "mla_device.cuh"
+#include "mla_launch.h"
 #include "mla_prompt.h"
 
 namespace mla {
-namespace {
+namespace ex {
 
-constexpr int kTok = 16;       // rows of a block
+constexpr int kThreads = 384;
+constexpr int kEpiWarp0 = 4, kRowWarp0 = 8;
+constexpr int BM = 128, BK = 64, kChunks = kLatent / BK;
 
-__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+template <int NT_>
+struct Cfg {
+  static constexpr int NT = NT_;
+  static constexpr int kHeads = NT / kNope;                 // heads of a tile
+  static constexpr int kABytes = kChunks * BM * 128;        // 128 KB
+  static constexpr int kBBytes = NT * BK * 2;
+  static constexpr int kStages = (96 * 1024) / kBBytes;
+  static constexpr int kOffB = kABytes;
+  static constexpr int kOffBar = kOffB + kStages * kBBytes;
+  // full[S], empty[S], a_full[8], a_free[8], acc_full[2], acc_empty[2]
+  static constexpr int kBars = 2 * kStages + 2 * kChunks + 4;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+  static constexpr int kTmemCols = 2 * NT;
+  static constexpr uint32_t kIdescK = idesc_bf16(BM, NT, false, false);
+  static constexpr uint32_t kIdescV = idesc_bf16(BM, NT, false, true);
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
 
-__device__ __forceinline__ uint16_t to_bf(float x) { return static_cast<uint16_t>(pack_bf16x2(x, 0.f)); }
-
-// One block: 16 rows, one head; thread n < 128 a key column, else a value column.
-template <bool kFp8>
-__global__ void __launch_bounds__(256) expand_kernel(const ExpandParams p) {
-  __shared__ float c[kLatent][kTok];
-  const int t0 = blockIdx.x * kTok, h = blockIdx.y;
-  for (int i = threadIdx.x; i < kTok * kRow; i += 256) {
-    const int k = i / kRow, d = i - k * kRow, t = t0 + k;
-    float x = 0.f;
-    if (t < p.tokens) {
-      long long slot = __ldg(p.kv_indices + t);
-      if (slot < 0 || slot >= p.num_slots) {
-        record_status(p.status, MLA_ERR_INDEX_OOB);
-        slot = 0;
-      }
-      if constexpr (kFp8) {
-        x = e4m3x2_value(p.kv_cache[slot * kRow + d]).x;
-      } else {
-        x = bf(reinterpret_cast<const uint16_t*>(p.kv_cache)[slot * kRow + d]);
-      }
-      if (d >= kLatent && h == 0) p.k_rope[static_cast<size_t>(t) * kRope + d - kLatent] = to_bf(kFp8 ? x * p.kv_scale : x);
-    }
-    if (d < kLatent) c[d][k] = x;
-  }
-  __syncthreads();
-  const int n = threadIdx.x & 127;
-  const bool key = threadIdx.x < 128;
-  const uint16_t* w = key ? p.w_kc + (static_cast<size_t>(h) * kNope + n) * kLatent
-                          : p.w_vc + static_cast<size_t>(h) * kLatent * kNope + n;
-  const int step = key ? 1 : kNope;
-  float acc[kTok];
-#pragma unroll
-  for (int k = 0; k < kTok; ++k) acc[k] = 0.f;
-  for (int r = 0; r < kLatent; ++r) {
-    const float x = bf(__ldg(w + static_cast<size_t>(r) * step));
-#pragma unroll
-    for (int k = 0; k < kTok; ++k) acc[k] = fmaf(c[r][k], x, acc[k]);
-  }
-  uint16_t* out = key ? p.k_nope : p.v;
-#pragma unroll
-  for (int k = 0; k < kTok; ++k)
-    if (t0 + k < p.tokens)
-      out[(static_cast<size_t>(t0 + k) * p.heads + h) * kNope + n] = to_bf(kFp8 ? acc[k] * p.kv_scale : acc[k]);
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) return;
 }
 
-}  // namespace
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
+  const float2 f = e4m3x2_value(codes);
+  return pack_bf16x2(f.x, f.y);                             // exact
+}
 
-int launch_expand(const ExpandParams& p, bool fp8, cudaStream_t stream) {
-  const dim3 grid((p.tokens + kTok - 1) / kTok, p.heads, 1);
-  if (fp8) expand_kernel<true><<<grid, 256, 0, stream>>>(p);
-  else expand_kernel<false><<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+template <bool kFp8, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    expand_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const ExpandParams p) {
+  using C = Cfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return base + C::kOffBar + 8u * i; };
+  auto full = [&](int s) { return bar(s); };
+  auto empty = [&](int s) { return bar(C::kStages + s); };
+  auto a_full = [&](int k) { return bar(2 * C::kStages + k); };
+  auto a_free = [&](int k) { return bar(2 * C::kStages + kChunks + k); };
+  auto acc_full = [&](int i) { return bar(2 * C::kStages + 2 * kChunks + i); };
+  auto acc_empty = [&](int i) { return bar(2 * C::kStages + 2 * kChunks + 2 + i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  const WaitCtx wc{abort_flag, p.status};
+
+  // this CTA's tiles: rows outer, columns (keys of the heads, then values) inner
+  const int groups = (p.heads + C::kHeads - 1) / C::kHeads;
+  const int cols = 2 * groups;
+  const long long tiles = static_cast<long long>((p.tokens + BM - 1) / BM) * cols;
+  const int t0 = static_cast<int>(tiles * blockIdx.x / gridDim.x);
+  const int t1 = static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
+    for (int k = 0; k < kChunks; ++k) { mbar_init(a_full(k), 4); mbar_init(a_free(k), 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), 4); }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    // ---------------------------------------------------- weights producer
+    if (lane == 0) {
+      uint32_t c = 0;
+      bool ok = true;
+      for (int t = t0; t < t1 && ok; ++t) {
+        const int col = t % cols, h = (col % groups) * C::kHeads;
+        for (int k = 0; k < kChunks; ++k, ++c) {
+          const uint32_t s = c % C::kStages;
+          if (c >= C::kStages && !mbar_wait(empty(s), ((c / C::kStages) - 1) & 1, wc)) { ok = false; break; }
+          const uint32_t dst = base + C::kOffB + s * C::kBBytes;
+          mbar_arrive_expect_tx(full(s), C::kBBytes);
+          if (col < groups) {
+            tma_load_2d(dst, &tm_k, k * BK, h * kNope, full(s));              // NT rows of 64
+          } else {
+#pragma unroll
+            for (int j = 0; j < NT / 64; ++j)                                 // 64 rows of 64
+              tma_load_2d(dst + j * (BK * 128), &tm_v, 64 * (j & 1), (h + (j >> 1)) * kLatent + k * BK, full(s));
+          }
+        }
+      }
+      if (!ok)                                               // no copy outlives the block
+        for (uint32_t d = c > C::kStages ? c - C::kStages : 0; d < c; ++d)
+          drain_wait(full(d % C::kStages), (d / C::kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      auto D = [](uint64_t d, uint32_t off) -> uint64_t { return d + (off >> 4); };
+      uint32_t c = 0, i = 0, block = 0;
+      bool ok = true;
+      for (int t = t0; t < t1 && ok; ++t, ++i) {
+        const bool fresh = t == t0 || t % cols == 0;         // the first tile of a block of rows
+        const bool last = t + 1 == t1 || (t + 1) % cols == 0;
+        const bool key = t % cols < groups;
+        const uint32_t buf = i & 1;
+        if (i >= 2 && !mbar_wait(acc_empty(buf), ((i >> 1) - 1) & 1, wc)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem + buf * NT;
+        for (int k = 0; k < kChunks; ++k, ++c) {
+          const uint32_t s = c % C::kStages;
+          if (fresh && !mbar_wait(a_full(k), block & 1, wc)) { ok = false; break; }
+          if (!mbar_wait(full(s), (c / C::kStages) & 1, wc)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t da = sdesc(base + k * (BM * 128), 16, 1024);
+          if (key) {
+            const uint64_t db = sdesc(base + C::kOffB + s * C::kBBytes, 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < BK / 16; ++ks)
+              umma_ss(d, D(da, ks * 32), D(db, ks * 32), C::kIdescK, (k | ks) != 0 ? 1u : 0u);
+          } else {
+            const uint64_t db = sdesc(base + C::kOffB + s * C::kBBytes, BK * 128, 1024);
+#pragma unroll
+            for (int ks = 0; ks < BK / 16; ++ks)
+              umma_ss(d, D(da, ks * 32), D(db, ks * 2048), C::kIdescV, (k | ks) != 0 ? 1u : 0u);
+          }
+          umma_commit(empty(s));
+          if (last) umma_commit(a_free(k));
+        }
+        if (!ok) break;
+        umma_commit(acc_full(buf));
+        if (last) ++block;
+      }
+      if (!ok) {                                             // products in flight end before TMEM is given back
+        umma_commit(acc_full(i & 1));
+        drain_wait(acc_full(i & 1), (i >> 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kRowWarp0) {
+    // ------------------------------------------------------------------ rows
+    const int rt = threadIdx.x - 32 * kRowWarp0;             // 0..127
+    const int sub = rt & 7;                                  // 16-byte piece of a row's chunk
+    uint32_t block = 0;
+    for (int t = t0; t < t1; t = (t / cols + 1) * cols, ++block) {
+      const int m0 = (t / cols) * BM;
+      // a thread's rows are 16 i + rt / 8
+      long long row[8];
+      bool oob = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = min(m0 + 16 * i + (rt >> 3), p.tokens - 1);
+        long long slot = __ldg(p.kv_indices + r);
+        if (slot < 0 || slot >= p.num_slots) { oob = true; slot = 0; }
+        row[i] = slot * (kFp8 ? kRow : 2 * kRow);
+      }
+      if (oob) record_status(p.status, MLA_ERR_INDEX_OOB);
+      bool ok = true;
+      constexpr int kStep = kFp8 ? 2 : 1;                    // chunks that 16 bytes a lane cover
+      auto load = [&](int k, uint4 (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = __ldg(reinterpret_cast<const uint4*>(p.kv_cache + row[i] + k * (kFp8 ? 64 : 128)) + sub);
+      };
+      uint4 next[8];
+      load(0, next);
+#pragma unroll 1
+      for (int k = 0; k < kChunks; k += kStep) {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = next[i];
+        if (k + kStep < kChunks) load(k + kStep, next);
+        if (block > 0) {
+          for (int j = 0; j < kStep && ok; ++j) {
+            if (lane == 0) ok = mbar_wait(a_free(k + j), (block - 1) & 1, wc);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+          }
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 16 * i + (rt >> 3);
+          if constexpr (kFp8) {
+            // 16 codes: pieces 2 (sub & 3) and + 1 of chunk k + sub / 4
+            uint8_t* dst = smem + (k + (sub >> 2)) * (BM * 128) + r * 128;
+            const int c = 2 * (sub & 3);
+            *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) << 4)) =
+                make_uint4(e4m3x2_to_bf16x2(v[i].x), e4m3x2_to_bf16x2(v[i].x >> 16), e4m3x2_to_bf16x2(v[i].y),
+                           e4m3x2_to_bf16x2(v[i].y >> 16));
+            *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (r & 7)) << 4)) =
+                make_uint4(e4m3x2_to_bf16x2(v[i].z), e4m3x2_to_bf16x2(v[i].z >> 16), e4m3x2_to_bf16x2(v[i].w),
+                           e4m3x2_to_bf16x2(v[i].w >> 16));
+          } else {
+            *reinterpret_cast<uint4*>(smem + k * (BM * 128) + r * 128 + ((sub ^ (r & 7)) << 4)) = v[i];
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+          for (int j = 0; j < kStep; ++j) mbar_arrive(a_full(k + j));
+      }
+      if (!ok) break;
+      if (t % cols == 0) {                                   // the CTA with the block's first tile writes its rope keys
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = m0 + 16 * i + (rt >> 3);
+          if (r >= p.tokens) continue;
+          uint4* dst = reinterpret_cast<uint4*>(p.k_rope + static_cast<size_t>(r) * kRope) + sub;
+          if constexpr (kFp8) {
+            const uint2 c = __ldg(reinterpret_cast<const uint2*>(p.kv_cache + row[i] + kLatent) + sub);
+            auto val = [&](uint32_t codes) {
+              const float2 f = e4m3x2_value(codes);
+              return pack_bf16x2(f.x * p.kv_scale, f.y * p.kv_scale);
+            };
+            *dst = make_uint4(val(c.x), val(c.x >> 16), val(c.y), val(c.y >> 16));
+          } else {
+            *dst = __ldg(reinterpret_cast<const uint4*>(p.kv_cache + row[i] + 2 * kLatent) + sub);
+          }
+        }
+      }
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------- epilogue
+    const int q = warp - kEpiWarp0;
+    const float scale = kFp8 ? p.kv_scale : 1.f;
+    uint32_t i = 0;
+    for (int t = t0; t < t1; ++t, ++i) {
+      const int col = t % cols, h = (col % groups) * C::kHeads;
+      const long long r = static_cast<long long>(t / cols) * BM + 32 * q + lane;
+      const uint32_t buf = i & 1;
+      bool ok = true;
+      if (lane == 0) ok = mbar_wait(acc_full(buf), (i >> 1) & 1, wc);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      uint16_t* out = (col < groups ? p.k_nope : p.v) + (r * p.heads + h) * kNope;
+      const int width = min(NT, (p.heads - h) * kNope);      // an odd last head: half a tile
+#pragma unroll 1
+      for (int c = 0; c < width; c += 32) {
+        uint32_t a[16], b[16];
+        const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * NT + c;
+        tmem_ld16(src, a);
+        tmem_ld16(src + 16, b);
+        tmem_wait_ld();
+        if (r < p.tokens) {
+          uint32_t w[8], x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            w[e] = pack_bf16x2(__uint_as_float(a[2 * e]) * scale, __uint_as_float(a[2 * e + 1]) * scale);
+            x[e] = pack_bf16x2(__uint_as_float(b[2 * e]) * scale, __uint_as_float(b[2 * e + 1]) * scale);
+          }
+          if (p.wide_stores) {
+            st_global_v8(out + c, w);
+            st_global_v8(out + c + 16, x);
+          } else {
+            st_global_v4(out + c, w[0], w[1], w[2], w[3]);
+            st_global_v4(out + c + 8, w[4], w[5], w[6], w[7]);
+            st_global_v4(out + c + 16, x[0], x[1], x[2], x[3]);
+            st_global_v4(out + c + 24, x[4], x[5], x[6], x[7]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty(buf));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+template <bool kFp8, int NT>
+int launch(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid, cudaStream_t stream) {
+  using C = Cfg<NT>;
+  if (!set_smem_limit(reinterpret_cast<const void*>(&expand_kernel<kFp8, NT>), C::kSmemBytes)) return MLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, expand_kernel<kFp8, NT>, tm_k, tm_v, p) != cudaSuccess) return MLA_ERR_CUDA;
+  return cudaPeekAtLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace ex
+
+// Columns of a tile: 256 (two heads' keys or values) unless that gives fewer
+// tiles than SMs, where 128 halves the longest CTA.
+int expand_tile_cols(int tokens, int heads, int sms) {
+  const long long blocks = (tokens + ex::BM - 1) / ex::BM;
+  return blocks * 2 * ((heads + 1) / 2) < sms ? 128 : 256;
+}
+
+int launch_expand(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int tile_cols, int sms,
+                  bool fp8, cudaStream_t stream) {
+  const int per = tile_cols / kNope;
+  const long long tiles = static_cast<long long>((p.tokens + ex::BM - 1) / ex::BM) * 2 * ((p.heads + per - 1) / per);
+  if (tiles > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
+  const int grid = static_cast<int>(tiles < sms ? tiles : sms);
+  if (tile_cols == 128)
+    return fp8 ? ex::launch<true, 128>(p, tm_k, tm_v, grid, stream) : ex::launch<false, 128>(p, tm_k, tm_v, grid, stream);
+  return fp8 ? ex::launch<true, 256>(p, tm_k, tm_v, grid, stream) : ex::launch<false, 256>(p, tm_k, tm_v, grid, stream);
 }
 
 }  // namespace mla

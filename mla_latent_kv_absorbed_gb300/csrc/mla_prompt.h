@@ -59,6 +59,7 @@ struct ExpandParams {
   int* status;                // status word, or null
   long long num_slots;
   int tokens, heads;
+  int wide_stores;            // k_nope and v are 32-byte aligned
   float kv_scale;             // FP8 cache only
 };
 
@@ -108,7 +109,11 @@ struct PrefillParams {
 
 int launch_rope_query(const RopeQueryParams& p, const RopeFreqs& f, cudaStream_t stream);
 int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, cudaStream_t stream);
-int launch_expand(const ExpandParams& p, bool fp8, cudaStream_t stream);
+// tm_k over w_kc as [heads * 128, 512] (box tile_cols rows x 64), tm_v over
+// w_vc as [heads * 512, 128] (box 64 x 64).
+int expand_tile_cols(int tokens, int heads, int sms);
+int launch_expand(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int tile_cols, int sms,
+                  bool fp8, cudaStream_t stream);
 // tm_q over q as [rows, heads, 192] (box 128 rows x 64), tm_k and tm_v over
 // [keys, heads, 128] (boxes of 128 and 64 keys x 64), tm_kr over [keys, 64].
 int launch_prefill(const PrefillParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_kr,

@@ -40,7 +40,7 @@ EncodeTiledFn encode_fn() {
 }
 
 // bf16 [rows, heads, width] with strides in elements (heads 0: [rows, width]),
-// boxes of `box_rows` rows of one head x 64 values, 128-byte swizzle; reads
+// boxes of `box_rows` (<= 256) rows of one head x 64 values, 128-byte swizzle; reads
 // past the last row give zeros.  The stride of a dimension of one is not used.
 bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride,
               int width, int box_rows) {
@@ -207,7 +207,16 @@ int expand(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, i
   p.tokens = tokens;
   p.heads = num_heads;
   p.kv_scale = kv_scale;
-  return launch_expand(p, fp8, reinterpret_cast<cudaStream_t>(stream));
+  p.wide_stores = aligned(k_nope, 32) && aligned(v, 32);
+  const int sms = device_sm_count();
+  if (sms < 1) return MLA_ERR_CUDA;
+  const int cols = expand_tile_cols(tokens, num_heads, sms);
+  CUtensorMap tm_k, tm_v;
+  const int64_t H = num_heads;
+  if (!make_map(&tm_k, w_kc, H * kNope, kLatent, 0, 0, kLatent, cols) ||
+      !make_map(&tm_v, w_vc, H * kLatent, kNope, 0, 0, kNope, 64))
+    return MLA_ERR_CUDA;
+  return launch_expand(p, tm_k, tm_v, cols, sms, fp8, reinterpret_cast<cudaStream_t>(stream));
 }
 }  // namespace
 
