@@ -428,26 +428,40 @@ def decode_step_host(q_nope, q_rope, kv_indptr, kv_indices, kv_cache, sm_scale, 
 # ---- the prompt side: rotary positions, latent expansion, expanded attention ----
 
 def _need(where, name, t, dtype, shape, dense=True) -> None:
-    """The ABI passes no lengths and no types: a tensor of another type, shape (None: any size), layout or
-    device is refused here, before any launch.  dense: contiguous; else only the last dimension is."""
+    """The ABI passes no lengths and no types: a tensor of another type, shape, layout or device is refused
+    here, before any launch.  dense: contiguous; else only the last dimension is."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and (t.is_contiguous() or not dense and t.stride(-1) == 1):
+        return
     if t.dtype is not dtype:
         raise ValueError(f"{where}: {name} is {t.dtype}, {dtype} is wanted")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, {tuple('*' if w is None else w for w in shape)} "
-                         "is wanted")
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, {tuple(shape)} is wanted")
     if t.numel() and not (t.is_contiguous() if dense else (t.stride(-1) == 1 or t.shape[-1] == 1)):
         raise ValueError(f"{where}: {name} is not laid out {'densely' if dense else 'with its last dimension together'}")
     if not t.is_cuda:
         raise ValueError(f"{where}: {name} is not on a CUDA device")
 
 
-def _one_device(where, *tensors) -> None:
-    """Every tensor on the current device: the launch goes there."""
+def _sizes(where, name, t, dims):
+    """The shape of a tensor that sets the sizes of a call."""
+    if t.dim() != dims:
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, {dims} dimensions are wanted")
+    return t.shape
+
+
+def _launch_stream(where, stream, *tensors):
+    """The stream to launch on (the current one when none is given).  Every tensor has to be on the current
+    device: the launch goes there."""
     import torch
-    cur = torch.cuda.current_device()
+    try:                                             # what current_device and current_stream look up, without
+        cur = torch._C._cuda_getDevice()             # their objects: a third of a small call's host time
+        raw = torch._C._cuda_getCurrentRawStream(cur) if stream is None else None
+    except AttributeError:
+        cur, raw = torch.cuda.current_device(), None
     for t in tensors:
         if t is not None and t.get_device() != cur:
-            raise ValueError(f"{where}: a tensor is on cuda:{t.get_device()}, the current device is cuda:{cur}")
+            raise ValueError(f"{where}: a tensor is on device {t.device}, the current device is cuda:{cur}")
+    return (raw or None) if raw is not None else _stream_handle(stream)
 
 
 _ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
@@ -471,7 +485,7 @@ def _freqs_ptr(where, freqs):
     if not isinstance(freqs, np.ndarray) or freqs.dtype != np.uint64 or freqs.shape != (32,) or \
             not freqs.flags.c_contiguous:
         raise ValueError(f"{where}: freqs is the uint64 array of rope_frequencies")
-    return freqs.ctypes.data
+    return freqs.__array_interface__["data"][0]
 
 
 def rope_query(q, positions, freqs, q_rope, q_nope=None, amplitude: float = 1.0, interleaved: bool = True,
@@ -481,36 +495,38 @@ def rope_query(q, positions, freqs, q_rope, q_nope=None, amplitude: float = 1.0,
     q_nope: optional dense bf16 [T, H, nope] that receives the rest of each head."""
     import torch
     w = "mla_rope_query"
-    T, H, D = q.shape if q.dim() == 3 else (-1, -1, -1)
+    bf = torch.bfloat16
+    T, H, D = _sizes(w, "q", q, 3)
     nope = D - 64
-    _need(w, "q", q, torch.bfloat16, (None, None, None), dense=False)
+    _need(w, "q", q, bf, (T, H, D), dense=False)
     if nope < 0:
         raise ValueError(f"{w}: q has {D} values a head, at least the 64 rotary ones are wanted")
     _need(w, "positions", positions, torch.int32, (T,))
-    _need(w, "q_rope", q_rope, torch.bfloat16, (T, H, 64), dense=False)
+    _need(w, "q_rope", q_rope, bf, (T, H, 64), dense=False)
     if q_nope is not None:
-        _need(w, "q_nope", q_nope, torch.bfloat16, (T, H, nope))
-    _one_device(w, q, positions, q_rope, q_nope)
+        _need(w, "q_nope", q_nope, bf, (T, H, nope))
+    fr, st = _freqs_ptr(w, freqs), _launch_stream(w, stream, q, positions, q_rope, q_nope)
     if T == 0 or H == 0:
         return
-    st = _lib.mla_rope_query(q.data_ptr(), q.stride(0), q.stride(1), positions.data_ptr(), T, H, nope,
-                             _freqs_ptr(w, freqs), float(amplitude), int(bool(interleaved)), q_rope.data_ptr(),
-                             q_rope.stride(0), q_rope.stride(1), _ptr(q_nope), _stream_handle(stream))
+    (qt, qh, _), (rt, rh, _) = q.stride(), q_rope.stride()
+    st = _lib.mla_rope_query(q.data_ptr(), qt, qh, positions.data_ptr(), T, H, nope, fr, amplitude,
+                             1 if interleaved else 0, q_rope.data_ptr(), rt, rh, _ptr(q_nope), st)
     if st != MLA_OK:
         raise MLAError(st, w)
 
 
-def _rope_append(w, cache_dtype, kv_cache, slots, rows, positions, freqs, norm_weight, workspace):
+def _rope_append(w, cache_dtype, kv_cache, slots, rows, positions, freqs, norm_weight, workspace, stream):
     import torch
-    T = rows.shape[0] if rows.dim() == 2 else -1
-    _need(w, "kv_cache", kv_cache, cache_dtype, (None, 576))
-    _need(w, "rows", rows, torch.bfloat16, (None, 576), dense=False)
+    T = _sizes(w, "rows", rows, 2)[0]
+    N = _sizes(w, "kv_cache", kv_cache, 2)[0]
+    _need(w, "kv_cache", kv_cache, cache_dtype, (N, 576))
+    _need(w, "rows", rows, torch.bfloat16, (T, 576), dense=False)
     _need(w, "slots", slots, torch.int32, (T,))
     _need(w, "positions", positions, torch.int32, (T,))
     if norm_weight is not None:
         _need(w, "norm_weight", norm_weight, torch.bfloat16, (512,))
-    _one_device(w, kv_cache, rows, slots, positions, norm_weight, workspace)
-    return T, _freqs_ptr(w, freqs)
+    return (N, T, rows.stride(0), _freqs_ptr(w, freqs),
+            _launch_stream(w, stream, kv_cache, rows, slots, positions, norm_weight, workspace))
 
 
 def rope_append_kv(kv_cache, slots, rows, positions, freqs, norm_weight=None, eps: float = 1e-6,
@@ -519,10 +535,11 @@ def rope_append_kv(kv_cache, slots, rows, positions, freqs, norm_weight=None, ep
     <- bf16 [T, 576] (rows may be a slice of a wider projection); norm_weight bf16 [512] or None (no norm)."""
     import torch
     w = "mla_rope_append_kv"
-    T, fr = _rope_append(w, torch.bfloat16, kv_cache, slots, rows, positions, freqs, norm_weight, workspace)
-    st = _lib.mla_rope_append_kv(kv_cache.data_ptr(), kv_cache.shape[0], slots.data_ptr(), rows.data_ptr(),
-                                 rows.stride(0), positions.data_ptr(), T, _ptr(norm_weight), float(eps), fr,
-                                 float(amplitude), int(bool(interleaved)), _ptr(workspace), _stream_handle(stream))
+    N, T, rs, fr, st = _rope_append(w, torch.bfloat16, kv_cache, slots, rows, positions, freqs, norm_weight,
+                                    workspace, stream)
+    st = _lib.mla_rope_append_kv(kv_cache.data_ptr(), N, slots.data_ptr(), rows.data_ptr(), rs,
+                                 positions.data_ptr(), T, _ptr(norm_weight), eps, fr, amplitude,
+                                 1 if interleaved else 0, _ptr(workspace), st)
     if st != MLA_OK:
         raise MLAError(st, w)
 
@@ -532,41 +549,41 @@ def rope_append_kv_fp8(kv_cache, slots, rows, positions, freqs, kv_scale, norm_w
     """rope_append_kv into an FP8 cache: uint8 [num_slots, 576] E4M3 codes of the values / kv_scale."""
     import torch
     w = "mla_rope_append_kv_fp8"
-    T, fr = _rope_append(w, torch.uint8, kv_cache, slots, rows, positions, freqs, norm_weight, workspace)
-    st = _lib.mla_rope_append_kv_fp8(kv_cache.data_ptr(), kv_cache.shape[0], slots.data_ptr(), rows.data_ptr(),
-                                     rows.stride(0), positions.data_ptr(), T, _ptr(norm_weight), float(eps), fr,
-                                     float(amplitude), int(bool(interleaved)), float(kv_scale), _ptr(workspace),
-                                     _stream_handle(stream))
+    N, T, rs, fr, st = _rope_append(w, torch.uint8, kv_cache, slots, rows, positions, freqs, norm_weight, workspace,
+                                    stream)
+    st = _lib.mla_rope_append_kv_fp8(kv_cache.data_ptr(), N, slots.data_ptr(), rows.data_ptr(), rs,
+                                     positions.data_ptr(), T, _ptr(norm_weight), eps, fr, amplitude,
+                                     1 if interleaved else 0, kv_scale, _ptr(workspace), st)
     if st != MLA_OK:
         raise MLAError(st, w)
 
 
-def _expand(w, cache_dtype, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace):
+def _expand(w, cache_dtype, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace, stream):
     import torch
-    T = kv_indices.shape[0] if kv_indices.dim() == 1 else -1
-    H = w_kc.shape[0] if w_kc.dim() == 3 else -1
     bf = torch.bfloat16
-    _need(w, "kv_cache", kv_cache, cache_dtype, (None, 576))
-    _need(w, "kv_indices", kv_indices, torch.int32, (None,))
-    _need(w, "w_kc", w_kc, bf, (None, 128, 512))
+    N = _sizes(w, "kv_cache", kv_cache, 2)[0]
+    T = _sizes(w, "kv_indices", kv_indices, 1)[0]
+    H = _sizes(w, "w_kc", w_kc, 3)[0]
+    _need(w, "kv_cache", kv_cache, cache_dtype, (N, 576))
+    _need(w, "kv_indices", kv_indices, torch.int32, (T,))
+    _need(w, "w_kc", w_kc, bf, (H, 128, 512))
     _need(w, "w_vc", w_vc, bf, (H, 512, 128))
     _need(w, "k_nope", k_nope, bf, (T, H, 128))
     _need(w, "k_rope", k_rope, bf, (T, 64))
     _need(w, "v", v, bf, (T, H, 128))
-    _one_device(w, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace)
-    return T, H
+    return N, T, H, _launch_stream(w, stream, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace)
 
 
 def expand_kv(kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace=None, stream=None) -> None:
     """Per-head keys and values of the cached rows kv_indices int32 [T]: k_nope[t,h,:] = c_t . w_kc[h]^T and
     v[t,h,:] = c_t . w_vc[h] (bf16 [T,H,128]), k_rope[t,:] the rows' rope keys (bf16 [T,64])."""
     import torch
-    T, H = _expand("mla_expand_kv", torch.bfloat16, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace)
-    st = _lib.mla_expand_kv(kv_cache.data_ptr(), kv_cache.shape[0], kv_indices.data_ptr(), T, w_kc.data_ptr(),
-                            w_vc.data_ptr(), H, k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), _ptr(workspace),
-                            _stream_handle(stream))
+    w = "mla_expand_kv"
+    N, T, H, st = _expand(w, torch.bfloat16, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace, stream)
+    st = _lib.mla_expand_kv(kv_cache.data_ptr(), N, kv_indices.data_ptr(), T, w_kc.data_ptr(), w_vc.data_ptr(), H,
+                            k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), _ptr(workspace), st)
     if st != MLA_OK:
-        raise MLAError(st, "mla_expand_kv")
+        raise MLAError(st, w)
 
 
 def expand_kv_fp8(kv_cache, kv_scale, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace=None,
@@ -574,10 +591,10 @@ def expand_kv_fp8(kv_cache, kv_scale, kv_indices, w_kc, w_vc, k_nope, k_rope, v,
     """expand_kv from an FP8 cache: uint8 [num_slots, 576] E4M3 codes (value = code x kv_scale)."""
     import torch
     w = "mla_expand_kv_fp8"
-    T, H = _expand(w, torch.uint8, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace)
-    st = _lib.mla_expand_kv_fp8(kv_cache.data_ptr(), kv_cache.shape[0], float(kv_scale), kv_indices.data_ptr(), T,
-                                w_kc.data_ptr(), w_vc.data_ptr(), H, k_nope.data_ptr(), k_rope.data_ptr(),
-                                v.data_ptr(), _ptr(workspace), _stream_handle(stream))
+    N, T, H, st = _expand(w, torch.uint8, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace, stream)
+    st = _lib.mla_expand_kv_fp8(kv_cache.data_ptr(), N, kv_scale, kv_indices.data_ptr(), T, w_kc.data_ptr(),
+                                w_vc.data_ptr(), H, k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(),
+                                _ptr(workspace), st)
     if st != MLA_OK:
         raise MLAError(st, w)
 
@@ -620,13 +637,12 @@ def prefill_run(plan_host, plan_dev, q, k_nope, k_rope, v, sm_scale: float, out,
     _need(w, "out", out, bf, (nq, H, 128))
     if lse is not None:
         _need(w, "lse", lse, torch.float32, (nq, H))
-    _need(w, "workspace", workspace, torch.uint8, (None,))
-    _one_device(w, plan_dev, q, k_nope, k_rope, v, out, lse, workspace)
-    st = _lib.mla_prefill_run(plan_host.ctypes.data, plan_dev.data_ptr(), q.data_ptr(), q.stride(0), q.stride(1),
-                              k_nope.data_ptr(), k_nope.stride(0), k_nope.stride(1), k_rope.data_ptr(),
-                              k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1), float(sm_scale),
-                              out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
-                              _stream_handle(stream))
+    _need(w, "workspace", workspace, torch.uint8, (workspace.numel(),))
+    st = _launch_stream(w, stream, plan_dev, q, k_nope, k_rope, v, out, lse, workspace)
+    (qt, qh, _), (kt, kh, _), (vt, vh, _) = q.stride(), k_nope.stride(), v.stride()
+    st = _lib.mla_prefill_run(plan_host.ctypes.data, plan_dev.data_ptr(), q.data_ptr(), qt, qh, k_nope.data_ptr(), kt,
+                              kh, k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), vt, vh, sm_scale,
+                              out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), st)
     if st != MLA_OK:
         raise MLAError(st, w)
 
