@@ -12,11 +12,14 @@
 // stream.  A column tile is NT columns: the keys, or the values, of NT / 128
 // heads; w_kc is K-major as it lies, w_vc N-major.
 //   warp 0      TMA producer of the weights, 64-deep chunks in a ring
-//   warp 1      TMEM allocator, MMA issuer: M = 128, N = NT, two accumulators
+//   warp 1      TMEM allocator, MMA issuer: two accumulators in turn
 //   warps 4-7   epilogue: a TMEM lane is a row; 32-byte stores
 //   warps 8-11  rows: gather, swizzle (128-byte atoms), rope keys
-// Bound: the tensor core at many rows (512 MACs an output byte pair), the
-// weights' bytes at few.
+// kPair: two CTAs of a cluster work on one tile of 256 rows x 256 columns
+// (cta_group::2): each holds its 128 rows and half of the weights' columns,
+// CTA 0 issues for both.  That halves the weights that every SM reads from L2,
+// which bounded the single-CTA form (1.07 GB in 134 us at 4096 rows x 128
+// heads).
 #include "mla_device.cuh"
 #include "mla_launch.h"
 #include "mla_prompt.h"
@@ -28,12 +31,14 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarp0 = 4, kRowWarp0 = 8;
 constexpr int BM = 128, BK = 64, kChunks = kLatent / BK;
 
-template <int NT_>
+template <int NT_, bool kPair>
 struct Cfg {
   static constexpr int NT = NT_;
   static constexpr int kHeads = NT / kNope;                 // heads of a tile
+  static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kABytes = kChunks * BM * 128;        // 128 KB
-  static constexpr int kBBytes = NT * BK * 2;
+  static constexpr int kCols = NT / kCtas;                  // of a tile's columns, those this CTA loads
+  static constexpr int kBBytes = kCols * BK * 2;
   static constexpr int kStages = (96 * 1024) / kBBytes;
   static constexpr int kOffB = kABytes;
   static constexpr int kOffBar = kOffB + kStages * kBBytes;
@@ -42,8 +47,8 @@ struct Cfg {
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
   static constexpr int kTmemCols = 2 * NT;
-  static constexpr uint32_t kIdescK = idesc_bf16(BM, NT, false, false);
-  static constexpr uint32_t kIdescV = idesc_bf16(BM, NT, false, true);
+  static constexpr uint32_t kIdescK = idesc_bf16(kCtas * BM, NT, false, false);
+  static constexpr uint32_t kIdescV = idesc_bf16(kCtas * BM, NT, false, true);
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
@@ -58,11 +63,46 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
   return pack_bf16x2(f.x, f.y);                             // exact
 }
 
-template <bool kFp8, int NT>
+// ---- the two-CTA forms of the tensor core's and the copy engine's instructions
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void umma_ss2(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs when the products issued so far are done.
+__device__ __forceinline__ void umma_commit2(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// A load into this CTA's shared memory whose bytes are counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, int x, int y, uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar_cluster)
+      : "memory");
+}
+
+template <bool kFp8, int NT, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const ExpandParams p) {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, kPair>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -79,30 +119,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const WaitCtx wc{abort_flag, p.status};
 
-  // this CTA's tiles: rows outer, columns (keys of the heads, then values) inner
+  const uint32_t rank = kPair ? cluster_ctarank() : 0;
+  // this CTA's (pair's) tiles: rows outer, columns (keys of the heads, then values) inner
   const int groups = (p.heads + C::kHeads - 1) / C::kHeads;
   const int cols = 2 * groups;
-  const long long tiles = static_cast<long long>((p.tokens + BM - 1) / BM) * cols;
-  const int t0 = static_cast<int>(tiles * blockIdx.x / gridDim.x);
-  const int t1 = static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x);
+  const int tile_rows = C::kCtas * BM;
+  const long long tiles = static_cast<long long>((p.tokens + tile_rows - 1) / tile_rows) * cols;
+  const int worker = blockIdx.x / C::kCtas, workers = gridDim.x / C::kCtas;
+  const int t0 = static_cast<int>(tiles * worker / workers);
+  const int t1 = static_cast<int>(tiles * (worker + 1) / workers);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
-    for (int k = 0; k < kChunks; ++k) { mbar_init(a_full(k), 4); mbar_init(a_free(k), 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), 4); }
+    for (int k = 0; k < kChunks; ++k) { mbar_init(a_full(k), 4 * C::kCtas); mbar_init(a_free(k), 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), 4 * C::kCtas); }
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc2(smem_u32(tmem_slot), C::kTmemCols);
+      tmem_relinquish2();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+      tmem_relinquish();
+    }
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) cluster_sync_all();                  // both CTAs' barriers exist before any remote use
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
@@ -119,24 +168,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t s = c % C::kStages;
           if (c >= C::kStages && !mbar_wait(empty(s), ((c / C::kStages) - 1) & 1, wc)) { ok = false; break; }
           const uint32_t dst = base + C::kOffB + s * C::kBBytes;
-          mbar_arrive_expect_tx(full(s), C::kBBytes);
+          // both halves of a pair's tile are counted on CTA 0's barrier
+          if (rank == 0) mbar_arrive_expect_tx(full(s), C::kCtas * C::kBBytes);
+          const int hh = h + static_cast<int>(rank) * (C::kCols / kNope);
+          const uint32_t fb = kPair ? mapa_shared(full(s), 0) : full(s);
+          auto load = [&](uint32_t d, const CUtensorMap* m, int x, int y) {
+            if constexpr (kPair) tma_load_2d_pair(d, m, x, y, fb);
+            else tma_load_2d(d, m, x, y, fb);
+          };
           if (col < groups) {
-            tma_load_2d(dst, &tm_k, k * BK, h * kNope, full(s));              // NT rows of 64
+            load(dst, &tm_k, k * BK, hh * kNope);                             // kCols rows of 64
           } else {
 #pragma unroll
-            for (int j = 0; j < NT / 64; ++j)                                 // 64 rows of 64
-              tma_load_2d(dst + j * (BK * 128), &tm_v, 64 * (j & 1), (h + (j >> 1)) * kLatent + k * BK, full(s));
+            for (int j = 0; j < C::kCols / 64; ++j)                           // 64 rows of 64
+              load(dst + j * (BK * 128), &tm_v, 64 * (j & 1), (hh + (j >> 1)) * kLatent + k * BK);
           }
         }
       }
-      if (!ok)                                               // no copy outlives the block
+      if (!ok && rank == 0)                                  // no copy outlives the block
         for (uint32_t d = c > C::kStages ? c - C::kStages : 0; d < c; ++d)
           drain_wait(full(d % C::kStages), (d / C::kStages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
+      auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+        if constexpr (kPair) umma_ss2(d, a, b, idesc, acc);
+        else umma_ss(d, a, b, idesc, acc);
+      };
+      auto commit = [](uint32_t b) {
+        if constexpr (kPair) umma_commit2(b);
+        else umma_commit(b);
+      };
       auto D = [](uint64_t d, uint32_t off) -> uint64_t { return d + (off >> 4); };
       uint32_t c = 0, i = 0, block = 0;
       bool ok = true;
@@ -145,35 +209,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool last = t + 1 == t1 || (t + 1) % cols == 0;
         const bool key = t % cols < groups;
         const uint32_t buf = i & 1;
-        if (i >= 2 && !mbar_wait(acc_empty(buf), ((i >> 1) - 1) & 1, wc)) { ok = false; break; }
+        if (i >= 2 && !mbar_wait<kPair>(acc_empty(buf), ((i >> 1) - 1) & 1, wc)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + buf * NT;
         for (int k = 0; k < kChunks; ++k, ++c) {
           const uint32_t s = c % C::kStages;
-          if (fresh && !mbar_wait(a_full(k), block & 1, wc)) { ok = false; break; }
-          if (!mbar_wait(full(s), (c / C::kStages) & 1, wc)) { ok = false; break; }
+          if (fresh && !mbar_wait<kPair>(a_full(k), block & 1, wc)) { ok = false; break; }
+          if (!mbar_wait<kPair>(full(s), (c / C::kStages) & 1, wc)) { ok = false; break; }
           tc_fence_after();
           const uint64_t da = sdesc(base + k * (BM * 128), 16, 1024);
           if (key) {
             const uint64_t db = sdesc(base + C::kOffB + s * C::kBBytes, 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
-              umma_ss(d, D(da, ks * 32), D(db, ks * 32), C::kIdescK, (k | ks) != 0 ? 1u : 0u);
+              mma(d, D(da, ks * 32), D(db, ks * 32), C::kIdescK, (k | ks) != 0 ? 1u : 0u);
           } else {
             const uint64_t db = sdesc(base + C::kOffB + s * C::kBBytes, BK * 128, 1024);
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
-              umma_ss(d, D(da, ks * 32), D(db, ks * 2048), C::kIdescV, (k | ks) != 0 ? 1u : 0u);
+              mma(d, D(da, ks * 32), D(db, ks * 2048), C::kIdescV, (k | ks) != 0 ? 1u : 0u);
           }
-          umma_commit(empty(s));
-          if (last) umma_commit(a_free(k));
+          commit(empty(s));
+          if (last) commit(a_free(k));
         }
         if (!ok) break;
-        umma_commit(acc_full(buf));
+        commit(acc_full(buf));
         if (last) ++block;
       }
       if (!ok) {                                             // products in flight end before TMEM is given back
-        umma_commit(acc_full(i & 1));
+        commit(acc_full(i & 1));
         drain_wait(acc_full(i & 1), (i >> 1) & 1);
       }
     }
@@ -184,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sub = rt & 7;                                  // 16-byte piece of a row's chunk
     uint32_t block = 0;
     for (int t = t0; t < t1; t = (t / cols + 1) * cols, ++block) {
-      const int m0 = (t / cols) * BM;
+      const int m0 = (t / cols) * tile_rows + static_cast<int>(rank) * BM;
       // a thread's rows are 16 i + rt / 8
       long long row[8];
       bool oob = false;
@@ -238,7 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
-          for (int j = 0; j < kStep; ++j) mbar_arrive(a_full(k + j));
+          for (int j = 0; j < kStep; ++j) {
+            if constexpr (kPair) mbar_arrive_cluster(a_full(k + j), 0);
+            else mbar_arrive(a_full(k + j));
+          }
       }
       if (!ok) break;
       if (t % cols == 0) {                                   // the CTA with the block's first tile writes its rope keys
@@ -267,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t i = 0;
     for (int t = t0; t < t1; ++t, ++i) {
       const int col = t % cols, h = (col % groups) * C::kHeads;
-      const long long r = static_cast<long long>(t / cols) * BM + 32 * q + lane;
+      const long long r = static_cast<long long>(t / cols) * tile_rows + rank * BM + 32 * q + lane;
       const uint32_t buf = i & 1;
       bool ok = true;
       if (lane == 0) ok = mbar_wait(acc_full(buf), (i >> 1) & 1, wc);
@@ -303,50 +370,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty(buf));
+      if (lane == 0) {
+        if constexpr (kPair) mbar_arrive_cluster(acc_empty(buf), 0);
+        else mbar_arrive(acc_empty(buf));
+      }
     }
   }
   tc_fence_before();
-  __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  __syncwarp();
+  if constexpr (kPair) {
+    cluster_sync_all();                                     // no CTA leaves while the other signals it or uses its TMEM
+    if (warp == 1) tmem_dealloc2(tmem, C::kTmemCols);
+  } else {
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  }
 }
 
-template <bool kFp8, int NT>
+template <bool kFp8, int NT, bool kPair>
 int launch(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid, cudaStream_t stream) {
-  using C = Cfg<NT>;
-  if (!set_smem_limit(reinterpret_cast<const void*>(&expand_kernel<kFp8, NT>), C::kSmemBytes)) return MLA_ERR_CUDA;
+  using C = Cfg<NT, kPair>;
+  const auto kernel = &expand_kernel<kFp8, NT, kPair>;
+  if (!set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes)) return MLA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C::kCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, expand_kernel<kFp8, NT>, tm_k, tm_v, p) != cudaSuccess) return MLA_ERR_CUDA;
+  cfg.numAttrs = kPair ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, p) != cudaSuccess) return MLA_ERR_CUDA;
   return cudaPeekAtLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace ex
 
-// Columns of a tile: 256 (two heads' keys or values) unless that gives fewer
-// tiles than SMs, where 128 halves the longest CTA.
-int expand_tile_cols(int tokens, int heads, int sms) {
+// Tiles: 128 rows x 128 columns where two-head tiles would give fewer tiles
+// than SMs (the longest CTA is halved), 256 x 256 on CTA pairs otherwise; 128 x
+// 256 for a single block of rows, whose pair would compute nothing.
+ExpandTiling expand_tiling(int tokens, int heads, int sms) {
   const long long blocks = (tokens + ex::BM - 1) / ex::BM;
-  return blocks * 2 * ((heads + 1) / 2) < sms ? 128 : 256;
+  const long long groups = 2ll * ((heads + 1) / 2);
+  if (blocks * groups < sms) return {128, false};
+  return {256, blocks > 1 && sms > 1};
 }
 
-int launch_expand(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int tile_cols, int sms,
+int launch_expand(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, ExpandTiling tiling, int sms,
                   bool fp8, cudaStream_t stream) {
-  const int per = tile_cols / kNope;
-  const long long tiles = static_cast<long long>((p.tokens + ex::BM - 1) / ex::BM) * 2 * ((p.heads + per - 1) / per);
-  if (tiles > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
-  const int grid = static_cast<int>(tiles < sms ? tiles : sms);
-  if (tile_cols == 128)
-    return fp8 ? ex::launch<true, 128>(p, tm_k, tm_v, grid, stream) : ex::launch<false, 128>(p, tm_k, tm_v, grid, stream);
-  return fp8 ? ex::launch<true, 256>(p, tm_k, tm_v, grid, stream) : ex::launch<false, 256>(p, tm_k, tm_v, grid, stream);
+  const int per = tiling.cols / kNope, rows = tiling.pair ? 2 * ex::BM : ex::BM;
+  const long long tiles = (p.tokens + static_cast<long long>(rows) - 1) / rows * 2 * ((p.heads + per - 1) / per);
+  if (tiles > 0x3FFFFFFFll) return MLA_ERR_UNSUPPORTED;
+  const int workers = tiling.pair ? sms / 2 : sms;
+  const int grid = static_cast<int>(tiles < workers ? tiles : workers) * (tiling.pair ? 2 : 1);
+  if (tiling.pair)
+    return fp8 ? ex::launch<true, 256, true>(p, tm_k, tm_v, grid, stream)
+               : ex::launch<false, 256, true>(p, tm_k, tm_v, grid, stream);
+  if (tiling.cols == 128)
+    return fp8 ? ex::launch<true, 128, false>(p, tm_k, tm_v, grid, stream)
+               : ex::launch<false, 128, false>(p, tm_k, tm_v, grid, stream);
+  return fp8 ? ex::launch<true, 256, false>(p, tm_k, tm_v, grid, stream)
+             : ex::launch<false, 256, false>(p, tm_k, tm_v, grid, stream);
 }
 
 }  // namespace mla

@@ -109,10 +109,15 @@ struct PrefillParams {
 
 int launch_rope_query(const RopeQueryParams& p, const RopeFreqs& f, cudaStream_t stream);
 int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, cudaStream_t stream);
-// tm_k over w_kc as [heads * 128, 512] (box tile_cols rows x 64), tm_v over
-// w_vc as [heads * 512, 128] (box 64 x 64).
-int expand_tile_cols(int tokens, int heads, int sms);
-int launch_expand(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int tile_cols, int sms,
+// How the expansion is tiled: columns of a tile, and whether CTA pairs share
+// one.  tm_k over w_kc as [heads * 128, 512] (box: the rows that one CTA loads,
+// x 64), tm_v over w_vc as [heads * 512, 128] (box 64 x 64).
+struct ExpandTiling {
+  int cols;
+  bool pair;
+};
+ExpandTiling expand_tiling(int tokens, int heads, int sms);
+int launch_expand(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, ExpandTiling tiling, int sms,
                   bool fp8, cudaStream_t stream);
 // tm_q over q as [rows, heads, 192] (box 128 rows x 64), tm_k and tm_v over
 // [keys, heads, 128] (boxes of 128 and 64 keys x 64), tm_kr over [keys, 64].

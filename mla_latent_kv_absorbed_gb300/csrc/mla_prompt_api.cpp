@@ -210,13 +210,13 @@ int expand(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, i
   p.wide_stores = aligned(k_nope, 32) && aligned(v, 32);
   const int sms = device_sm_count();
   if (sms < 1) return MLA_ERR_CUDA;
-  const int cols = expand_tile_cols(tokens, num_heads, sms);
+  const ExpandTiling tiling = expand_tiling(tokens, num_heads, sms);
   CUtensorMap tm_k, tm_v;
   const int64_t H = num_heads;
-  if (!make_map(&tm_k, w_kc, H * kNope, kLatent, 0, 0, kLatent, cols) ||
+  if (!make_map(&tm_k, w_kc, H * kNope, kLatent, 0, 0, kLatent, tiling.pair ? tiling.cols / 2 : tiling.cols) ||
       !make_map(&tm_v, w_vc, H * kLatent, kNope, 0, 0, kNope, 64))
     return MLA_ERR_CUDA;
-  return launch_expand(p, tm_k, tm_v, cols, sms, fp8, reinterpret_cast<cudaStream_t>(stream));
+  return launch_expand(p, tm_k, tm_v, tiling, sms, fp8, reinterpret_cast<cudaStream_t>(stream));
 }
 }  // namespace
 
