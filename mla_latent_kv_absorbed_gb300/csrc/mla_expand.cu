@@ -13,7 +13,10 @@
 // heads; w_kc is K-major as it lies, w_vc N-major.
 //   warp 0      TMA producer of the weights, 64-deep chunks in a ring
 //   warp 1      TMEM allocator, MMA issuer: two accumulators in turn
-//   warps 4-7   epilogue: a TMEM lane is a row; 32-byte stores
+//   warps 4-7   epilogue: a TMEM lane is a row; 32 rows x 64 columns at a time
+//               through shared memory, stored by TMA (lane by lane, 32 bytes a
+//               row, the stores took as long as two tiles' products: 129 us
+//               at 4096 rows x 128 heads)
 //   warps 8-11  rows: gather, swizzle (128-byte atoms), rope keys
 // kPair: two CTAs of a cluster work on one tile of 256 rows x 256 columns
 // (cta_group::2): each holds its 128 rows and half of the weights' columns,
@@ -30,6 +33,7 @@ namespace ex {
 constexpr int kThreads = 384;
 constexpr int kEpiWarp0 = 4, kRowWarp0 = 8;
 constexpr int BM = 128, BK = 64, kChunks = kLatent / BK;
+constexpr int kSlab = 32 * 128;
 
 template <int NT_, bool kPair>
 struct Cfg {
@@ -39,9 +43,10 @@ struct Cfg {
   static constexpr int kABytes = kChunks * BM * 128;        // 128 KB
   static constexpr int kCols = NT / kCtas;                  // of a tile's columns, those this CTA loads
   static constexpr int kBBytes = kCols * BK * 2;
-  static constexpr int kStages = (96 * 1024) / kBBytes;
+  static constexpr int kStages = (64 * 1024) / kBBytes;
   static constexpr int kOffB = kABytes;
-  static constexpr int kOffBar = kOffB + kStages * kBBytes;
+  static constexpr int kOffOut = kOffB + kStages * kBBytes; // per epilogue warp two slabs of 32 rows x 64 columns
+  static constexpr int kOffBar = kOffOut + 4 * 2 * kSlab;
   // full[S], empty[S], a_full[8], a_free[8], acc_full[2], acc_empty[2]
   static constexpr int kBars = 2 * kStages + 2 * kChunks + 4;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
@@ -98,9 +103,18 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, 
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+// At most one of this thread's committed stores has yet to read its source.
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+
 template <bool kFp8, int NT, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_ko, const __grid_constant__ CUtensorMap tm_vo,
                   const ExpandParams p) {
   using C = Cfg<NT, kPair>;
   extern __shared__ uint8_t smem_raw[];
@@ -331,41 +345,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------- epilogue
     const int q = warp - kEpiWarp0;
     const float scale = kFp8 ? p.kv_scale : 1.f;
-    uint32_t i = 0;
+    uint32_t i = 0, slab = 0;
     for (int t = t0; t < t1; ++t, ++i) {
       const int col = t % cols, h = (col % groups) * C::kHeads;
-      const long long r = static_cast<long long>(t / cols) * tile_rows + rank * BM + 32 * q + lane;
+      const int r0 = (t / cols) * tile_rows + static_cast<int>(rank) * BM + 32 * q;
       const uint32_t buf = i & 1;
       bool ok = true;
       if (lane == 0) ok = mbar_wait(acc_full(buf), (i >> 1) & 1, wc);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      uint16_t* out = (col < groups ? p.k_nope : p.v) + (r * p.heads + h) * kNope;
       const int width = min(NT, (p.heads - h) * kNope);      // an odd last head: half a tile
 #pragma unroll 1
-      for (int c = 0; c < width; c += 32) {
-        uint32_t a[16], b[16];
+      for (int c = 0; c < width; c += 64, ++slab) {
+        uint32_t a[64];
         const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * NT + c;
-        tmem_ld16(src, a);
-        tmem_ld16(src + 16, b);
-        tmem_wait_ld();
-        if (r < p.tokens) {
-          uint32_t w[8], x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            w[e] = pack_bf16x2(__uint_as_float(a[2 * e]) * scale, __uint_as_float(a[2 * e + 1]) * scale);
-            x[e] = pack_bf16x2(__uint_as_float(b[2 * e]) * scale, __uint_as_float(b[2 * e + 1]) * scale);
-          }
-          if (p.wide_stores) {
-            st_global_v8(out + c, w);
-            st_global_v8(out + c + 16, x);
-          } else {
-            st_global_v4(out + c, w[0], w[1], w[2], w[3]);
-            st_global_v4(out + c + 8, w[4], w[5], w[6], w[7]);
-            st_global_v4(out + c + 16, x[0], x[1], x[2], x[3]);
-            st_global_v4(out + c + 24, x[4], x[5], x[6], x[7]);
-          }
+        for (int e = 0; e < 4; ++e) tmem_ld16(src + 16 * e, *reinterpret_cast<uint32_t(*)[16]>(a + 16 * e));
+        tmem_wait_ld();
+        uint8_t* dst = smem + C::kOffOut + (2 * q + (slab & 1)) * kSlab;
+        if (lane == 0) bulk_wait_read1();                    // the store before the last has read its slab
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            w[x] = pack_bf16x2(__uint_as_float(a[8 * e + 2 * x]) * scale, __uint_as_float(a[8 * e + 2 * x + 1]) * scale);
+          *reinterpret_cast<uint4*>(dst + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (r0 < p.tokens)                                 // rows past the last are not written
+            tma_store_3d(col < groups ? &tm_ko : &tm_vo, smem_u32(dst), c & 64, h + (c >> 7), r0);
+          bulk_commit();
         }
       }
       tc_fence_before();
@@ -375,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else mbar_arrive(acc_empty(buf));
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncwarp();
@@ -388,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kFp8, int NT, bool kPair>
-int launch(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int grid, cudaStream_t stream) {
+int launch(const ExpandParams& p, const CUtensorMap (&tm)[4], int grid, cudaStream_t stream) {
   using C = Cfg<NT, kPair>;
   const auto kernel = &expand_kernel<kFp8, NT, kPair>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes)) return MLA_ERR_CUDA;
@@ -406,37 +421,31 @@ int launch(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, p) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, tm[0], tm[1], tm[2], tm[3], p) != cudaSuccess) return MLA_ERR_CUDA;
   return cudaPeekAtLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace ex
 
-// Tiles: 128 rows x 128 columns where two-head tiles would give fewer tiles
-// than SMs (the longest CTA is halved), 256 x 256 on CTA pairs otherwise; 128 x
-// 256 for a single block of rows, whose pair would compute nothing.
+// 256 rows x 256 columns on CTA pairs, or 128 x 128 on single CTAs where the
+// former would leave SMs idle or a pair's second half without rows.
 ExpandTiling expand_tiling(int tokens, int heads, int sms) {
   const long long blocks = (tokens + ex::BM - 1) / ex::BM;
   const long long groups = 2ll * ((heads + 1) / 2);
-  if (blocks * groups < sms) return {128, false};
-  return {256, blocks > 1 && sms > 1};
+  if (blocks < 2 || blocks * groups < sms) return {128, false};
+  return {256, true};
 }
 
-int launch_expand(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, ExpandTiling tiling, int sms,
-                  bool fp8, cudaStream_t stream) {
+int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[4], ExpandTiling tiling, int sms, bool fp8,
+                  cudaStream_t stream) {
   const int per = tiling.cols / kNope, rows = tiling.pair ? 2 * ex::BM : ex::BM;
   const long long tiles = (p.tokens + static_cast<long long>(rows) - 1) / rows * 2 * ((p.heads + per - 1) / per);
   if (tiles > 0x3FFFFFFFll) return MLA_ERR_UNSUPPORTED;
   const int workers = tiling.pair ? sms / 2 : sms;
   const int grid = static_cast<int>(tiles < workers ? tiles : workers) * (tiling.pair ? 2 : 1);
   if (tiling.pair)
-    return fp8 ? ex::launch<true, 256, true>(p, tm_k, tm_v, grid, stream)
-               : ex::launch<false, 256, true>(p, tm_k, tm_v, grid, stream);
-  if (tiling.cols == 128)
-    return fp8 ? ex::launch<true, 128, false>(p, tm_k, tm_v, grid, stream)
-               : ex::launch<false, 128, false>(p, tm_k, tm_v, grid, stream);
-  return fp8 ? ex::launch<true, 256, false>(p, tm_k, tm_v, grid, stream)
-             : ex::launch<false, 256, false>(p, tm_k, tm_v, grid, stream);
+    return fp8 ? ex::launch<true, 256, true>(p, tm, grid, stream) : ex::launch<false, 256, true>(p, tm, grid, stream);
+  return fp8 ? ex::launch<true, 128, false>(p, tm, grid, stream) : ex::launch<false, 128, false>(p, tm, grid, stream);
 }
 
 }  // namespace mla

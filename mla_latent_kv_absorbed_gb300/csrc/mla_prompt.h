@@ -51,15 +51,10 @@ struct RopeAppendParams {
 struct ExpandParams {
   const uint8_t* kv_cache;    // [num_slots, 576] bf16 or E4M3
   const int32_t* kv_indices;  // [tokens]
-  const uint16_t* w_kc;       // [heads, 128, 512]
-  const uint16_t* w_vc;       // [heads, 512, 128]
-  uint16_t* k_nope;           // [tokens, heads, 128]
   uint16_t* k_rope;           // [tokens, 64]
-  uint16_t* v;                // [tokens, heads, 128]
   int* status;                // status word, or null
   long long num_slots;
   int tokens, heads;
-  int wide_stores;            // k_nope and v are 32-byte aligned
   float kv_scale;             // FP8 cache only
 };
 
@@ -110,15 +105,15 @@ struct PrefillParams {
 int launch_rope_query(const RopeQueryParams& p, const RopeFreqs& f, cudaStream_t stream);
 int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, cudaStream_t stream);
 // How the expansion is tiled: columns of a tile, and whether CTA pairs share
-// one.  tm_k over w_kc as [heads * 128, 512] (box: the rows that one CTA loads,
-// x 64), tm_v over w_vc as [heads * 512, 128] (box 64 x 64).
+// one.  Maps: w_kc as [heads * 128, 512] (box: 128 rows x 64), w_vc as [heads *
+// 512, 128] (box 64 x 64), k_nope and v as [tokens, heads, 128] (box 32 rows x 64).
 struct ExpandTiling {
   int cols;
   bool pair;
 };
 ExpandTiling expand_tiling(int tokens, int heads, int sms);
-int launch_expand(const ExpandParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, ExpandTiling tiling, int sms,
-                  bool fp8, cudaStream_t stream);
+int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[4], ExpandTiling tiling, int sms, bool fp8,
+                  cudaStream_t stream);
 // tm_q over q as [rows, heads, 192] (box 128 rows x 64), tm_k and tm_v over
 // [keys, heads, 128] (boxes of 128 and 64 keys x 64), tm_kr over [keys, 64].
 int launch_prefill(const PrefillParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_kr,

@@ -197,26 +197,22 @@ int expand(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, i
   ExpandParams p{};
   p.kv_cache = static_cast<const uint8_t*>(kv_cache);
   p.kv_indices = kv_indices;
-  p.w_kc = static_cast<const uint16_t*>(w_kc);
-  p.w_vc = static_cast<const uint16_t*>(w_vc);
-  p.k_nope = static_cast<uint16_t*>(k_nope);
   p.k_rope = static_cast<uint16_t*>(k_rope);
-  p.v = static_cast<uint16_t*>(v);
   p.status = static_cast<int*>(workspace);
   p.num_slots = num_slots;
   p.tokens = tokens;
   p.heads = num_heads;
   p.kv_scale = kv_scale;
-  p.wide_stores = aligned(k_nope, 32) && aligned(v, 32);
   const int sms = device_sm_count();
   if (sms < 1) return MLA_ERR_CUDA;
-  const ExpandTiling tiling = expand_tiling(tokens, num_heads, sms);
-  CUtensorMap tm_k, tm_v;
   const int64_t H = num_heads;
-  if (!make_map(&tm_k, w_kc, H * kNope, kLatent, 0, 0, kLatent, tiling.pair ? tiling.cols / 2 : tiling.cols) ||
-      !make_map(&tm_v, w_vc, H * kLatent, kNope, 0, 0, kNope, 64))
+  CUtensorMap tm[4];
+  if (!make_map(&tm[0], w_kc, H * kNope, kLatent, 0, 0, kLatent, 128) ||
+      !make_map(&tm[1], w_vc, H * kLatent, kNope, 0, 0, kNope, 64) ||
+      !make_map(&tm[2], k_nope, tokens, H * kNope, H, kNope, kNope, 32) ||
+      !make_map(&tm[3], v, tokens, H * kNope, H, kNope, kNope, 32))
     return MLA_ERR_CUDA;
-  return launch_expand(p, tm_k, tm_v, tiling, sms, fp8, reinterpret_cast<cudaStream_t>(stream));
+  return launch_expand(p, tm, expand_tiling(tokens, num_heads, sms), sms, fp8, reinterpret_cast<cudaStream_t>(stream));
 }
 }  // namespace
 
