@@ -13,16 +13,18 @@
 // heads; w_kc is K-major as it lies, w_vc N-major.
 //   warp 0      TMA producer of the weights, 64-deep chunks in a ring
 //   warp 1      TMEM allocator, MMA issuer: two accumulators in turn
-//   warps 4-7   epilogue: a TMEM lane is a row; 32 rows x 64 columns at a time
-//               through shared memory, stored by TMA (lane by lane, 32 bytes a
-//               row, the stores took as long as two tiles' products: 129 us
-//               at 4096 rows x 128 heads)
-//   warps 8-11  rows: gather, swizzle (128-byte atoms), rope keys
+//   warps 4-11  epilogue: a TMEM lane is a row; 32 rows x 32 columns at a time
+//               through shared memory, stored by TMA; two warps share a lane
+//               quadrant and take half of the columns each (four warps needed
+//               6500 cycles a tile, the products 4100)
+//   warps 12-15 rows: gather, swizzle (128-byte atoms), rope keys
 // kPair: two CTAs of a cluster work on one tile of 256 rows x 256 columns
 // (cta_group::2): each holds its 128 rows and half of the weights' columns,
 // CTA 0 issues for both.  That halves the weights that every SM reads from L2,
 // which bounded the single-CTA form (1.07 GB in 134 us at 4096 rows x 128
 // heads).
+#include <type_traits>
+
 #include "mla_device.cuh"
 #include "mla_launch.h"
 #include "mla_prompt.h"
@@ -30,10 +32,10 @@
 namespace mla {
 namespace ex {
 
-constexpr int kThreads = 384;
-constexpr int kEpiWarp0 = 4, kRowWarp0 = 8;
+constexpr int kThreads = 512;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kRowWarp0 = 12;
 constexpr int BM = 128, BK = 64, kChunks = kLatent / BK;
-constexpr int kSlab = 32 * 128;
+constexpr int kSlab = 32 * 64;
 
 template <int NT_, bool kPair>
 struct Cfg {
@@ -43,10 +45,10 @@ struct Cfg {
   static constexpr int kABytes = kChunks * BM * 128;        // 128 KB
   static constexpr int kCols = NT / kCtas;                  // of a tile's columns, those this CTA loads
   static constexpr int kBBytes = kCols * BK * 2;
-  static constexpr int kStages = (64 * 1024) / kBBytes;
+  static constexpr int kStages = (80 * 1024) / kBBytes;
   static constexpr int kOffB = kABytes;
-  static constexpr int kOffOut = kOffB + kStages * kBBytes; // per epilogue warp two slabs of 32 rows x 64 columns
-  static constexpr int kOffBar = kOffOut + 4 * 2 * kSlab;
+  static constexpr int kOffOut = kOffB + kStages * kBBytes; // per epilogue warp a slab of 32 rows x 32 columns
+  static constexpr int kOffBar = kOffOut + kEpiWarps * kSlab;
   // full[S], empty[S], a_full[8], a_free[8], acc_full[2], acc_empty[2]
   static constexpr int kBars = 2 * kStages + 2 * kChunks + 4;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
@@ -103,13 +105,31 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, 
       : "memory");
 }
 
-__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
-               "r"(src), "r"(x), "r"(y), "r"(z)
-               : "memory");
+__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int x, int y, int z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(map),
+      "r"(src), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
 }
-// At most one of this thread's committed stores has yet to read its source.
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N of this thread's committed groups have landed.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Arrive on the barrier at this offset in CTA 0, ordering nothing: what it
+// tells (a TMEM read has come back) is already in registers.  With release
+// semantics at cluster scope it waited for the stores before it, about 4800
+// cycles a tile.
+__device__ __forceinline__ void mbar_arrive_leader_relaxed(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b32 rb;\n\t"
+      "mapa.shared::cluster.u32 rb, %0, 0;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [rb];\n\t}" ::"r"(bar)
+      : "memory");
+}
 
 template <bool kFp8, int NT, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -146,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
     for (int k = 0; k < kChunks; ++k) { mbar_init(a_full(k), 4 * C::kCtas); mbar_init(a_free(k), 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), 4 * C::kCtas); }
+    for (int i = 0; i < 2; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), kEpiWarps * C::kCtas); }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -229,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kChunks; ++k, ++c) {
           const uint32_t s = c % C::kStages;
           if (fresh && !mbar_wait<kPair>(a_full(k), block & 1, wc)) { ok = false; break; }
-          if (!mbar_wait<kPair>(full(s), (c / C::kStages) & 1, wc)) { ok = false; break; }
+          if (!mbar_wait(full(s), (c / C::kStages) & 1, wc)) { ok = false; break; }
           tc_fence_after();
           const uint64_t da = sdesc(base + k * (BM * 128), 16, 1024);
           if (key) {
@@ -275,51 +295,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (oob) record_status(p.status, MLA_ERR_INDEX_OOB);
       bool ok = true;
-      constexpr int kStep = kFp8 ? 2 : 1;                    // chunks that 16 bytes a lane cover
-      auto load = [&](int k, uint4 (&v)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] = __ldg(reinterpret_cast<const uint4*>(p.kv_cache + row[i] + k * (kFp8 ? 64 : 128)) + sub);
+      // chunk k's place is free once the block before has used it
+      auto wait_free = [&](int k) {
+        if (block == 0) return;
+        bool f = true;
+        if (lane == 0) f = mbar_wait(a_free(k), (block - 1) & 1, wc);
+        ok = __shfl_sync(0xffffffffu, f, 0) && ok;
       };
-      uint4 next[8];
-      load(0, next);
-#pragma unroll 1
-      for (int k = 0; k < kChunks; k += kStep) {
-        uint4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = next[i];
-        if (k + kStep < kChunks) load(k + kStep, next);
-        if (block > 0) {
-          for (int j = 0; j < kStep && ok; ++j) {
-            if (lane == 0) ok = mbar_wait(a_free(k + j), (block - 1) & 1, wc);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-          }
-          if (!ok) break;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 16 * i + (rt >> 3);
-          if constexpr (kFp8) {
-            // 16 codes: pieces 2 (sub & 3) and + 1 of chunk k + sub / 4
-            uint8_t* dst = smem + (k + (sub >> 2)) * (BM * 128) + r * 128;
-            const int c = 2 * (sub & 3);
-            *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) << 4)) =
-                make_uint4(e4m3x2_to_bf16x2(v[i].x), e4m3x2_to_bf16x2(v[i].x >> 16), e4m3x2_to_bf16x2(v[i].y),
-                           e4m3x2_to_bf16x2(v[i].y >> 16));
-            *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (r & 7)) << 4)) =
-                make_uint4(e4m3x2_to_bf16x2(v[i].z), e4m3x2_to_bf16x2(v[i].z >> 16), e4m3x2_to_bf16x2(v[i].w),
-                           e4m3x2_to_bf16x2(v[i].w >> 16));
-          } else {
-            *reinterpret_cast<uint4*>(smem + k * (BM * 128) + r * 128 + ((sub ^ (r & 7)) << 4)) = v[i];
-          }
-        }
+      auto landed = [&](int k) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0)
-          for (int j = 0; j < kStep; ++j) {
-            if constexpr (kPair) mbar_arrive_cluster(a_full(k + j), 0);
-            else mbar_arrive(a_full(k + j));
+        if (lane == 0) {
+          if constexpr (kPair) mbar_arrive_cluster(a_full(k), 0);
+          else mbar_arrive(a_full(k));
+        }
+      };
+      if constexpr (kFp8) {
+        // 16 codes a lane are two pieces of chunk k + sub / 4: two chunks at a time, two of those in flight
+        uint4 v[2][8];
+        auto load = [&](int k, uint4 (&x)[8]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(p.kv_cache + row[i] + k * 64) + sub);
+        };
+        load(0, v[0]);
+        load(2, v[1]);
+#pragma unroll
+        for (int g = 0; g < kChunks / 2; ++g) {
+          wait_free(2 * g);
+          wait_free(2 * g + 1);
+          if (!ok) break;
+          uint4 (&x)[8] = v[g & 1];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 16 * i + (rt >> 3), c = 2 * (sub & 3);
+            uint8_t* dst = smem + (2 * g + (sub >> 2)) * (BM * 128) + r * 128;
+            *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) << 4)) =
+                make_uint4(e4m3x2_to_bf16x2(x[i].x), e4m3x2_to_bf16x2(x[i].x >> 16), e4m3x2_to_bf16x2(x[i].y),
+                           e4m3x2_to_bf16x2(x[i].y >> 16));
+            *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (r & 7)) << 4)) =
+                make_uint4(e4m3x2_to_bf16x2(x[i].z), e4m3x2_to_bf16x2(x[i].z >> 16), e4m3x2_to_bf16x2(x[i].w),
+                           e4m3x2_to_bf16x2(x[i].w >> 16));
           }
+          if (g + 2 < kChunks / 2) load(2 * g + 4, x);
+          landed(2 * g);
+          landed(2 * g + 1);
+        }
+      } else {
+        auto load = [&](int k) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 16 * i + (rt >> 3);
+            cp_async16(base + k * (BM * 128) + r * 128 + ((sub ^ (r & 7)) << 4), p.kv_cache + row[i] + k * 128 + sub * 16);
+          }
+        };
+        // four chunks on their way; the first block's all at once, as it has nothing to wait for
+        auto run = [&](auto lag) {
+          constexpr int kLag = decltype(lag)::value;
+#pragma unroll
+          for (int k = 0; k < kChunks + kLag; ++k) {
+            if (k < kChunks && ok) wait_free(k);
+            if (k < kChunks && ok) load(k);
+            cp_async_commit();                               // empty groups keep the count
+            if (k >= kLag) {
+              cp_async_wait<kLag>();
+              if (ok) landed(k - kLag);
+            }
+          }
+        };
+        if (block == 0) run(std::integral_constant<int, kChunks - 1>{});
+        else run(std::integral_constant<int, 3>{});
       }
       if (!ok) break;
       if (t % cols == 0) {                                   // the CTA with the block's first tile writes its rope keys
@@ -343,9 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------- epilogue
-    const int q = warp - kEpiWarp0;
+    const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const float scale = kFp8 ? p.kv_scale : 1.f;
-    uint32_t i = 0, slab = 0;
+    // the output streams through L2; the weights, read by every block of rows, should stay
+    const uint64_t policy = l2_policy_evict_first();
+    uint8_t* slab = smem + C::kOffOut + (warp - kEpiWarp0) * kSlab;
+    uint32_t i = 0;
     for (int t = t0; t < t1; ++t, ++i) {
       const int col = t % cols, h = (col % groups) * C::kHeads;
       const int r0 = (t / cols) * tile_rows + static_cast<int>(rank) * BM + 32 * q;
@@ -355,37 +402,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      const int width = min(NT, (p.heads - h) * kNope);      // an odd last head: half a tile
+      const int end = min((half + 1) * (NT / 2), (p.heads - h) * kNope);   // an odd last head: half a tile
 #pragma unroll 1
-      for (int c = 0; c < width; c += 64, ++slab) {
-        uint32_t a[64];
+      for (int c = half * (NT / 2); c < end; c += 32) {
+        uint32_t a[16], b[16];
         const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * NT + c;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tmem_ld16(src + 16 * e, *reinterpret_cast<uint32_t(*)[16]>(a + 16 * e));
+        tmem_ld16(src, a);
+        tmem_ld16(src + 16, b);
         tmem_wait_ld();
-        uint8_t* dst = smem + C::kOffOut + (2 * q + (slab & 1)) * kSlab;
-        if (lane == 0) bulk_wait_read1();                    // the store before the last has read its slab
+        if (lane == 0) bulk_wait_read();                     // the store before has read the slab
         __syncwarp();
+        // rows of 64 bytes, their 16-byte pieces in the order of the 64-byte swizzle
+        auto put = [&](const uint32_t (&x)[16], int e) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          uint32_t w[4];
+          for (int y = 0; y < 2; ++y) {
+            uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = pack_bf16x2(__uint_as_float(a[8 * e + 2 * x]) * scale, __uint_as_float(a[8 * e + 2 * x + 1]) * scale);
-          *reinterpret_cast<uint4*>(dst + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+            for (int z = 0; z < 4; ++z)
+              w[z] = pack_bf16x2(__uint_as_float(x[8 * y + 2 * z]) * scale, __uint_as_float(x[8 * y + 2 * z + 1]) * scale);
+            *reinterpret_cast<uint4*>(slab + lane * 64 + (((e + y) ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        };
+        put(a, 0);
+        put(b, 2);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           if (r0 < p.tokens)                                 // rows past the last are not written
-            tma_store_3d(col < groups ? &tm_ko : &tm_vo, smem_u32(dst), c & 64, h + (c >> 7), r0);
+            tma_store_3d(col < groups ? &tm_ko : &tm_vo, smem_u32(slab), c & 127, h + (c >> 7), r0, policy);
           bulk_commit();
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (kPair) mbar_arrive_cluster(acc_empty(buf), 0);
+        if constexpr (kPair) mbar_arrive_leader_relaxed(acc_empty(buf));
         else mbar_arrive(acc_empty(buf));
       }
     }

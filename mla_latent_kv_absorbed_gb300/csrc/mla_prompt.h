@@ -106,7 +106,7 @@ int launch_rope_query(const RopeQueryParams& p, const RopeFreqs& f, cudaStream_t
 int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, cudaStream_t stream);
 // How the expansion is tiled: columns of a tile, and whether CTA pairs share
 // one.  Maps: w_kc as [heads * 128, 512] (box: 128 rows x 64), w_vc as [heads *
-// 512, 128] (box 64 x 64), k_nope and v as [tokens, heads, 128] (box 32 rows x 64).
+// 512, 128] (box 64 x 64), k_nope and v as [tokens, heads, 128] (box 32 rows x 32).
 struct ExpandTiling {
   int cols;
   bool pair;
