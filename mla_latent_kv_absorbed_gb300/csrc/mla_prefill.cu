@@ -115,6 +115,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // After a wait has given up: the same bounded wait, blind to the abort flag,
 // for copies and products that are still in flight.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
@@ -249,7 +259,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kIssuer) {
     // ----------------------------------------------------------- MMA issuer
-    if (lane == 0 && n > 0) {
+    // The whole warp runs the loop and one elected lane issues: loop counters
+    // and descriptors are then uniform to the compiler, which keeps them in
+    // uniform registers.
+    if (n > 0) {
+      const bool lead = elect_one();
       const uint32_t idesc_s = idesc_bf16(128, 128, false, false) | (p.negate ? 1u << 13 : 0u);   // -Q
       constexpr uint32_t kIdescO = idesc_bf16(128, 128, false, true);
       auto D = [](uint64_t d, uint32_t off) -> uint64_t { return d + (off >> 4); };
@@ -263,10 +277,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint64_t da = sdesc(base + kOffQ + (3 * w + i) * kBlock, 16, 1024);
           const uint64_t db = sdesc(base + kOffK + s * kBlock, 16, 1024);
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_ss(d, D(da, 32 * k), D(db, 32 * k), idesc_s, (i | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k) umma_ss(d, D(da, 32 * k), D(db, 32 * k), idesc_s, (i | k) != 0 ? 1u : 0u);
+          }
         }
-        umma_commit(bar(bSFull + w));
+        if (lead) umma_commit(bar(bSFull + w));
       };
       auto pv = [&](int t, int w) {
         const uint32_t a = tmem + kTmemS + 128 * w, d = tmem + kTmemO + 128 * w;
@@ -279,11 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t < whole && !mbar_wait(bar(bVFull + s), (c / kVSlots) & 1, wc)) { ok = false; return; }
           tc_fence_after();
           const uint64_t db = sdesc(base + kOffV + s * kBlock, kBlock / 2, 1024);
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_ts(d, a + 32 * i + 8 * k, D(db, 2048 * k), kIdescO, t > 0 || (i | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              umma_ts(d, a + 32 * i + 8 * k, D(db, 2048 * k), kIdescO, t > 0 || (i | k) != 0 ? 1u : 0u);
+          }
         }
-        umma_commit(bar(bPvDone + w));
+        if (lead) umma_commit(bar(bPvDone + w));
       };
       if (n_a > 0) {
         ok = mbar_wait(bar(bQFull), 0, wc);
@@ -293,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait(bar(bQFull + 1), 0, wc);
         if (ok) qk(0, 1);
       }
-      if (ok) umma_commit(bar(bKFree));
+      if (ok && lead) umma_commit(bar(bKFree));
       for (int t = 0; t < n && ok; ++t) {
         for (int w = 0; w < 2 && ok; ++w) {
           const int nw = w ? n_b : n_a;
@@ -304,10 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && t + 1 < nw) qk(t + 1, w);
         }
         if (!ok) break;
-        umma_commit(bar(bVFree + (t & 1)));
-        if (t + 1 < n) umma_commit(bar(bKFree + ((t + 1) & 1)));
+        if (lead) {
+          umma_commit(bar(bVFree + (t & 1)));
+          if (t + 1 < n) umma_commit(bar(bKFree + ((t + 1) & 1)));
+        }
       }
-      umma_commit(bar(bDrain));
+      if (lead) umma_commit(bar(bDrain));
       drain_wait(bar(bDrain), 0);              // every MMA has finished before TMEM is given back
     }
     __syncwarp();
