@@ -65,6 +65,16 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) return;
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
   const float2 f = e4m3x2_value(codes);
   return pack_bf16x2(f.x, f.y);                             // exact
@@ -226,7 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
-    if (lane == 0 && rank == 0) {
+    // The whole warp runs the loop and one elected lane issues: loop counters
+    // and descriptors are then uniform to the compiler, which keeps them in
+    // uniform registers.
+    if (rank == 0) {
+      const bool lead = elect_one();
       auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
         if constexpr (kPair) umma_ss2(d, a, b, idesc, acc);
         else umma_ss(d, a, b, idesc, acc);
@@ -256,22 +270,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t db = sdesc(base + C::kOffB + s * C::kBBytes, 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
-              mma(d, D(da, ks * 32), D(db, ks * 32), C::kIdescK, (k | ks) != 0 ? 1u : 0u);
+              if (lead) mma(d, D(da, ks * 32), D(db, ks * 32), C::kIdescK, (k | ks) != 0 ? 1u : 0u);
           } else {
             const uint64_t db = sdesc(base + C::kOffB + s * C::kBBytes, BK * 128, 1024);
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
-              mma(d, D(da, ks * 32), D(db, ks * 2048), C::kIdescV, (k | ks) != 0 ? 1u : 0u);
+              if (lead) mma(d, D(da, ks * 32), D(db, ks * 2048), C::kIdescV, (k | ks) != 0 ? 1u : 0u);
           }
-          commit(empty(s));
-          if (last) commit(a_free(k));
+          if (lead) {
+            commit(empty(s));
+            if (last) commit(a_free(k));
+          }
         }
         if (!ok) break;
-        commit(acc_full(buf));
+        if (lead) commit(acc_full(buf));
         if (last) ++block;
       }
       if (!ok) {                                             // products in flight end before TMEM is given back
-        commit(acc_full(i & 1));
+        if (lead) commit(acc_full(i & 1));
         drain_wait(acc_full(i & 1), (i >> 1) & 1);
       }
     }

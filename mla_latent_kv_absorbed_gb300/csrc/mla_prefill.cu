@@ -33,17 +33,18 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kProducer = 8, kIssuer = 9, kGuard = 10;
-constexpr int kKSlots = 5, kVSlots = 3;               // 16 KB each: a key tile takes 3 slots, its values 2
+constexpr int kSlots = 8;                             // of 16 KB: 5 a tile in turn, 3 of keys, 2 of values
 constexpr int kBlock = 16384;
 constexpr int kOffQ = 0;                              // 2 row tiles x 3 blocks of 128 rows x 64 dims
-constexpr int kOffK = 6 * kBlock;                     // ring of 128 keys x 64 dims
-constexpr int kOffV = kOffK + kKSlots * kBlock;       // ring of 64 keys x 128 dims (two 64-dim chunks)
-constexpr int kOffBar = kOffV + kVSlots * kBlock;
+// The ring, in the order of use: keys of tile t as blocks 5t .. 5t+2 (128 keys
+// x 64 dims), its values as 5t+3, 5t+4 (64 keys x 128 dims, two 64-dim chunks).
+constexpr int kOffRing = 6 * kBlock;
+constexpr int kOffBar = kOffRing + kSlots * kBlock;
 enum Bar : int {
   bQFull = 0,                    // [2]
-  bKFull = bQFull + 2,           // [5] per slot
-  bVFull = bKFull + kKSlots,     // [3] per slot (tiles that every row sees whole)
-  bKFree = bVFull + kVSlots,     // [2] key tile t on t & 1: its QK products are done
+  bKFull = bQFull + 2,           // [2] key tile t on t & 1
+  bVFull = bKFull + 2,           // [2] its values (tiles that every row sees whole)
+  bKFree = bVFull + 2,           // [2] key tile t on t & 1: its QK products are done
   bVFree = bKFree + 2,           // [2]
   bSFull = bVFree + 2,           // [2] per row tile
   bPFull = bSFull + 2,           // [2]
@@ -206,35 +207,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(base + kOffQ + (3 * w + i) * kBlock, &tm_q, 64 * i, h, it.q0 + 128 * w, bar(bQFull + w));
       };
       bool ok = true;
-      int k_armed = 0, v_armed = 0;                           // blocks on their way or landed
+      int k_armed = 0, v_armed = 0;                           // tiles on their way or landed
+      // the place of block c, once the block before in it (c - 8) has been used
+      auto place = [&](int c) -> uint32_t {
+        if (c >= kSlots) {
+          const int u = (c - kSlots) / 5;
+          const int b = (c - kSlots) % 5 < 3 ? bKFree : bVFree;
+          ok = mbar_wait(bar(b + (u & 1)), (u >> 1) & 1, wc);
+        }
+        return base + kOffRing + (c % kSlots) * kBlock;
+      };
       auto load_k = [&](int t) {
         for (int i = 0; i < 3 && ok; ++i) {
-          const int c = 3 * t + i;
-          if (c >= kKSlots) {                                 // the slot's last tile: t - 2, or t - 1 for i = 2
-            const int u = (c - kKSlots) / 3;
-            if (!mbar_wait(bar(bKFree + (u & 1)), (u >> 1) & 1, wc)) { ok = false; break; }
-          }
-          const int s = c % kKSlots;
-          const uint32_t dst = base + kOffK + s * kBlock, b = bar(bKFull + s);
-          mbar_arrive_expect_tx(b, kBlock);
-          k_armed = c + 1;
+          const uint32_t dst = place(5 * t + i), b = bar(bKFull + (t & 1));
+          if (!ok) break;
+          if (i == 0) mbar_arrive_expect_tx(b, 3 * kBlock);
+          k_armed = t + 1;
           if (i < 2) tma_load_3d(dst, &tm_k, 64 * i, h, it.k0 + t * kPfKeys, b);
           else tma_load_2d(dst, &tm_kr, 0, it.k0 + t * kPfKeys, b);
         }
       };
       auto load_v = [&](int t) {
         for (int i = 0; i < 2 && ok; ++i) {
-          const int c = 2 * t + i;
-          if (c >= kVSlots) {
-            const int u = (c - kVSlots) / 2;
-            if (!mbar_wait(bar(bVFree + (u & 1)), (u >> 1) & 1, wc)) { ok = false; break; }
-          }
-          const int s = c % kVSlots;
-          const uint32_t dst = base + kOffV + s * kBlock;
-          const uint32_t b = t < whole ? bar(bVFull + s) : bar(bVMasked + t - whole);
-          v_armed = c + 1;
-          if (t < whole) mbar_arrive_expect_tx(b, kBlock);
-          else if (i == 0) mbar_arrive_expect_tx(b, 2 * kBlock);
+          const uint32_t dst = place(5 * t + 3 + i);
+          if (!ok) break;
+          const uint32_t b = t < whole ? bar(bVFull + (t & 1)) : bar(bVMasked + t - whole);
+          v_armed = t + 1;
+          if (i == 0) mbar_arrive_expect_tx(b, 2 * kBlock);
           for (int k = 0; k < 2; ++k)
             tma_load_3d(dst + k * (kBlock / 2), &tm_v, 64 * k, h, it.k0 + t * kPfKeys + 64 * i, b);
         }
@@ -249,11 +248,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {                                              // no copy outlives the block
         if (n_a > 0) drain_wait(bar(bQFull), 0);
         if (n_b > 0) drain_wait(bar(bQFull + 1), 0);
-        for (int c = max(0, k_armed - kKSlots); c < k_armed; ++c)
-          drain_wait(bar(bKFull + c % kKSlots), (c / kKSlots) & 1);
-        for (int c = max(0, v_armed - kVSlots); c < v_armed; ++c)
-          if (c / 2 < whole) drain_wait(bar(bVFull + c % kVSlots), (c / kVSlots) & 1);
-          else if (c & 1) drain_wait(bar(bVMasked + c / 2 - whole), 0);
+        for (int t = max(0, k_armed - 2); t < k_armed; ++t) drain_wait(bar(bKFull + (t & 1)), (t >> 1) & 1);
+        for (int t = max(0, v_armed - 2); t < v_armed; ++t)
+          drain_wait(t < whole ? bar(bVFull + (t & 1)) : bar(bVMasked + t - whole), t < whole ? (t >> 1) & 1 : 0);
       }
     }
     __syncwarp();
@@ -268,15 +265,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdescO = idesc_bf16(128, 128, false, true);
       auto D = [](uint64_t d, uint32_t off) -> uint64_t { return d + (off >> 4); };
       bool ok = true;
+      auto block_at = [&](int c) -> uint32_t { return base + kOffRing + (c % kSlots) * kBlock; };
       // scores of key tile t for row tile w
       auto qk = [&](int t, int w) {
         const uint32_t d = tmem + kTmemS + 128 * w;
+#pragma unroll
         for (int i = 0; i < 3; ++i) {
-          const int c = 3 * t + i, s = c % kKSlots;
-          if (!mbar_wait(bar(bKFull + s), (c / kKSlots) & 1, wc)) { ok = false; return; }
-          tc_fence_after();
           const uint64_t da = sdesc(base + kOffQ + (3 * w + i) * kBlock, 16, 1024);
-          const uint64_t db = sdesc(base + kOffK + s * kBlock, 16, 1024);
+          const uint64_t db = sdesc(block_at(5 * t + i), 16, 1024);
           if (lead) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) umma_ss(d, D(da, 32 * k), D(db, 32 * k), idesc_s, (i | k) != 0 ? 1u : 0u);
@@ -286,15 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto pv = [&](int t, int w) {
         const uint32_t a = tmem + kTmemS + 128 * w, d = tmem + kTmemO + 128 * w;
-        if (t >= whole && (!mbar_wait(bar(bVMasked + t - whole), 0, wc) || !mbar_wait(bar(bVClean + t - whole), 0, wc))) {
-          ok = false;
-          return;
-        }
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int c = 2 * t + i, s = c % kVSlots;
-          if (t < whole && !mbar_wait(bar(bVFull + s), (c / kVSlots) & 1, wc)) { ok = false; return; }
-          tc_fence_after();
-          const uint64_t db = sdesc(base + kOffV + s * kBlock, kBlock / 2, 1024);
+          const uint64_t db = sdesc(block_at(5 * t + 3 + i), kBlock / 2, 1024);
           if (lead) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -303,26 +293,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lead) umma_commit(bar(bPvDone + w));
       };
-      if (n_a > 0) {
-        ok = mbar_wait(bar(bQFull), 0, wc);
-        if (ok) qk(0, 0);
-      }
+      // a tile's keys and values are waited for once, before row tile A's products (B's when A has none left)
+      auto wait_k = [&](int t) { return mbar_wait(bar(bKFull + (t & 1)), (t >> 1) & 1, wc); };
+      auto wait_v = [&](int t) {
+        if (t < whole) return mbar_wait(bar(bVFull + (t & 1)), (t >> 1) & 1, wc);
+        return mbar_wait(bar(bVMasked + t - whole), 0, wc) && mbar_wait(bar(bVClean + t - whole), 0, wc);
+      };
+      ok = (n_a == 0 || mbar_wait(bar(bQFull), 0, wc)) && wait_k(0);
+      tc_fence_after();
+      if (ok && n_a > 0) qk(0, 0);
       if (ok && n_b > 0) {
         ok = mbar_wait(bar(bQFull + 1), 0, wc);
+        tc_fence_after();
         if (ok) qk(0, 1);
       }
       if (ok && lead) umma_commit(bar(bKFree));
       for (int t = 0; t < n && ok; ++t) {
+        bool have_v = false, have_k = false;
         for (int w = 0; w < 2 && ok; ++w) {
           const int nw = w ? n_b : n_a;
           if (t >= nw) continue;
-          if (!mbar_wait(bar(bPFull + w), t & 1, wc)) { ok = false; break; }
+          if (!have_v) ok = wait_v(t);
+          have_v = true;
+          ok = ok && mbar_wait(bar(bPFull + w), t & 1, wc);
+          if (!ok) break;
           tc_fence_after();
           pv(t, w);
-          if (ok && t + 1 < nw) qk(t + 1, w);
+          if (t + 1 >= nw) continue;
+          if (!have_k) ok = wait_k(t + 1);
+          have_k = true;
+          tc_fence_after();
+          if (ok) qk(t + 1, w);
         }
-        if (!ok) break;
-        if (lead) {
+        if (ok && lead) {
           umma_commit(bar(bVFree + (t & 1)));
           if (t + 1 < n) umma_commit(bar(bKFree + ((t + 1) & 1)));
         }
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = whole; t < n; ++t) {
       const int j = t - whole;
       if (!warp_wait(bar(bVMasked + j), 0, wc, lane)) break;
-      uint8_t* half = smem + kOffV + ((2 * t + g) % kVSlots) * kBlock;
+      uint8_t* half = smem + kOffRing + ((5 * t + 3 + g) % kSlots) * kBlock;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int r = 32 * m + lane;                          // key 64 g + r of the tile
