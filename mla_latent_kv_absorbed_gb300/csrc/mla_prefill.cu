@@ -4,10 +4,12 @@
 // j up to the causal limit of row i (the sequences' ends aligned), in one pass
 // over the keys with the running maximum and sum.
 //
-// One CTA takes one item (up to 256 query rows, their keys) for one head: two
-// row tiles A and B of 128, each with its scores and its output in TMEM (4 x
-// 128 columns: all of it), so that one tile's softmax runs while the tensor
-// core works for the other.  Key tiles of 128:
+// One CTA an SM works through items (up to 256 query rows, their keys) for one
+// head each, taken from a counter in the plan's order (heaviest first): two row
+// tiles A and B of 128, each with its scores and its output in TMEM (4 x 128
+// columns: all of it), so that one tile's softmax runs while the tensor core
+// works for the other.  The next item's loads and first scores overlap the
+// item's last product and epilogue.  Key tiles of 128:
 //   S = Q K^T       M = 128, N = 128, 12 steps of K = 16 (128 + 64 dims), both
 //                   operands from shared memory
 //   P = exp2(..)    in registers, one row a thread; written back as bf16 over
@@ -19,11 +21,14 @@
 // bits at any magnitude, sums are fp32), and O is rescaled in TMEM only then.
 //
 // Warps: 0-3 softmax and epilogue of tile A, 4-7 of tile B, 8 TMA producer, 9
-// MMA issuer, 10-11 the guard.  A tile that some row sees only in part is
+// MMA issuer, 10 the guard.  A tile that some row sees only in part is
 // masked by index in the softmax, but a zero weight times a value that is not
 // finite is NaN in the matrix product: the guard clears those values (and the
 // rows behind the last key) in shared memory before the product reads them,
 // notes the keys, and the epilogue adds them to the rows that do see them.
+#include <algorithm>
+#include <type_traits>
+
 #include "mla_device.cuh"
 #include "mla_launch.h"
 #include "mla_prompt.h"
@@ -31,7 +36,10 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 384;
+using TileA = std::integral_constant<int, 0>;
+using TileB = std::integral_constant<int, 1>;
+
+constexpr int kThreads = 352;                         // 184 registers a thread: a row's 128 scores stay in them
 constexpr int kProducer = 8, kIssuer = 9, kGuard = 10;
 constexpr int kSlots = 8;                             // of 16 KB: 5 a tile in turn, 3 of keys, 2 of values
 constexpr int kBlock = 16384;
@@ -40,29 +48,37 @@ constexpr int kOffQ = 0;                              // 2 row tiles x 3 blocks 
 // x 64 dims), its values as 5t+3, 5t+4 (64 keys x 128 dims, two 64-dim chunks).
 constexpr int kOffRing = 6 * kBlock;
 constexpr int kOffBar = kOffRing + kSlots * kBlock;
+constexpr int kSched = 4;                             // items announced ahead
+constexpr int kMasked = 8;                            // masked tiles told apart: two items' worth and more
+constexpr int kConsumers = 8 + 1 + 1;                 // warps that read an announced item
 enum Bar : int {
-  bQFull = 0,                    // [2]
-  bKFull = bQFull + 2,           // [2] key tile t on t & 1
-  bVFull = bKFull + 2,           // [2] its values (tiles that every row sees whole)
-  bKFree = bVFull + 2,           // [2] key tile t on t & 1: its QK products are done
+  bQFull = 0,                    // [2] per row tile
+  bQFree = bQFull + 2,           // the item's last scores are done
+  bKFull = bQFree + 1,           // [2] key tile T on T & 1, T counting the CTA's tiles over all items
+  bVFull = bKFull + 2,           // [2] the values of whole tile U (that every row sees whole) on U & 1
+  bKFree = bVFull + 2,           // [2] its QK products are done
   bVFree = bKFree + 2,           // [2]
   bSFull = bVFree + 2,           // [2] per row tile
   bPFull = bSFull + 2,           // [2]
   bPvDone = bPFull + 2,          // [2]
-  bVMasked = bPvDone + 2,        // [3] the values of the item's masked tiles have landed
-  bVClean = bVMasked + 3,        // [3] and the guard has been over them
-  bDrain = bVClean + 3,
+  bVMasked = bPvDone + 2,         // [8] the values of masked tile M (on M & 7) have landed
+  bVClean = bVMasked + kMasked,  // [8] and the guard has been over them
+  bSched = bVClean + kMasked,    // [4] an item has been announced
+  bSchedFree = bSched + kSched,  // [4] and read by every warp
+  bDrain = bSchedFree + kSched,
   kBars
 };
-constexpr int kOffMisc = kOffBar + 8 * kBars;         // TMEM address, abort flag, then the guard's key masks
-constexpr int kOffBad = kOffMisc + 16;                // [3][4] words: bit j = key j of the masked tile
-constexpr int kSmemBytes = kOffBad + 48 + 1024;
+constexpr int kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16;   // TMEM address, abort flag
+constexpr int kOffBad = kOffMisc + 16;                // [8][4] words: bit j = key j of masked tile M
+constexpr int kOffSched = kOffBad + 16 * kMasked;     // [4] announced items, 8 words each
+constexpr int kSmemBytes = kOffSched + 32 * kSched + 1024;
+static_assert(kOffSched % 16 == 0, "announced items are read as 16-byte words");
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;          // S_A, S_B, O_A, O_B: 128 columns each
 constexpr float kSlack = 8.f;                         // log2 growth of the maximum that moves the reference
 
 struct Item {
-  int q0, nq, k0, nk, off, part;
+  int q0, nq, k0, nk, off, part, h;
 };
 
 // The item's words, or false (and MLA_ERR_PLAN_MISMATCH) when it does not lie
@@ -70,11 +86,28 @@ struct Item {
 __device__ __forceinline__ bool load_item(const PrefillParams& p, int i, Item& it) {
   const int4 a = __ldg(reinterpret_cast<const int4*>(p.items) + 2 * i);
   const int4 b = __ldg(reinterpret_cast<const int4*>(p.items) + 2 * i + 1);
-  it = Item{a.y, a.z, a.w, b.x, b.y, b.z};
+  it = Item{a.y, a.z, a.w, b.x, b.y, b.z, 0};
   return it.q0 >= 0 && it.nq >= 1 && it.nq <= kPfRows && it.q0 <= p.q_tokens - it.nq && it.k0 >= 0 && it.nk >= 0 &&
          it.k0 <= p.kv_tokens - it.nk && it.part >= -1 && it.part < p.partials && it.off >= -kPfNoLimit &&
          it.off <= kPfNoLimit && (it.nk == 0 || it.nk <= it.off + it.nq);
 }
+
+// What an item asks of each row tile.
+struct Shape {
+  int n_a, n_b, n;             // key tiles that some row of A, of B, of either sees
+  int whole;                   // the first of them are seen whole by every row; at most three follow
+  __device__ __forceinline__ explicit Shape(const Item& it) {
+    auto tiles = [&](int w) -> int {
+      if (it.nq <= 128 * w) return 0;
+      const int last = min(it.nk, it.off + min(it.nq, 128 * w + 128));    // keys that the tile's last row sees
+      return last > 0 ? (last + kPfKeys - 1) / kPfKeys : 0;
+    };
+    n_a = tiles(0);
+    n_b = tiles(1);
+    n = max(n_a, n_b);
+    whole = min(n, min(max(it.off + 1, 0), it.nk) / kPfKeys);
+  }
+};
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
@@ -85,7 +118,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
 }
 
 // 32 lanes x 32 consecutive columns.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
       "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -96,16 +129,40 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
+// The products with their shared-memory descriptors in halves: the upper word
+// (strides, layout) is a constant, only the lower one (address, leading stride)
+// changes from MMA to MMA.
+template <uint32_t kHigh>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kHigh)
       : "memory");
 }
+template <uint32_t kHigh>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kHigh)
+      : "memory");
+}
+// The words of sdesc(addr, lbo, 1024) for 128-byte-swizzled atoms.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | kLayoutSw128 << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return addr >> 4 | (lbo >> 4) << 16; }
 
 __device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7F80u) == 0x7F80u; }
 
@@ -113,7 +170,9 @@ __device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bi
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& wc, int lane) {
   bool ok = true;
   if (lane == 0) ok = mbar_wait(bar, parity, wc);
-  return __shfl_sync(0xffffffffu, ok, 0);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok;
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -147,14 +206,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + kOffBad);
+  int* sched = reinterpret_cast<int*>(smem + kOffSched);
   const WaitCtx wc{abort_flag, p.status};
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i >= bPFull && i < bPFull + 2 ? 4 : i >= bVClean && i < bVClean + 3 ? 2 : 1);
+    for (int i = 0; i < kBars; ++i) {
+      const bool four = i >= bPFull && i < bPFull + 2;
+      const bool all = i >= bSchedFree && i < bSchedFree + kSched;
+      mbar_init(bar(i), four ? 4 : all ? kConsumers : 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x < 12) bad[threadIdx.x] = 0;
   if (warp == kIssuer) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -172,215 +235,288 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  // blocks are numbered group of heads by group, items (heaviest first) within it, heads innermost
-  int h, item;
-  {
-    const int per_group = p.n_items * p.head_group;
-    const int g = blockIdx.x / per_group, rest = blockIdx.x - g * per_group;
-    const int in_group = min(p.head_group, p.heads - g * p.head_group);
-    item = rest / in_group;
-    h = g * p.head_group + rest - item * in_group;
-  }
-  Item it;
-  bool good = load_item(p, item, it);
-  if (!good) {
-    if (threadIdx.x == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
-    it.nk = it.nq = 0;
-  }
-  // key tiles of each row tile, and the first that some row sees only in part
-  auto tiles_of = [&](int w) -> int {
-    if (it.nq <= 128 * w) return 0;
-    const int last = min(it.nk, it.off + min(it.nq, 128 * w + 128));    // keys that the tile's last row sees
-    return last > 0 ? (last + kPfKeys - 1) / kPfKeys : 0;
+  // The k-th item announced to this CTA, for every consumer warp: false when there is none left (or on an abort).
+  auto announced = [&](uint32_t k, Item& it) -> bool {
+    volatile const int* w = sched + 8 * (k % kSched);
+    it = Item{w[0], w[1], w[2], w[3], w[4], w[5], w[6]};
+    return w[7] != 0;
   };
-  const int n_a = tiles_of(0), n_b = tiles_of(1);
-  const int n = max(n_a, n_b);
-  const int whole = min(max(it.off + 1, 0), it.nk) / kPfKeys;           // tiles that every row sees whole
-  // (whole <= n, and at most three tiles follow: nk <= off + 256)
+  auto release_item = [&](uint32_t k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(bSchedFree + k % kSched));
+  };
+  auto next_item = [&](uint32_t k, Item& it) -> bool {
+    if (!warp_wait(bar(bSched + k % kSched), (k / kSched) & 1, wc, lane)) return false;
+    const bool there = announced(k, it);
+    release_item(k);
+    return there;
+  };
 
   if (warp == kProducer) {
-    // ------------------------------------------------------------- producer
-    if (lane == 0 && n > 0) {
-      auto load_q = [&](int w) {
-        mbar_arrive_expect_tx(bar(bQFull + w), 3 * kBlock);
-        for (int i = 0; i < 3; ++i)
-          tma_load_3d(base + kOffQ + (3 * w + i) * kBlock, &tm_q, 64 * i, h, it.q0 + 128 * w, bar(bQFull + w));
-      };
+    // ------------------------------------------------ producer and scheduler
+    if (lane == 0) {
+      const int total = p.n_items * p.heads;
       bool ok = true;
-      int k_armed = 0, v_armed = 0;                           // tiles on their way or landed
-      // the place of block c, once the block before in it (c - 8) has been used
-      auto place = [&](int c) -> uint32_t {
-        if (c >= kSlots) {
-          const int u = (c - kSlots) / 5;
-          const int b = (c - kSlots) % 5 < 3 ? bKFree : bVFree;
-          ok = mbar_wait(bar(b + (u & 1)), (u >> 1) & 1, wc);
+      // block `w` of the launch: items are numbered group of heads by group, heaviest first within it, heads innermost
+      auto fetch = [&](int w, Item& it) {
+        const int per_group = p.n_items * p.head_group;
+        const int g = w / per_group, rest = w - g * per_group;
+        const int in_group = min(p.head_group, p.heads - g * p.head_group);
+        const int item = rest / in_group;
+        if (!load_item(p, item, it)) {
+          record_status(p.status, MLA_ERR_PLAN_MISMATCH);
+          it.nk = it.nq = 0;
         }
-        return base + kOffRing + (c % kSlots) * kBlock;
+        it.h = g * p.head_group + rest - item * in_group;
       };
-      auto load_k = [&](int t) {
-        for (int i = 0; i < 3 && ok; ++i) {
-          const uint32_t dst = place(5 * t + i), b = bar(bKFull + (t & 1));
-          if (!ok) break;
-          if (i == 0) mbar_arrive_expect_tx(b, 3 * kBlock);
-          k_armed = t + 1;
-          if (i < 2) tma_load_3d(dst, &tm_k, 64 * i, h, it.k0 + t * kPfKeys, b);
-          else tma_load_2d(dst, &tm_kr, 0, it.k0 + t * kPfKeys, b);
+      auto announce = [&](uint32_t k, const Item& it, bool there) {
+        const int s = k % kSched;
+        if (k >= kSched && !mbar_wait(bar(bSchedFree + s), ((k / kSched) - 1) & 1, wc)) { ok = false; return; }
+        reinterpret_cast<int4*>(sched)[2 * s] = make_int4(it.q0, it.nq, it.k0, it.nk);
+        reinterpret_cast<int4*>(sched)[2 * s + 1] = make_int4(it.off, it.part, it.h, there ? 1 : 0);
+        mbar_arrive(bar(bSched + s));
+      };
+      int tbase = 0, ubase = 0, mbase = 0;                    // tiles before this item: all, whole, masked
+      uint32_t q_items[2] = {0, 0}, busy = 0;                 // items with queries in the row tile, in either
+      int k_armed = 0, q_bar[2] = {-1, -1};                   // what may be in flight: key tiles, query tiles,
+      int v_new = -1, v_old = -1;                             // the last two tiles' values (barrier * 2 + parity)
+      Item it;
+      fetch(blockIdx.x, it);
+      announce(0, it, true);
+      for (uint32_t k = 0; ok; ++k) {
+        const Shape sh(it);
+        auto load_q = [&](auto W) {
+          constexpr int w = W.value;
+          q_bar[w] = q_items[w] & 1;
+          ++q_items[w];
+          mbar_arrive_expect_tx(bar(bQFull + w), 3 * kBlock);
+          for (int i = 0; i < 3; ++i)
+            tma_load_3d(base + kOffQ + (3 * w + i) * kBlock, &tm_q, 64 * i, it.h, it.q0 + 128 * w, bar(bQFull + w));
+        };
+        // the place of block c, once the block before in it (c - 8) has been used
+        auto place = [&](int c) -> uint32_t {
+          if (c >= kSlots) {
+            const int u = (c - kSlots) / 5;
+            const int b = (c - kSlots) % 5 < 3 ? bKFree : bVFree;
+            ok = mbar_wait(bar(b + (u & 1)), (u >> 1) & 1, wc);
+          }
+          return base + kOffRing + (c % kSlots) * kBlock;
+        };
+        auto load_k = [&](int t) {
+          const int T = tbase + t;
+          for (int i = 0; i < 3 && ok; ++i) {
+            const uint32_t dst = place(5 * T + i), b = bar(bKFull + (T & 1));
+            if (!ok) break;
+            if (i == 0) mbar_arrive_expect_tx(b, 3 * kBlock);
+            k_armed = T + 1;
+            if (i < 2) tma_load_3d(dst, &tm_k, 64 * i, it.h, it.k0 + t * kPfKeys, b);
+            else tma_load_2d(dst, &tm_kr, 0, it.k0 + t * kPfKeys, b);
+          }
+        };
+        auto load_v = [&](int t) {
+          const int T = tbase + t, U = ubase + t, M = mbase + t - sh.whole;
+          for (int i = 0; i < 2 && ok; ++i) {
+            const uint32_t dst = place(5 * T + 3 + i);
+            if (!ok) break;
+            const int b = t < sh.whole ? bVFull + (U & 1) : bVMasked + M % kMasked;
+            if (i == 0) {
+              v_old = v_new;
+              v_new = 2 * b + (t < sh.whole ? (U >> 1) & 1 : (M / kMasked) & 1);
+            }
+            if (i == 0) mbar_arrive_expect_tx(bar(b), 2 * kBlock);
+            for (int x = 0; x < 2; ++x)
+              tma_load_3d(dst + x * (kBlock / 2), &tm_v, 64 * x, it.h, it.k0 + t * kPfKeys + 64 * i, bar(b));
+          }
+        };
+        Item next{};
+        bool more = false;
+        auto look_ahead = [&] {
+          const int w = atomicAdd(p.status + kWsCounter, 1) + static_cast<int>(gridDim.x);
+          more = w < total;
+          if (more) fetch(w, next);
+          announce(k + 1, next, more);
+        };
+        if (sh.n > 0 && busy++ > 0) ok = mbar_wait(bar(bQFree), (busy - 2) & 1, wc);   // the item before's queries
+        if (ok && sh.n_a > 0) load_q(TileA{});
+        if (ok && sh.n > 0) load_k(0);
+        if (ok && sh.n_b > 0) load_q(TileB{});
+        if (ok && sh.n > 0) load_v(0);
+        if (ok) look_ahead();                                 // the ring is full: its latency costs nothing here
+        for (int t = 1; t < sh.n && ok; ++t) {
+          load_k(t);
+          if (ok) load_v(t);
         }
-      };
-      auto load_v = [&](int t) {
-        for (int i = 0; i < 2 && ok; ++i) {
-          const uint32_t dst = place(5 * t + 3 + i);
-          if (!ok) break;
-          const uint32_t b = t < whole ? bar(bVFull + (t & 1)) : bar(bVMasked + t - whole);
-          v_armed = t + 1;
-          if (i == 0) mbar_arrive_expect_tx(b, 2 * kBlock);
-          for (int k = 0; k < 2; ++k)
-            tma_load_3d(dst + k * (kBlock / 2), &tm_v, 64 * k, h, it.k0 + t * kPfKeys + 64 * i, b);
-        }
-      };
-      if (n_a > 0) load_q(0);
-      load_k(0);
-      if (n_b > 0) load_q(1);
-      for (int t = 0; t < n && ok; ++t) {
-        load_v(t);
-        if (ok && t + 1 < n) load_k(t + 1);
+        tbase += sh.n;
+        ubase += sh.whole;
+        mbase += sh.n - sh.whole;
+        if (!more) break;
+        it = next;
       }
       if (!ok) {                                              // no copy outlives the block
-        if (n_a > 0) drain_wait(bar(bQFull), 0);
-        if (n_b > 0) drain_wait(bar(bQFull + 1), 0);
-        for (int t = max(0, k_armed - 2); t < k_armed; ++t) drain_wait(bar(bKFull + (t & 1)), (t >> 1) & 1);
-        for (int t = max(0, v_armed - 2); t < v_armed; ++t)
-          drain_wait(t < whole ? bar(bVFull + (t & 1)) : bar(bVMasked + t - whole), t < whole ? (t >> 1) & 1 : 0);
+        if (q_bar[0] >= 0) drain_wait(bar(bQFull), q_bar[0]);
+        if (q_bar[1] >= 0) drain_wait(bar(bQFull + 1), q_bar[1]);
+        for (int T = max(0, k_armed - 2); T < k_armed; ++T) drain_wait(bar(bKFull + (T & 1)), (T >> 1) & 1);
+        if (v_old >= 0) drain_wait(bar(v_old >> 1), v_old & 1);
+        if (v_new >= 0) drain_wait(bar(v_new >> 1), v_new & 1);
       }
     }
     __syncwarp();
   } else if (warp == kIssuer) {
     // ----------------------------------------------------------- MMA issuer
-    // The whole warp runs the loop and one elected lane issues: loop counters
-    // and descriptors are then uniform to the compiler, which keeps them in
-    // uniform registers.
-    if (n > 0) {
-      const bool lead = elect_one();
-      const uint32_t idesc_s = idesc_bf16(128, 128, false, false) | (p.negate ? 1u << 13 : 0u);   // -Q
-      constexpr uint32_t kIdescO = idesc_bf16(128, 128, false, true);
-      auto D = [](uint64_t d, uint32_t off) -> uint64_t { return d + (off >> 4); };
-      bool ok = true;
-      auto block_at = [&](int c) -> uint32_t { return base + kOffRing + (c % kSlots) * kBlock; };
-      // scores of key tile t for row tile w
-      auto qk = [&](int t, int w) {
-        const uint32_t d = tmem + kTmemS + 128 * w;
+    // The whole warp runs the loop and one elected lane issues.  Everything the
+    // loop depends on is made uniform for the compiler (votes of waits,
+    // reductions of the item's words), which then keeps counters and
+    // descriptors in uniform registers: an MMA is issued in 64 cycles, not 115.
+    auto uwait = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, wc)); };
+    auto uniform = [](int x) -> int { return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(x))); };
+    auto shape_of = [&](const Item& it) {
+      Shape sh(it);
+      sh.n_a = uniform(sh.n_a);
+      sh.n_b = uniform(sh.n_b);
+      sh.n = uniform(sh.n);
+      sh.whole = uniform(sh.whole);
+      return sh;
+    };
+    const bool lead = elect_one();
+    const uint32_t idesc_s = idesc_bf16(128, 128, false, false) | (p.negate ? 1u << 13 : 0u);   // -Q
+    constexpr uint32_t kIdescO = idesc_bf16(128, 128, false, true);
+    auto block_at = [&](int c) -> uint32_t { return base + kOffRing + (c % kSlots) * kBlock; };
+    // scores of key tile T for row tile w
+    auto qk = [&](int T, int w) {
+      const uint32_t d = tmem + kTmemS + 128 * w;
+      const uint32_t a = desc_low(base + kOffQ + 3 * w * kBlock, 16);
+      const uint32_t b0 = desc_low(block_at(5 * T), 16), b1 = desc_low(block_at(5 * T + 1), 16),
+                     b2 = desc_low(block_at(5 * T + 2), 16);
+      if (lead) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const uint64_t da = sdesc(base + kOffQ + (3 * w + i) * kBlock, 16, 1024);
-          const uint64_t db = sdesc(block_at(5 * t + i), 16, 1024);
-          if (lead) {
+        for (int k = 0; k < 12; ++k)
+          mma_ss<kDescHigh>(d, a + (k >> 2) * (kBlock >> 4) + 2 * (k & 3), (k < 4 ? b0 : k < 8 ? b1 : b2) + 2 * (k & 3),
+                            idesc_s, k > 0);
+        umma_commit(bar(bSFull + w));
+      }
+    };
+    auto pv = [&](int T, int w, bool first) {
+      const uint32_t a = tmem + kTmemS + 128 * w, d = tmem + kTmemO + 128 * w;
+      const uint32_t b0 = desc_low(block_at(5 * T + 3), kBlock / 2), b1 = desc_low(block_at(5 * T + 4), kBlock / 2);
+      if (lead) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) umma_ss(d, D(da, 32 * k), D(db, 32 * k), idesc_s, (i | k) != 0 ? 1u : 0u);
-          }
-        }
-        if (lead) umma_commit(bar(bSFull + w));
-      };
-      auto pv = [&](int t, int w) {
-        const uint32_t a = tmem + kTmemS + 128 * w, d = tmem + kTmemO + 128 * w;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint64_t db = sdesc(block_at(5 * t + 3 + i), kBlock / 2, 1024);
-          if (lead) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_ts(d, a + 32 * i + 8 * k, D(db, 2048 * k), kIdescO, t > 0 || (i | k) != 0 ? 1u : 0u);
-          }
-        }
-        if (lead) umma_commit(bar(bPvDone + w));
-      };
-      // a tile's keys and values are waited for once, before row tile A's products (B's when A has none left)
-      auto wait_k = [&](int t) { return mbar_wait(bar(bKFull + (t & 1)), (t >> 1) & 1, wc); };
-      auto wait_v = [&](int t) {
-        if (t < whole) return mbar_wait(bar(bVFull + (t & 1)), (t >> 1) & 1, wc);
-        return mbar_wait(bar(bVMasked + t - whole), 0, wc) && mbar_wait(bar(bVClean + t - whole), 0, wc);
-      };
-      ok = (n_a == 0 || mbar_wait(bar(bQFull), 0, wc)) && wait_k(0);
+        for (int k = 0; k < 8; ++k)
+          mma_ts<kDescHigh>(d, a + 8 * k, (k < 4 ? b0 : b1) + 128 * (k & 3), kIdescO, !first || k > 0);
+        umma_commit(bar(bPvDone + w));
+      }
+    };
+    auto wait_k = [&](int T) { return uwait(bKFull + (T & 1), (T >> 1) & 1); };
+    int tbase = 0, ubase = 0, mbase = 0;
+    uint32_t items_a = 0, items_b = 0, steps_a = 0, steps_b = 0;   // per row tile: items begun, P tiles taken
+    bool ok = true;
+    Item it;
+    // A wait that gives up makes `ok` false; what is issued until the check at the end of the tile stays inside
+    // shared memory and TMEM.
+    for (uint32_t k = 0; ok && __all_sync(0xffffffffu, next_item(k, it)); ++k) {
+      const Shape sh = shape_of(it);
+      if (sh.n == 0) continue;
+      // the first scores: they may run while the epilogue of the item before reads its output
+      if (sh.n_a > 0) ok = uwait(bQFull, items_a++ & 1);
+      ok &= wait_k(tbase);
       tc_fence_after();
-      if (ok && n_a > 0) qk(0, 0);
-      if (ok && n_b > 0) {
-        ok = mbar_wait(bar(bQFull + 1), 0, wc);
+      if (sh.n_a > 0) qk(tbase, 0);
+      if (sh.n_b > 0) {
+        ok &= uwait(bQFull + 1, items_b++ & 1);
         tc_fence_after();
-        if (ok) qk(0, 1);
+        qk(tbase, 1);
       }
-      if (ok && lead) umma_commit(bar(bKFree));
-      for (int t = 0; t < n && ok; ++t) {
-        bool have_v = false, have_k = false;
-        for (int w = 0; w < 2 && ok; ++w) {
-          const int nw = w ? n_b : n_a;
-          if (t >= nw) continue;
-          if (!have_v) ok = wait_v(t);
-          have_v = true;
-          ok = ok && mbar_wait(bar(bPFull + w), t & 1, wc);
-          if (!ok) break;
+      if (lead) {
+        umma_commit(bar(bKFree + (tbase & 1)));
+        if (sh.n == 1) umma_commit(bar(bQFree));
+      }
+      for (int t = 0; t < sh.n && ok; ++t) {
+        const int T = tbase + t, U = ubase + t, M = mbase + t - sh.whole;
+        ok &= t < sh.whole ? uwait(bVFull + (U & 1), (U >> 1) & 1)
+                           : uwait(bVClean + M % kMasked, (M / kMasked) & 1);
+        // P of an item's first tile also tells that its warps have read the output of the item before
+        if (t < sh.n_a) {
+          ok &= uwait(bPFull, steps_a++ & 1);
           tc_fence_after();
-          pv(t, w);
-          if (t + 1 >= nw) continue;
-          if (!have_k) ok = wait_k(t + 1);
-          have_k = true;
-          tc_fence_after();
-          if (ok) qk(t + 1, w);
+          pv(T, 0, t == 0);
         }
-        if (ok && lead) {
-          umma_commit(bar(bVFree + (t & 1)));
-          if (t + 1 < n) umma_commit(bar(bKFree + ((t + 1) & 1)));
+        if (t + 1 < sh.n) {
+          ok &= wait_k(T + 1);
+          tc_fence_after();
+        }
+        if (t + 1 < sh.n_a) qk(T + 1, 0);
+        if (t < sh.n_b) {
+          ok &= uwait(bPFull + 1, steps_b++ & 1);
+          tc_fence_after();
+          pv(T, 1, t == 0);
+        }
+        if (t + 1 < sh.n_b) qk(T + 1, 1);
+        if (lead) {
+          umma_commit(bar(bVFree + (T & 1)));
+          if (t + 1 < sh.n) umma_commit(bar(bKFree + ((T + 1) & 1)));
+          if (t + 2 == sh.n) umma_commit(bar(bQFree));
         }
       }
-      if (lead) umma_commit(bar(bDrain));
-      drain_wait(bar(bDrain), 0);              // every MMA has finished before TMEM is given back
+      tbase += sh.n;
+      ubase += sh.whole;
+      mbase += sh.n - sh.whole;
     }
+    if (lead) umma_commit(bar(bDrain));
+    drain_wait(bar(bDrain), 0);                               // every MMA has finished before TMEM is given back
     __syncwarp();
   } else if (warp >= kGuard) {
     // ---------------------------------------------------------------- guard
-    const int g = warp - kGuard;                              // which half of a tile's keys
-    for (int t = whole; t < n; ++t) {
-      const int j = t - whole;
-      if (!warp_wait(bar(bVMasked + j), 0, wc, lane)) break;
-      uint8_t* half = smem + kOffRing + ((5 * t + 3 + g) % kSlots) * kBlock;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int r = 32 * m + lane;                          // key 64 g + r of the tile
-        const bool there = t * kPfKeys + 64 * g + r < it.nk;
-        // x * 0 is NaN exactly where x is not finite
-        __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
-        const __nv_bfloat162 zero = acc;
-        for (int c = 0; c < 16; ++c) {
-          // chunks of 16 bytes in an order that keeps the lanes of a quarter warp on different banks
-          uint4* q = reinterpret_cast<uint4*>(half + (c >> 3) * (kBlock / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-          if (there) {
-            uint4 v = *q;
-            const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc = __hfma2(b[e], zero, acc);
-          } else {
-            *q = make_uint4(0, 0, 0, 0);
-          }
-        }
-        const float2 sum = __bfloat1622float2(acc);
-        const bool found = sum.x != 0.f || sum.y != 0.f;      // NaN compares unequal
-        const uint32_t mask = __ballot_sync(0xffffffffu, found);
-        if (found) {
+    int tbase = 0, M = 0;
+    Item it;
+    bool ok = true;
+    for (uint32_t k = 0; ok && next_item(k, it); ++k) {
+      const Shape sh(it);
+      for (int t = sh.whole; t < sh.n; ++t, ++M) {
+        ok = warp_wait(bar(bVMasked + M % kMasked), (M / kMasked) & 1, wc, lane);
+        if (!ok) break;
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+          uint8_t* half = smem + kOffRing + ((5 * (tbase + t) + 3 + (m >> 1)) % kSlots) * kBlock;
+          const int r = 32 * (m & 1) + lane;                  // row of this half's 64: key 32 m + lane of the tile
+          const bool there = t * kPfKeys + 32 * m + lane < it.nk;
+          // x * 0 is NaN exactly where x is not finite
+          __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
+          const __nv_bfloat162 zero = acc;
+#pragma unroll 4
           for (int c = 0; c < 16; ++c) {
-            uint4* q = reinterpret_cast<uint4*>(half + (c >> 3) * (kBlock / 2) + r * 128 + ((c & 7) << 4));
-            uint4 v = *q;
-            uint32_t* b = reinterpret_cast<uint32_t*>(&v);
+            // chunks of 16 bytes in an order that keeps the lanes of a quarter warp on different banks
+            uint4* q = reinterpret_cast<uint4*>(half + (c >> 3) * (kBlock / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            if (there) {
+              uint4 v = *q;
+              const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (not_finite(b[e])) b[e] &= 0xFFFF0000u;
-              if (not_finite(b[e] >> 16)) b[e] &= 0x0000FFFFu;
+              for (int e = 0; e < 4; ++e) acc = __hfma2(b[e], zero, acc);
+            } else {
+              *q = make_uint4(0, 0, 0, 0);
             }
-            *q = v;
           }
+          const float2 sum = __bfloat1622float2(acc);
+          const bool found = sum.x != 0.f || sum.y != 0.f;    // NaN compares unequal
+          const uint32_t mask = __ballot_sync(0xffffffffu, found);
+          if (found) {
+            for (int c = 0; c < 16; ++c) {
+              uint4* q = reinterpret_cast<uint4*>(half + (c >> 3) * (kBlock / 2) + r * 128 + ((c & 7) << 4));
+              uint4 v = *q;
+              uint32_t* b = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (not_finite(b[e])) b[e] &= 0xFFFF0000u;
+                if (not_finite(b[e] >> 16)) b[e] &= 0x0000FFFFu;
+              }
+              *q = v;
+            }
+          }
+          if (lane == 0) bad[4 * (M % kMasked) + m] = mask;
         }
-        if (lane == 0) bad[4 * j + 2 * g + m] = mask;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bVClean + M % kMasked));
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(bVClean + j));
+      tbase += sh.n;
     }
   } else {
     // -------------------------------------------------- softmax and epilogue
@@ -388,142 +524,180 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = 128 * w + 32 * (warp & 3) + lane;         // row of the item
     const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + kTmemS + 128 * w + quad, to = tmem + kTmemO + 128 * w + quad;
-    const int nw = w ? n_b : n_a;
-    const int seen = min(it.nk, it.off + row + 1);            // keys that this row sees (<= 0: none)
-    const int first_masked = min(max(it.off + 128 * w + 1, 0), it.nk) / kPfKeys;   // of this row tile
-    float ref = -INFINITY, sum = 0.f;
+    uint32_t step = 0;                                        // key tiles of this row tile, over all items
+    int mbase = 0;
     bool ok = true;
-    for (int t = 0; t < nw; ++t) {
-      ok = warp_wait(bar(bSFull + w), t & 1, wc, lane);
+    for (uint32_t k = 0; ok; ++k) {
+      ok = warp_wait(bar(bSched + k % kSched), (k / kSched) & 1, wc, lane);
       if (!ok) break;
-      tc_fence_after();
-      uint32_t s[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
-      tmem_wait_ld();
-      if (t >= first_masked) {
-        const int left = seen - t * kPfKeys;
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= left) s[c] = 0xFF800000u;
+      // The item's words are read here for the loop over the keys and again for the epilogue: 128 scores and
+      // what the loop needs fill the registers, and spills would pass through the shared memory's bandwidth,
+      // which the products need.
+      int nw, seen, first_masked;
+      {
+        Item it;
+        if (!announced(k, it)) {
+          release_item(k);
+          break;
+        }
+        const Shape sh(it);
+        nw = w ? sh.n_b : sh.n_a;
+        seen = min(it.nk, it.off + row + 1);                  // keys that this row sees (<= 0: none)
+        first_masked = min(max(it.off + 128 * w + 1, 0), it.nk) / kPfKeys;   // of this row tile
       }
-      float m0 = __uint_as_float(s[0]), m1 = __uint_as_float(s[1]), m2 = __uint_as_float(s[2]),
-            m3 = __uint_as_float(s[3]);
-#pragma unroll
-      for (int c = 4; c < 124; c += 8) {
-        m0 = max3(m0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        m1 = max3(m1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-        m2 = max3(m2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
-        m3 = max3(m3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
-      }
-      m0 = max3(m0, __uint_as_float(s[124]), __uint_as_float(s[125]));
-      m1 = max3(m1, __uint_as_float(s[126]), __uint_as_float(s[127]));
-      const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
-      const bool move = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
-      if (t == 0) {
-        if (move) ref = top;
-      } else if (__any_sync(0xffffffffu, move)) {
-        // the product before this one has finished: O is this warp's to rescale
-        ok = warp_wait(bar(bPvDone + w), (t - 1) & 1, wc, lane);
+      float ref = -INFINITY, sum = 0.f;
+      for (int t = 0; t < nw; ++t, ++step) {
+        ok = warp_wait(bar(bSFull + w), step & 1, wc, lane);
         if (!ok) break;
         tc_fence_after();
-        const float f = move ? (ref == -INFINITY ? 0.f : ex2_approx(ref - top)) : 1.f;
-        if (move) ref = top;
-        sum *= f;
+        uint32_t s[4][32];
+        auto load_scores = [&] {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t o[16];
-          tmem_ld16(to + 16 * c, o);
+          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
           tmem_wait_ld();
+          if (t >= first_masked) {
+            const int left = seen - t * kPfKeys;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tmem_st16(to + 16 * c, o);
+            for (int c = 0; c < 128; ++c)
+              if (c >= left) s[c / 32][c % 32] = 0xFF800000u;
+          }
+        };
+        load_scores();
+        float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            m0 = max3(m0, __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+            m1 = max3(m1, __uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3]));
+            m2 = max3(m2, __uint_as_float(s[c][e + 4]), __uint_as_float(s[c][e + 5]));
+            m3 = max3(m3, __uint_as_float(s[c][e + 6]), __uint_as_float(s[c][e + 7]));
+          }
+        const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
+        const bool move = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
+        if (t == 0) {
+          if (move) ref = top;
+        } else if (__any_sync(0xffffffffu, move)) {
+          // the product before this one has finished: O is this warp's to rescale
+          ok = warp_wait(bar(bPvDone + w), (step - 1) & 1, wc, lane);
+          if (!ok) break;
+          tc_fence_after();
+          const float f = move ? (ref == -INFINITY ? 0.f : ex2_approx(ref - top)) : 1.f;
+          if (move) ref = top;
+          sum *= f;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            uint32_t o[8];
+            tmem_ld8(to + 8 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st8(to + 8 * c, o);
+          }
+          load_scores();                                      // again: held over the rescaling they would be spilled
         }
-      }
-      const float sub = ref == -INFINITY ? 0.f : -ref;
-      const float2 sc = make_float2(p.scale_log2, p.scale_log2), sb = make_float2(sub, sub);
-      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+        const float sub = ref == -INFINITY ? 0.f : -ref;
+        const float2 sc = make_float2(p.scale_log2, p.scale_log2), sb = make_float2(sub, sub);
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w32[32];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float2 x = f2_fma(make_float2(__uint_as_float(s[64 * c + 2 * e]), __uint_as_float(s[64 * c + 2 * e + 1])), sc, sb);
-          const float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-          if (e & 1) acc1 = f2_add(acc1, y);
-          else acc0 = f2_add(acc0, y);
-          w32[e] = pack_bf16x2(y.x, y.y);
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = f2_fma(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), sc, sb);
+            const float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            if (e & 1) acc1 = f2_add(acc1, y);
+            else acc0 = f2_add(acc0, y);
+            pk[e] = pack_bf16x2(y.x, y.y);
+          }
+          tmem_st16(ts + 16 * c, pk);
         }
-        tmem_st32(ts + 32 * c, w32);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bPFull + w));
+        sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(bPFull + w));
-      sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
-    }
-    if (ok && nw > 0) {
-      ok = warp_wait(bar(bPvDone + w), (nw - 1) & 1, wc, lane);
-      tc_fence_after();
-      for (int t = whole; t < nw && ok; ++t) ok = warp_wait(bar(bVClean + t - whole), 0, wc, lane);
-    }
-    if (ok && 128 * w < it.nq) {                              // the whole warp: tcgen05.ld is collective
-      const bool any = nw > 0 && !(sum == 0.f);
-      const float inv = any ? 1.f / sum : 0.f;
-      const float lse = any ? (ref + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-      const bool live = row < it.nq;
-      const size_t out_row = static_cast<size_t>(it.q0 + row) * p.heads + h;
-      const size_t part_row = (static_cast<size_t>(max(it.part, 0)) * p.heads + h) * kPfRows + row;
-      if (live) {
-        if (it.part >= 0) p.part_lse[part_row] = lse;
-        else if (p.lse) p.lse[out_row] = lse;
+      if (ok && nw > 0) {
+        ok = warp_wait(bar(bPvDone + w), (step - 1) & 1, wc, lane);
+        tc_fence_after();
       }
-      uint32_t dirty = 0;
-      for (int i = 0; i < 12; ++i) dirty |= bad[i];
+      Item it;
+      announced(k, it);
+      release_item(k);
+      const Shape sh(it);
+      uint32_t dirty = 0;                                     // some masked tile of this row tile had its values cleared
+      for (int t = sh.whole; t < nw && ok; ++t) {
+        const int M = mbase + t - sh.whole;
+        ok = warp_wait(bar(bVClean + M % kMasked), (M / kMasked) & 1, wc, lane);
+        for (int i = 0; i < 4; ++i) dirty |= bad[4 * (M % kMasked) + i];
+      }
+      if (ok && 128 * w < it.nq) {                            // the whole warp: tcgen05.ld is collective
+        const bool any = nw > 0 && !(sum == 0.f);
+        const float inv = any ? 1.f / sum : 0.f;
+        const float lse = any ? (ref + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        const bool live = row < it.nq;
+        const size_t out_row = static_cast<size_t>(it.q0 + row) * p.heads + it.h;
+        const size_t part_row = (static_cast<size_t>(max(it.part, 0)) * p.heads + it.h) * kPfRows + row;
+        if (live) {
+          if (it.part >= 0) p.part_lse[part_row] = lse;
+          else if (p.lse) p.lse[out_row] = lse;
+        }
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t o[32];
-        if (nw > 0) {
-          tmem_ld32(to + c, o);
-          tmem_wait_ld();
-        }
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t o[32];
+          if (nw > 0) {
+            tmem_ld32(to + c, o);
+            tmem_wait_ld();
+          }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-        if (!live) continue;
-        if (dirty) {
-          // values that the guard took out: a key that this row sees gives its infinity or NaN to the sum
-          for (int i = 0; i < 12; ++i)
-            for (uint32_t m = bad[i]; m; m &= m - 1) {
-              const int key = (whole + (i >> 2)) * kPfKeys + 32 * (i & 3) + __ffs(m) - 1;
-              if (key >= seen) continue;
-              const uint16_t* v = p.v + (it.k0 + key) * p.v_ts + h * p.v_hs + c;
+          for (int e = 0; e < 32; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+          if (!live) continue;
+          if (dirty) {
+            // values that the guard took out: a key that this row sees gives its infinity or NaN to the sum
+            for (int t = sh.whole; t < nw; ++t)
+              for (int i = 0; i < 4; ++i)
+                for (uint32_t m = bad[4 * ((mbase + t - sh.whole) % kMasked) + i]; m; m &= m - 1) {
+                  const int key = t * kPfKeys + 32 * i + __ffs(m) - 1;
+                  if (key >= seen) continue;
+                  const uint16_t* v = p.v + (it.k0 + key) * p.v_ts + it.h * p.v_hs + c;
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (not_finite(v[e]))
-                  o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(static_cast<uint32_t>(v[e]) << 16));
+                  for (int e = 0; e < 32; ++e)
+                    if (not_finite(v[e]))
+                      o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(static_cast<uint32_t>(v[e]) << 16));
+                }
+          }
+          if (it.part >= 0) {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + part_row * kNope + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kNope + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t* x = o + 8 * e;
+              dst[e] = make_uint4(pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                  pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                  pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                                  pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
             }
-        }
-        if (it.part >= 0) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + part_row * kNope + c);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kNope + c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t* x = o + 8 * e;
-            dst[e] = make_uint4(pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                                pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                                pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
-                                pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
           }
         }
       }
+      mbase += sh.n - sh.whole;
     }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kIssuer) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0) {
+    // the last block to finish leaves the counter at zero for the next launch
+    __threadfence();
+    if (atomicAdd(p.status + kWsDone, 1) == static_cast<int>(gridDim.x) - 1) {
+      p.status[kWsCounter] = 0;
+      p.status[kWsDone] = 0;
+    }
+  }
 }
 
 // Joins the pieces of a cut tile: one warp a (row, head), 4 values a lane.
@@ -582,7 +756,9 @@ int launch_prefill(const PrefillParams& p, const CUtensorMap& tm_q, const CUtens
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(p.n_items * p.heads, 1, 1);
+  const int sms = device_sm_count();
+  if (sms < 1) return MLA_ERR_CUDA;
+  cfg.gridDim = dim3(std::min(p.n_items * p.heads, sms), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   if (cudaLaunchKernelEx(&cfg, prefill_kernel, tm_q, tm_k, tm_kr, tm_v, p) != cudaSuccess) return MLA_ERR_CUDA;

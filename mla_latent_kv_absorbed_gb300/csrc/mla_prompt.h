@@ -72,6 +72,10 @@ constexpr int kPfRows = 256;          // query rows of an item, at most
 constexpr int kPfKeys = 128;          // keys of a tile
 constexpr int32_t kPfNoLimit = 0x3FFFFFFF;   // off of an item without a causal limit
 
+// Words of the workspace's status header that the prefill kernel counts in
+// (zero between launches): items handed out, blocks that have finished.
+constexpr int kWsCounter = 16, kWsDone = 17;
+
 inline int pf_items_off(const int32_t*) { return kPfHeaderWords; }
 inline int pf_merge_off(const int32_t* h) { return kPfHeaderWords + kPfItemWords * h[kPItems]; }
 // Workspace: status header, partial outputs [partials][heads][256][128] fp32,

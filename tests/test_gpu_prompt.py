@@ -327,6 +327,15 @@ def _attention_bound(ref, mag):
 LSE_ATOL = 2.0 ** -11      # a score's 2^-12, and the fp32 sum of at most 4096 weights (2^-12)
 
 
+MANY = [
+    # more (tile, head) items than SMs, so that blocks take several in turn: with and without a second row tile,
+    # whole and partly seen key tiles, rows without keys
+    ([1, 7, 33, 100, 140, 260, 300, 0, 129], [1, 7, 33, 100, 140, 260, 300, 9, 129], 64, True),
+    ([130, 64, 5, 280], [700, 64, 0, 100], 80, True),
+    ([300, 1, 1, 1, 200], [300, 400, 128, 129, 513], 48, False),
+]
+
+
 def _attention_inputs(seed, nq, nk, H):
     return [_normal(seed, nq, H, 192), _normal(seed + 1, nk, H, 128), _normal(seed + 2, nk, 64), _normal(seed + 3, nk, H, 128)]
 
@@ -374,6 +383,23 @@ def test_prefill(ql, kl, H, causal):
     _check_attention(out, lse, ref, ref_lse, mag)
     again, none = _attend(B.Prefiller(qp, kp, H, causal), q, k, kr, v, lse=False)
     assert none is None and torch.equal(again, out)             # no order of atomics, and lse is optional
+
+
+@pytest.mark.parametrize("ql,kl,H,causal", MANY)
+def test_prefill_of_more_items_than_sms(ql, kl, H, causal):
+    torch, B = _t()
+    qp, kp = _indptr(ql), _indptr(kl)
+    (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(11 + H, int(qp[-1]), int(kp[-1]), H)
+    ref, ref_lse, mag = P.prefill_attention(xq, xk, xr, xv, qp, kp, SM, causal)
+    plan = B.Prefiller(qp, kp, H, causal)
+    out, lse = _attend(plan, q, k, kr, v)
+    _check_attention(out, lse, ref, ref_lse, mag)
+    # one call behind the other, without a wait between them
+    outs = [torch.empty_like(out) for _ in range(6)]
+    for o in outs:
+        plan.run(q, k, kr, v, SM, o)
+    assert plan.check() == 0
+    assert all(torch.equal(o, out) for o in outs)
 
 
 @pytest.mark.parametrize("ql,kl,H,causal", [([3], [4000], 1, True), ([64, 1], [3500, 700], 2, True),
