@@ -21,7 +21,7 @@
 // bits at any magnitude, sums are fp32), and O is rescaled in TMEM only then.
 //
 // Warps: 0-3 softmax and epilogue of tile A, 4-7 of tile B, 8 TMA producer, 9
-// MMA issuer, 10 the guard.  A tile that some row sees only in part is
+// MMA issuer, 10-11 the guard.  A tile that some row sees only in part is
 // masked by index in the softmax, but a zero weight times a value that is not
 // finite is NaN in the matrix product: the guard clears those values (and the
 // rows behind the last key) in shared memory before the product reads them,
@@ -39,7 +39,7 @@ namespace {
 using TileA = std::integral_constant<int, 0>;
 using TileB = std::integral_constant<int, 1>;
 
-constexpr int kThreads = 352;                         // 184 registers a thread: a row's 128 scores stay in them
+constexpr int kThreads = 384;
 constexpr int kProducer = 8, kIssuer = 9, kGuard = 10;
 constexpr int kSlots = 8;                             // of 16 KB: 5 a tile in turn, 3 of keys, 2 of values
 constexpr int kBlock = 16384;
@@ -50,7 +50,7 @@ constexpr int kOffRing = 6 * kBlock;
 constexpr int kOffBar = kOffRing + kSlots * kBlock;
 constexpr int kSched = 4;                             // items announced ahead
 constexpr int kMasked = 8;                            // masked tiles told apart: two items' worth and more
-constexpr int kConsumers = 8 + 1 + 1;                 // warps that read an announced item
+constexpr int kConsumers = 8 + 1 + 2;                 // warps that read an announced item
 enum Bar : int {
   bQFull = 0,                    // [2] per row tile
   bQFree = bQFull + 2,           // the item's last scores are done
@@ -212,8 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
       const bool four = i >= bPFull && i < bPFull + 2;
+      const bool two = i >= bVClean && i < bVClean + kMasked;
       const bool all = i >= bSchedFree && i < bSchedFree + kSched;
-      mbar_init(bar(i), four ? 4 : all ? kConsumers : 1);
+      mbar_init(bar(i), four ? 4 : two ? 2 : all ? kConsumers : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto wait_k = [&](int T) { return uwait(bKFull + (T & 1), (T >> 1) & 1); };
     int tbase = 0, ubase = 0, mbase = 0;
-    uint32_t items_a = 0, items_b = 0, steps_a = 0, steps_b = 0;   // per row tile: items begun, P tiles taken
+    uint32_t items = 0, steps = 0;                            // bit w: parity of row tile w's items begun, P tiles taken
     bool ok = true;
     Item it;
     // A wait that gives up makes `ok` false; what is issued until the check at the end of the tile stays inside
@@ -416,14 +417,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Shape sh = shape_of(it);
       if (sh.n == 0) continue;
       // the first scores: they may run while the epilogue of the item before reads its output
-      if (sh.n_a > 0) ok = uwait(bQFull, items_a++ & 1);
-      ok &= wait_k(tbase);
-      tc_fence_after();
-      if (sh.n_a > 0) qk(tbase, 0);
-      if (sh.n_b > 0) {
-        ok &= uwait(bQFull + 1, items_b++ & 1);
+      ok = wait_k(tbase);
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {
+        if ((w ? sh.n_b : sh.n_a) == 0) continue;
+        ok &= uwait(bQFull + w, (items >> w) & 1);
+        items ^= 1u << w;
         tc_fence_after();
-        qk(tbase, 1);
+        qk(tbase, w);
       }
       if (lead) {
         umma_commit(bar(bKFree + (tbase & 1)));
@@ -434,22 +435,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok &= t < sh.whole ? uwait(bVFull + (U & 1), (U >> 1) & 1)
                            : uwait(bVClean + M % kMasked, (M / kMasked) & 1);
         // P of an item's first tile also tells that its warps have read the output of the item before
-        if (t < sh.n_a) {
-          ok &= uwait(bPFull, steps_a++ & 1);
-          tc_fence_after();
-          pv(T, 0, t == 0);
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+          const int nw = w ? sh.n_b : sh.n_a;
+          if (t < nw) {
+            ok &= uwait(bPFull + w, (steps >> w) & 1);
+            steps ^= 1u << w;
+            tc_fence_after();
+            pv(T, w, t == 0);
+          }
+          if (w == 0 && t + 1 < sh.n) ok &= wait_k(T + 1);
+          if (t + 1 < nw) {
+            tc_fence_after();
+            qk(T + 1, w);
+          }
         }
-        if (t + 1 < sh.n) {
-          ok &= wait_k(T + 1);
-          tc_fence_after();
-        }
-        if (t + 1 < sh.n_a) qk(T + 1, 0);
-        if (t < sh.n_b) {
-          ok &= uwait(bPFull + 1, steps_b++ & 1);
-          tc_fence_after();
-          pv(T, 1, t == 0);
-        }
-        if (t + 1 < sh.n_b) qk(T + 1, 1);
         if (lead) {
           umma_commit(bar(bVFree + (T & 1)));
           if (t + 1 < sh.n) umma_commit(bar(bKFree + ((T + 1) & 1)));
@@ -465,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kGuard) {
     // ---------------------------------------------------------------- guard
+    const int g = warp - kGuard;                              // which half of a tile's keys
     int tbase = 0, M = 0;
     Item it;
     bool ok = true;
@@ -473,26 +474,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = sh.whole; t < sh.n; ++t, ++M) {
         ok = warp_wait(bar(bVMasked + M % kMasked), (M / kMasked) & 1, wc, lane);
         if (!ok) break;
+        uint8_t* half = smem + kOffRing + ((5 * (tbase + t) + 3 + g) % kSlots) * kBlock;
 #pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-          uint8_t* half = smem + kOffRing + ((5 * (tbase + t) + 3 + (m >> 1)) % kSlots) * kBlock;
+        for (int m = 2 * g; m < 2 * g + 2; ++m) {
           const int r = 32 * (m & 1) + lane;                  // row of this half's 64: key 32 m + lane of the tile
           const bool there = t * kPfKeys + 32 * m + lane < it.nk;
+          // chunks of 16 bytes in an order that keeps the lanes of a quarter warp on different banks
+          auto chunk = [&](int c) {
+            return reinterpret_cast<uint4*>(half + (c >> 3) * (kBlock / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+          };
+          uint4 v[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) v[c] = *chunk(c);
           // x * 0 is NaN exactly where x is not finite
           __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
           const __nv_bfloat162 zero = acc;
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            // chunks of 16 bytes in an order that keeps the lanes of a quarter warp on different banks
-            uint4* q = reinterpret_cast<uint4*>(half + (c >> 3) * (kBlock / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-            if (there) {
-              uint4 v = *q;
-              const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc = __hfma2(b[e], zero, acc);
-            } else {
-              *q = make_uint4(0, 0, 0, 0);
-            }
+          for (int c = 0; c < 16; ++c) {
+            const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v[c]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc = __hfma2(b[e], zero, acc);
+          }
+          if (!there) {
+            acc = zero;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) *chunk(c) = make_uint4(0, 0, 0, 0);
           }
           const float2 sum = __bfloat1622float2(acc);
           const bool found = sum.x != 0.f || sum.y != 0.f;    // NaN compares unequal
@@ -652,8 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-          if (!live) continue;
-          if (dirty) {
+          if (dirty && live) {
             // values that the guard took out: a key that this row sees gives its infinity or NaN to the sum
             for (int t = sh.whole; t < nw; ++t)
               for (int i = 0; i < 4; ++i)
@@ -667,19 +672,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                       o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(static_cast<uint32_t>(v[e]) << 16));
                 }
           }
+          // Four lanes exchange blocks, so that a store writes whole sectors of a row: row by row, 16 bytes a
+          // lane, the stores took a third of the epilogue.  After it lane i of four holds block i of their rows.
+          const int mate = lane & 3, first = row - mate;      // the first of the four lanes' rows
           if (it.part >= 0) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + part_row * kNope + c);
+            transpose4_blocks<8>(o, lane);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int x = 0; x < 4; ++x) {
+              if (first + x >= it.nq) break;
+              uint4* dst = reinterpret_cast<uint4*>(p.part_o + (part_row - mate + x) * kNope + c + 8 * mate);
+              dst[0] = make_uint4(o[8 * x], o[8 * x + 1], o[8 * x + 2], o[8 * x + 3]);
+              dst[1] = make_uint4(o[8 * x + 4], o[8 * x + 5], o[8 * x + 6], o[8 * x + 7]);
+            }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * kNope + c);
+            uint32_t b[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t* x = o + 8 * e;
-              dst[e] = make_uint4(pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                                  pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                                  pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
-                                  pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
+            for (int e = 0; e < 16; ++e) b[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            transpose4_blocks<4>(b, lane);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              if (first + x >= it.nq) break;
+              const size_t r = static_cast<size_t>(it.q0 + first + x) * p.heads + it.h;
+              *reinterpret_cast<uint4*>(p.out + r * kNope + c + 8 * mate) =
+                  make_uint4(b[4 * x], b[4 * x + 1], b[4 * x + 2], b[4 * x + 3]);
             }
           }
         }
