@@ -12,7 +12,7 @@
 // item's last product and epilogue.  Key tiles of 128:
 //   S = Q K^T       M = 128, N = 128, 12 steps of K = 16 (128 + 64 dims), both
 //                   operands from shared memory
-//   P = exp2(..)    in registers, one row a thread; written back as bf16 over
+//   P = exp2(..)    in registers, two threads a row; written back as bf16 over
 //                   the scores' own columns
 //   O += P V        A from TMEM, V as it lies in memory (N-major), 8 steps
 // Bound: the tensor core.  A key tile against both row tiles is 2 x 20 MMAs of
@@ -20,8 +20,13 @@
 // tile's maximum exceeds it by 2^8: weights stay below 2^8 (bf16 keeps their 8
 // bits at any magnitude, sums are fp32), and O is rescaled in TMEM only then.
 //
-// Warps: 0-3 softmax and epilogue of tile A, 4-7 of tile B, 8 TMA producer, 9
-// MMA issuer, 10-11 the guard.  A tile that some row sees only in part is
+// A row tile's scores, weights and product follow one another (the weights lie
+// over the scores), so its key tile takes as long as that chain; the other row
+// tile fills half of it.  Hence two threads a row: with one (1500 cycles a
+// tile instead of ~800) the chain was 4000 cycles, 2600 of them products.
+//
+// Warps: 0-7 softmax and epilogue of tile A, 8-15 of tile B, 16 TMA producer,
+// 17 MMA issuer, 18-19 the guard.  A tile that some row sees only in part is
 // masked by index in the softmax, but a zero weight times a value that is not
 // finite is NaN in the matrix product: the guard clears those values (and the
 // rows behind the last key) in shared memory before the product reads them,
@@ -39,8 +44,8 @@ namespace {
 using TileA = std::integral_constant<int, 0>;
 using TileB = std::integral_constant<int, 1>;
 
-constexpr int kThreads = 384;
-constexpr int kProducer = 8, kIssuer = 9, kGuard = 10;
+constexpr int kThreads = 640;
+constexpr int kProducer = 16, kIssuer = 17, kGuard = 18;
 constexpr int kSlots = 8;                             // of 16 KB: 5 a tile in turn, 3 of keys, 2 of values
 constexpr int kBlock = 16384;
 constexpr int kOffQ = 0;                              // 2 row tiles x 3 blocks of 128 rows x 64 dims
@@ -50,7 +55,7 @@ constexpr int kOffRing = 6 * kBlock;
 constexpr int kOffBar = kOffRing + kSlots * kBlock;
 constexpr int kSched = 4;                             // items announced ahead
 constexpr int kMasked = 8;                            // masked tiles told apart: two items' worth and more
-constexpr int kConsumers = 8 + 1 + 2;                 // warps that read an announced item
+constexpr int kConsumers = 16 + 1 + 2;                // warps that read an announced item
 enum Bar : int {
   bQFull = 0,                    // [2] per row tile
   bQFree = bQFull + 2,           // the item's last scores are done
@@ -71,7 +76,8 @@ enum Bar : int {
 constexpr int kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16;   // TMEM address, abort flag
 constexpr int kOffBad = kOffMisc + 16;                // [8][4] words: bit j = key j of masked tile M
 constexpr int kOffSched = kOffBad + 16 * kMasked;     // [4] announced items, 8 words each
-constexpr int kSmemBytes = kOffSched + 32 * kSched + 1024;
+constexpr int kOffMeet = kOffSched + 32 * kSched;      // [8][32] floats: where a row's two threads meet
+constexpr int kSmemBytes = kOffMeet + 1024 + 1024;
 static_assert(kOffSched % 16 == 0, "announced items are read as 16-byte words");
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;          // S_A, S_B, O_A, O_B: 128 columns each
@@ -211,10 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const bool four = i >= bPFull && i < bPFull + 2;
+      const bool eight = i >= bPFull && i < bPFull + 2;
       const bool two = i >= bVClean && i < bVClean + kMasked;
       const bool all = i >= bSchedFree && i < bSchedFree + kSched;
-      mbar_init(bar(i), four ? 4 : two ? 2 : all ? kConsumers : 1);
+      mbar_init(bar(i), eight ? 8 : two ? 2 : all ? kConsumers : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -526,19 +532,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // -------------------------------------------------- softmax and epilogue
-    const int w = warp >> 2;                                  // row tile
+    // Two threads a row, in warps `warp` and `warp` ^ 4: each takes half of a
+    // tile's keys and half of the output's columns.  They meet at a named
+    // barrier of their 64 threads and agree on the reference maximum there.
+    const int w = warp >> 3, half = (warp >> 2) & 1;          // row tile, half
     const int row = 128 * w + 32 * (warp & 3) + lane;         // row of the item
+    const int pair_bar = 1 + 4 * w + (warp & 3);
+    float* meet = reinterpret_cast<float*>(smem + kOffMeet) + 32 * (pair_bar - 1) + lane;
     const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + kTmemS + 128 * w + quad, to = tmem + kTmemO + 128 * w + quad;
+    const uint32_t ts = tmem + kTmemS + 128 * w + 64 * half + quad;   // the half's scores
+    const uint32_t tp = tmem + kTmemS + 128 * w + 32 * half + quad;   // its weights
+    const uint32_t to = tmem + kTmemO + 128 * w + 64 * half + quad;   // the half of the output
+    // Combines a value of the row's two threads; both return the result.
+    auto both = [&](float mine, auto op) -> float {
+      if (half == 0) *meet = mine;
+      named_bar_sync(pair_bar, 64);
+      if (half == 1) {
+        mine = op(mine, *meet);
+        *meet = mine;
+      }
+      named_bar_sync(pair_bar, 64);
+      if (half == 0) mine = *meet;
+      return mine;
+    };
     uint32_t step = 0;                                        // key tiles of this row tile, over all items
     int mbase = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       ok = warp_wait(bar(bSched + k % kSched), (k / kSched) & 1, wc, lane);
       if (!ok) break;
-      // The item's words are read here for the loop over the keys and again for the epilogue: 128 scores and
-      // what the loop needs fill the registers, and spills would pass through the shared memory's bandwidth,
-      // which the products need.
+      // The item's words are read here for the loop over the keys and again for the epilogue: held in between
+      // they would cost registers that the scores need.
       int nw, seen, first_masked;
       {
         Item it;
@@ -548,30 +572,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const Shape sh(it);
         nw = w ? sh.n_b : sh.n_a;
-        seen = min(it.nk, it.off + row + 1);                  // keys that this row sees (<= 0: none)
+        seen = min(it.nk, it.off + row + 1) - 64 * half;      // of the half's keys, counted from its first, those this row sees
         first_masked = min(max(it.off + 128 * w + 1, 0), it.nk) / kPfKeys;   // of this row tile
       }
       float ref = -INFINITY, sum = 0.f;
       for (int t = 0; t < nw; ++t, ++step) {
         ok = warp_wait(bar(bSFull + w), step & 1, wc, lane);
-        if (!ok) break;
         tc_fence_after();
-        uint32_t s[4][32];
+        uint32_t s[2][32];
         auto load_scores = [&] {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+          tmem_ld32(ts, s[0]);
+          tmem_ld32(ts + 32, s[1]);
           tmem_wait_ld();
           if (t >= first_masked) {
             const int left = seen - t * kPfKeys;
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
+            for (int c = 0; c < 64; ++c)
               if (c >= left) s[c / 32][c % 32] = 0xFF800000u;
           }
         };
         load_scores();
         float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             m0 = max3(m0, __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
@@ -579,44 +602,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             m2 = max3(m2, __uint_as_float(s[c][e + 4]), __uint_as_float(s[c][e + 5]));
             m3 = max3(m3, __uint_as_float(s[c][e + 6]), __uint_as_float(s[c][e + 7]));
           }
-        const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
-        const bool move = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
-        if (t == 0) {
-          if (move) ref = top;
-        } else if (__any_sync(0xffffffffu, move)) {
-          // the product before this one has finished: O is this warp's to rescale
-          ok = warp_wait(bar(bPvDone + w), (step - 1) & 1, wc, lane);
-          if (!ok) break;
-          tc_fence_after();
-          const float f = move ? (ref == -INFINITY ? 0.f : ex2_approx(ref - top)) : 1.f;
-          if (move) ref = top;
-          sum *= f;
+        float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
+        // some row of the two warps has outgrown its reference (a wait that gave up ends both warps here, too)
+        auto outgrown = [&] { return top > ref + kSlack || (ref == -INFINITY && top > -INFINITY); };
+        tc_fence_before();
+        const bool settle = named_bar_or(pair_bar, 64, outgrown() || !ok);
+        tc_fence_after();
+        if (settle) {
+          ok = both(ok ? 1.f : 0.f, [](float a, float b) { return fminf(a, b); }) > 0.f;
+          if (ok) {
+            top = both(top, [](float a, float b) { return fmaxf(a, b); });
+            const bool move = outgrown();
+            if (t == 0) {
+              if (move) ref = top;
+            } else {
+              // the product before this one has finished: O is these warps' to rescale
+              ok = warp_wait(bar(bPvDone + w), (step - 1) & 1, wc, lane);
+              tc_fence_after();
+              const float f = move ? (ref == -INFINITY ? 0.f : ex2_approx(ref - top)) : 1.f;
+              if (move) ref = top;
+              sum *= f;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            uint32_t o[8];
-            tmem_ld8(to + 8 * c, o);
-            tmem_wait_ld();
+              for (int c = 0; c < 8; ++c) {
+                uint32_t o[8];
+                tmem_ld8(to + 8 * c, o);
+                tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st8(to + 8 * c, o);
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st8(to + 8 * c, o);
+              }
+              load_scores();                                  // again: held over the rescaling they would be spilled
+              tc_fence_before();
+              named_bar_sync(pair_bar, 64);
+              tc_fence_after();
+            }
           }
-          load_scores();                                      // again: held over the rescaling they would be spilled
         }
+        if (!ok) break;
         const float sub = ref == -INFINITY ? 0.f : -ref;
         const float2 sc = make_float2(p.scale_log2, p.scale_log2), sb = make_float2(sub, sub);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+        // The weights go over columns 0-63 of the tile's scores, which both warps have read: the second half's
+        // lie over scores of the first half's warp, which has passed the barrier above.
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
+          uint32_t pk[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 x = f2_fma(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), sc, sb);
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t* z = s[c / 2] + 16 * (c & 1) + 2 * e;
+            const float2 x = f2_fma(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])), sc, sb);
             const float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             if (e & 1) acc1 = f2_add(acc1, y);
             else acc0 = f2_add(acc0, y);
             pk[e] = pack_bf16x2(y.x, y.y);
           }
-          tmem_st16(ts + 16 * c, pk);
+          tmem_st8(tp + 8 * c, pk);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -638,36 +678,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(bar(bVClean + M % kMasked), (M / kMasked) & 1, wc, lane);
         for (int i = 0; i < 4; ++i) dirty |= bad[4 * (M % kMasked) + i];
       }
-      if (ok && 128 * w < it.nq) {                            // the whole warp: tcgen05.ld is collective
+      if (128 * w < it.nq) {                                  // both warps, whole: they meet, and tcgen05.ld is collective
+        sum = both(sum, [](float a, float b) { return a + b; });
+        ok = both(ok ? 1.f : 0.f, [](float a, float b) { return fminf(a, b); }) > 0.f;
+        if (!ok) break;
         const bool any = nw > 0 && !(sum == 0.f);
         const float inv = any ? 1.f / sum : 0.f;
         const float lse = any ? (ref + log2f(sum)) * 0.69314718055994531f : -INFINITY;
         const bool live = row < it.nq;
         const size_t out_row = static_cast<size_t>(it.q0 + row) * p.heads + it.h;
         const size_t part_row = (static_cast<size_t>(max(it.part, 0)) * p.heads + it.h) * kPfRows + row;
-        if (live) {
+        if (live && half == 0) {
           if (it.part >= 0) p.part_lse[part_row] = lse;
           else if (p.lse) p.lse[out_row] = lse;
         }
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t o[32];
+        for (int c = 64 * half; c < 64 * half + 64; c += 16) {
+          uint32_t o[16];
           if (nw > 0) {
-            tmem_ld32(to + c, o);
+            tmem_ld16(to + (c & 48), o);
             tmem_wait_ld();
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+          for (int e = 0; e < 16; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
           if (dirty && live) {
             // values that the guard took out: a key that this row sees gives its infinity or NaN to the sum
+            const int all = min(it.nk, it.off + row + 1);
             for (int t = sh.whole; t < nw; ++t)
               for (int i = 0; i < 4; ++i)
                 for (uint32_t m = bad[4 * ((mbase + t - sh.whole) % kMasked) + i]; m; m &= m - 1) {
                   const int key = t * kPfKeys + 32 * i + __ffs(m) - 1;
-                  if (key >= seen) continue;
+                  if (key >= all) continue;
                   const uint16_t* v = p.v + (it.k0 + key) * p.v_ts + it.h * p.v_hs + c;
 #pragma unroll
-                  for (int e = 0; e < 32; ++e)
+                  for (int e = 0; e < 16; ++e)
                     if (not_finite(v[e]))
                       o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(static_cast<uint32_t>(v[e]) << 16));
                 }
@@ -676,26 +720,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           // lane, the stores took a third of the epilogue.  After it lane i of four holds block i of their rows.
           const int mate = lane & 3, first = row - mate;      // the first of the four lanes' rows
           if (it.part >= 0) {
-            transpose4_blocks<8>(o, lane);
+            transpose4_blocks<4>(o, lane);
+            float* dst = p.part_o + (part_row - mate) * kNope + c + 4 * mate;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              if (first + x >= it.nq) break;
-              uint4* dst = reinterpret_cast<uint4*>(p.part_o + (part_row - mate + x) * kNope + c + 8 * mate);
-              dst[0] = make_uint4(o[8 * x], o[8 * x + 1], o[8 * x + 2], o[8 * x + 3]);
-              dst[1] = make_uint4(o[8 * x + 4], o[8 * x + 5], o[8 * x + 6], o[8 * x + 7]);
-            }
+            for (int x = 0; x < 4; ++x)
+              if (first + x < it.nq)
+                *reinterpret_cast<uint4*>(dst + x * kNope) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
           } else {
-            uint32_t b[16];
+            uint32_t b[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) b[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-            transpose4_blocks<4>(b, lane);
+            for (int e = 0; e < 8; ++e) b[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            transpose4_blocks<2>(b, lane);
+            uint16_t* dst = p.out + (out_row - static_cast<size_t>(mate) * p.heads) * kNope + c + 4 * mate;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              if (first + x >= it.nq) break;
-              const size_t r = static_cast<size_t>(it.q0 + first + x) * p.heads + it.h;
-              *reinterpret_cast<uint4*>(p.out + r * kNope + c + 8 * mate) =
-                  make_uint4(b[4 * x], b[4 * x + 1], b[4 * x + 2], b[4 * x + 3]);
-            }
+            for (int x = 0; x < 4; ++x)
+              if (first + x < it.nq)
+                *reinterpret_cast<uint2*>(dst + static_cast<size_t>(x) * p.heads * kNope) = make_uint2(b[2 * x], b[2 * x + 1]);
           }
         }
       }
