@@ -172,6 +172,21 @@ __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { retu
 
 __device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7F80u) == 0x7F80u; }
 
+// Multiplies 64 columns of the thread's TMEM lane by f.  Rare, and out of line:
+// inlined, its registers push values of the loop over the keys into memory.
+__device__ __noinline__ void rescale_columns(uint32_t taddr, float f) {
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(taddr + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+    tmem_st16(taddr + c, o);
+  }
+  tmem_wait_st();
+}
+
 // The warp waits through its first lane; every lane returns the outcome.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& wc, int lane) {
   bool ok = true;
@@ -622,15 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float f = move ? (ref == -INFINITY ? 0.f : ex2_approx(ref - top)) : 1.f;
               if (move) ref = top;
               sum *= f;
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                uint32_t o[8];
-                tmem_ld8(to + 8 * c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st8(to + 8 * c, o);
-              }
+              rescale_columns(to, f);
               load_scores();                                  // again: held over the rescaling they would be spilled
               tc_fence_before();
               named_bar_sync(pair_bar, 64);
