@@ -9,8 +9,9 @@
 //     time: the group's keys and values stay in L2 while all its rows pass;
 //   * where whole items would leave SMs idle (few rows over long keys), an
 //     item's keys are cut into pieces of whole tiles whose partial outputs a
-//     second kernel joins.  The cut is the one, among a few equal shares of
-//     the mean load, whose greedy schedule ends first.
+//     second kernel joins.  Tried are the cuts that fill the SMs once, twice,
+//     ... with pieces of about equal cost; taken is the one whose greedy
+//     schedule ends first, if it ends before the uncut one.
 // The plan is deterministic: equal inputs give identical words.
 #include <algorithm>
 #include <cstdint>
@@ -31,24 +32,38 @@ struct Piece {
   long long cost;
 };
 
-constexpr long long kItemCost = 30;      // an item's prologue and epilogue, in tenths of a key tile
-constexpr long long kPieceCost = 15;     // a partial output written and read again
+// Costs in tenths of a key tile against two row tiles (about 460 cycles each;
+// measured over a ragged batch): an item's first loads and its epilogue, a
+// partial output written and read again, the joining kernel's launch.
+constexpr long long kItemCost = 14;
+constexpr long long kPieceCost = 4;
+constexpr long long kJoinCost = 12;
 constexpr long long kL2Bytes = 64ll << 20;
 
 inline int key_tiles(int nk) { return (nk + kPfKeys - 1) / kPfKeys; }
-// A key tile against two row tiles costs 10, against one 7.
-inline long long tile_cost(int nq) { return nq > kPfRows / 2 ? 10 : 7; }
+// One row tile has no other to fill its softmax's time: 8 of 10.
+inline long long tile_cost(int nq) { return nq > kPfRows / 2 ? 10 : 8; }
+
+// Parts of a tile whose keys are cut into pieces of at most `cap` (0: not cut), none under four key tiles.
+int parts_of(const Tile& t, long long cap) {
+  const int nt = key_tiles(t.nk);
+  if (cap <= 0 || nt <= 1) return 1;
+  const long long most = std::max<long long>(4, cap / tile_cost(t.nq));
+  return static_cast<int>((nt + most - 1) / most);
+}
+
+long long count_pieces(const std::vector<Tile>& tiles, long long cap) {
+  long long n = 0;
+  for (const Tile& t : tiles) n += parts_of(t, cap);
+  return n;
+}
 
 void cut(const std::vector<Tile>& tiles, long long cap, std::vector<Piece>& pieces) {
   pieces.clear();
   for (size_t i = 0; i < tiles.size(); ++i) {
     const int nt = key_tiles(tiles[i].nk);
     const long long c = tile_cost(tiles[i].nq);
-    int parts = 1;
-    if (cap > 0 && nt > 1) {
-      const long long most = std::max<long long>(4, cap / c);             // key tiles of a piece
-      parts = static_cast<int>((nt + most - 1) / most);
-    }
+    const int parts = parts_of(tiles[i], cap);
     for (int k = 0; k < parts; ++k) {
       const int a = static_cast<int>(static_cast<long long>(nt) * k / parts);
       const int e = static_cast<int>(static_cast<long long>(nt) * (k + 1) / parts);
@@ -58,18 +73,30 @@ void cut(const std::vector<Tile>& tiles, long long cap, std::vector<Piece>& piec
   std::stable_sort(pieces.begin(), pieces.end(), [](const Piece& x, const Piece& y) { return x.cost > y.cost; });
 }
 
-// End of the greedy schedule of the pieces, `heads` times each, on `sms`.
-long long makespan(const std::vector<Piece>& pieces, int heads, int sms) {
+// Heads whose items are launched together: their keys and values should stay
+// in L2 while the rows pass; the groups are of about equal size, so that the
+// last one has enough items to even out the SMs.
+int group_of(int heads, long long kv_tokens, size_t pieces, int sms) {
+  const long long per_head = std::max<long long>(1, kv_tokens * 2 * kNope * 2);
+  long long group = std::max<long long>(kL2Bytes / per_head, pieces ? (2ll * sms + pieces - 1) / pieces : 1);
+  group = std::min<long long>(heads, std::max<long long>(1, group));
+  const long long groups = (heads + group - 1) / group;
+  return static_cast<int>((heads + groups - 1) / groups);
+}
+
+// End of the greedy schedule of the pieces in launch order on `sms`.
+long long makespan(const std::vector<Piece>& pieces, int heads, int group, int sms) {
   std::priority_queue<long long, std::vector<long long>, std::greater<long long>> free_at;
   for (int i = 0; i < sms; ++i) free_at.push(0);
   long long end = 0;
-  for (const Piece& p : pieces)
-    for (int h = 0; h < heads; ++h) {
-      const long long t = free_at.top() + p.cost;
-      free_at.pop();
-      free_at.push(t);
-      end = std::max(end, t);
-    }
+  for (int h0 = 0; h0 < heads; h0 += group)
+    for (const Piece& p : pieces)
+      for (int h = h0; h < std::min(heads, h0 + group); ++h) {
+        const long long t = free_at.top() + p.cost;
+        free_at.pop();
+        free_at.push(t);
+        end = std::max(end, t);
+      }
   return end;
 }
 
@@ -96,14 +123,23 @@ int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int c
     most = std::max(most, p.cost);
   }
   const long long mean = (total + num_sms - 1) / num_sms;
+  const long long whole = static_cast<long long>(tiles.size()) * H;
   // the schedule of many items, none of them long, cannot be improved by cutting
-  if (!tiles.empty() && !(static_cast<long long>(best.size()) * H >= 8ll * num_sms && most <= mean / 2)) {
-    long long end = makespan(best, H, num_sms);
-    for (int share = 1; share <= 6; ++share) {
-      const long long cap = std::max<long long>(1, mean / share - kItemCost - kPieceCost);
-      cut(tiles, cap, trial);
-      if (trial.size() == tiles.size() || trial.size() > 65535) continue;
-      const long long e = makespan(trial, H, num_sms) + 2 * kItemCost;    // the joining kernel
+  if (!tiles.empty() && whole <= (1 << 16) && !(whole >= 8ll * num_sms && most <= mean / 2)) {
+    long long end = makespan(best, H, group_of(H, kp[B], best.size(), num_sms), num_sms);
+    long long waves = whole / num_sms + 1;
+    for (int tried = 0; tried < 5; ++tried, ++waves) {
+      const long long pieces = waves * num_sms / H;           // that fill the SMs `waves` times
+      if (pieces <= static_cast<long long>(tiles.size()) || pieces > 65535) continue;
+      long long lo = 1, hi = most;                            // the smallest cap with no more pieces than that
+      while (lo < hi) {
+        const long long mid = (lo + hi) / 2;
+        if (count_pieces(tiles, mid) <= pieces) hi = mid;
+        else lo = mid + 1;
+      }
+      cut(tiles, lo, trial);
+      if (trial.size() == tiles.size()) continue;
+      const long long e = makespan(trial, H, group_of(H, kp[B], trial.size(), num_sms), num_sms) + kJoinCost;
       if (e < end) {
         end = e;
         best.swap(trial);
@@ -124,10 +160,7 @@ int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int c
                             static_cast<long long>(kPfMergeWords) * merges;
   const long long blocks = static_cast<long long>(best.size()) * H;
   if (n_words > 0x7FFFFFFFll || blocks > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
-  const long long per_head = std::max<long long>(1, static_cast<long long>(kp[B]) * 2 * kNope * 2);
-  long long group = std::max<long long>(kL2Bytes / per_head,
-                                        best.empty() ? 1 : (2ll * num_sms + best.size() - 1) / best.size());
-  group = std::min<long long>(H, std::max<long long>(1, group));
+  const int group = group_of(H, kp[B], best.size(), num_sms);
   words.assign(static_cast<size_t>(n_words), 0);
   words[kPMagic] = kPfMagic;
   words[kPVersion] = kPfVersion;
@@ -139,7 +172,7 @@ int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int c
   words[kPItems] = static_cast<int32_t>(best.size());
   words[kPPartials] = partials;
   words[kPMerges] = merges;
-  words[kPHeadGroup] = static_cast<int32_t>(group);
+  words[kPHeadGroup] = group;
   words[kPTotalWords] = static_cast<int32_t>(n_words);
   words[kPNumSms] = num_sms;
   int32_t* w = words.data() + kPfHeaderWords;

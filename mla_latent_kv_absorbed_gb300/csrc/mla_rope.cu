@@ -12,6 +12,7 @@
 // turn from the conversion to 24 bits).  No table is read and no position is
 // too large.  Sums and products are fp32, rounded once to the output's type.
 #include "mla_device.cuh"
+#include "mla_launch.h"
 #include "mla_prompt.h"
 
 namespace mla {
@@ -35,148 +36,206 @@ __device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
 }
 
 // ------------------------------------------------------------------- query --
-// A block takes one token and `heads_per_block` heads.  Eight lanes move a
-// head's rotary part, 16 bytes each; the 32 pairs' cos and sin are computed
-// once a block, by warp 0, while the other loads are in flight.
+// Work is cut into units of one token and up to 32 J heads; a block walks
+// units.  Eight lanes move a head's rotary part, 16 bytes each (half layout:
+// four lanes, both halves), and a thread has J heads in flight.  The 32 pairs'
+// cos and sin are computed once a unit, by warp 0, while the loads are on
+// their way; each of its lanes keeps its pair's frequency in a register (read
+// from the parameters by lane it is a replay a lane, once a block).
+// Bound: HBM (the rotary part read and written once).
 constexpr int kQThreads = 256;
 
+template <int J>
 __global__ void __launch_bounds__(kQThreads) rope_query_kernel(const RopeQueryParams p,
-                                                               const __grid_constant__ RopeFreqs f,
-                                                               int heads_per_block) {
-  __shared__ float2 cs[kPairs];
+                                                               const __grid_constant__ RopeFreqs f, int units) {
+  __shared__ __align__(16) float2 cs_of[2][kPairs];
+  const int tid = threadIdx.x;
+  const uint64_t freq = tid < kPairs ? f.f[tid] : 0;
   griddep_wait();
   griddep_launch_dependents();
-  const int chunks = (p.heads + heads_per_block - 1) / heads_per_block;
-  const int t = blockIdx.x / chunks;
-  const int h0 = (blockIdx.x % chunks) * heads_per_block;
-  const int nh = min(heads_per_block, p.heads - h0);
-  if (threadIdx.x < kPairs)
-    cs[threadIdx.x] = phase_cos_sin(f.f[threadIdx.x], __ldg(p.positions + t), f.amplitude);
-  __syncthreads();
-  const uint16_t* src = p.q + t * p.q_ts + h0 * p.q_hs;
-  uint16_t* dst = p.q_rope + t * p.r_ts + h0 * p.r_hs;
-  if (f.interleaved) {
-    for (int i = threadIdx.x; i < nh * 8; i += kQThreads) {
-      const int h = i >> 3, d = (i & 7) * 8;
-      uint4 v = *reinterpret_cast<const uint4*>(src + h * p.q_hs + p.nope + d);
-      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+  constexpr int kHeads = 32 * J;
+  const int chunks = (p.heads + kHeads - 1) / kHeads;
+  const int pieces = p.nope / 8;
+  // the copy of the rest of the heads: a thread's piece, its first head and the heads a pass covers
+  const int span = pieces > 0 && pieces <= kQThreads ? kQThreads / pieces : 0;
+  const int ch = span ? tid / pieces : 0, cd = span ? (tid - ch * pieces) * 8 : 0;
+  int buf = 0;
+  for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
+    const int t = u / chunks, h0 = (u - t * chunks) * kHeads;
+    const int nh = min(kHeads, p.heads - h0);
+    const uint16_t* src = p.q + t * p.q_ts + h0 * p.q_hs;
+    uint16_t* dst = p.q_rope + t * p.r_ts + h0 * p.r_hs;
+    const float4* cs = reinterpret_cast<const float4*>(cs_of[buf]);
+    if (f.interleaved) {
+      const int h = tid >> 3, d = (tid & 7) * 8;
+      uint4 v[J];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float a = bf_lo(w[k]), b = bf_hi(w[k]);
-        rotate(a, b, cs[d / 2 + k]);
-        w[k] = pack_bf16x2(a, b);
-      }
-      *reinterpret_cast<uint4*>(dst + h * p.r_hs + d) = v;
-    }
-  } else {
-    for (int i = threadIdx.x; i < nh * 4; i += kQThreads) {
-      const int h = i >> 2, d = (i & 3) * 8;
-      const uint16_t* s = src + h * p.q_hs + p.nope + d;
-      uint4 va = *reinterpret_cast<const uint4*>(s), vb = *reinterpret_cast<const uint4*>(s + 32);
-      uint32_t* wa = reinterpret_cast<uint32_t*>(&va);
-      uint32_t* wb = reinterpret_cast<uint32_t*>(&vb);
+      for (int j = 0; j < J; ++j)
+        if (h + 32 * j < nh) v[j] = *reinterpret_cast<const uint4*>(src + (h + 32 * j) * p.q_hs + p.nope + d);
+      if (tid < kPairs) cs_of[buf][tid] = phase_cos_sin(freq, __ldg(p.positions + t), f.amplitude);
+      __syncthreads();
+      const float4 c01 = cs[d / 4], c23 = cs[d / 4 + 1];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float a0 = bf_lo(wa[k]), b0 = bf_lo(wb[k]), a1 = bf_hi(wa[k]), b1 = bf_hi(wb[k]);
-        rotate(a0, b0, cs[d + 2 * k]);
-        rotate(a1, b1, cs[d + 2 * k + 1]);
-        wa[k] = pack_bf16x2(a0, a1);
-        wb[k] = pack_bf16x2(b0, b1);
+      for (int j = 0; j < J; ++j) {
+        if (h + 32 * j >= nh) continue;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v[j]);
+        auto turn = [&](uint32_t& x, float c, float sn) {
+          float a = bf_lo(x), b = bf_hi(x);
+          rotate(a, b, make_float2(c, sn));
+          x = pack_bf16x2(a, b);
+        };
+        turn(w[0], c01.x, c01.y);
+        turn(w[1], c01.z, c01.w);
+        turn(w[2], c23.x, c23.y);
+        turn(w[3], c23.z, c23.w);
+        *reinterpret_cast<uint4*>(dst + (h + 32 * j) * p.r_hs + d) = v[j];
       }
-      *reinterpret_cast<uint4*>(dst + h * p.r_hs + d) = va;
-      *reinterpret_cast<uint4*>(dst + h * p.r_hs + d + 32) = vb;
+    } else {
+      constexpr int kN = (J + 1) / 2;
+      const int h = tid >> 2, d = (tid & 3) * 8;
+      uint4 va[kN], vb[kN];
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        if (h + 64 * j < nh) {
+          const uint16_t* x = src + (h + 64 * j) * p.q_hs + p.nope + d;
+          va[j] = *reinterpret_cast<const uint4*>(x);
+          vb[j] = *reinterpret_cast<const uint4*>(x + 32);
+        }
+      if (tid < kPairs) cs_of[buf][tid] = phase_cos_sin(freq, __ldg(p.positions + t), f.amplitude);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        if (h + 64 * j >= nh) continue;
+        uint32_t* wa = reinterpret_cast<uint32_t*>(&va[j]);
+        uint32_t* wb = reinterpret_cast<uint32_t*>(&vb[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 c = cs[d / 2 + k];
+          float a0 = bf_lo(wa[k]), b0 = bf_lo(wb[k]), a1 = bf_hi(wa[k]), b1 = bf_hi(wb[k]);
+          rotate(a0, b0, make_float2(c.x, c.y));
+          rotate(a1, b1, make_float2(c.z, c.w));
+          wa[k] = pack_bf16x2(a0, a1);
+          wb[k] = pack_bf16x2(b0, b1);
+        }
+        uint16_t* y = dst + (h + 64 * j) * p.r_hs + d;
+        *reinterpret_cast<uint4*>(y) = va[j];
+        *reinterpret_cast<uint4*>(y + 32) = vb[j];
+      }
     }
-  }
-  if (p.q_nope) {
-    const int pieces = p.nope / 8;
-    uint16_t* out = p.q_nope + (static_cast<long long>(t) * p.heads + h0) * p.nope;
-    for (int i = threadIdx.x; i < nh * pieces; i += kQThreads) {
-      const int h = i / pieces, d = (i - h * pieces) * 8;
-      *reinterpret_cast<uint4*>(out + static_cast<long long>(h) * p.nope + d) =
-          *reinterpret_cast<const uint4*>(src + h * p.q_hs + d);
+    if (p.q_nope) {
+      uint16_t* out = p.q_nope + (static_cast<long long>(t) * p.heads + h0) * p.nope;
+      if (span) {
+        if (ch < span) {
+#pragma unroll 4
+          for (int h = ch; h < nh; h += span)
+            *reinterpret_cast<uint4*>(out + static_cast<long long>(h) * p.nope + cd) =
+                *reinterpret_cast<const uint4*>(src + h * p.q_hs + cd);
+        }
+      } else {
+        for (int i = tid; i < nh * pieces; i += kQThreads) {
+          const int h = i / pieces, d = (i - h * pieces) * 8;
+          *reinterpret_cast<uint4*>(out + static_cast<long long>(h) * p.nope + d) =
+              *reinterpret_cast<const uint4*>(src + h * p.q_hs + d);
+        }
+      }
     }
   }
 }
 
 // ------------------------------------------------------------------ append --
 // One warp a row: a lane holds 16 latent values (two 16-byte pieces) and one
-// rotary pair.  A slot outside [0, num_slots) is skipped and recorded.
+// rotary pair, and over all rows of the warp its pair's frequency and its part
+// of the norm's weight (read from the parameters by lane, a frequency is a
+// replay a lane: at one row a warp that took as long as the rows).  A slot
+// outside [0, num_slots) is skipped and recorded.
 constexpr int kAThreads = 256;
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kAThreads) rope_append_kernel(const RopeAppendParams p,
-                                                                const __grid_constant__ RopeFreqs f) {
+                                                                const __grid_constant__ RopeFreqs f, int warps) {
+  const int lane = threadIdx.x & 31;
+  const int warp = blockIdx.x * (kAThreads / 32) + (threadIdx.x >> 5);
+  const uint64_t freq = f.f[lane];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * (kAThreads / 32) + (threadIdx.x >> 5);
-  if (t >= p.tokens) return;
-  const long long slot = __ldg(p.slots + t);
-  const int pos = __ldg(p.positions + t);
-  const uint16_t* src = p.rows + t * p.row_stride;
-  const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(src) + lane);
-  const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(src) + 32 + lane);
-  const uint16_t* rs = src + kLatent;
-  const int ia = f.interleaved ? 2 * lane : lane, ib = f.interleaved ? 2 * lane + 1 : lane + kPairs;
-  float ra = __uint_as_float(static_cast<uint32_t>(__ldg(rs + ia)) << 16);
-  float rb = __uint_as_float(static_cast<uint32_t>(__ldg(rs + ib)) << 16);
-  if (slot < 0 || slot >= p.num_slots) {
-    if (lane == 0) record_status(p.status, MLA_ERR_INDEX_OOB);
-    return;
-  }
-  rotate(ra, rb, phase_cos_sin(f.f[lane], pos, f.amplitude));
-  const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = bf_lo(w[i]);
-    x[2 * i + 1] = bf_hi(w[i]);
-  }
+  uint4 g0 = make_uint4(0, 0, 0, 0), g1 = g0;
   if (p.weight) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(ss * (1.f / kLatent) + p.eps);
-    const uint4 g0 = __ldg(reinterpret_cast<const uint4*>(p.weight) + lane);
-    const uint4 g1 = __ldg(reinterpret_cast<const uint4*>(p.weight) + 32 + lane);
-    const uint32_t g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+    g0 = __ldg(reinterpret_cast<const uint4*>(p.weight) + lane);
+    g1 = __ldg(reinterpret_cast<const uint4*>(p.weight) + 32 + lane);
+  }
+  for (int t = warp; t < p.tokens; t += warps) {
+    const long long slot = __ldg(p.slots + t);
+    const int pos = __ldg(p.positions + t);
+    const uint16_t* src = p.rows + t * p.row_stride;
+    const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(src) + lane);
+    const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(src) + 32 + lane);
+    const uint16_t* rs = src + kLatent;
+    const int ia = f.interleaved ? 2 * lane : lane, ib = f.interleaved ? 2 * lane + 1 : lane + kPairs;
+    float ra, rb;
+    if (f.interleaved) {
+      const uint32_t r = __ldg(reinterpret_cast<const uint32_t*>(rs) + lane);
+      ra = bf_lo(r);
+      rb = bf_hi(r);
+    } else {
+      ra = __uint_as_float(static_cast<uint32_t>(__ldg(rs + ia)) << 16);
+      rb = __uint_as_float(static_cast<uint32_t>(__ldg(rs + ib)) << 16);
+    }
+    if (slot < 0 || slot >= p.num_slots) {
+      if (lane == 0) record_status(p.status, MLA_ERR_INDEX_OOB);
+      continue;
+    }
+    rotate(ra, rb, phase_cos_sin(freq, pos, f.amplitude));
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    float x[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      x[2 * i] = x[2 * i] * r * bf_lo(g[i]);
-      x[2 * i + 1] = x[2 * i + 1] * r * bf_hi(g[i]);
+      x[2 * i] = bf_lo(w[i]);
+      x[2 * i + 1] = bf_hi(w[i]);
     }
-  }
-  if constexpr (kFp8) {
-    uint8_t* dst = static_cast<uint8_t*>(p.kv_cache) + slot * kRow;
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = e4m3x2(__fdiv_rn(x[4 * i], p.kv_scale), __fdiv_rn(x[4 * i + 1], p.kv_scale)) |
-             e4m3x2(__fdiv_rn(x[4 * i + 2], p.kv_scale), __fdiv_rn(x[4 * i + 3], p.kv_scale)) << 16;
-    reinterpret_cast<uint2*>(dst)[lane] = make_uint2(c[0], c[1]);
-    reinterpret_cast<uint2*>(dst)[32 + lane] = make_uint2(c[2], c[3]);
-    const uint32_t r2 = e4m3x2(__fdiv_rn(ra, p.kv_scale), __fdiv_rn(rb, p.kv_scale));
-    dst[kLatent + ia] = static_cast<uint8_t>(r2);
-    dst[kLatent + ib] = static_cast<uint8_t>(r2 >> 8);
-  } else {
-    uint16_t* dst = static_cast<uint16_t*>(p.kv_cache) + slot * kRow;
-    uint4 o0 = v0, o1 = v1;                       // without a norm the latent's bits pass unchanged
     if (p.weight) {
-      o0 = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
-      o1 = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
-                      pack_bf16x2(x[14], x[15]));
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = rsqrtf(ss * (1.f / kLatent) + p.eps);
+      const uint32_t g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[2 * i] = x[2 * i] * r * bf_lo(g[i]);
+        x[2 * i + 1] = x[2 * i + 1] * r * bf_hi(g[i]);
+      }
     }
-    reinterpret_cast<uint4*>(dst)[lane] = o0;
-    reinterpret_cast<uint4*>(dst)[32 + lane] = o1;
-    const uint32_t r2 = pack_bf16x2(ra, rb);
-    if (f.interleaved) {
-      reinterpret_cast<uint32_t*>(dst + kLatent)[lane] = r2;
+    if constexpr (kFp8) {
+      uint8_t* dst = static_cast<uint8_t*>(p.kv_cache) + slot * kRow;
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c[i] = e4m3x2(__fdiv_rn(x[4 * i], p.kv_scale), __fdiv_rn(x[4 * i + 1], p.kv_scale)) |
+               e4m3x2(__fdiv_rn(x[4 * i + 2], p.kv_scale), __fdiv_rn(x[4 * i + 3], p.kv_scale)) << 16;
+      reinterpret_cast<uint2*>(dst)[lane] = make_uint2(c[0], c[1]);
+      reinterpret_cast<uint2*>(dst)[32 + lane] = make_uint2(c[2], c[3]);
+      const uint32_t r2 = e4m3x2(__fdiv_rn(ra, p.kv_scale), __fdiv_rn(rb, p.kv_scale));
+      dst[kLatent + ia] = static_cast<uint8_t>(r2);
+      dst[kLatent + ib] = static_cast<uint8_t>(r2 >> 8);
     } else {
-      dst[kLatent + ia] = static_cast<uint16_t>(r2);
-      dst[kLatent + ib] = static_cast<uint16_t>(r2 >> 16);
+      uint16_t* dst = static_cast<uint16_t*>(p.kv_cache) + slot * kRow;
+      uint4 o0 = v0, o1 = v1;                       // without a norm the latent's bits pass unchanged
+      if (p.weight) {
+        o0 = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                        pack_bf16x2(x[6], x[7]));
+        o1 = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
+                        pack_bf16x2(x[14], x[15]));
+      }
+      reinterpret_cast<uint4*>(dst)[lane] = o0;
+      reinterpret_cast<uint4*>(dst)[32 + lane] = o1;
+      const uint32_t r2 = pack_bf16x2(ra, rb);
+      if (f.interleaved) {
+        reinterpret_cast<uint32_t*>(dst + kLatent)[lane] = r2;
+      } else {
+        dst[kLatent + ia] = static_cast<uint16_t>(r2);
+        dst[kLatent + ib] = static_cast<uint16_t>(r2 >> 16);
+      }
     }
   }
 }
@@ -198,18 +257,29 @@ int launch_dependent(Kernel* kernel, int blocks, int threads, cudaStream_t strea
 
 }  // namespace
 
+// Heads of a unit: 128 where the units then still give every SM several
+// blocks, else 32.
 int launch_rope_query(const RopeQueryParams& p, const RopeFreqs& f, cudaStream_t stream) {
-  const int per_block = 32;
-  const long long blocks = static_cast<long long>(p.tokens) * ((p.heads + per_block - 1) / per_block);
-  if (blocks > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
-  return launch_dependent(rope_query_kernel, static_cast<int>(blocks), kQThreads, stream, p, f, per_block);
+  const int sms = device_sm_count();
+  if (sms < 1) return MLA_ERR_CUDA;
+  const bool wide = static_cast<long long>(p.tokens) * ((p.heads + 127) / 128) >= 4ll * sms && p.heads > 32;
+  const int per = wide ? 128 : 32;
+  const long long units = static_cast<long long>(p.tokens) * ((p.heads + per - 1) / per);
+  if (units > 0x3FFFFFFFll) return MLA_ERR_UNSUPPORTED;
+  const int grid = static_cast<int>(units < 8ll * sms ? units : 8ll * sms);   // 8 blocks of 256 threads fill an SM
+  return wide ? launch_dependent(rope_query_kernel<4>, grid, kQThreads, stream, p, f, static_cast<int>(units))
+              : launch_dependent(rope_query_kernel<1>, grid, kQThreads, stream, p, f, static_cast<int>(units));
 }
 
 int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, cudaStream_t stream) {
-  constexpr int kRows = kAThreads / 32;
-  const int blocks = static_cast<int>((p.tokens + static_cast<long long>(kRows) - 1) / kRows);
-  return fp8 ? launch_dependent(rope_append_kernel<true>, blocks, kAThreads, stream, p, f)
-             : launch_dependent(rope_append_kernel<false>, blocks, kAThreads, stream, p, f);
+  const int sms = device_sm_count();
+  if (sms < 1) return MLA_ERR_CUDA;
+  constexpr int kWarps = kAThreads / 32;
+  // as many warps as the SMs hold, each the same number of rows
+  const long long rows = (p.tokens + 64ll * sms - 1) / (64ll * sms);
+  const int grid = static_cast<int>((p.tokens + rows * kWarps - 1) / (rows * kWarps));
+  return fp8 ? launch_dependent(rope_append_kernel<true>, grid, kAThreads, stream, p, f, grid * kWarps)
+             : launch_dependent(rope_append_kernel<false>, grid, kAThreads, stream, p, f, grid * kWarps);
 }
 
 }  // namespace mla
