@@ -46,6 +46,7 @@ struct RopeAppendParams {
   int tokens;
   float eps;
   float kv_scale;             // FP8 cache only
+  float kv_recip;             // 1 / kv_scale where a product with it is the quotient exactly, else 0
 };
 
 struct ExpandParams {

@@ -166,6 +166,9 @@ int rope_append(void* kv_cache, int64_t num_slots, const int32_t* slots, const v
   p.tokens = tokens;
   p.eps = eps;
   p.kv_scale = kv_scale;
+  int exponent = 0;
+  if (std::frexp(kv_scale, &exponent) == 0.5f && std::isnormal(kv_scale) && std::isnormal(1.f / kv_scale))
+    p.kv_recip = 1.f / kv_scale;
   return launch_rope_append(p, f, fp8, reinterpret_cast<cudaStream_t>(stream));
 }
 }  // namespace

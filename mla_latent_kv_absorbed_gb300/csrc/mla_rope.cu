@@ -46,7 +46,7 @@ __device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
 constexpr int kQThreads = 256;
 
 template <int J>
-__global__ void __launch_bounds__(kQThreads) rope_query_kernel(const RopeQueryParams p,
+__global__ void __launch_bounds__(kQThreads, 4) rope_query_kernel(const RopeQueryParams p,
                                                                const __grid_constant__ RopeFreqs f, int units) {
   __shared__ __align__(16) float2 cs_of[2][kPairs];
   const int tid = threadIdx.x;
@@ -150,12 +150,21 @@ __global__ void __launch_bounds__(kQThreads) rope_query_kernel(const RopeQueryPa
 // outside [0, num_slots) is skipped and recorded.
 constexpr int kAThreads = 256;
 
+constexpr int kABlocks = 3;      // blocks an SM holds: a row being worked on and the next one on its way a warp
+
+// x / scale in fp32; by its reciprocal where that is exact (a power of two).
+__device__ __forceinline__ float unscale(float x, const RopeAppendParams& p) {
+  return p.kv_recip != 0.f ? x * p.kv_recip : __fdiv_rn(x, p.kv_scale);
+}
+
 template <bool kFp8>
-__global__ void __launch_bounds__(kAThreads) rope_append_kernel(const RopeAppendParams p,
-                                                                const __grid_constant__ RopeFreqs f, int warps) {
+__global__ void __launch_bounds__(kAThreads, kABlocks) rope_append_kernel(const RopeAppendParams p,
+                                                                          const __grid_constant__ RopeFreqs f,
+                                                                          int warps) {
   const int lane = threadIdx.x & 31;
   const int warp = blockIdx.x * (kAThreads / 32) + (threadIdx.x >> 5);
   const uint64_t freq = f.f[lane];
+  const int ia = f.interleaved ? 2 * lane : lane, ib = f.interleaved ? 2 * lane + 1 : lane + kPairs;
   griddep_wait();
   griddep_launch_dependents();
   uint4 g0 = make_uint4(0, 0, 0, 0), g1 = g0;
@@ -163,28 +172,35 @@ __global__ void __launch_bounds__(kAThreads) rope_append_kernel(const RopeAppend
     g0 = __ldg(reinterpret_cast<const uint4*>(p.weight) + lane);
     g1 = __ldg(reinterpret_cast<const uint4*>(p.weight) + 32 + lane);
   }
-  for (int t = warp; t < p.tokens; t += warps) {
-    const long long slot = __ldg(p.slots + t);
-    const int pos = __ldg(p.positions + t);
+  struct Row {
+    int slot, pos;
+    uint4 v0, v1;
+    uint32_t r;                  // the rotary pair
+  };
+  auto load = [&](int t) {
+    Row x;
     const uint16_t* src = p.rows + t * p.row_stride;
-    const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(src) + lane);
-    const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(src) + 32 + lane);
-    const uint16_t* rs = src + kLatent;
-    const int ia = f.interleaved ? 2 * lane : lane, ib = f.interleaved ? 2 * lane + 1 : lane + kPairs;
-    float ra, rb;
-    if (f.interleaved) {
-      const uint32_t r = __ldg(reinterpret_cast<const uint32_t*>(rs) + lane);
-      ra = bf_lo(r);
-      rb = bf_hi(r);
-    } else {
-      ra = __uint_as_float(static_cast<uint32_t>(__ldg(rs + ia)) << 16);
-      rb = __uint_as_float(static_cast<uint32_t>(__ldg(rs + ib)) << 16);
-    }
+    x.slot = __ldg(p.slots + t);
+    x.pos = __ldg(p.positions + t);
+    x.v0 = __ldg(reinterpret_cast<const uint4*>(src) + lane);
+    x.v1 = __ldg(reinterpret_cast<const uint4*>(src) + 32 + lane);
+    if (f.interleaved) x.r = __ldg(reinterpret_cast<const uint32_t*>(src + kLatent) + lane);
+    else x.r = static_cast<uint32_t>(__ldg(src + kLatent + ia)) | static_cast<uint32_t>(__ldg(src + kLatent + ib)) << 16;
+    return x;
+  };
+  if (warp >= p.tokens) return;
+  Row next = load(warp);
+  for (int t = warp; t < p.tokens; t += warps) {
+    const Row cur = next;
+    if (t + warps < p.tokens) next = load(t + warps);
+    const long long slot = cur.slot;
+    const uint4 v0 = cur.v0, v1 = cur.v1;
+    float ra = bf_lo(cur.r), rb = bf_hi(cur.r);
     if (slot < 0 || slot >= p.num_slots) {
       if (lane == 0) record_status(p.status, MLA_ERR_INDEX_OOB);
       continue;
     }
-    rotate(ra, rb, phase_cos_sin(freq, pos, f.amplitude));
+    rotate(ra, rb, phase_cos_sin(freq, cur.pos, f.amplitude));
     const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     float x[16];
 #pragma unroll
@@ -211,11 +227,11 @@ __global__ void __launch_bounds__(kAThreads) rope_append_kernel(const RopeAppend
       uint32_t c[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        c[i] = e4m3x2(__fdiv_rn(x[4 * i], p.kv_scale), __fdiv_rn(x[4 * i + 1], p.kv_scale)) |
-               e4m3x2(__fdiv_rn(x[4 * i + 2], p.kv_scale), __fdiv_rn(x[4 * i + 3], p.kv_scale)) << 16;
+        c[i] = e4m3x2(unscale(x[4 * i], p), unscale(x[4 * i + 1], p)) |
+               e4m3x2(unscale(x[4 * i + 2], p), unscale(x[4 * i + 3], p)) << 16;
       reinterpret_cast<uint2*>(dst)[lane] = make_uint2(c[0], c[1]);
       reinterpret_cast<uint2*>(dst)[32 + lane] = make_uint2(c[2], c[3]);
-      const uint32_t r2 = e4m3x2(__fdiv_rn(ra, p.kv_scale), __fdiv_rn(rb, p.kv_scale));
+      const uint32_t r2 = e4m3x2(unscale(ra, p), unscale(rb, p));
       dst[kLatent + ia] = static_cast<uint8_t>(r2);
       dst[kLatent + ib] = static_cast<uint8_t>(r2 >> 8);
     } else {
@@ -266,7 +282,7 @@ int launch_rope_query(const RopeQueryParams& p, const RopeFreqs& f, cudaStream_t
   const int per = wide ? 128 : 32;
   const long long units = static_cast<long long>(p.tokens) * ((p.heads + per - 1) / per);
   if (units > 0x3FFFFFFFll) return MLA_ERR_UNSUPPORTED;
-  const int grid = static_cast<int>(units < 8ll * sms ? units : 8ll * sms);   // 8 blocks of 256 threads fill an SM
+  const int grid = static_cast<int>(units < 4ll * sms ? units : 4ll * sms);   // what the SMs hold at once
   return wide ? launch_dependent(rope_query_kernel<4>, grid, kQThreads, stream, p, f, static_cast<int>(units))
               : launch_dependent(rope_query_kernel<1>, grid, kQThreads, stream, p, f, static_cast<int>(units));
 }
@@ -276,7 +292,8 @@ int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, 
   if (sms < 1) return MLA_ERR_CUDA;
   constexpr int kWarps = kAThreads / 32;
   // as many warps as the SMs hold, each the same number of rows
-  const long long rows = (p.tokens + 64ll * sms - 1) / (64ll * sms);
+  const long long held = static_cast<long long>(sms) * kABlocks * kWarps;
+  const long long rows = (p.tokens + held - 1) / held;
   const int grid = static_cast<int>((p.tokens + rows * kWarps - 1) / (rows * kWarps));
   return fp8 ? launch_dependent(rope_append_kernel<true>, grid, kAThreads, stream, p, f, grid * kWarps)
              : launch_dependent(rope_append_kernel<false>, grid, kAThreads, stream, p, f, grid * kWarps);
