@@ -18,6 +18,7 @@
 //               quadrant and take half of the columns each (four warps needed
 //               6500 cycles a tile, the products 4100)
 //   warps 12-15 rows: gather, swizzle (128-byte atoms), rope keys
+//   warp 2      (CTA 1 of a pair) tells CTA 0 of landed rows
 // kPair: two CTAs of a cluster work on one tile of 256 rows x 256 columns
 // (cta_group::2): each holds its 128 rows and half of the weights' columns,
 // CTA 0 issues for both.  That halves the weights that every SM reads from L2,
@@ -121,8 +122,9 @@ __device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int 
       "r"(src), "r"(x), "r"(y), "r"(z), "l"(policy)
       : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes, or 16 zero bytes with nothing read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest N of this thread's committed groups have landed.
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
-    for (int k = 0; k < kChunks; ++k) { mbar_init(a_full(k), 4 * C::kCtas); mbar_init(a_free(k), 1); }
+    for (int k = 0; k < kChunks; ++k) { mbar_init(a_full(k), kPair && rank == 0 ? 5 : 4); mbar_init(a_free(k), 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), kEpiWarps * C::kCtas); }
     *abort_flag = 0;
     fence_mbar_init();
@@ -292,6 +294,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp == 2 && rank == 1) {
+    // Tells CTA 0 of this CTA's rows.  From a warp of its own: a release at cluster scope waits for what its
+    // warp has in flight, and the row warps have the next chunks' copies (1200 cycles a chunk).
+    if (lane == 0) {
+      uint32_t block = 0;
+      bool ok = true;
+      for (int t = t0; t < t1 && ok; t = (t / cols + 1) * cols, ++block)
+        for (int k = 0; k < kChunks && ok; ++k) {
+          ok = mbar_wait(a_full(k), block & 1, wc);
+          if (ok) mbar_arrive_cluster(a_full(k), 0);
+        }
+    }
+    __syncwarp();
   } else if (warp >= kRowWarp0) {
     // ------------------------------------------------------------------ rows
     const int rt = threadIdx.x - 32 * kRowWarp0;             // 0..127
@@ -299,88 +314,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t block = 0;
     for (int t = t0; t < t1; t = (t / cols + 1) * cols, ++block) {
       const int m0 = (t / cols) * tile_rows + static_cast<int>(rank) * BM;
-      // a thread's rows are 16 i + rt / 8
+      // a thread's rows are 16 i + rt / 8; the rows past the last are zeros, not read (one row read for all of
+      // them is 128 reads of the same lines, 6 us)
       long long row[8];
       bool oob = false;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = min(m0 + 16 * i + (rt >> 3), p.tokens - 1);
-        long long slot = __ldg(p.kv_indices + r);
+        const int r = m0 + 16 * i + (rt >> 3);
+        long long slot = r < p.tokens ? __ldg(p.kv_indices + r) : 0;
         if (slot < 0 || slot >= p.num_slots) { oob = true; slot = 0; }
-        row[i] = slot * (kFp8 ? kRow : 2 * kRow);
+        row[i] = r < p.tokens ? slot * (kFp8 ? kRow : 2 * kRow) : -1;
       }
       if (oob) record_status(p.status, MLA_ERR_INDEX_OOB);
       bool ok = true;
       // chunk k's place is free once the block before has used it
       auto wait_free = [&](int k) {
-        if (block == 0) return;
+        if (block == 0 || !ok) return;
         bool f = true;
         if (lane == 0) f = mbar_wait(a_free(k), (block - 1) & 1, wc);
         ok = __shfl_sync(0xffffffffu, f, 0) && ok;
       };
-      auto landed = [&](int k) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (kPair) mbar_arrive_cluster(a_full(k), 0);
-          else mbar_arrive(a_full(k));
-        }
-      };
-      if constexpr (kFp8) {
-        // 16 codes a lane are two pieces of chunk k + sub / 4: two chunks at a time, two of those in flight
-        uint4 v[2][8];
-        auto load = [&](int k, uint4 (&x)[8]) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(p.kv_cache + row[i] + k * 64) + sub);
-        };
-        load(0, v[0]);
-        load(2, v[1]);
-#pragma unroll
-        for (int g = 0; g < kChunks / 2; ++g) {
-          wait_free(2 * g);
-          wait_free(2 * g + 1);
-          if (!ok) break;
-          uint4 (&x)[8] = v[g & 1];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = 16 * i + (rt >> 3), c = 2 * (sub & 3);
-            uint8_t* dst = smem + (2 * g + (sub >> 2)) * (BM * 128) + r * 128;
-            *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) << 4)) =
-                make_uint4(e4m3x2_to_bf16x2(x[i].x), e4m3x2_to_bf16x2(x[i].x >> 16), e4m3x2_to_bf16x2(x[i].y),
-                           e4m3x2_to_bf16x2(x[i].y >> 16));
-            *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (r & 7)) << 4)) =
-                make_uint4(e4m3x2_to_bf16x2(x[i].z), e4m3x2_to_bf16x2(x[i].z >> 16), e4m3x2_to_bf16x2(x[i].w),
-                           e4m3x2_to_bf16x2(x[i].w >> 16));
-          }
-          if (g + 2 < kChunks / 2) load(2 * g + 4, x);
-          landed(2 * g);
-          landed(2 * g + 1);
-        }
-      } else {
-        auto load = [&](int k) {
+      // 16 bytes a lane and row: an eighth of a bf16 chunk's row; a quarter of an FP8 chunk's, for half the rows
+      // each of the chunk's two lane groups (rows 16 i + rt / 8 with i even for lanes of sub < 4, odd for others)
+      auto load = [&](int k) {
+        const uint32_t chunk = base + k * (BM * 128);
+        if constexpr (kFp8) {
+          // the codes wait in the chunk's upper half, 64 bytes a row, until they are widened over it
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = 16 * i + (rt >> 3);
-            cp_async16(base + k * (BM * 128) + r * 128 + ((sub ^ (r & 7)) << 4), p.kv_cache + row[i] + k * 128 + sub * 16);
+            if ((i & 1) == (sub >> 2))
+              cp_async16(chunk + BM * 64 + r * 64 + (sub & 3) * 16, p.kv_cache + max(row[i], 0ll) + k * 64 + (sub & 3) * 16,
+                         row[i] >= 0);
           }
-        };
-        // four chunks on their way; the first block's all at once, as it has nothing to wait for
-        auto run = [&](auto lag) {
-          constexpr int kLag = decltype(lag)::value;
+        } else {
 #pragma unroll
-          for (int k = 0; k < kChunks + kLag; ++k) {
-            if (k < kChunks && ok) wait_free(k);
-            if (k < kChunks && ok) load(k);
-            cp_async_commit();                               // empty groups keep the count
-            if (k >= kLag) {
-              cp_async_wait<kLag>();
-              if (ok) landed(k - kLag);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const int r = 16 * i + (rt >> 3);
+            cp_async16(chunk + r * 128 + ((sub ^ (r & 7)) << 4), p.kv_cache + max(row[i], 0ll) + k * 128 + sub * 16,
+                       row[i] >= 0);
           }
-        };
-        if (block == 0) run(std::integral_constant<int, kChunks - 1>{});
-        else run(std::integral_constant<int, 3>{});
-      }
+        }
+      };
+      auto landed = [&](int k) {
+        if constexpr (kFp8) {
+          // each thread widens what it loaded itself, once all have taken theirs into registers
+          uint8_t* chunk = smem + k * (BM * 128);
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 16 * (2 * i + (sub >> 2)) + (rt >> 3);
+            x[i] = *reinterpret_cast<const uint4*>(chunk + BM * 64 + r * 64 + (sub & 3) * 16);
+          }
+          named_bar_sync(1, 128);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 16 * (2 * i + (sub >> 2)) + (rt >> 3), c = 2 * (sub & 3);
+            *reinterpret_cast<uint4*>(chunk + r * 128 + ((c ^ (r & 7)) << 4)) =
+                make_uint4(e4m3x2_to_bf16x2(x[i].x), e4m3x2_to_bf16x2(x[i].x >> 16), e4m3x2_to_bf16x2(x[i].y),
+                           e4m3x2_to_bf16x2(x[i].y >> 16));
+            *reinterpret_cast<uint4*>(chunk + r * 128 + (((c + 1) ^ (r & 7)) << 4)) =
+                make_uint4(e4m3x2_to_bf16x2(x[i].z), e4m3x2_to_bf16x2(x[i].z >> 16), e4m3x2_to_bf16x2(x[i].w),
+                           e4m3x2_to_bf16x2(x[i].w >> 16));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(a_full(k));
+      };
+      // four chunks on their way; the first block's all at once, as it has nothing to wait for
+      auto run = [&](auto lag) {
+        constexpr int kLag = decltype(lag)::value;
+#pragma unroll 1                                               // (code run once comes slowly: the loop stays short)
+        for (int k = 0; k < kChunks + kLag; ++k) {
+          if (k < kChunks) wait_free(k);
+          if (k < kChunks && ok) load(k);
+          cp_async_commit();                                 // empty groups keep the count
+          if (k >= kLag) {
+            cp_async_wait<kLag>();
+            landed(k - kLag);                                // (after a wait that gave up, of what is there)
+          }
+        }
+      };
+      if (block == 0) run(std::integral_constant<int, kChunks - 1>{});
+      else run(std::integral_constant<int, 3>{});
       if (!ok) break;
       if (t % cols == 0) {                                   // the CTA with the block's first tile writes its rope keys
 #pragma unroll
