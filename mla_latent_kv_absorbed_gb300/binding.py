@@ -481,11 +481,19 @@ def rope_frequencies(theta: float = 10000.0, scaling: str = "none", factor: floa
     return freqs
 
 
+def _host_ptr(a) -> int:
+    """Address of a numpy array (through the buffer protocol: a third of `ctypes.data`'s time)."""
+    try:
+        return ctypes.addressof(ctypes.c_char.from_buffer(a))
+    except TypeError:                                # a read-only array
+        return a.ctypes.data
+
+
 def _freqs_ptr(where, freqs):
     if not isinstance(freqs, np.ndarray) or freqs.dtype != np.uint64 or freqs.shape != (32,) or \
             not freqs.flags.c_contiguous:
         raise ValueError(f"{where}: freqs is the uint64 array of rope_frequencies")
-    return freqs.__array_interface__["data"][0]
+    return _host_ptr(freqs)
 
 
 def rope_query(q, positions, freqs, q_rope, q_nope=None, amplitude: float = 1.0, interleaved: bool = True,
@@ -626,9 +634,11 @@ def prefill_run(plan_host, plan_dev, q, k_nope, k_rope, v, sm_scale: float, out,
     that are multiples of 8), out bf16 [Tq,H,128], lse fp32 [Tq,H] or None, workspace uint8 (zero-filled once)."""
     import torch
     w, bf = "mla_prefill_run", torch.bfloat16
-    if not isinstance(plan_host, np.ndarray) or plan_host.dtype != np.int32 or plan_host.shape[0] < 16:
+    if not isinstance(plan_host, np.ndarray) or plan_host.dtype != np.int32 or plan_host.size < 16 or \
+            not plan_host.flags.c_contiguous:
         raise ValueError(f"{w}: plan_host is the int32 array of prefill_plan")
-    H, nq, nk = int(plan_host[_P_HEADS]), int(plan_host[_P_Q]), int(plan_host[_P_KV])
+    head = plan_host[:16].tolist()
+    H, nq, nk = head[_P_HEADS], head[_P_Q], head[_P_KV]
     _need(w, "plan_dev", plan_dev, torch.int32, (plan_host.shape[0],))
     _need(w, "q", q, bf, (nq, H, 192), dense=False)
     _need(w, "k_nope", k_nope, bf, (nk, H, 128), dense=False)
@@ -640,7 +650,7 @@ def prefill_run(plan_host, plan_dev, q, k_nope, k_rope, v, sm_scale: float, out,
     _need(w, "workspace", workspace, torch.uint8, (workspace.numel(),))
     st = _launch_stream(w, stream, plan_dev, q, k_nope, k_rope, v, out, lse, workspace)
     (qt, qh, _), (kt, kh, _), (vt, vh, _) = q.stride(), k_nope.stride(), v.stride()
-    st = _lib.mla_prefill_run(plan_host.ctypes.data, plan_dev.data_ptr(), q.data_ptr(), qt, qh, k_nope.data_ptr(), kt,
+    st = _lib.mla_prefill_run(_host_ptr(plan_host), plan_dev.data_ptr(), q.data_ptr(), qt, qh, k_nope.data_ptr(), kt,
                               kh, k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), vt, vh, sm_scale,
                               out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), st)
     if st != MLA_OK:
