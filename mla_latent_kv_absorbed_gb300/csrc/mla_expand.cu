@@ -330,9 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // chunk k's place is free once the block before has used it
       auto wait_free = [&](int k) {
         if (block == 0 || !ok) return;
-        bool f = true;
-        if (lane == 0) f = mbar_wait(a_free(k), (block - 1) & 1, wc);
-        ok = __shfl_sync(0xffffffffu, f, 0) && ok;
+        ok = __all_sync(0xffffffffu, mbar_wait(a_free(k), (block - 1) & 1, wc));
       };
       // 16 bytes a lane and row: an eighth of a bf16 chunk's row; a quarter of an FP8 chunk's, for half the rows
       // each of the chunk's two lane groups (rows 16 i + rt / 8 with i even for lanes of sub < 4, odd for others)
@@ -430,10 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int col = t % cols, h = (col % groups) * C::kHeads;
       const int r0 = (t / cols) * tile_rows + static_cast<int>(rank) * BM + 32 * q;
       const uint32_t buf = i & 1;
-      bool ok = true;
-      if (lane == 0) ok = mbar_wait(acc_full(buf), (i >> 1) & 1, wc);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(acc_full(buf), (i >> 1) & 1, wc))) break;
       tc_fence_after();
       const int end = min((half + 1) * (NT / 2), (p.heads - h) * kNope);   // an odd last head: half a tile
 #pragma unroll 1
