@@ -46,24 +46,26 @@ using TileB = std::integral_constant<int, 1>;
 
 constexpr int kThreads = 640;
 constexpr int kProducer = 16, kIssuer = 17, kGuard = 18;
-constexpr int kSlots = 8;                             // of 16 KB: 5 a tile in turn, 3 of keys, 2 of values
 constexpr int kBlock = 16384;
 constexpr int kOffQ = 0;                              // 2 row tiles x 3 blocks of 128 rows x 64 dims
 // The ring, in the order of use: keys of tile t as blocks 5t .. 5t+2 (128 keys
 // x 64 dims), its values as 5t+3, 5t+4 (64 keys x 128 dims, two 64-dim chunks).
+// A pair's CTA has half of each: blocks of 64 keys x 64 dims.
 constexpr int kOffRing = 6 * kBlock;
-constexpr int kOffBar = kOffRing + kSlots * kBlock;
+constexpr int kRingBytes = 8 * kBlock;
+constexpr int kOffBar = kOffRing + kRingBytes;
+constexpr int kDepth = 4;                             // tiles told apart: more than the ring holds
 constexpr int kSched = 4;                             // items announced ahead
 constexpr int kMasked = 8;                            // masked tiles told apart: two items' worth and more
-constexpr int kConsumers = 16 + 1 + 2;                // warps that read an announced item
+constexpr int kConsumers = 16 + 1 + 2;                // warps that read an announced item (in CTA 1: no issuer, but the producer)
 enum Bar : int {
   bQFull = 0,                    // [2] per row tile
   bQFree = bQFull + 2,           // the item's last scores are done
-  bKFull = bQFree + 1,           // [2] key tile T on T & 1, T counting the CTA's tiles over all items
-  bVFull = bKFull + 2,           // [2] the values of whole tile U (that every row sees whole) on U & 1
-  bKFree = bVFull + 2,           // [2] its QK products are done
-  bVFree = bKFree + 2,           // [2]
-  bSFull = bVFree + 2,           // [2] per row tile
+  bKFull = bQFree + 1,           // [4] key tile T on T & 3, T counting the CTA's tiles over all items
+  bVFull = bKFull + kDepth,      // [4] the values of whole tile U (that every row sees whole) on U & 3
+  bKFree = bVFull + kDepth,      // [4] its QK products are done
+  bVFree = bKFree + kDepth,      // [4]
+  bSFull = bVFree + kDepth,           // [2] per row tile
   bPFull = bSFull + 2,           // [2]
   bPvDone = bPFull + 2,          // [2]
   bVMasked = bPvDone + 2,         // [8] the values of masked tile M (on M & 7) have landed
@@ -74,8 +76,8 @@ enum Bar : int {
   kBars
 };
 constexpr int kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16;   // TMEM address, abort flag
-constexpr int kOffBad = kOffMisc + 16;                // [8][4] words: bit j = key j of masked tile M
-constexpr int kOffSched = kOffBad + 16 * kMasked;     // [4] announced items, 8 words each
+constexpr int kOffBad = kOffMisc + 16;                // [8][2][4] words: bit j = key j of masked tile M, by the CTA that saw it
+constexpr int kOffSched = kOffBad + 32 * kMasked;     // [4] announced items, 8 words each
 constexpr int kOffMeet = kOffSched + 32 * kSched;      // [8][32] floats: where a row's two threads meet
 constexpr int kSmemBytes = kOffMeet + 1024 + 1024;
 static_assert(kOffSched % 16 == 0, "announced items are read as 16-byte words");
@@ -83,17 +85,22 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;          // S_A, S_B, O_A, O_B: 128 columns each
 constexpr float kSlack = 8.f;                         // log2 growth of the maximum that moves the reference
 
+// Rows of a row tile's products: one CTA's 128, or a pair's 256.
+template <bool kPair>
+constexpr int kTileRows = kPair ? 256 : 128;
+
 struct Item {
   int q0, nq, k0, nk, off, part, h;
 };
 
 // The item's words, or false (and MLA_ERR_PLAN_MISMATCH) when it does not lie
 // inside the arrays of this launch or has keys past its last row's limit.
+template <bool kPair>
 __device__ __forceinline__ bool load_item(const PrefillParams& p, int i, Item& it) {
   const int4 a = __ldg(reinterpret_cast<const int4*>(p.items) + 2 * i);
   const int4 b = __ldg(reinterpret_cast<const int4*>(p.items) + 2 * i + 1);
   it = Item{a.y, a.z, a.w, b.x, b.y, b.z, 0};
-  return it.q0 >= 0 && it.nq >= 1 && it.nq <= kPfRows && it.q0 <= p.q_tokens - it.nq && it.k0 >= 0 && it.nk >= 0 &&
+  return it.q0 >= 0 && it.nq >= 1 && it.nq <= 2 * kTileRows<kPair> && it.q0 <= p.q_tokens - it.nq && it.k0 >= 0 && it.nk >= 0 &&
          it.k0 <= p.kv_tokens - it.nk && it.part >= -1 && it.part < p.partials && it.off >= -kPfNoLimit &&
          it.off <= kPfNoLimit && (it.nk == 0 || it.nk <= it.off + it.nq);
 }
@@ -101,11 +108,11 @@ __device__ __forceinline__ bool load_item(const PrefillParams& p, int i, Item& i
 // What an item asks of each row tile.
 struct Shape {
   int n_a, n_b, n;             // key tiles that some row of A, of B, of either sees
-  int whole;                   // the first of them are seen whole by every row; at most three follow
-  __device__ __forceinline__ explicit Shape(const Item& it) {
+  int whole;                   // the first of them are seen whole by every row; at most three (a pair: five) follow
+  __device__ __forceinline__ Shape(const Item& it, int rows) {
     auto tiles = [&](int w) -> int {
-      if (it.nq <= 128 * w) return 0;
-      const int last = min(it.nk, it.off + min(it.nq, 128 * w + 128));    // keys that the tile's last row sees
+      if (it.nq <= rows * w) return 0;
+      const int last = min(it.nk, it.off + min(it.nq, rows * w + rows));  // keys that the tile's last row sees
       return last > 0 ? (last + kPfKeys - 1) / kPfKeys : 0;
     };
     n_a = tiles(0);
@@ -123,6 +130,46 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
       : "memory");
 }
 
+// ---- the two-CTA forms: a load counted on a barrier of either CTA, products of
+// 256 rows issued by CTA 0, commits to both.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, int x, int y, uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar_cluster)
+      : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+// Arrive on the barrier at this offset in CTA 0; orders nothing but TMEM
+// accesses that the caller has waited for and fenced (a release at cluster
+// scope waits for global stores on their way).
+__device__ __forceinline__ void arrive_leader_relaxed(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b32 rb;\n\t"
+      "mapa.shared::cluster.u32 rb, %0, 0;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [rb];\n\t}" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void st_cluster_b32(uint32_t addr_cluster, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr_cluster), "r"(v) : "memory");
+}
+
 // 32 lanes x 32 consecutive columns.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -138,8 +185,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 // The products with their shared-memory descriptors in halves: the upper word
 // (strides, layout) is a constant, only the lower one (address, leading stride)
 // changes from MMA to MMA.
-template <uint32_t kHigh>
+template <uint32_t kHigh, bool kPair>
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, bool accumulate) {
+  if constexpr (kPair) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kHigh)
+      : "memory");
+    return;
+  }
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
       "mov.b64 da, {%1, %5};\n\t"
@@ -149,8 +207,18 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t
       "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kHigh)
       : "memory");
 }
-template <uint32_t kHigh>
+template <uint32_t kHigh, bool kPair>
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, bool accumulate) {
+  if constexpr (kPair) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kHigh)
+      : "memory");
+    return;
+  }
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
       "mov.b64 db, {%2, %5};\n\t"
@@ -182,8 +250,9 @@ __device__ __noinline__ void rescale_columns(uint32_t taddr, float f) {
 
 // The warp waits, every lane for itself (through one lane and a shuffle it took
 // 7% of the kernel's time longer); all return the same outcome.
+template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& wc) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
+  return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, wc));
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -204,6 +273,7 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) return;
 }
 
+template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_v,
@@ -219,20 +289,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + kOffBad);
   int* sched = reinterpret_cast<int*>(smem + kOffSched);
   const WaitCtx wc{abort_flag, p.status};
+  constexpr int kRingBlock = kPair ? kBlock / 2 : kBlock, kSlots = kRingBytes / kRingBlock;
+  constexpr int kCtas = kPair ? 2 : 1;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0;
+  const uint32_t peer = rank ^ 1u;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
       const bool eight = i >= bPFull && i < bPFull + 2;
       const bool two = i >= bVClean && i < bVClean + kMasked;
       const bool all = i >= bSchedFree && i < bSchedFree + kSched;
-      mbar_init(bar(i), eight ? 8 : two ? 2 : all ? kConsumers : 1);
+      mbar_init(bar(i), eight ? 8 * kCtas : two ? 2 * kCtas : all ? kConsumers * kCtas : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
+  for (int i = threadIdx.x; i < 8 * kMasked; i += kThreads) bad[i] = 0;
   if (warp == kIssuer) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), 512);
+      tmem_relinquish();
+    }
   }
   if (warp == kProducer && lane == 0) {
     tma_prefetch_desc(&tm_q);
@@ -241,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) cluster_sync_all();              // both CTAs' barriers exist before any remote use
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
@@ -255,10 +336,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto release_item = [&](uint32_t k) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar(bSchedFree + k % kSched));
+    if (lane == 0) {
+      if constexpr (kPair) mbar_arrive_cluster(bar(bSchedFree + k % kSched), 0);
+      else mbar_arrive(bar(bSchedFree + k % kSched));
+    }
   };
   auto next_item = [&](uint32_t k, Item& it) -> bool {
-    if (!warp_wait(bar(bSched + k % kSched), (k / kSched) & 1, wc)) return false;
+    if (!warp_wait<kPair>(bar(bSched + k % kSched), (k / kSched) & 1, wc)) return false;
     const bool there = announced(k, it);
     release_item(k);
     return there;
@@ -275,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g = w / per_group, rest = w - g * per_group;
         const int in_group = min(p.head_group, p.heads - g * p.head_group);
         const int item = rest / in_group;
-        if (!load_item(p, item, it)) {
+        if (!load_item<kPair>(p, item, it)) {
           record_status(p.status, MLA_ERR_PLAN_MISMATCH);
           it.nk = it.nq = 0;
         }
@@ -283,46 +367,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto announce = [&](uint32_t k, const Item& it, bool there) {
         const int s = k % kSched;
-        if (k >= kSched && !mbar_wait(bar(bSchedFree + s), ((k / kSched) - 1) & 1, wc)) { ok = false; return; }
+        if (k >= kSched && !mbar_wait<kPair>(bar(bSchedFree + s), ((k / kSched) - 1) & 1, wc)) { ok = false; return; }
+        if constexpr (kPair) {
+          // to CTA 1 as stores that its barrier counts (its producer arms it)
+          const uint32_t to = mapa_shared(base + kOffSched + 32 * s, 1), tb = mapa_shared(bar(bSched + s), 1);
+          st_async_v4(to, it.q0, it.nq, it.k0, it.nk, tb);
+          st_async_v4(to + 16, it.off, it.part, it.h, there ? 1 : 0, tb);
+        }
         reinterpret_cast<int4*>(sched)[2 * s] = make_int4(it.q0, it.nq, it.k0, it.nk);
         reinterpret_cast<int4*>(sched)[2 * s + 1] = make_int4(it.off, it.part, it.h, there ? 1 : 0);
         mbar_arrive(bar(bSched + s));
+      };
+      // CTA 1's producer: the k-th item as CTA 0 announces it; false when there is none left (or on an abort)
+      auto hear = [&](uint32_t k, Item& it) -> bool {
+        mbar_arrive_expect_tx(bar(bSched + k % kSched), 32);
+        ok = mbar_wait<kPair>(bar(bSched + k % kSched), (k / kSched) & 1, wc);
+        if (!ok) return false;
+        const bool there = announced(k, it);
+        mbar_arrive_cluster(bar(bSchedFree + k % kSched), 0);
+        return there;
       };
       int tbase = 0, ubase = 0, mbase = 0;                    // tiles before this item: all, whole, masked
       uint32_t q_items[2] = {0, 0}, busy = 0;                 // items with queries in the row tile, in either
       int k_armed = 0, q_bar[2] = {-1, -1};                   // what may be in flight: key tiles, query tiles,
       int v_new = -1, v_old = -1;                             // the last two tiles' values (barrier * 2 + parity)
       Item it;
-      fetch(blockIdx.x, it);
-      announce(0, it, true);
+      if (rank == 0) {
+        fetch(blockIdx.x / kCtas, it);
+        announce(0, it, true);
+      } else {
+        hear(0, it);                                          // (every pair has an item)
+      }
       for (uint32_t k = 0; ok; ++k) {
-        const Shape sh(it);
+        const Shape sh(it, kTileRows<kPair>);
+        auto load_3d = [&](uint32_t dst, const CUtensorMap* m, int x, int z, int b) {
+          if constexpr (kPair) tma_load_3d_pair(dst, m, x, it.h, z, mapa_shared(bar(b), 0));
+          else tma_load_3d(dst, m, x, it.h, z, bar(b));
+        };
         auto load_q = [&](auto W) {
           constexpr int w = W.value;
           q_bar[w] = q_items[w] & 1;
           ++q_items[w];
-          mbar_arrive_expect_tx(bar(bQFull + w), 3 * kBlock);
+          // (a pair's barriers of landed queries, keys and values are CTA 0's, which counts both halves)
+          if (rank == 0) mbar_arrive_expect_tx(bar(bQFull + w), kCtas * 3 * kBlock);
           for (int i = 0; i < 3; ++i)
-            tma_load_3d(base + kOffQ + (3 * w + i) * kBlock, &tm_q, 64 * i, it.h, it.q0 + 128 * w, bar(bQFull + w));
+            load_3d(base + kOffQ + (3 * w + i) * kBlock, &tm_q, 64 * i, it.q0 + kTileRows<kPair> * w + 128 * static_cast<int>(rank),
+                    bQFull + w);
         };
-        // the place of block c, once the block before in it (c - 8) has been used
+        // the place of block c, once the block before in it (c - kSlots) has been used
         auto place = [&](int c) -> uint32_t {
           if (c >= kSlots) {
             const int u = (c - kSlots) / 5;
             const int b = (c - kSlots) % 5 < 3 ? bKFree : bVFree;
-            ok = mbar_wait(bar(b + (u & 1)), (u >> 1) & 1, wc);
+            ok = mbar_wait(bar(b + u % kDepth), (u / kDepth) & 1, wc);
           }
-          return base + kOffRing + (c % kSlots) * kBlock;
+          return base + kOffRing + (c % kSlots) * kRingBlock;
         };
         auto load_k = [&](int t) {
           const int T = tbase + t;
           for (int i = 0; i < 3 && ok; ++i) {
-            const uint32_t dst = place(5 * T + i), b = bar(bKFull + (T & 1));
+            const uint32_t dst = place(5 * T + i);
+            const int b = bKFull + T % kDepth, key = it.k0 + t * kPfKeys + 64 * static_cast<int>(rank);
             if (!ok) break;
-            if (i == 0) mbar_arrive_expect_tx(b, 3 * kBlock);
+            if (i == 0 && rank == 0) mbar_arrive_expect_tx(bar(b), 3 * kBlock);
             k_armed = T + 1;
-            if (i < 2) tma_load_3d(dst, &tm_k, 64 * i, it.h, it.k0 + t * kPfKeys, b);
-            else tma_load_2d(dst, &tm_kr, 0, it.k0 + t * kPfKeys, b);
+            if (i < 2) load_3d(dst, &tm_k, 64 * i, key, b);
+            else if constexpr (kPair) tma_load_2d_pair(dst, &tm_kr, 0, key, mapa_shared(bar(b), 0));
+            else tma_load_2d(dst, &tm_kr, 0, key, bar(b));
           }
         };
         auto load_v = [&](int t) {
@@ -330,20 +441,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 2 && ok; ++i) {
             const uint32_t dst = place(5 * T + 3 + i);
             if (!ok) break;
-            const int b = t < sh.whole ? bVFull + (U & 1) : bVMasked + M % kMasked;
+            // masked tiles' values are counted by the CTA whose guard goes over them
+            const bool masked = t >= sh.whole;
+            const int b = masked ? bVMasked + M % kMasked : bVFull + U % kDepth;
             if (i == 0) {
               v_old = v_new;
-              v_new = 2 * b + (t < sh.whole ? (U >> 1) & 1 : (M / kMasked) & 1);
+              v_new = 2 * b + (masked ? (M / kMasked) & 1 : (U / kDepth) & 1);
+              if (masked) mbar_arrive_expect_tx(bar(b), 2 * kRingBlock);
+              else if (rank == 0) mbar_arrive_expect_tx(bar(b), 2 * kBlock);
             }
-            if (i == 0) mbar_arrive_expect_tx(bar(b), 2 * kBlock);
-            for (int x = 0; x < 2; ++x)
-              tma_load_3d(dst + x * (kBlock / 2), &tm_v, 64 * x, it.h, it.k0 + t * kPfKeys + 64 * i, bar(b));
+            const int key = it.k0 + t * kPfKeys + 64 * i;
+            if constexpr (kPair) {
+              if (masked) tma_load_3d(dst, &tm_v, 64 * static_cast<int>(rank), it.h, key, bar(b));
+              else load_3d(dst, &tm_v, 64 * static_cast<int>(rank), key, b);
+            } else {
+              for (int x = 0; x < 2; ++x) tma_load_3d(dst + x * (kBlock / 2), &tm_v, 64 * x, it.h, key, bar(b));
+            }
           }
         };
         Item next{};
         bool more = false;
         auto look_ahead = [&] {
-          const int w = atomicAdd(p.status + kWsCounter, 1) + static_cast<int>(gridDim.x);
+          if (rank != 0) {
+            more = hear(k + 1, next);
+            return;
+          }
+          const int w = atomicAdd(p.status + kWsCounter, 1) + static_cast<int>(gridDim.x) / kCtas;
           more = w < total;
           if (more) fetch(w, next);
           announce(k + 1, next, more);
@@ -364,12 +487,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!more) break;
         it = next;
       }
-      if (!ok) {                                              // no copy outlives the block
-        if (q_bar[0] >= 0) drain_wait(bar(bQFull), q_bar[0]);
-        if (q_bar[1] >= 0) drain_wait(bar(bQFull + 1), q_bar[1]);
-        for (int T = max(0, k_armed - 2); T < k_armed; ++T) drain_wait(bar(bKFull + (T & 1)), (T >> 1) & 1);
-        if (v_old >= 0) drain_wait(bar(v_old >> 1), v_old & 1);
-        if (v_new >= 0) drain_wait(bar(v_new >> 1), v_new & 1);
+      if (!ok) {                                              // no copy outlives the block (a pair: the pair)
+        if (rank == 0) {
+          if (q_bar[0] >= 0) drain_wait(bar(bQFull), q_bar[0]);
+          if (q_bar[1] >= 0) drain_wait(bar(bQFull + 1), q_bar[1]);
+          for (int T = max(0, k_armed - kDepth); T < k_armed; ++T) drain_wait(bar(bKFull + T % kDepth), (T / kDepth) & 1);
+        }
+        for (int x : {v_old, v_new})
+          if (x >= 0 && (rank == 0 || (x >> 1) >= bVMasked)) drain_wait(bar(x >> 1), x & 1);
       }
     }
     __syncwarp();
@@ -379,11 +504,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // descriptors are then uniform to the compiler (64 cycles an MMA; run by a
     // single lane, 118).  The loop is kept short: what it does between the
     // products is not hidden, as the tensor core's queue holds about four MMAs.
-    auto uwait = [&](int b, uint32_t parity) -> bool { return mbar_wait(bar(b), parity, wc); };
+    auto uwait = [&](int b, uint32_t parity) -> bool { return mbar_wait<kPair>(bar(b), parity, wc); };
     const bool lead = elect_one();
-    const uint32_t idesc_s = idesc_bf16(128, 128, false, false) | (p.negate ? 1u << 13 : 0u);   // -Q
-    constexpr uint32_t kIdescO = idesc_bf16(128, 128, false, true);
-    auto block_at = [&](int c) -> uint32_t { return base + kOffRing + (c % kSlots) * kBlock; };
+    const uint32_t idesc_s = idesc_bf16(kTileRows<kPair>, 128, false, false) | (p.negate ? 1u << 13 : 0u);   // -Q
+    constexpr uint32_t kIdescO = idesc_bf16(kTileRows<kPair>, 128, false, true);
+    auto block_at = [&](int c) -> uint32_t { return base + kOffRing + (c % kSlots) * kRingBlock; };
     // scores of key tile T for row tile w
     auto qk = [&](int T, int w) {
       const uint32_t d = tmem + kTmemS + 128 * w;
@@ -393,9 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lead) {
 #pragma unroll
         for (int k = 0; k < 12; ++k)
-          mma_ss<kDescHigh>(d, a + (k >> 2) * (kBlock >> 4) + 2 * (k & 3), (k < 4 ? b0 : k < 8 ? b1 : b2) + 2 * (k & 3),
+          mma_ss<kDescHigh, kPair>(d, a + (k >> 2) * (kBlock >> 4) + 2 * (k & 3), (k < 4 ? b0 : k < 8 ? b1 : b2) + 2 * (k & 3),
                             idesc_s, k > 0);
-        umma_commit(bar(bSFull + w));
+        commit<kPair>(bar(bSFull + w));
       }
     };
     auto pv = [&](int T, int w, bool first) {
@@ -404,19 +529,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lead) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_ts<kDescHigh>(d, a + 8 * k, (k < 4 ? b0 : b1) + 128 * (k & 3), kIdescO, !first || k > 0);
-        umma_commit(bar(bPvDone + w));
+          mma_ts<kDescHigh, kPair>(d, a + 8 * k, (k < 4 ? b0 : b1) + 128 * (k & 3), kIdescO, !first || k > 0);
+        commit<kPair>(bar(bPvDone + w));
       }
     };
-    auto wait_k = [&](int T) { return uwait(bKFull + (T & 1), (T >> 1) & 1); };
+    auto wait_k = [&](int T) { return uwait(bKFull + T % kDepth, (T / kDepth) & 1); };
     int tbase = 0, ubase = 0, mbase = 0;
     uint32_t items = 0, steps = 0;                            // bit w: parity of row tile w's items begun, P tiles taken
     bool ok = true;
     Item it;
     // A wait that gives up makes `ok` false; what is issued until the check at the end of the tile stays inside
     // shared memory and TMEM.
-    for (uint32_t k = 0; ok && next_item(k, it); ++k) {
-      const Shape sh(it);
+    for (uint32_t k = 0; rank == 0 && ok && next_item(k, it); ++k) {
+      const Shape sh(it, kTileRows<kPair>);
       if (sh.n == 0) continue;
       // the first scores: they may run while the epilogue of the item before reads its output
       ok = wait_k(tbase);
@@ -429,12 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         qk(tbase, w);
       }
       if (lead) {
-        umma_commit(bar(bKFree + (tbase & 1)));
-        if (sh.n == 1) umma_commit(bar(bQFree));
+        commit<kPair>(bar(bKFree + tbase % kDepth));
+        if (sh.n == 1) commit<kPair>(bar(bQFree));
       }
       for (int t = 0; t < sh.n && ok; ++t) {
         const int T = tbase + t, U = ubase + t, M = mbase + t - sh.whole;
-        ok &= t < sh.whole ? uwait(bVFull + (U & 1), (U >> 1) & 1)
+        ok &= t < sh.whole ? uwait(bVFull + U % kDepth, (U / kDepth) & 1)
                            : uwait(bVClean + M % kMasked, (M / kMasked) & 1);
         // P of an item's first tile also tells that its warps have read the output of the item before
 #pragma unroll 1
@@ -453,17 +578,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (lead) {
-          umma_commit(bar(bVFree + (T & 1)));
-          if (t + 1 < sh.n) umma_commit(bar(bKFree + ((T + 1) & 1)));
-          if (t + 2 == sh.n) umma_commit(bar(bQFree));
+          commit<kPair>(bar(bVFree + T % kDepth));
+          if (t + 1 < sh.n) commit<kPair>(bar(bKFree + (T + 1) % kDepth));
+          if (t + 2 == sh.n) commit<kPair>(bar(bQFree));
         }
       }
       tbase += sh.n;
       ubase += sh.whole;
       mbase += sh.n - sh.whole;
     }
-    if (lead) umma_commit(bar(bDrain));
-    drain_wait(bar(bDrain), 0);                               // every MMA has finished before TMEM is given back
+    if (rank == 0) {
+      if (lead) commit<kPair>(bar(bDrain));
+      drain_wait(bar(bDrain), 0);                             // every MMA has finished before TMEM is given back
+    }
     __syncwarp();
   } else if (warp >= kGuard) {
     // ---------------------------------------------------------------- guard
@@ -472,11 +599,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it;
     bool ok = true;
     for (uint32_t k = 0; ok && next_item(k, it); ++k) {
-      const Shape sh(it);
+      const Shape sh(it, kTileRows<kPair>);
       for (int t = sh.whole; t < sh.n; ++t, ++M) {
         ok = warp_wait(bar(bVMasked + M % kMasked), (M / kMasked) & 1, wc);
         if (!ok) break;
-        uint8_t* half = smem + kOffRing + ((5 * (tbase + t) + 3 + g) % kSlots) * kBlock;
+        uint8_t* half = smem + kOffRing + ((5 * (tbase + t) + 3 + g) % kSlots) * kRingBlock;
 #pragma unroll 1
         for (int m = 2 * g; m < 2 * g + 2; ++m) {
           const int r = 32 * (m & 1) + lane;                  // row of this half's 64: key 32 m + lane of the tile
@@ -485,14 +612,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto chunk = [&](int c) {
             return reinterpret_cast<uint4*>(half + (c >> 3) * (kBlock / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
           };
-          uint4 v[16];
+          constexpr int kChunks = kPair ? 8 : 16;             // of a key's values that lie here
+          uint4 v[kChunks];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) v[c] = *chunk(c);
+          for (int c = 0; c < kChunks; ++c) v[c] = *chunk(c);
           // x * 0 is NaN exactly where x is not finite
           __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
           const __nv_bfloat162 zero = acc;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
+          for (int c = 0; c < kChunks; ++c) {
             const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v[c]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc = __hfma2(b[e], zero, acc);
@@ -500,13 +628,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!there) {
             acc = zero;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) *chunk(c) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < kChunks; ++c) *chunk(c) = make_uint4(0, 0, 0, 0);
           }
           const float2 sum = __bfloat1622float2(acc);
           const bool found = sum.x != 0.f || sum.y != 0.f;    // NaN compares unequal
           const uint32_t mask = __ballot_sync(0xffffffffu, found);
           if (found) {
-            for (int c = 0; c < 16; ++c) {
+            for (int c = 0; c < kChunks; ++c) {
               uint4* q = reinterpret_cast<uint4*>(half + (c >> 3) * (kBlock / 2) + r * 128 + ((c & 7) << 4));
               uint4 v = *q;
               uint32_t* b = reinterpret_cast<uint32_t*>(&v);
@@ -518,11 +646,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               *q = v;
             }
           }
-          if (lane == 0) bad[4 * (M % kMasked) + m] = mask;
+          if (lane == 0) {
+            const int at = 8 * (M % kMasked) + 4 * static_cast<int>(rank) + m;
+            bad[at] = mask;
+            if constexpr (kPair) st_cluster_b32(mapa_shared(base + kOffBad + 4 * at, peer), mask);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bVClean + M % kMasked));
+        if (lane == 0) {
+          if constexpr (kPair) mbar_arrive_cluster(bar(bVClean + M % kMasked), peer);
+          mbar_arrive(bar(bVClean + M % kMasked));
+        }
       }
       tbase += sh.n;
     }
@@ -532,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tile's keys and half of the output's columns.  They meet at a named
     // barrier of their 64 threads and agree on the reference maximum there.
     const int w = warp >> 3, half = (warp >> 2) & 1;          // row tile, half
-    const int row = 128 * w + 32 * (warp & 3) + lane;         // row of the item
+    const int row0 = kTileRows<kPair> * w + 128 * static_cast<int>(rank);   // this CTA's first row of it
+    const int row = row0 + 32 * (warp & 3) + lane;            // row of the item
     const int pair_bar = 1 + 4 * w + (warp & 3);
     float* meet = reinterpret_cast<float*>(smem + kOffMeet) + 32 * (pair_bar - 1) + lane;
     const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -555,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int mbase = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
-      ok = warp_wait(bar(bSched + k % kSched), (k / kSched) & 1, wc);
+      ok = warp_wait<kPair>(bar(bSched + k % kSched), (k / kSched) & 1, wc);
       if (!ok) break;
       // The item's words are read here for the loop over the keys and again for the epilogue: held in between
       // they would cost registers that the scores need.
@@ -566,10 +702,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           release_item(k);
           break;
         }
-        const Shape sh(it);
+        const Shape sh(it, kTileRows<kPair>);
         nw = w ? sh.n_b : sh.n_a;
         seen = min(it.nk, it.off + row + 1) - 64 * half;      // of the half's keys, counted from its first, those this row sees
-        first_masked = min(max(it.off + 128 * w + 1, 0), it.nk) / kPfKeys;   // of this row tile
+        first_masked = min(max(it.off + row0 + 1, 0), it.nk) / kPfKeys;   // of this CTA's rows
       }
       float ref = -INFINITY, sum = 0.f;
       for (int t = 0; t < nw; ++t, ++step) {
@@ -649,7 +785,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bPFull + w));
+        if (lane == 0) {
+          if constexpr (kPair) arrive_leader_relaxed(bar(bPFull + w));
+          else mbar_arrive(bar(bPFull + w));
+        }
         sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
       }
       if (ok && nw > 0) {
@@ -659,14 +798,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item it;
       announced(k, it);
       release_item(k);
-      const Shape sh(it);
+      const Shape sh(it, kTileRows<kPair>);
       uint32_t dirty = 0;                                     // some masked tile of this row tile had its values cleared
       for (int t = sh.whole; t < nw && ok; ++t) {
         const int M = mbase + t - sh.whole;
-        ok = warp_wait(bar(bVClean + M % kMasked), (M / kMasked) & 1, wc);
-        for (int i = 0; i < 4; ++i) dirty |= bad[4 * (M % kMasked) + i];
+        ok = warp_wait<kPair>(bar(bVClean + M % kMasked), (M / kMasked) & 1, wc);
+        for (int i = 0; i < 8; ++i) dirty |= bad[8 * (M % kMasked) + i];
       }
-      if (128 * w < it.nq) {                                  // both warps, whole: they meet, and tcgen05.ld is collective
+      if (row0 < it.nq) {                                  // both warps, whole: they meet, and tcgen05.ld is collective
         sum = both(sum, [](float a, float b) { return a + b; });
         ok = both(ok ? 1.f : 0.f, [](float a, float b) { return fminf(a, b); }) > 0.f;
         if (!ok) break;
@@ -675,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lse = any ? (ref + log2f(sum)) * 0.69314718055994531f : -INFINITY;
         const bool live = row < it.nq;
         const size_t out_row = static_cast<size_t>(it.q0 + row) * p.heads + it.h;
-        const size_t part_row = (static_cast<size_t>(max(it.part, 0)) * p.heads + it.h) * kPfRows + row;
+        const size_t part_row = (static_cast<size_t>(max(it.part, 0)) * p.heads + it.h) * (2 * kTileRows<kPair>) + row;
         if (live && half == 0) {
           if (it.part >= 0) p.part_lse[part_row] = lse;
           else if (p.lse) p.lse[out_row] = lse;
@@ -694,7 +833,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int all = min(it.nk, it.off + row + 1);
             for (int t = sh.whole; t < nw; ++t)
               for (int i = 0; i < 4; ++i)
-                for (uint32_t m = bad[4 * ((mbase + t - sh.whole) % kMasked) + i]; m; m &= m - 1) {
+                for (uint32_t m = bad[8 * ((mbase + t - sh.whole) % kMasked) + i] |
+                                  bad[8 * ((mbase + t - sh.whole) % kMasked) + 4 + i];
+                     m; m &= m - 1) {
                   const int key = t * kPfKeys + 32 * i + __ffs(m) - 1;
                   if (key >= all) continue;
                   const uint16_t* v = p.v + (it.k0 + key) * p.v_ts + it.h * p.v_hs + c;
@@ -731,8 +872,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
-  if (warp == kIssuer) tmem_dealloc(tmem, 512);
+  __syncwarp();
+  if constexpr (kPair) {
+    cluster_sync_all();                                       // no CTA leaves while the other signals it
+    if (warp == kIssuer) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  } else {
+    __syncthreads();
+    if (warp == kIssuer) tmem_dealloc(tmem, 512);
+  }
   if (threadIdx.x == 0) {
     // the last block to finish leaves the counter at zero for the next launch
     __threadfence();
@@ -749,7 +896,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
   griddep_launch_dependents();
   const int4 e = __ldg(reinterpret_cast<const int4*>(p.merges) + blockIdx.y);
   const int q0 = e.x, nq = e.y, p0 = e.z, p1 = e.w;
-  if (q0 < 0 || nq < 1 || nq > kPfRows || q0 > p.q_tokens - nq || p0 < 0 || p1 <= p0 || p1 > p.partials) {
+  if (q0 < 0 || nq < 1 || nq > p.rows || q0 > p.q_tokens - nq || p0 < 0 || p1 <= p0 || p1 > p.partials) {
     if (threadIdx.x == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
     return;
   }
@@ -760,14 +907,14 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
   float m = -INFINITY;
   bool bad = false;
   for (int k = p0; k < p1; ++k) {
-    const float s = p.part_lse[(static_cast<size_t>(k) * p.heads + h) * kPfRows + r];
+    const float s = p.part_lse[(static_cast<size_t>(k) * p.heads + h) * p.rows + r];
     bad |= s != s;
     m = fmaxf(m, s);
   }
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
   for (int k = p0; k < p1; ++k) {
-    const size_t row = (static_cast<size_t>(k) * p.heads + h) * kPfRows + r;
+    const size_t row = (static_cast<size_t>(k) * p.heads + h) * p.rows + r;
     const float s = p.part_lse[row];
     if (s == -INFINITY) continue;                          // nothing seen in this piece
     const float w = expf(s - m);
@@ -791,22 +938,30 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
 int launch_prefill(const PrefillParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_kr,
                    const CUtensorMap& tm_v, cudaStream_t stream) {
   if (p.n_items <= 0) return MLA_OK;
-  if (!set_smem_limit(reinterpret_cast<const void*>(&prefill_kernel), kSmemBytes)) return MLA_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const bool pair = p.rows > kPfRows;
+  const auto kernel = pair ? &prefill_kernel<true> : &prefill_kernel<false>;
+  if (!set_smem_limit(reinterpret_cast<const void*>(kernel), kSmemBytes)) return MLA_ERR_CUDA;
   const int sms = device_sm_count();
   if (sms < 1) return MLA_ERR_CUDA;
-  cfg.gridDim = dim3(std::min(p.n_items * p.heads, sms), 1, 1);
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pair ? 2 : 1;
+  const int workers = pair ? std::max(1, sms / 2) : sms;
+  cfg.gridDim = dim3(std::min(p.n_items * p.heads, workers) * (pair ? 2 : 1), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
-  if (cudaLaunchKernelEx(&cfg, prefill_kernel, tm_q, tm_k, tm_kr, tm_v, p) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, tm_q, tm_k, tm_kr, tm_v, p) != cudaSuccess) return MLA_ERR_CUDA;
+  cfg.numAttrs = 1;
   if (p.n_merges > 0) {
-    cfg.gridDim = dim3((kPfRows * p.heads + 7) / 8, p.n_merges, 1);
+    cfg.gridDim = dim3((p.rows * p.heads + 7) / 8, p.n_merges, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, prefill_merge_kernel, p) != cudaSuccess) return MLA_ERR_CUDA;

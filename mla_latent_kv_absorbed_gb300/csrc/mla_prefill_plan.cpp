@@ -2,7 +2,8 @@
 // of the kernel takes, and in what order items are launched.
 //
 //   * an item is up to 256 query rows of one request (two tiles of 128) and
-//     the keys they see, for every head; causal items end at the last key of
+//     the keys they see, for every head, or 512 for a pair of CTAs: whichever
+//     of the two schedules ends first; causal items end at the last key of
 //     their last row, so no tile without a visible key is visited;
 //   * items are launched heaviest first (blocks start in launch order as SMs
 //     fall free, so the short ones fill the end), for a group of heads at a
@@ -41,29 +42,34 @@ constexpr long long kJoinCost = 12;
 constexpr long long kL2Bytes = 64ll << 20;
 
 inline int key_tiles(int nk) { return (nk + kPfKeys - 1) / kPfKeys; }
-// One row tile has no other to fill its softmax's time: 8 of 10.
-inline long long tile_cost(int nq) { return nq > kPfRows / 2 ? 10 : 8; }
+// One row tile has no other to fill its softmax's time: 8 of 10.  A pair's two
+// tiles of 256 rows take nine tenths of what one CTA's two of 128 do, on
+// two SMs.
+inline long long tile_cost(int nq, int rows) {
+  if (rows == kPfRows) return nq > rows / 2 ? 10 : 8;
+  return nq > rows / 2 ? 9 : 8;
+}
 
 // Parts of a tile whose keys are cut into pieces of at most `cap` (0: not cut), none under four key tiles.
-int parts_of(const Tile& t, long long cap) {
+int parts_of(const Tile& t, int rows, long long cap) {
   const int nt = key_tiles(t.nk);
   if (cap <= 0 || nt <= 1) return 1;
-  const long long most = std::max<long long>(4, cap / tile_cost(t.nq));
+  const long long most = std::max<long long>(4, cap / tile_cost(t.nq, rows));
   return static_cast<int>((nt + most - 1) / most);
 }
 
-long long count_pieces(const std::vector<Tile>& tiles, long long cap) {
+long long count_pieces(const std::vector<Tile>& tiles, int rows, long long cap) {
   long long n = 0;
-  for (const Tile& t : tiles) n += parts_of(t, cap);
+  for (const Tile& t : tiles) n += parts_of(t, rows, cap);
   return n;
 }
 
-void cut(const std::vector<Tile>& tiles, long long cap, std::vector<Piece>& pieces) {
+void cut(const std::vector<Tile>& tiles, int rows, long long cap, std::vector<Piece>& pieces) {
   pieces.clear();
   for (size_t i = 0; i < tiles.size(); ++i) {
     const int nt = key_tiles(tiles[i].nk);
-    const long long c = tile_cost(tiles[i].nq);
-    const int parts = parts_of(tiles[i], cap);
+    const long long c = tile_cost(tiles[i].nq, rows);
+    const int parts = parts_of(tiles[i], rows, cap);
     for (int k = 0; k < parts; ++k) {
       const int a = static_cast<int>(static_cast<long long>(nt) * k / parts);
       const int e = static_cast<int>(static_cast<long long>(nt) * (k + 1) / parts);
@@ -102,48 +108,74 @@ long long makespan(const std::vector<Piece>& pieces, int heads, int group, int s
 
 }  // namespace
 
-int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int causal, int num_sms,
-                       std::vector<int32_t>& words) {
-  std::vector<Tile> tiles;
+namespace {
+
+// The tiles of `rows` query rows and their pieces in launch order; returns the
+// end of the greedy schedule.
+long long plan_rows(const int32_t* qp, const int32_t* kp, int B, int H, int causal, int rows, int workers,
+                    std::vector<Tile>& tiles, std::vector<Piece>& best) {
+  tiles.clear();
   for (int b = 0; b < B; ++b) {
     const int lq = qp[b + 1] - qp[b], lk = kp[b + 1] - kp[b];
-    for (int r = 0; r < lq; r += kPfRows) {
-      const int nq = std::min(kPfRows, lq - r);
+    for (int r = 0; r < lq; r += rows) {
+      const int nq = std::min(rows, lq - r);
       // row r + i sees keys j <= r + i + lk - lq
       const long long off = causal ? static_cast<long long>(r) + lk - lq : kPfNoLimit;
       const long long seen = std::min<long long>(lk, std::max<long long>(0, off + nq));
       tiles.push_back({b, qp[b] + r, nq, kp[b], static_cast<int>(seen), static_cast<int>(off)});
     }
   }
-  std::vector<Piece> best, trial;
-  cut(tiles, 0, best);
+  cut(tiles, rows, 0, best);
   long long total = 0, most = 0;
   for (const Piece& p : best) {
     total += p.cost * H;
     most = std::max(most, p.cost);
   }
-  const long long mean = (total + num_sms - 1) / num_sms;
+  const long long mean = (total + workers - 1) / workers;
   const long long whole = static_cast<long long>(tiles.size()) * H;
+  if (tiles.empty()) return 0;
+  if (whole > (1 << 16)) return mean + most;                  // too many to simulate, and none long against the mean
+  long long end = makespan(best, H, group_of(H, kp[B], best.size(), workers), workers);
   // the schedule of many items, none of them long, cannot be improved by cutting
-  if (!tiles.empty() && whole <= (1 << 16) && !(whole >= 8ll * num_sms && most <= mean / 2)) {
-    long long end = makespan(best, H, group_of(H, kp[B], best.size(), num_sms), num_sms);
-    long long waves = whole / num_sms + 1;
-    for (int tried = 0; tried < 5; ++tried, ++waves) {
-      const long long pieces = waves * num_sms / H;           // that fill the SMs `waves` times
-      if (pieces <= static_cast<long long>(tiles.size()) || pieces > 65535) continue;
-      long long lo = 1, hi = most;                            // the smallest cap with no more pieces than that
-      while (lo < hi) {
-        const long long mid = (lo + hi) / 2;
-        if (count_pieces(tiles, mid) <= pieces) hi = mid;
-        else lo = mid + 1;
-      }
-      cut(tiles, lo, trial);
-      if (trial.size() == tiles.size()) continue;
-      const long long e = makespan(trial, H, group_of(H, kp[B], trial.size(), num_sms), num_sms) + kJoinCost;
-      if (e < end) {
-        end = e;
-        best.swap(trial);
-      }
+  if (whole >= 8ll * workers && most <= mean / 2) return end;
+  std::vector<Piece> trial;
+  long long waves = whole / workers + 1;
+  for (int tried = 0; tried < 5; ++tried, ++waves) {
+    const long long pieces = waves * workers / H;             // that fill the SMs `waves` times
+    if (pieces <= static_cast<long long>(tiles.size()) || pieces > 65535) continue;
+    long long lo = 1, hi = most;                              // the smallest cap with no more pieces than that
+    while (lo < hi) {
+      const long long mid = (lo + hi) / 2;
+      if (count_pieces(tiles, rows, mid) <= pieces) hi = mid;
+      else lo = mid + 1;
+    }
+    cut(tiles, rows, lo, trial);
+    if (trial.size() == tiles.size()) continue;
+    const long long e = makespan(trial, H, group_of(H, kp[B], trial.size(), workers), workers) + kJoinCost;
+    if (e < end) {
+      end = e;
+      best.swap(trial);
+    }
+  }
+  return end;
+}
+
+}  // namespace
+
+int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int causal, int num_sms,
+                       std::vector<int32_t>& words) {
+  std::vector<Tile> tiles;
+  std::vector<Piece> best;
+  int rows = kPfRows, workers = num_sms;
+  const long long end = plan_rows(qp, kp, B, H, causal, rows, workers, tiles, best);
+  if (num_sms >= 2) {
+    std::vector<Tile> pair_tiles;
+    std::vector<Piece> pair_best;
+    if (plan_rows(qp, kp, B, H, causal, 2 * kPfRows, num_sms / 2, pair_tiles, pair_best) < end) {
+      tiles.swap(pair_tiles);
+      best.swap(pair_best);
+      rows = 2 * kPfRows;
+      workers = num_sms / 2;
     }
   }
   // partial slots, in tile order, and the merge entries
@@ -160,7 +192,7 @@ int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int c
                             static_cast<long long>(kPfMergeWords) * merges;
   const long long blocks = static_cast<long long>(best.size()) * H;
   if (n_words > 0x7FFFFFFFll || blocks > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
-  const int group = group_of(H, kp[B], best.size(), num_sms);
+  const int group = group_of(H, kp[B], best.size(), workers);
   words.assign(static_cast<size_t>(n_words), 0);
   words[kPMagic] = kPfMagic;
   words[kPVersion] = kPfVersion;
@@ -175,6 +207,7 @@ int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int c
   words[kPHeadGroup] = group;
   words[kPTotalWords] = static_cast<int32_t>(n_words);
   words[kPNumSms] = num_sms;
+  words[kPRows] = rows;
   int32_t* w = words.data() + kPfHeaderWords;
   for (const Piece& p : best) {
     const Tile& t = tiles[p.tile];

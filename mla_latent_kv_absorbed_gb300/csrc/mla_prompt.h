@@ -65,11 +65,12 @@ constexpr int32_t kPfVersion = 1;
 constexpr int kPfHeaderWords = 16;
 enum PfHeader : int {
   kPMagic = 0, kPVersion, kPBatch, kPHeads, kPCausal, kPQTokens, kPKvTokens, kPItems, kPPartials, kPMerges,
-  kPHeadGroup /* heads whose items are launched together */, kPTotalWords, kPNumSms
+  kPHeadGroup /* heads whose items are launched together */, kPTotalWords, kPNumSms,
+  kPRows /* query rows of an item, at most: 256, or 512 for CTA pairs */
 };
 constexpr int kPfItemWords = 8;       // request, q0, nq, k0, nk, off, partial (or -1), 0
 constexpr int kPfMergeWords = 4;      // q0, nq, first partial, last partial + 1
-constexpr int kPfRows = 256;          // query rows of an item, at most
+constexpr int kPfRows = 256;          // query rows of one CTA's item, at most
 constexpr int kPfKeys = 128;          // keys of a tile
 constexpr int32_t kPfNoLimit = 0x3FFFFFFF;   // off of an item without a causal limit
 
@@ -79,13 +80,13 @@ constexpr int kWsCounter = 16, kWsDone = 17;
 
 inline int pf_items_off(const int32_t*) { return kPfHeaderWords; }
 inline int pf_merge_off(const int32_t* h) { return kPfHeaderWords + kPfItemWords * h[kPItems]; }
-// Workspace: status header, partial outputs [partials][heads][256][128] fp32,
-// partial log-sum-exps [partials][heads][256].
+// Workspace: status header, partial outputs [partials][heads][rows][128] fp32,
+// partial log-sum-exps [partials][heads][rows].
 inline size_t pf_part_lse_off(const int32_t* h) {
-  return kWsHeaderBytes + static_cast<size_t>(h[kPPartials]) * h[kPHeads] * kPfRows * kNope * 4;
+  return kWsHeaderBytes + static_cast<size_t>(h[kPPartials]) * h[kPHeads] * h[kPRows] * kNope * 4;
 }
 inline size_t pf_workspace_bytes(const int32_t* h) {
-  return pf_part_lse_off(h) + static_cast<size_t>(h[kPPartials]) * h[kPHeads] * kPfRows * 4;
+  return pf_part_lse_off(h) + static_cast<size_t>(h[kPPartials]) * h[kPHeads] * h[kPRows] * 4;
 }
 
 int build_prefill_plan(const int32_t* q_indptr, const int32_t* kv_indptr, int batch, int heads, int causal,
@@ -101,7 +102,7 @@ struct PrefillParams {
   float* part_o;
   float* part_lse;
   int* status;
-  int n_items, n_merges, heads, head_group, partials;
+  int n_items, n_merges, heads, head_group, partials, rows;
   int q_tokens, kv_tokens;
   float scale_log2;           // |sm_scale| * log2(e), > 0
   int negate;                 // sm_scale < 0: the scores are those of -q
@@ -120,7 +121,8 @@ ExpandTiling expand_tiling(int tokens, int heads, int sms);
 int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[4], ExpandTiling tiling, int sms, bool fp8,
                   cudaStream_t stream);
 // tm_q over q as [rows, heads, 192] (box 128 rows x 64), tm_k and tm_v over
-// [keys, heads, 128] (boxes of 128 and 64 keys x 64), tm_kr over [keys, 64].
+// [keys, heads, 128] (boxes of 128 - for CTA pairs 64 - and 64 keys x 64), tm_kr
+// over [keys, 64] (box as tm_k's).
 int launch_prefill(const PrefillParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_kr,
                    const CUtensorMap& tm_v, cudaStream_t stream);
 

@@ -270,7 +270,7 @@ bool prefill_header_ok(const int32_t* h) {
   if (!h || h[kPMagic] != kPfMagic || h[kPVersion] != kPfVersion) return false;
   if (h[kPBatch] < 0 || h[kPHeads] < 1 || h[kPHeads] > 65535 || h[kPQTokens] < 0 || h[kPKvTokens] < 0 ||
       h[kPItems] < 0 || h[kPPartials] < 0 || h[kPMerges] < 0 || h[kPMerges] > 65535 || h[kPHeadGroup] < 1 ||
-      h[kPHeadGroup] > h[kPHeads])
+      h[kPHeadGroup] > h[kPHeads] || (h[kPRows] != kPfRows && h[kPRows] != 2 * kPfRows))
     return false;
   if (static_cast<long long>(h[kPItems]) * h[kPHeads] > 0x7FFFFFFFll) return false;
   const long long words = kPfHeaderWords + static_cast<long long>(kPfItemWords) * h[kPItems] +
@@ -323,6 +323,8 @@ int mla_prefill_run(const int32_t* plan_host, const int32_t* plan_dev, const voi
   p.heads = H;
   p.head_group = plan_host[kPHeadGroup];
   p.partials = plan_host[kPPartials];
+  p.rows = plan_host[kPRows];
+  const int key_box = p.rows > kPfRows ? kPfKeys / 2 : kPfKeys;
   p.q_tokens = plan_host[kPQTokens];
   p.kv_tokens = plan_host[kPKvTokens];
   // the kernel takes maxima of the products before it scales them: a positive
@@ -334,8 +336,8 @@ int mla_prefill_run(const int32_t* plan_host, const int32_t* plan_dev, const voi
   if (!make_map(&tm_q, q, nq, q_token_stride, H, q_head_stride, kQk, 128)) return MLA_ERR_CUDA;
   if (nk == 0) {
     tm_k = tm_kr = tm_v = tm_q;                 // nothing is loaded through them
-  } else if (!make_map(&tm_k, k_nope, nk, k_token_stride, H, k_head_stride, kNope, 128) ||
-             !make_map(&tm_kr, k_rope, nk, k_rope_stride, 0, 0, kRope, 128) ||
+  } else if (!make_map(&tm_k, k_nope, nk, k_token_stride, H, k_head_stride, kNope, key_box) ||
+             !make_map(&tm_kr, k_rope, nk, k_rope_stride, 0, 0, kRope, key_box) ||
              !make_map(&tm_v, v, nk, v_token_stride, H, v_head_stride, kNope, 64)) {
     return MLA_ERR_CUDA;
   }

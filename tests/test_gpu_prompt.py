@@ -402,6 +402,49 @@ def test_prefill_of_more_items_than_sms(ql, kl, H, causal):
     assert all(torch.equal(o, out) for o in outs)
 
 
+def _on_pairs(plan, qp, kp, H, causal):
+    """The same batch in items of 512 rows, which pairs of CTAs work on (a plan takes them where it expects that
+    schedule to end first)."""
+    torch, _ = _t()
+    items = []
+    for b in range(len(qp) - 1):
+        lq, lk = int(qp[b + 1] - qp[b]), int(kp[b + 1] - kp[b])
+        for r in range(0, lq, 512):
+            nq, off = min(512, lq - r), r + lk - lq if causal else 0x3FFFFFFF
+            items.append([b, int(qp[b]) + r, nq, int(kp[b]), min(lk, max(0, off + nq)), off, -1, 0])
+    items.sort(key=lambda i: -i[4])
+    words = plan.plan_host[:16].tolist()
+    words[7:12] = [len(items), 0, 0, H, 16 + 8 * len(items)]
+    words[13] = 512
+    plan.plan_host = np.array(words + sum(items, []), dtype=np.int32)
+    plan.plan_dev = torch.from_numpy(plan.plan_host).cuda()
+    return plan
+
+
+PAIRS = [
+    ([512], [512], 2, True), ([513], [513], 2, True), ([1030], [1100], 3, True), ([700, 300], [900, 300], 2, True),
+    ([600], [50], 1, True), ([520, 5, 0, 511], [520, 700, 9, 1000], 3, False),
+    ([300, 600, 1000, 40], [300, 900, 1000, 40], 24, True), ([1], [4000], 1, True), ([260], [129], 2, True),
+    ([1, 7, 33, 100, 140, 260, 300, 0, 129], [1, 7, 33, 100, 140, 260, 300, 9, 129], 33, True),
+]
+
+
+@pytest.mark.parametrize("ql,kl,H,causal", PAIRS)
+def test_prefill_on_cta_pairs(ql, kl, H, causal):
+    torch, B = _t()
+    qp, kp = _indptr(ql), _indptr(kl)
+    plan = _on_pairs(B.Prefiller(qp, kp, H, causal), qp, kp, H, causal)
+    (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(31 + H, int(qp[-1]), int(kp[-1]), H)
+    ref, ref_lse, mag = P.prefill_attention(xq, xk, xr, xv, qp, kp, SM, causal)
+    out, lse = _attend(plan, q, k, kr, v)
+    _check_attention(out, lse, ref, ref_lse, mag)
+    outs = [torch.empty_like(out) for _ in range(6)]
+    for o in outs:
+        plan.run(q, k, kr, v, SM, o)
+    assert plan.check() == 0
+    assert all(torch.equal(o, out) for o in outs)
+
+
 @pytest.mark.parametrize("ql,kl,H,causal", [([3], [4000], 1, True), ([64, 1], [3500, 700], 2, True),
                                             ([300], [4000], 1, False), ([200], [3300], 2, True)])
 def test_prefill_cut_along_the_keys(ql, kl, H, causal):
@@ -470,18 +513,22 @@ def test_prefill_strides():
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("causal", [True, False])
-def test_prefill_keeps_what_is_masked_out(bad, causal):
+@pytest.mark.parametrize("pairs", [False, True])
+def test_prefill_keeps_what_is_masked_out(bad, causal, pairs):
     # keys and values that are not finite reach the rows that see them, and no other: neither the rows before
     # them (causal) nor another request's
     torch, B = _t()
     ql, kl, H = [40, 200, 30], [40, 330, 30], 2
     qp, kp = _indptr(ql), _indptr(kl)
+    plan = B.Prefiller(qp, kp, H, causal)
+    if pairs:
+        plan = _on_pairs(plan, qp, kp, H, causal)
     (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(9, int(qp[-1]), int(kp[-1]), H)
     at = int(kp[1]) + 330 - 60                                   # a key of the second request, and a value before it
     v[at - 9, 1, 17] = bad
     k[at, 0, 3] = bad
     ref, ref_lse, mag = P.prefill_attention(xq, xk, xr, xv, qp, kp, SM, causal)
-    out, lse = _attend(B.Prefiller(qp, kp, H, causal), q, k, kr, v)
+    out, lse = _attend(plan, q, k, kr, v)
     o, l = _f64(out), lse.double().cpu().numpy()
     sees_v = np.zeros(o.shape, dtype=bool)
     sees_k = np.zeros(o.shape[:2], dtype=bool)

@@ -117,14 +117,15 @@ def _plan_cases():
 def test_prefill_plan_covers_every_row_and_key_once(B, sms, causal):
     for qp, kp, H in _plan_cases():
         plan, ws = B.prefill_plan(qp, kp, H, causal, num_sms=sms)
-        n, partials, merges, group = (int(plan[i]) for i in (7, 8, 9, 10))
+        n, partials, merges, group, R = (int(plan[i]) for i in (7, 8, 9, 10, 13))
+        assert R in (256, 512)
         assert plan.size == 16 + 8 * n + 4 * merges and 1 <= group <= H
-        assert ws == 256 + partials * H * 256 * 129 * 4
+        assert ws == 256 + partials * H * R * 129 * 4
         seen, used = {}, set()
         for b, q0, nq, k0, nk, off, part, _ in plan[16:16 + 8 * n].reshape(-1, 8).tolist():
             lq, lk = qp[b + 1] - qp[b], kp[b + 1] - kp[b]
-            assert qp[b] <= q0 and q0 + nq <= qp[b + 1] and 1 <= nq <= 256 and (q0 - qp[b]) % 256 == 0
-            assert nq == min(256, qp[b + 1] - q0)
+            assert qp[b] <= q0 and q0 + nq <= qp[b + 1] and 1 <= nq <= R and (q0 - qp[b]) % R == 0
+            assert nq == min(R, qp[b + 1] - q0)
             assert nk >= 0 and kp[b] <= k0 and k0 + nk <= kp[b + 1]
             if causal:       # row r of the item sees the piece's keys j <= r + off
                 assert off == (q0 - qp[b]) + lk - lq - (k0 - kp[b])
@@ -132,10 +133,10 @@ def test_prefill_plan_covers_every_row_and_key_once(B, sms, causal):
             used.add(part) if part >= 0 else None
             seen.setdefault(q0, []).append((k0 - kp[b], nk, part, b, nq))
         for b in range(len(qp) - 1):
-            for q0 in range(qp[b], qp[b + 1], 256):
+            for q0 in range(qp[b], qp[b + 1], R):
                 pieces = sorted(seen.pop(q0))
                 lq, lk = qp[b + 1] - qp[b], kp[b + 1] - kp[b]
-                nq = min(256, qp[b + 1] - q0)
+                nq = min(R, qp[b + 1] - q0)
                 last = lk if not causal else min(lk, max(0, q0 - qp[b] + nq + lk - lq))
                 at = 0
                 for k, nk, part, bb, _ in pieces:
@@ -153,7 +154,7 @@ def test_prefill_plan_cuts_long_keys_of_few_rows_only(B):
     few, _ = B.prefill_plan([0, 64], [0, 65536], 16, True, num_sms=152)
     assert few[8] > 1 and few[9] == 1
     many, _ = B.prefill_plan([0, 8192], [0, 8192], 128, True, num_sms=152)
-    assert many[8] == 0 and many[7] == 32
+    assert many[8] == 0 and many[7] == 8192 // many[13]
     # heaviest first
     nk = many[16:].reshape(-1, 8)[:, 4]
     assert (np.diff(nk) <= 0).all()
