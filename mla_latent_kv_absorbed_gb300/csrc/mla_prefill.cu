@@ -60,8 +60,8 @@ constexpr int kMasked = 8;                            // masked tiles told apart
 constexpr int kConsumers = 16 + 1 + 2;                // warps that read an announced item (in CTA 1: no issuer, but the producer)
 enum Bar : int {
   bQFull = 0,                    // [2] per row tile
-  bQFree = bQFull + 2,           // the item's last scores are done
-  bKFull = bQFree + 1,           // [4] key tile T on T & 3, T counting the CTA's tiles over all items
+  bQFree = bQFull + 2,           // [2] the row tile's last scores of the item are done
+  bKFull = bQFree + 2,           // [4] key tile T on T & 3, T counting the CTA's tiles over all items
   bVFull = bKFull + kDepth,      // [4] the values of whole tile U (that every row sees whole) on U & 3
   bKFree = bVFull + kDepth,      // [4] its QK products are done
   bVFree = bKFree + kDepth,      // [4]
@@ -76,6 +76,7 @@ enum Bar : int {
   kBars
 };
 constexpr int kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16;   // TMEM address, abort flag
+constexpr int kOffFound = kOffMisc + 8;               // nonzero once some mask in kOffBad was
 constexpr int kOffBad = kOffMisc + 16;                // [8][2][4] words: bit j = key j of masked tile M, by the CTA that saw it
 constexpr int kOffSched = kOffBad + 32 * kMasked;     // [4] announced items, 8 words each
 constexpr int kOffMeet = kOffSched + 32 * kSched;      // [8][32] floats: where a row's two threads meet
@@ -109,6 +110,7 @@ __device__ __forceinline__ bool load_item(const PrefillParams& p, int i, Item& i
 struct Shape {
   int n_a, n_b, n;             // key tiles that some row of A, of B, of either sees
   int whole;                   // the first of them are seen whole by every row; at most three (a pair: five) follow
+  Shape() = default;
   __device__ __forceinline__ Shape(const Item& it, int rows) {
     auto tiles = [&](int w) -> int {
       if (it.nq <= rows * w) return 0;
@@ -122,6 +124,10 @@ struct Shape {
   }
 };
 
+__device__ __forceinline__ void tma_prefetch_3d(const void* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -248,6 +254,38 @@ __device__ __noinline__ void rescale_columns(uint32_t taddr, float f) {
   tmem_wait_st();
 }
 
+// 64 columns of the output from TMEM, times inv, as bf16 (a piece: fp32) to the
+// thread's row.  Four lanes exchange blocks of 16 bytes, so that a store writes
+// 64 bytes of a row: `dst` is block lane & 3 of the first of their rows, `rows`
+// how many of the four there are.  Out of line for the same reason; with all its
+// registers free it takes 1700 cycles where 16 columns at a time in the caller
+// took 4500.
+template <typename T>
+__device__ __noinline__ void store_columns(uint32_t taddr, float inv, T* dst, size_t stride, int rows) {
+  constexpr bool kHalf = sizeof(T) == 2;
+  constexpr int kCols = kHalf ? 32 : 16;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 64; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(taddr + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int y = 0; y < 32; y += kCols) {
+      uint32_t b[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        b[e] = kHalf ? pack_bf16x2(__uint_as_float(o[(2 * e) & 31]) * inv, __uint_as_float(o[(2 * e + 1) & 31]) * inv)
+                     : __float_as_uint(__uint_as_float(o[(y + e) & 31]) * inv);
+      transpose4_blocks<4>(b, lane);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (x < rows)
+          *reinterpret_cast<uint4*>(dst + x * stride + c + y) = make_uint4(b[4 * x], b[4 * x + 1], b[4 * x + 2], b[4 * x + 3]);
+    }
+  }
+}
+
 // The warp waits, every lane for itself (through one lane and a shuffle it took
 // 7% of the kernel's time longer); all return the same outcome.
 template <bool kCluster = false>
@@ -302,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(i), eight ? 8 * kCtas : two ? 2 * kCtas : all ? kConsumers * kCtas : 1);
     }
     *abort_flag = 0;
+    *reinterpret_cast<int*>(smem + kOffFound) = 0;
     fence_mbar_init();
   }
   for (int i = threadIdx.x; i < 8 * kMasked; i += kThreads) bad[i] = 0;
@@ -388,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return there;
       };
       int tbase = 0, ubase = 0, mbase = 0;                    // tiles before this item: all, whole, masked
-      uint32_t q_items[2] = {0, 0}, busy = 0;                 // items with queries in the row tile, in either
+      uint32_t q_items[2] = {0, 0};                           // items with queries in the row tile
       int k_armed = 0, q_bar[2] = {-1, -1};                   // what may be in flight: key tiles, query tiles,
       int v_new = -1, v_old = -1;                             // the last two tiles' values (barrier * 2 + parity)
       Item it;
@@ -406,6 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto load_q = [&](auto W) {
           constexpr int w = W.value;
+          if (q_items[w] > 0) ok = mbar_wait(bar(bQFree + w), (q_items[w] - 1) & 1, wc);   // the last item's queries
+          if (!ok) return;
           q_bar[w] = q_items[w] & 1;
           ++q_items[w];
           // (a pair's barriers of landed queries, keys and values are CTA 0's, which counts both halves)
@@ -471,12 +512,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (more) fetch(w, next);
           announce(k + 1, next, more);
         };
-        if (sh.n > 0 && busy++ > 0) ok = mbar_wait(bar(bQFree), (busy - 2) & 1, wc);   // the item before's queries
-        if (ok && sh.n_a > 0) load_q(TileA{});
+        // The next item's queries are asked for when a row tile's last scores of this one are done; from L2 they
+        // are there sooner.
+        auto prefetch_q = [&] {
+          const Shape ns(next, kTileRows<kPair>);
+          for (int w = 0; w < 2; ++w)
+            for (int i = 0; i < 3 && (w ? ns.n_b : ns.n_a) > 0; ++i)
+              tma_prefetch_3d(&tm_q, 64 * i, next.h, next.q0 + kTileRows<kPair> * w + 128 * static_cast<int>(rank));
+        };
+        if (sh.n_a > 0) load_q(TileA{});
         if (ok && sh.n > 0) load_k(0);
         if (ok && sh.n_b > 0) load_q(TileB{});
         if (ok && sh.n > 0) load_v(0);
         if (ok) look_ahead();                                 // the ring is full: its latency costs nothing here
+        if (ok && more) prefetch_q();
         for (int t = 1; t < sh.n && ok; ++t) {
           load_k(t);
           if (ok) load_v(t);
@@ -509,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc_s = idesc_bf16(kTileRows<kPair>, 128, false, false) | (p.negate ? 1u << 13 : 0u);   // -Q
     constexpr uint32_t kIdescO = idesc_bf16(kTileRows<kPair>, 128, false, true);
     auto block_at = [&](int c) -> uint32_t { return base + kOffRing + (c % kSlots) * kRingBlock; };
-    // scores of key tile T for row tile w
-    auto qk = [&](int T, int w) {
+    // scores of key tile T for row tile w; its last of the item: the queries are free
+    auto qk = [&](int T, int w, bool last) {
       const uint32_t d = tmem + kTmemS + 128 * w;
       const uint32_t a = desc_low(base + kOffQ + 3 * w * kBlock, 16);
       const uint32_t b0 = desc_low(block_at(5 * T), 16), b1 = desc_low(block_at(5 * T + 1), 16),
@@ -521,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ss<kDescHigh, kPair>(d, a + (k >> 2) * (kBlock >> 4) + 2 * (k & 3), (k < 4 ? b0 : k < 8 ? b1 : b2) + 2 * (k & 3),
                             idesc_s, k > 0);
         commit<kPair>(bar(bSFull + w));
+        if (last) commit<kPair>(bar(bQFree + w));
       }
     };
     auto pv = [&](int T, int w, bool first) {
@@ -533,29 +583,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit<kPair>(bar(bPvDone + w));
       }
     };
-    auto wait_k = [&](int T) { return uwait(bKFull + T % kDepth, (T / kDepth) & 1); };
     int tbase = 0, ubase = 0, mbase = 0;
-    uint32_t items = 0, steps = 0;                            // bit w: parity of row tile w's items begun, P tiles taken
+    uint32_t items = 0, steps = 0;                            // bit w: parity of row tile w's items begun, of its P arrivals
     bool ok = true;
-    Item it;
-    // A wait that gives up makes `ok` false; what is issued until the check at the end of the tile stays inside
+    // A wait that gives up makes `ok` false; what is issued until the check at the end of the step stays inside
     // shared memory and TMEM.
-    for (uint32_t k = 0; rank == 0 && ok && next_item(k, it); ++k) {
-      const Shape sh(it, kTileRows<kPair>);
-      if (sh.n == 0) continue;
+    Shape sh{}, next{};
+    bool more = rank == 0, there = false;                     // items may follow; `next` is one, and has keys
+    uint32_t k = 0;
+    auto look_ahead = [&] {
+      Item it;
+      more = next_item(k++, it);
+      if (more) next = Shape(it, kTileRows<kPair>);
+      there = more && next.n > 0;
+    };
+    int k_landed = -1;                                        // the last key tile waited for
+    // A CTA of its own: its chain of products and softmax has no slack, and the loop below, which looks into the next
+    // item, takes 4% more there (16% a causal prompt of 4096 rows).
+    auto free_queries = [&] {
+      if (sh.n_a > 0) commit<kPair>(bar(bQFree));
+      if (sh.n_b > 0) commit<kPair>(bar(bQFree + 1));
+    };
+    while (!kPair && ok) {
+      do look_ahead();
+      while (more && !there);
+      if (!there) break;
+      sh = next;
       // the first scores: they may run while the epilogue of the item before reads its output
-      ok = wait_k(tbase);
+      ok = uwait(bKFull + tbase % kDepth, (tbase / kDepth) & 1);
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {
-        if ((w ? sh.n_b : sh.n_a) == 0) continue;
+        if ((w ? sh.n_b : sh.n_a) == 0) {
+          if (lead) commit<kPair>(bar(bSFull + w));           // an empty step
+          continue;
+        }
         ok &= uwait(bQFull + w, (items >> w) & 1);
         items ^= 1u << w;
         tc_fence_after();
-        qk(tbase, w);
+        qk(tbase, w, false);
       }
       if (lead) {
         commit<kPair>(bar(bKFree + tbase % kDepth));
-        if (sh.n == 1) commit<kPair>(bar(bQFree));
+        if (sh.n == 1) free_queries();
       }
       for (int t = 0; t < sh.n && ok; ++t) {
         const int T = tbase + t, U = ubase + t, M = mbase + t - sh.whole;
@@ -571,21 +640,87 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             pv(T, w, t == 0);
           }
-          if (w == 0 && t + 1 < sh.n) ok &= wait_k(T + 1);
+          if (w == 0 && t + 1 < sh.n) ok &= uwait(bKFull + (T + 1) % kDepth, ((T + 1) / kDepth) & 1);
           if (t + 1 < nw) {
             tc_fence_after();
-            qk(T + 1, w);
+            qk(T + 1, w, false);
           }
         }
         if (lead) {
           commit<kPair>(bar(bVFree + T % kDepth));
           if (t + 1 < sh.n) commit<kPair>(bar(bKFree + (T + 1) % kDepth));
-          if (t + 2 == sh.n) commit<kPair>(bar(bQFree));
+          if (t + 2 == sh.n) free_queries();
+        }
+      }
+      for (int w = 0; w < 2; ++w)
+        if ((w ? sh.n_b : sh.n_a) == 0) {
+          ok &= uwait(bPFull + w, (steps >> w) & 1);
+          steps ^= 1u << w;
+          if (lead) commit<kPair>(bar(bPvDone + w));
+        }
+      tbase += sh.n;
+      ubase += sh.whole;
+      mbase += sh.n - sh.whole;
+    }
+    while (kPair && ok) {
+      // Step t of the item: each row tile's product of key tile t and its scores of tile t + 1, or of the next item's
+      // first, which then run while the epilogue of this one reads its output.  Step -1, of no item, begins the first
+      // item and one behind an item without keys.
+      uint32_t begun = 0;                                     // bit w: the next item's first scores of row tile w are issued
+      for (int t = sh.n > 0 ? 0 : -1; t < sh.n && ok; ++t) {
+        const int T = tbase + t, U = ubase + t, M = mbase + t - sh.whole;
+        if (t < 0) {
+          while (more && !there) look_ahead();
+        } else {
+          // (one item only: the announcement of a second may wait for the softmax of this one)
+          if (t == max(0, sh.n - 2) && more) look_ahead();
+          ok &= t < sh.whole ? uwait(bVFull + U % kDepth, (U / kDepth) & 1)
+                             : uwait(bVClean + M % kMasked, (M / kMasked) & 1);
+        }
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+          const int nw = w ? sh.n_b : sh.n_a;
+          // P of an item's first tile also tells that its warps have finished with the item before (a row tile without
+          // keys takes an empty step for that alone)
+          if (t >= 0 && t < max(nw, 1)) {
+            ok &= uwait(bPFull + w, (steps >> w) & 1);
+            steps ^= 1u << w;
+            tc_fence_after();
+            if (nw > 0) pv(T, w, t == 0);
+            else if (lead) commit<kPair>(bar(bPvDone + w));
+          }
+          int tile = T + 1, left = nw - t - 1;                // row tile's key tiles from there on
+          if (left <= 0) {
+            // The next item's keys lie in the ring beside what this one still needs: 10 of a pair's 16 blocks one
+            // tile before the last, 5 (of 8) in the last.
+            if (!there || (begun >> w & 1) || !(t + 1 == sh.n || (kPair && t + 2 == sh.n))) continue;
+            begun |= 1u << w;
+            tile = tbase + sh.n;
+            left = w ? next.n_b : next.n_a;
+            if (left == 0) {
+              if (lead) commit<kPair>(bar(bSFull + w));
+              continue;
+            }
+            ok &= uwait(bQFull + w, (items >> w) & 1);
+            items ^= 1u << w;
+          }
+          if (tile != k_landed) ok &= uwait(bKFull + tile % kDepth, (tile / kDepth) & 1);
+          k_landed = tile;
+          tc_fence_after();
+          qk(tile, w, left == 1);
+        }
+        if (lead) {
+          if (t >= 0) commit<kPair>(bar(bVFree + T % kDepth));
+          if (t + 1 < sh.n || there) commit<kPair>(bar(bKFree + (T + 1) % kDepth));
         }
       }
       tbase += sh.n;
       ubase += sh.whole;
       mbase += sh.n - sh.whole;
+      if (there) sh = next;
+      else if (more) sh = Shape{};
+      else break;
+      there = false;
     }
     if (rank == 0) {
       if (lead) commit<kPair>(bar(bDrain));
@@ -649,7 +784,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             const int at = 8 * (M % kMasked) + 4 * static_cast<int>(rank) + m;
             bad[at] = mask;
-            if constexpr (kPair) st_cluster_b32(mapa_shared(base + kOffBad + 4 * at, peer), mask);
+            if (mask) *reinterpret_cast<volatile int*>(smem + kOffFound) = 1;
+            if constexpr (kPair) {
+              st_cluster_b32(mapa_shared(base + kOffBad + 4 * at, peer), mask);
+              if (mask) st_cluster_b32(mapa_shared(base + kOffFound, peer), 1);
+            }
           }
         }
         fence_proxy_async_smem();
@@ -687,6 +826,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (half == 0) mine = *meet;
       return mine;
     };
+    auto arrive_p = [&] {
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kPair) arrive_leader_relaxed(bar(bPFull + w));
+        else mbar_arrive(bar(bPFull + w));
+      }
+    };
     uint32_t step = 0;                                        // key tiles of this row tile, over all items
     int mbase = 0;
     bool ok = true;
@@ -695,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // The item's words are read here for the loop over the keys and again for the epilogue: held in between
       // they would cost registers that the scores need.
-      int nw, seen, first_masked;
+      int nw, seen;
       {
         Item it;
         if (!announced(k, it)) {
@@ -704,8 +850,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const Shape sh(it, kTileRows<kPair>);
         nw = w ? sh.n_b : sh.n_a;
+        if (nw == 0 && sh.n > 0) {                            // the empty step
+          ok = warp_wait(bar(bSFull + w), step++ & 1, wc);
+          arrive_p();
+        }
         seen = min(it.nk, it.off + row + 1) - 64 * half;      // of the half's keys, counted from its first, those this row sees
-        first_masked = min(max(it.off + row0 + 1, 0), it.nk) / kPfKeys;   // of this CTA's rows
       }
       float ref = -INFINITY, sum = 0.f;
       for (int t = 0; t < nw; ++t, ++step) {
@@ -716,8 +865,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(ts, s[0]);
           tmem_ld32(ts + 32, s[1]);
           tmem_wait_ld();
-          if (t >= first_masked) {
-            const int left = seen - t * kPfKeys;
+          const int left = seen - t * kPfKeys;
+          if (left < 64) {
 #pragma unroll
             for (int c = 0; c < 64; ++c)
               if (c >= left) s[c / 32][c % 32] = 0xFF800000u;
@@ -784,11 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (kPair) arrive_leader_relaxed(bar(bPFull + w));
-          else mbar_arrive(bar(bPFull + w));
-        }
+        arrive_p();
         sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
       }
       if (ok && nw > 0) {
@@ -797,18 +942,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       Item it;
       announced(k, it);
-      release_item(k);
       const Shape sh(it, kTileRows<kPair>);
       uint32_t dirty = 0;                                     // some masked tile of this row tile had its values cleared
-      for (int t = sh.whole; t < nw && ok; ++t) {
-        const int M = mbase + t - sh.whole;
+      if (ok && nw > sh.whole) {                              // the guard's notes up to this row tile's last
+        const int M = mbase + nw - 1 - sh.whole;
         ok = warp_wait<kPair>(bar(bVClean + M % kMasked), (M / kMasked) & 1, wc);
-        for (int i = 0; i < 8; ++i) dirty |= bad[8 * (M % kMasked) + i];
+        if (*reinterpret_cast<volatile int*>(smem + kOffFound))
+          for (int t = sh.whole; t < nw; ++t)
+            for (int i = 0; i < 8; ++i) dirty |= bad[8 * ((mbase + t - sh.whole) % kMasked) + i];
       }
       if (row0 < it.nq) {                                  // both warps, whole: they meet, and tcgen05.ld is collective
-        sum = both(sum, [](float a, float b) { return a + b; });
-        ok = both(ok ? 1.f : 0.f, [](float a, float b) { return fminf(a, b); }) > 0.f;
+        if (half == 0) *meet = sum;
+        ok = !named_bar_or(pair_bar, 64, !ok);
         if (!ok) break;
+        if (half == 1) {
+          sum += *meet;
+          *meet = sum;
+        }
+        named_bar_sync(pair_bar, 64);
+        if (half == 0) sum = *meet;
         const bool any = nw > 0 && !(sum == 0.f);
         const float inv = any ? 1.f / sum : 0.f;
         const float lse = any ? (ref + log2f(sum)) * 0.69314718055994531f : -INFINITY;
@@ -819,8 +971,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (it.part >= 0) p.part_lse[part_row] = lse;
           else if (p.lse) p.lse[out_row] = lse;
         }
+        // all but rows without a key and tiles of which the guard has taken out values
+        const int mate = lane & 3, first = row - mate;        // of the first of four lanes' rows
+        const bool plain = __all_sync(0xffffffffu, any) && dirty == 0;
+        if (plain && it.part < 0)
+          store_columns(to, inv, p.out + (out_row - static_cast<size_t>(mate) * p.heads) * kNope + 64 * half + 8 * mate,
+                        static_cast<size_t>(p.heads) * kNope, it.nq - first);
+        else if (plain)
+          store_columns(to, inv, p.part_o + (part_row - mate) * kNope + 64 * half + 4 * mate, static_cast<size_t>(kNope),
+                        it.nq - first);
 #pragma unroll 1
-        for (int c = 64 * half; c < 64 * half + 64; c += 16) {
+        for (int c = 64 * half; c < 64 * half + 64 && !plain; c += 16) {
           uint32_t o[16];
           if (nw > 0) {
             tmem_ld16(to + (c & 48), o);
@@ -845,9 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(static_cast<uint32_t>(v[e]) << 16));
                 }
           }
-          // Four lanes exchange blocks, so that a store writes whole sectors of a row: row by row, 16 bytes a
-          // lane, the stores took a third of the epilogue.  After it lane i of four holds block i of their rows.
-          const int mate = lane & 3, first = row - mate;      // the first of the four lanes' rows
+          // the same exchange, of 16 columns
           if (it.part >= 0) {
             transpose4_blocks<4>(o, lane);
             float* dst = p.part_o + (part_row - mate) * kNope + c + 4 * mate;
@@ -869,6 +1028,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mbase += sh.n - sh.whole;
+      __syncwarp();
+      if (lane == 0) {                                        // the item's words have been read
+        if constexpr (kPair) arrive_leader_relaxed(bar(bSchedFree + k % kSched));
+        else mbar_arrive(bar(bSchedFree + k % kSched));
+      }
     }
   }
   tc_fence_before();
