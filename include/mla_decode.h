@@ -613,7 +613,8 @@ int mla_expand_kv_fp8(const void* kv_cache, int64_t num_slots, float kv_scale, c
  *   num_sms, plan, plan_words, plan_words_needed, workspace_bytes: as for
  *   mla_decode_plan.
  * Errors: those of mla_decode_plan; any num_heads of 1 .. 65535 is supported;
- * MLA_ERR_UNSUPPORTED for 2^30 - 1 or more queries or keys. */
+ * MLA_ERR_UNSUPPORTED for 2^30 - 1 or more queries or keys, or more than
+ * 2^31 - 2^16 - 1 tiles over all heads. */
 int mla_prefill_plan(const int32_t* q_indptr, const int32_t* kv_indptr, int32_t batch, int32_t num_heads,
                      int32_t causal, int32_t num_sms, int32_t* plan, size_t plan_words, size_t* plan_words_needed,
                      size_t* workspace_bytes);
@@ -622,7 +623,8 @@ int mla_prefill_plan(const int32_t* q_indptr, const int32_t* kv_indptr, int32_t 
  *
  *   s_ij = sm_scale (q_i . [k_nope_j, k_rope_j]);   lse_i = ln sum_j exp(s_ij);
  *   out_i = sum_j softmax(s_i)_j v_j                 over the keys row i sees.
- * A row that sees no key gets out = 0 and lse = -inf.  Values of keys that a
+ * A row that sees no key, or none with a score above -inf, gets out = 0 and
+ * lse = -inf.  Values of keys that a
  * row does not see never reach it, whatever they are.
  *   plan_host, plan_dev  the words of mla_prefill_plan, on both sides
  *              (plan_dev 16-byte aligned).
@@ -634,7 +636,7 @@ int mla_prefill_plan(const int32_t* q_indptr, const int32_t* kv_indptr, int32_t 
  *              k_nope, k_rope and v are not looked at when there are no keys.
  *   Strides are at least the width of what lies there (192, 128, 64), where
  *   there is more than one row or head, and below 2^38.
- *   out        device bf16 [q rows, heads, 128] dense; the weights of the
+ *   out        device bf16 [q rows, heads, 128] dense, apart from the inputs; the weights of the
  *              values are rounded to bf16, sums are fp32.
  *   lse        device fp32 [q rows, heads] or NULL.
  *   workspace  device, at least the plan's workspace_bytes, 16-byte aligned,

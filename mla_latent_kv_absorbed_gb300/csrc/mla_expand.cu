@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = 16 * (2 * i + (sub >> 2)) + (rt >> 3);
             x[i] = *reinterpret_cast<const uint4*>(chunk + BM * 64 + r * 64 + (sub & 3) * 16);
           }
-          named_bar_sync(1, 128);
+          ok = !named_bar_or(1, 128, !ok);                   // (all four warps leave after the same block)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = 16 * (2 * i + (sub >> 2)) + (rt >> 3), c = 2 * (sub & 3);

@@ -837,7 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int mbase = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
-      ok = warp_wait<kPair>(bar(bSched + k % kSched), (k / kSched) & 1, wc);
+      // (a wait that gives up ends both warps of a row at the same place: neither is left at their barrier)
+      ok = !named_bar_or(pair_bar, 64, !warp_wait<kPair>(bar(bSched + k % kSched), (k / kSched) & 1, wc));
       if (!ok) break;
       // The item's words are read here for the loop over the keys and again for the epilogue: held in between
       // they would cost registers that the scores need.
@@ -906,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               rescale_columns(to, f);
               load_scores();                                  // again: held over the rescaling they would be spilled
               tc_fence_before();
-              named_bar_sync(pair_bar, 64);
+              ok = !named_bar_or(pair_bar, 64, !ok);
               tc_fence_after();
             }
           }
@@ -951,10 +952,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = sh.whole; t < nw; ++t)
             for (int i = 0; i < 8; ++i) dirty |= bad[8 * ((mbase + t - sh.whole) % kMasked) + i];
       }
+      if (half == 0) *meet = sum;
+      ok = !named_bar_or(pair_bar, 64, !ok);
+      if (!ok) break;
       if (row0 < it.nq) {                                  // both warps, whole: they meet, and tcgen05.ld is collective
-        if (half == 0) *meet = sum;
-        ok = !named_bar_or(pair_bar, 64, !ok);
-        if (!ok) break;
         if (half == 1) {
           sum += *meet;
           *meet = sum;

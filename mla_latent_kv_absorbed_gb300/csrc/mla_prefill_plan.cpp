@@ -40,6 +40,7 @@ constexpr long long kItemCost = 14;
 constexpr long long kPieceCost = 4;
 constexpr long long kJoinCost = 12;
 constexpr long long kL2Bytes = 64ll << 20;
+constexpr int kMostSms = 4096;        // planned for: more than any device has
 
 inline int key_tiles(int nk) { return (nk + kPfKeys - 1) / kPfKeys; }
 // One row tile has no other to fill its softmax's time: 8 of 10.  A pair's two
@@ -106,10 +107,6 @@ long long makespan(const std::vector<Piece>& pieces, int heads, int group, int s
   return end;
 }
 
-}  // namespace
-
-namespace {
-
 // The tiles of `rows` query rows and their pieces in launch order; returns the
 // end of the greedy schedule.
 long long plan_rows(const int32_t* qp, const int32_t* kp, int B, int H, int causal, int rows, int workers,
@@ -166,16 +163,17 @@ int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int c
                        std::vector<int32_t>& words) {
   std::vector<Tile> tiles;
   std::vector<Piece> best;
-  int rows = kPfRows, workers = num_sms;
+  const int sms = std::min(num_sms, kMostSms);
+  int rows = kPfRows, workers = sms;
   const long long end = plan_rows(qp, kp, B, H, causal, rows, workers, tiles, best);
-  if (num_sms >= 2) {
+  if (sms >= 2) {
     std::vector<Tile> pair_tiles;
     std::vector<Piece> pair_best;
-    if (plan_rows(qp, kp, B, H, causal, 2 * kPfRows, num_sms / 2, pair_tiles, pair_best) < end) {
+    if (plan_rows(qp, kp, B, H, causal, 2 * kPfRows, sms / 2, pair_tiles, pair_best) < end) {
       tiles.swap(pair_tiles);
       best.swap(pair_best);
       rows = 2 * kPfRows;
-      workers = num_sms / 2;
+      workers = sms / 2;
     }
   }
   // partial slots, in tile order, and the merge entries
@@ -191,7 +189,7 @@ int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int c
   const long long n_words = kPfHeaderWords + static_cast<long long>(kPfItemWords) * best.size() +
                             static_cast<long long>(kPfMergeWords) * merges;
   const long long blocks = static_cast<long long>(best.size()) * H;
-  if (n_words > 0x7FFFFFFFll || blocks > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
+  if (n_words > 0x7FFFFFFFll || blocks > kPfMaxBlocks) return MLA_ERR_UNSUPPORTED;
   const int group = group_of(H, kp[B], best.size(), workers);
   words.assign(static_cast<size_t>(n_words), 0);
   words[kPMagic] = kPfMagic;

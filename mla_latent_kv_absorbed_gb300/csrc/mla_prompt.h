@@ -72,6 +72,7 @@ constexpr int kPfItemWords = 8;       // request, q0, nq, k0, nk, off, partial (
 constexpr int kPfMergeWords = 4;      // q0, nq, first partial, last partial + 1
 constexpr int kPfRows = 256;          // query rows of one CTA's item, at most
 constexpr int kPfKeys = 128;          // keys of a tile
+constexpr long long kPfMaxBlocks = 0x7FFF0000;   // items x heads: every block of the launch counts one past them
 constexpr int32_t kPfNoLimit = 0x3FFFFFFF;   // off of an item without a causal limit
 
 // Words of the workspace's status header that the prefill kernel counts in

@@ -272,7 +272,7 @@ bool prefill_header_ok(const int32_t* h) {
       h[kPItems] < 0 || h[kPPartials] < 0 || h[kPMerges] < 0 || h[kPMerges] > 65535 || h[kPHeadGroup] < 1 ||
       h[kPHeadGroup] > h[kPHeads] || (h[kPRows] != kPfRows && h[kPRows] != 2 * kPfRows))
     return false;
-  if (static_cast<long long>(h[kPItems]) * h[kPHeads] > 0x7FFFFFFFll) return false;
+  if (static_cast<long long>(h[kPItems]) * h[kPHeads] > kPfMaxBlocks) return false;
   const long long words = kPfHeaderWords + static_cast<long long>(kPfItemWords) * h[kPItems] +
                           static_cast<long long>(kPfMergeWords) * h[kPMerges];
   return words == h[kPTotalWords];

@@ -549,6 +549,33 @@ def test_prefill_keeps_what_is_masked_out(bad, causal, pairs):
         assert np.isnan(o[sees_k]).all() and np.isnan(l[sees_k]).all()
 
 
+@pytest.mark.parametrize("pairs", [False, True])
+def test_prefill_keeps_its_notes_until_they_are_read(pairs):
+    # values that are not finite in partly seen tiles, of items with two row tiles, and behind each of those items
+    # several with one row tile, which the block goes on to while the second row tile's output is still written
+    torch, B = _t()
+    L = 512 if pairs else 256
+    big, small = 152 if not pairs else 76, 900
+    ql = [L] * big + [64] * small
+    qp = kp = _indptr(ql)
+    plan = B.Prefiller(qp, kp, 1)
+    if pairs:
+        plan = _on_pairs(plan, qp, kp, 1, True)
+    (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(21, int(qp[-1]), int(kp[-1]), 1)
+    ref, ref_lse, mag = P.prefill_attention(xq, xk, xr, xv, qp, kp, SM, True)
+    first = L - 126                                              # the first of the keys with a bad value
+    sees = np.zeros(ref.shape, dtype=bool)
+    for b in range(big):
+        v[int(kp[b]) + first:int(kp[b]) + L, 0, 5] = float("inf")
+        sees[int(qp[b]) + first:int(qp[b]) + L, 0, 5] = True
+    out, lse = _attend(plan, q, k, kr, v)
+    o = _f64(out)
+    assert (o[sees] == np.inf).all()
+    assert np.isfinite(o[~sees]).all()
+    assert (np.abs(o - ref)[~sees] <= _attention_bound(ref, mag)[~sees]).all()
+    assert np.abs(lse.double().cpu().numpy() - ref_lse).max() <= LSE_ATOL
+
+
 def test_prefill_leaves_rows_behind_the_last_sequence():
     torch, B = _t()
     qp = kp = _indptr([100, 60])

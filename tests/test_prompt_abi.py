@@ -173,6 +173,8 @@ def test_prefill_plan_refuses_bad_arguments(B):
     assert f(qp=(1, 5)) == 1 and f(kp=(1, 9)) == 1 and f(qp=(0, -1)) == 1 and f(b=2, qp=(0, 5, 4), kp=(0, 1, 2)) == 1
     assert f(b=-1) == 1 and f(H=0) == 1 and f(H=65536) == 1 and f(causal=2) == 1 and f(sms=-1) == 1
     assert f(kp=(0, (1 << 30) - 1)) == 2 and f(qp=(0, (1 << 30) - 1)) == 2
+    assert f(qp=(0, 1 << 24), kp=(0, 0), H=65535) == 2         # more tiles than a launch counts
+    assert f(sms=2 ** 31 - 1) == 0
     buf = np.zeros(24, dtype=np.int32)
     assert f(plan=buf.ctypes.data, words=23) == 3 and f(plan=buf.ctypes.data, words=24) == 0
     assert lib.mla_prefill_plan(None, buf.ctypes.data, 0, 1, 1, 152, None, 0, None, None) == 1
