@@ -33,23 +33,25 @@ struct Piece {
   long long cost;
 };
 
-// Costs in tenths of a key tile against two row tiles (about 460 cycles each;
-// measured over a ragged batch): an item's first loads and its epilogue, a
-// partial output written and read again, the joining kernel's launch.
-constexpr long long kItemCost = 14;
-constexpr long long kPieceCost = 4;
-constexpr long long kJoinCost = 12;
+// Costs in twentieths of a key tile against two row tiles of one CTA (a unit is
+// about 180 cycles; traced over causal and ragged batches): a partial output
+// written and read again, the joining kernel's launch.
+constexpr long long kPieceCost = 8;
+constexpr long long kJoinCost = 24;
 constexpr long long kL2Bytes = 64ll << 20;
 constexpr int kMostSms = 4096;        // planned for: more than any device has
 
 inline int key_tiles(int nk) { return (nk + kPfKeys - 1) / kPfKeys; }
-// One row tile has no other to fill its softmax's time: 8 of 10.  A pair's two
-// tiles of 256 rows take nine tenths of what one CTA's two of 128 do, on
-// two SMs.
+// A key tile: 3630 cycles against two row tiles; one has no other to fill its
+// softmax's time (3080).  A pair's two tiles of 256 rows take 3250, on two SMs
+// (counted lower: without a causal limit one CTA's take 4100).
 inline long long tile_cost(int nq, int rows) {
-  if (rows == kPfRows) return nq > rows / 2 ? 10 : 8;
-  return nq > rows / 2 ? 9 : 8;
+  if (rows == kPfRows) return nq > rows / 2 ? 20 : 17;
+  return nq > rows / 2 ? 17 : 16;
 }
+// An item's first loads and scores and its epilogue, as far as nothing fills
+// them: 7300 cycles, a pair's 10000.
+inline long long item_cost(int rows) { return rows == kPfRows ? 40 : 54; }
 
 // Parts of a tile whose keys are cut into pieces of at most `cap` (0: not cut), none under four key tiles.
 int parts_of(const Tile& t, int rows, long long cap) {
@@ -74,7 +76,7 @@ void cut(const std::vector<Tile>& tiles, int rows, long long cap, std::vector<Pi
     for (int k = 0; k < parts; ++k) {
       const int a = static_cast<int>(static_cast<long long>(nt) * k / parts);
       const int e = static_cast<int>(static_cast<long long>(nt) * (k + 1) / parts);
-      pieces.push_back({static_cast<int>(i), a, e - a, c * (e - a) + kItemCost + (parts > 1 ? kPieceCost : 0)});
+      pieces.push_back({static_cast<int>(i), a, e - a, c * (e - a) + item_cost(rows) + (parts > 1 ? kPieceCost : 0)});
     }
   }
   std::stable_sort(pieces.begin(), pieces.end(), [](const Piece& x, const Piece& y) { return x.cost > y.cost; });
