@@ -21,9 +21,27 @@
 // bits at any magnitude, sums are fp32), and O is rescaled in TMEM only then.
 //
 // A row tile's scores, weights and product follow one another (the weights lie
-// over the scores), so its key tile takes as long as that chain; the other row
-// tile fills half of it.  Hence two threads a row: with one (1500 cycles a
-// tile instead of ~800) the chain was 4000 cycles, 2600 of them products.
+// over the scores), so its key tile takes as long as that chain: 1260 cycles of
+// softmax, 250-600 until the issuer has seen it, 1280 of products, 500 until
+// the next scores are seen - 3630 for a step of both row tiles, of which 2580
+// are products.  Hence two threads a row: with one the softmax took 1500 and
+// the step 4000.  Three forms, chosen by the plan:
+//   kPair   two CTAs of a cluster and 512 rows (cta_group::2: products of 256
+//           rows, CTA 0 issues).  Each CTA holds half of the keys and values,
+//           a step takes 3250 cycles for twice the rows, and the ring holds
+//           3.2 key tiles instead of 1.6; but an item's ends (first scores,
+//           epilogue, up to five partly seen tiles) cost 10000 cycles instead
+//           of 7300, and items are coarser.  4096 causal rows x 128 heads: 478
+//           us (1437 TFLOP/s) against 499 with single CTAs; 8192 x 64 heads
+//           827 against 892, without a causal limit 1538 against 1925; but
+//           1024 x 128 heads 66 against 61.
+//   kSolo   no item has more than 128 rows: one row tile, whose scores take
+//           turns in both score buffers (the next key tile's are formed under
+//           the softmax of this one), and the second tile's queries' place is
+//           ring (2.2 key tiles).  Bound by HBM: 64 rows over 65536 and 32064
+//           keys x 16 heads take 143 us (5.7 TB/s); with the general form,
+//           whose step of one row tile is the chain of 3080 cycles, 159; with
+//           two score buffers and the general form's ring 178.
 //
 // Warps: 0-7 softmax and epilogue of tile A, 8-15 of tile B, 16 TMA producer,
 // 17 MMA issuer, 18-19 the guard.  A tile that some row sees only in part is
@@ -53,11 +71,13 @@ constexpr int kOffQ = 0;                              // 2 row tiles x 3 blocks 
 // A pair's CTA has half of each: blocks of 64 keys x 64 dims.
 constexpr int kOffRing = 6 * kBlock;
 constexpr int kRingBytes = 8 * kBlock;
+constexpr int kOffRingSolo = 3 * kBlock;              // a launch of items with one row tile: from behind its queries on
 constexpr int kOffBar = kOffRing + kRingBytes;
 constexpr int kDepth = 4;                             // tiles told apart: more than the ring holds
 constexpr int kSched = 4;                             // items announced ahead
 constexpr int kMasked = 8;                            // masked tiles told apart: two items' worth and more
-constexpr int kConsumers = 16 + 1 + 2;                // warps that read an announced item (in CTA 1: no issuer, but the producer)
+constexpr int kConsumers = 16 + 1 + 2;                // warps that read an announced item (in CTA 1: no issuer, but the
+                                                      // producer; 8 fewer where there is no second row tile)
 enum Bar : int {
   bQFull = 0,                    // [2] per row tile
   bQFree = bQFull + 2,           // [2] the row tile's last scores of the item are done
@@ -66,7 +86,8 @@ enum Bar : int {
   bKFree = bVFull + kDepth,      // [4] its QK products are done
   bVFree = bKFree + kDepth,      // [4]
   bSFull = bVFree + kDepth,           // [2] per row tile
-  bPFull = bSFull + 2,           // [2]
+  bSOdd = bSFull + 2,            // odd key tiles of an item, in a launch of items with one row tile
+  bPFull = bSOdd + 1,            // [2] per row tile; with one, of even and odd key tiles
   bPvDone = bPFull + 2,          // [2]
   bVMasked = bPvDone + 2,         // [8] the values of masked tile M (on M & 7) have landed
   bVClean = bVMasked + kMasked,  // [8] and the guard has been over them
@@ -96,12 +117,12 @@ struct Item {
 
 // The item's words, or false (and MLA_ERR_PLAN_MISMATCH) when it does not lie
 // inside the arrays of this launch or has keys past its last row's limit.
-template <bool kPair>
+template <bool kPair, bool kSolo>
 __device__ __forceinline__ bool load_item(const PrefillParams& p, int i, Item& it) {
   const int4 a = __ldg(reinterpret_cast<const int4*>(p.items) + 2 * i);
   const int4 b = __ldg(reinterpret_cast<const int4*>(p.items) + 2 * i + 1);
   it = Item{a.y, a.z, a.w, b.x, b.y, b.z, 0};
-  return it.q0 >= 0 && it.nq >= 1 && it.nq <= 2 * kTileRows<kPair> && it.q0 <= p.q_tokens - it.nq && it.k0 >= 0 && it.nk >= 0 &&
+  return it.q0 >= 0 && it.nq >= 1 && it.nq <= (kSolo ? 1 : 2) * kTileRows<kPair> && it.q0 <= p.q_tokens - it.nq && it.k0 >= 0 && it.nk >= 0 &&
          it.k0 <= p.kv_tokens - it.nk && it.part >= -1 && it.part < p.partials && it.off >= -kPfNoLimit &&
          it.off <= kPfNoLimit && (it.nk == 0 || it.nk <= it.off + it.nq);
 }
@@ -311,7 +332,7 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) return;
 }
 
-template <bool kPair>
+template <bool kPair, bool kSolo>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_v,
@@ -327,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + kOffBad);
   int* sched = reinterpret_cast<int*>(smem + kOffSched);
   const WaitCtx wc{abort_flag, p.status};
-  constexpr int kRingBlock = kPair ? kBlock / 2 : kBlock, kSlots = kRingBytes / kRingBlock;
+  constexpr int kRingBlock = kPair ? kBlock / 2 : kBlock;
+  constexpr int kRing = kSolo ? kOffRingSolo : kOffRing, kSlots = (kOffBar - kRing) / kRingBlock;
   constexpr int kCtas = kPair ? 2 : 1;
   const uint32_t rank = kPair ? cluster_ctarank() : 0;
   const uint32_t peer = rank ^ 1u;
@@ -337,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool eight = i >= bPFull && i < bPFull + 2;
       const bool two = i >= bVClean && i < bVClean + kMasked;
       const bool all = i >= bSchedFree && i < bSchedFree + kSched;
-      mbar_init(bar(i), eight ? 8 * kCtas : two ? 2 * kCtas : all ? kConsumers * kCtas : 1);
+      mbar_init(bar(i), eight ? 8 * kCtas : two ? 2 * kCtas : all ? (kConsumers - (kSolo ? 8 : 0)) * kCtas : 1);
     }
     *abort_flag = 0;
     *reinterpret_cast<int*>(smem + kOffFound) = 0;
@@ -398,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g = w / per_group, rest = w - g * per_group;
         const int in_group = min(p.head_group, p.heads - g * p.head_group);
         const int item = rest / in_group;
-        if (!load_item<kPair>(p, item, it)) {
+        if (!load_item<kPair, kSolo>(p, item, it)) {
           record_status(p.status, MLA_ERR_PLAN_MISMATCH);
           it.nk = it.nq = 0;
         }
@@ -462,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int b = (c - kSlots) % 5 < 3 ? bKFree : bVFree;
             ok = mbar_wait(bar(b + u % kDepth), (u / kDepth) & 1, wc);
           }
-          return base + kOffRing + (c % kSlots) * kRingBlock;
+          return base + kRing + (c % kSlots) * kRingBlock;
         };
         auto load_k = [&](int t) {
           const int T = tbase + t;
@@ -557,10 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool lead = elect_one();
     const uint32_t idesc_s = idesc_bf16(kTileRows<kPair>, 128, false, false) | (p.negate ? 1u << 13 : 0u);   // -Q
     constexpr uint32_t kIdescO = idesc_bf16(kTileRows<kPair>, 128, false, true);
-    auto block_at = [&](int c) -> uint32_t { return base + kOffRing + (c % kSlots) * kRingBlock; };
+    auto block_at = [&](int c) -> uint32_t { return base + kRing + (c % kSlots) * kRingBlock; };
     // scores of key tile T for row tile w; its last of the item: the queries are free
-    auto qk = [&](int T, int w, bool last) {
-      const uint32_t d = tmem + kTmemS + 128 * w;
+    auto qk = [&](int T, int w, bool last, int odd = 0) {
+      const uint32_t d = tmem + kTmemS + 128 * (w + odd);
       const uint32_t a = desc_low(base + kOffQ + 3 * w * kBlock, 16);
       const uint32_t b0 = desc_low(block_at(5 * T), 16), b1 = desc_low(block_at(5 * T + 1), 16),
                      b2 = desc_low(block_at(5 * T + 2), 16);
@@ -569,12 +591,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 12; ++k)
           mma_ss<kDescHigh, kPair>(d, a + (k >> 2) * (kBlock >> 4) + 2 * (k & 3), (k < 4 ? b0 : k < 8 ? b1 : b2) + 2 * (k & 3),
                             idesc_s, k > 0);
-        commit<kPair>(bar(bSFull + w));
+        commit<kPair>(bar(bSFull + w + 2 * odd));
         if (last) commit<kPair>(bar(bQFree + w));
       }
     };
-    auto pv = [&](int T, int w, bool first) {
-      const uint32_t a = tmem + kTmemS + 128 * w, d = tmem + kTmemO + 128 * w;
+    auto pv = [&](int T, int w, bool first, int odd = 0) {
+      const uint32_t a = tmem + kTmemS + 128 * (w + odd), d = tmem + kTmemO + 128 * w;
       const uint32_t b0 = desc_low(block_at(5 * T + 3), kBlock / 2), b1 = desc_low(block_at(5 * T + 4), kBlock / 2);
       if (lead) {
 #pragma unroll
@@ -584,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     int tbase = 0, ubase = 0, mbase = 0;
-    uint32_t items = 0, steps = 0;                            // bit w: parity of row tile w's items begun, of its P arrivals
+    uint32_t items = 0, steps = 0;                            // bit w: parity of row tile w's items begun, of its P barrier
     bool ok = true;
     // A wait that gives up makes `ok` false; what is issued until the check at the end of the step stays inside
     // shared memory and TMEM.
@@ -600,11 +622,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k_landed = -1;                                        // the last key tile waited for
     // A CTA of its own: its chain of products and softmax has no slack, and the loop below, which looks into the next
     // item, takes 4% more there (16% a causal prompt of 4096 rows).
+    // One row tile in every item: the scores of the next key tile are formed, in a second buffer, under the softmax
+    // of this one.
+    while (kSolo && ok) {
+      do look_ahead();
+      while (more && !there);
+      if (!there) break;
+      sh = next;
+      ok = uwait(bKFull + tbase % kDepth, (tbase / kDepth) & 1) && uwait(bQFull, items & 1);
+      items ^= 1u;
+      tc_fence_after();
+      qk(tbase, 0, sh.n == 1);
+      if (lead) commit<kPair>(bar(bKFree + tbase % kDepth));
+      for (int t = 0; t < sh.n && ok; ++t) {
+        const int T = tbase + t, U = ubase + t, M = mbase + t - sh.whole;
+        if (t + 1 < sh.n) {
+          ok &= uwait(bKFull + (T + 1) % kDepth, ((T + 1) / kDepth) & 1);
+          tc_fence_after();
+          qk(T + 1, 0, t + 2 == sh.n, ~t & 1);
+          if (lead) commit<kPair>(bar(bKFree + (T + 1) % kDepth));
+        }
+        ok &= t < sh.whole ? uwait(bVFull + U % kDepth, (U / kDepth) & 1)
+                           : uwait(bVClean + M % kMasked, (M / kMasked) & 1);
+        // (the softmax may be a tile ahead here: even and odd tiles' weights have a barrier each)
+        ok &= uwait(bPFull + (t & 1), (steps >> (t & 1)) & 1);
+        steps ^= 1u << (t & 1);
+        tc_fence_after();
+        pv(T, 0, t == 0, t & 1);
+        if (lead) commit<kPair>(bar(bVFree + T % kDepth));
+      }
+      tbase += sh.n;
+      ubase += sh.whole;
+      mbase += sh.n - sh.whole;
+    }
     auto free_queries = [&] {
       if (sh.n_a > 0) commit<kPair>(bar(bQFree));
       if (sh.n_b > 0) commit<kPair>(bar(bQFree + 1));
     };
-    while (!kPair && ok) {
+    while (!kPair && !kSolo && ok) {
       do look_ahead();
       while (more && !there);
       if (!there) break;
@@ -738,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = sh.whole; t < sh.n; ++t, ++M) {
         ok = warp_wait(bar(bVMasked + M % kMasked), (M / kMasked) & 1, wc);
         if (!ok) break;
-        uint8_t* half = smem + kOffRing + ((5 * (tbase + t) + 3 + g) % kSlots) * kRingBlock;
+        uint8_t* half = smem + kRing + ((5 * (tbase + t) + 3 + g) % kSlots) * kRingBlock;
 #pragma unroll 1
         for (int m = 2 * g; m < 2 * g + 2; ++m) {
           const int r = 32 * (m & 1) + lane;                  // row of this half's 64: key 32 m + lane of the tile
@@ -800,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tbase += sh.n;
     }
-  } else {
+  } else if (!kSolo || warp < 8) {
     // -------------------------------------------------- softmax and epilogue
     // Two threads a row, in warps `warp` and `warp` ^ 4: each takes half of a
     // tile's keys and half of the output's columns.  They meet at a named
@@ -826,14 +881,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (half == 0) mine = *meet;
       return mine;
     };
-    auto arrive_p = [&] {
+    auto arrive_p = [&](int t) {
       __syncwarp();
       if (lane == 0) {
         if constexpr (kPair) arrive_leader_relaxed(bar(bPFull + w));
-        else mbar_arrive(bar(bPFull + w));
+        else mbar_arrive(bar(bPFull + (kSolo ? t & 1 : w)));
       }
     };
     uint32_t step = 0;                                        // key tiles of this row tile, over all items
+    uint32_t scores = 0;                                      // kSolo: parities of the two score barriers
     int mbase = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
@@ -851,20 +907,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const Shape sh(it, kTileRows<kPair>);
         nw = w ? sh.n_b : sh.n_a;
-        if (nw == 0 && sh.n > 0) {                            // the empty step
+        if (!kSolo && nw == 0 && sh.n > 0) {                  // the empty step
           ok = warp_wait(bar(bSFull + w), step++ & 1, wc);
-          arrive_p();
+          arrive_p(0);
         }
         seen = min(it.nk, it.off + row + 1) - 64 * half;      // of the half's keys, counted from its first, those this row sees
       }
       float ref = -INFINITY, sum = 0.f;
       for (int t = 0; t < nw; ++t, ++step) {
-        ok = warp_wait(bar(bSFull + w), step & 1, wc);
+        uint32_t buf = 0;
+        if constexpr (kSolo) {
+          buf = 128 * (t & 1);
+          ok = warp_wait(bar(buf ? bSOdd : bSFull), (buf ? scores >> 1 : scores) & 1, wc);
+          scores ^= buf ? 2 : 1;
+        } else {
+          ok = warp_wait(bar(bSFull + w), step & 1, wc);
+        }
         tc_fence_after();
         uint32_t s[2][32];
         auto load_scores = [&] {
-          tmem_ld32(ts, s[0]);
-          tmem_ld32(ts + 32, s[1]);
+          tmem_ld32(ts + buf, s[0]);
+          tmem_ld32(ts + buf + 32, s[1]);
           tmem_wait_ld();
           const int left = seen - t * kPfKeys;
           if (left < 64) {
@@ -930,11 +993,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             else acc0 = f2_add(acc0, y);
             pk[e] = pack_bf16x2(y.x, y.y);
           }
-          tmem_st8(tp + 8 * c, pk);
+          tmem_st8(tp + buf + 8 * c, pk);
         }
         tmem_wait_st();
         tc_fence_before();
-        arrive_p();
+        arrive_p(t);
         sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
       }
       if (ok && nw > 0) {
@@ -1104,7 +1167,7 @@ int launch_prefill(const PrefillParams& p, const CUtensorMap& tm_q, const CUtens
                    const CUtensorMap& tm_v, cudaStream_t stream) {
   if (p.n_items <= 0) return MLA_OK;
   const bool pair = p.rows > kPfRows;
-  const auto kernel = pair ? &prefill_kernel<true> : &prefill_kernel<false>;
+  const auto kernel = pair ? &prefill_kernel<true, false> : p.solo ? &prefill_kernel<false, true> : &prefill_kernel<false, false>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), kSmemBytes)) return MLA_ERR_CUDA;
   const int sms = device_sm_count();
   if (sms < 1) return MLA_ERR_CUDA;

@@ -208,6 +208,7 @@ int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int c
   words[kPTotalWords] = static_cast<int32_t>(n_words);
   words[kPNumSms] = num_sms;
   words[kPRows] = rows;
+  words[kPSolo] = std::all_of(tiles.begin(), tiles.end(), [](const Tile& t) { return t.nq <= kPfRows / 2; }) ? 1 : 0;
   int32_t* w = words.data() + kPfHeaderWords;
   for (const Piece& p : best) {
     const Tile& t = tiles[p.tile];

@@ -270,7 +270,8 @@ bool prefill_header_ok(const int32_t* h) {
   if (!h || h[kPMagic] != kPfMagic || h[kPVersion] != kPfVersion) return false;
   if (h[kPBatch] < 0 || h[kPHeads] < 1 || h[kPHeads] > 65535 || h[kPQTokens] < 0 || h[kPKvTokens] < 0 ||
       h[kPItems] < 0 || h[kPPartials] < 0 || h[kPMerges] < 0 || h[kPMerges] > 65535 || h[kPHeadGroup] < 1 ||
-      h[kPHeadGroup] > h[kPHeads] || (h[kPRows] != kPfRows && h[kPRows] != 2 * kPfRows))
+      h[kPHeadGroup] > h[kPHeads] || (h[kPRows] != kPfRows && h[kPRows] != 2 * kPfRows) ||
+      (h[kPSolo] != 0 && h[kPSolo] != 1))
     return false;
   if (static_cast<long long>(h[kPItems]) * h[kPHeads] > kPfMaxBlocks) return false;
   const long long words = kPfHeaderWords + static_cast<long long>(kPfItemWords) * h[kPItems] +
@@ -324,6 +325,7 @@ int mla_prefill_run(const int32_t* plan_host, const int32_t* plan_dev, const voi
   p.head_group = plan_host[kPHeadGroup];
   p.partials = plan_host[kPPartials];
   p.rows = plan_host[kPRows];
+  p.solo = plan_host[kPSolo] != 0;
   const int key_box = p.rows > kPfRows ? kPfKeys / 2 : kPfKeys;
   p.q_tokens = plan_host[kPQTokens];
   p.kv_tokens = plan_host[kPKvTokens];

@@ -549,6 +549,28 @@ def test_prefill_keeps_what_is_masked_out(bad, causal, pairs):
         assert np.isnan(o[sees_k]).all() and np.isnan(l[sees_k]).all()
 
 
+@pytest.mark.parametrize("ql,kl,H,causal", [
+    ([64] * 4, [4000, 3000, 3500, 4096], 48, True),              # several items a block, of many key tiles
+    ([128, 1, 17, 100] * 9, [700, 1290, 5, 2000] * 9, 12, True),
+    ([128] * 5 + [3] * 60, [128] * 5 + [400] * 60, 8, False),
+    ([100] * 3, [0, 30, 3100], 70, True),
+])
+def test_prefill_of_one_row_tile(ql, kl, H, causal):
+    # at most 128 rows a request
+    torch, B = _t()
+    qp, kp = _indptr(ql), _indptr(kl)
+    (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(41 + H, int(qp[-1]), int(kp[-1]), H)
+    ref, ref_lse, mag = P.prefill_attention(xq, xk, xr, xv, qp, kp, SM, causal)
+    plan = B.Prefiller(qp, kp, H, causal)
+    out, lse = _attend(plan, q, k, kr, v)
+    _check_attention(out, lse, ref, ref_lse, mag)
+    outs = [torch.empty_like(out) for _ in range(6)]
+    for o in outs:
+        plan.run(q, k, kr, v, SM, o)
+    assert plan.check() == 0
+    assert all(torch.equal(o, out) for o in outs)
+
+
 @pytest.mark.parametrize("pairs", [False, True])
 def test_prefill_keeps_its_notes_until_they_are_read(pairs):
     # values that are not finite in partly seen tiles, of items with two row tiles, and behind each of those items
