@@ -88,7 +88,7 @@ enum Bar : int {
   bSFull = bVFree + kDepth,           // [2] per row tile
   bSOdd = bSFull + 2,            // odd key tiles of an item, in a launch of items with one row tile
   bPFull = bSOdd + 1,            // [2] per row tile; with one, of even and odd key tiles
-  bPvDone = bPFull + 2,          // [2]
+  bPvDone = bPFull + 2,          // [2] the same
   bVMasked = bPvDone + 2,         // [8] the values of masked tile M (on M & 7) have landed
   bVClean = bVMasked + kMasked,  // [8] and the guard has been over them
   bSched = bVClean + kMasked,    // [4] an item has been announced
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           mma_ts<kDescHigh, kPair>(d, a + 8 * k, (k < 4 ? b0 : b1) + 128 * (k & 3), kIdescO, !first || k > 0);
-        commit<kPair>(bar(bPvDone + w));
+        commit<kPair>(bar(bPvDone + w + odd));
       }
     };
     int tbase = 0, ubase = 0, mbase = 0;
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok &= t < sh.whole ? uwait(bVFull + U % kDepth, (U / kDepth) & 1)
                            : uwait(bVClean + M % kMasked, (M / kMasked) & 1);
-        // (the softmax may be a tile ahead here: even and odd tiles' weights have a barrier each)
+        // (the softmax may be a tile ahead here: even and odd tiles have barriers of their own)
         ok &= uwait(bPFull + (t & 1), (steps >> (t & 1)) & 1);
         steps ^= 1u << (t & 1);
         tc_fence_after();
@@ -889,7 +889,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     uint32_t step = 0;                                        // key tiles of this row tile, over all items
-    uint32_t scores = 0;                                      // kSolo: parities of the two score barriers
+    uint32_t scores = 0;                                      // kSolo: parities of even and odd key tiles' barriers
+    // until the last product issued, that of key tile t of the item, is done
+    auto wait_product = [&](int t) -> bool {
+      if constexpr (kSolo) return warp_wait(bar(bPvDone + (t & 1)), (~scores >> (t & 1)) & 1, wc);
+      return warp_wait(bar(bPvDone + w), (step - 1) & 1, wc);
+    };
     int mbase = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
@@ -962,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (move) ref = top;
             } else {
               // the product before this one has finished: O is these warps' to rescale
-              ok = warp_wait(bar(bPvDone + w), (step - 1) & 1, wc);
+              ok = wait_product(t - 1);
               tc_fence_after();
               const float f = move ? (ref == -INFINITY ? 0.f : ex2_approx(ref - top)) : 1.f;
               if (move) ref = top;
@@ -1001,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
       }
       if (ok && nw > 0) {
-        ok = warp_wait(bar(bPvDone + w), (step - 1) & 1, wc);
+        ok = wait_product(nw - 1);
         tc_fence_after();
       }
       Item it;
