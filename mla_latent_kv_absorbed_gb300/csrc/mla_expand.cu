@@ -23,7 +23,11 @@
 // (cta_group::2): each holds its 128 rows and half of the weights' columns,
 // CTA 0 issues for both.  That halves the weights that every SM reads from L2,
 // which bounded the single-CTA form (1.07 GB in 134 us at 4096 rows x 128
-// heads).
+// heads).  Bound: the weights from L2 still: with them there a tile of 256 x 256
+// takes 4200 cycles (32 MMAs of 128), but late, 5500-6100 through most of the
+// kernel, as beside the rows there is room for five stages of 16 KB.  4096 rows x
+// 128 heads take 103 us (1340 TFLOP/s, 0.70 of cuBLAS's rate), 8191 rows x 32
+// heads from E4M3 49 us, 257 rows x 16 heads 6.3 us.
 #include <type_traits>
 
 #include "mla_device.cuh"
@@ -507,12 +511,15 @@ int launch(const ExpandParams& p, const CUtensorMap (&tm)[4], int grid, cudaStre
 
 }  // namespace ex
 
-// 256 rows x 256 columns on CTA pairs, or 128 x 128 on single CTAs where the
-// former would leave SMs idle or a pair's second half without rows.
+// 256 rows x 256 columns on CTA pairs, or 128 x 128 on single CTAs where there
+// are few tiles: the end of the schedule is finer then, and a pair's second half
+// may have no rows.  us on pairs and single CTAs: 256 rows x 64 heads 10.1 and
+// 8.7, 600 x 64 18.6 and 16.1, 1024 x 64 22.0 and 22.3, 1536 x 64 27.2 and 29.6,
+// 1024 x 128 33.2 and 40.5; E4M3 rows 0.5 to 1 us in the pairs' favour beside that.
 ExpandTiling expand_tiling(int tokens, int heads, int sms) {
   const long long blocks = (tokens + ex::BM - 1) / ex::BM;
   const long long groups = 2ll * ((heads + 1) / 2);
-  if (blocks < 2 || blocks * groups < sms) return {128, false};
+  if (blocks * groups < 4ll * sms) return {128, false};
   return {256, true};
 }
 

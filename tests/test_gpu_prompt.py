@@ -231,7 +231,7 @@ def _expand_bound(ref, lat, w, eq, scale=1.0):
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("T,H", [(1, 1), (1, 16), (2, 5), (127, 16), (128, 1), (129, 3), (300, 16), (64, 33), (515, 2),
-                                 (100, 160), (1290, 33), (2560, 17)])
+                                 (100, 160), (1290, 33), (2560, 17), (4700, 17), (1290, 61)])
 def test_expand(fp8, T, H):
     torch, B = _t()
     N, scale = T + 77, 2.0 ** -5
