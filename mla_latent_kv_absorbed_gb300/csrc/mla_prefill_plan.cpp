@@ -39,6 +39,7 @@ struct Piece {
 constexpr long long kPieceCost = 8;
 constexpr long long kJoinCost = 24;
 constexpr long long kL2Bytes = 64ll << 20;
+constexpr int kMostTiles = 1 << 17;   // of an item: a quarter of a second, well under the limit of a wait for its last
 constexpr int kMostSms = 4096;        // planned for: more than any device has
 
 inline int key_tiles(int nk) { return (nk + kPfKeys - 1) / kPfKeys; }
@@ -53,11 +54,11 @@ inline long long tile_cost(int nq, int rows) {
 // them: 7300 cycles, a pair's 10000.
 inline long long item_cost(int rows) { return rows == kPfRows ? 40 : 54; }
 
-// Parts of a tile whose keys are cut into pieces of at most `cap` (0: not cut), none under four key tiles.
+// Parts of a tile whose keys are cut into pieces of at most `cap` (0: as few as can be), none under four key tiles.
 int parts_of(const Tile& t, int rows, long long cap) {
   const int nt = key_tiles(t.nk);
-  if (cap <= 0 || nt <= 1) return 1;
-  const long long most = std::max<long long>(4, cap / tile_cost(t.nq, rows));
+  if (nt <= 1) return 1;
+  const long long most = cap <= 0 ? kMostTiles : std::min<long long>(kMostTiles, std::max<long long>(4, cap / tile_cost(t.nq, rows)));
   return static_cast<int>((nt + most - 1) / most);
 }
 
@@ -191,7 +192,7 @@ int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int c
   const long long n_words = kPfHeaderWords + static_cast<long long>(kPfItemWords) * best.size() +
                             static_cast<long long>(kPfMergeWords) * merges;
   const long long blocks = static_cast<long long>(best.size()) * H;
-  if (n_words > 0x7FFFFFFFll || blocks > kPfMaxBlocks) return MLA_ERR_UNSUPPORTED;
+  if (n_words > 0x7FFFFFFFll || blocks > kPfMaxBlocks || merges > 65535) return MLA_ERR_UNSUPPORTED;
   const int group = group_of(H, kp[B], best.size(), workers);
   words.assign(static_cast<size_t>(n_words), 0);
   words[kPMagic] = kPfMagic;

@@ -150,6 +150,22 @@ def test_prefill_plan_covers_every_row_and_key_once(B, sms, causal):
         assert np.array_equal(plan, again)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_plan_bounds_the_keys_of_an_item(B, causal):
+    # 1000 rows over 2^28 keys on one SM: nothing to gain from a cut, but no item may keep its warps waiting long
+    plan, ws = B.prefill_plan([0, 1000], [0, 1 << 28], 1, causal, num_sms=1)
+    n = int(plan[7])
+    items = plan[16:16 + 8 * n].reshape(-1, 8)
+    assert (items[:, 4] <= 1 << 24).all() and (items[:, 6] >= 0).all()
+    for q0 in sorted(set(items[:, 1].tolist())):
+        mine = items[items[:, 1] == q0]
+        mine = mine[np.argsort(mine[:, 3])]
+        assert mine[0, 3] == 0 and (mine[1:, 3] == mine[:-1, 3] + mine[:-1, 4]).all()
+        last = (1 << 28) if not causal else min(1 << 28, q0 + int(mine[0, 2]) + (1 << 28) - 1000)
+        assert mine[-1, 3] + mine[-1, 4] == last
+    assert ws == 256 + int(plan[8]) * int(plan[13]) * 129 * 4
+
+
 def test_prefill_plan_cuts_long_keys_of_few_rows_only(B):
     few, _ = B.prefill_plan([0, 64], [0, 65536], 16, True, num_sms=152)
     assert few[8] > 1 and few[9] == 1
