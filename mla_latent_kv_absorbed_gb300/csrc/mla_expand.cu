@@ -13,10 +13,10 @@
 // heads; w_kc is K-major as it lies, w_vc N-major.
 //   warp 0      TMA producer of the weights, 64-deep chunks in a ring
 //   warp 1      TMEM allocator, MMA issuer: two accumulators in turn
-//   warps 4-11  epilogue: a TMEM lane is a row; 32 rows x 32 columns at a time
-//               through shared memory, stored by TMA; two warps share a lane
-//               quadrant and take half of the columns each (four warps needed
-//               6500 cycles a tile, the products 4100)
+//   warps 4-11  epilogue: a TMEM lane is a row; 32 columns at a time, exchanged
+//               between four lanes and stored in rows of 64 bytes; two warps
+//               share a lane quadrant and take half of the columns each (four
+//               warps needed 6500 cycles a tile, the products 4100)
 //   warps 12-15 rows: gather, swizzle (128-byte atoms), rope keys
 //   warp 2      (CTA 1 of a pair) tells CTA 0 of landed rows
 // kPair: two CTAs of a cluster work on one tile of 256 rows x 256 columns
@@ -25,9 +25,10 @@
 // which bounded the single-CTA form (1.07 GB in 134 us at 4096 rows x 128
 // heads).  Bound: the weights from L2 still: with them there a tile of 256 x 256
 // takes 4200 cycles (32 MMAs of 128), but late, 5500-6100 through most of the
-// kernel, as beside the rows there is room for five stages of 16 KB.  4096 rows x
-// 128 heads take 103 us (1340 TFLOP/s, 0.70 of cuBLAS's rate), 8191 rows x 32
-// heads from E4M3 49 us, 257 rows x 16 heads 6.3 us.
+// kernel, as beside the rows there is room for six stages of 16 KB (four: 112 us,
+// five: 103, and the output stored through shared memory in the sixth's place).
+// 4096 rows x 128 heads take 98 us (1404 TFLOP/s, 0.74 of cuBLAS's rate), 8191
+// rows x 32 heads from E4M3 49 us, 257 rows x 16 heads 6.1 us.
 #include <type_traits>
 
 #include "mla_device.cuh"
@@ -40,7 +41,6 @@ namespace ex {
 constexpr int kThreads = 512;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kRowWarp0 = 12;
 constexpr int BM = 128, BK = 64, kChunks = kLatent / BK;
-constexpr int kSlab = 32 * 64;
 
 template <int NT_, bool kPair>
 struct Cfg {
@@ -50,10 +50,9 @@ struct Cfg {
   static constexpr int kABytes = kChunks * BM * 128;        // 128 KB
   static constexpr int kCols = NT / kCtas;                  // of a tile's columns, those this CTA loads
   static constexpr int kBBytes = kCols * BK * 2;
-  static constexpr int kStages = (80 * 1024) / kBBytes;
+  static constexpr int kStages = (96 * 1024) / kBBytes;
   static constexpr int kOffB = kABytes;
-  static constexpr int kOffOut = kOffB + kStages * kBBytes; // per epilogue warp a slab of 32 rows x 32 columns
-  static constexpr int kOffBar = kOffOut + kEpiWarps * kSlab;
+  static constexpr int kOffBar = kOffB + kStages * kBBytes;
   // full[S], empty[S], a_full[8], a_free[8], acc_full[2], acc_empty[2]
   static constexpr int kBars = 2 * kStages + 2 * kChunks + 4;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
@@ -120,12 +119,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, 
       : "memory");
 }
 
-__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int x, int y, int z, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(map),
-      "r"(src), "r"(x), "r"(y), "r"(z), "l"(policy)
-      : "memory");
-}
 // 16 bytes, or 16 zero bytes with nothing read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -150,7 +143,6 @@ __device__ __forceinline__ void mbar_arrive_leader_relaxed(uint32_t bar) {
 template <bool kFp8, int NT, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_ko, const __grid_constant__ CUtensorMap tm_vo,
                   const ExpandParams p) {
   using C = Cfg<NT, kPair>;
   extern __shared__ uint8_t smem_raw[];
@@ -424,9 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------- epilogue
     const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const float scale = kFp8 ? p.kv_scale : 1.f;
-    // the output streams through L2; the weights, read by every block of rows, should stay
-    const uint64_t policy = l2_policy_evict_first();
-    uint8_t* slab = smem + C::kOffOut + (warp - kEpiWarp0) * kSlab;
+    // the output streams through L2 (__stcs); the weights, read by every block of rows, should stay
+    const int mate = lane & 3;
     uint32_t i = 0;
     for (int t = t0; t < t1; ++t, ++i) {
       const int col = t % cols, h = (col % groups) * C::kHeads;
@@ -437,34 +428,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int end = min((half + 1) * (NT / 2), (p.heads - h) * kNope);   // an odd last head: half a tile
 #pragma unroll 1
       for (int c = half * (NT / 2); c < end; c += 32) {
-        uint32_t a[16], b[16];
+        uint32_t a[16], b[16], w[16];
         const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * NT + c;
         tmem_ld16(src, a);
         tmem_ld16(src + 16, b);
         tmem_wait_ld();
-        if (lane == 0) bulk_wait_read();                     // the store before has read the slab
-        __syncwarp();
-        // rows of 64 bytes, their 16-byte pieces in the order of the 64-byte swizzle
-        auto put = [&](const uint32_t (&x)[16], int e) {
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint32_t w[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-              w[z] = pack_bf16x2(__uint_as_float(x[8 * y + 2 * z]) * scale, __uint_as_float(x[8 * y + 2 * z + 1]) * scale);
-            *reinterpret_cast<uint4*>(slab + lane * 64 + (((e + y) ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        };
-        put(a, 0);
-        put(b, 2);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (r0 < p.tokens)                                 // rows past the last are not written
-            tma_store_3d(col < groups ? &tm_ko : &tm_vo, smem_u32(slab), c & 127, h + (c >> 7), r0, policy);
-          bulk_commit();
+        for (int e = 0; e < 8; ++e) {
+          w[e] = pack_bf16x2(__uint_as_float(a[2 * e]) * scale, __uint_as_float(a[2 * e + 1]) * scale);
+          w[8 + e] = pack_bf16x2(__uint_as_float(b[2 * e]) * scale, __uint_as_float(b[2 * e + 1]) * scale);
         }
+        // four lanes exchange blocks of 16 bytes, so that a store writes 64 bytes of a row
+        transpose4_blocks<4>(w, lane);
+        uint16_t* dst = (col < groups ? p.k_nope : p.v) +
+                        (static_cast<size_t>(r0 + lane - mate) * p.heads + h + (c >> 7)) * kNope + (c & 127) + 8 * mate;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (r0 + lane - mate + x < p.tokens)
+            __stcs(reinterpret_cast<uint4*>(dst + static_cast<size_t>(x) * p.heads * kNope),
+                   make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]));
       }
       tc_fence_before();
       __syncwarp();
@@ -473,7 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         else mbar_arrive(acc_empty(buf));
       }
     }
-    if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncwarp();
@@ -487,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kFp8, int NT, bool kPair>
-int launch(const ExpandParams& p, const CUtensorMap (&tm)[4], int grid, cudaStream_t stream) {
+int launch(const ExpandParams& p, const CUtensorMap (&tm)[2], int grid, cudaStream_t stream) {
   using C = Cfg<NT, kPair>;
   const auto kernel = &expand_kernel<kFp8, NT, kPair>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes)) return MLA_ERR_CUDA;
@@ -505,7 +486,7 @@ int launch(const ExpandParams& p, const CUtensorMap (&tm)[4], int grid, cudaStre
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, tm[0], tm[1], tm[2], tm[3], p) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, tm[0], tm[1], p) != cudaSuccess) return MLA_ERR_CUDA;
   return cudaPeekAtLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -523,7 +504,7 @@ ExpandTiling expand_tiling(int tokens, int heads, int sms) {
   return {256, true};
 }
 
-int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[4], ExpandTiling tiling, int sms, bool fp8,
+int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[2], ExpandTiling tiling, int sms, bool fp8,
                   cudaStream_t stream) {
   const int per = tiling.cols / kNope, rows = tiling.pair ? 2 * ex::BM : ex::BM;
   const long long tiles = (p.tokens + static_cast<long long>(rows) - 1) / rows * 2 * ((p.heads + per - 1) / per);

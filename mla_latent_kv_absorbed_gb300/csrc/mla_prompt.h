@@ -52,6 +52,7 @@ struct RopeAppendParams {
 struct ExpandParams {
   const uint8_t* kv_cache;    // [num_slots, 576] bf16 or E4M3
   const int32_t* kv_indices;  // [tokens]
+  uint16_t *k_nope, *v;       // [tokens, heads, 128]
   uint16_t* k_rope;           // [tokens, 64]
   int* status;                // status word, or null
   long long num_slots;
@@ -115,13 +116,13 @@ int launch_rope_query(const RopeQueryParams& p, const RopeFreqs& f, cudaStream_t
 int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, cudaStream_t stream);
 // How the expansion is tiled: columns of a tile, and whether CTA pairs share
 // one.  Maps: w_kc as [heads * 128, 512] (box: 128 rows x 64), w_vc as [heads *
-// 512, 128] (box 64 x 64), k_nope and v as [tokens, heads, 128] (box 32 rows x 32).
+// 512, 128] (box 64 x 64).
 struct ExpandTiling {
   int cols;
   bool pair;
 };
 ExpandTiling expand_tiling(int tokens, int heads, int sms);
-int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[4], ExpandTiling tiling, int sms, bool fp8,
+int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[2], ExpandTiling tiling, int sms, bool fp8,
                   cudaStream_t stream);
 // tm_q over q as [rows, heads, 192] (box 128 rows x 64), tm_k and tm_v over
 // [keys, heads, 128] (boxes of 128 - for CTA pairs 64 - and 64 keys x 64), tm_kr

@@ -40,11 +40,10 @@ EncodeTiledFn encode_fn() {
 }
 
 // bf16 [rows, heads, width] with strides in elements (heads 0: [rows, width]),
-// boxes of `box_rows` (<= 256) rows of one head x `box_cols` values, swizzled over
-// their whole width (64: 128 bytes, 32: 64); reads
-// past the last row give zeros.  The stride of a dimension of one is not used.
+// boxes of `box_rows` (<= 256) rows of one head x 64 values in the 128-byte
+// swizzle; reads past the last row give zeros.  The stride of a dimension of one is not used.
 bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride,
-              int width, int box_rows, int box_cols = 64) {
+              int width, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t rs = static_cast<cuuint64_t>(rows > 1 ? row_stride : width) * 2;
@@ -52,14 +51,14 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t row_stride
   const int rank = heads > 0 ? 3 : 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[2] = {hs, rs};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), 1, static_cast<cuuint32_t>(box_rows)}, step[3] = {1, 1, 1};
+  cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)}, step[3] = {1, 1, 1};
   if (rank == 2) {
     dims[1] = dims[2];
     strides[0] = rs;
     box[1] = box[2];
   }
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -202,6 +201,8 @@ int expand(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, i
   ExpandParams p{};
   p.kv_cache = static_cast<const uint8_t*>(kv_cache);
   p.kv_indices = kv_indices;
+  p.k_nope = static_cast<uint16_t*>(k_nope);
+  p.v = static_cast<uint16_t*>(v);
   p.k_rope = static_cast<uint16_t*>(k_rope);
   p.status = static_cast<int*>(workspace);
   p.num_slots = num_slots;
@@ -211,11 +212,9 @@ int expand(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, i
   const int sms = device_sm_count();
   if (sms < 1) return MLA_ERR_CUDA;
   const int64_t H = num_heads;
-  CUtensorMap tm[4];
+  CUtensorMap tm[2];
   if (!make_map(&tm[0], w_kc, H * kNope, kLatent, 0, 0, kLatent, 128) ||
-      !make_map(&tm[1], w_vc, H * kLatent, kNope, 0, 0, kNope, 64) ||
-      !make_map(&tm[2], k_nope, tokens, H * kNope, H, kNope, kNope, 32, 32) ||
-      !make_map(&tm[3], v, tokens, H * kNope, H, kNope, kNope, 32, 32))
+      !make_map(&tm[1], w_vc, H * kLatent, kNope, 0, 0, kNope, 64))
     return MLA_ERR_CUDA;
   return launch_expand(p, tm, expand_tiling(tokens, num_heads, sms), sms, fp8, reinterpret_cast<cudaStream_t>(stream));
 }
