@@ -414,17 +414,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const int total = p.n_items * p.heads;
       bool ok = true;
-      // block `w` of the launch: items are numbered group of heads by group, heaviest first within it, heads innermost
+      // block `w` of the launch: items are numbered group of heads by group, heaviest first within it, heads
+      // innermost; behind them the tail's items for all heads at once
+      const int body = p.n_items - p.n_tail;
       auto fetch = [&](int w, Item& it) {
-        const int per_group = p.n_items * p.head_group;
-        const int g = w / per_group, rest = w - g * per_group;
-        const int in_group = min(p.head_group, p.heads - g * p.head_group);
-        const int item = rest / in_group;
+        const bool tail = w >= body * p.heads;
+        const int per_group = body * p.head_group;
+        const int g = tail ? 0 : w / per_group, rest = w - (tail ? body * p.heads : g * per_group);
+        const int in_group = tail ? p.heads : min(p.head_group, p.heads - g * p.head_group);
+        const int item = (tail ? body : 0) + rest / in_group;
         if (!load_item<kPair, kSolo>(p, item, it)) {
           record_status(p.status, MLA_ERR_PLAN_MISMATCH);
           it.nk = it.nq = 0;
         }
-        it.h = g * p.head_group + rest - item * in_group;
+        it.h = g * p.head_group + rest % in_group;
       };
       auto announce = [&](uint32_t k, const Item& it, bool there) {
         const int s = k % kSched;

@@ -7,7 +7,10 @@
 //     their last row, so no tile without a visible key is visited;
 //   * items are launched heaviest first (blocks start in launch order as SMs
 //     fall free, so the short ones fill the end), for a group of heads at a
-//     time: the group's keys and values stay in L2 while all its rows pass;
+//     time: the group's keys and values stay in L2 while all its rows pass.
+//     The shortest items of all groups are kept for the very end, where that
+//     evens out the SMs (12 ragged requests x 32 heads: SMs ended between 105
+//     and 135 us without);
 //   * where whole items would leave SMs idle (few rows over long keys), an
 //     item's keys are cut into pieces of whole tiles whose partial outputs a
 //     second kernel joins.  Tried are the cuts that fill the SMs once, twice,
@@ -94,20 +97,42 @@ int group_of(int heads, long long kv_tokens, size_t pieces, int sms) {
   return static_cast<int>((heads + groups - 1) / groups);
 }
 
-// End of the greedy schedule of the pieces in launch order on `sms`.
-long long makespan(const std::vector<Piece>& pieces, int heads, int group, int sms) {
+// End of the greedy schedule of the pieces in launch order on `sms`, the last `tail` of them behind all heads' others.
+long long makespan(const std::vector<Piece>& pieces, int heads, int group, int sms, size_t tail = 0) {
   std::priority_queue<long long, std::vector<long long>, std::greater<long long>> free_at;
   for (int i = 0; i < sms; ++i) free_at.push(0);
   long long end = 0;
+  auto take = [&](long long cost) {
+    const long long t = free_at.top() + cost;
+    free_at.pop();
+    free_at.push(t);
+    end = std::max(end, t);
+  };
   for (int h0 = 0; h0 < heads; h0 += group)
-    for (const Piece& p : pieces)
-      for (int h = h0; h < std::min(heads, h0 + group); ++h) {
-        const long long t = free_at.top() + p.cost;
-        free_at.pop();
-        free_at.push(t);
-        end = std::max(end, t);
-      }
+    for (size_t i = 0; i + tail < pieces.size(); ++i)
+      for (int h = h0; h < std::min(heads, h0 + group); ++h) take(pieces[i].cost);
+  for (size_t i = pieces.size() - tail; i < pieces.size(); ++i)
+    for (int h = 0; h < heads; ++h) take(pieces[i].cost);
   return end;
+}
+
+// How many of the pieces to keep for the end: up to a quarter of the work (they find less of their keys in L2).
+size_t tail_of(const std::vector<Piece>& pieces, int heads, int group, int sms) {
+  if (group >= heads || pieces.size() < 2 || static_cast<long long>(pieces.size()) * heads > (1 << 16)) return 0;
+  long long total = 0;
+  for (const Piece& p : pieces) total += p.cost;
+  long long end = makespan(pieces, heads, group, sms), sum = 0;
+  size_t best = 0, n = 0;
+  for (int part = 1; part <= 4; ++part) {               // a sixteenth of the work, an eighth, ...
+    while (n + 1 < pieces.size() && 16 * (sum + pieces[pieces.size() - 1 - n].cost) <= total * part)
+      sum += pieces[pieces.size() - 1 - n++].cost;
+    const long long e = makespan(pieces, heads, group, sms, n);
+    if (e < end) {
+      end = e;
+      best = n;
+    }
+  }
+  return best;
 }
 
 // The tiles of `rows` query rows and their pieces in launch order; returns the
@@ -208,6 +233,7 @@ int build_prefill_plan(const int32_t* qp, const int32_t* kp, int B, int H, int c
   words[kPHeadGroup] = group;
   words[kPTotalWords] = static_cast<int32_t>(n_words);
   words[kPNumSms] = num_sms;
+  words[kPTail] = static_cast<int32_t>(tail_of(best, H, group, workers));
   words[kPRows] = rows;
   words[kPSolo] = std::all_of(tiles.begin(), tiles.end(), [](const Tile& t) { return t.nq <= kPfRows / 2; }) ? 1 : 0;
   int32_t* w = words.data() + kPfHeaderWords;

@@ -68,7 +68,8 @@ enum PfHeader : int {
   kPMagic = 0, kPVersion, kPBatch, kPHeads, kPCausal, kPQTokens, kPKvTokens, kPItems, kPPartials, kPMerges,
   kPHeadGroup /* heads whose items are launched together */, kPTotalWords, kPNumSms,
   kPRows /* query rows of an item, at most: 256, or 512 for CTA pairs */,
-  kPSolo /* no item has more than 128 */
+  kPSolo /* no item has more than 128 */,
+  kPTail /* of the items, the last so many wait until all heads' others have been handed out */
 };
 constexpr int kPfItemWords = 8;       // request, q0, nq, k0, nk, off, partial (or -1), 0
 constexpr int kPfMergeWords = 4;      // q0, nq, first partial, last partial + 1
@@ -105,7 +106,7 @@ struct PrefillParams {
   float* part_o;
   float* part_lse;
   int* status;
-  int n_items, n_merges, heads, head_group, partials, rows;
+  int n_items, n_tail, n_merges, heads, head_group, partials, rows;
   bool solo;                  // no item has more than 128 rows
   int q_tokens, kv_tokens;
   float scale_log2;           // |sm_scale| * log2(e), > 0

@@ -270,7 +270,7 @@ bool prefill_header_ok(const int32_t* h) {
   if (h[kPBatch] < 0 || h[kPHeads] < 1 || h[kPHeads] > 65535 || h[kPQTokens] < 0 || h[kPKvTokens] < 0 ||
       h[kPItems] < 0 || h[kPPartials] < 0 || h[kPMerges] < 0 || h[kPMerges] > 65535 || h[kPHeadGroup] < 1 ||
       h[kPHeadGroup] > h[kPHeads] || (h[kPRows] != kPfRows && h[kPRows] != 2 * kPfRows) ||
-      (h[kPSolo] != 0 && h[kPSolo] != 1))
+      (h[kPSolo] != 0 && h[kPSolo] != 1) || h[kPTail] < 0 || h[kPTail] > h[kPItems])
     return false;
   if (static_cast<long long>(h[kPItems]) * h[kPHeads] > kPfMaxBlocks) return false;
   const long long words = kPfHeaderWords + static_cast<long long>(kPfItemWords) * h[kPItems] +
@@ -319,6 +319,7 @@ int mla_prefill_run(const int32_t* plan_host, const int32_t* plan_dev, const voi
   p.part_lse = reinterpret_cast<float*>(ws + pf_part_lse_off(plan_host));
   p.status = reinterpret_cast<int*>(ws);
   p.n_items = plan_host[kPItems];
+  p.n_tail = plan_host[kPTail];
   p.n_merges = plan_host[kPMerges];
   p.heads = H;
   p.head_group = plan_host[kPHeadGroup];

@@ -402,6 +402,21 @@ def test_prefill_of_more_items_than_sms(ql, kl, H, causal):
     assert all(torch.equal(o, out) for o in outs)
 
 
+@pytest.mark.parametrize("group,tail", [(64, 0), (7, 0), (1, 3), (7, 5), (64, 2), (20, -1)])
+def test_prefill_in_any_order_of_items(group, tail):
+    # groups of heads (the last one smaller) and items kept for the end change the order alone
+    torch, B = _t()
+    qp = _indptr([1, 7, 33, 100, 140, 260, 300, 0, 129, 600])
+    H = 64
+    (q, _), (k, _), (kr, _), (v, _) = _attention_inputs(77, int(qp[-1]), int(qp[-1]), H)
+    plan = B.Prefiller(qp, qp, H)
+    want, want_lse = _attend(plan, q, k, kr, v)
+    plan.plan_host[10], plan.plan_host[15] = group, int(plan.plan_host[7]) if tail < 0 else tail
+    plan.plan_dev = torch.from_numpy(plan.plan_host).cuda()
+    out, lse = _attend(plan, q, k, kr, v)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 def _on_pairs(plan, qp, kp, H, causal):
     """The same batch in items of 512 rows, which pairs of CTAs work on (a plan takes them where it expects that
     schedule to end first)."""
@@ -415,7 +430,7 @@ def _on_pairs(plan, qp, kp, H, causal):
     items.sort(key=lambda i: -i[4])
     words = plan.plan_host[:16].tolist()
     words[7:12] = [len(items), 0, 0, H, 16 + 8 * len(items)]
-    words[13] = 512
+    words[13], words[15] = 512, 0
     plan.plan_host = np.array(words + sum(items, []), dtype=np.int32)
     plan.plan_dev = torch.from_numpy(plan.plan_host).cuda()
     return plan

@@ -166,6 +166,19 @@ def test_prefill_plan_bounds_the_keys_of_an_item(B, causal):
     assert ws == 256 + int(plan[8]) * int(plan[13]) * 129 * 4
 
 
+def test_prefill_plan_keeps_short_items_for_the_end(B):
+    # many heads whose keys do not fit L2 together, rows of very different lengths
+    ql = [1500, 1, 640, 2047, 333, 16, 1024, 129, 800, 257, 64]
+    qp = np.cumsum([0] + ql)
+    plan, _ = B.prefill_plan(qp, qp, 64, True, num_sms=152)
+    n, tail = int(plan[7]), int(plan[15])
+    assert plan[10] < 64 and 0 < tail < n
+    cost = plan[16:16 + 8 * n].reshape(-1, 8)[:, 4]
+    assert cost[n - tail:].sum() * 3 <= cost.sum()
+    one, _ = B.prefill_plan(qp, qp, 1, True, num_sms=152)
+    assert one[15] == 0
+
+
 def test_prefill_plan_cuts_long_keys_of_few_rows_only(B):
     few, _ = B.prefill_plan([0, 64], [0, 65536], 16, True, num_sms=152)
     assert few[8] > 1 and few[9] == 1
@@ -211,6 +224,10 @@ def test_prefill_run_refuses_bad_arguments(B):
     for i in (0, 1, 11):                                   # magic, version, word count
         bad = plan.copy()
         bad[i] += 1
+        assert f(ph=bad) == 1
+    for i, x in ((13, 300), (14, 2), (15, -1), (15, int(plan[7]) + 1)):   # rows of an item, one row tile, items kept for the end
+        bad = plan.copy()
+        bad[i] = x
         assert f(ph=bad) == 1
     assert f(wsb=need - 1) == 3 and f(ws=None) == 1 and f(ws=fake + 8) == 1
     assert f(scale=float("inf")) == 1
