@@ -41,7 +41,8 @@
 //           ring (2.2 key tiles).  Bound by HBM: 64 rows over 65536 and 32064
 //           keys x 16 heads take 143 us (5.7 TB/s); with the general form,
 //           whose step of one row tile is the chain of 3080 cycles, 159; with
-//           two score buffers and the general form's ring 178.
+//           two score buffers and the general form's ring 178.  (140 since the
+//           joining kernel takes the pieces' rows four at a time.)
 //
 // Warps: 0-7 softmax and epilogue of tile A, 8-15 of tile B, 16 TMA producer,
 // 17 MMA issuer, 18-19 the guard.  A tile that some row sees only in part is
@@ -1127,6 +1128,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of a cut tile: one warp a (row, head), 4 values a lane.
+// Bound: latency (10 MB of pieces where it was measured); with the pieces' weights
+// and rows one after the other the call took 3 us longer.
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -1140,26 +1143,37 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int r = i / p.heads, h = i - r * p.heads;
   if (r >= nq) return;
+  // A lane takes a piece's log-sum-exp (32 pieces at a time), then the pieces' rows come four at a time.
+  auto lse_of = [&](int k) -> float {
+    return k < p1 ? p.part_lse[(static_cast<size_t>(k) * p.heads + h) * p.rows + r] : -INFINITY;
+  };
   float m = -INFINITY;
   bool bad = false;
-  for (int k = p0; k < p1; ++k) {
-    const float s = p.part_lse[(static_cast<size_t>(k) * p.heads + h) * p.rows + r];
+  for (int k = p0; k < p1; k += 32) {
+    const float s = lse_of(k + lane);
     bad |= s != s;
     m = fmaxf(m, s);
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  bad = __any_sync(0xffffffffu, bad);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-  for (int k = p0; k < p1; ++k) {
-    const size_t row = (static_cast<size_t>(k) * p.heads + h) * p.rows + r;
-    const float s = p.part_lse[row];
-    if (s == -INFINITY) continue;                          // nothing seen in this piece
-    const float w = expf(s - m);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + row * kNope + 4 * lane);
-    l += w;
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
+  for (int k = p0; k < p1; k += 32) {
+    const float s = lse_of(k + lane);
+    const float e = s == -INFINITY ? 0.f : expf(s - m);    // 0: nothing seen in this piece
+    const int n = min(32, p1 - k);
+#pragma unroll 4
+    for (int x = 0; x < n; ++x) {
+      const float w = __shfl_sync(0xffffffffu, e, x);
+      const float4 v = *reinterpret_cast<const float4*>(
+          p.part_o + ((static_cast<size_t>(k + x) * p.heads + h) * p.rows + r) * kNope + 4 * lane);
+      l += w;
+      o.x = fmaf(w, v.x, o.x);
+      o.y = fmaf(w, v.y, o.y);
+      o.z = fmaf(w, v.z, o.z);
+      o.w = fmaf(w, v.w, o.w);
+    }
   }
   const bool any = l > 0.f || bad || l != l;
   const float inv = any ? 1.f / l : 0.f;
