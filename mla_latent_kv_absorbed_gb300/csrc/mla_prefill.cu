@@ -12,7 +12,7 @@
 // item's last product and epilogue.  Key tiles of 128:
 //   S = Q K^T       M = 128, N = 128, 12 steps of K = 16 (128 + 64 dims), both
 //                   operands from shared memory
-//   P = exp2(..)    in registers, two threads a row; written back as bf16 over
+//   P = exp2(..)    in registers, four threads a row; written back as bf16 over
 //                   the scores' own columns
 //   O += P V        A from TMEM, V as it lies in memory (N-major), 8 steps
 // Bound: the tensor core.  A key tile against both row tiles is 2 x 20 MMAs of
@@ -21,11 +21,18 @@
 // bits at any magnitude, sums are fp32), and O is rescaled in TMEM only then.
 //
 // A row tile's scores, weights and product follow one another (the weights lie
-// over the scores), so its key tile takes as long as that chain: 1260 cycles of
-// softmax, 250-600 until the issuer has seen it, 1280 of products, 500 until
-// the next scores are seen - 3630 for a step of both row tiles, of which 2580
-// are products.  Hence two threads a row: with one the softmax took 1500 and
-// the step 4000.  Three forms, chosen by the plan:
+// over the scores), so its key tile takes as long as that chain: 1300 cycles of
+// softmax (200 to load, 240 to vote on the reference, 800 for the weights: 20
+// exponentials a cycle, 150 to store), 250-600 until the issuer has seen it, 1280
+// of products, 500 until the next scores are seen - 3630 for a step of both row
+// tiles, of which 2580 are products.  All softmax warps take one row tile, then
+// the other: four threads a row, whose quarter of a tile's scores stays in
+// registers.  With half of the warps on each (two threads a row, half a tile)
+// the long prompts took as long, but registers spilled and items' ends, which
+// fall on one row tile at a time, were slower: 140 us instead of 137 for the chunk
+// below, 8.5 instead of 8.0 for four requests of 1 to 100 rows; with one thread a
+// row the step took 4000.
+// Three forms, chosen by the plan:
 //   kPair   two CTAs of a cluster and 512 rows (cta_group::2: products of 256
 //           rows, CTA 0 issues).  Each CTA holds half of the keys and values,
 //           a step takes 3250 cycles for twice the rows, and the ring holds
@@ -41,11 +48,11 @@
 //           ring (2.2 key tiles).  Bound by HBM: 64 rows over 65536 and 32064
 //           keys x 16 heads take 143 us (5.7 TB/s); with the general form,
 //           whose step of one row tile is the chain of 3080 cycles, 159; with
-//           two score buffers and the general form's ring 178.  (140 since the
-//           joining kernel takes the pieces' rows four at a time.)
+//           two score buffers and the general form's ring 178.  (137 by now, with
+//           the joining kernel's loads four at a time and four threads a row.)
 //
-// Warps: 0-7 softmax and epilogue of tile A, 8-15 of tile B, 16 TMA producer,
-// 17 MMA issuer, 18-19 the guard.  A tile that some row sees only in part is
+// Warps: 0-15 softmax and epilogue, 16 TMA producer, 17 MMA issuer, 18-19 the
+// guard.  A tile that some row sees only in part is
 // masked by index in the softmax, but a zero weight times a value that is not
 // finite is NaN in the matrix product: the guard clears those values (and the
 // rows behind the last key) in shared memory before the product reads them,
@@ -77,8 +84,7 @@ constexpr int kOffBar = kOffRing + kRingBytes;
 constexpr int kDepth = 4;                             // tiles told apart: more than the ring holds
 constexpr int kSched = 4;                             // items announced ahead
 constexpr int kMasked = 8;                            // masked tiles told apart: two items' worth and more
-constexpr int kConsumers = 16 + 1 + 2;                // warps that read an announced item (in CTA 1: no issuer, but the
-                                                      // producer; 8 fewer where there is no second row tile)
+constexpr int kConsumers = 16 + 1 + 2;                // warps that read an announced item (in CTA 1: no issuer, but the producer)
 enum Bar : int {
   bQFull = 0,                    // [2] per row tile
   bQFree = bQFull + 2,           // [2] the row tile's last scores of the item are done
@@ -101,7 +107,7 @@ constexpr int kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16;   // TMEM address
 constexpr int kOffFound = kOffMisc + 8;               // nonzero once some mask in kOffBad was
 constexpr int kOffBad = kOffMisc + 16;                // [8][2][4] words: bit j = key j of masked tile M, by the CTA that saw it
 constexpr int kOffSched = kOffBad + 32 * kMasked;     // [4] announced items, 8 words each
-constexpr int kOffMeet = kOffSched + 32 * kSched;      // [8][32] floats: where a row's two threads meet
+constexpr int kOffMeet = kOffSched + 32 * kSched;      // [4][2][32] floats: where a row's four threads meet
 constexpr int kSmemBytes = kOffMeet + 1024 + 1024;
 static_assert(kOffSched % 16 == 0, "announced items are read as 16-byte words");
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -261,11 +267,11 @@ __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { retu
 
 __device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7F80u) == 0x7F80u; }
 
-// Multiplies 64 columns of the thread's TMEM lane by f.  Rare, and out of line:
+// Multiplies 32 columns of the thread's TMEM lane by f.  Rare, and out of line:
 // inlined, its registers push values of the loop over the keys into memory.
 __device__ __noinline__ void rescale_columns(uint32_t taddr, float f) {
 #pragma unroll 1
-  for (int c = 0; c < 64; c += 16) {
+  for (int c = 0; c < 32; c += 16) {
     uint32_t o[16];
     tmem_ld16(taddr + c, o);
     tmem_wait_ld();
@@ -276,35 +282,32 @@ __device__ __noinline__ void rescale_columns(uint32_t taddr, float f) {
   tmem_wait_st();
 }
 
-// 64 columns of the output from TMEM, times inv, as bf16 (a piece: fp32) to the
+// 32 columns of the output from TMEM, times inv, as bf16 (a piece: fp32) to the
 // thread's row.  Four lanes exchange blocks of 16 bytes, so that a store writes
 // 64 bytes of a row: `dst` is block lane & 3 of the first of their rows, `rows`
 // how many of the four there are.  Out of line for the same reason; with all its
-// registers free it takes 1700 cycles where 16 columns at a time in the caller
-// took 4500.
+// registers free it takes 1700 cycles for 64 columns where 16 at a time in the
+// caller took 4500.
 template <typename T>
 __device__ __noinline__ void store_columns(uint32_t taddr, float inv, T* dst, size_t stride, int rows) {
   constexpr bool kHalf = sizeof(T) == 2;
   constexpr int kCols = kHalf ? 32 : 16;
   const int lane = threadIdx.x & 31;
+  uint32_t o[32];
+  tmem_ld32(taddr, o);
+  tmem_wait_ld();
 #pragma unroll
-  for (int c = 0; c < 64; c += 32) {
-    uint32_t o[32];
-    tmem_ld32(taddr + c, o);
-    tmem_wait_ld();
+  for (int y = 0; y < 32; y += kCols) {
+    uint32_t b[16];
 #pragma unroll
-    for (int y = 0; y < 32; y += kCols) {
-      uint32_t b[16];
+    for (int e = 0; e < 16; ++e)
+      b[e] = kHalf ? pack_bf16x2(__uint_as_float(o[(2 * e) & 31]) * inv, __uint_as_float(o[(2 * e + 1) & 31]) * inv)
+                   : __float_as_uint(__uint_as_float(o[(y + e) & 31]) * inv);
+    transpose4_blocks<4>(b, lane);
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        b[e] = kHalf ? pack_bf16x2(__uint_as_float(o[(2 * e) & 31]) * inv, __uint_as_float(o[(2 * e + 1) & 31]) * inv)
-                     : __float_as_uint(__uint_as_float(o[(y + e) & 31]) * inv);
-      transpose4_blocks<4>(b, lane);
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (x < rows)
-          *reinterpret_cast<uint4*>(dst + x * stride + c + y) = make_uint4(b[4 * x], b[4 * x + 1], b[4 * x + 2], b[4 * x + 3]);
-    }
+    for (int x = 0; x < 4; ++x)
+      if (x < rows)
+        *reinterpret_cast<uint4*>(dst + x * stride + y) = make_uint4(b[4 * x], b[4 * x + 1], b[4 * x + 2], b[4 * x + 3]);
   }
 }
 
@@ -357,10 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const bool eight = i >= bPFull && i < bPFull + 2;
+      const bool softmax = i >= bPFull && i < bPFull + 2;
       const bool two = i >= bVClean && i < bVClean + kMasked;
       const bool all = i >= bSchedFree && i < bSchedFree + kSched;
-      mbar_init(bar(i), eight ? 8 * kCtas : two ? 2 * kCtas : all ? (kConsumers - (kSolo ? 8 : 0)) * kCtas : 1);
+      mbar_init(bar(i), softmax ? 16 * kCtas : two ? 2 * kCtas : all ? kConsumers * kCtas : 1);
     }
     *abort_flag = 0;
     *reinterpret_cast<int*>(smem + kOffFound) = 0;
@@ -859,248 +862,254 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tbase += sh.n;
     }
-  } else if (!kSolo || warp < 8) {
+  } else {
     // -------------------------------------------------- softmax and epilogue
-    // Two threads a row, in warps `warp` and `warp` ^ 4: each takes half of a
-    // tile's keys and half of the output's columns.  They meet at a named
-    // barrier of their 64 threads and agree on the reference maximum there.
-    const int w = warp >> 3, half = (warp >> 2) & 1;          // row tile, half
-    const int row0 = kTileRows<kPair> * w + 128 * static_cast<int>(rank);   // this CTA's first row of it
-    const int row = row0 + 32 * (warp & 3) + lane;            // row of the item
-    const int pair_bar = 1 + 4 * w + (warp & 3);
-    float* meet = reinterpret_cast<float*>(smem + kOffMeet) + 32 * (pair_bar - 1) + lane;
-    const uint32_t quad = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + kTmemS + 128 * w + 64 * half + quad;   // the half's scores
-    const uint32_t tp = tmem + kTmemS + 128 * w + 32 * half + quad;   // its weights
-    const uint32_t to = tmem + kTmemO + 128 * w + 64 * half + quad;   // the half of the output
-    // Combines a value of the row's two threads; both return the result.
-    auto both = [&](float mine, auto op) -> float {
-      if (half == 0) *meet = mine;
-      named_bar_sync(pair_bar, 64);
-      if (half == 1) {
-        mine = op(mine, *meet);
-        *meet = mine;
+    // All 16 warps work on one row tile, then on the other: four threads a row, in the warps of one TMEM lane
+    // quadrant, each with a quarter of a tile's keys and of the output's columns.  They meet at a named barrier of
+    // their 128 threads and agree on the reference maximum there.
+    const int quarter = warp >> 2, quad = warp & 3;
+    const int row_a = 128 * static_cast<int>(rank) + 32 * quad + lane;   // row of the item, in row tile A
+    const int quad_bar = 1 + quad;
+    float* meet = reinterpret_cast<float*>(smem + kOffMeet) + 64 * quad + lane;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+    const uint32_t ts = at + kTmemS + 32 * quarter, tp = at + kTmemS + 16 * quarter, to = at + kTmemO + 32 * quarter;
+    // Combines a value of the row's four threads, in a fixed order; all return the result.
+    auto all4 = [&](float mine, auto op) -> float {
+      if (quarter >= 2) meet[32 * (quarter - 2)] = mine;
+      named_bar_sync(quad_bar, 128);
+      if (quarter < 2) mine = op(mine, meet[32 * quarter]);
+      if (quarter == 1) meet[32] = mine;
+      named_bar_sync(quad_bar, 128);
+      if (quarter == 0) {
+        mine = op(mine, meet[32]);
+        meet[0] = mine;
       }
-      named_bar_sync(pair_bar, 64);
-      if (half == 0) mine = *meet;
-      return mine;
+      named_bar_sync(quad_bar, 128);
+      return meet[0];                                         // (the next to write it comes through a barrier first)
     };
-    auto arrive_p = [&](int t) {
+    auto agree = [&](bool fine) -> bool { return !named_bar_or(quad_bar, 128, !fine); };
+    uint32_t scores = 0;                                      // bit b: parity of score barrier b
+    auto arrive_p = [&](int b) {
       __syncwarp();
       if (lane == 0) {
-        if constexpr (kPair) arrive_leader_relaxed(bar(bPFull + w));
-        else mbar_arrive(bar(bPFull + (kSolo ? t & 1 : w)));
+        if constexpr (kPair) arrive_leader_relaxed(bar(bPFull + b));
+        else mbar_arrive(bar(bPFull + b));
       }
-    };
-    uint32_t step = 0;                                        // key tiles of this row tile, over all items
-    uint32_t scores = 0;                                      // kSolo: parities of even and odd key tiles' barriers
-    // until the last product issued, that of key tile t of the item, is done
-    auto wait_product = [&](int t) -> bool {
-      if constexpr (kSolo) return warp_wait(bar(bPvDone + (t & 1)), (~scores >> (t & 1)) & 1, wc);
-      return warp_wait(bar(bPvDone + w), (step - 1) & 1, wc);
     };
     int mbase = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
-      // (a wait that gives up ends both warps of a row at the same place: neither is left at their barrier)
-      ok = !named_bar_or(pair_bar, 64, !warp_wait<kPair>(bar(bSched + k % kSched), (k / kSched) & 1, wc));
+      // (a wait that gives up ends all warps of a row at the same place: none is left at their barrier)
+      ok = agree(warp_wait<kPair>(bar(bSched + k % kSched), (k / kSched) & 1, wc));
       if (!ok) break;
-      // The item's words are read here for the loop over the keys and again for the epilogue: held in between
-      // they would cost registers that the scores need.
-      int nw, seen;
+      // The item's words are read here for the loop over the keys and again for the epilogue.
+      int n_a, n_b, n, seen_a, nk;
       {
         Item it;
-        if (!announced(k, it)) {
+        const bool there = announced(k, it);
+        if (!there) {
           release_item(k);
           break;
         }
         const Shape sh(it, kTileRows<kPair>);
-        nw = w ? sh.n_b : sh.n_a;
-        if (!kSolo && nw == 0 && sh.n > 0) {                  // the empty step
-          ok = warp_wait(bar(bSFull + w), step++ & 1, wc);
-          arrive_p(0);
-        }
-        seen = min(it.nk, it.off + row + 1) - 64 * half;      // of the half's keys, counted from its first, those this row sees
+        n_a = sh.n_a;
+        n_b = sh.n_b;
+        n = sh.n;
+        nk = it.nk;
+        seen_a = it.off + row_a + 1;                          // keys that the row sees, had the item more of them
       }
-      float ref = -INFINITY, sum = 0.f;
-      for (int t = 0; t < nw; ++t, ++step) {
-        uint32_t buf = 0;
-        if constexpr (kSolo) {
-          buf = 128 * (t & 1);
-          ok = warp_wait(bar(buf ? bSOdd : bSFull), (buf ? scores >> 1 : scores) & 1, wc);
-          scores ^= buf ? 2 : 1;
-        } else {
-          ok = warp_wait(bar(bSFull + w), step & 1, wc);
-        }
-        tc_fence_after();
-        uint32_t s[2][32];
-        auto load_scores = [&] {
-          tmem_ld32(ts + buf, s[0]);
-          tmem_ld32(ts + buf + 32, s[1]);
-          tmem_wait_ld();
-          const int left = seen - t * kPfKeys;
-          if (left < 64) {
+      float ref = -INFINITY, sum = 0.f, ref_other = -INFINITY, sum_other = 0.f;   // of this row tile, of the other
+#pragma unroll 1
+      for (int x = 0; x < 2 * (n + 1); ++x) {
+        const int t = x >> 1, w = x & 1, nw = w ? n_b : n_a;
+        const int b = kSolo ? t & 1 : w;                      // score buffer, and the barriers'
+        if (kSolo && w) continue;
+        if (t < nw) {
+          ok = warp_wait(bar(kSolo && b ? bSOdd : bSFull + w), (scores >> b) & 1, wc);
+          scores ^= 1u << b;
+          tc_fence_after();
+          uint32_t s[32];
+          auto load_scores = [&] {
+            tmem_ld32(ts + 128 * b, s);
+            tmem_wait_ld();
+            // of the quarter's keys, those this row sees
+            const int left = min(nk, seen_a + kTileRows<kPair> * w) - t * kPfKeys - 32 * quarter;
+            if (left < 32) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c >= left) s[c / 32][c % 32] = 0xFF800000u;
+              for (int c = 0; c < 32; ++c)
+                if (c >= left) s[c] = 0xFF800000u;
+            }
+          };
+          load_scores();
+          float m0 = -INFINITY, m1 = m0;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            m0 = max3(m0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+            m1 = max3(m1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
           }
-        };
-        load_scores();
-        float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            m0 = max3(m0, __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-            m1 = max3(m1, __uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3]));
-            m2 = max3(m2, __uint_as_float(s[c][e + 4]), __uint_as_float(s[c][e + 5]));
-            m3 = max3(m3, __uint_as_float(s[c][e + 6]), __uint_as_float(s[c][e + 7]));
+          float top = fmaxf(m0, m1) * p.scale_log2;
+          // some row of the four warps has outgrown its reference (a wait that gave up ends all of them here, too)
+          auto outgrown = [&] { return top > ref + kSlack || (ref == -INFINITY && top > -INFINITY); };
+          tc_fence_before();
+          const bool settle = named_bar_or(quad_bar, 128, outgrown() || !ok);
+          tc_fence_after();
+          if (settle) {
+            ok = agree(ok);
+            if (ok) {
+              top = all4(top, [](float a, float b) { return fmaxf(a, b); });
+              const bool move = outgrown();
+              if (t == 0) {
+                if (move) ref = top;
+              } else {
+                // the product before this one has finished: O is these warps' to rescale
+                if constexpr (kSolo) ok = warp_wait(bar(bPvDone + (b ^ 1)), (~scores >> (b ^ 1)) & 1, wc);
+                else ok = warp_wait(bar(bPvDone + w), (scores >> w) & 1, wc);
+                tc_fence_after();
+                const float f = move ? (ref == -INFINITY ? 0.f : ex2_approx(ref - top)) : 1.f;
+                if (move) ref = top;
+                sum *= f;
+                rescale_columns(to + 128 * w, f);
+                load_scores();
+                tc_fence_before();
+                ok = agree(ok);
+                tc_fence_after();
+              }
+            }
           }
-        float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
-        // some row of the two warps has outgrown its reference (a wait that gave up ends both warps here, too)
-        auto outgrown = [&] { return top > ref + kSlack || (ref == -INFINITY && top > -INFINITY); };
-        tc_fence_before();
-        const bool settle = named_bar_or(pair_bar, 64, outgrown() || !ok);
-        tc_fence_after();
-        if (settle) {
-          ok = both(ok ? 1.f : 0.f, [](float a, float b) { return fminf(a, b); }) > 0.f;
-          if (ok) {
-            top = both(top, [](float a, float b) { return fmaxf(a, b); });
-            const bool move = outgrown();
-            if (t == 0) {
-              if (move) ref = top;
-            } else {
-              // the product before this one has finished: O is these warps' to rescale
-              ok = wait_product(t - 1);
-              tc_fence_after();
-              const float f = move ? (ref == -INFINITY ? 0.f : ex2_approx(ref - top)) : 1.f;
-              if (move) ref = top;
-              sum *= f;
-              rescale_columns(to, f);
-              load_scores();                                  // again: held over the rescaling they would be spilled
-              tc_fence_before();
-              ok = !named_bar_or(pair_bar, 64, !ok);
-              tc_fence_after();
+          if (!ok) break;
+          const float sub = ref == -INFINITY ? 0.f : -ref;
+          const float2 sc = make_float2(p.scale_log2, p.scale_log2), sb = make_float2(sub, sub);
+          float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+          // The weights go over columns 0-63 of the tile's scores, which all four warps have read: they have passed
+          // the barrier above.
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t* z = s + 16 * c + 2 * e;
+              const float2 v = f2_fma(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])), sc, sb);
+              const float2 y = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+              if (e & 1) acc1 = f2_add(acc1, y);
+              else acc0 = f2_add(acc0, y);
+              pk[e] = pack_bf16x2(y.x, y.y);
+            }
+            tmem_st8(tp + 128 * b + 8 * c, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          arrive_p(b);
+          sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+        } else if (t == nw) {
+          // ------ the row tile's end: its output
+          Item it;
+          announced(k, it);
+          const Shape sh(it, kTileRows<kPair>);
+          if (!kSolo && nw == 0 && n > 0) {                   // an empty step
+            ok = warp_wait(bar(bSFull + w), (scores >> w) & 1, wc);
+            scores ^= 1u << w;
+            arrive_p(w);
+          }
+          if (nw > 0) {
+            const int last = kSolo ? (nw - 1) & 1 : w;
+            ok = warp_wait(bar(bPvDone + last), (~scores >> last) & 1, wc);
+            tc_fence_after();
+          }
+          uint32_t dirty = 0;                                 // some masked tile of this row tile had its values cleared
+          if (ok && nw > sh.whole) {                          // the guard's notes up to this row tile's last
+            const int M = mbase + nw - 1 - sh.whole;
+            ok = warp_wait<kPair>(bar(bVClean + M % kMasked), (M / kMasked) & 1, wc);
+            if (*reinterpret_cast<volatile int*>(smem + kOffFound))
+              for (int u = sh.whole; u < nw; ++u)
+                for (int i = 0; i < 8; ++i) dirty |= bad[8 * ((mbase + u - sh.whole) % kMasked) + i];
+          }
+          ok = agree(ok);
+          if (!ok) break;
+          const int row = row_a + kTileRows<kPair> * w;
+          if (row - lane - 32 * quad < it.nq) {               // all warps of this CTA: they meet
+            sum = all4(sum, [](float a, float b) { return a + b; });
+            const bool any = nw > 0 && !(sum == 0.f);
+            const float inv = any ? 1.f / sum : 0.f;
+            const float lse = any ? (ref + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+            const bool live = row < it.nq;
+            const size_t out_row = static_cast<size_t>(it.q0 + row) * p.heads + it.h;
+            const size_t part_row = (static_cast<size_t>(max(it.part, 0)) * p.heads + it.h) * (2 * kTileRows<kPair>) + row;
+            if (live && quarter == 0) {
+              if (it.part >= 0) p.part_lse[part_row] = lse;
+              else if (p.lse) p.lse[out_row] = lse;
+            }
+            // all but rows without a key and tiles of which the guard has taken out values
+            const int mate = lane & 3, first = row - mate;    // of the first of four lanes' rows
+            const bool plain = __all_sync(0xffffffffu, any) && dirty == 0;
+            if (plain && it.part < 0)
+              store_columns(to + 128 * w, inv, p.out + (out_row - static_cast<size_t>(mate) * p.heads) * kNope + 32 * quarter + 8 * mate,
+                            static_cast<size_t>(p.heads) * kNope, it.nq - first);
+            else if (plain)
+              store_columns(to + 128 * w, inv, p.part_o + (part_row - mate) * kNope + 32 * quarter + 4 * mate, static_cast<size_t>(kNope),
+                            it.nq - first);
+#pragma unroll 1
+            for (int c = 32 * quarter; c < 32 * quarter + 32 && !plain; c += 16) {
+              uint32_t o[16];
+              if (nw > 0) {
+                tmem_ld16(to + 128 * w + (c & 16), o);
+                tmem_wait_ld();
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+              if (dirty && live) {
+                // values that the guard took out: a key that this row sees gives its infinity or NaN to the sum
+                const int all = min(it.nk, it.off + row + 1);
+                for (int u = sh.whole; u < nw; ++u)
+                  for (int i = 0; i < 4; ++i)
+                    for (uint32_t m = bad[8 * ((mbase + u - sh.whole) % kMasked) + i] |
+                                      bad[8 * ((mbase + u - sh.whole) % kMasked) + 4 + i];
+                         m; m &= m - 1) {
+                      const int key = u * kPfKeys + 32 * i + __ffs(m) - 1;
+                      if (key >= all) continue;
+                      const uint16_t* v = p.v + (it.k0 + key) * p.v_ts + it.h * p.v_hs + c;
+#pragma unroll
+                      for (int e = 0; e < 16; ++e)
+                        if (not_finite(v[e]))
+                          o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(static_cast<uint32_t>(v[e]) << 16));
+                    }
+              }
+              // the same exchange, of 16 columns
+              if (it.part >= 0) {
+                transpose4_blocks<4>(o, lane);
+                float* dst = p.part_o + (part_row - mate) * kNope + c + 4 * mate;
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  if (first + y < it.nq)
+                    *reinterpret_cast<uint4*>(dst + y * kNope) = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+              } else {
+                uint32_t h[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                transpose4_blocks<2>(h, lane);
+                uint16_t* dst = p.out + (out_row - static_cast<size_t>(mate) * p.heads) * kNope + c + 4 * mate;
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  if (first + y < it.nq)
+                    *reinterpret_cast<uint2*>(dst + static_cast<size_t>(y) * p.heads * kNope) = make_uint2(h[2 * y], h[2 * y + 1]);
+              }
             }
           }
         }
-        if (!ok) break;
-        const float sub = ref == -INFINITY ? 0.f : -ref;
-        const float2 sc = make_float2(p.scale_log2, p.scale_log2), sb = make_float2(sub, sub);
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-        // The weights go over columns 0-63 of the tile's scores, which both warps have read: the second half's
-        // lie over scores of the first half's warp, which has passed the barrier above.
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t* z = s[c / 2] + 16 * (c & 1) + 2 * e;
-            const float2 x = f2_fma(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])), sc, sb);
-            const float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            if (e & 1) acc1 = f2_add(acc1, y);
-            else acc0 = f2_add(acc0, y);
-            pk[e] = pack_bf16x2(y.x, y.y);
-          }
-          tmem_st8(tp + buf + 8 * c, pk);
+        if constexpr (!kSolo) {
+          const float r = ref, a = sum;
+          ref = ref_other;
+          sum = sum_other;
+          ref_other = r;
+          sum_other = a;
         }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive_p(t);
-        sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
       }
-      if (ok && nw > 0) {
-        ok = wait_product(nw - 1);
-        tc_fence_after();
-      }
-      Item it;
-      announced(k, it);
-      const Shape sh(it, kTileRows<kPair>);
-      uint32_t dirty = 0;                                     // some masked tile of this row tile had its values cleared
-      if (ok && nw > sh.whole) {                              // the guard's notes up to this row tile's last
-        const int M = mbase + nw - 1 - sh.whole;
-        ok = warp_wait<kPair>(bar(bVClean + M % kMasked), (M / kMasked) & 1, wc);
-        if (*reinterpret_cast<volatile int*>(smem + kOffFound))
-          for (int t = sh.whole; t < nw; ++t)
-            for (int i = 0; i < 8; ++i) dirty |= bad[8 * ((mbase + t - sh.whole) % kMasked) + i];
-      }
-      if (half == 0) *meet = sum;
-      ok = !named_bar_or(pair_bar, 64, !ok);
       if (!ok) break;
-      if (row0 < it.nq) {                                  // both warps, whole: they meet, and tcgen05.ld is collective
-        if (half == 1) {
-          sum += *meet;
-          *meet = sum;
-        }
-        named_bar_sync(pair_bar, 64);
-        if (half == 0) sum = *meet;
-        const bool any = nw > 0 && !(sum == 0.f);
-        const float inv = any ? 1.f / sum : 0.f;
-        const float lse = any ? (ref + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-        const bool live = row < it.nq;
-        const size_t out_row = static_cast<size_t>(it.q0 + row) * p.heads + it.h;
-        const size_t part_row = (static_cast<size_t>(max(it.part, 0)) * p.heads + it.h) * (2 * kTileRows<kPair>) + row;
-        if (live && half == 0) {
-          if (it.part >= 0) p.part_lse[part_row] = lse;
-          else if (p.lse) p.lse[out_row] = lse;
-        }
-        // all but rows without a key and tiles of which the guard has taken out values
-        const int mate = lane & 3, first = row - mate;        // of the first of four lanes' rows
-        const bool plain = __all_sync(0xffffffffu, any) && dirty == 0;
-        if (plain && it.part < 0)
-          store_columns(to, inv, p.out + (out_row - static_cast<size_t>(mate) * p.heads) * kNope + 64 * half + 8 * mate,
-                        static_cast<size_t>(p.heads) * kNope, it.nq - first);
-        else if (plain)
-          store_columns(to, inv, p.part_o + (part_row - mate) * kNope + 64 * half + 4 * mate, static_cast<size_t>(kNope),
-                        it.nq - first);
-#pragma unroll 1
-        for (int c = 64 * half; c < 64 * half + 64 && !plain; c += 16) {
-          uint32_t o[16];
-          if (nw > 0) {
-            tmem_ld16(to + (c & 48), o);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-          if (dirty && live) {
-            // values that the guard took out: a key that this row sees gives its infinity or NaN to the sum
-            const int all = min(it.nk, it.off + row + 1);
-            for (int t = sh.whole; t < nw; ++t)
-              for (int i = 0; i < 4; ++i)
-                for (uint32_t m = bad[8 * ((mbase + t - sh.whole) % kMasked) + i] |
-                                  bad[8 * ((mbase + t - sh.whole) % kMasked) + 4 + i];
-                     m; m &= m - 1) {
-                  const int key = t * kPfKeys + 32 * i + __ffs(m) - 1;
-                  if (key >= all) continue;
-                  const uint16_t* v = p.v + (it.k0 + key) * p.v_ts + it.h * p.v_hs + c;
-#pragma unroll
-                  for (int e = 0; e < 16; ++e)
-                    if (not_finite(v[e]))
-                      o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(static_cast<uint32_t>(v[e]) << 16));
-                }
-          }
-          // the same exchange, of 16 columns
-          if (it.part >= 0) {
-            transpose4_blocks<4>(o, lane);
-            float* dst = p.part_o + (part_row - mate) * kNope + c + 4 * mate;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (first + x < it.nq)
-                *reinterpret_cast<uint4*>(dst + x * kNope) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-          } else {
-            uint32_t b[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-            transpose4_blocks<2>(b, lane);
-            uint16_t* dst = p.out + (out_row - static_cast<size_t>(mate) * p.heads) * kNope + c + 4 * mate;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (first + x < it.nq)
-                *reinterpret_cast<uint2*>(dst + static_cast<size_t>(x) * p.heads * kNope) = make_uint2(b[2 * x], b[2 * x + 1]);
-          }
-        }
+      {
+        Item it;
+        announced(k, it);
+        const Shape sh(it, kTileRows<kPair>);
+        mbase += sh.n - sh.whole;
       }
-      mbase += sh.n - sh.whole;
       __syncwarp();
       if (lane == 0) {                                        // the item's words have been read
         if constexpr (kPair) arrive_leader_relaxed(bar(bSchedFree + k % kSched));
