@@ -624,8 +624,11 @@ int mla_prefill_plan(const int32_t* q_indptr, const int32_t* kv_indptr, int32_t 
  *   s_ij = sm_scale (q_i . [k_nope_j, k_rope_j]);   lse_i = ln sum_j exp(s_ij);
  *   out_i = sum_j softmax(s_i)_j v_j                 over the keys row i sees.
  * A row that sees no key, or none with a score above -inf, gets out = 0 and
- * lse = -inf.  Values of keys that a
- * row does not see never reach it, whatever they are.
+ * lse = -inf, whatever the values are.  Values of keys that a row does not see
+ * never reach it.  An infinite or NaN value of a key that it sees with a score
+ * above -inf leaves that column of its output infinite or NaN, however small
+ * the key's weight (which of the two is not promised once the weight is below
+ * 2^-126); with a score of -inf, beside others above it, it may or may not.
  *   plan_host, plan_dev  the words of mla_prefill_plan, on both sides
  *              (plan_dev 16-byte aligned).
  *   q          device bf16: head h of row i at q + i*q_token_stride +

@@ -1056,8 +1056,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-              if (dirty && live) {
-                // values that the guard took out: a key that this row sees gives its infinity or NaN to the sum
+              if (dirty && live && any) {
+                // values that the guard took out: a key that this row sees gives its infinity or NaN to the sum (a
+                // row without a score above -inf has no sum)
                 const int all = min(it.nk, it.off + row + 1);
                 for (int u = sh.whole; u < nw; ++u)
                   for (int i = 0; i < 4; ++i)

@@ -564,6 +564,52 @@ def test_prefill_keeps_what_is_masked_out(bad, causal, pairs):
         assert np.isnan(o[sees_k]).all() and np.isnan(l[sees_k]).all()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("ql,kl,pairs", [([40], [200], False), ([200], [330], False), ([600], [800], True)])
+def test_prefill_rows_without_a_score_above_minus_infinity(ql, kl, pairs, bad):
+    # such a row has no weights: whatever the values are, in tiles that all rows see whole and in partly seen ones,
+    # its output is zero
+    torch, B = _t()
+    qp, kp, H = _indptr(ql), _indptr(kl), 2
+    plan = B.Prefiller(qp, kp, H)
+    if pairs:
+        plan = _on_pairs(plan, qp, kp, H, True)
+    (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(15, ql[0], kl[0], H)
+    ref, ref_lse, mag = P.prefill_attention(xq, xk, xr, xv, qp, kp, SM)
+    none = [ql[0] // 2, ql[0] - 3, ql[0] - 1]
+    k[:, 0, 5] = -k[:, 0, 5].abs() - 0.5
+    q[none, 0, 5] = float("inf")
+    v[[3, kl[0] - 2, kl[0] - 30], 0, 9] = bad
+    out, lse = _attend(plan, q, k, kr, v)
+    assert (out[none, 0] == 0).all()
+    assert torch.isneginf(lse[none, 0]).all()
+    _check_attention(out[:, 1:], lse[:, 1:], ref[:, 1:], ref_lse[:, 1:], mag[:, 1:])
+
+
+@pytest.mark.parametrize("at", [10, 330 - 4])
+@pytest.mark.parametrize("pairs", [False, True])
+def test_prefill_values_that_are_not_finite_under_a_vanished_weight(pairs, at):
+    # a score some 400 below the others: its weight is zero in fp32, but the value it weighs is not finite, and so is
+    # the sum, in a tile that every row sees whole and in a partly seen one
+    torch, B = _t()
+    qp, kp = _indptr([200]), _indptr([330])
+    plan = B.Prefiller(qp, kp, 1)
+    if pairs:
+        plan = _on_pairs(plan, qp, kp, 1, True)
+    q = torch.full((200, 1, 192), 4.0, dtype=torch.bfloat16, device="cuda")
+    k = torch.full((330, 1, 128), 4.0, dtype=torch.bfloat16, device="cuda")
+    kr = torch.zeros((330, 64), dtype=torch.bfloat16, device="cuda")
+    v = torch.ones((330, 1, 128), dtype=torch.bfloat16, device="cuda")
+    k[at] = -8.0
+    v[at, 0, 7] = float("inf")
+    out, lse = _attend(plan, q, k, kr, v)
+    sees = torch.arange(200, device="cuda") + 130 >= at
+    assert not torch.isfinite(out[sees, 0, 7]).any()
+    assert torch.isfinite(out[~sees]).all()
+    rest = [c for c in range(128) if c != 7]
+    assert (out[:, 0, rest] == 1).all() and torch.isfinite(lse).all()
+
+
 @pytest.mark.parametrize("ql,kl,H,causal", [
     ([64] * 4, [4000, 3000, 3500, 4096], 48, True),              # several items a block, of many key tiles
     ([128, 1, 17, 100] * 9, [700, 1290, 5, 2000] * 9, 12, True),
