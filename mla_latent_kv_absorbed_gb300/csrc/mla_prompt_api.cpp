@@ -4,6 +4,7 @@
 // throws across the boundary.
 #include <cmath>
 #include <cstring>
+#include <limits>
 #include <new>
 #include <vector>
 
@@ -329,9 +330,10 @@ int mla_prefill_run(const int32_t* plan_host, const int32_t* plan_dev, const voi
   const int key_box = p.rows > kPfRows ? kPfKeys / 2 : kPfKeys;
   p.q_tokens = plan_host[kPQTokens];
   p.kv_tokens = plan_host[kPKvTokens];
-  // the kernel takes maxima of the products before it scales them: a positive
-  // scale (0 becomes one that leaves every finite score at 0 in fp32)
-  p.scale_log2 = std::fmax(std::fabs(sm_scale) * 1.4426950408889634f, 1e-30f);
+  // the kernel takes maxima of the products before it scales them, and masks
+  // them by -inf: a positive scale.  0 becomes the smallest number, 2^-149,
+  // which leaves every finite fp32 score (below 2^128) under 2^-21.
+  p.scale_log2 = std::fmax(std::fabs(sm_scale) * 1.4426950408889634f, std::numeric_limits<float>::denorm_min());
   p.negate = sm_scale < 0.f;
   if (!std::isfinite(p.scale_log2)) return MLA_ERR_INVALID_ARG;
   CUtensorMap tm_q, tm_k, tm_kr, tm_v;

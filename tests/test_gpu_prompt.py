@@ -506,6 +506,23 @@ def test_prefill_of_any_scale(sm):
     assert np.abs(lse.cpu().numpy() - ref_lse).max() <= 4 * LSE_ATOL
 
 
+@pytest.mark.parametrize("sm", [0.0, -0.0, 1e-38, 3e-36, -3e-36])
+def test_prefill_of_scales_near_zero(sm):
+    # scores of up to 1e37 before the scale: zero weighs every key alike, and a tiny scale is not another one
+    torch, B = _t()
+    qp, kp = _indptr([150]), _indptr([200])
+    (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(6, 150, 200, 2)
+    q, k, kr = q * 2.0 ** 59, k * 2.0 ** 59, kr * 2.0 ** 59      # exact: 2^118 is 3e35
+    f = 2.0 ** 59
+    ref, ref_lse, mag = P.prefill_attention(xq * f, xk * f, xr * f, xv, qp, kp, float(np.float32(sm)))
+    out, lse = _attend(B.Prefiller(qp, kp, 2), q, k, kr, v, sm=sm)
+    # scaled scores of at most 60: 192 products to 2^-22 of the sum of their magnitudes (under 200 * sm * 2^118), the
+    # scale itself to 2^-24 (a subnormal one: its last bit, 2^-149, times 2^118 * 60)
+    off = 200 * abs(sm) * 2.0 ** 118 * 2.0 ** -21 + 2.0 ** -24
+    _within(_f64(out), ref, _attention_bound(ref, mag) + 2 * off * mag, "out")
+    assert np.abs(lse.cpu().numpy() - ref_lse).max() <= LSE_ATOL + off
+
+
 def test_prefill_strides():
     # q out of a wider projection; keys and values as the halves of one [T, H, 256] projection; heads outermost
     torch, B = _t()
