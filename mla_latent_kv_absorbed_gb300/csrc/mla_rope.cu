@@ -5,12 +5,13 @@
 //   (x0, x1) -> a (x0 cos - x1 sin,  x1 cos + x0 sin)
 //   latent y = x * rsqrt(mean x^2 + eps) * w
 //
-// The angle is exact at any position: f_i is a 64-bit fraction of a turn, so
-// position * f_i in 64-bit integers drops whole turns by wrapping and leaves
-// the phase to 2^-64 * position turns; its upper 32 bits, as a signed fraction
-// in [-1/2, 1/2), become the argument of sincospif (error: 2^-25 of a half
-// turn from the conversion to 24 bits).  No table is read and no position is
-// too large.  Sums and products are fp32, rounded once to the output's type.
+// f_i is a 64-bit fraction of a turn, so position * f_i in 64-bit integers drops
+// whole turns by wrapping, without an error of its own; as a signed fraction in
+// [-1/2, 1/2) it becomes the argument of sincospif, rounded to 24 bits.  All 64
+// bits take part: the slowest pairs turn by 1e-9 of a turn a position, and of the
+// upper 32 bits alone their sines would keep few digits.  No table is read and no
+// position is too large.  Sums and products are fp32, rounded once to the
+// output's type.
 #include "mla_device.cuh"
 #include "mla_launch.h"
 #include "mla_prompt.h"
@@ -20,9 +21,8 @@ namespace {
 
 __device__ __forceinline__ float2 phase_cos_sin(uint64_t freq, int position, float amplitude) {
   const uint64_t turn = freq * static_cast<uint64_t>(static_cast<int64_t>(position));
-  const int hi = static_cast<int>(turn >> 32);              // turns * 2^32, wrapped to [-1/2, 1/2)
   float s, c;
-  sincospif(static_cast<float>(hi) * 0x1p-31f, &s, &c);     // 2 * turns half turns
+  sincospif(__ll2float_rn(static_cast<long long>(turn)) * 0x1p-63f, &s, &c);   // wrapped to [-1, 1) half turns
   return make_float2(c * amplitude, s * amplitude);
 }
 

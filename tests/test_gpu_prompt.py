@@ -99,6 +99,36 @@ def test_rope_query_at_the_ends_of_the_positions(interleaved):
 
 
 @pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("kw", [dict(theta=1e6, scaling="linear", factor=40.0), dict(scaling="yarn", factor=40.0),
+                                dict(theta=1e7, scaling="yarn", factor=160.0)])
+def test_small_angles_keep_their_relative_precision(kw, interleaved):
+    # the slowest pairs turn by 1e-9 of a turn and less a position: with x1 = 0 the second value is x0 times a sine of
+    # that size, one rounding and 2^-20 of it (the angle's conversion to 24 bits, sincospi, the product) off
+    torch, B = _t()
+    pos = np.array([1, 2, 3, 7, -1, -5, 100, 4095], dtype=np.int32)
+    T = len(pos)
+    first = np.zeros(64, dtype=bool)
+    first[0::2 if interleaved else 1] = True
+    if not interleaved:
+        first[32:] = False
+    q = torch.zeros((T, 1, 64), dtype=torch.bfloat16, device="cuda")
+    q[..., torch.from_numpy(first).cuda()] = 1.5
+    out = torch.empty_like(q)
+    p, fr = torch.from_numpy(pos).cuda(), B.rope_frequencies(**kw)
+    B.rope_query(q, p, fr, out, interleaved=interleaved)
+    ref = P.rope_rotate(_f64(q), pos, _inv(kw), interleaved)
+    bound = (BF + 2.0 ** -20) * np.abs(ref)
+    sines = np.abs(ref[..., ~first]) < 1.0                      # (near a zero of a cosine the angle's own error counts)
+    err = np.abs(_f64(out) - ref)
+    assert (err[..., ~first][sines] <= bound[..., ~first][sines]).all(), (err / np.abs(ref))[..., ~first].max()
+    cache = torch.zeros((T, 576), dtype=torch.bfloat16, device="cuda")
+    rows = torch.zeros((T, 576), dtype=torch.bfloat16, device="cuda")
+    rows[:, 512:] = q[:, 0]
+    B.rope_append_kv(cache, torch.arange(T, dtype=torch.int32, device="cuda"), rows, p, fr, interleaved=interleaved)
+    assert torch.equal(cache[:, 512:], out[:, 0])
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
 def test_rope_query_in_place_and_strided(interleaved):
     # a query cut out of a wider projection, rotated where it lies; and heads outermost
     torch, B = _t()
