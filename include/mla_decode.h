@@ -486,7 +486,8 @@ int mla_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slots, c
  * instead of the absorbed form's 576 + 512 ("MLA and torch.compile: v0.3's two
  * sources", section "MLA: starting from a 439-line commit": prefill takes the
  * ordinary path, decode the absorbing one).  All activations and weights are
- * bf16; strides are in elements, non-negative multiples of 8. */
+ * bf16; strides are in elements, non-negative multiples of 8 below 2^38 (that of
+ * a dimension of one is not looked at). */
 
 /* mla_rope_frequencies -- host only.  The rotary frequencies of the 64-wide
  * part, as the 64-bit fractions of a turn per position that the calls below

@@ -19,9 +19,10 @@ inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintp
 inline bool ready(const void* p, uintptr_t n = 16) { return p && aligned(p, n); }
 
 // A stride in elements that keeps 16-byte pieces aligned (bf16) and, in bytes,
-// below a tensor map's 2^40; `n` rows of `width` must not overlap.
-inline bool stride_ok(int64_t s, int64_t n = 1, int64_t width = 0) {
-  return s >= 0 && s < (1ll << 38) && s % 8 == 0 && (n <= 1 || s >= width);
+// below a tensor map's 2^40; the `n` rows of `width` must not overlap.  That of a
+// dimension of one is not used: anything.
+inline bool stride_ok(int64_t s, int64_t n, int64_t width = 0) {
+  return n <= 1 || (s >= width && s < (1ll << 38) && s % 8 == 0);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -112,8 +113,8 @@ int mla_rope_query(const void* q, int64_t q_token_stride, int64_t q_head_stride,
   if (!rope_args(freqs, amplitude, interleaved, &f)) return MLA_ERR_INVALID_ARG;
   if (tokens < 0 || num_heads < 1 || num_heads > 65535 || nope_dim < 0) return MLA_ERR_INVALID_ARG;
   if (nope_dim % 8 != 0 || nope_dim > 65536) return MLA_ERR_UNSUPPORTED;
-  if (!stride_ok(q_token_stride) || !stride_ok(q_head_stride) || !stride_ok(rope_token_stride) ||
-      !stride_ok(rope_head_stride))
+  if (!stride_ok(q_token_stride, tokens) || !stride_ok(q_head_stride, num_heads) ||
+      !stride_ok(rope_token_stride, tokens) || !stride_ok(rope_head_stride, num_heads))
     return MLA_ERR_INVALID_ARG;
   // rows of the output must not overlap, whichever of tokens and heads is outer
   const int64_t T = tokens, H = num_heads;

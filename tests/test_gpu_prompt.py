@@ -798,6 +798,36 @@ def test_two_prefills_at_once_with_their_own_workspaces():
         _check_attention(out, None, ref, ref_lse, mag)
 
 
+def test_strides_of_a_dimension_of_one_are_not_looked_at():
+    # one token cut out of an array whose rows are no multiple of 8 apart, one head likewise
+    torch, B = _t()
+    fr, pos = B.rope_frequencies(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    slot = torch.tensor([2], dtype=torch.int32, device="cuda")
+    rows = _normal(1, 1, 579)[0][:, :576]
+    assert rows.stride(0) == 579
+    cache = torch.zeros((4, 576), dtype=torch.bfloat16, device="cuda")
+    codes = torch.zeros((4, 576), dtype=torch.uint8, device="cuda")
+    B.rope_append_kv(cache, slot, rows, pos, fr)
+    B.rope_append_kv_fp8(codes, slot, rows, pos, fr, 1.0)
+    assert torch.equal(cache[2], rows[0])
+    assert torch.equal(codes[2].view(torch.float8_e4m3fn).float(), rows[0].to(torch.float8_e4m3fn).float())
+    # a token stride, then a head stride, that nothing steps by
+    x = _normal(2, 1, 3 * 192)[0]
+    q = x.as_strided((1, 3, 192), (577, 192, 1))
+    one = x.as_strided((3, 1, 192), (192, 193, 1))
+    for t in (q, one):
+        out = torch.empty(192, dtype=torch.bfloat16, device="cuda")
+        out = out.as_strided(t[..., 128:].shape, tuple(67 if n == 1 else 64 for n in t.shape[:2]) + (1,))
+        B.rope_query(t, torch.zeros(t.shape[0], dtype=torch.int32, device="cuda"), fr, out)
+        assert torch.equal(out.contiguous(), t[..., 128:].contiguous())
+    qp = _indptr([1])
+    (a, xa), (k, xk), (kr, xr), (v, xv) = _attention_inputs(4, 1, 1, 1)
+    ref, ref_lse, mag = P.prefill_attention(xa, xk, xr, xv, qp, qp, SM)
+    off = lambda t: t.as_strided(t.shape, tuple(s + 1 if n == 1 else s for n, s in zip(t.shape, t.stride())))  # noqa: E731
+    out, lse = _attend(B.Prefiller(qp, qp, 1), off(a), off(k), off(kr), off(v))
+    _check_attention(out, lse, ref, ref_lse, mag)
+
+
 # ---------------------------------------------------------------- as they run together
 
 @pytest.mark.parametrize("fp8", [False, True])
