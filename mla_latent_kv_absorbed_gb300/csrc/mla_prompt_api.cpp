@@ -25,6 +25,13 @@ inline bool stride_ok(int64_t s, int64_t n, int64_t width = 0) {
   return n <= 1 || (s >= width && s < (1ll << 38) && s % 8 == 0);
 }
 
+// Whether `n` rotary parts, `step` apart, lie apart and end before the next of
+// `outer` such groups, `stride` apart (by division: (n - 1) * step may pass 64 bits).
+inline bool inside(int64_t n, int64_t step, int64_t outer, int64_t stride) {
+  if (n > 1 && step < kRope) return false;
+  return outer <= 1 || (stride >= kRope && (n <= 1 || n - 1 <= (stride - kRope) / step));
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -118,10 +125,8 @@ int mla_rope_query(const void* q, int64_t q_token_stride, int64_t q_head_stride,
     return MLA_ERR_INVALID_ARG;
   // rows of the output must not overlap, whichever of tokens and heads is outer
   const int64_t T = tokens, H = num_heads;
-  const bool heads_inner = (H == 1 || rope_head_stride >= kRope) &&
-                           (T <= 1 || rope_token_stride >= (H - 1) * rope_head_stride + kRope);
-  const bool tokens_inner = (T <= 1 || rope_token_stride >= kRope) &&
-                            (H == 1 || rope_head_stride >= (T - 1) * rope_token_stride + kRope);
+  const bool heads_inner = inside(H, rope_head_stride, T, rope_token_stride);
+  const bool tokens_inner = inside(T, rope_token_stride, H, rope_head_stride);
   if (!heads_inner && !tokens_inner) return MLA_ERR_INVALID_ARG;
   if (tokens == 0) return MLA_OK;
   if (!ready(q) || !ready(positions, 4) || !ready(q_rope) || (q_nope && !aligned(q_nope, 16)))

@@ -59,6 +59,15 @@ def test_rope_query_refuses_bad_arguments(B):
     assert f(rhs=56) == 1 and f(rts=64, rhs=64) == 1 and f(rts=64, rhs=192) == 1
 
 
+def test_rope_query_refuses_rows_that_overlap_far_apart(B):
+    # heads as far apart as tokens, over more tokens than 64 bits of elements hold
+    lib, fake = B.library(), _fake_ptr()
+    fr = B.rope_frequencies()
+    for T, stride in (((1 << 29) + 1, 1 << 34), ((1 << 30) - 1, (1 << 38) - 8), ((1 << 27) + 3, 1 << 37)):
+        assert lib.mla_rope_query(fake, 384, 192, fake, T, 2, 128, fr.ctypes.data, F(1.0), 1, fake, stride, stride,
+                                  None, None) == 1, (T, stride)
+
+
 def test_rope_append_refuses_bad_arguments(B):
     lib, fake = B.library(), _fake_ptr()
     fr = B.rope_frequencies()
