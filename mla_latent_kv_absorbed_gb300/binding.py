@@ -626,7 +626,7 @@ def prefill_plan(q_indptr_host, kv_indptr_host, num_heads: int, causal: bool = T
     return plan, int(ws.value)
 
 
-_P_HEADS, _P_Q, _P_KV = 3, 5, 6                      # prefill plan header words
+_P_HEADS, _P_Q, _P_KV, _P_WORDS = 3, 5, 6, 11        # prefill plan header words
 
 
 def prefill_run(plan_host, plan_dev, q, k_nope, k_rope, v, sm_scale: float, out, lse, workspace, stream=None) -> None:
@@ -638,6 +638,8 @@ def prefill_run(plan_host, plan_dev, q, k_nope, k_rope, v, sm_scale: float, out,
             not plan_host.flags.c_contiguous:
         raise ValueError(f"{w}: plan_host is the int32 array of prefill_plan")
     head = plan_host[:16].tolist()
+    if head[_P_WORDS] != plan_host.size:             # (plan_dev has as many; the kernel reads what the header counts)
+        raise ValueError(f"{w}: plan_host has {plan_host.size} words, its header counts {head[_P_WORDS]}")
     H, nq, nk = head[_P_HEADS], head[_P_Q], head[_P_KV]
     _need(w, "plan_dev", plan_dev, torch.int32, (plan_host.shape[0],))
     _need(w, "q", q, bf, (nq, H, 192), dense=False)

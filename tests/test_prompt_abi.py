@@ -286,3 +286,15 @@ def test_wrappers_refuse_tensors_that_do_not_fit(B):
     no("plan_host is the int32", lambda: B.prefill_run(plan.astype(np.int64), pd, z(3, 2, 192), k, kr, v, 0.1, out,
                                                        None, z(1)))
     no("not on a CUDA device", lambda: B.prefill_run(plan, pd, z(3, 2, 192), k, kr, v, 0.1, out, None, z(1)))
+
+
+def test_prefill_run_refuses_a_plan_that_is_cut_short(B):
+    # the library reads the plan's items on the device as the header counts them: an array that ends before them is
+    # refused, on both sides, and one that goes on behind them too
+    import torch
+    plan, need = B.prefill_plan([0, 3, 300], [0, 5, 400], 2, num_sms=152)
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)  # noqa: E731
+    for ph in (plan[:16], plan[:-1], np.r_[plan, plan[-1:]], plan[:15], plan[:0]):
+        with pytest.raises(ValueError, match="plan_host"):
+            B.prefill_run(ph, torch.from_numpy(ph.copy()), z(300, 2, 192), z(400, 2, 128), z(400, 64), z(400, 2, 128), 0.1,
+                          z(300, 2, 128), None, z(need, dt=torch.uint8))
