@@ -449,6 +449,11 @@ def _sizes(where, name, t, dims):
     return t.shape
 
 
+def _status_word(where, workspace) -> None:
+    if workspace is not None and workspace.numel() * workspace.element_size() < 4:
+        raise ValueError(f"{where}: workspace has no room for the status word")
+
+
 def _launch_stream(where, stream, *tensors):
     """The stream to launch on (the current one when none is given).  Every tensor has to be on the current
     device: the launch goes there."""
@@ -525,6 +530,7 @@ def rope_query(q, positions, freqs, q_rope, q_nope=None, amplitude: float = 1.0,
 
 def _rope_append(w, cache_dtype, kv_cache, slots, rows, positions, freqs, norm_weight, workspace, stream):
     import torch
+    _status_word(w, workspace)
     T = _sizes(w, "rows", rows, 2)[0]
     N = _sizes(w, "kv_cache", kv_cache, 2)[0]
     _need(w, "kv_cache", kv_cache, cache_dtype, (N, 576))
@@ -568,6 +574,7 @@ def rope_append_kv_fp8(kv_cache, slots, rows, positions, freqs, kv_scale, norm_w
 
 def _expand(w, cache_dtype, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace, stream):
     import torch
+    _status_word(w, workspace)
     bf = torch.bfloat16
     N = _sizes(w, "kv_cache", kv_cache, 2)[0]
     T = _sizes(w, "kv_indices", kv_indices, 1)[0]

@@ -298,3 +298,19 @@ def test_prefill_run_refuses_a_plan_that_is_cut_short(B):
         with pytest.raises(ValueError, match="plan_host"):
             B.prefill_run(ph, torch.from_numpy(ph.copy()), z(300, 2, 192), z(400, 2, 128), z(400, 64), z(400, 2, 128), 0.1,
                           z(300, 2, 128), None, z(need, dt=torch.uint8))
+
+
+def test_wrappers_refuse_a_workspace_without_a_status_word(B):
+    # the kernels write four bytes there
+    import torch
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)  # noqa: E731
+    i32, u8, fr = torch.int32, torch.uint8, B.rope_frequencies()
+    rows, pos = z(3, 576), z(3, dt=i32)
+    heads = (z(2, 128, 512), z(2, 512, 128), z(3, 2, 128), z(3, 64), z(3, 2, 128))
+    for ws in (z(0, dt=u8), z(3, dt=u8)):
+        for call in (lambda: B.rope_append_kv(z(9, 576), pos, rows, pos, fr, workspace=ws),
+                     lambda: B.rope_append_kv_fp8(z(9, 576, dt=u8), pos, rows, pos, fr, 1.0, workspace=ws),
+                     lambda: B.expand_kv(z(9, 576), pos, *heads, workspace=ws),
+                     lambda: B.expand_kv_fp8(z(9, 576, dt=u8), 1.0, pos, *heads, workspace=ws)):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
