@@ -48,7 +48,7 @@ typedef enum {
   MLA_OK = 0,
   MLA_ERR_INVALID_ARG = 1,   /* null/misaligned pointer, bad size, malformed kv_indptr, bad plan */
   MLA_ERR_UNSUPPORTED = 2,   /* head count or dtype the library does not build */
-  MLA_ERR_WORKSPACE = 3,     /* plan or workspace buffer too small */
+  MLA_ERR_WORKSPACE = 3,     /* plan or workspace buffer too small; as a device status: its counters were not zero */
   MLA_ERR_CUDA = 4,          /* a CUDA runtime call failed (launch, attribute, device query) */
   MLA_ERR_TIMEOUT = 5,       /* a device-side wait exceeded its limit (~1 s); the kernel returned early */
   MLA_ERR_INDEX_OOB = 6,     /* a kv_indices value was outside [0, num_slots); row 0 was read instead */
@@ -644,8 +644,10 @@ int mla_prefill_plan(const int32_t* q_indptr, const int32_t* kv_indptr, int32_t 
  *              values are rounded to bf16, sums are fp32.
  *   lse        device fp32 [q rows, heads] or NULL.
  *   workspace  device, at least the plan's workspace_bytes, 16-byte aligned,
- *              zero-filled before first use (status word as for mla_decode_run;
- *              calls sharing one must not overlap on the GPU).
+ *              zero-filled before first use (status word as for mla_decode_run,
+ *              and counters that are zero between calls; calls sharing one must
+ *              not overlap on the GPU).  Counters found otherwise are reported as
+ *              MLA_ERR_WORKSPACE: rows may be missing, fill it with zeros again.
  * Safe to capture in a CUDA graph.  Errors as for mla_decode_run; with no
  * query row nothing is launched.  A plan_dev that does not lie inside the
  * arrays of plan_host is skipped item by item with MLA_ERR_PLAN_MISMATCH. */

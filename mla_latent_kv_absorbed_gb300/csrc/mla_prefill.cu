@@ -466,7 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         hear(0, it);                                          // (every pair has an item)
       }
+      int worked = 0;
       for (uint32_t k = 0; ok; ++k) {
+        ++worked;
         const Shape sh(it, kTileRows<kPair>);
         auto load_3d = [&](uint32_t dst, const CUtensorMap* m, int x, int z, int b) {
           if constexpr (kPair) tma_load_3d_pair(dst, m, x, it.h, z, mapa_shared(bar(b), 0));
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return;
           }
           const int w = atomicAdd(p.status + kWsCounter, 1) + static_cast<int>(gridDim.x) / kCtas;
-          more = w < total;
+          more = static_cast<uint32_t>(w) < static_cast<uint32_t>(total);   // (a counter that was not zero may be negative)
           if (more) fetch(w, next);
           announce(k + 1, next, more);
         };
@@ -565,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!more) break;
         it = next;
       }
+      if (rank == 0) atomicAdd(p.status + kWsWorked, worked);
       if (!ok) {                                              // no copy outlives the block (a pair: the pair)
         if (rank == 0) {
           if (q_bar[0] >= 0) drain_wait(bar(bQFull), q_bar[0]);
@@ -1128,11 +1131,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kIssuer) tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0) {
-    // the last block to finish leaves the counter at zero for the next launch
+    // The last block to finish leaves the counters at zero for the next launch.  All items have been worked on by then
+    // (unless a wait gave up: its status stands); fewer or more say that the counters were not zero, or that another
+    // launch used them.
     __threadfence();
-    if (atomicAdd(p.status + kWsDone, 1) == static_cast<int>(gridDim.x) - 1) {
+    const int blocks = static_cast<int>(gridDim.x), done = atomicAdd(p.status + kWsDone, 1);
+    if (done == blocks - 1) {
+      if (atomicExch(p.status + kWsWorked, 0) != p.n_items * p.heads) record_status(p.status, MLA_ERR_WORKSPACE);
       p.status[kWsCounter] = 0;
       p.status[kWsDone] = 0;
+    } else if (done < 0 || done >= blocks) {
+      record_status(p.status, MLA_ERR_WORKSPACE);
     }
   }
 }

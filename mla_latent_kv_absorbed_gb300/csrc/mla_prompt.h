@@ -79,8 +79,9 @@ constexpr long long kPfMaxBlocks = 0x7FFF0000;   // items x heads: every block o
 constexpr int32_t kPfNoLimit = 0x3FFFFFFF;   // off of an item without a causal limit
 
 // Words of the workspace's status header that the prefill kernel counts in
-// (zero between launches): items handed out, blocks that have finished.
-constexpr int kWsCounter = 16, kWsDone = 17;
+// (zero between launches): items handed out, blocks that have finished, items
+// worked on.
+constexpr int kWsCounter = 16, kWsDone = 17, kWsWorked = 18;
 
 inline int pf_items_off(const int32_t*) { return kPfHeaderWords; }
 inline int pf_merge_off(const int32_t* h) { return kPfHeaderWords + kPfItemWords * h[kPItems]; }
