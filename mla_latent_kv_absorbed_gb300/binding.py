@@ -715,7 +715,8 @@ class Decoder:
 
 
 class Prefiller:
-    """Convenience holder: plan a batch's prompt attention once, then run it on device tensors."""
+    """Convenience holder: plan a batch's prompt attention once, then run it on device tensors.  Ready on every stream
+    once it is made; its runs share one workspace, so they follow one another (on one stream, or ordered by events)."""
 
     def __init__(self, q_indptr_host, kv_indptr_host, num_heads: int, causal: bool = True, device="cuda",
                  num_sms: int = 0):
@@ -723,6 +724,8 @@ class Prefiller:
         self.plan_host, self.workspace_bytes = prefill_plan(q_indptr_host, kv_indptr_host, num_heads, causal, num_sms)
         self.plan_dev = torch.from_numpy(self.plan_host).to(device)
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=device)
+        # a run on another stream does not wait for the zeros
+        torch.cuda.current_stream(self.workspace.device).synchronize()
 
     def run(self, q, k_nope, k_rope, v, sm_scale, out, lse=None, stream=None):
         prefill_run(self.plan_host, self.plan_dev, q, k_nope, k_rope, v, sm_scale, out, lse, self.workspace, stream)

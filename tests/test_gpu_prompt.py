@@ -809,6 +809,23 @@ def test_prefill_on_another_stream_and_replayed():
     assert plan.check() == 0
 
 
+def test_prefiller_is_ready_on_every_stream():
+    # made while its own stream is busy, in memory that held something else, and run on another stream at once
+    torch, B = _t()
+    qp, kp = _indptr([300] * 4), _indptr([300] * 4)
+    H = 60
+    (q, _), (k, _), (kr, _), (v, _) = _attention_inputs(23, 1200, 1200, H)
+    want, _ = _attend(B.Prefiller(qp, kp, H), q, k, kr, v)
+    out, side = torch.zeros_like(want), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.full((256,), 77, dtype=torch.uint8, device="cuda")    # (the allocator gives this block out again)
+    torch.cuda._sleep(100_000_000)
+    plan = B.Prefiller(qp, kp, H)
+    plan.run(q, k, kr, v, SM, out, stream=side)
+    side.synchronize()
+    assert plan.check() == 0 and torch.equal(out, want)
+
+
 def test_two_prefills_at_once_with_their_own_workspaces():
     torch, B = _t()
     qp, kp = _indptr([5]), _indptr([4000])
