@@ -454,19 +454,24 @@ def _status_word(where, workspace) -> None:
         raise ValueError(f"{where}: workspace has no room for the status word")
 
 
-def _launch_stream(where, stream, *tensors):
-    """The stream to launch on (the current one when none is given).  Every tensor has to be on the current
-    device: the launch goes there."""
+def _current(stream):
+    """The current device, and the handle of `stream` or of the device's current stream."""
     import torch
     try:                                             # what current_device and current_stream look up, without
         cur = torch._C._cuda_getDevice()             # their objects: a third of a small call's host time
-        raw = torch._C._cuda_getCurrentRawStream(cur) if stream is None else None
+        return cur, torch._C._cuda_getCurrentRawStream(cur) if stream is None else _stream_handle(stream) or 0
     except AttributeError:
-        cur, raw = torch.cuda.current_device(), None
+        return torch.cuda.current_device(), _stream_handle(stream) or 0
+
+
+def _launch_stream(where, stream, *tensors):
+    """The stream to launch on (the current one when none is given).  Every tensor has to be on the current
+    device: the launch goes there."""
+    cur, raw = _current(stream)
     for t in tensors:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"{where}: a tensor is on device {t.device}, the current device is cuda:{cur}")
-    return (raw or None) if raw is not None else _stream_handle(stream)
+    return raw or None
 
 
 _ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
@@ -724,11 +729,19 @@ class Prefiller:
         self.plan_host, self.workspace_bytes = prefill_plan(q_indptr_host, kv_indptr_host, num_heads, causal, num_sms)
         self.plan_dev = torch.from_numpy(self.plan_host).to(device)
         self.workspace = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=device)
-        # a run on another stream does not wait for the zeros
-        torch.cuda.current_stream(self.workspace.device).synchronize()
+        home = torch.cuda.current_stream(self.workspace.device)
+        home.synchronize()                           # a run on another stream does not wait for the zeros
+        self._streams = {home.cuda_stream}
 
     def run(self, q, k_nope, k_rope, v, sm_scale, out, lse=None, stream=None):
-        prefill_run(self.plan_host, self.plan_dev, q, k_nope, k_rope, v, sm_scale, out, lse, self.workspace, stream)
+        handle = _current(stream)[1]
+        if handle not in self._streams:              # the allocator keeps plan and workspace until its work is done
+            import torch
+            where = torch.cuda.ExternalStream(handle, device=self.workspace.device)
+            for t in (self.plan_dev, self.workspace):
+                t.record_stream(where)
+            self._streams.add(handle)
+        prefill_run(self.plan_host, self.plan_dev, q, k_nope, k_rope, v, sm_scale, out, lse, self.workspace, handle)
 
     def check(self, stream=None) -> int:
         return check_errors(self.workspace, stream)

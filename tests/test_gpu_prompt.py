@@ -826,6 +826,26 @@ def test_prefiller_is_ready_on_every_stream():
     assert plan.check() == 0 and torch.equal(out, want)
 
 
+def test_prefiller_dropped_before_its_work_is_done():
+    # its plan and workspace stay its own until the stream that runs it has finished
+    torch, B = _t()
+    qp, kp = _indptr([3]), _indptr([4000])
+    (q, _), (k, _), (kr, _), (v, _) = _attention_inputs(24, 3, 4000, 2)
+    want, _ = _attend(B.Prefiller(qp, kp, 2), q, k, kr, v)
+    out, side = torch.zeros_like(want), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plan = B.Prefiller(qp, kp, 2)
+    held = {t.data_ptr(): t.numel() * t.element_size() for t in (plan.plan_dev, plan.workspace)}
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    plan.run(q, k, kr, v, SM, out, stream=side)
+    del plan
+    new = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in held.values()]
+    assert not held.keys() & {t.data_ptr() for t in new}
+    side.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_two_prefills_at_once_with_their_own_workspaces():
     torch, B = _t()
     qp, kp = _indptr([5]), _indptr([4000])
