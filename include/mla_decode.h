@@ -505,7 +505,8 @@ int mla_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slots, c
  *                       looked at.
  *   freqs               host uint64[32], written.
  * The position times freqs[i] modulo 2^64 is the angle as a fraction of a
- * turn, exactly: no position loses precision.
+ * turn.  That product loses nothing at any position; freqs[i] itself comes from
+ * double arithmetic and is within 2^-55 of a turn (2^-24 at the farthest position).
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (another scaling). */
 int mla_rope_frequencies(double theta, int32_t scaling, double factor, int32_t original_positions, double beta_fast,
                          double beta_slow, uint64_t* freqs);
@@ -531,9 +532,10 @@ int mla_rope_frequencies(double theta, int32_t scaling, double factor, int32_t o
  *   q_nope     NULL, or device bf16 [tokens, heads, nope_dim] dense: the rest
  *              of each head is copied there (what mla_absorb_query takes).
  * Errors: MLA_ERR_INVALID_ARG for null or non-16-byte-aligned pointers
- * (positions: 4), tokens < 0, num_heads < 1, bad strides (q_rope's rows
- * overlapping included); MLA_ERR_UNSUPPORTED for another nope_dim or more than
- * 2^31 - 1 blocks of work.  Nothing is launched then, nor for tokens == 0. */
+ * (positions: 4), tokens < 0, num_heads outside 1 .. 65535, bad strides
+ * (q_rope's rows overlapping included); MLA_ERR_UNSUPPORTED for another nope_dim
+ * or more than 2^30 - 1 blocks of work (a token and 32 heads; 128 heads where
+ * there are many).  Nothing is launched then, nor for tokens == 0. */
 int mla_rope_query(const void* q, int64_t q_token_stride, int64_t q_head_stride, const int32_t* positions,
                    int32_t tokens, int32_t num_heads, int32_t nope_dim, const uint64_t* freqs, float amplitude,
                    int32_t interleaved, void* q_rope, int64_t rope_token_stride, int64_t rope_head_stride,
@@ -544,7 +546,8 @@ int mla_rope_query(const void* q, int64_t q_token_stride, int64_t q_head_stride,
  * mla_append_kv for rows as the projection leaves them: the latent is
  * normalised (y = x / sqrt(mean x^2 + eps) * norm_weight over its 512 values;
  * norm_weight NULL: unchanged), the rope key rotated as in mla_rope_query, and
- * the row written to its slot; fp32 arithmetic, one rounding.
+ * the row written to its slot; fp32 arithmetic, one rounding (the sum of squares
+ * included: a row whose values pass 2^59 may overflow it and becomes zeros).
  *   kv_cache     device bf16 [num_slots, 576], written in place.
  *   slots        device int32 [tokens], distinct (two rows to one slot: any
  *                part of either may win).
@@ -587,8 +590,9 @@ int mla_rope_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slo
  *   k_nope, v   device bf16 [tokens, num_heads, 128];  k_rope  [tokens, 64].
  *   workspace   NULL, or a decode workspace (its status word).
  * Errors: MLA_ERR_INVALID_ARG for null or misaligned pointers (16 bytes;
- * kv_indices 4), tokens < 0, num_heads < 1, num_slots < 1; nothing is launched
- * then, nor for tokens == 0. */
+ * kv_indices 4), tokens < 0, num_heads outside 1 .. 65535, num_slots < 1;
+ * MLA_ERR_UNSUPPORTED for more than 2^30 - 1 tiles of work (128 tokens and one
+ * head's keys or values); nothing is launched then, nor for tokens == 0. */
 int mla_expand_kv(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, int32_t tokens,
                   const void* w_kc, const void* w_vc, int32_t num_heads, void* k_nope, void* k_rope, void* v,
                   void* workspace, void* stream);

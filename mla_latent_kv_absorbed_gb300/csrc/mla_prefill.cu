@@ -83,7 +83,11 @@ constexpr int kOffRingSolo = 3 * kBlock;              // a launch of items with 
 constexpr int kOffBar = kOffRing + kRingBytes;
 constexpr int kDepth = 4;                             // tiles told apart: more than the ring holds
 constexpr int kSched = 4;                             // items announced ahead
-constexpr int kMasked = 8;                            // masked tiles told apart: two items' worth and more
+// Masked tiles told apart.  An item has up to three of them, on pairs five, so that the notes that a tile's overwrite
+// are of an item that ended three tiles before it or more.  They have been read by then: the tile's place in the ring
+// (3.2 tiles at most) is free only when a tile at most three before it has had its products, that tile is of a later
+// item than the notes, and its weights come from warps that are through with the items before.
+constexpr int kMasked = 8;
 constexpr int kConsumers = 16 + 1 + 2;                // warps that read an announced item (in CTA 1: no issuer, but the producer)
 enum Bar : int {
   bQFull = 0,                    // [2] per row tile

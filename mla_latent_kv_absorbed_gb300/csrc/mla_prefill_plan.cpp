@@ -159,7 +159,7 @@ long long plan_rows(const int32_t* qp, const int32_t* kp, int B, int H, int caus
   const long long mean = (total + workers - 1) / workers;
   const long long whole = static_cast<long long>(tiles.size()) * H;
   if (tiles.empty()) return 0;
-  if (whole > (1 << 16)) return mean + most;                  // too many to simulate, and none long against the mean
+  if (whole > (1 << 16)) return mean + most;                  // too many to simulate (a long one among them stays whole)
   long long end = makespan(best, H, group_of(H, kp[B], best.size(), workers), workers);
   // the schedule of many items, none of them long, cannot be improved by cutting
   if (whole >= 8ll * workers && most <= mean / 2) return end;
