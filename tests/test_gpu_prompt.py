@@ -505,6 +505,103 @@ def test_prefill_cut_along_the_keys(ql, kl, H, causal):
     _check_attention(whole, None, ref, ref_lse, mag, "whole")
 
 
+def _cut(plan, qp, kp, H, causal, rows, parts):
+    """The same batch in items of `rows` rows whose keys are cut into up to `parts` pieces of whole tiles."""
+    torch, _ = _t()
+    items, joins, slot = [], [], 0
+    for b in range(len(qp) - 1):
+        lq, lk = int(qp[b + 1] - qp[b]), int(kp[b + 1] - kp[b])
+        for r in range(0, lq, rows):
+            nq, off = min(rows, lq - r), r + lk - lq if causal else 0x3FFFFFFF
+            seen = min(lk, max(0, off + nq))
+            tiles = (seen + 127) // 128
+            n = max(1, min(parts, tiles))
+            for k in range(n):
+                a, e = 128 * (tiles * k // n), 128 * (tiles * (k + 1) // n)
+                items.append([b, int(qp[b]) + r, nq, int(kp[b]) + a, min(seen, e) - a, off - a if causal else off,
+                              slot + k if n > 1 else -1, 0])
+            if n > 1:
+                joins.append([int(qp[b]) + r, nq, slot, slot + n])
+                slot += n
+    words = plan.plan_host[:16].tolist()
+    words[7:12] = [len(items), slot, len(joins), H, 16 + 8 * len(items) + 4 * len(joins)]
+    words[13:16] = [rows, int(all(i[2] <= 128 for i in items) and rows == 256), 0]
+    plan.plan_host = np.array(words + sum(items, []) + sum(joins, []), dtype=np.int32)
+    plan.plan_dev = torch.from_numpy(plan.plan_host).cuda()
+    plan.workspace = torch.zeros(256 + slot * H * rows * 129 * 4, dtype=torch.uint8, device="cuda")
+    return plan
+
+
+CUT = [
+    # rows of an item, pieces: one row tile, two, and pairs, whose items have up to 512 rows
+    ([100, 128, 1, 17], [700, 1290, 900, 60], 2, 256, 4), ([256, 129, 300], [900, 1500, 130], 2, 256, 3),
+    ([512], [1700], 1, 512, 5), ([1100, 300], [1500, 2000], 2, 512, 4), ([513, 290], [513, 100], 2, 512, 9),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("ql,kl,H,rows,parts", CUT)
+def test_prefill_cut_along_the_keys_in_every_form(ql, kl, H, rows, parts, causal):
+    torch, B = _t()
+    qp, kp = _indptr(ql), _indptr(kl)
+    plan = _cut(B.Prefiller(qp, kp, H, causal), qp, kp, H, causal, rows, parts)
+    assert plan.plan_host[8] > 1 and plan.plan_host[13] == rows
+    (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(61 + H, int(qp[-1]), int(kp[-1]), H)
+    ref, ref_lse, mag = P.prefill_attention(xq, xk, xr, xv, qp, kp, SM, causal)
+    out, lse = _attend(plan, q, k, kr, v)
+    _check_attention(out, lse, ref, ref_lse, mag)
+    outs = [torch.empty_like(out) for _ in range(3)]
+    for o in outs:
+        plan.run(q, k, kr, v, SM, o)
+    assert plan.check() == 0
+    assert all(torch.equal(o, out) for o in outs)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("ql,kl,H,rows,parts", CUT)
+def test_prefill_cut_items_keep_what_is_masked_out(ql, kl, H, rows, parts, causal, bad):
+    # values that are not finite in partly seen tiles of a cut item reach the rows that see them, through the join
+    torch, B = _t()
+    qp, kp = _indptr(ql), _indptr(kl)
+    plan = _cut(B.Prefiller(qp, kp, H, causal), qp, kp, H, causal, rows, parts)
+    (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(71 + H, int(qp[-1]), int(kp[-1]), H)
+    ref, ref_lse, mag = P.prefill_attention(xq, xk, xr, xv, qp, kp, SM, causal)
+    sees = np.zeros(ref.shape, dtype=bool)
+    for b, back in zip(range(len(ql)), (5, 60, 1, 33)):
+        key = kl[b] - min(back, kl[b])
+        v[int(kp[b]) + key, H - 1, 17 + b] = bad
+        last = np.arange(ql[b]) + (kl[b] - ql[b] if causal else kl[b])
+        sees[int(qp[b]):int(qp[b + 1]), H - 1, 17 + b] = last >= key
+    out, lse = _attend(plan, q, k, kr, v)
+    o = _f64(out)
+    assert sees.any() and np.array_equal(o[sees], np.full(int(sees.sum()), bad), equal_nan=True)
+    assert np.isfinite(o[~sees]).all()
+    assert (np.abs(o - ref)[~sees] <= _attention_bound(ref, mag)[~sees]).all()
+    l = lse.cpu().numpy()
+    empty = np.isneginf(ref_lse)
+    assert np.array_equal(np.isneginf(l), empty) and np.abs(l[~empty] - ref_lse[~empty]).max() <= LSE_ATOL
+
+
+@pytest.mark.parametrize("n,keys,H", [(400, 4096, 16), (1024, 4096, 8), (300, 2048, 32), (512, 16384, 32)])
+def test_prefill_of_a_chunk_that_continues_a_long_context(n, keys, H):
+    # items of 512 rows on CTA pairs whose keys the plan cuts; some rows of each row tile against the oracle
+    torch, B = _t()
+    qp, kp = _indptr([n]), _indptr([keys])
+    plan = B.Prefiller(qp, kp, H, num_sms=152)
+    assert plan.plan_host[13] == 512 and plan.plan_host[8] > 1
+    (q, xq), (k, xk), (kr, xr), (v, xv) = _attention_inputs(81, n, keys, H)
+    out, lse = _attend(plan, q, k, kr, v)
+    o, l = _f64(out), lse.cpu().numpy()
+    for i in sorted({0, 1, 127, 128, 200, 255, 256, 260, n - 130, n - 2, n - 1}):
+        seen = keys - n + i + 1
+        ref, ref_lse, mag = P.prefill_attention(xq[i:i + 1], xk[:seen], xr[:seen], xv[:seen], [0, 1], [0, seen], SM)
+        _within(o[i:i + 1], ref, _attention_bound(ref, mag), f"row {i}")
+        # the sum of so many weights in fp32: four partial sums a tile and pieces of at most 2^14 keys
+        assert np.abs(l[i:i + 1] - ref_lse).max() <= LSE_ATOL + keys * 2.0 ** -24
+    assert np.isfinite(o).all()
+
+
 @pytest.mark.parametrize("scale", [8.0, 60.0])
 def test_prefill_of_peaked_scores(scale):
     # large scores: the running maximum moves a lot, and most weights vanish; a key that grows along the
