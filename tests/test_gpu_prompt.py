@@ -205,6 +205,60 @@ def test_rope_append(fp8, T, norm, interleaved, kw, stride, amplitude):
     assert torch.equal(cache[rest], before[rest])
 
 
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("scale", [0.0371, 3.0, 1e-3])
+def test_rope_append_of_any_fp8_scale(scale, norm):
+    # scales that are no power of two divide; values past 448 scales saturate, infinities with them, NaN stays NaN
+    torch, B = _t()
+    T = 70
+    s32 = float(np.float32(scale))
+    rows, x = _normal(T, T, 576, scale=2.0)
+    rows[1] *= 4096.0
+    rows[2, 512:] *= 2048.0
+    x = _f64(rows)
+    w, xw = _normal(T + 1, 512)
+    pos = np.random.default_rng(3).integers(0, 163840, T).astype(np.int32)
+    cache = torch.zeros((T, 576), dtype=torch.uint8, device="cuda")
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    B.rope_append_kv_fp8(cache, slots, rows, torch.from_numpy(pos).cuda(), B.rope_frequencies(**YARN), scale,
+                         norm_weight=w if norm else None)
+    ref = P.append_values(x, pos, _inv(YARN), xw if norm else None)
+    slack = 2.0 ** -18 * np.abs(ref)                            # as in test_rope_append; the division adds 2^-24
+    slack[:, 512:] += 2.0 ** -19 * np.abs(x[:, 512:]).max(axis=1, keepdims=True) * 2
+    want = np.clip(ref / s32, -448, 448)
+    bound = np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -10) + slack / s32
+    got = _f64(cache.view(torch.float8_e4m3fn))
+    _within(got, want, bound, "append fp8")
+    assert (np.abs(ref / s32) > 500).any() and (np.abs(got)[np.abs(ref / s32) > 500] == 448).all()
+    if not norm:
+        # latents that are not finite, as mla_append_kv_fp8 quantises them
+        rows[3, 5], rows[3, 6], rows[3, 7], rows[3, 8] = float("inf"), float("-inf"), float("nan"), 1e30
+        B.rope_append_kv_fp8(cache, slots, rows, torch.from_numpy(pos).cuda(), B.rope_frequencies(**YARN), scale)
+        codes = O.quantize_rows_e4m3(rows.contiguous().cpu().view(torch.int16).numpy().view(np.uint16), s32)
+        assert np.array_equal(cache[:, :512].cpu().numpy(), codes[:, :512])
+        assert cache[3, 5:9].tolist() == [0x7E, 0xFE, 0x7F, 0x7E]
+
+
+@pytest.mark.parametrize("T,H", [(37, 3), (700, 33)])
+@pytest.mark.parametrize("scale", [0.0371, 3.0])
+def test_expand_of_any_fp8_scale(T, H, scale):
+    torch, B = _t()
+    s32 = float(np.float32(scale))
+    cache, x = _codes(T, T)
+    x = x * s32
+    wk, xk = _normal(T + 2, H, 128, 512, scale=512 ** -0.5)
+    wv, xv = _normal(T + 3, H, 512, 128, scale=512 ** -0.5)
+    bf = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    k, kr, v = bf(T, H, 128), bf(T, 64), bf(T, H, 128)
+    B.expand_kv_fp8(cache, scale, torch.arange(T, dtype=torch.int32, device="cuda"), wk, wv, k, kr, v)
+    lat = x[:, :512]
+    rk, rv = P.expand_rows(lat, xk, xv)
+    _within(_f64(k), rk, _expand_bound(rk, lat, xk, "tr,hnr->thn"), "k")
+    _within(_f64(v), rv, _expand_bound(rv, lat, xv, "tr,hrn->thn"), "v")
+    # code times scale in fp32 (2^-24), then to bf16
+    _within(_f64(kr), x[:, 512:], (BF + 2.0 ** -22) * np.abs(x[:, 512:]), "k_rope")
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_rope_append_skips_and_reports_bad_slots(fp8):
     torch, B = _t()
