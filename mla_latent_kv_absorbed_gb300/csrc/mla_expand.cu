@@ -63,28 +63,12 @@ struct Cfg {
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity))
-    if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) return;
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
   const float2 f = e4m3x2_value(codes);
   return pack_bf16x2(f.x, f.y);                             // exact
 }
 
-// ---- the two-CTA forms of the tensor core's and the copy engine's instructions
+// ---- the two-CTA forms of the tensor core's instructions
 __device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
 }
@@ -103,21 +87,6 @@ __device__ __forceinline__ void umma_ss2(uint32_t d_tmem, uint64_t adesc, uint64
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrives on the barrier at this offset in both CTAs when the products issued so far are done.
-__device__ __forceinline__ void umma_commit2(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-// A load into this CTA's shared memory whose bytes are counted on a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, int x, int y, uint32_t bar_cluster) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar_cluster)
-      : "memory");
-}
 
 // 16 bytes, or 16 zero bytes with nothing read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
@@ -127,18 +96,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 // All but the newest N of this thread's committed groups have landed.
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// Arrive on the barrier at this offset in CTA 0, ordering nothing: what it
-// tells (a TMEM read has come back) is already in registers.  With release
-// semantics at cluster scope it waited for the stores before it, about 4800
-// cycles a tile.
-__device__ __forceinline__ void mbar_arrive_leader_relaxed(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .b32 rb;\n\t"
-      "mapa.shared::cluster.u32 rb, %0, 0;\n\t"
-      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [rb];\n\t}" ::"r"(bar)
-      : "memory");
-}
 
 template <bool kFp8, int NT, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -451,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
+        // (with release semantics it waited for the stores before it, about 4800 cycles a tile)
         if constexpr (kPair) mbar_arrive_leader_relaxed(acc_empty(buf));
         else mbar_arrive(acc_empty(buf));
       }

@@ -150,13 +150,6 @@ __device__ __forceinline__ bool item_in_request(const DecodeParams& p, int b, in
   return lo <= s && e <= hi;
 }
 
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) return;
-  }
-}
-
 // 2^k as a float, for -126 <= k <= 127.
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 

@@ -169,7 +169,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
 }
 
 // ---- the two-CTA forms: a load counted on a barrier of either CTA, products of
-// 256 rows issued by CTA 0, commits to both.
+// 256 rows issued by CTA 0, commits to both (mla_device.cuh has the others).
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar_cluster) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
@@ -177,32 +177,10 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, 
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, int x, int y, uint32_t bar_cluster) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar_cluster)
-      : "memory");
-}
 template <bool kPair>
 __device__ __forceinline__ void commit(uint32_t bar) {
-  if constexpr (kPair)
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-  else
-    umma_commit(bar);
-}
-// Arrive on the barrier at this offset in CTA 0; orders nothing but TMEM
-// accesses that the caller has waited for and fenced (a release at cluster
-// scope waits for global stores on their way).
-__device__ __forceinline__ void arrive_leader_relaxed(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .b32 rb;\n\t"
-      "mapa.shared::cluster.u32 rb, %0, 0;\n\t"
-      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [rb];\n\t}" ::"r"(bar)
-      : "memory");
+  if constexpr (kPair) umma_commit2(bar);
+  else umma_commit(bar);
 }
 __device__ __forceinline__ void st_cluster_b32(uint32_t addr_cluster, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr_cluster), "r"(v) : "memory");
@@ -320,24 +298,6 @@ __device__ __noinline__ void store_columns(uint32_t taddr, float inv, T* dst, si
 template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& wc) {
   return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, wc));
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
-// After a wait has given up: the same bounded wait, blind to the abort flag,
-// for copies and products that are still in flight.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity))
-    if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) return;
 }
 
 template <bool kPair, bool kSolo>
@@ -634,8 +594,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       there = more && next.n > 0;
     };
     int k_landed = -1;                                        // the last key tile waited for
-    // A CTA of its own: its chain of products and softmax has no slack, and the loop below, which looks into the next
-    // item, takes 4% more there (16% a causal prompt of 4096 rows).
     // One row tile in every item: the scores of the next key tile are formed, in a second buffer, under the softmax
     // of this one.
     while (kSolo && ok) {
@@ -673,6 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (sh.n_a > 0) commit<kPair>(bar(bQFree));
       if (sh.n_b > 0) commit<kPair>(bar(bQFree + 1));
     };
+    // A CTA of its own: its chain of products and softmax has no slack, and the pairs' loop, which looks into the next
+    // item, takes 4% more there (16% a causal prompt of 4096 rows).
     while (!kPair && !kSolo && ok) {
       do look_ahead();
       while (more && !there);
@@ -760,9 +720,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           int tile = T + 1, left = nw - t - 1;                // row tile's key tiles from there on
           if (left <= 0) {
-            // The next item's keys lie in the ring beside what this one still needs: 10 of a pair's 16 blocks one
-            // tile before the last, 5 (of 8) in the last.
-            if (!there || (begun >> w & 1) || !(t + 1 == sh.n || (kPair && t + 2 == sh.n))) continue;
+            // The next item's keys lie in the ring beside what this one still needs: 10 of its 16 blocks one tile
+            // before the last.
+            if (!there || (begun >> w & 1) || t + 2 < sh.n) continue;
             begun |= 1u << w;
             tile = tbase + sh.n;
             left = w ? next.n_b : next.n_a;
@@ -899,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto arrive_p = [&](int b) {
       __syncwarp();
       if (lane == 0) {
-        if constexpr (kPair) arrive_leader_relaxed(bar(bPFull + b));
+        if constexpr (kPair) mbar_arrive_leader_relaxed(bar(bPFull + b));
         else mbar_arrive(bar(bPFull + b));
       }
     };

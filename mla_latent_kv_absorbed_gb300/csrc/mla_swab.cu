@@ -135,14 +135,6 @@ __device__ __forceinline__ bool item_in_request(const DecodeParams& p, int b, in
   return lo <= s && e <= hi;
 }
 
-// Bounded wait that ignores the abort flag (used to drain in-flight copies).
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) return;
-  }
-}
-
 // Max (or sum) over the 64 threads of a warp pair -- the two warps that hold
 // the same heads -- of v[i] for every i; both warps get the result.  `red` is
 // [2 bufs][2 pairs][2 warps][K]; `k` alternates the buffer.

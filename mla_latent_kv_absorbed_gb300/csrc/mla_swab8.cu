@@ -127,12 +127,6 @@ __device__ __forceinline__ bool item_in_request(const DecodeParams& p, int b, in
   const int lo = __ldg(p.kv_indptr + b), hi = __ldg(p.kv_indptr + b + 1);
   return lo <= s && e <= hi;
 }
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer() - t0 > MLA_WAIT_LIMIT_NS) return;
-  }
-}
 
 // Max (or sum) over the two warps of a pair of v[i] for every i (both warps
 // get the result); `red` is [2 bufs][2 pairs][2 warps][K].
