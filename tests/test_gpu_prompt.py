@@ -87,6 +87,22 @@ def test_rope_query(T, H, nope, interleaved, kw, amplitude, split):
 
 
 @pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("T,H,nope", [(100, 160, 128), (90, 130, 64), (5, 3, 2064), (3, 2, 65536), (700, 33, 200),
+                                      (80, 300, 8)])
+def test_rope_query_of_many_heads_and_wide_ones(T, H, nope, interleaved):
+    # units of 128 heads with a rest, blocks that take several, heads whose other part is wider than a block moves at once
+    torch, B = _t()
+    q, x = _normal(T + nope, T, H, nope + 64)
+    pos = np.random.default_rng(T).integers(0, 163840, T).astype(np.int32)
+    out = torch.full((T, H, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    rest = torch.full((T, H, nope), float("nan"), dtype=torch.bfloat16, device="cuda")
+    B.rope_query(q, torch.from_numpy(pos).cuda(), B.rope_frequencies(**YARN), out, q_nope=rest, interleaved=interleaved)
+    ref = P.rope_rotate(x[..., nope:], pos, _inv(YARN), interleaved)
+    _within(_f64(out), ref, _rope_bound(ref, x[..., nope:]), "rope")
+    assert torch.equal(rest, q[..., :nope])
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
 def test_rope_query_at_the_ends_of_the_positions(interleaved):
     torch, B = _t()
     pos = np.array([0, 1, -1, 2 ** 24 + 1, 2 ** 31 - 1, -2 ** 31], dtype=np.int32)
@@ -278,6 +294,40 @@ def test_rope_append_skips_and_reports_bad_slots(fp8):
     if not fp8:
         assert torch.equal(cache[7], rows[4])                   # position 0, no norm: the row itself
     call(None)                                                  # without a status word
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_rope_append_of_more_rows_than_warps(fp8, interleaved):
+    # a warp takes several rows, the next one's loads ahead, with slots outside the cache among them
+    torch, B = _t()
+    T, N, scale = 9001, 9500, 2.0 ** -5
+    rows, x = _normal(7, T, 576)
+    w, xw = _normal(8, 512)
+    rng = np.random.default_rng(9)
+    slots, pos = rng.permutation(N)[:T].astype(np.int32), rng.integers(0, 163840, T).astype(np.int32)
+    lost = rng.permutation(T)[:300]
+    slots[lost[:100]], slots[lost[100:200]], slots[lost[200:]] = -1, N, 2 ** 31 - 1
+    cache = torch.zeros((N, 576), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    args = (cache, torch.from_numpy(slots).cuda(), rows, torch.from_numpy(pos).cuda(), B.rope_frequencies(**YARN))
+    if fp8:
+        B.rope_append_kv_fp8(*args, scale, norm_weight=w, interleaved=interleaved, workspace=ws)
+    else:
+        B.rope_append_kv(*args, norm_weight=w, interleaved=interleaved, workspace=ws)
+    assert B.check_errors(ws) == 6
+    there = np.setdiff1d(np.arange(T), lost)
+    ref = P.append_values(x[there], pos[there], _inv(YARN), xw, 1e-6, interleaved)
+    slack = 2.0 ** -18 * np.abs(ref)                            # as in test_rope_append
+    slack[:, 512:] += 2.0 ** -19 * np.abs(x[there, 512:]).max(axis=1, keepdims=True) * 2
+    got = cache[torch.from_numpy(slots[there]).long().cuda()]
+    if fp8:
+        want = np.clip(ref / scale, -448, 448)
+        _within(_f64(got.view(torch.float8_e4m3fn)), want, np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -10) + slack / scale, "rows")
+    else:
+        _within(_f64(got), ref, BF * np.abs(ref) + slack, "rows")
+    rest = np.setdiff1d(np.arange(N), slots[there])
+    assert not cache[torch.from_numpy(rest).cuda()].any()
 
 
 @pytest.mark.parametrize("fp8", [False, True])
