@@ -618,8 +618,8 @@ int mla_expand_kv_fp8(const void* kv_cache, int64_t num_slots, float kv_scale, c
  *   num_sms, plan, plan_words, plan_words_needed, workspace_bytes: as for
  *   mla_decode_plan.
  * Errors: those of mla_decode_plan; any num_heads of 1 .. 65535 is supported;
- * MLA_ERR_UNSUPPORTED for 2^30 - 1 or more queries or keys, or more than
- * 2^31 - 2^16 - 1 tiles over all heads. */
+ * MLA_ERR_UNSUPPORTED for 2^30 - 1 or more queries or keys, more than 2^31 -
+ * 2^16 - 1 tiles over all heads, or 2^16 or more of them with their keys cut. */
 int mla_prefill_plan(const int32_t* q_indptr, const int32_t* kv_indptr, int32_t batch, int32_t num_heads,
                      int32_t causal, int32_t num_sms, int32_t* plan, size_t plan_words, size_t* plan_words_needed,
                      size_t* workspace_bytes);

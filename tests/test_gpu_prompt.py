@@ -950,6 +950,20 @@ def test_prefill_bad_device_plan_is_reported_not_followed():
         assert (out == 7).all(), (word, value)
 
 
+def test_prefill_bad_device_join_is_reported_not_followed():
+    # the entry of a cut tile's join: first row, rows, first piece, one past the last
+    torch, B = _t()
+    qp, kp = _indptr([100]), _indptr([1500])
+    (q, _), (k, _), (kr, _), (v, _) = _attention_inputs(4, 100, 1500, 2)
+    for word, value in ((0, -1), (0, 1), (1, 0), (1, 257), (2, -1), (2, 4), (3, 5), (3, 0)):
+        plan = _cut(B.Prefiller(qp, kp, 2), qp, kp, 2, True, 256, 4)
+        plan.plan_dev[16 + 8 * 4 + word] = value
+        out = torch.full((100, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        plan.run(q, k, kr, v, SM, out)
+        assert plan.check() == 7, (word, value)
+        assert (out == 7).all(), (word, value)
+
+
 @pytest.mark.parametrize("ql,kl,H,pairs", [([3, 100, 200], [3, 100, 200], 80, False), ([5], [40], 2, False),
                                            ([600, 100], [600, 100], 60, True), ([64] * 4, [300] * 4, 60, False)])
 @pytest.mark.parametrize("word,value", [(16, 5), (16, 1 << 20), (16, -3), (16, 2 ** 31 - 1), (17, -1), (17, 1 << 30),
