@@ -88,7 +88,8 @@ constexpr int kSched = 4;                             // items announced ahead
 // (3.2 tiles at most) is free only when a tile at most three before it has had its products, that tile is of a later
 // item than the notes, and its weights come from warps that are through with the items before.
 constexpr int kMasked = 8;
-constexpr int kConsumers = 16 + 1 + 2;                // warps that read an announced item (in CTA 1: no issuer, but the producer)
+constexpr int kConsumers = 4 + 1 + 2;                 // arrivals that give an announced item back: of the softmax warps one for a
+                                                      // row's four, issuer (in CTA 1: producer), guard
 enum Bar : int {
   bQFull = 0,                    // [2] per row tile
   bQFree = bQFull + 2,           // [2] the row tile's last scores of the item are done
@@ -874,10 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         Item it;
         const bool there = announced(k, it);
-        if (!there) {
-          release_item(k);
-          break;
-        }
+        if (!there) break;
         const Shape sh(it, kTileRows<kPair>);
         n_a = sh.n_a;
         n_b = sh.n_b;
@@ -969,9 +967,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
         } else if (t == nw) {
           // ------ the row tile's end: its output
-          // Across the pair the item's words are given back here, an item later: that release waits for the warp's
-          // output stores, which are done by now (right behind them it took 5% of the kernel's time, here under 1%).
-          if (kPair && w == 0 && k > 0) release_item(k - 1);
           Item it;
           announced(k, it);
           const Shape sh(it, kTileRows<kPair>);
@@ -995,6 +990,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ok = agree(ok);
           if (!ok) break;
+          // The words of the item before are given back: the row's four warps have read them.  Across the pair that
+          // release waits for the warp's output stores, which are done by now (right behind them it took 5% of the
+          // kernel's time).
+          if (w == 0 && k > 0 && quarter == 0) release_item(k - 1);
           const int row = row_a + kTileRows<kPair> * w;
           if (row - lane - 32 * quad < it.nq) {               // all warps of this CTA: they meet
             sum = all4(sum, [](float a, float b) { return a + b; });
@@ -1081,7 +1080,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Shape sh(it, kTileRows<kPair>);
         mbase += sh.n - sh.whole;
       }
-      if constexpr (!kPair) release_item(k);                  // the item's words have been read
     }
   }
   tc_fence_before();
