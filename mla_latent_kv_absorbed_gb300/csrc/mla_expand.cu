@@ -27,8 +27,8 @@
 // takes 4200 cycles (32 MMAs of 128), but late, 5500-6100 through most of the
 // kernel, as beside the rows there is room for six stages of 16 KB (four: 112 us,
 // five: 103, and the output stored through shared memory in the sixth's place).
-// 4096 rows x 128 heads take 98 us (1404 TFLOP/s, 0.74 of cuBLAS's rate), 8191
-// rows x 32 heads from E4M3 49 us, 257 rows x 16 heads 6.1 us.
+// 4096 rows x 128 heads take 97 us (1415 TFLOP/s, 0.71 of cuBLAS's rate), 8191
+// rows x 32 heads from E4M3 48 us, 257 rows x 16 heads 6.2 us.
 #include <type_traits>
 
 #include "mla_device.cuh"

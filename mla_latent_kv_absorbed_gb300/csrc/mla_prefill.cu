@@ -21,11 +21,13 @@
 // bits at any magnitude, sums are fp32), and O is rescaled in TMEM only then.
 //
 // A row tile's scores, weights and product follow one another (the weights lie
-// over the scores), so its key tile takes as long as that chain: 1300 cycles of
-// softmax (200 to load, 240 to vote on the reference, 800 for the weights: 20
-// exponentials a cycle, 150 to store), 250-600 until the issuer has seen it, 1280
-// of products, 500 until the next scores are seen - 3630 for a step of both row
-// tiles, of which 2580 are products.  All softmax warps take one row tile, then
+// over the scores), so its key tile takes as long as that chain.  Traced, the
+// softmax takes 250-300 cycles to load, mask and find the maximum, 130 to vote on
+// the reference, 710 for the weights (23 exponentials a cycle), 20 to hand them
+// over, and then waits for the other row tile's scores, 380 cycles in a causal
+// prompt of 4096 rows, 540 without a causal limit: 3540 for a step of both row
+// tiles (fitted over causal and ragged batches), about 4000 without a limit, of
+// which 2580 are products.  All softmax warps take one row tile, then
 // the other: four threads a row, whose quarter of a tile's scores stays in
 // registers.  With half of the warps on each (two threads a row, half a tile)
 // the long prompts took as long, but registers spilled and items' ends, which
@@ -35,21 +37,26 @@
 // Three forms, chosen by the plan:
 //   kPair   two CTAs of a cluster and 512 rows (cta_group::2: products of 256
 //           rows, CTA 0 issues).  Each CTA holds half of the keys and values,
-//           a step takes 3250 cycles for twice the rows, and the ring holds
+//           a step takes 3070 cycles for twice the rows, and the ring holds
 //           3.2 key tiles instead of 1.6; but an item's ends (first scores,
-//           epilogue, up to five partly seen tiles) cost 10000 cycles instead
-//           of 7300, and items are coarser.  4096 causal rows x 128 heads: 478
-//           us (1437 TFLOP/s) against 499 with single CTAs; 8192 x 64 heads
-//           827 against 892, without a causal limit 1538 against 1925; but
-//           1024 x 128 heads 66 against 61.
+//           epilogue, up to five partly seen tiles) cost 11400 cycles instead
+//           of 7800, and items are coarser.  us on pairs and on single CTAs:
+//             causal     1024 x 128 heads 69 and 60, 2048 x 128 163 and 158,
+//                        4096 x 128 502 and 514, 8192 x 64 889 and 949
+//             no limit   1024 x 128 91 and 91, 2048 x 128 239 and 270,
+//                        4096 x 128 887 and 1020, 8192 x 64 1671 and 1951
+//             keys cut   512 rows over 65536 x 16 heads 224 and 268, 1024 over
+//                        32768 x 32 466 and 530, 2048 over 16384 x 32 448 and 495
+//           (the SM clock between 1.75 and 2.07 GHz under the power cap; the
+//           long ones vary by 3% from run to run).
 //   kSolo   no item has more than 128 rows: one row tile, whose scores take
 //           turns in both score buffers (the next key tile's are formed under
 //           the softmax of this one), and the second tile's queries' place is
 //           ring (2.2 key tiles).  Bound by HBM: 64 rows over 65536 and 32064
-//           keys x 16 heads take 143 us (5.7 TB/s); with the general form,
-//           whose step of one row tile is the chain of 3080 cycles, 159; with
-//           two score buffers and the general form's ring 178.  (137 by now, with
-//           the joining kernel's loads four at a time and four threads a row.)
+//           keys x 16 heads take 137 us (5.9 TB/s), with the general form 155.
+//           From L2 a key tile takes 1930 cycles, the general form's step of one
+//           row tile, a chain without a second one beside it, 2740.  (Two score
+//           buffers with the general form's ring took 178 us where this took 143.)
 //
 // Warps: 0-15 softmax and epilogue, 16 TMA producer, 17 MMA issuer, 18-19 the
 // guard.  A tile that some row sees only in part is
@@ -269,8 +276,8 @@ __device__ __noinline__ void rescale_columns(uint32_t taddr, float f) {
 // thread's row.  Four lanes exchange blocks of 16 bytes, so that a store writes
 // 64 bytes of a row: `dst` is block lane & 3 of the first of their rows, `rows`
 // how many of the four there are.  Out of line for the same reason; with all its
-// registers free it takes 1700 cycles for 64 columns where 16 at a time in the
-// caller took 4500.
+// registers free 64 columns of two threads a row took 1700 cycles where 16 at a
+// time in the caller took 4500.
 template <typename T>
 __device__ __noinline__ void store_columns(uint32_t taddr, float inv, T* dst, size_t stride, int rows) {
   constexpr bool kHalf = sizeof(T) == 2;

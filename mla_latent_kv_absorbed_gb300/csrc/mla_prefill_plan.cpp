@@ -37,8 +37,11 @@ struct Piece {
 };
 
 // Costs in twentieths of a key tile against two row tiles of one CTA (a unit is
-// about 180 cycles; traced over causal and ragged batches): a partial output
-// written and read again, the joining kernel's launch.
+// about 180 cycles): a partial output written and read again, the joining
+// kernel's launch.  They were fitted to causal and ragged batches while two
+// threads shared a row of scores; beside each stands what the kernel takes with
+// four.  Both sides of the choice between the forms are measured in
+// mla_prefill.cu: at each size there the plan takes the faster one.
 constexpr long long kPieceCost = 8;
 constexpr long long kJoinCost = 24;
 constexpr long long kL2Bytes = 64ll << 20;
@@ -46,15 +49,15 @@ constexpr int kMostTiles = 1 << 17;   // of an item: a quarter of a second, well
 constexpr int kMostSms = 4096;        // planned for: more than any device has
 
 inline int key_tiles(int nk) { return (nk + kPfKeys - 1) / kPfKeys; }
-// A key tile: 3630 cycles against two row tiles; one has no other to fill its
-// softmax's time (3080).  A pair's two tiles of 256 rows take 3250, on two SMs
-// (counted lower: without a causal limit one CTA's take 4100).
+// A key tile: 3540 cycles against two row tiles (about 4000 without a causal
+// limit); one has no other to fill its softmax's time (2740).  A pair's two tiles
+// of 256 rows take 3070, on two SMs.
 inline long long tile_cost(int nq, int rows) {
   if (rows == kPfRows) return nq > rows / 2 ? 20 : 17;
   return nq > rows / 2 ? 17 : 16;
 }
 // An item's first loads and scores and its epilogue, as far as nothing fills
-// them: 7300 cycles, a pair's 10000.
+// them: 7800 cycles, a pair's 11400.
 inline long long item_cost(int rows) { return rows == kPfRows ? 40 : 54; }
 
 // Parts of a tile whose keys are cut into pieces of at most `cap` (0: as few as can be), none under four key tiles.

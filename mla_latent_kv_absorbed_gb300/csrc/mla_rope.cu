@@ -43,8 +43,8 @@ __device__ __forceinline__ void rotate(float& a, float& b, float2 cs) {
 // their way; each of its lanes keeps its pair's frequency in a register (read
 // from the parameters by lane it is a replay a lane, once a block).
 // Bound: HBM (the rotary part read and written once).  8191 tokens x 128 heads
-// take 43.9 us (6.1 TB/s, 0.90 of a plain copy's rate); 64 tokens x 128 heads
-// with the copy of the rest 2.8 us, which is a launch and a round trip.
+// take 44.0 us (6.1 TB/s, 0.91 of a plain copy's rate); 64 tokens x 128 heads
+// with the copy of the rest 2.9 us, which is a launch and a round trip.
 constexpr int kQThreads = 256;
 
 template <int J>
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kQThreads, 4) rope_query_kernel(const RopeQuer
 // replay a lane: at one row a warp that took as long as the rows).  A slot
 // outside [0, num_slots) is skipped and recorded.  Bound: HBM for long prompts,
 // else the launch and the dependent trip to the slot and back: 16384 rows take
-// 8.9 us (4.3 TB/s), 5000 rows into an E4M3 cache 4.3 us, 4 rows 1.9 us.
+// 9.0 us (4.2 TB/s), 5000 rows into an E4M3 cache 4.3 us, 4 rows 2.0 us.
 constexpr int kAThreads = 256;
 
 constexpr int kABlocks = 3;      // blocks an SM holds: a row being worked on and the next one on its way a warp
