@@ -721,7 +721,8 @@ class Decoder:
 
 class Prefiller:
     """Convenience holder: plan a batch's prompt attention once, then run it on device tensors.  Ready on every stream
-    once it is made; its runs share one workspace, so they follow one another (on one stream, or ordered by events)."""
+    once it is made; its runs share one workspace, so they follow one another (on one stream, or ordered by events).  It
+    may be dropped while a torch stream still runs it; one made elsewhere (a handle, an ExternalStream) has to be done."""
 
     def __init__(self, q_indptr_host, kv_indptr_host, num_heads: int, causal: bool = True, device="cuda",
                  num_sms: int = 0):
@@ -734,12 +735,15 @@ class Prefiller:
         self._streams = {home.cuda_stream}
 
     def run(self, q, k_nope, k_rope, v, sm_scale, out, lse=None, stream=None):
-        handle = _current(stream)[1]
-        if handle not in self._streams:              # the allocator keeps plan and workspace until its work is done
+        cur, handle = _current(stream)
+        if handle not in self._streams:
             import torch
-            where = torch.cuda.ExternalStream(handle, device=self.workspace.device)
-            for t in (self.plan_dev, self.workspace):
-                t.record_stream(where)
+            where = torch.cuda.current_stream(cur) if stream is None else stream
+            # The allocator keeps plan and workspace until a stream of torch's own is done with them.  It may not be told
+            # of a stream that others made (torch numbers it by its handle): that may be gone when they are freed.
+            if isinstance(where, torch.cuda.Stream) and (handle == 0 or where.stream_id != handle):
+                for t in (self.plan_dev, self.workspace):
+                    t.record_stream(where)
             self._streams.add(handle)
         prefill_run(self.plan_host, self.plan_dev, q, k_nope, k_rope, v, sm_scale, out, lse, self.workspace, handle)
 

@@ -1061,6 +1061,33 @@ def test_prefiller_dropped_before_its_work_is_done():
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("how", ["handle", "given", "current"])
+def test_prefiller_outlives_a_stream_made_elsewhere(how):
+    # such a stream may be destroyed once its work is done: nothing is recorded on it when the memory is given back
+    import ctypes
+    torch, B = _t()
+    qp, kp = _indptr([3]), _indptr([4000])
+    (q, _), (k, _), (kr, _), (v, _) = _attention_inputs(24, 3, 4000, 2)
+    want, _ = _attend(B.Prefiller(qp, kp, 2), q, k, kr, v)
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    raw = ctypes.c_void_p()
+    assert int(torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(raw))) == 0
+    plan = B.Prefiller(qp, kp, 2)
+    other = torch.cuda.ExternalStream(raw.value)
+    if how == "current":
+        with torch.cuda.stream(other):
+            plan.run(q, k, kr, v, SM, out)
+    else:
+        plan.run(q, k, kr, v, SM, out, stream=raw.value if how == "handle" else other)
+    other.synchronize()
+    assert torch.equal(out, want)
+    assert int(torch.cuda.cudart().cudaStreamDestroy(raw.value)) == 0
+    del plan
+    assert B.Prefiller(qp, kp, 2).check() == 0
+    torch.cuda.synchronize()
+
+
 def test_two_prefills_at_once_with_their_own_workspaces():
     torch, B = _t()
     qp, kp = _indptr([5]), _indptr([4000])
