@@ -479,6 +479,27 @@ int mla_decode_run_fp8(const int32_t* plan_host, const int32_t* plan_dev, const 
 int mla_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slots, const void* rows, int32_t batch,
                       float kv_scale, void* workspace, void* stream);
 
+/* ---- FP8 latent cache with a scale for every row -------------------------
+ * The same 576 codes a row, and a float32 scale for every page of the cache
+ * (a page is one row, shared by all heads): value = code value x
+ * kv_scales[slot].  A loud token then neither clips nor coarsens the others, and
+ * nothing has to be calibrated.  Rows are written by mla_rope_append_kv_fp8_rows
+ * (further down, with mla_expand_kv_fp8_rows).  Readers take a scale outside
+ * [2^-64, 2^64] as the nearer end, a NaN as 2^-64. */
+
+/* mla_decode_run_fp8_rows -- asynchronous on `stream`.
+ *
+ * mla_decode_run_fp8 over such a cache.
+ *   kv_scales  device float32 [num_slots], 4-byte aligned; read at the slots
+ *              that kv_indices names (at slot 0 for one outside the cache).
+ *   all other arguments, plan, workspace and launches as for mla_decode_run_fp8.
+ * Errors as for mla_decode_run_fp8, and MLA_ERR_INVALID_ARG for a null or
+ * misaligned kv_scales (not looked at when no request has a row). */
+int mla_decode_run_fp8_rows(const int32_t* plan_host, const int32_t* plan_dev, const void* q_nope, const void* q_rope,
+                            const void* kv_cache, int64_t num_slots, const float* kv_scales, const int32_t* kv_indptr,
+                            const int32_t* kv_indices, float sm_scale, void* out, int32_t out_dtype, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- the prompt side ------------------------------------------------------
  * What stands before the decode: rotary positions, a row's way into the cache,
  * and a prompt's attention in the EXPANDED form (per-head keys and values made
@@ -573,6 +594,17 @@ int mla_rope_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slo
                            float eps, const uint64_t* freqs, float amplitude, int32_t interleaved, float kv_scale,
                            void* workspace, void* stream);
 
+/* mla_rope_append_kv_fp8_rows -- the same into a cache with a scale for every
+ * row: with m = the largest magnitude of the row's 576 fp32 values (a NaN is not
+ * counted), kv_scales[slot] = m / 448 kept inside [2^-64, 2^64], and the codes
+ * are those of value x (1 / kv_scales[slot]), rounded once, magnitudes past 448
+ * to 448.  A row of zeros gets the scale 2^-64.
+ *   kv_scales  device float32 [num_slots], 4-byte aligned, written at the slots. */
+int mla_rope_append_kv_fp8_rows(void* kv_cache, float* kv_scales, int64_t num_slots, const int32_t* slots,
+                                const void* rows, int64_t row_stride, const int32_t* positions, int32_t tokens,
+                                const void* norm_weight, float eps, const uint64_t* freqs, float amplitude,
+                                int32_t interleaved, void* workspace, void* stream);
+
 /* mla_expand_kv -- asynchronous on `stream`.
  *
  * Per-head keys and values of cached rows: with c_t = the latent of row
@@ -602,6 +634,13 @@ int mla_expand_kv(const void* kv_cache, int64_t num_slots, const int32_t* kv_ind
 int mla_expand_kv_fp8(const void* kv_cache, int64_t num_slots, float kv_scale, const int32_t* kv_indices,
                       int32_t tokens, const void* w_kc, const void* w_vc, int32_t num_heads, void* k_nope,
                       void* k_rope, void* v, void* workspace, void* stream);
+
+/* mla_expand_kv_fp8_rows -- the same from a cache with a scale for every row:
+ * kv_scales device float32 [num_slots], 4-byte aligned; each token's fp32 sums
+ * are multiplied by its row's scale. */
+int mla_expand_kv_fp8_rows(const void* kv_cache, const float* kv_scales, int64_t num_slots, const int32_t* kv_indices,
+                           int32_t tokens, const void* w_kc, const void* w_vc, int32_t num_heads, void* k_nope,
+                           void* k_rope, void* v, void* workspace, void* stream);
 
 /* mla_prefill_plan -- host only, no device work, deterministic.
  *
@@ -660,6 +699,152 @@ int mla_prefill_run(const int32_t* plan_host, const int32_t* plan_dev, const voi
                     const void* k_rope, int64_t k_rope_stride, const void* v, int64_t v_token_stride,
                     int64_t v_head_stride, float sm_scale, void* out, float* lse, void* workspace,
                     size_t workspace_bytes, void* stream);
+
+/* ---- between two steps ----------------------------------------------------
+ * What a speculative serving step does once the target has scored its drafts
+ * (mla_decode_run_multi_query, mla_decode_run_tree): decide which drafts hold,
+ * cut the requests' lists of rows to them, fork and free requests, and keep the
+ * pool of rows in order.  All of it stays on the device, without a host copy or
+ * an allocation, and can be captured. */
+
+/* mla_verify_drafts -- asynchronous on `stream`.
+ *
+ * The walk down each request's drafts ("[sglang] EAGLE 트리 검증 어텐션
+ * 최적화", section "들어가며"), from given random numbers.  Draft 0 is the token
+ * that the last step ended with: it stands, and target row i is the target's
+ * distribution of the token after draft i (what the W = q_len queries of a
+ * multi-query or tree decode give).  With node = 0 at first, the node's children
+ * c are tried in their order:
+ *   sampled drafts (draft_probs; a chain): accepted when u_c q_c(x_c) < t(x_c),
+ *       q_c = the draft row c, which draft c was drawn from;
+ *   chosen drafts (no draft_probs; a chain or a tree): accepted when
+ *       u_c (1 - the t of the node's rejected children so far) < t(x_c); a child
+ *       whose token a rejected sibling had counts t = 0;
+ * with t = the node's target row, x = tokens, u = uniforms.  An accepted child
+ * is the next node; without one the walk ends.  Of what is left of the node's
+ * row,
+ *   r_v = max(t_v - q_v, 0) after a rejected sampled draft, t_v off the rejected
+ *         children's tokens for chosen ones, t_v where nothing was rejected,
+ * the next token is the lowest v with sum_(w <= v) r_w > u_0 sum_w r_w, or -1
+ * when nothing is left.  The comparisons are made in 64 bits and the sums are
+ * good to about 2^-45 of the whole; entries are probabilities: values outside
+ * [0, 1] count as the nearer end, NaN as 0.  With u_0 >= 1 or NaN the token is
+ * the last one with r > 0; u_c is taken as 0 when it is negative or NaN.
+ *   target_probs   device fp32: row i of request b at + b*target_batch_stride +
+ *                  i*target_row_stride, vocab values together.  Strides in
+ *                  elements, 0 .. 2^40 - 1.
+ *   draft_probs    NULL, or device fp32 likewise (row 0 is not looked at).
+ *   tokens         device int32 [batch, q_len].  A token of a draft other than
+ *                  the first outside [0, vocab) is not accepted, and recorded as
+ *                  MLA_ERR_INDEX_OOB.
+ *   tree_parents   NULL (a chain: draft i extends draft i - 1), or device int32
+ *                  [batch, q_len] as for mla_decode_run_tree: parents[0] = -1, an
+ *                  earlier draft for the others.  -1 for another than the first
+ *                  is a draft that nothing reaches; any other entry outside
+ *                  [-1, i) is one too, and recorded as MLA_ERR_TREE.
+ *   uniforms       device fp32 [batch, q_len], in [0, 1): entry 0 draws the next
+ *                  token, entry c decides on draft c.
+ *   path           device int32 [batch, q_len], written: the accepted drafts in
+ *                  their order (the first is 0), then -1.
+ *   accepted       device int32 [batch], written: how many (at least 1).
+ *   next_token     device int32 [batch], written.
+ *   workspace      NULL, or a workspace (its status word).
+ * Pointers are 4-byte aligned (workspace 16); outputs apart from the inputs.
+ * Errors: MLA_ERR_INVALID_ARG for bad pointers, sizes or strides;
+ * MLA_ERR_UNSUPPORTED for q_len > 64 and for draft_probs with tree_parents.
+ * Nothing is launched then, nor for batch == 0. */
+int mla_verify_drafts(const float* target_probs, int64_t target_batch_stride, int64_t target_row_stride,
+                      const float* draft_probs, int64_t draft_batch_stride, int64_t draft_row_stride,
+                      const int32_t* tokens, const int32_t* tree_parents, const float* uniforms, int32_t batch,
+                      int32_t q_len, int32_t vocab, int32_t* path, int32_t* accepted, int32_t* next_token,
+                      void* workspace, void* stream);
+
+/* mla_slots_workspace_bytes -- host.  Workspace of the calls below for a pool of
+ * num_slots rows (0 for a num_slots outside 1 .. 2^31 - 1).  Zero-filled before
+ * its first use; a status word as for mla_decode_run, and a set of slots that is
+ * empty between calls, so that calls that share one must not overlap on the GPU.
+ * One made for more slots serves a smaller pool as well. */
+size_t mla_slots_workspace_bytes(int64_t num_slots);
+
+/* mla_repack_requests -- asynchronous on `stream`.
+ *
+ * The lists of rows of the next step's requests: request r continues request
+ * sources[r] of the old lists (any number may continue the same: forks; what
+ * none continues is freed; -1 starts with no rows).  With path and accepted
+ * (mla_verify_drafts), the last q_len rows of an old request are its drafts, and
+ * its successors keep the rows before them and the accepted drafts' rows, in
+ * the path's order; without, all rows.
+ *   kv_indptr, kv_indices  device int32 [batch + 1], [entries].
+ *   sources     device int32 [new_batch].
+ *   path, accepted  both NULL, or device int32 [batch, q_len] and [batch].
+ *   new_indptr, new_indices  device int32 [new_batch + 1], [capacity], written;
+ *               entries of new_indices past the last list are left as they were.
+ *   freed, freed_count  both NULL, or device int32 [freed_capacity] and [1],
+ *               written: the slots of the old lists that no new list holds,
+ *               ascending, and their number; entries past them are left as they
+ *               were.
+ *   num_slots   rows of the pool.   workspace  of mla_slots_workspace_bytes.
+ * Bad contents are recorded (mla_check_errors), never followed:
+ * MLA_ERR_PLAN_MISMATCH for a source outside [-1, batch) (taken as -1), a
+ * kv_indptr that leaves [0, entries] or falls (clipped), a request with fewer
+ * rows than drafts (kept whole); MLA_ERR_TREE for an accepted or path entry out
+ * of range (clipped); MLA_ERR_INDEX_OOB for a slot outside the pool (copied, and
+ * freed by no one; looked for only with freed); MLA_ERR_WORKSPACE when a list
+ * passes capacity, or the freed slots freed_capacity (the rest is not written).
+ * Pointers are 4-byte aligned (workspace 16); outputs apart from the inputs.
+ * Errors: MLA_ERR_INVALID_ARG for bad pointers or sizes, one of a pair without
+ * the other; MLA_ERR_UNSUPPORTED for q_len > 64 (with path);
+ * MLA_ERR_WORKSPACE for too small a workspace.  Nothing is launched then. */
+int mla_repack_requests(const int32_t* kv_indptr, const int32_t* kv_indices, int64_t entries, int32_t batch,
+                        const int32_t* sources, int32_t new_batch, const int32_t* path, const int32_t* accepted,
+                        int32_t q_len, int32_t* new_indptr, int32_t* new_indices, int64_t capacity, int64_t num_slots,
+                        int32_t* freed, int64_t freed_capacity, int32_t* freed_count, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* mla_copy_rows -- asynchronous on `stream`.
+ *
+ * dst[l, dst_slots[i]] = src[l, src_slots[i]] for i < rows and l < layers: rows
+ * of any of the caches here, in all layers at once, with their scales.
+ *   src_cache, dst_cache  device, row s of layer l at byte (l * layer_rows + s) *
+ *               row_bytes; row_bytes 1152 (bf16) or 576 (FP8).  They may be the
+ *               same, when no destination is also a source.
+ *   src_scales, dst_scales  both NULL, or device fp32 [layers, layer_rows] (FP8
+ *               rows with a scale each).
+ *   src_num_slots, dst_num_slots  slots of a layer; layer_rows at least as many
+ *               (not looked at for one layer).
+ *   src_slots, dst_slots  device int32 [rows]; destinations distinct (of two
+ *               rows to one slot any part of either may win).  A pair with a slot
+ *               out of range is skipped, and recorded as MLA_ERR_INDEX_OOB.
+ *   workspace   NULL, or a workspace (its status word).
+ * Caches and workspace are 16-byte aligned, the rest 4.
+ * Errors: MLA_ERR_INVALID_ARG; MLA_ERR_UNSUPPORTED for another row_bytes.
+ * Nothing is launched then, nor for rows == 0 or layers == 0. */
+int mla_copy_rows(const void* src_cache, const float* src_scales, int64_t src_num_slots, int64_t src_layer_rows,
+                  const int32_t* src_slots, void* dst_cache, float* dst_scales, int64_t dst_num_slots,
+                  int64_t dst_layer_rows, const int32_t* dst_slots, int32_t rows, int32_t layers, int32_t row_bytes,
+                  void* workspace, void* stream);
+
+/* mla_compact_cache -- asynchronous on `stream`.
+ *
+ * Moves the rows that lists name into the lowest slots of the pool, in all
+ * layers, and rewrites the lists: with n distinct live slots, the k-th live slot
+ * from n on (ascending) goes to the k-th free slot below n; what lies below n
+ * stays.  Slots n .. num_slots - 1 are free afterwards (their rows as they were).
+ *   kv_cache, kv_scales, layer_rows, layers, row_bytes  as for mla_copy_rows.
+ *   kv_indptr   device int32 [batch + 1]: its last entry, at most `entries`, is
+ *               how much of kv_indices is live (the lists of mla_repack_requests
+ *               as they are).
+ *   kv_indices, new_indices  device int32 [entries]; new_indices is written up
+ *               to the last list, and may be kv_indices itself.  A slot outside
+ *               the pool is recorded as MLA_ERR_INDEX_OOB and kept.
+ *   live_count  device int32 [1], written: n.
+ *   workspace   of mla_slots_workspace_bytes(num_slots).
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (row_bytes),
+ * MLA_ERR_WORKSPACE; nothing is launched then. */
+int mla_compact_cache(void* kv_cache, float* kv_scales, int64_t num_slots, int64_t layer_rows, int32_t layers,
+                      int32_t row_bytes, const int32_t* kv_indptr, int32_t batch, const int32_t* kv_indices,
+                      int64_t entries, int32_t* new_indices, int32_t* live_count, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* mla_check_errors -- synchronises `stream`, reads the workspace status word,
  * clears it, and returns it (MLA_OK when the kernels found nothing wrong), or

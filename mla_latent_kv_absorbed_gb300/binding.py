@@ -29,7 +29,9 @@ EXPORTS = ("mla_status_string", "mla_abi_version", "mla_decode_plan", "mla_decod
            "mla_merge_two_states", "mla_decode_fp8_workspace_bytes", "mla_decode_run_fp8", "mla_append_kv_fp8",
            "mla_decode_graph_sizes", "mla_decode_run_graph", "mla_noalloc_check_errors", "mla_decode_run_tree",
            "mla_probe_wait_limit", "mla_rope_frequencies", "mla_rope_query", "mla_rope_append_kv",
-           "mla_rope_append_kv_fp8", "mla_expand_kv", "mla_expand_kv_fp8", "mla_prefill_plan", "mla_prefill_run")
+           "mla_rope_append_kv_fp8", "mla_expand_kv", "mla_expand_kv_fp8", "mla_prefill_plan", "mla_prefill_run",
+           "mla_decode_run_fp8_rows", "mla_rope_append_kv_fp8_rows", "mla_expand_kv_fp8_rows", "mla_verify_drafts",
+           "mla_slots_workspace_bytes", "mla_repack_requests", "mla_copy_rows", "mla_compact_cache")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 if not os.path.exists(LIB_PATH):
@@ -118,6 +120,26 @@ _lib.mla_prefill_plan.argtypes = [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _sz, _c
 _lib.mla_prefill_run.restype = ctypes.c_int
 _lib.mla_prefill_run.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _f32, _vp,
                                  _vp, _vp, _sz, _vp]
+_lib.mla_decode_run_fp8_rows.restype = ctypes.c_int
+_lib.mla_decode_run_fp8_rows.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _f32, _vp, _i32, _vp, _vp, _sz,
+                                         _vp]
+_lib.mla_rope_append_kv_fp8_rows.restype = ctypes.c_int
+_lib.mla_rope_append_kv_fp8_rows.argtypes = [_vp, _vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _f32, _vp, _f32, _i32, _vp,
+                                             _vp]
+_lib.mla_expand_kv_fp8_rows.restype = ctypes.c_int
+_lib.mla_expand_kv_fp8_rows.argtypes = [_vp, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp]
+_lib.mla_verify_drafts.restype = ctypes.c_int
+_lib.mla_verify_drafts.argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                   _vp]
+_lib.mla_slots_workspace_bytes.restype = _sz
+_lib.mla_slots_workspace_bytes.argtypes = [_i64]
+_lib.mla_repack_requests.restype = ctypes.c_int
+_lib.mla_repack_requests.argtypes = [_vp, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _i64, _i64, _vp, _i64,
+                                     _vp, _vp, _sz, _vp]
+_lib.mla_copy_rows.restype = ctypes.c_int
+_lib.mla_copy_rows.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i32, _i32, _i32, _vp, _vp]
+_lib.mla_compact_cache.restype = ctypes.c_int
+_lib.mla_compact_cache.argtypes = [_vp, _vp, _i64, _i64, _i32, _i32, _vp, _i32, _vp, _i64, _vp, _vp, _vp, _sz, _vp]
 
 
 class MLAError(RuntimeError):
@@ -170,7 +192,7 @@ def decode_plan(kv_indptr_host, num_heads: int, num_sms: int = 0):
     return plan, int(ws.value)
 
 
-_H_BATCH, _H_WORKERS, _H_ITEMS = 2, 6, 8      # plan header words (include/mla_decode.h)
+_H_BATCH, _H_HEADS, _H_WORKERS, _H_ITEMS = 2, 3, 6, 8      # plan header words (include/mla_decode.h)
 
 
 def plan_nnz(plan_host) -> int:
@@ -348,6 +370,42 @@ def decode_run_fp8(plan_host, plan_dev, q_nope, q_rope, kv_cache, kv_scale, kv_i
                                  int(workspace.numel() * workspace.element_size()), _stream_handle(stream))
     if st != MLA_OK:
         raise MLAError(st, "mla_decode_run_fp8")
+
+
+def decode_run_fp8_rows(plan_host, plan_dev, q_nope, q_rope, kv_cache, kv_scales, kv_indptr, kv_indices, sm_scale, out,
+                        lse, workspace, stream=None) -> None:
+    """Decode over an FP8 cache with a scale for every row: kv_cache uint8 [num_slots, 576] E4M3 codes, kv_scales
+    float32 [num_slots] (value = code x kv_scales[slot]); other tensors as for decode_run, in their types and shapes;
+    workspace of decode_fp8_workspace_bytes(plan) bytes, zero-filled once."""
+    import torch
+    w = "mla_decode_run_fp8_rows"
+    plan_host = np.ascontiguousarray(plan_host, dtype=np.int32)
+    if plan_host.size < 16:
+        raise ValueError(f"{w}: plan_host is the int32 array of decode_plan")
+    _check_csr(plan_host, kv_indptr, kv_indices, w)
+    B, H = int(plan_host[_H_BATCH]), int(plan_host[_H_HEADS])
+    N = _sizes(w, "kv_cache", kv_cache, 2)[0]
+    _need(w, "plan_dev", plan_dev, torch.int32, (plan_host.size,))
+    _need(w, "q_nope", q_nope, torch.bfloat16, (B, H, 512))
+    _need(w, "q_rope", q_rope, torch.bfloat16, (B, H, 64))
+    _need(w, "kv_cache", kv_cache, torch.uint8, (N, 576))
+    _need(w, "kv_scales", kv_scales, torch.float32, (N,))
+    _need(w, "kv_indptr", kv_indptr, torch.int32, (B + 1,))
+    if kv_indices is not None:
+        _need(w, "kv_indices", kv_indices, torch.int32, (kv_indices.numel(),))
+    out_dtype = _out_dtype(out, w)
+    _need(w, "out", out, out.dtype, (B, H, 512))
+    if lse is not None:
+        _need(w, "lse", lse, torch.float32, (B, H))
+    _need(w, "workspace", workspace, torch.uint8, (workspace.numel(),))
+    st = _launch_stream(w, stream, plan_dev, q_nope, q_rope, kv_cache, kv_scales, kv_indptr, kv_indices, out, lse,
+                        workspace)
+    st = _lib.mla_decode_run_fp8_rows(plan_host.ctypes.data, plan_dev.data_ptr(), q_nope.data_ptr(), q_rope.data_ptr(),
+                                      kv_cache.data_ptr(), N, kv_scales.data_ptr(), kv_indptr.data_ptr(),
+                                      _ptr(kv_indices), float(sm_scale), out.data_ptr(), out_dtype, _ptr(lse),
+                                      workspace.data_ptr(), workspace.numel(), st)
+    if st != MLA_OK:
+        raise MLAError(st, w)
 
 
 def append_kv_fp8(kv_cache, slots, rows, kv_scale, workspace=None, stream=None) -> None:
@@ -533,7 +591,8 @@ def rope_query(q, positions, freqs, q_rope, q_nope=None, amplitude: float = 1.0,
         raise MLAError(st, w)
 
 
-def _rope_append(w, cache_dtype, kv_cache, slots, rows, positions, freqs, norm_weight, workspace, stream):
+def _rope_append(w, cache_dtype, kv_cache, slots, rows, positions, freqs, norm_weight, workspace, stream,
+                 kv_scales=None):
     import torch
     _status_word(w, workspace)
     T = _sizes(w, "rows", rows, 2)[0]
@@ -545,7 +604,7 @@ def _rope_append(w, cache_dtype, kv_cache, slots, rows, positions, freqs, norm_w
     if norm_weight is not None:
         _need(w, "norm_weight", norm_weight, torch.bfloat16, (512,))
     return (N, T, rows.stride(0), _freqs_ptr(w, freqs),
-            _launch_stream(w, stream, kv_cache, rows, slots, positions, norm_weight, workspace))
+            _launch_stream(w, stream, kv_cache, rows, slots, positions, norm_weight, workspace, kv_scales))
 
 
 def rope_append_kv(kv_cache, slots, rows, positions, freqs, norm_weight=None, eps: float = 1e-6,
@@ -577,7 +636,24 @@ def rope_append_kv_fp8(kv_cache, slots, rows, positions, freqs, kv_scale, norm_w
         raise MLAError(st, w)
 
 
-def _expand(w, cache_dtype, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace, stream):
+def rope_append_kv_fp8_rows(kv_cache, kv_scales, slots, rows, positions, freqs, norm_weight=None, eps: float = 1e-6,
+                            amplitude: float = 1.0, interleaved: bool = True, workspace=None, stream=None) -> None:
+    """rope_append_kv into an FP8 cache with a scale for every row: uint8 [num_slots, 576] E4M3 codes and float32
+    kv_scales [num_slots], the row's largest magnitude / 448 (value = code x scale)."""
+    import torch
+    w = "mla_rope_append_kv_fp8_rows"
+    N, T, rs, fr, st = _rope_append(w, torch.uint8, kv_cache, slots, rows, positions, freqs, norm_weight, workspace,
+                                    stream, kv_scales)
+    _need(w, "kv_scales", kv_scales, torch.float32, (N,))
+    st = _lib.mla_rope_append_kv_fp8_rows(kv_cache.data_ptr(), kv_scales.data_ptr(), N, slots.data_ptr(),
+                                          rows.data_ptr(), rs, positions.data_ptr(), T, _ptr(norm_weight), eps, fr,
+                                          amplitude, 1 if interleaved else 0, _ptr(workspace), st)
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
+def _expand(w, cache_dtype, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace, stream,
+            kv_scales=None):
     import torch
     _status_word(w, workspace)
     bf = torch.bfloat16
@@ -591,7 +667,7 @@ def _expand(w, cache_dtype, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v,
     _need(w, "k_nope", k_nope, bf, (T, H, 128))
     _need(w, "k_rope", k_rope, bf, (T, 64))
     _need(w, "v", v, bf, (T, H, 128))
-    return N, T, H, _launch_stream(w, stream, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace)
+    return N, T, H, _launch_stream(w, stream, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace, kv_scales)
 
 
 def expand_kv(kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace=None, stream=None) -> None:
@@ -615,6 +691,21 @@ def expand_kv_fp8(kv_cache, kv_scale, kv_indices, w_kc, w_vc, k_nope, k_rope, v,
     st = _lib.mla_expand_kv_fp8(kv_cache.data_ptr(), N, kv_scale, kv_indices.data_ptr(), T, w_kc.data_ptr(),
                                 w_vc.data_ptr(), H, k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(),
                                 _ptr(workspace), st)
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
+def expand_kv_fp8_rows(kv_cache, kv_scales, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace=None,
+                       stream=None) -> None:
+    """expand_kv from an FP8 cache with a scale for every row: float32 kv_scales [num_slots]."""
+    import torch
+    w = "mla_expand_kv_fp8_rows"
+    N, T, H, st = _expand(w, torch.uint8, kv_cache, kv_indices, w_kc, w_vc, k_nope, k_rope, v, workspace, stream,
+                          kv_scales)
+    _need(w, "kv_scales", kv_scales, torch.float32, (N,))
+    st = _lib.mla_expand_kv_fp8_rows(kv_cache.data_ptr(), kv_scales.data_ptr(), N, kv_indices.data_ptr(), T,
+                                     w_kc.data_ptr(), w_vc.data_ptr(), H, k_nope.data_ptr(), k_rope.data_ptr(),
+                                     v.data_ptr(), _ptr(workspace), st)
     if st != MLA_OK:
         raise MLAError(st, w)
 
@@ -667,6 +758,164 @@ def prefill_run(plan_host, plan_dev, q, k_nope, k_rope, v, sm_scale: float, out,
     st = _lib.mla_prefill_run(_host_ptr(plan_host), plan_dev.data_ptr(), q.data_ptr(), qt, qh, k_nope.data_ptr(), kt,
                               kh, k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), vt, vh, sm_scale,
                               out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), st)
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
+# ---- between two steps: drafts verified, lists of rows rewritten, rows moved ----
+
+def verify_drafts(target_probs, tokens, uniforms, path, accepted, next_token, draft_probs=None, parents=None,
+                  workspace=None, stream=None) -> None:
+    """Which drafts of a speculative step hold, and the token that follows them: target_probs fp32 [B, W, V] (row i:
+    the distribution after draft i; draft 0 is the last token itself), tokens int32 and uniforms fp32 [B, W] (entry 0
+    draws the next token) -> path int32 [B, W] (accepted drafts, then -1), accepted and next_token int32 [B].
+    draft_probs fp32 [B, W, V]: what the drafts of a chain were sampled from; parents int32 [B, W]: a tree of chosen
+    drafts; neither: a chain of chosen drafts.  Batch and row strides are free, the vocabulary lies together."""
+    import torch
+    w = "mla_verify_drafts"
+    _status_word(w, workspace)
+    f32, i32 = torch.float32, torch.int32
+    B, W, V = _sizes(w, "target_probs", target_probs, 3)
+    _need(w, "target_probs", target_probs, f32, (B, W, V), dense=False)
+    _need(w, "tokens", tokens, i32, (B, W))
+    _need(w, "uniforms", uniforms, f32, (B, W))
+    _need(w, "path", path, i32, (B, W))
+    _need(w, "accepted", accepted, i32, (B,))
+    _need(w, "next_token", next_token, i32, (B,))
+    db = dr = 0
+    if draft_probs is not None:
+        _need(w, "draft_probs", draft_probs, f32, (B, W, V), dense=False)
+        db, dr, _ = draft_probs.stride()
+    if parents is not None:
+        _need(w, "parents", parents, i32, (B, W))
+    st = _launch_stream(w, stream, target_probs, tokens, uniforms, path, accepted, next_token, draft_probs, parents,
+                        workspace)
+    tb, tr, _ = target_probs.stride()
+    st = _lib.mla_verify_drafts(target_probs.data_ptr(), tb, tr, _ptr(draft_probs), db, dr, tokens.data_ptr(),
+                                _ptr(parents), uniforms.data_ptr(), B, W, V, path.data_ptr(), accepted.data_ptr(),
+                                next_token.data_ptr(), _ptr(workspace), st)
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
+def slots_workspace_bytes(num_slots: int) -> int:
+    """Workspace bytes of repack_requests and compact_cache for a pool of num_slots rows (zero-filled once)."""
+    n = int(_lib.mla_slots_workspace_bytes(int(num_slots)))
+    if n == 0:
+        raise MLAError(1, "mla_slots_workspace_bytes")
+    return n
+
+
+def repack_requests(kv_indptr, kv_indices, sources, new_indptr, new_indices, num_slots: int, workspace, path=None,
+                    accepted=None, freed=None, freed_count=None, stream=None) -> None:
+    """The lists of the next step's requests: request r continues request sources[r] (int32 [B'], -1: no rows) of
+    kv_indptr int32 [B + 1] / kv_indices int32, with path int32 [B, W] and accepted int32 [B] of verify_drafts cut to
+    the accepted of its last W rows -> new_indptr int32 [B' + 1], new_indices int32 (its size is the room).  freed
+    int32 and freed_count int32 [1] take the slots that no new list holds, ascending, and their number."""
+    import torch
+    w, i32 = "mla_repack_requests", torch.int32
+    B1 = _sizes(w, "kv_indptr", kv_indptr, 1)[0]
+    N1 = _sizes(w, "sources", sources, 1)[0]
+    if B1 < 1:
+        raise ValueError(f"{w}: kv_indptr must hold batch + 1 entries")
+    _need(w, "kv_indptr", kv_indptr, i32, (B1,))
+    _need(w, "kv_indices", kv_indices, i32, (kv_indices.numel(),))
+    _need(w, "sources", sources, i32, (N1,))
+    _need(w, "new_indptr", new_indptr, i32, (N1 + 1,))
+    _need(w, "new_indices", new_indices, i32, (new_indices.numel(),))
+    _need(w, "workspace", workspace, torch.uint8, (workspace.numel(),))
+    W = 0
+    if (path is None) != (accepted is None) or (freed is None) != (freed_count is None):
+        raise ValueError(f"{w}: path goes with accepted, freed with freed_count")
+    if path is not None:
+        W = _sizes(w, "path", path, 2)[1]
+        _need(w, "path", path, i32, (B1 - 1, W))
+        _need(w, "accepted", accepted, i32, (B1 - 1,))
+    if freed is not None:
+        _need(w, "freed", freed, i32, (freed.numel(),))
+        _need(w, "freed_count", freed_count, i32, (1,))
+    st = _launch_stream(w, stream, kv_indptr, kv_indices, sources, new_indptr, new_indices, path, accepted, freed,
+                        freed_count, workspace)
+    st = _lib.mla_repack_requests(kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(), B1 - 1,
+                                  sources.data_ptr(), N1, _full(path), _full(accepted), W, new_indptr.data_ptr(),
+                                  new_indices.data_ptr(), new_indices.numel(), int(num_slots), _full(freed),
+                                  0 if freed is None else freed.numel(), _full(freed_count), workspace.data_ptr(),
+                                  workspace.numel(), st)
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
+def _full(t) -> Optional[int]:
+    """Address of an optional tensor; that of an empty one is not null (null means it is not there)."""
+    return None if t is None else t.data_ptr() or 16
+
+
+def _layers(w, name, cache, scales):
+    """(slots, rows from a layer to the next, layers, bytes of a row) of a cache [N, 576] or [L, N, 576] in bf16 or
+    E4M3 codes, and of its scales [N] or [L, N]."""
+    import torch
+    if cache.dtype not in (torch.bfloat16, torch.uint8) or cache.dim() not in (2, 3) or cache.shape[-1] != 576:
+        raise ValueError(f"{w}: {name} is {cache.dtype} {tuple(cache.shape)}, bfloat16 or uint8 [.., slots, 576] is wanted")
+    L, N = (1, cache.shape[0]) if cache.dim() == 2 else cache.shape[:2]
+    rows = N if L <= 1 else cache.stride(0) // 576
+    if N and L and (cache.stride(-1) != 1 or (N > 1 and cache.stride(-2) != 576) or (L > 1 and cache.stride(0) % 576)):
+        raise ValueError(f"{w}: {name}'s rows do not lie one after another")
+    if scales is not None:
+        if cache.dtype is not torch.uint8:
+            raise ValueError(f"{w}: {name} has scales, its rows are not 8-bit")
+        _need(w, name + "'s scales", scales, torch.float32, cache.shape[:-1], dense=False)
+        if L > 1 and scales.stride(0) != rows:
+            raise ValueError(f"{w}: {name}'s scales lie {scales.stride(0)} apart a layer, its rows {rows}")
+    return N, rows, L, 576 * cache.element_size()
+
+
+def copy_rows(src_cache, src_slots, dst_cache, dst_slots, src_scales=None, dst_scales=None, workspace=None,
+              stream=None) -> None:
+    """dst_cache[.., dst_slots[i]] = src_cache[.., src_slots[i]] in every layer: caches [N, 576] or [L, N, 576] of one
+    type (bf16 or E4M3 codes), slots int32 [n]; float32 scales [N] or [L, N] go with their rows.  Both caches may be the
+    same one when no destination is also a source."""
+    import torch
+    w = "mla_copy_rows"
+    _status_word(w, workspace)
+    sn, sr, L, nbytes = _layers(w, "src_cache", src_cache, src_scales)
+    dn, dr, dl, dbytes = _layers(w, "dst_cache", dst_cache, dst_scales)
+    if L != dl or nbytes != dbytes:
+        raise ValueError(f"{w}: the caches differ in layers or type")
+    if (src_scales is None) != (dst_scales is None):
+        raise ValueError(f"{w}: src_scales goes with dst_scales")
+    n = _sizes(w, "src_slots", src_slots, 1)[0]
+    _need(w, "src_slots", src_slots, torch.int32, (n,))
+    _need(w, "dst_slots", dst_slots, torch.int32, (n,))
+    st = _launch_stream(w, stream, src_cache, src_slots, dst_cache, dst_slots, src_scales, dst_scales, workspace)
+    if n and (not sn or not dn):
+        raise ValueError(f"{w}: a cache has no slots")
+    st = _lib.mla_copy_rows(src_cache.data_ptr(), _ptr(src_scales), sn, sr, src_slots.data_ptr(), dst_cache.data_ptr(),
+                            _ptr(dst_scales), dn, dr, dst_slots.data_ptr(), n, L, nbytes, _ptr(workspace), st)
+    if st != MLA_OK:
+        raise MLAError(st, w)
+
+
+def compact_cache(kv_cache, kv_indptr, kv_indices, new_indices, live_count, workspace, kv_scales=None,
+                  stream=None) -> None:
+    """Move the rows that kv_indices[: kv_indptr[-1]] names into the lowest slots, in every layer, and rewrite the
+    lists into new_indices (kv_indices itself will do): kv_cache [N, 576] or [L, N, 576], live_count int32 [1] takes
+    the number of live slots, workspace of slots_workspace_bytes(N) bytes."""
+    import torch
+    w, i32 = "mla_compact_cache", torch.int32
+    N, rows, L, nbytes = _layers(w, "kv_cache", kv_cache, kv_scales)
+    B1 = _sizes(w, "kv_indptr", kv_indptr, 1)[0]
+    if B1 < 1:
+        raise ValueError(f"{w}: kv_indptr must hold batch + 1 entries")
+    n = kv_indices.numel()
+    _need(w, "kv_indptr", kv_indptr, i32, (B1,))
+    _need(w, "kv_indices", kv_indices, i32, (n,))
+    _need(w, "new_indices", new_indices, i32, (n,))
+    _need(w, "live_count", live_count, i32, (1,))
+    _need(w, "workspace", workspace, torch.uint8, (workspace.numel(),))
+    st = _launch_stream(w, stream, kv_cache, kv_indptr, kv_indices, new_indices, live_count, workspace, kv_scales)
+    st = _lib.mla_compact_cache(kv_cache.data_ptr(), _ptr(kv_scales), N, rows, L, nbytes, kv_indptr.data_ptr(), B1 - 1,
+                                kv_indices.data_ptr(), n, new_indices.data_ptr(), live_count.data_ptr(),
+                                workspace.data_ptr(), workspace.numel(), st)
     if st != MLA_OK:
         raise MLAError(st, w)
 

@@ -592,10 +592,12 @@ int mla_decode_fp8_workspace_bytes(const int32_t* plan_host, size_t* workspace_b
   return MLA_OK;
 }
 
-int mla_decode_run_fp8(const int32_t* plan_host, const int32_t* plan_dev, const void* q_nope, const void* q_rope,
-                       const void* kv_cache, int64_t num_slots, float kv_scale, const int32_t* kv_indptr,
-                       const int32_t* kv_indices, float sm_scale, void* out, int32_t out_dtype, float* lse,
-                       void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+// rows: every row has a scale of its own in kv_scales, else kv_scale is that of all.
+int decode_fp8(const int32_t* plan_host, const int32_t* plan_dev, const void* q_nope, const void* q_rope,
+               const void* kv_cache, int64_t num_slots, float kv_scale, bool rows, const float* kv_scales,
+               const int32_t* kv_indptr, const int32_t* kv_indices, float sm_scale, void* out, int32_t out_dtype,
+               float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   if (!plan_header_ok(plan_host) || !plan_dev) return MLA_ERR_INVALID_ARG;
   if (out_dtype != 0 && out_dtype != 1) return MLA_ERR_UNSUPPORTED;
   if (!std::isfinite(sm_scale) || !std::isfinite(kv_scale) || !(kv_scale > 0.f)) return MLA_ERR_INVALID_ARG;
@@ -634,10 +636,12 @@ int mla_decode_run_fp8(const int32_t* plan_host, const int32_t* plan_dev, const 
   p.max_partials = plan_host[kHPartials];
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.q_len = 1;
+  if (rows && (!kv_scales || (reinterpret_cast<uintptr_t>(kv_scales) & 3u) != 0)) return MLA_ERR_INVALID_ARG;
   Fp8Params p8{};
   p8.img = ws + wl.img;
   p8.fac = reinterpret_cast<const float*>(ws + wl.fac);
   p8.kv_scale = kv_scale;
+  p8.kv_scales = rows ? kv_scales : nullptr;
   Fp8PrepParams pp{};
   pp.q_nope = static_cast<const uint16_t*>(q_nope);
   pp.q_rope = static_cast<const uint16_t*>(q_rope);
@@ -659,10 +663,27 @@ int mla_decode_run_fp8(const int32_t* plan_host, const int32_t* plan_dev, const 
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return MLA_ERR_CUDA;
   const int rc = plan_host[kHVariant] == kVariantSwab ? launch_swab8(H, tm_lat, tm_rope, p, p8, pp, plan_host[kHWorkers], st)
-                                                        : launch_pair8(H, tm_lat, tm_rope, p, kv_scale,
+                                                        : launch_pair8(H, tm_lat, tm_rope, p, kv_scale, p8.kv_scales,
                                                                        plan_host[kHWorkers], st);
   if (rc != MLA_OK) return rc;
   return mla_decode_merge(plan_host, plan_dev, out, out_dtype, lse, workspace, workspace_bytes, stream);
+}
+}  // namespace
+
+int mla_decode_run_fp8(const int32_t* plan_host, const int32_t* plan_dev, const void* q_nope, const void* q_rope,
+                       const void* kv_cache, int64_t num_slots, float kv_scale, const int32_t* kv_indptr,
+                       const int32_t* kv_indices, float sm_scale, void* out, int32_t out_dtype, float* lse,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_fp8(plan_host, plan_dev, q_nope, q_rope, kv_cache, num_slots, kv_scale, false, nullptr, kv_indptr,
+                    kv_indices, sm_scale, out, out_dtype, lse, workspace, workspace_bytes, stream);
+}
+
+int mla_decode_run_fp8_rows(const int32_t* plan_host, const int32_t* plan_dev, const void* q_nope, const void* q_rope,
+                            const void* kv_cache, int64_t num_slots, const float* kv_scales, const int32_t* kv_indptr,
+                            const int32_t* kv_indices, float sm_scale, void* out, int32_t out_dtype, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_fp8(plan_host, plan_dev, q_nope, q_rope, kv_cache, num_slots, 1.f, true, kv_scales, kv_indptr,
+                    kv_indices, sm_scale, out, out_dtype, lse, workspace, workspace_bytes, stream);
 }
 
 int mla_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slots, const void* rows, int32_t batch,

@@ -378,6 +378,12 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// The scale that a row of an 8-bit cache is read and written with: what its
+// caller holds, kept where a scale's logarithm and reciprocal are good fp32
+// numbers (a NaN becomes the smallest).
+constexpr float kRowScaleMin = 0x1p-64f, kRowScaleMax = 0x1p64f;
+__device__ __forceinline__ float row_scale(float s) { return fminf(fmaxf(s, kRowScaleMin), kRowScaleMax); }
+
 // Two values as E4M3 hi + lo parts (low byte = a): hi = e4m3(x), lo =
 // e4m3(f16(x) - hi), the difference taken exactly in f16 (x rounded to f16
 // has 11 significant bits, hi 4); for 0 <= x <= 256 the pair keeps x to

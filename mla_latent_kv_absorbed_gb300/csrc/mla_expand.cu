@@ -2,8 +2,8 @@
 // and values,
 //   k[t, h, n] = sum_r c_t[r] w_kc[h, n, r],   v[t, h, n] = sum_r c_t[r] w_vc[h, r, n],
 // and the rope key that all heads share.  c_t is the 512-wide latent of the
-// row (an FP8 row's code values, kv_scale applied to the sums); fp32 sums, one
-// rounding.
+// row (an FP8 row's code values, kv_scale - or the row's own scale - applied to
+// the sums); fp32 sums, one rounding.
 //
 // One matrix product [tokens, 512] x [512, 256 heads] whose left side is
 // gathered.  A CTA keeps the whole depth of 128 rows in shared memory (128
@@ -97,11 +97,12 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-template <bool kFp8, int NT, bool kPair>
+template <CacheForm kForm, int NT, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const ExpandParams p) {
   using C = Cfg<NT, kPair>;
+  constexpr bool kFp8 = kForm != CacheForm::kBf16, kRows = kForm == CacheForm::kRowScaled;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -358,9 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4* dst = reinterpret_cast<uint4*>(p.k_rope + static_cast<size_t>(r) * kRope) + sub;
           if constexpr (kFp8) {
             const uint2 c = __ldg(reinterpret_cast<const uint2*>(p.kv_cache + row[i] + kLatent) + sub);
+            float scale = p.kv_scale;
+            if constexpr (kRows) scale = row_scale(__ldg(p.kv_scales + row[i] / kRow));
             auto val = [&](uint32_t codes) {
               const float2 f = e4m3x2_value(codes);
-              return pack_bf16x2(f.x * p.kv_scale, f.y * p.kv_scale);
+              return pack_bf16x2(f.x * scale, f.y * scale);
             };
             *dst = make_uint4(val(c.x), val(c.x >> 16), val(c.y), val(c.y >> 16));
           } else {
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------- epilogue
     const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
-    const float scale = kFp8 ? p.kv_scale : 1.f;
+    float scale = kForm == CacheForm::kScaled ? p.kv_scale : 1.f;
     // the output streams through L2 (__stcs); the weights, read by every block of rows, should stay
     const int mate = lane & 3;
     uint32_t i = 0;
@@ -380,6 +383,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int col = t % cols, h = (col % groups) * C::kHeads;
       const int r0 = (t / cols) * tile_rows + static_cast<int>(rank) * BM + 32 * q;
       const uint32_t buf = i & 1;
+      if constexpr (kRows) {
+        // a lane's accumulator row is a token: its scale, once a block of rows, while the products run
+        if ((t == t0 || col == 0) && r0 + lane < p.tokens) {
+          const int slot = __ldg(p.kv_indices + r0 + lane);
+          scale = row_scale(__ldg(p.kv_scales + (slot >= 0 && static_cast<long long>(slot) < p.num_slots ? slot : 0)));
+        }
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(acc_full(buf), (i >> 1) & 1, wc))) break;
       tc_fence_after();
       const int end = min((half + 1) * (NT / 2), (p.heads - h) * kNope);   // an odd last head: half a tile
@@ -425,10 +435,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kFp8, int NT, bool kPair>
+template <CacheForm kForm, int NT, bool kPair>
 int launch(const ExpandParams& p, const CUtensorMap (&tm)[2], int grid, cudaStream_t stream) {
   using C = Cfg<NT, kPair>;
-  const auto kernel = &expand_kernel<kFp8, NT, kPair>;
+  const auto kernel = &expand_kernel<kForm, NT, kPair>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes)) return MLA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, 1, 1);
@@ -462,16 +472,21 @@ ExpandTiling expand_tiling(int tokens, int heads, int sms) {
   return {256, true};
 }
 
-int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[2], ExpandTiling tiling, int sms, bool fp8,
+int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[2], ExpandTiling tiling, int sms, CacheForm form,
                   cudaStream_t stream) {
   const int per = tiling.cols / kNope, rows = tiling.pair ? 2 * ex::BM : ex::BM;
   const long long tiles = (p.tokens + static_cast<long long>(rows) - 1) / rows * 2 * ((p.heads + per - 1) / per);
   if (tiles > 0x3FFFFFFFll) return MLA_ERR_UNSUPPORTED;
   const int workers = tiling.pair ? sms / 2 : sms;
   const int grid = static_cast<int>(tiles < workers ? tiles : workers) * (tiling.pair ? 2 : 1);
-  if (tiling.pair)
-    return fp8 ? ex::launch<true, 256, true>(p, tm, grid, stream) : ex::launch<false, 256, true>(p, tm, grid, stream);
-  return fp8 ? ex::launch<true, 128, false>(p, tm, grid, stream) : ex::launch<false, 128, false>(p, tm, grid, stream);
+  auto go = [&](auto form_of) {
+    constexpr CacheForm kForm = decltype(form_of)::value;
+    return tiling.pair ? ex::launch<kForm, 256, true>(p, tm, grid, stream)
+                       : ex::launch<kForm, 128, false>(p, tm, grid, stream);
+  };
+  if (form == CacheForm::kBf16) return go(std::integral_constant<CacheForm, CacheForm::kBf16>{});
+  if (form == CacheForm::kScaled) return go(std::integral_constant<CacheForm, CacheForm::kScaled>{});
+  return go(std::integral_constant<CacheForm, CacheForm::kRowScaled>{});
 }
 
 }  // namespace mla

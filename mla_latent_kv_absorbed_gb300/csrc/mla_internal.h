@@ -108,6 +108,7 @@ struct Fp8Params {
   const uint8_t* img;         // [B] query images (4H x 288 bytes each)
   const float* fac;           // [B, H] per-head factors 2^-a
   float kv_scale;             // cache value = E4M3 code value x kv_scale
+  const float* kv_scales;     // a scale for each slot [num_slots], in the place of kv_scale, or null
 };
 
 // FP8 query prep: bf16 q_nope / q_rope -> query images and factors.

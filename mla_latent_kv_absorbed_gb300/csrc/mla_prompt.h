@@ -17,6 +17,10 @@ constexpr int kPairs = kRope / 2;     // rotated pairs of a head
 constexpr int kNope = 128;            // per-head key width beside the rope part, and value width
 constexpr int kQk = kNope + kRope;    // 192
 
+// What a cache row holds: bf16 values; E4M3 codes with one scale for the whole
+// cache; E4M3 codes with a scale for each row.
+enum class CacheForm { kBf16, kScaled, kRowScaled };
+
 // Frequencies of the 32 pairs as 64-bit fractions of a turn per position
 // (passed by value: they are constants of the model), and the factor on cos
 // and sin.
@@ -47,6 +51,7 @@ struct RopeAppendParams {
   float eps;
   float kv_scale;             // FP8 cache only
   float kv_recip;             // 1 / kv_scale where a product with it is the quotient exactly, else 0
+  float* kv_scales;           // [num_slots] (row-scaled cache only)
 };
 
 struct ExpandParams {
@@ -58,6 +63,7 @@ struct ExpandParams {
   long long num_slots;
   int tokens, heads;
   float kv_scale;             // FP8 cache only
+  const float* kv_scales;     // [num_slots] (row-scaled cache only)
 };
 
 // ---- prefill plan words --------------------------------------------------
@@ -115,7 +121,7 @@ struct PrefillParams {
 };
 
 int launch_rope_query(const RopeQueryParams& p, const RopeFreqs& f, cudaStream_t stream);
-int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, cudaStream_t stream);
+int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, CacheForm form, cudaStream_t stream);
 // How the expansion is tiled: columns of a tile, and whether CTA pairs share
 // one.  Maps: w_kc as [heads * 128, 512] (box: 128 rows x 64), w_vc as [heads *
 // 512, 128] (box 64 x 64).
@@ -124,7 +130,7 @@ struct ExpandTiling {
   bool pair;
 };
 ExpandTiling expand_tiling(int tokens, int heads, int sms);
-int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[2], ExpandTiling tiling, int sms, bool fp8,
+int launch_expand(const ExpandParams& p, const CUtensorMap (&tm)[2], ExpandTiling tiling, int sms, CacheForm form,
                   cudaStream_t stream);
 // tm_q over q as [rows, heads, 192] (box 128 rows x 64), tm_k and tm_v over
 // [keys, heads, 128] (boxes of 128 - for CTA pairs 64 - and 64 keys x 64), tm_kr

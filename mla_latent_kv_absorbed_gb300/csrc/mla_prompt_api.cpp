@@ -149,16 +149,18 @@ int mla_rope_query(const void* q, int64_t q_token_stride, int64_t q_head_stride,
 namespace {
 int rope_append(void* kv_cache, int64_t num_slots, const int32_t* slots, const void* rows, int64_t row_stride,
                 const int32_t* positions, int32_t tokens, const void* norm_weight, float eps, const uint64_t* freqs,
-                float amplitude, int32_t interleaved, bool fp8, float kv_scale, void* workspace, void* stream) {
+                float amplitude, int32_t interleaved, CacheForm form, float kv_scale, float* kv_scales,
+                void* workspace, void* stream) {
   RopeFreqs f;
   if (!rope_args(freqs, amplitude, interleaved, &f)) return MLA_ERR_INVALID_ARG;
   if (tokens < 0 || num_slots < 1 || num_slots > 0x7FFFFFFFll || !std::isfinite(eps) || !(eps >= 0.f))
     return MLA_ERR_INVALID_ARG;
-  if (fp8 && (!std::isfinite(kv_scale) || !(kv_scale > 0.f))) return MLA_ERR_INVALID_ARG;
+  if (form == CacheForm::kScaled && (!std::isfinite(kv_scale) || !(kv_scale > 0.f))) return MLA_ERR_INVALID_ARG;
   if (!stride_ok(row_stride, tokens, kRow)) return MLA_ERR_INVALID_ARG;
   if (tokens == 0) return MLA_OK;
   if (!ready(kv_cache) || !ready(slots, 4) || !ready(rows) || !ready(positions, 4) ||
-      (norm_weight && !aligned(norm_weight, 16)) || (workspace && !aligned(workspace, 16)))
+      (norm_weight && !aligned(norm_weight, 16)) || (workspace && !aligned(workspace, 16)) ||
+      (form == CacheForm::kRowScaled && !ready(kv_scales, 4)))
     return MLA_ERR_INVALID_ARG;
   RopeAppendParams p{};
   p.kv_cache = kv_cache;
@@ -172,10 +174,11 @@ int rope_append(void* kv_cache, int64_t num_slots, const int32_t* slots, const v
   p.tokens = tokens;
   p.eps = eps;
   p.kv_scale = kv_scale;
+  p.kv_scales = kv_scales;
   int exponent = 0;
   if (std::frexp(kv_scale, &exponent) == 0.5f && std::isnormal(kv_scale) && std::isnormal(1.f / kv_scale))
     p.kv_recip = 1.f / kv_scale;
-  return launch_rope_append(p, f, fp8, reinterpret_cast<cudaStream_t>(stream));
+  return launch_rope_append(p, f, form, reinterpret_cast<cudaStream_t>(stream));
 }
 }  // namespace
 
@@ -183,7 +186,7 @@ int mla_rope_append_kv(void* kv_cache, int64_t num_slots, const int32_t* slots, 
                        const int32_t* positions, int32_t tokens, const void* norm_weight, float eps,
                        const uint64_t* freqs, float amplitude, int32_t interleaved, void* workspace, void* stream) {
   return rope_append(kv_cache, num_slots, slots, rows, row_stride, positions, tokens, norm_weight, eps, freqs,
-                     amplitude, interleaved, false, 1.f, workspace, stream);
+                     amplitude, interleaved, CacheForm::kBf16, 1.f, nullptr, workspace, stream);
 }
 
 int mla_rope_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slots, const void* rows,
@@ -191,17 +194,26 @@ int mla_rope_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slo
                            float eps, const uint64_t* freqs, float amplitude, int32_t interleaved, float kv_scale,
                            void* workspace, void* stream) {
   return rope_append(kv_cache, num_slots, slots, rows, row_stride, positions, tokens, norm_weight, eps, freqs,
-                     amplitude, interleaved, true, kv_scale, workspace, stream);
+                     amplitude, interleaved, CacheForm::kScaled, kv_scale, nullptr, workspace, stream);
+}
+
+int mla_rope_append_kv_fp8_rows(void* kv_cache, float* kv_scales, int64_t num_slots, const int32_t* slots,
+                                const void* rows, int64_t row_stride, const int32_t* positions, int32_t tokens,
+                                const void* norm_weight, float eps, const uint64_t* freqs, float amplitude,
+                                int32_t interleaved, void* workspace, void* stream) {
+  return rope_append(kv_cache, num_slots, slots, rows, row_stride, positions, tokens, norm_weight, eps, freqs,
+                     amplitude, interleaved, CacheForm::kRowScaled, 1.f, kv_scales, workspace, stream);
 }
 
 namespace {
 int expand(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, int32_t tokens, const void* w_kc,
-           const void* w_vc, int32_t num_heads, bool fp8, float kv_scale, void* k_nope, void* k_rope, void* v,
-           void* workspace, void* stream) {
+           const void* w_vc, int32_t num_heads, CacheForm form, float kv_scale, const float* kv_scales, void* k_nope,
+           void* k_rope, void* v, void* workspace, void* stream) {
   if (tokens < 0 || num_heads < 1 || num_heads > 65535 || num_slots < 1 || num_slots > 0x7FFFFFFFll)
     return MLA_ERR_INVALID_ARG;
-  if (fp8 && (!std::isfinite(kv_scale) || !(kv_scale > 0.f))) return MLA_ERR_INVALID_ARG;
+  if (form == CacheForm::kScaled && (!std::isfinite(kv_scale) || !(kv_scale > 0.f))) return MLA_ERR_INVALID_ARG;
   if (tokens == 0) return MLA_OK;
+  if (form == CacheForm::kRowScaled && !ready(kv_scales, 4)) return MLA_ERR_INVALID_ARG;
   if (!ready(kv_cache) || !ready(kv_indices, 4) || !ready(w_kc) || !ready(w_vc) || !ready(k_nope) || !ready(k_rope) ||
       !ready(v) || (workspace && !aligned(workspace, 16)))
     return MLA_ERR_INVALID_ARG;
@@ -216,6 +228,7 @@ int expand(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, i
   p.tokens = tokens;
   p.heads = num_heads;
   p.kv_scale = kv_scale;
+  p.kv_scales = kv_scales;
   const int sms = device_sm_count();
   if (sms < 1) return MLA_ERR_CUDA;
   const int64_t H = num_heads;
@@ -223,22 +236,29 @@ int expand(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, i
   if (!make_map(&tm[0], w_kc, H * kNope, kLatent, 0, 0, kLatent, 128) ||
       !make_map(&tm[1], w_vc, H * kLatent, kNope, 0, 0, kNope, 64))
     return MLA_ERR_CUDA;
-  return launch_expand(p, tm, expand_tiling(tokens, num_heads, sms), sms, fp8, reinterpret_cast<cudaStream_t>(stream));
+  return launch_expand(p, tm, expand_tiling(tokens, num_heads, sms), sms, form, reinterpret_cast<cudaStream_t>(stream));
 }
 }  // namespace
 
 int mla_expand_kv(const void* kv_cache, int64_t num_slots, const int32_t* kv_indices, int32_t tokens,
                   const void* w_kc, const void* w_vc, int32_t num_heads, void* k_nope, void* k_rope, void* v,
                   void* workspace, void* stream) {
-  return expand(kv_cache, num_slots, kv_indices, tokens, w_kc, w_vc, num_heads, false, 1.f, k_nope, k_rope, v,
-                workspace, stream);
+  return expand(kv_cache, num_slots, kv_indices, tokens, w_kc, w_vc, num_heads, CacheForm::kBf16, 1.f, nullptr, k_nope,
+                k_rope, v, workspace, stream);
 }
 
 int mla_expand_kv_fp8(const void* kv_cache, int64_t num_slots, float kv_scale, const int32_t* kv_indices,
                       int32_t tokens, const void* w_kc, const void* w_vc, int32_t num_heads, void* k_nope,
                       void* k_rope, void* v, void* workspace, void* stream) {
-  return expand(kv_cache, num_slots, kv_indices, tokens, w_kc, w_vc, num_heads, true, kv_scale, k_nope, k_rope, v,
-                workspace, stream);
+  return expand(kv_cache, num_slots, kv_indices, tokens, w_kc, w_vc, num_heads, CacheForm::kScaled, kv_scale, nullptr,
+                k_nope, k_rope, v, workspace, stream);
+}
+
+int mla_expand_kv_fp8_rows(const void* kv_cache, const float* kv_scales, int64_t num_slots, const int32_t* kv_indices,
+                           int32_t tokens, const void* w_kc, const void* w_vc, int32_t num_heads, void* k_nope,
+                           void* k_rope, void* v, void* workspace, void* stream) {
+  return expand(kv_cache, num_slots, kv_indices, tokens, w_kc, w_vc, num_heads, CacheForm::kRowScaled, 1.f, kv_scales,
+                k_nope, k_rope, v, workspace, stream);
 }
 
 int mla_prefill_plan(const int32_t* q_indptr, const int32_t* kv_indptr, int32_t batch, int32_t num_heads,

@@ -161,7 +161,10 @@ __device__ __forceinline__ float unscale(float x, const RopeAppendParams& p) {
   return p.kv_recip != 0.f ? x * p.kv_recip : __fdiv_rn(x, p.kv_scale);
 }
 
-template <bool kFp8>
+// kRowScaled: the row's largest magnitude (five exchanges of the warp's lanes)
+// gives its scale, and the codes are those of the values times its reciprocal,
+// one fp32 rounding from the quotient.
+template <CacheForm kForm>
 __global__ void __launch_bounds__(kAThreads, kABlocks) rope_append_kernel(const RopeAppendParams p,
                                                                           const __grid_constant__ RopeFreqs f,
                                                                           int warps) {
@@ -226,16 +229,30 @@ __global__ void __launch_bounds__(kAThreads, kABlocks) rope_append_kernel(const 
         x[2 * i + 1] = x[2 * i + 1] * r * bf_hi(g[i]);
       }
     }
-    if constexpr (kFp8) {
+    if constexpr (kForm != CacheForm::kBf16) {
       uint8_t* dst = static_cast<uint8_t*>(p.kv_cache) + slot * kRow;
+      [[maybe_unused]] float recip = 0.f;
+      if constexpr (kForm == CacheForm::kRowScaled) {
+        float top = fmaxf(fabsf(ra), fabsf(rb));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float scale = row_scale(__fdiv_rn(top, 448.f));
+        recip = __frcp_rn(scale);
+        if (lane == 0) p.kv_scales[slot] = scale;
+      }
+      auto code = [&](float v) {
+        if constexpr (kForm == CacheForm::kRowScaled) return v * recip;
+        else return unscale(v, p);
+      };
       uint32_t c[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        c[i] = e4m3x2(unscale(x[4 * i], p), unscale(x[4 * i + 1], p)) |
-               e4m3x2(unscale(x[4 * i + 2], p), unscale(x[4 * i + 3], p)) << 16;
+        c[i] = e4m3x2(code(x[4 * i]), code(x[4 * i + 1])) | e4m3x2(code(x[4 * i + 2]), code(x[4 * i + 3])) << 16;
       reinterpret_cast<uint2*>(dst)[lane] = make_uint2(c[0], c[1]);
       reinterpret_cast<uint2*>(dst)[32 + lane] = make_uint2(c[2], c[3]);
-      const uint32_t r2 = e4m3x2(unscale(ra, p), unscale(rb, p));
+      const uint32_t r2 = e4m3x2(code(ra), code(rb));
       dst[kLatent + ia] = static_cast<uint8_t>(r2);
       dst[kLatent + ib] = static_cast<uint8_t>(r2 >> 8);
     } else {
@@ -292,7 +309,7 @@ int launch_rope_query(const RopeQueryParams& p, const RopeFreqs& f, cudaStream_t
               : launch_dependent(rope_query_kernel<1>, grid, kQThreads, stream, p, f, static_cast<int>(units));
 }
 
-int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, cudaStream_t stream) {
+int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, CacheForm form, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms < 1) return MLA_ERR_CUDA;
   constexpr int kWarps = kAThreads / 32;
@@ -300,8 +317,10 @@ int launch_rope_append(const RopeAppendParams& p, const RopeFreqs& f, bool fp8, 
   const long long held = static_cast<long long>(sms) * kABlocks * kWarps;
   const long long rows = (p.tokens + held - 1) / held;
   const int grid = static_cast<int>((p.tokens + rows * kWarps - 1) / (rows * kWarps));
-  return fp8 ? launch_dependent(rope_append_kernel<true>, grid, kAThreads, stream, p, f, grid * kWarps)
-             : launch_dependent(rope_append_kernel<false>, grid, kAThreads, stream, p, f, grid * kWarps);
+  const auto kernel = form == CacheForm::kBf16  ? &rope_append_kernel<CacheForm::kBf16>
+                      : form == CacheForm::kScaled ? &rope_append_kernel<CacheForm::kScaled>
+                                                   : &rope_append_kernel<CacheForm::kRowScaled>;
+  return launch_dependent(kernel, grid, kAThreads, stream, p, f, grid * kWarps);
 }
 
 }  // namespace mla

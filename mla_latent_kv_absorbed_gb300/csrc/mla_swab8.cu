@@ -37,6 +37,13 @@
 // atom c+2 follows atom c so one 128-row descriptor covers both halves; R1 is
 // the rope from dim 544 (the h1 rope at K offset 0).
 //
+// kRows: every row has a scale of its own, r_t.  The exponents carry it,
+//   e_t = sm_scale log2(e) r_t (q . code_t) + log2 r_t,
+// so that 2^(e_t - m_ref) is the weight of the row's codes and its product with
+// 1 / r_t (before the weight is rounded) the row's share of the sum.  A softmax thread has one token of a tile
+// for all its heads, so that the scale is a register of its own, loaded a tile
+// ahead and its slot number two tiles ahead.
+//
 // Warp roles (one CTA per SM, persistent over the plan's work items):
 //   warps 0-3   softmax / epilogue (TMEM lane quadrants 0-3)
 //   warp 4      QK issuer and query-image loader
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(256) q8_prep_kernel(const Fp8PrepParams p) {
 }
 
 // ------------------------------------------------------------ decode kernel --
-template <int NH>
+template <int NH, bool kRows>
 __global__ void __launch_bounds__(kThreads, 1)
     swab8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const DecodeParams p, const Fp8Params p8) {
@@ -488,8 +495,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       r = __shfl_sync(0xffffffffu, r, 0);
       if (!r) aborted = true;
     };
+    // kRows: this thread's token of the tiles to come, over all items
+    [[maybe_unused]] int n_it = it0, n_s = 0, n_n = 0, n_t0 = 0;      // the tile whose slot number is loaded next
+    [[maybe_unused]] auto next_slot = [&]() -> int {
+      while (n_t0 >= n_n) {                        // the next usable item
+        if (n_it >= it1) return 0;
+        const int b = items[4 * n_it], s = items[4 * n_it + 1], e = items[4 * n_it + 2];
+        ++n_it;
+        if (!item_ok(p, nnz, b, s, e)) continue;
+        n_s = s;
+        n_n = e - s;
+        n_t0 = 0;
+      }
+      const int slot = __ldg(p.kv_indices + n_s + min(n_t0 + t, n_n - 1));
+      n_t0 += T;
+      return slot;
+    };
+    [[maybe_unused]] auto scale_at = [&](int slot) -> float {
+      return __ldg(p8.kv_scales + (slot >= 0 && static_cast<long long>(slot) < p.num_slots ? slot : 0));
+    };
+    [[maybe_unused]] int slot_next = 0;
+    [[maybe_unused]] float sc_next = 1.f;
+    if constexpr (kRows) {
+      sc_next = scale_at(next_slot());
+      slot_next = next_slot();
+    }
     griddep_wait();   // the per-head factors come from the prep kernel
-    const float kv_scale = p8.kv_scale;
+    const float kv_scale = kRows ? 1.f : p8.kv_scale;
 
     for (int it = it0; it < it1; ++it) {
       const int b = items[4 * it], s = items[4 * it + 1], e = items[4 * it + 2];
@@ -502,6 +534,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = e - s, nt = (n + T - 1) / T;
       for (int j = 0; j < nt; ++j, ++g) {
         const uint32_t buf = g & 1;
+        [[maybe_unused]] float sc = 1.f, sc_log = 0.f, sc_inv = 1.f;
+        if constexpr (kRows) {
+          sc = row_scale(sc_next);
+          sc_log = __log2f(sc);
+          sc_inv = __frcp_rn(sc);
+          sc_next = scale_at(slot_next);
+          slot_next = next_slot();
+        }
         wait(bar(C::bSFull + buf), (g >> 1) & 1);
         tc_fence_after();
         float ps[NH];
@@ -534,7 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sv[kHalf];
 #pragma unroll
         for (int k = 0; k < kHalf; ++k)
-          sv[k] = valid ? (own[k] + X[((1 - pair) * kHalf + k) * T + t]) * fac[k] : -INFINITY;
+          sv[k] = !valid  ? -INFINITY
+                  : kRows ? fmaf((own[k] + X[((1 - pair) * kHalf + k) * T + t]) * fac[k], sc, sc_log)
+                          : (own[k] + X[((1 - pair) * kHalf + k) * T + t]) * fac[k];
         if (j == 0) {
 #pragma unroll
           for (int k = 0; k < kHalf; ++k) { m_ref[k] = sv[k]; l_part[k] = 0.f; }
@@ -591,8 +633,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 hv = e4m3x2_value(h2);
           const uint32_t l2 = e4m3x2((p0 - hv.x) * 32.f, (p1 - hv.y) * 32.f);
           const float2 lv = e4m3x2_value(l2);
-          l_part[k] += fmaf(lv.x, kLoWeight, hv.x);
-          l_part[k + 1] += fmaf(lv.y, kLoWeight, hv.y);
+          if constexpr (kRows) {
+            // (a soft row's share of the sum can be large where its weight is a few of the smallest steps)
+            l_part[k] = fmaf(p0, sc_inv, l_part[k]);
+            l_part[k + 1] = fmaf(p1, sc_inv, l_part[k + 1]);
+          } else {
+            l_part[k] += fmaf(lv.x, kLoWeight, hv.x);
+            l_part[k + 1] += fmaf(lv.y, kLoWeight, hv.y);
+          }
           phi[k >> 1] = h2;
           plo[k >> 1] = l2;
         }
@@ -743,11 +791,12 @@ __global__ void __launch_bounds__(kAppendPieces * kAppendRows) append_fp8_kernel
   *reinterpret_cast<uint4*>(p.kv_cache + slot * kRow + 16 * piece) = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-template <int NH>
+template <int NH, bool kRows>
 int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p, const Fp8Params& p8,
            const Fp8PrepParams& pp, int grid, cudaStream_t stream) {
   using C = Cfg<NH>;
-  if (!set_smem_limit(reinterpret_cast<const void*>(&swab8_kernel<NH>), C::kSmemBytes)) return MLA_ERR_CUDA;
+  const auto kernel = &swab8_kernel<NH, kRows>;
+  if (!set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes)) return MLA_ERR_CUDA;
   const int warps = pp.rows;
   // a plain launch (full stream order): the decode kernel below, its
   // programmatic dependent, starts gathering cache rows before it waits, which
@@ -764,7 +813,7 @@ int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodePa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, swab8_kernel<NH>, tm_lat, tm_rope, p, p8) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, tm_lat, tm_rope, p, p8) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_CUDA;
   }
@@ -775,8 +824,13 @@ int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodePa
 
 int launch_swab8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p,
                  const Fp8Params& p8, const Fp8PrepParams& pp, int grid, cudaStream_t stream) {
-  if (heads == 16) return swab8::launch<16>(tm_lat, tm_rope, p, p8, pp, grid, stream);
-  if (heads == 32) return swab8::launch<32>(tm_lat, tm_rope, p, p8, pp, grid, stream);
+  const bool rows = p8.kv_scales != nullptr;
+  if (heads == 16)
+    return rows ? swab8::launch<16, true>(tm_lat, tm_rope, p, p8, pp, grid, stream)
+                : swab8::launch<16, false>(tm_lat, tm_rope, p, p8, pp, grid, stream);
+  if (heads == 32)
+    return rows ? swab8::launch<32, true>(tm_lat, tm_rope, p, p8, pp, grid, stream)
+                : swab8::launch<32, false>(tm_lat, tm_rope, p, p8, pp, grid, stream);
   return MLA_ERR_UNSUPPORTED;
 }
 

@@ -1,0 +1,363 @@
+// Verification of drafted tokens against the target's probabilities, from
+// given random numbers ("[sglang] EAGLE 트리 검증 어텐션 최적화", section
+// "들어가며": the drafts of a tree are verified in one pass of the target).
+//
+//   node = draft 0;  for the node's children c in their order:
+//     accepted  iff  u_c a_c < t_node(x_c);  then node = c and the walk goes on
+//     a_c = q_c(x_c) for drafts sampled from q, or what the rejected siblings
+//     left of the node's mass, 1 - sum t_node(x), for chosen drafts
+//   what is left:  r_v = max(t_v - q_v, 0)  |  t_v off the rejected siblings
+//   next token  =  the lowest v with  sum_{w <= v} r_w > u_0 sum_w r_w
+//
+// (The first form keeps the target's distribution for sampled drafts: the token
+// comes with q(x) min(1, t/q) + the rejected rest spread as max(t - q, 0); the
+// second walks the inverse of the node's distribution child by child.)
+//
+// A pick near a border of the running sum is decided by the sum's last bits,
+// so sums are held to about 48 bits: t - q in fp32 with its exact error (t > q
+// >= 0: t - d and the rest are exact), both added to a pair of fp32 numbers with
+// the addition's exact error, pairs joined in 64 bits.  That is 17 fp32
+// operations an element; in 64 bits they would take the SM longer than the
+// element's eight bytes from memory (one two-hundredth of the fp32 rate).
+//
+// One cluster of CTAs a request, each a stretch of the row: every CTA walks the
+// drafts itself (one warp, a few hundred bytes, the same answer), sums its
+// stretch, and hands the sum to all others through distributed shared memory;
+// the one whose stretch holds the pick finds the warp's part of it, which the
+// CTA's warps sum again in eighths, and one warp scans the right eighth.  The
+// second and third reads are of kilobytes that lie in L1 or L2.
+#include "mla_device.cuh"
+#include "mla_launch.h"
+#include "mla_serving.h"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxCluster = 16;
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+// A probability: NaN and negative values count as 0, values past 1 as 1.
+__device__ __forceinline__ float prob(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+
+// What a request's drafts left: the row that the next token is drawn from.
+struct Walk {
+  int node;                   // the last accepted draft
+  int below;                  // the rejected draft whose q is taken off, or -1
+  int excluded;               // tokens whose mass is taken out
+};
+
+// One warp: lane i has drafts i and 32 + i.
+__device__ __forceinline__ Walk walk_drafts(const VerifyParams& p, int b, int lane, bool write, int32_t* gone) {
+  const int W = p.width;
+  int par[2], tok[2];
+  float t[2], q[2], u[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = lane + 32 * k;
+    par[k] = -2;
+    tok[k] = -1;
+    t[k] = q[k] = u[k] = 0.f;
+    if (i >= W) continue;
+    const long long at = static_cast<long long>(b) * W + i;
+    int up = p.parents ? __ldg(p.parents + at) : i - 1;
+    tok[k] = __ldg(p.tokens + at);
+    u[k] = __ldg(p.uniforms + at);
+    if (up < -1 || up >= i) {
+      if (write) record_status(p.status, MLA_ERR_TREE);
+      up = -1;
+    }
+    par[k] = i == 0 ? -2 : up;                     // a second child of the context is nobody's child here
+    if (i > 0 && (tok[k] < 0 || tok[k] >= p.vocab)) {
+      if (write) record_status(p.status, MLA_ERR_INDEX_OOB);
+      tok[k] = -1;
+    }
+    if (par[k] >= 0 && tok[k] >= 0) {
+      t[k] = prob(__ldg(p.target + b * p.t_bs + par[k] * p.t_rs + tok[k]));
+      if (p.draft) q[k] = prob(__ldg(p.draft + b * p.d_bs + i * p.d_rs + tok[k]));
+    }
+  }
+  auto both = [&](bool lo, bool hi) {
+    return static_cast<unsigned long long>(__ballot_sync(0xffffffffu, lo)) |
+           static_cast<unsigned long long>(__ballot_sync(0xffffffffu, hi)) << 32;
+  };
+  auto of = [&](const auto (&v)[2], int c) {
+    const auto lo = __shfl_sync(0xffffffffu, v[0], c & 31), hi = __shfl_sync(0xffffffffu, v[1], c & 31);
+    return c < 32 ? lo : hi;
+  };
+  int path[2] = {lane == 0 ? 0 : -1, -1};
+  int node = 0, count = 1;
+  unsigned long long rejected = 0;
+  for (bool moved = true; moved;) {                // at most W - 1 children are tried in all
+    unsigned long long kids = both(par[0] == node, par[1] == node);
+    rejected = 0;
+    double left = 1.0;
+    moved = false;
+    while (kids) {
+      const int c = __ffsll(static_cast<long long>(kids)) - 1;
+      kids &= kids - 1;
+      const int x = of(tok, c);
+      const bool again = both((rejected >> lane & 1) && tok[0] == x, (rejected >> (32 + lane) & 1) && tok[1] == x) != 0;
+      const double mass = again ? 0.0 : static_cast<double>(of(t, c));
+      const double against = p.draft ? static_cast<double>(of(q, c)) : left;
+      if (static_cast<double>(fmaxf(of(u, c), 0.f)) * against < mass) {
+        node = c;
+        path[0] = lane == count ? c : path[0];
+        path[1] = lane + 32 == count ? c : path[1];
+        ++count;
+        moved = true;
+        break;
+      }
+      rejected |= 1ull << c;
+      left = fmax(left - mass, 0.0);
+    }
+  }
+  if (write) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (lane + 32 * k < W) p.path[static_cast<long long>(b) * W + lane + 32 * k] = path[k];
+    if (lane == 0) p.accepted[b] = count;
+  }
+  Walk w{node, -1, 0};
+  if (p.draft) {
+    if (rejected) w.below = __ffsll(static_cast<long long>(rejected)) - 1;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bool mine = (rejected >> (lane + 32 * k) & 1) && tok[k] >= 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, mine);
+      if (mine) gone[w.excluded + __popc(m & ((1u << lane) - 1))] = tok[k];
+      w.excluded += __popc(m);
+    }
+  }
+  return w;
+}
+
+// Which of `n` parts, in their order, the running sum passes `thr` in (the last
+// with any mass where rounding or a number of 1 leaves it short; 0 without mass),
+// and the sum before it.
+__device__ __forceinline__ int pick(const double* sum, int n, double thr, double& before) {
+  int at = 0;
+  double run = 0.0;
+  before = 0.0;
+  for (int i = 0; i < n; ++i) {
+    const double s = sum[i];
+    if (s > 0.0) {
+      at = i;
+      before = run;
+      if (run + s > thr) break;
+    }
+    run += s;
+  }
+  return at;
+}
+
+__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) {
+  __shared__ double cta_sum[kMaxCluster], warp_sum[kWarps], part_sum[kWarps];
+  __shared__ int32_t gone[kMaxDrafts];
+  __shared__ Walk walk;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_ctarank());
+  const int b = blockIdx.x / C;
+  griddep_wait();
+  griddep_launch_dependents();
+  cluster_arrive();                                // (the other CTAs run: their shared memory may be written)
+  if (warp == 0) {
+    const Walk w = walk_drafts(p, b, lane, rank == 0, gone);
+    if (lane == 0) walk = w;
+  }
+  __syncthreads();
+  const float* P = p.target + b * p.t_bs + walk.node * p.t_rs;
+  const float* Q = walk.below >= 0 ? p.draft + b * p.d_bs + walk.below * p.d_rs : nullptr;
+  const int n_gone = walk.excluded;
+  // the row in blocks of four elements that lie on 16 bytes: element v is in block (v + lead) / 4
+  const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(P) >> 2 & 3);
+  const bool q_wide = Q && (reinterpret_cast<uintptr_t>(Q) >> 2 & 3) == static_cast<uintptr_t>(lead);
+  const int V = p.vocab;
+  const int blocks = static_cast<int>((static_cast<long long>(V) + lead + 3) / 4);
+  const int per = (blocks + C * kWarps - 1) / (C * kWarps);
+  auto first = [&](int part) { return static_cast<int>(min(static_cast<long long>(part) * per, static_cast<long long>(blocks))); };
+
+  // the four t and q of block k; elements outside the row and taken-out tokens are 0
+  auto load = [&](int k, float (&t)[4], float (&q)[4]) {
+    const int v0 = 4 * k - lead;
+    const bool whole = v0 >= 0 && v0 + 4 <= V;
+    if (whole) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(P + v0));
+      t[0] = x.x, t[1] = x.y, t[2] = x.z, t[3] = x.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = v0 + i >= 0 && v0 + i < V ? __ldg(P + v0 + i) : 0.f;
+    }
+    if (q_wide && whole) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(Q + v0));
+      q[0] = x.x, q[1] = x.y, q[2] = x.z, q[3] = x.w;
+    } else if (Q) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = v0 + i >= 0 && v0 + i < V ? __ldg(Q + v0 + i) : 0.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = 0.f;
+    }
+  };
+  auto clean = [&](int k, float (&t)[4], float (&q)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t[i] = prob(t[i]);
+      q[i] = prob(q[i]);
+    }
+    for (int g = 0; g < n_gone; ++g) {
+      const int at = gone[g] + lead - 4 * k;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = at == i ? 0.f : t[i];
+    }
+  };
+  // sum of max(t - q, 0) over blocks [k0, k1), by a warp; in every lane
+  auto sum_of = [&](int k0, int k1) {
+    float s = 0.f, e = 0.f;
+    constexpr int kDeep = 4;
+    for (int k = k0 + lane; k < k1; k += 32 * kDeep) {
+      float t[kDeep][4], q[kDeep][4];
+#pragma unroll
+      for (int j = 0; j < kDeep; ++j)
+        if (k + 32 * j < k1) load(k + 32 * j, t[j], q[j]);
+#pragma unroll
+      for (int j = 0; j < kDeep; ++j) {
+        if (k + 32 * j >= k1) continue;
+        clean(k + 32 * j, t[j], q[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool more = t[j][i] > q[j][i];
+          const float d = more ? __fsub_rn(t[j][i], q[j][i]) : 0.f;
+          const float de = more ? __fsub_rn(__fsub_rn(t[j][i], d), q[j][i]) : 0.f;
+          const float n = __fadd_rn(s, d);
+          const float z = __fsub_rn(n, s);
+          const float err = __fadd_rn(__fsub_rn(s, __fsub_rn(n, z)), __fsub_rn(d, z));
+          e += err + de;
+          s = n;
+        }
+      }
+    }
+    double all = static_cast<double>(s) + static_cast<double>(e);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    return all;
+  };
+
+  const int mine = rank * kWarps + warp;
+  const double part = sum_of(first(mine), first(mine + 1));
+  if (lane == 0) warp_sum[warp] = part;
+  __syncwarp();
+  cluster_wait();
+  __syncthreads();
+  if (tid < C) {
+    double all = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) all += warp_sum[i];
+    st_cluster_f64(mapa_shared(smem_u32(cta_sum + rank), tid), all);
+  }
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  double total = 0.0;
+  for (int i = 0; i < C; ++i) total += cta_sum[i];
+  if (!(total > 0.0)) {
+    if (rank == 0 && tid == 0) p.next[b] = -1;
+    return;
+  }
+  double thr = static_cast<double>(__ldg(p.uniforms + static_cast<long long>(b) * p.width)) * total;
+  double before;
+  if (pick(cta_sum, C, thr, before) != rank) return;
+  thr -= before;
+  const int w = pick(warp_sum, kWarps, thr, before);
+  thr -= before;
+  // the warp's part in eighths
+  const int k0 = first(rank * kWarps + w), k1 = first(rank * kWarps + w + 1);
+  const int eighth = (k1 - k0 + kWarps - 1) / kWarps;
+  const int e0 = min(k0 + warp * eighth, k1), e1 = min(e0 + eighth, k1);
+  const double sub = sum_of(e0, e1);
+  if (lane == 0) part_sum[warp] = sub;
+  __syncthreads();
+  if (pick(part_sum, kWarps, thr, before) != warp) return;
+  thr -= before;
+  // 32 blocks at a time, a block a lane
+  double run = 0.0;
+  int last = -1;
+  for (int k = e0; k < e1; k += 32) {
+    float t[4], q[4];
+    double r[4] = {0.0, 0.0, 0.0, 0.0}, s = 0.0;
+    if (k + lane < e1) {
+      load(k + lane, t, q);
+      clean(k + lane, t, q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[i] = t[i] > q[i] ? static_cast<double>(t[i]) - static_cast<double>(q[i]) : 0.0;
+        s += r[i];
+      }
+    }
+    double upto = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint32_t some = __ballot_sync(0xffffffffu, s > 0.0);
+    const uint32_t past = __ballot_sync(0xffffffffu, s > 0.0 && run + upto > thr);
+    // the first lane past the number, or, to fall back on, the last one with mass
+    const int who = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : -1;
+    int v = -1;
+    if (who == lane) {
+      double x = run + (upto - s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool over = v >= 0 && past && x > thr;   // passed at an earlier element
+        x += r[i];
+        if (!over && r[i] > 0.0) v = 4 * (k + lane) - lead + i;
+      }
+    }
+    if (who >= 0) last = __shfl_sync(0xffffffffu, v, who);
+    if (past) break;
+    run += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (lane == 0) p.next[b] = last;
+}
+
+}  // namespace
+
+// CTAs a request: as many as give the SMs work, up to the cluster's limit, and
+// each warp of them at least a block a lane.
+int launch_verify(const VerifyParams& p, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  if (sms < 1) return MLA_ERR_CUDA;
+  int ctas = 1;
+  while (ctas < 8 && static_cast<long long>(p.batch) * ctas < 8ll * sms && p.vocab / (2 * ctas * kWarps) >= 128) ctas *= 2;
+  const long long grid = static_cast<long long>(p.batch) * ctas;
+  if (grid > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, verify_kernel, p) != cudaSuccess) return MLA_ERR_CUDA;
+  return cudaPeekAtLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace mla
