@@ -59,10 +59,14 @@ int launch_swab8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rop
 
 // FP8-cache decode for H in 48..128 (a two-CTA cluster per worker, the query
 // split in-kernel); grid = 2 * workers.  tm_lat: uint8 [num_slots, 576], box
-// {128, 1}, 128-byte swizzle; tm_rope: box {32, 1}, 32-byte swizzle.  kv_scales:
-// a scale for each slot in the place of kv_scale, or null.
+// {128, 1}, 128-byte swizzle; tm_rope: box {32, 1}, 32-byte swizzle.
 int launch_pair8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p,
-                 float kv_scale, const float* kv_scales, int workers, cudaStream_t stream);
+                 float kv_scale, int workers, cudaStream_t stream);
+
+// The same over a cache with a scale for each row, kv_scales [num_slots].
+// tm_rope: box {64, 1}, 64-byte swizzle.
+int launch_rows8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p,
+                 const float* kv_scales, int workers, cudaStream_t stream);
 
 // Bytes of one request's query image for the FP8 decode.
 size_t fp8_image_bytes(int heads);

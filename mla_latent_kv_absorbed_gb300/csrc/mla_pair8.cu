@@ -36,16 +36,6 @@
 // absolute for the small weights.  The epilogue multiplies O by
 // kv_scale / l; the score decode multiplies by sm_scale * log2(e) * kv_scale.
 //
-// kRows: every row has a scale of its own, r_t.  The exponents then carry it,
-//   e_t = sm_scale log2(e) r_t (q . code_t) + log2 r_t,
-// so that 2^(e_t - m) is the weight of the row's codes and its product with
-// 1 / r_t the row's share of the sum: one multiply-add in the place of the
-// factor and one in the place of the sum's addition, and the reference maximum
-// is that of the weights which the 8-bit parts have to hold.  The three numbers
-// of a tile's 64 rows, the same for every head, come through shared memory from
-// the rope producer (a row's scale hangs on its slot number: two dependent
-// loads, each a tile ahead).
-//
 // TMEM (512 columns per CTA): O_c [0,256) fp32; the query's hi part [256,320)
 // and lo part [320,384) (4 codes per column); two score buffers [384,512).
 //
@@ -120,22 +110,12 @@ constexpr int bOEmpty = bOFull + 1;
 constexpr int bXFull = bOEmpty + 1;          // [kXSlots] the peer's rows have landed in this CTA's slot
 constexpr int bXFree = bXFull + kXSlots;     // [kXSlots] the PEER's slot may take this CTA's next rows
 constexpr int bDrain = bXFree + kXSlots;
-constexpr int kScSlots = 4;                  // kRows: tiles whose rows' numbers are held
-constexpr int kScDelay = 2;                  // a tile's numbers are written this many tiles after its gathers
-constexpr int bScFull = bDrain + 1;          // [kScSlots]
-constexpr int bScEmpty = bScFull + kScSlots; // [kScSlots]
-constexpr int kScSlot = 3 * T * 4;           // factors, log2 of the scales, reciprocals
-template <bool kRows>
-struct Tail {                                // the end of shared memory
-  static constexpr int kNumBars = kRows ? bScEmpty + kScSlots : bDrain + 1;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffLast = kOffMisc + 16;      // [kLatBlocks + kRopeSlots] last armed use
-  static constexpr int kItemCache = kRows ? 32 : 64;  // this CTA's first work items, copied to shared memory
-  static constexpr int kOffItems = (kOffLast + 4 * (kLatBlocks + kRopeSlots) + 15) / 16 * 16;
-  static constexpr int kOffSc = kOffItems + 16 * kItemCache;
-  static constexpr int kSmemBytes = kOffSc + (kRows ? kScSlots * kScSlot : 0) + 1024;
-  static_assert(kSmemBytes <= 232448, "shared memory budget");
-};
+constexpr int kNumBars = bDrain + 1;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;
+constexpr int kOffLast = kOffMisc + 16;      // [kLatBlocks + kRopeSlots] last armed use
+constexpr int kItemCache = 64;              // this CTA's first work items, copied to shared memory
+constexpr int kOffItems = (kOffLast + 4 * (kLatBlocks + kRopeSlots) + 15) / 16 * 16;
+constexpr int kSmemBytes = kOffItems + 16 * kItemCache + 1024;
 constexpr int kTmO = 0, kTmQHi = 256, kTmQLo = 320, kTmS = 384;
 constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);     // M=128 heads, N=64 tokens
 constexpr uint32_t kIdescQKLo = idesc_f8(kFmtE5M2, kFmtE4M3, 128, T, false, false);   // the query's E5M2 low part
@@ -143,6 +123,7 @@ constexpr uint32_t kIdescPV = idesc_e4m3(128, 256, false, true);    // N=256 dim
 static_assert(kProducers == 5, "producers 0-3 gather the latent atoms, producer 4 the rope");
 static_assert(kThreads == 736, "23 warps");
 static_assert(kLead < kLatBlocks && kRopeLead <= kRopeSlots, "a ring slot's phase must not be lapped while waited on");
+static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kXSlots <= 3, "the rescale's wait on PV(g-1) relies on PV(g-3) being complete");
 static_assert(kOffRope % 1024 == 0 && kOffQR % 1024 == 0 && kOffX % 1024 == 0 && kXSlot % 1024 == 0 &&
                   kOffXE % 16 == 0 && kOffBar % 8 == 0,
@@ -186,13 +167,9 @@ __device__ __forceinline__ float pow2i(int k) { return __uint_as_float(static_ca
 constexpr float kEncBias = 12582912.0f;      // 1.5 * 2^23
 constexpr float kDecHi = 2160066560.0f;      // 2^31 + 2^23 + 2^22 = 515 * 2^22 (exact in fp32)
 
-template <bool kRows>
 __global__ void __launch_bounds__(kThreads, 1)
     pair8_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kr,
-                 const DecodeParams p, const float kv_scale, const float* __restrict__ kv_scales) {
-  constexpr int kOffMisc = Tail<kRows>::kOffMisc, kOffLast = Tail<kRows>::kOffLast;
-  constexpr int kOffItems = Tail<kRows>::kOffItems, kItemCache = Tail<kRows>::kItemCache;
-  constexpr int kOffSc = Tail<kRows>::kOffSc;
+                 const DecodeParams p, const float kv_scale) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -236,8 +213,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(bOFull), 1);
     mbar_init(bar(bOEmpty), kRowWarps);
     mbar_init(bar(bDrain), 2);                   // both issuers' final commits
-    if constexpr (kRows)
-      for (int i = 0; i < kScSlots; ++i) { mbar_init(bar(bScFull + i), 1); mbar_init(bar(bScEmpty + i), kRowWarps); }
     for (int i = 0; i < kLatBlocks + kRopeSlots; ++i) last_armed[i] = -1;
     *abort_flag = 0;
     fence_mbar_init();
@@ -305,59 +280,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = __ldg(p.kv_indices + s + min(t0 + 4 * grp + k, n - 1));
     };
-    // kRows, the rope producer (lane i has tokens i and 32 + i of a tile): the
-    // slots are loaded with those of the gathers, the scales once the tile's
-    // gathers are out, and the numbers made of them written kScDelay tiles
-    // later - late enough that the wait for their place holds up no gather,
-    // and still before the tile's scores are there.
-    [[maybe_unused]] int sc_slot[2] = {0, 0}, sc_cur[2] = {0, 0};
-    [[maybe_unused]] float sc_val[2] = {1.f, 1.f}, sc_hold[2] = {1.f, 1.f};
-    [[maybe_unused]] auto load_sc_slots = [&](int t0) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) sc_slot[i] = __ldg(p.kv_indices + s + min(t0 + lane + 32 * i, n - 1));
-    };
-    [[maybe_unused]] auto scale_step = [&](uint32_t g, bool more) -> bool {
-      if (g >= kScDelay) {
-        const uint32_t k = g - kScDelay, sl = k % kScSlots;
-        bool free = true;
-        if (lane == 0 && k >= kScSlots) free = mbar_wait(bar(bScEmpty + sl), (k / kScSlots - 1) & 1, wc);
-        if (!__shfl_sync(0xffffffffu, free, 0)) return false;
-        float* dst = reinterpret_cast<float*>(smem + kOffSc + sl * kScSlot);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float r = row_scale(sc_hold[i]);
-          dst[lane + 32 * i] = r * p.scale_log2;
-          dst[T + lane + 32 * i] = __log2f(r);
-          dst[2 * T + lane + 32 * i] = __frcp_rn(r);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bScFull + sl));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sc_hold[i] = sc_val[i];
-        if (more) {
-          const int slot = sc_cur[i];
-          sc_val[i] = __ldg(kv_scales + (slot >= 0 && static_cast<long long>(slot) < p.num_slots ? slot : 0));
-        }
-      }
-      return true;
-    };
     next_item();
     int t0 = 0;
     int vn[4] = {0, 0, 0, 0};
     if (it < it1) load_slots(0, vn);
-    if constexpr (kRows)
-      if (pw == 4 && it < it1) load_sc_slots(0);
     uint32_t g = 0;
     bool ok = true;
     while (it < it1 && ok) {
       int v[4];
       bool oob = false;
-      if constexpr (kRows) {
-        sc_cur[0] = sc_slot[0];
-        sc_cur[1] = sc_slot[1];
-      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         v[k] = vn[k];
@@ -372,8 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         t0 = 0;
       }
       if (it < it1) load_slots(t0, vn);
-      if constexpr (kRows)
-        if (pw == 4 && it < it1) load_sc_slots(t0);
       if (lane == 0 && pw == 0) MLA_TRACE_EVENT(0, g);
       {
         const bool rope = pw == 4;
@@ -397,9 +326,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_gather4(base + kOffRope + slot * kRopeAtom + grp * 128, &tm_kr, 512 + 32 * static_cast<int>(cta),
                         v[0], v[1], v[2], v[3], full, pol);
           if (lane == 0) atomicMax(last_armed + kLatBlocks + slot, static_cast<int>(use));
-          if constexpr (kRows) {
-            if (!scale_step(g, true)) { ok = false; break; }
-          }
         } else {
           if (lane == 0 && pw == 0) mbar_arrive_expect_tx(full, kLatBlock);
           __syncwarp();
@@ -412,9 +338,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++g;
     }
-    if constexpr (kRows)
-      if (pw == 4)
-        for (uint32_t i = 0; i < kScDelay && ok; ++i) ok = scale_step(g + i, false);
     named_bar_sync(9, 32 * kProducers);
     if (pw == 0 && lane < kLatBlocks + kRopeSlots) {
       const int u = last_armed[lane];
@@ -643,9 +566,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 st2 = f2_pack(st_p, st_p), sth2 = f2_pack(256.f * st_p, 256.f * st_p);
       const float2 dec2 = f2_pack(-kDecHi * st_p, -kDecHi * st_p);
       const float2 sl2 = f2_pack(sl_kv, sl_kv), qf2 = f2_pack(q_fac, q_fac);
-      // kRows: factors of this half's 32 rows, then log2 of their scales at + T and reciprocals at + 2 T
-      [[maybe_unused]] const float* sc = reinterpret_cast<const float*>(smem + kOffSc + (g % kScSlots) * kScSlot) + th * TH;
-      if constexpr (kRows) wait(bar(bScFull + g % kScSlots), (g / kScSlots) & 1, false);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {            // 8 tokens per 16-byte chunk
         const uint32_t c = static_cast<uint32_t>(4 * th + k);
@@ -667,12 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 fl = f2_pack(__uint_as_float(__byte_perm(lo2, 0x4B000000u, 0x7660)),
                                     __uint_as_float(__byte_perm(lo2, 0x4B000000u, 0x7661)));
           const float2 sp = f2_fma(fl, st2, f2_fma(f, sth2, dec2));
-          const float2 sum = f2_fma(f2_pack(__uint_as_float(sv[t]), __uint_as_float(sv[t + 1])), qf2, sp);
-          float2 s2;
-          if constexpr (kRows)
-            s2 = f2_fma(sum, *reinterpret_cast<const float2*>(sc + t), *reinterpret_cast<const float2*>(sc + T + t));
-          else
-            s2 = f2_mul(sum, sl2);
+          const float2 s2 = f2_mul(f2_fma(f2_pack(__uint_as_float(sv[t]), __uint_as_float(sv[t + 1])), qf2, sp), sl2);
           sv[t] = __float_as_uint(s2.x);
           sv[t + 1] = __float_as_uint(s2.y);
         }
@@ -754,11 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float a = ex2_approx(d.x), e2 = ex2_approx(d.y);
           uint32_t h2, l2;
           e4m3x2_split(a, e2, h2, l2);
-          // four independent sums (fp32 P, as the bf16 kernel)
-          if constexpr (kRows)
-            l4[i & 3] = f2_fma(f2_pack(a, e2), *reinterpret_cast<const float2*>(sc + 2 * T + t), l4[i & 3]);
-          else
-            l4[i & 3] = f2_add(l4[i & 3], f2_pack(a, e2));
+          l4[i & 3] = f2_add(l4[i & 3], f2_pack(a, e2));   // four independent sums (fp32 P, as the bf16 kernel)
           if (i & 1) {
             ph[i >> 1] |= h2 << 16;
             pl[i >> 1] |= l2 << 16;
@@ -777,8 +688,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       l_sum += l2.x + l2.y;
       fence_proxy_async_smem();
       __syncwarp();
-      if constexpr (kRows)
-        if (lane == 0 && !aborted) mbar_arrive(bar(bScEmpty + g % kScSlots));
       if (lane == 0 && !aborted) mbar_arrive(bar(bPFull + xs));
       if (threadIdx.x == 0) MLA_TRACE_EVENT(7, g);
     };
@@ -795,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool part_ok = part < p.max_partials;   // a device-only plan naming a partial past the workspace
       if (!part_ok && threadIdx.x == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
       if (!aborted && part_ok) {
-        const float inv = lsum > 0.f ? (kRows ? 1.f : kv_scale) / lsum : 0.f;   // no valid score: out = 0
+        const float inv = lsum > 0.f ? kv_scale / lsum : 0.f;   // no valid score: out = 0
         // rows of this warp's lane group (4 lanes): after the block transpose
         // lane i of group m holds columns 8i..8i+7 (fp32) of rows 4m..4m+3 of
         // the warp's 32, so each store instruction writes whole 128-byte lines
@@ -991,15 +900,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace pair8
 
 int launch_pair8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p,
-                 float kv_scale, const float* kv_scales, int workers, cudaStream_t stream) {
+                 float kv_scale, int workers, cudaStream_t stream) {
   if (heads < 48 || heads > 128 || heads % 16 != 0) return MLA_ERR_UNSUPPORTED;
-  const auto kernel = kv_scales ? &pair8::pair8_kernel<true> : &pair8::pair8_kernel<false>;
-  const int smem_bytes = kv_scales ? pair8::Tail<true>::kSmemBytes : pair8::Tail<false>::kSmemBytes;
-  if (!set_smem_limit(reinterpret_cast<const void*>(kernel), smem_bytes)) return MLA_ERR_CUDA;
+  if (!set_smem_limit(reinterpret_cast<const void*>(&pair8::pair8_kernel), pair8::kSmemBytes)) return MLA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2 * workers, 1, 1);
   cfg.blockDim = dim3(pair8::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes;
+  cfg.dynamicSmemBytes = pair8::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1010,7 +917,7 @@ int launch_pair8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rop
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kernel, tm_lat, tm_rope, p, kv_scale, kv_scales) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, pair8::pair8_kernel, tm_lat, tm_rope, p, kv_scale) != cudaSuccess) return MLA_ERR_CUDA;
   return cudaPeekAtLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

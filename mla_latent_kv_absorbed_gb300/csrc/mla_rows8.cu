@@ -1,0 +1,725 @@
+// Absorbed MLA decode over an FP8 (E4M3) latent cache with a scale for every
+// row, for many heads (H = 48..128, step 16) on sm_103a.  ("MLA and
+// torch.compile: v0.3's two sources", section "MLA: starting from a 439-line
+// commit": the FP8 KV cache; "实现差距：MLA 与 DeepSeek V3", section 2.4: the
+// latent and rope dot products summed and scaled, FA2-style online softmax, the
+// latent rows reused as the values.)
+//
+// A worker is a cluster of two CTAs, and each takes half of the HEADS: all of
+// the scores, the softmax and the output of a head are one CTA's, and nothing
+// but cache rows passes between the two.  Of a tile's 64 rows each CTA gathers
+// 32 and multicasts them to both, so that a row is read once for all heads.
+//
+// Row t has codes x_t and the scale r_t; the exponents carry the scale,
+//   e_t = sm_scale log2(e) r_t (q . x_t) + log2 r_t,
+// so that w_t = 2^(e_t - m) is the weight of the row's codes, w_t / r_t its
+// share of the sum, and the reference m that of the weights which the 8-bit
+// parts below have to hold.
+//
+// Both products are kind::f8f6f4 and take the codes as they lie in shared
+// memory.  The query is two E4M3 parts, q 2^a = hi + lo / 32 (a puts the head's
+// largest element into [128, 256)), stacked on M: rows 0-63 of A are the hi parts
+// of the CTA's heads, rows 64-127 the lo parts, in tensor memory.
+//   S[128 x 64 rows] = [hi; lo] X^T          16 K-steps from TMEM, 2 of the rope
+// The weights, at most 256, are parts that add up in one accumulator:
+//   out bf16   hi + lo, both E4M3: 8 significant bits, or 2^-10 absolute
+//   out fp32   two more, E4M3 and E5M2: 16 bits, or 2^-14 absolute (the largest
+//              weight is 32 or more) - what an fp32 result is asked for
+//   O^T[512 dims x heads] += X^T W^T         4 blocks of 128 dims, 2 K-steps of
+//                                            32 rows a part
+// The parts' errors are the weights' own; the sum l takes them unrounded.
+//
+// A tile is 18 products of 32 cycles and 16 (fp32: 32) of 48, which shared
+// memory sets (4 KB of X^T and 2 KB of W^T at 128 bytes a cycle): 1340 cycles a
+// tile (fp32 2110) against 580 for its bytes at the measured bandwidth.
+//
+// TMEM (512 columns): O^T [0, 256), the query [256, 384), two score buffers.
+//
+// Warps:
+//   0-7    softmax and epilogue.  A thread of lane quadrant q reads its part
+//          (hi: q < 2) of a head's scores for 32 rows, exchanges half of them with
+//          the thread that has the other part, and goes on with 16 rows.
+//   8-15   the next item's query: largest element, parts in registers while the
+//          item before is worked on, then into TMEM and shared memory
+//   16     QK issuer      17  TMEM allocator, PV issuer
+//   18     gathers of the latents, 32 a tile, one a lane
+//   19     gathers of the rope keys; the numbers made of the rows' scales
+#include "mla_device.cuh"
+#include "mla_launch.h"
+
+namespace mla {
+namespace rows8 {
+
+constexpr int T = 64;                                // rows of a tile
+constexpr int kSoftWarps = 8, kQueryWarps = 8;
+constexpr int kQueryWarp0 = 8, kQkWarp = 16, kPvWarp = 17, kLatentWarp = 18, kRopeWarp = 19;
+constexpr int kThreads = 32 * 20;
+constexpr int kAtom = T * 128;                       // 64 rows x 128 dims
+constexpr int kRopeOff = 4 * kAtom;
+constexpr int kUnit = 4 * kAtom + T * 64;            // a tile: 36 KB
+constexpr int kQr = 128 * 64;                        // rope query: [hi; lo] x 64 dims (64-byte swizzle)
+constexpr int kPPair = 64 * 128;                     // two parts of the weights: 64 heads x (64 + 64) rows
+constexpr int kXBytes = kSoftWarps * 32 * 64;        // scores on their way to the thread of the other part
+constexpr int kScSlots = 3;                          // tiles whose rows' numbers are held
+constexpr int kScDelay = 2;                          // they are written this many tiles after the gathers
+constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the scales, reciprocals
+constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
+constexpr float kLoWeight = 1.f / 32.f;              // value of a query's lo part
+constexpr float kTop = 5.f, kLag = 3.f;              // weights are 2^(e - m + kTop) with e <= m + kLag
+constexpr int kBarPair0 = 1, kBarAll = 5, kBarVote = 6, kBarGather = 7;   // named barriers
+constexpr int kTmO = 0, kTmQ = 256, kTmS = 384;
+constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);
+
+template <bool kFine>
+struct Cfg {
+  static constexpr int kPairs = kFine ? 2 : 1;       // pairs of weight parts
+  static constexpr int kUnits = kFine ? 4 : 5;
+  static constexpr int kPBuf = kPairs * kPPair;
+  static constexpr int kOffQr = kUnits * kUnit;
+  static constexpr int kOffP = kOffQr + kQr;
+  static constexpr int kOffX = kOffP + 2 * kPBuf;
+  static constexpr int kOffSc = kOffX + kXBytes;
+  static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [2][4][64] maxima, sums
+  static constexpr int kOffBc = kOffRed + 2 * 4 * 64 * 4;       // [64] rescaling factors, 1 / l
+  static constexpr int kOffFac = kOffBc + 64 * 4;               // [2][64] 2^-a of an item's heads
+  static constexpr int kOffBar = kOffFac + 2 * 64 * 4;
+  static constexpr int bFull = 0;                    // [kUnits] a tile's rows have landed, both CTAs' halves
+  static constexpr int bEmpty = bFull + kUnits;      // [kUnits] both CTAs have used it
+  static constexpr int bQFull = bEmpty + kUnits;
+  static constexpr int bQEmpty = bQFull + 1;
+  static constexpr int bFacFull = bQEmpty + 1;       // [2]
+  static constexpr int bFacEmpty = bFacFull + 2;     // [2]
+  static constexpr int bSFull = bFacEmpty + 2;       // [2]
+  static constexpr int bSEmpty = bSFull + 2;         // [2]
+  static constexpr int bPFull = bSEmpty + 2;         // [2]
+  static constexpr int bPDone = bPFull + 2;          // [2]
+  static constexpr int bOFull = bPDone + 2;
+  static constexpr int bOEmpty = bOFull + 1;
+  static constexpr int bScFull = bOEmpty + 1;        // [kScSlots]
+  static constexpr int bScEmpty = bScFull + kScSlots;
+  static constexpr int bDrain = bScEmpty + kScSlots;
+  static constexpr int kNumBars = bDrain + 1;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffLast = kOffMisc + 16;     // [kUnits] last armed use
+  static constexpr int kOffItems = (kOffLast + 4 * kUnits + 15) / 16 * 16;
+  static constexpr int kSmemBytes = kOffItems + 16 * kItemCache + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(kUnit % 1024 == 0 && kOffQr % 1024 == 0 && kOffP % 1024 == 0 && kOffX % 16 == 0 && kOffBar % 8 == 0,
+                "alignment");
+};
+
+__device__ __forceinline__ bool item_ok(const DecodeParams& p, int nnz, int b, int s, int e) {
+  return b >= 0 && b < p.batch && 0 <= s && s < e && e <= nnz;
+}
+__device__ __forceinline__ bool item_in_request(const DecodeParams& p, int b, int s, int e) {
+  const int lo = __ldg(p.kv_indptr + b), hi = __ldg(p.kv_indptr + b + 1);
+  return lo <= s && e <= hi;
+}
+
+// A gather of four rows into the same place of both CTAs, counted on the
+// barrier of each.
+__device__ __forceinline__ void tma_gather4_both(uint32_t dst, const void* map, int x, const int (&y)[4], uint32_t bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      ".multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8, %9;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar), "h"(static_cast<uint16_t>(3)), "l"(policy)
+      : "memory");
+}
+
+template <bool kFine>
+__global__ void __launch_bounds__(kThreads, 1)
+    rows8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
+                 const DecodeParams p, const float* __restrict__ kv_scales) {
+  using C = Cfg<kFine>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = static_cast<int>(cluster_ctarank());
+  auto bar = [&](int i) -> uint32_t { return base + C::kOffBar + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  int* last_armed = reinterpret_cast<int*>(smem + C::kOffLast);
+  const WaitCtx wc{abort_flag, p.status};
+  const int w = blockIdx.x >> 1;
+  const int Hc = p.heads >> 1;                       // this CTA's heads: [cta * Hc, (cta + 1) * Hc)
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bFull + i), 1); mbar_init(bar(C::bEmpty + i), 2); }
+    mbar_init(bar(C::bQFull), kQueryWarps);
+    mbar_init(bar(C::bQEmpty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::bFacFull + i), 2); mbar_init(bar(C::bFacEmpty + i), kSoftWarps);
+      mbar_init(bar(C::bSFull + i), 1); mbar_init(bar(C::bSEmpty + i), kSoftWarps);
+      mbar_init(bar(C::bPFull + i), kSoftWarps); mbar_init(bar(C::bPDone + i), 1);
+    }
+    mbar_init(bar(C::bOFull), 1);
+    mbar_init(bar(C::bOEmpty), kSoftWarps);
+    for (int i = 0; i < kScSlots; ++i) { mbar_init(bar(C::bScFull + i), 1); mbar_init(bar(C::bScEmpty + i), kSoftWarps); }
+    mbar_init(bar(C::bDrain), 2);
+    for (int i = 0; i < C::kUnits; ++i) last_armed[i] = -1;
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kPvWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == kLatentWarp && lane == 0) tma_prefetch_desc(&tm_lat);
+  if (warp == kRopeWarp && lane == 0) tma_prefetch_desc(&tm_rope);
+  tc_fence_before();
+  cluster_sync_all();                                // both CTAs' barriers exist before any remote use
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  int it0, it1;
+  plan_items(p, w, it0, it1);
+  const int32_t* items = p.plan + p.items_off;
+  int32_t* s_items = reinterpret_cast<int32_t*>(smem + C::kOffItems);
+  const int n_cached = min(max(it1 - it0, 0), kItemCache);
+  for (int i = threadIdx.x; i < 4 * n_cached; i += blockDim.x) s_items[i] = items[4 * it0 + i];
+  __syncthreads();
+  auto item_w = [&](int it, int k) -> int {
+    return it - it0 < kItemCache ? s_items[4 * (it - it0) + k] : items[4 * it + k];
+  };
+  const int nnz = __ldg(p.kv_indptr + p.batch);
+  griddep_launch_dependents();
+  bool aborted = false;                              // of the softmax and query warps
+
+  if (warp == kLatentWarp || warp == kRopeWarp) {
+    // ------------------------------------------------------------- producers
+    // Latents: lane l gathers rows 4 (l / 4) .. of this CTA's half of the tile,
+    // atom l % 4.  Rope keys: lanes 0-7, four rows each.  An out-of-range slot
+    // reads row 0 and sets MLA_ERR_INDEX_OOB, the ragged tail repeats the last
+    // valid slot.  The slots are loaded a tile ahead.
+    const bool rope = warp == kRopeWarp;
+    const int grp = rope ? lane & 7 : lane >> 2;
+    const int tb = 32 * cta + 4 * grp;
+    const bool active = !rope || lane < 8;
+    const int x = rope ? kLatent : 128 * (lane & 3);
+    const uint32_t dst = rope ? kRopeOff + tb * 64 : (lane & 3) * kAtom + tb * 128;
+    const uint64_t pol = l2_policy_evict_first();
+    int it = it0, s = 0, n = 0, t0 = 0;
+    auto next_item = [&]() {
+      for (; it < it1; ++it) {
+        const int b = item_w(it, 0), s0 = item_w(it, 1), e = item_w(it, 2);
+        if (item_ok(p, nnz, b, s0, e)) {
+          if (rope && lane == 0 && cta == 0 && !item_in_request(p, b, s0, e)) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
+          s = s0;
+          n = e - s0;
+          return;
+        }
+        if (rope && lane == 0 && cta == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
+      }
+    };
+    int vn[4] = {0, 0, 0, 0}, sn[2] = {0, 0};
+    auto load_slots = [&]() {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) vn[k] = __ldg(p.kv_indices + s + min(t0 + tb + k, n - 1));
+      if (rope)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sn[i] = __ldg(p.kv_indices + s + min(t0 + lane + 32 * i, n - 1));
+    };
+    // The rope producer also makes the numbers of the rows' scales (lane i has
+    // rows i and 32 + i): a tile's scales are loaded once its gathers are out,
+    // the numbers written kScDelay tiles later.
+    float val[2] = {1.f, 1.f}, hold[2] = {1.f, 1.f};
+    auto scale_step = [&](uint32_t g, const int* slot) -> bool {
+      if (g >= kScDelay) {
+        const uint32_t k = g - kScDelay, sl = k % kScSlots;
+        bool free = true;
+        if (lane == 0 && k >= kScSlots) free = mbar_wait(bar(C::bScEmpty + sl), (k / kScSlots - 1) & 1, wc);
+        if (!__shfl_sync(0xffffffffu, free, 0)) return false;
+        float* out = reinterpret_cast<float*>(smem + C::kOffSc + sl * kScSlot);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float r = row_scale(hold[i]);
+          out[lane + 32 * i] = r * p.scale_log2;
+          out[T + lane + 32 * i] = __log2f(r);
+          out[2 * T + lane + 32 * i] = __frcp_rn(r);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::bScFull + sl));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        hold[i] = val[i];
+        if (slot) val[i] = __ldg(kv_scales + (slot[i] >= 0 && static_cast<long long>(slot[i]) < p.num_slots ? slot[i] : 0));
+      }
+      return true;
+    };
+    next_item();
+    if (it < it1) load_slots();
+    uint32_t g = 0;
+    bool ok = true;
+    while (it < it1 && ok) {
+      int v[4];
+      const int sv[2] = {sn[0], sn[1]};
+      bool oob = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = vn[k];
+        if (v[k] < 0 || static_cast<long long>(v[k]) >= p.num_slots) { oob = true; v[k] = 0; }
+      }
+      if (oob && rope) record_status(p.status, MLA_ERR_INDEX_OOB);
+      t0 += T;
+      if (t0 >= n) {
+        ++it;
+        next_item();
+        t0 = 0;
+      }
+      if (it < it1) load_slots();
+      const uint32_t slot = g % C::kUnits, use = g / C::kUnits;
+      bool e_ok = true;
+      if (lane == 0 && use > 0) e_ok = mbar_wait<true>(bar(C::bEmpty + slot), (use - 1) & 1, wc);
+      if (!__shfl_sync(0xffffffffu, e_ok, 0)) { ok = false; break; }
+      if (!rope && lane == 0) {
+        mbar_arrive_expect_tx(bar(C::bFull + slot), kUnit);
+        last_armed[slot] = static_cast<int>(use);
+      }
+      __syncwarp();
+      if (active) tma_gather4_both(base + slot * kUnit + dst, rope ? &tm_rope : &tm_lat, x, v, bar(C::bFull + slot), pol);
+      if (rope && !scale_step(g, sv)) { ok = false; break; }
+      ++g;
+    }
+    if (rope)
+      for (uint32_t i = 0; i < kScDelay && ok; ++i) ok = scale_step(g + i, nullptr);
+    named_bar_sync(kBarGather, 64);
+    if (!rope && lane < C::kUnits) {                 // no copy outlives the block
+      const int u = last_armed[lane];
+      if (u >= 0) drain_wait(bar(C::bFull + lane), u & 1);
+    }
+    __syncwarp();
+  } else if (warp == kQkWarp) {
+    // ------------------------------------------------------------- QK issuer
+    if (lane == 0) {
+      const uint64_t dk = sdesc(base, 16, 1024);
+      const uint64_t dr = sdesc(base + kRopeOff, 16, 512, kLayoutSw64);
+      const uint64_t dq = sdesc(base + C::kOffQr, 16, 512, kLayoutSw64);
+      auto D = [](uint64_t d, uint32_t byte_off) -> uint64_t { return d + (byte_off >> 4); };
+      uint32_t g = 0, nitem = 0;
+      bool ok = true;
+      for (int it = it0; it < it1 && ok; ++it) {
+        const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
+        if (!item_ok(p, nnz, b, s, e)) continue;
+        const int nt = (e - s + T - 1) / T;
+        if (!mbar_wait(bar(C::bQFull), nitem & 1, wc)) break;
+        for (int j = 0; j < nt; ++j, ++g) {
+          const uint32_t buf = g & 1, slot = g % C::kUnits;
+          const uint32_t d_s = tmem + kTmS + buf * T;
+          if (g >= 2 && !mbar_wait(bar(C::bSEmpty + buf), ((g >> 1) - 1) & 1, wc)) { ok = false; break; }
+          if (!mbar_wait<true>(bar(C::bFull + slot), (g / C::kUnits) & 1, wc)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t bk = D(dk, slot * kUnit), br = D(dr, slot * kUnit);
+#pragma unroll
+          for (int k = 0; k < 16; ++k)               // 512 latent dims, A from TMEM
+            umma_ts_f8(d_s, tmem + kTmQ + 8 * k, D(bk, (k >> 2) * kAtom + (k & 3) * 32), kIdescQK, k != 0 ? 1u : 0u);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) umma_ss_f8(d_s, D(dq, 32 * k), D(br, 32 * k), kIdescQK, 1u);
+          umma_commit(bar(C::bSFull + buf));
+          if (j == nt - 1) umma_commit(bar(C::bQEmpty));
+        }
+        ++nitem;
+      }
+      umma_commit(bar(C::bDrain));
+      drain_wait(bar(C::bDrain), 0);
+    }
+    __syncwarp();
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------- PV issuer
+    if (lane == 0) {
+      const int cols = (Hc + 15) & ~15;              // columns that hold heads
+      const uint32_t idesc4 = idesc_e4m3(128, cols, true, false);
+      const uint32_t idesc5 = idesc_f8(kFmtE4M3, kFmtE5M2, 128, cols, true, false);
+      const uint64_t dv = sdesc(base, kAtom, 1024);
+      const uint64_t dp = sdesc(base + C::kOffP, 16, 1024);
+      auto D = [](uint64_t d, uint32_t byte_off) -> uint64_t { return d + (byte_off >> 4); };
+      uint32_t g = 0, nitem = 0;
+      bool ok = true;
+      for (int it = it0; it < it1 && ok; ++it) {
+        const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
+        if (!item_ok(p, nnz, b, s, e)) continue;
+        const int nt = (e - s + T - 1) / T;
+        for (int j = 0; j < nt; ++j, ++g) {
+          const uint32_t buf = g & 1, slot = g % C::kUnits;
+          if (!mbar_wait(bar(C::bPFull + buf), (g >> 1) & 1, wc)) { ok = false; break; }
+          if (j == 0 && nitem > 0 && !mbar_wait(bar(C::bOEmpty), (nitem - 1) & 1, wc)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t av = D(dv, slot * kUnit), bp = D(dp, buf * C::kPBuf);
+#pragma unroll
+          for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {         // 32 rows
+              const uint64_t a = D(av, mb * kAtom + 4096 * ks);
+              const uint32_t d = tmem + kTmO + 64 * mb;
+              umma_ss_f8(d, a, D(bp, 32 * ks), idesc4, (j == 0 && ks == 0) ? 0u : 1u);
+              umma_ss_f8(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
+              if constexpr (kFine) {
+                umma_ss_f8(d, a, D(bp, kPPair + 32 * ks), idesc4, 1u);
+                umma_ss_f8(d, a, D(bp, kPPair + 64 + 32 * ks), idesc5, 1u);
+              }
+            }
+          umma_commit_mc(bar(C::bEmpty + slot), 3);  // both CTAs may fill it again once both have used it
+          umma_commit(bar(C::bPDone + buf));
+          if (j == nt - 1) umma_commit(bar(C::bOFull));
+        }
+        ++nitem;
+      }
+      umma_commit(bar(C::bDrain));
+      drain_wait(bar(C::bDrain), 0);
+    }
+    __syncwarp();
+  } else if (warp >= kQueryWarp0) {
+    // ------------------------------------------------------- the items' queries
+    // Row 32 q + lane of A: part q / 2 of head 32 (q % 2) + lane.  Two warps share
+    // a quadrant, each 256 latent and 32 rope dims of its rows.
+    const int q = warp & 3, half = (warp >> 2) & 1;
+    const int row = 32 * q + lane, hl = row & 63;
+    const bool lo = q >= 2, head_ok = hl < Hc;
+    auto wait = [&](uint32_t bb, uint32_t par) {
+      if (aborted) return;
+      bool r = true;
+      if (lane == 0) r = mbar_wait(bb, par, wc);
+      if (!__shfl_sync(0xffffffffu, r, 0)) aborted = true;
+    };
+    uint32_t nitem = 0;
+    for (int it = it0; it < it1; ++it) {
+      const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
+      if (!item_ok(p, nnz, b, s, e)) continue;
+      const size_t at = static_cast<size_t>(b) * p.heads + cta * Hc + hl;
+      const uint4* qn = reinterpret_cast<const uint4*>(p.q_nope + at * kLatent);
+      const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + at * kRope);
+      auto absmax8 = [](const uint4& v, float m) {
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
+        return m;
+      };
+      float amax = 0.f;
+      if (head_ok) {
+#pragma unroll 8
+        for (int i = 0; i < 64; ++i) amax = absmax8(__ldg(qn + i), amax);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = absmax8(__ldg(qr + i), amax);
+      }
+      int a = 0;
+      if (amax > 0.f && amax <= 3.0e38f) {
+        int ex;
+        frexpf(amax, &ex);
+        a = min(126, max(-126, 8 - ex));
+      }
+      const float up = ldexpf(1.f, a);
+      if (half == 0 && !lo) {
+        // the softmax warps have read what item nitem - 2 left here
+        if (nitem >= 2) wait(bar(C::bFacEmpty + (nitem & 1)), ((nitem >> 1) - 1) & 1);
+        reinterpret_cast<float*>(smem + C::kOffFac)[64 * (nitem & 1) + hl] = ldexpf(1.f, -a);
+        __syncwarp();
+        if (lane == 0 && !aborted) mbar_arrive(bar(C::bFacFull + (nitem & 1)));
+      }
+      // 8 bf16 values to 8 codes of this row's part
+      auto part8 = [&](const uint4& v, uint32_t& w0, uint32_t& w1) {
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u0 = __uint_as_float(x[i] << 16) * up, u1 = __uint_as_float(x[i] & 0xFFFF0000u) * up;
+          c[i] = e4m3x2(u0, u1);
+          if (lo) {
+            const float2 hv = e4m3x2_value(c[i]);
+            c[i] = e4m3x2((u0 - hv.x) * 32.f, (u1 - hv.y) * 32.f);
+          }
+        }
+        w0 = c[0] | (c[1] << 16);
+        w1 = c[2] | (c[3] << 16);
+      };
+      uint32_t code[4][16], rope[8];
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          part8(head_ok ? __ldg(qn + 32 * half + 8 * c + k) : zero, code[c][2 * k], code[c][2 * k + 1]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) part8(head_ok ? __ldg(qr + 4 * half + k) : zero, rope[2 * k], rope[2 * k + 1]);
+      if (nitem > 0) wait(bar(C::bQEmpty), (nitem - 1) & 1);
+      tc_fence_after();
+      if (!aborted) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tmem_st16(tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmQ + 64 * half + 16 * c, code[c]);
+        tmem_wait_st();
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<uint4*>(smem + C::kOffQr + (row >> 3) * 512 + (row & 7) * 64 +
+                                    (((2 * half + c) ^ ((row >> 1) & 3)) << 4)) =
+              make_uint4(rope[4 * c], rope[4 * c + 1], rope[4 * c + 2], rope[4 * c + 3]);
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && !aborted) mbar_arrive(bar(C::bQFull));
+      ++nitem;
+    }
+  } else {
+    // ------------------------------------------------------- softmax, epilogue
+    const int q = warp & 3, th = warp >> 2, part = q >> 1;
+    const int hl = 32 * (q & 1) + lane;              // head of this CTA
+    const uint32_t quad = static_cast<uint32_t>(32 * q) << 16;
+    float4* x_own = reinterpret_cast<float4*>(smem + C::kOffX) + warp * 128 + lane;
+    const float4* x_other = reinterpret_cast<const float4*>(smem + C::kOffX) + (warp ^ 2) * 128 + lane;
+    float* red = reinterpret_cast<float*>(smem + C::kOffRed);
+    float* bc = reinterpret_cast<float*>(smem + C::kOffBc);
+    const int four = 2 * th + part;                  // which 16 rows of a tile
+    float m_ref = 0.f, l_sum = 0.f, fac = 1.f;
+    int rk = 0;
+    auto wait = [&](uint32_t bb, uint32_t par) {
+      if (aborted) return;
+      bool r = true;
+      if (lane == 0) r = mbar_wait(bb, par, wc);
+      if (!__shfl_sync(0xffffffffu, r, 0)) aborted = true;
+    };
+    // this head's four values, of the four threads that share it
+    auto share = [&](float v, float (&all)[4]) {
+      float* r = red + (rk & 1) * 256;
+      r[four * 64 + hl] = v;
+      named_bar_sync(kBarAll, 32 * kSoftWarps);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) all[i] = r[i * 64 + hl];
+      ++rk;
+    };
+    uint32_t g = 0, nitem = 0;
+    for (int it = it0; it < it1; ++it) {
+      const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2), dest = item_w(it, 3);
+      if (!item_ok(p, nnz, b, s, e)) continue;
+      const int n = e - s, nt = (n + T - 1) / T;
+      wait(bar(C::bFacFull + (nitem & 1)), (nitem >> 1) & 1);
+      fac = reinterpret_cast<const float*>(smem + C::kOffFac)[64 * (nitem & 1) + hl];
+      __syncwarp();
+      if (lane == 0 && !aborted) mbar_arrive(bar(C::bFacEmpty + (nitem & 1)));
+      for (int j = 0; j < nt; ++j, ++g) {
+        const uint32_t buf = g & 1;
+        wait(bar(C::bSFull + buf), (g >> 1) & 1);
+        uint32_t sv[32];
+        if (!aborted) {
+          tc_fence_after();
+          tmem_ld16(tmem + quad + kTmS + T * buf + 32 * th, *reinterpret_cast<uint32_t(*)[16]>(sv));
+          tmem_ld16(tmem + quad + kTmS + T * buf + 32 * th + 16, *reinterpret_cast<uint32_t(*)[16]>(sv + 16));
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sv[i] = 0;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && !aborted) mbar_arrive(bar(C::bSEmpty + buf));
+        // the thread of the hi part keeps rows 0-15 of these 32, that of the lo part rows 16-31
+        float x[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int keep = 4 * k, send = 16 + 4 * k;
+          if (part == 0) {
+            x_own[32 * k] = make_float4(__uint_as_float(sv[send]), __uint_as_float(sv[send + 1]),
+                                        __uint_as_float(sv[send + 2]), __uint_as_float(sv[send + 3]));
+          } else {
+            x_own[32 * k] = make_float4(__uint_as_float(sv[keep]), __uint_as_float(sv[keep + 1]),
+                                        __uint_as_float(sv[keep + 2]), __uint_as_float(sv[keep + 3]));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[4 * k + i] = part == 0 ? __uint_as_float(sv[keep + i]) : __uint_as_float(sv[send + i]) * kLoWeight;
+        }
+        named_bar_sync(kBarPair0 + 2 * (q & 1) + th, 64);
+        const float w_other = part == 0 ? kLoWeight : 1.f;
+        wait(bar(C::bScFull + g % kScSlots), (g / kScSlots) & 1);
+        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 4 * four;
+        float mx = -INFINITY;
+        const int nvalid = n - j * T - 16 * four;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 o = x_other[32 * k], f = sc[k], lg = sc[T / 4 + k];
+          const float ov[4] = {o.x, o.y, o.z, o.w}, fv[4] = {f.x, f.y, f.z, f.w}, lv[4] = {lg.x, lg.y, lg.z, lg.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v = fmaf(fmaf(ov[i], w_other, x[4 * k + i]) * fac, fv[i], lv[i]);
+            x[4 * k + i] = 4 * k + i < nvalid ? v : -INFINITY;
+            mx = fmaxf(mx, x[4 * k + i]);
+          }
+        }
+        if (j == 0) {
+          float all[4];
+          share(mx, all);
+          m_ref = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+          l_sum = 0.f;
+        } else if (named_bar_or(kBarVote, 32 * kSoftWarps, mx > m_ref + kLag)) {
+          float all[4];
+          share(mx, all);
+          const float mn = fmaxf(m_ref, fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])));
+          const float alpha = ex2_approx(m_ref - mn);
+          m_ref = mn;
+          l_sum *= alpha;
+          if (four == 0) bc[hl] = alpha;
+          named_bar_sync(kBarAll, 32 * kSoftWarps);
+          wait(bar(C::bPDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
+          tc_fence_after();
+          if (!aborted) {
+            // this warp's 32 dims of blocks 2 th and 2 th + 1, 16 heads at a time
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              const uint32_t ta = tmem + quad + kTmO + 128 * th + 16 * c;
+              tmem_ld16(ta, o);
+              tmem_wait_ld();
+              const float4* al = reinterpret_cast<const float4*>(bc) + 4 * (c & 3);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 f = al[i];
+                o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f.x);
+                o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f.y);
+                o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f.z);
+                o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f.w);
+              }
+              tmem_st16(ta, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // weights and their parts; 16 rows are one 16-byte chunk of each
+        uint32_t w0[4], w1[4], w2[4], w3[4];
+        const float shift = kTop - m_ref;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 iv = sc[2 * T / 4 + k];
+          uint32_t c0[2], c1[2], c2[2], c3[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float a = ex2_approx(x[4 * k + 2 * i] + shift), z = ex2_approx(x[4 * k + 2 * i + 1] + shift);
+            l_sum = fmaf(a, i ? iv.z : iv.x, l_sum);
+            l_sum = fmaf(z, i ? iv.w : iv.y, l_sum);
+            if constexpr (kFine) {
+              c0[i] = e4m3x2(a, z);
+              float2 h = e4m3x2_value(c0[i]);
+              float ra = a - h.x, rz = z - h.y;      // (exact, like the next two)
+              c1[i] = e4m3x2(ra, rz);
+              h = e4m3x2_value(c1[i]);
+              ra -= h.x;
+              rz -= h.y;
+              c2[i] = e4m3x2(ra, rz);
+              h = e4m3x2_value(c2[i]);
+              c3[i] = e5m2x2(ra - h.x, rz - h.y);
+            } else {
+              e4m3x2_split(a, z, c0[i], c1[i]);
+            }
+          }
+          w0[k] = c0[0] | (c0[1] << 16);
+          w1[k] = c1[0] | (c1[1] << 16);
+          if constexpr (kFine) {
+            w2[k] = c2[0] | (c2[1] << 16);
+            w3[k] = c3[0] | (c3[1] << 16);
+          }
+        }
+        if (g >= 2) wait(bar(C::bPDone + buf), ((g >> 1) - 1) & 1);
+        if (!aborted) {
+          uint8_t* row = smem + C::kOffP + buf * C::kPBuf + hl * 128;
+          const int sw = hl & 7;
+          *reinterpret_cast<uint4*>(row + ((four ^ sw) << 4)) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+          *reinterpret_cast<uint4*>(row + (((4 + four) ^ sw) << 4)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          if constexpr (kFine) {
+            *reinterpret_cast<uint4*>(row + kPPair + ((four ^ sw) << 4)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+            *reinterpret_cast<uint4*>(row + kPPair + (((4 + four) ^ sw) << 4)) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && !aborted) {
+          mbar_arrive(bar(C::bPFull + buf));
+          mbar_arrive(bar(C::bScEmpty + g % kScSlots));
+        }
+      }
+      // ---------------------------------------------------------------- epilogue
+      const bool part_ok = dest < p.max_partials;    // a device-only plan naming a partial past the workspace
+      if (!part_ok && threadIdx.x == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
+      float all[4];
+      share(l_sum, all);
+      const float l = (all[0] + all[1]) + (all[2] + all[3]);
+      const size_t row0 = static_cast<size_t>(dest < 0 ? b : dest) * p.heads + cta * Hc;
+      if (four == 0) {
+        bc[hl] = l > 0.f ? 1.f / l : 0.f;
+        if (hl < Hc && !aborted && part_ok) {
+          const float lse = l > 0.f ? (m_ref + __log2f(l) - kTop) * 0.69314718055994531f : -INFINITY;
+          if (dest >= 0) p.part_lse[row0 + hl] = lse;
+          else if (p.lse) p.lse[row0 + hl] = lse;
+        }
+      }
+      named_bar_sync(kBarAll, 32 * kSoftWarps);
+      wait(bar(C::bOFull), nitem & 1);
+      tc_fence_after();
+      const bool half_out = dest < 0 && p.out_bf16;
+      float* dst_f = dest >= 0 ? p.part_o + row0 * kLatent : static_cast<float*>(p.out) + row0 * kLatent;
+      __nv_bfloat16* dst_h = static_cast<__nv_bfloat16*>(p.out) + row0 * kLatent;
+      if (!aborted && part_ok) {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {                // block c / 2, 16 of this warp's 32 heads
+          const int h0 = 32 * th + 16 * (c & 1), d = 128 * (c >> 1) + 32 * q + lane;
+          if (h0 >= Hc) continue;
+          uint32_t o[16];
+          tmem_ld16(tmem + quad + kTmO + 64 * (c >> 1) + h0, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (h0 + i >= Hc) break;
+            const float v = __uint_as_float(o[i]) * bc[h0 + i];
+            if (half_out) dst_h[static_cast<size_t>(h0 + i) * kLatent + d] = __float2bfloat16_rn(v);
+            else dst_f[static_cast<size_t>(h0 + i) * kLatent + d] = v;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && !aborted) mbar_arrive(bar(C::bOEmpty));
+      ++nitem;
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync_all();                                // no CTA leaves while the other may still write or signal to it
+  tc_fence_after();
+  if (warp == kPvWarp) tmem_dealloc(tmem, 512);
+}
+
+template <bool kFine>
+int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p, const float* kv_scales,
+           int workers, cudaStream_t stream) {
+  const auto kernel = &rows8_kernel<kFine>;
+  if (!set_smem_limit(reinterpret_cast<const void*>(kernel), Cfg<kFine>::kSmemBytes)) return MLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * workers, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg<kFine>::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, tm_lat, tm_rope, p, kv_scales) != cudaSuccess) return MLA_ERR_CUDA;
+  return cudaPeekAtLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace rows8
+
+int launch_rows8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p,
+                 const float* kv_scales, int workers, cudaStream_t stream) {
+  if (heads < 48 || heads > 128 || heads % 16 != 0) return MLA_ERR_UNSUPPORTED;
+  return p.out_bf16 ? rows8::launch<false>(tm_lat, tm_rope, p, kv_scales, workers, stream)
+                    : rows8::launch<true>(tm_lat, tm_rope, p, kv_scales, workers, stream);
+}
+
+}  // namespace mla

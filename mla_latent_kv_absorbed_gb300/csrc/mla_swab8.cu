@@ -44,6 +44,13 @@
 // for all its heads, so that the scale is a register of its own, loaded a tile
 // ahead and its slot number two tiles ahead.
 //
+// kFine (fp32 output of the row-scaled form): two parts more, so that the
+// weights keep 16 bits.  The third is added to the hi accumulator, the fourth,
+// times 32, to the lo one; a weight's four are the same row's bytes 0-63 and
+// 64-127 of the hi and the lo row.  Weights then are 2^(e - m_ref + 5), at most
+// 256 and the largest at least 32, which puts the parts' smallest step at 2^-14
+// of 32.
+//
 // Warp roles (one CTA per SM, persistent over the plan's work items):
 //   warps 0-3   softmax / epilogue (TMEM lane quadrants 0-3)
 //   warp 4      QK issuer and query-image loader
@@ -57,6 +64,8 @@
 // the first tiles overlap it, and only the QK and softmax warps wait for it.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "mla_device.cuh"
 #include "mla_launch.h"
@@ -284,12 +293,14 @@ __global__ void __launch_bounds__(256) q8_prep_kernel(const Fp8PrepParams p) {
 }
 
 // ------------------------------------------------------------ decode kernel --
-template <int NH, bool kRows>
+template <int NH, bool kRows, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1)
     swab8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const DecodeParams p, const Fp8Params p8) {
   using C = Cfg<NH>;
   constexpr int kHalf = C::kHalf;
+  // a weight is 2^(e - m_ref + kUp), and the reference moves once a score passes it by kLag
+  constexpr float kUp = kFine ? 5.f : 0.f, kLag = kFine ? 3.f : 8.f;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -457,9 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb) {
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-              umma_ss_f8(tmem + C::kTmO + mb * 2 * NH, sdesc(ub + atom_pos(mb) * kAtom + 4096 * ks, kAtom, 1024),
-                         sdesc(pb + 32 * ks, 16, 1024), C::kIdescPV, (j == 0 && ks == 0) ? 0u : 1u);
+            for (int ks = 0; ks < 2; ++ks) {
+              const uint64_t a = sdesc(ub + atom_pos(mb) * kAtom + 4096 * ks, kAtom, 1024);
+              umma_ss_f8(tmem + C::kTmO + mb * 2 * NH, a, sdesc(pb + 32 * ks, 16, 1024), C::kIdescPV,
+                         (j == 0 && ks == 0) ? 0u : 1u);
+              if constexpr (kFine)
+                umma_ss_f8(tmem + C::kTmO + mb * 2 * NH, a, sdesc(pb + 64 + 32 * ks, 16, 1024), C::kIdescPV, 1u);
+            }
             if (j == nt - 1 && (mb & 1)) umma_commit(bar(C::bOBlk + (mb >> 1)));
           }
           umma_commit(bar(C::bEmpty + us));
@@ -585,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           bool need = false;
 #pragma unroll
-          for (int k = 0; k < kHalf; ++k) need |= sv[k] > m_ref[k] + 8.f;
+          for (int k = 0; k < kHalf; ++k) need |= sv[k] > m_ref[k] + kLag;
           need = named_bar_or(kBarVote, 128, need);
           if (need) {
             float mt[kHalf], alpha[kHalf];
@@ -626,9 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // weights: hi + lo / 32 in E4M3, summed as the MMA will see them
         uint32_t phi[kHalf / 2], plo[kHalf / 2];
+        [[maybe_unused]] uint32_t ph3[kFine ? kHalf / 2 : 1], pl4[kFine ? kHalf / 2 : 1];
 #pragma unroll
         for (int k = 0; k < kHalf; k += 2) {
-          const float p0 = ex2_approx(sv[k] - m_ref[k]), p1 = ex2_approx(sv[k + 1] - m_ref[k + 1]);
+          const float p0 = ex2_approx(sv[k] - m_ref[k] + kUp), p1 = ex2_approx(sv[k + 1] - m_ref[k + 1] + kUp);
           const uint32_t h2 = e4m3x2(p0, p1);
           const float2 hv = e4m3x2_value(h2);
           const uint32_t l2 = e4m3x2((p0 - hv.x) * 32.f, (p1 - hv.y) * 32.f);
@@ -643,6 +659,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           phi[k >> 1] = h2;
           plo[k >> 1] = l2;
+          if constexpr (kFine) {                       // (the differences are exact)
+            const float2 f2 = e4m3x2_value(l2);
+            const float r0 = p0 - hv.x - f2.x * kLoWeight, r1 = p1 - hv.y - f2.y * kLoWeight;
+            ph3[k >> 1] = e4m3x2(r0, r1);
+            const float2 t2 = e4m3x2_value(ph3[k >> 1]);
+            pl4[k >> 1] = e4m3x2((r0 - t2.x) * 32.f, (r1 - t2.y) * 32.f);
+          }
         }
         if (g >= 2) wait(bar(C::bPDone + buf), ((g >> 1) - 1) & 1);
         if (!aborted) {
@@ -655,6 +678,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             pb[sw128_off(h + 1, t)] = static_cast<uint8_t>(phi[k >> 1] >> 8);
             pb[sw128_off(NH + h, t)] = static_cast<uint8_t>(plo[k >> 1]);
             pb[sw128_off(NH + h + 1, t)] = static_cast<uint8_t>(plo[k >> 1] >> 8);
+            if constexpr (kFine) {
+              pb[sw128_off(h, T + t)] = static_cast<uint8_t>(ph3[k >> 1]);
+              pb[sw128_off(h + 1, T + t)] = static_cast<uint8_t>(ph3[k >> 1] >> 8);
+              pb[sw128_off(NH + h, T + t)] = static_cast<uint8_t>(pl4[k >> 1]);
+              pb[sw128_off(NH + h + 1, T + t)] = static_cast<uint8_t>(pl4[k >> 1] >> 8);
+            }
           }
         }
         fence_proxy_async_smem();
@@ -681,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float my_lse = 0.f;
 #pragma unroll
         for (int k = 0; k < kHalf; ++k)
-          if (lane == k) my_lse = (m_ref[k] + __log2f(l_tot[k])) * 0.69314718055994531f;
+          if (lane == k) my_lse = (m_ref[k] + __log2f(l_tot[k]) - kUp) * 0.69314718055994531f;
         if (!aborted && part_ok && wip == 0 && lane < kHalf) {
           const int h = pair * kHalf + lane;
           if (to_out) { if (p.lse) p.lse[static_cast<size_t>(b) * p.heads + h] = my_lse; }
@@ -791,11 +820,11 @@ __global__ void __launch_bounds__(kAppendPieces * kAppendRows) append_fp8_kernel
   *reinterpret_cast<uint4*>(p.kv_cache + slot * kRow + 16 * piece) = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-template <int NH, bool kRows>
+template <int NH, bool kRows, bool kFine>
 int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p, const Fp8Params& p8,
            const Fp8PrepParams& pp, int grid, cudaStream_t stream) {
   using C = Cfg<NH>;
-  const auto kernel = &swab8_kernel<NH, kRows>;
+  const auto kernel = &swab8_kernel<NH, kRows, kFine>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes)) return MLA_ERR_CUDA;
   const int warps = pp.rows;
   // a plain launch (full stream order): the decode kernel below, its
@@ -824,13 +853,14 @@ int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodePa
 
 int launch_swab8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p,
                  const Fp8Params& p8, const Fp8PrepParams& pp, int grid, cudaStream_t stream) {
-  const bool rows = p8.kv_scales != nullptr;
-  if (heads == 16)
-    return rows ? swab8::launch<16, true>(tm_lat, tm_rope, p, p8, pp, grid, stream)
-                : swab8::launch<16, false>(tm_lat, tm_rope, p, p8, pp, grid, stream);
-  if (heads == 32)
-    return rows ? swab8::launch<32, true>(tm_lat, tm_rope, p, p8, pp, grid, stream)
-                : swab8::launch<32, false>(tm_lat, tm_rope, p, p8, pp, grid, stream);
+  auto go = [&](auto nh) {
+    constexpr int NH = decltype(nh)::value;
+    if (!p8.kv_scales) return swab8::launch<NH, false, false>(tm_lat, tm_rope, p, p8, pp, grid, stream);
+    return p.out_bf16 ? swab8::launch<NH, true, false>(tm_lat, tm_rope, p, p8, pp, grid, stream)
+                      : swab8::launch<NH, true, true>(tm_lat, tm_rope, p, p8, pp, grid, stream);
+  };
+  if (heads == 16) return go(std::integral_constant<int, 16>{});
+  if (heads == 32) return go(std::integral_constant<int, 32>{});
   return MLA_ERR_UNSUPPORTED;
 }
 

@@ -206,14 +206,16 @@ def _check(args, indptr, status=0):
         z = torch.logsumexp(s, -1)
         p = torch.exp(s - z[:, None])
         ref = p @ x[:, :512]
-        # weights: 2^-8 of themselves, or 2^-15 of the head's largest weight of codes (hi and lo parts of E4M3);
-        # their sum is taken before they are rounded; scores: fp32 sums of 576 products, of which 2^-18 of the
-        # largest possible score is ample
+        # weights: 2^-8 of themselves, or 2^-15 of the head's largest weight of codes; for an fp32 output 2^-15 of
+        # themselves, or 2^-19 (two or four 8-bit parts; the head's largest weight is 32 or more).  Their sum is taken
+        # before they are rounded; scores: fp32 sums of 576 products, of which 2^-18 of the largest possible score is
+        # ample
+        own, least = (BF, 2.0 ** -15) if out.dtype is torch.bfloat16 else (2.0 ** -15, 2.0 ** -19)
         code = codes[at].view(torch.float8_e4m3fn).double()[:, :512].abs()
         r = scales[at].double().clamp(LOW, HIGH)
         top = (p * r).amax(1, keepdim=True)
         off = 2.0 ** -18 * (q[i].abs() @ x.abs().t()).amax(1, keepdim=True) * abs(sm)
-        bound = (BF + off) * (p @ x[:, :512].abs()) + 2.0 ** -15 * top * code.sum(0)
+        bound = (own + off) * (p @ x[:, :512].abs()) + least * top * code.sum(0)
         if out.dtype is torch.bfloat16:
             bound = bound + BF * (ref.abs() + bound)
         err = (out[i].double() - ref).abs()
@@ -224,19 +226,22 @@ def _check(args, indptr, status=0):
 LENS = [1, 2, 63, 64, 65, 0, 300, 129, 7, 1500, 0, 64]
 
 
-@pytest.mark.parametrize("H", [16, 32, 48, 80, 128])
+@pytest.mark.parametrize("H", [16, 32, 48, 80, 112, 128])
 @pytest.mark.parametrize("spread", [0.0, 3.0, 12.0])
-def test_decode(H, spread):
+@pytest.mark.parametrize("half", [False, True])
+def test_decode(H, spread, half):
+    torch, _ = _t()
     codes, scales = _cache(H, 4000, spread)
-    _check(*_decode(codes, scales, LENS, H, 5))
+    _check(*_decode(codes, scales, LENS, H, 5, dtype=torch.bfloat16 if half else torch.float32))
 
 
 @pytest.mark.parametrize("H", [16, 128])
 @pytest.mark.parametrize("lens", [[1], [33] * 200, [20000], [9000, 17, 30000]])
-def test_decode_few_long_and_many_short(H, lens):
+@pytest.mark.parametrize("half", [False, True])
+def test_decode_few_long_and_many_short(H, lens, half):
     torch, _ = _t()
     codes, scales = _cache(H + len(lens), sum(lens) + 9, 2.0)
-    _check(*_decode(codes, scales, lens, H, 6, dtype=torch.bfloat16))
+    _check(*_decode(codes, scales, lens, H, 6, dtype=torch.bfloat16 if half else torch.float32))
 
 
 @pytest.mark.parametrize("H", [32, 64])
