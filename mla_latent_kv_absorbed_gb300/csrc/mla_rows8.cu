@@ -5,10 +5,12 @@
 // latent and rope dot products summed and scaled, FA2-style online softmax, the
 // latent rows reused as the values.)
 //
-// A worker is a cluster of two CTAs, and each takes half of the HEADS: all of
-// the scores, the softmax and the output of a head are one CTA's, and nothing
-// but cache rows passes between the two.  Of a tile's 64 rows each CTA gathers
-// 32 and multicasts them to both, so that a row is read once for all heads.
+// A worker is two CTAs, and each takes half of the HEADS: all of the scores,
+// the softmax and the output of a head are one CTA's, and nothing passes between
+// the two.  Both gather every row, the second of them from L2.  (As a cluster
+// that gathers half of the rows each and multicasts them, a gather of four rows
+// took the TMA unit 47 cycles, and 40 of them a tile 1900; on its own one takes
+// about 14.)
 //
 // Row t has codes x_t and the scale r_t; the exponents carry the scale,
 //   e_t = sm_scale log2(e) r_t (q . x_t) + log2 r_t,
@@ -29,9 +31,11 @@
 //                                            32 rows a part
 // The parts' errors are the weights' own; the sum l takes them unrounded.
 //
-// A tile is 18 products of 32 cycles and 16 (fp32: 32) of 48, which shared
-// memory sets (4 KB of X^T and 2 KB of W^T at 128 bytes a cycle): 1340 cycles a
-// tile (fp32 2110) against 580 for its bytes at the measured bandwidth.
+// A tile is 18 and 16 (fp32: 32) products of 48 cycles, the least that one of
+// this width takes: 1650 cycles a tile (fp32 2430) against 580 for its bytes at
+// the measured bandwidth.  The softmax of a tile is a chain of waits and
+// exchanges of 2500 cycles, so its first half, up to the exchange of the parts,
+// is begun before the weights of the tile before are made.
 //
 // TMEM (512 columns): O^T [0, 256), the query [256, 384), two score buffers.
 //
@@ -41,9 +45,13 @@
 //          the thread that has the other part, and goes on with 16 rows.
 //   8-15   the next item's query: largest element, parts in registers while the
 //          item before is worked on, then into TMEM and shared memory
-//   16     QK issuer      17  TMEM allocator, PV issuer
-//   18     gathers of the latents, 32 a tile, one a lane
-//   19     gathers of the rope keys; the numbers made of the rows' scales
+//   16     TMEM allocator, issuer of all products: the scores of tile g + 2, then
+//          the weighted sum of tile g.  They run in that order, so that scores of
+//          g + 1 that are there say that the sum of g - 2 is done.
+//   17-20  gathers of the latents, an atom each: 16 of four rows a tile (a warp
+//          takes some 60 cycles for each of a burst, so they are spread)
+//   21     gathers of the rope keys
+//   22     the numbers made of the rows' scales
 #include "mla_device.cuh"
 #include "mla_launch.h"
 
@@ -52,16 +60,15 @@ namespace rows8 {
 
 constexpr int T = 64;                                // rows of a tile
 constexpr int kSoftWarps = 8, kQueryWarps = 8;
-constexpr int kQueryWarp0 = 8, kQkWarp = 16, kPvWarp = 17, kLatentWarp = 18, kRopeWarp = 19;
-constexpr int kThreads = 32 * 20;
+constexpr int kQueryWarp0 = 8, kMmaWarp = 16, kLatentWarp0 = 17, kRopeWarp = 21, kScaleWarp = 22;
+constexpr int kThreads = 32 * 23;
 constexpr int kAtom = T * 128;                       // 64 rows x 128 dims
 constexpr int kRopeOff = 4 * kAtom;
 constexpr int kUnit = 4 * kAtom + T * 64;            // a tile: 36 KB
 constexpr int kQr = 128 * 64;                        // rope query: [hi; lo] x 64 dims (64-byte swizzle)
 constexpr int kPPair = 64 * 128;                     // two parts of the weights: 64 heads x (64 + 64) rows
-constexpr int kXBytes = kSoftWarps * 32 * 64;        // scores on their way to the thread of the other part
+constexpr int kXBytes = kSoftWarps * 32 * 64;        // scores on their way to the thread of the other part, of a tile
 constexpr int kScSlots = 3;                          // tiles whose rows' numbers are held
-constexpr int kScDelay = 2;                          // they are written this many tiles after the gathers
 constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the scales, reciprocals
 constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
 constexpr float kLoWeight = 1.f / 32.f;              // value of a query's lo part
@@ -73,18 +80,19 @@ constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);
 template <bool kFine>
 struct Cfg {
   static constexpr int kPairs = kFine ? 2 : 1;       // pairs of weight parts
-  static constexpr int kUnits = kFine ? 4 : 5;
+  static constexpr int kUnits = 4;
   static constexpr int kPBuf = kPairs * kPPair;
   static constexpr int kOffQr = kUnits * kUnit;
   static constexpr int kOffP = kOffQr + kQr;
   static constexpr int kOffX = kOffP + 2 * kPBuf;
-  static constexpr int kOffSc = kOffX + kXBytes;
+  static constexpr int kOffSc = kOffX + 2 * kXBytes;
   static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [2][4][64] maxima, sums
   static constexpr int kOffBc = kOffRed + 2 * 4 * 64 * 4;       // [64] rescaling factors, 1 / l
   static constexpr int kOffFac = kOffBc + 64 * 4;               // [2][64] 2^-a of an item's heads
-  static constexpr int kOffBar = kOffFac + 2 * 64 * 4;
-  static constexpr int bFull = 0;                    // [kUnits] a tile's rows have landed, both CTAs' halves
-  static constexpr int bEmpty = bFull + kUnits;      // [kUnits] both CTAs have used it
+  static constexpr int kOffSlots = kOffFac + 2 * 64 * 4;        // [5][64] a tile's slots, for each gathering warp
+  static constexpr int kOffBar = kOffSlots + 5 * T * 4;
+  static constexpr int bFull = 0;                    // [kUnits] a tile's rows have landed
+  static constexpr int bEmpty = bFull + kUnits;      // [kUnits]
   static constexpr int bQFull = bEmpty + kUnits;
   static constexpr int bQEmpty = bQFull + 1;
   static constexpr int bFacFull = bQEmpty + 1;       // [2]
@@ -92,8 +100,7 @@ struct Cfg {
   static constexpr int bSFull = bFacEmpty + 2;       // [2]
   static constexpr int bSEmpty = bSFull + 2;         // [2]
   static constexpr int bPFull = bSEmpty + 2;         // [2]
-  static constexpr int bPDone = bPFull + 2;          // [2]
-  static constexpr int bOFull = bPDone + 2;
+  static constexpr int bOFull = bPFull + 2;
   static constexpr int bOEmpty = bOFull + 1;
   static constexpr int bScFull = bOEmpty + 1;        // [kScSlots]
   static constexpr int bScEmpty = bScFull + kScSlots;
@@ -116,17 +123,6 @@ __device__ __forceinline__ bool item_in_request(const DecodeParams& p, int b, in
   return lo <= s && e <= hi;
 }
 
-// A gather of four rows into the same place of both CTAs, counted on the
-// barrier of each.
-__device__ __forceinline__ void tma_gather4_both(uint32_t dst, const void* map, int x, const int (&y)[4], uint32_t bar,
-                                                 uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8, %9;" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar), "h"(static_cast<uint16_t>(3)), "l"(policy)
-      : "memory");
-}
-
 template <bool kFine>
 __global__ void __launch_bounds__(kThreads, 1)
     rows8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
@@ -137,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = static_cast<int>(cluster_ctarank());
+  const int cta = blockIdx.x & 1;                    // which half of the heads
   auto bar = [&](int i) -> uint32_t { return base + C::kOffBar + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -147,30 +143,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int Hc = p.heads >> 1;                       // this CTA's heads: [cta * Hc, (cta + 1) * Hc)
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bFull + i), 1); mbar_init(bar(C::bEmpty + i), 2); }
+    for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bFull + i), 1); mbar_init(bar(C::bEmpty + i), 1); }
     mbar_init(bar(C::bQFull), kQueryWarps);
     mbar_init(bar(C::bQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::bFacFull + i), 2); mbar_init(bar(C::bFacEmpty + i), kSoftWarps);
       mbar_init(bar(C::bSFull + i), 1); mbar_init(bar(C::bSEmpty + i), kSoftWarps);
-      mbar_init(bar(C::bPFull + i), kSoftWarps); mbar_init(bar(C::bPDone + i), 1);
+      mbar_init(bar(C::bPFull + i), kSoftWarps);
     }
     mbar_init(bar(C::bOFull), 1);
     mbar_init(bar(C::bOEmpty), kSoftWarps);
     for (int i = 0; i < kScSlots; ++i) { mbar_init(bar(C::bScFull + i), 1); mbar_init(bar(C::bScEmpty + i), kSoftWarps); }
-    mbar_init(bar(C::bDrain), 2);
+    mbar_init(bar(C::bDrain), 1);
     for (int i = 0; i < C::kUnits; ++i) last_armed[i] = -1;
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kPvWarp) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (warp == kLatentWarp && lane == 0) tma_prefetch_desc(&tm_lat);
+  if (warp == kLatentWarp0 && lane == 0) tma_prefetch_desc(&tm_lat);
   if (warp == kRopeWarp && lane == 0) tma_prefetch_desc(&tm_rope);
   tc_fence_before();
-  cluster_sync_all();                                // both CTAs' barriers exist before any remote use
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
@@ -188,82 +184,105 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   bool aborted = false;                              // of the softmax and query warps
 
-  if (warp == kLatentWarp || warp == kRopeWarp) {
-    // ------------------------------------------------------------- producers
-    // Latents: lane l gathers rows 4 (l / 4) .. of this CTA's half of the tile,
-    // atom l % 4.  Rope keys: lanes 0-7, four rows each.  An out-of-range slot
-    // reads row 0 and sets MLA_ERR_INDEX_OOB, the ragged tail repeats the last
-    // valid slot.  The slots are loaded a tile ahead.
+  if (warp == kScaleWarp) {
+    // --------------------------------------------------- the rows' scales
+    // Lane l has rows l and 32 + l of a tile.  Slots are loaded two tiles ahead
+    // and scales one (a random 4 bytes from memory), over all items.
+    int it = it0, s = 0, n = 0, t0 = 0;
+    auto next_slots = [&](int (&slot)[2]) -> bool {
+      while (t0 >= n) {                              // the next usable item
+        if (it >= it1) return false;
+        const int b = item_w(it, 0), s0 = item_w(it, 1), e = item_w(it, 2);
+        ++it;
+        if (!item_ok(p, nnz, b, s0, e)) {
+          if (lane == 0 && cta == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
+          continue;
+        }
+        if (lane == 0 && cta == 0 && !item_in_request(p, b, s0, e)) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
+        s = s0;
+        n = e - s0;
+        t0 = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) slot[i] = __ldg(p.kv_indices + s + min(t0 + lane + 32 * i, n - 1));
+      t0 += T;
+      return true;
+    };
+    auto load = [&](const int (&slot)[2], float (&r)[2]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool in = slot[i] >= 0 && static_cast<long long>(slot[i]) < p.num_slots;
+        if (!in) record_status(p.status, MLA_ERR_INDEX_OOB);
+        r[i] = __ldg(kv_scales + (in ? slot[i] : 0));
+      }
+    };
+    int slot[2] = {0, 0};
+    float next[2] = {1.f, 1.f};
+    bool more = next_slots(slot);
+    if (more) load(slot, next);
+    bool ahead = more && next_slots(slot);
+    for (uint32_t g = 0; more; ++g) {
+      const float r[2] = {row_scale(next[0]), row_scale(next[1])};
+      more = ahead;
+      if (more) {
+        load(slot, next);
+        ahead = next_slots(slot);
+      }
+      const uint32_t sl = g % kScSlots;
+      bool ok = true;
+      if (lane == 0 && g >= kScSlots) ok = mbar_wait(bar(C::bScEmpty + sl), (g / kScSlots - 1) & 1, wc);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      float* out = reinterpret_cast<float*>(smem + C::kOffSc + sl * kScSlot);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        out[lane + 32 * i] = r[i] * p.scale_log2;
+        out[T + lane + 32 * i] = __log2f(r[i]);
+        out[2 * T + lane + 32 * i] = __frcp_rn(r[i]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::bScFull + sl));
+    }
+  } else if (warp >= kLatentWarp0) {
+    // ------------------------------------------------------------- gathers
+    // A latent atom of the tile, or the rope keys, by 16 gathers of four rows.
+    // The warp loads and checks the slots (a tile ahead; lane l has rows l and 32
+    // + l) and leaves them in shared memory, one elected lane issues: the
+    // operands of a gather are uniform registers, and lanes that issue with their
+    // own make the compiler build them one lane after another (230 cycles each).
+    // An out-of-range slot reads row 0 (the scales' warp records it), the ragged
+    // tail repeats the last valid slot.
+    const bool lead = elect_one();
+    const int atom = warp - kLatentWarp0;
     const bool rope = warp == kRopeWarp;
-    const int grp = rope ? lane & 7 : lane >> 2;
-    const int tb = 32 * cta + 4 * grp;
-    const bool active = !rope || lane < 8;
-    const int x = rope ? kLatent : 128 * (lane & 3);
-    const uint32_t dst = rope ? kRopeOff + tb * 64 : (lane & 3) * kAtom + tb * 128;
+    const int x = rope ? kLatent : 128 * atom;
+    const uint32_t dst = base + (rope ? kRopeOff : atom * kAtom), step = rope ? 4 * 64 : 4 * 128;
+    const CUtensorMap* map = rope ? &tm_rope : &tm_lat;
+    int* slots = reinterpret_cast<int*>(smem + C::kOffSlots) + T * atom;
+    const int4* quads = reinterpret_cast<const int4*>(slots);
     const uint64_t pol = l2_policy_evict_first();
     int it = it0, s = 0, n = 0, t0 = 0;
     auto next_item = [&]() {
       for (; it < it1; ++it) {
         const int b = item_w(it, 0), s0 = item_w(it, 1), e = item_w(it, 2);
-        if (item_ok(p, nnz, b, s0, e)) {
-          if (rope && lane == 0 && cta == 0 && !item_in_request(p, b, s0, e)) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
-          s = s0;
-          n = e - s0;
-          return;
-        }
-        if (rope && lane == 0 && cta == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
+        if (!item_ok(p, nnz, b, s0, e)) continue;
+        s = s0;
+        n = e - s0;
+        return;
       }
     };
-    int vn[4] = {0, 0, 0, 0}, sn[2] = {0, 0};
+    int next[2] = {0, 0};
     auto load_slots = [&]() {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) vn[k] = __ldg(p.kv_indices + s + min(t0 + tb + k, n - 1));
-      if (rope)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) sn[i] = __ldg(p.kv_indices + s + min(t0 + lane + 32 * i, n - 1));
-    };
-    // The rope producer also makes the numbers of the rows' scales (lane i has
-    // rows i and 32 + i): a tile's scales are loaded once its gathers are out,
-    // the numbers written kScDelay tiles later.
-    float val[2] = {1.f, 1.f}, hold[2] = {1.f, 1.f};
-    auto scale_step = [&](uint32_t g, const int* slot) -> bool {
-      if (g >= kScDelay) {
-        const uint32_t k = g - kScDelay, sl = k % kScSlots;
-        bool free = true;
-        if (lane == 0 && k >= kScSlots) free = mbar_wait(bar(C::bScEmpty + sl), (k / kScSlots - 1) & 1, wc);
-        if (!__shfl_sync(0xffffffffu, free, 0)) return false;
-        float* out = reinterpret_cast<float*>(smem + C::kOffSc + sl * kScSlot);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float r = row_scale(hold[i]);
-          out[lane + 32 * i] = r * p.scale_log2;
-          out[T + lane + 32 * i] = __log2f(r);
-          out[2 * T + lane + 32 * i] = __frcp_rn(r);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::bScFull + sl));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        hold[i] = val[i];
-        if (slot) val[i] = __ldg(kv_scales + (slot[i] >= 0 && static_cast<long long>(slot[i]) < p.num_slots ? slot[i] : 0));
-      }
-      return true;
+      for (int i = 0; i < 2; ++i) next[i] = __ldg(p.kv_indices + s + min(t0 + lane + 32 * i, n - 1));
     };
     next_item();
     if (it < it1) load_slots();
     uint32_t g = 0;
-    bool ok = true;
-    while (it < it1 && ok) {
-      int v[4];
-      const int sv[2] = {sn[0], sn[1]};
-      bool oob = false;
+    while (it < it1) {
+      __syncwarp();                                  // (the slots of the tile before have been read)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = vn[k];
-        if (v[k] < 0 || static_cast<long long>(v[k]) >= p.num_slots) { oob = true; v[k] = 0; }
-      }
-      if (oob && rope) record_status(p.status, MLA_ERR_INDEX_OOB);
+      for (int i = 0; i < 2; ++i)
+        slots[lane + 32 * i] = next[i] < 0 || static_cast<long long>(next[i]) >= p.num_slots ? 0 : next[i];
       t0 += T;
       if (t0 >= n) {
         ++it;
@@ -272,101 +291,121 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (it < it1) load_slots();
       const uint32_t slot = g % C::kUnits, use = g / C::kUnits;
-      bool e_ok = true;
-      if (lane == 0 && use > 0) e_ok = mbar_wait<true>(bar(C::bEmpty + slot), (use - 1) & 1, wc);
-      if (!__shfl_sync(0xffffffffu, e_ok, 0)) { ok = false; break; }
-      if (!rope && lane == 0) {
-        mbar_arrive_expect_tx(bar(C::bFull + slot), kUnit);
-        last_armed[slot] = static_cast<int>(use);
+      if (!__all_sync(0xffffffffu, use == 0 || mbar_wait(bar(C::bEmpty + slot), (use - 1) & 1, wc))) break;
+      const uint32_t full = bar(C::bFull + slot), to = dst + slot * kUnit;
+      if (lead) {
+        if (atom == 0) {
+          mbar_arrive_expect_tx(full, kUnit);
+          last_armed[slot] = static_cast<int>(use);
+        }
+#pragma unroll
+        for (int i = 0; i < T / 4; ++i) {
+          const int4 y = quads[i];
+          tma_gather4(to + i * step, map, x, y.x, y.y, y.z, y.w, full, pol);
+        }
       }
-      __syncwarp();
-      if (active) tma_gather4_both(base + slot * kUnit + dst, rope ? &tm_rope : &tm_lat, x, v, bar(C::bFull + slot), pol);
-      if (rope && !scale_step(g, sv)) { ok = false; break; }
       ++g;
     }
-    if (rope)
-      for (uint32_t i = 0; i < kScDelay && ok; ++i) ok = scale_step(g + i, nullptr);
-    named_bar_sync(kBarGather, 64);
-    if (!rope && lane < C::kUnits) {                 // no copy outlives the block
+    __syncwarp();
+    named_bar_sync(kBarGather, 5 * 32);
+    if (atom == 0 && lane < C::kUnits) {             // no copy outlives the block
       const int u = last_armed[lane];
       if (u >= 0) drain_wait(bar(C::bFull + lane), u & 1);
     }
     __syncwarp();
-  } else if (warp == kQkWarp) {
-    // ------------------------------------------------------------- QK issuer
-    if (lane == 0) {
-      const uint64_t dk = sdesc(base, 16, 1024);
-      const uint64_t dr = sdesc(base + kRopeOff, 16, 512, kLayoutSw64);
-      const uint64_t dq = sdesc(base + C::kOffQr, 16, 512, kLayoutSw64);
-      auto D = [](uint64_t d, uint32_t byte_off) -> uint64_t { return d + (byte_off >> 4); };
-      uint32_t g = 0, nitem = 0;
-      bool ok = true;
-      for (int it = it0; it < it1 && ok; ++it) {
-        const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------------------- products
+    // The whole warp runs the loop and one elected lane issues, so that
+    // descriptors and counters stay in uniform registers.
+    const bool lead = elect_one();
+    const int cols = (Hc + 15) & ~15;                // columns that hold heads
+    const uint32_t idesc4 = idesc_e4m3(128, cols, true, false);
+    const uint32_t idesc5 = idesc_f8(kFmtE4M3, kFmtE5M2, 128, cols, true, false);
+    const uint64_t dk = sdesc(base, 16, 1024), dv = sdesc(base, kAtom, 1024);
+    const uint64_t dr = sdesc(base + kRopeOff, 16, 512, kLayoutSw64);
+    const uint64_t dq = sdesc(base + C::kOffQr, 16, 512, kLayoutSw64);
+    const uint64_t dp = sdesc(base + C::kOffP, 16, 1024);
+    auto D = [](uint64_t d, uint32_t byte_off) -> uint64_t { return d + (byte_off >> 4); };
+    struct Cursor {                                  // tile j of nt of usable item `count`
+      int it, j, nt;
+      uint32_t count;
+    };
+    auto find = [&](Cursor& c) {
+      for (; c.it < it1; ++c.it) {
+        const int b = item_w(c.it, 0), s = item_w(c.it, 1), e = item_w(c.it, 2);
         if (!item_ok(p, nnz, b, s, e)) continue;
-        const int nt = (e - s + T - 1) / T;
-        if (!mbar_wait(bar(C::bQFull), nitem & 1, wc)) break;
-        for (int j = 0; j < nt; ++j, ++g) {
-          const uint32_t buf = g & 1, slot = g % C::kUnits;
-          const uint32_t d_s = tmem + kTmS + buf * T;
-          if (g >= 2 && !mbar_wait(bar(C::bSEmpty + buf), ((g >> 1) - 1) & 1, wc)) { ok = false; break; }
-          if (!mbar_wait<true>(bar(C::bFull + slot), (g / C::kUnits) & 1, wc)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t bk = D(dk, slot * kUnit), br = D(dr, slot * kUnit);
-#pragma unroll
-          for (int k = 0; k < 16; ++k)               // 512 latent dims, A from TMEM
-            umma_ts_f8(d_s, tmem + kTmQ + 8 * k, D(bk, (k >> 2) * kAtom + (k & 3) * 32), kIdescQK, k != 0 ? 1u : 0u);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) umma_ss_f8(d_s, D(dq, 32 * k), D(br, 32 * k), kIdescQK, 1u);
-          umma_commit(bar(C::bSFull + buf));
-          if (j == nt - 1) umma_commit(bar(C::bQEmpty));
-        }
-        ++nitem;
+        c.nt = (e - s + T - 1) / T;
+        return;
       }
-      umma_commit(bar(C::bDrain));
-      drain_wait(bar(C::bDrain), 0);
-    }
-    __syncwarp();
-  } else if (warp == kPvWarp) {
-    // ------------------------------------------------------------- PV issuer
-    if (lane == 0) {
-      const int cols = (Hc + 15) & ~15;              // columns that hold heads
-      const uint32_t idesc4 = idesc_e4m3(128, cols, true, false);
-      const uint32_t idesc5 = idesc_f8(kFmtE4M3, kFmtE5M2, 128, cols, true, false);
-      const uint64_t dv = sdesc(base, kAtom, 1024);
-      const uint64_t dp = sdesc(base + C::kOffP, 16, 1024);
-      auto D = [](uint64_t d, uint32_t byte_off) -> uint64_t { return d + (byte_off >> 4); };
-      uint32_t g = 0, nitem = 0;
-      bool ok = true;
-      for (int it = it0; it < it1 && ok; ++it) {
-        const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
-        if (!item_ok(p, nnz, b, s, e)) continue;
-        const int nt = (e - s + T - 1) / T;
-        for (int j = 0; j < nt; ++j, ++g) {
-          const uint32_t buf = g & 1, slot = g % C::kUnits;
-          if (!mbar_wait(bar(C::bPFull + buf), (g >> 1) & 1, wc)) { ok = false; break; }
-          if (j == 0 && nitem > 0 && !mbar_wait(bar(C::bOEmpty), (nitem - 1) & 1, wc)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t av = D(dv, slot * kUnit), bp = D(dp, buf * C::kPBuf);
+    };
+    auto step = [&](Cursor& c) {
+      if (++c.j < c.nt) return;
+      c.j = 0;
+      ++c.it;
+      ++c.count;
+      find(c);
+    };
+    auto scores = [&](uint32_t g, const Cursor& c) -> bool {
+      const uint32_t buf = g & 1, slot = g % C::kUnits;
+      if (c.j == 0 && !mbar_wait(bar(C::bQFull), c.count & 1, wc)) return false;
+      if (g >= 2 && !mbar_wait(bar(C::bSEmpty + buf), ((g >> 1) - 1) & 1, wc)) return false;
+      if (!mbar_wait(bar(C::bFull + slot), (g / C::kUnits) & 1, wc)) return false;
+      tc_fence_after();
+      const uint32_t d_s = tmem + kTmS + buf * T;
+      const uint64_t bk = D(dk, slot * kUnit), br = D(dr, slot * kUnit);
+      if (lead) {
 #pragma unroll
-          for (int mb = 0; mb < 4; ++mb)
+        for (int k = 0; k < 16; ++k)                 // 512 latent dims, A from TMEM
+          umma_ts_f8(d_s, tmem + kTmQ + 8 * k, D(bk, (k >> 2) * kAtom + (k & 3) * 32), kIdescQK, k != 0 ? 1u : 0u);
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {         // 32 rows
-              const uint64_t a = D(av, mb * kAtom + 4096 * ks);
-              const uint32_t d = tmem + kTmO + 64 * mb;
-              umma_ss_f8(d, a, D(bp, 32 * ks), idesc4, (j == 0 && ks == 0) ? 0u : 1u);
-              umma_ss_f8(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
-              if constexpr (kFine) {
-                umma_ss_f8(d, a, D(bp, kPPair + 32 * ks), idesc4, 1u);
-                umma_ss_f8(d, a, D(bp, kPPair + 64 + 32 * ks), idesc5, 1u);
-              }
+        for (int k = 0; k < 2; ++k) umma_ss_f8(d_s, D(dq, 32 * k), D(br, 32 * k), kIdescQK, 1u);
+        umma_commit(bar(C::bSFull + buf));
+        if (c.j == c.nt - 1) umma_commit(bar(C::bQEmpty));
+      }
+      return true;
+    };
+    auto weighted = [&](uint32_t g, const Cursor& c) -> bool {
+      const uint32_t buf = g & 1, slot = g % C::kUnits;
+      if (!mbar_wait(bar(C::bPFull + buf), (g >> 1) & 1, wc)) return false;
+      if (c.j == 0 && c.count > 0 && !mbar_wait(bar(C::bOEmpty), (c.count - 1) & 1, wc)) return false;
+      tc_fence_after();
+      const uint64_t av = D(dv, slot * kUnit), bp = D(dp, buf * C::kPBuf);
+      if (lead) {
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {           // 32 rows
+            const uint64_t a = D(av, mb * kAtom + 4096 * ks);
+            const uint32_t d = tmem + kTmO + 64 * mb;
+            umma_ss_f8(d, a, D(bp, 32 * ks), idesc4, (c.j == 0 && ks == 0) ? 0u : 1u);
+            umma_ss_f8(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
+            if constexpr (kFine) {
+              umma_ss_f8(d, a, D(bp, kPPair + 32 * ks), idesc4, 1u);
+              umma_ss_f8(d, a, D(bp, kPPair + 64 + 32 * ks), idesc5, 1u);
             }
-          umma_commit_mc(bar(C::bEmpty + slot), 3);  // both CTAs may fill it again once both have used it
-          umma_commit(bar(C::bPDone + buf));
-          if (j == nt - 1) umma_commit(bar(C::bOFull));
-        }
-        ++nitem;
+          }
+        umma_commit(bar(C::bEmpty + slot));
+        if (c.j == c.nt - 1) umma_commit(bar(C::bOFull));
       }
+      return true;
+    };
+    Cursor qk{it0, 0, 0, 0}, pv{it0, 0, 0, 0};
+    find(qk);
+    find(pv);
+    uint32_t gq = 0, gp = 0;
+    bool ok = true;
+    while (ok && pv.it < it1) {
+      while (ok && qk.it < it1 && gq <= gp + 2) {
+        ok = scores(gq, qk);
+        ++gq;
+        step(qk);
+      }
+      if (!ok) break;
+      ok = weighted(gp, pv);
+      ++gp;
+      step(pv);
+    }
+    if (lead) {
       umma_commit(bar(C::bDrain));
       drain_wait(bar(C::bDrain), 0);
     }
@@ -435,21 +474,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         w0 = c[0] | (c[1] << 16);
         w1 = c[2] | (c[3] << 16);
       };
-      uint32_t code[4][16], rope[8];
+      // half of this warp's dims wait in registers, the other half comes from L1 once they are stored
+      uint32_t code[2][16], rope[8];
       const uint4 zero = make_uint4(0, 0, 0, 0);
+      auto codes = [&](int c0) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          part8(head_ok ? __ldg(qn + 32 * half + 8 * c + k) : zero, code[c][2 * k], code[c][2 * k + 1]);
+          for (int k = 0; k < 8; ++k)
+            part8(head_ok ? __ldg(qn + 32 * half + 8 * (c0 + c) + k) : zero, code[c][2 * k], code[c][2 * k + 1]);
+      };
+      codes(0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) part8(head_ok ? __ldg(qr + 4 * half + k) : zero, rope[2 * k], rope[2 * k + 1]);
       if (nitem > 0) wait(bar(C::bQEmpty), (nitem - 1) & 1);
       tc_fence_after();
+      const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmQ + 64 * half;
       if (!aborted) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_st16(tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmQ + 64 * half + 16 * c, code[c]);
+        tmem_st16(tq, code[0]);
+        tmem_st16(tq + 16, code[1]);
+      }
+      codes(2);
+      if (!aborted) {
+        tmem_st16(tq + 32, code[0]);
+        tmem_st16(tq + 48, code[1]);
         tmem_wait_st();
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -468,18 +516,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, th = warp >> 2, part = q >> 1;
     const int hl = 32 * (q & 1) + lane;              // head of this CTA
     const uint32_t quad = static_cast<uint32_t>(32 * q) << 16;
-    float4* x_own = reinterpret_cast<float4*>(smem + C::kOffX) + warp * 128 + lane;
-    const float4* x_other = reinterpret_cast<const float4*>(smem + C::kOffX) + (warp ^ 2) * 128 + lane;
     float* red = reinterpret_cast<float*>(smem + C::kOffRed);
     float* bc = reinterpret_cast<float*>(smem + C::kOffBc);
     const int four = 2 * th + part;                  // which 16 rows of a tile
     float m_ref = 0.f, l_sum = 0.f, fac = 1.f;
     int rk = 0;
-    auto wait = [&](uint32_t bb, uint32_t par) {
-      if (aborted) return;
-      bool r = true;
-      if (lane == 0) r = mbar_wait(bb, par, wc);
-      if (!__shfl_sync(0xffffffffu, r, 0)) aborted = true;
+    auto wait = [&](uint32_t bb, uint32_t par) {     // (every lane for itself: a third of the time of one for all)
+      if (!aborted && !__all_sync(0xffffffffu, mbar_wait(bb, par, wc))) aborted = true;
     };
     // this head's four values, of the four threads that share it
     auto share = [&](float v, float (&all)[4]) {
@@ -490,6 +533,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 4; ++i) all[i] = r[i * 64 + hl];
       ++rk;
     };
+    uint32_t kept[16];                               // this part's scores of a tile's 16 rows, on their way
+    float2 x[8];                                     // exponents of a tile's 16 rows
+    // Scores of tile g, from TMEM: the thread of the hi part keeps rows 0-15 of these 32 and sends the others, that
+    // of the lo part the other way round.
+    auto load_scores = [&](uint32_t g) {
+      wait(bar(C::bSFull + (g & 1)), (g >> 1) & 1);
+      uint32_t sent[16];
+      if (!aborted) {
+        tc_fence_after();
+        const uint32_t ts = tmem + quad + kTmS + T * (g & 1) + 32 * th;
+        tmem_ld16(ts + 16 * (1 - part), sent);
+        tmem_ld16(ts + 16 * part, kept);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) kept[i] = sent[i] = 0;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && !aborted) mbar_arrive(bar(C::bSEmpty + (g & 1)));
+      uint4* xo = reinterpret_cast<uint4*>(smem + C::kOffX + (g & 1) * kXBytes) + warp * 128 + lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) xo[32 * k] = make_uint4(sent[4 * k], sent[4 * k + 1], sent[4 * k + 2], sent[4 * k + 3]);
+    };
+    // the other part's scores and the exponents; their largest
+    const float w_own = part == 0 ? 1.f : kLoWeight, w_other = part == 0 ? kLoWeight : 1.f;
+    auto exponents = [&](uint32_t g, int left) -> float {
+      wait(bar(C::bScFull + g % kScSlots), (g / kScSlots) & 1);
+      named_bar_sync(kBarPair0 + 2 * (q & 1) + th, 64);
+      const float4* xi = reinterpret_cast<const float4*>(smem + C::kOffX + (g & 1) * kXBytes) + (warp ^ 2) * 128 + lane;
+      const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 4 * four;
+      const float2 f_own = f2_pack(fac * w_own, fac * w_own), f_other = f2_pack(fac * w_other, fac * w_other);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 o = xi[32 * k], f = sc[k], lg = sc[T / 4 + k];
+        float2 t = f2_mul(f2_pack(__uint_as_float(kept[4 * k]), __uint_as_float(kept[4 * k + 1])), f_own);
+        x[2 * k] = f2_fma(f2_fma(f2_pack(o.x, o.y), f_other, t), f2_pack(f.x, f.y), f2_pack(lg.x, lg.y));
+        t = f2_mul(f2_pack(__uint_as_float(kept[4 * k + 2]), __uint_as_float(kept[4 * k + 3])), f_own);
+        x[2 * k + 1] = f2_fma(f2_fma(f2_pack(o.z, o.w), f_other, t), f2_pack(f.z, f.w), f2_pack(lg.z, lg.w));
+      }
+      const int nvalid = left - 16 * four;
+      if (nvalid < 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (2 * i >= nvalid) x[i].x = -INFINITY;
+          if (2 * i + 1 >= nvalid) x[i].y = -INFINITY;
+        }
+      }
+      float m0 = fmaxf(x[0].x, x[0].y), m1 = fmaxf(x[1].x, x[1].y);
+#pragma unroll
+      for (int i = 2; i < 8; i += 2) {
+        m0 = max3(m0, x[i].x, x[i].y);
+        m1 = max3(m1, x[i + 1].x, x[i + 1].y);
+      }
+      return fmaxf(m0, m1);
+    };
     uint32_t g = 0, nitem = 0;
     for (int it = it0; it < it1; ++it) {
       const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2), dest = item_w(it, 3);
@@ -499,61 +598,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       fac = reinterpret_cast<const float*>(smem + C::kOffFac)[64 * (nitem & 1) + hl];
       __syncwarp();
       if (lane == 0 && !aborted) mbar_arrive(bar(C::bFacEmpty + (nitem & 1)));
+      l_sum = 0.f;
+      m_ref = -INFINITY;                             // (the first tile asks for a reference)
+      load_scores(g);
+      float mx = exponents(g, n);
       for (int j = 0; j < nt; ++j, ++g) {
         const uint32_t buf = g & 1;
-        wait(bar(C::bSFull + buf), (g >> 1) & 1);
-        uint32_t sv[32];
-        if (!aborted) {
-          tc_fence_after();
-          tmem_ld16(tmem + quad + kTmS + T * buf + 32 * th, *reinterpret_cast<uint32_t(*)[16]>(sv));
-          tmem_ld16(tmem + quad + kTmS + T * buf + 32 * th + 16, *reinterpret_cast<uint32_t(*)[16]>(sv + 16));
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) sv[i] = 0;
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && !aborted) mbar_arrive(bar(C::bSEmpty + buf));
-        // the thread of the hi part keeps rows 0-15 of these 32, that of the lo part rows 16-31
-        float x[16];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int keep = 4 * k, send = 16 + 4 * k;
-          if (part == 0) {
-            x_own[32 * k] = make_float4(__uint_as_float(sv[send]), __uint_as_float(sv[send + 1]),
-                                        __uint_as_float(sv[send + 2]), __uint_as_float(sv[send + 3]));
-          } else {
-            x_own[32 * k] = make_float4(__uint_as_float(sv[keep]), __uint_as_float(sv[keep + 1]),
-                                        __uint_as_float(sv[keep + 2]), __uint_as_float(sv[keep + 3]));
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[4 * k + i] = part == 0 ? __uint_as_float(sv[keep + i]) : __uint_as_float(sv[send + i]) * kLoWeight;
-        }
-        named_bar_sync(kBarPair0 + 2 * (q & 1) + th, 64);
-        const float w_other = part == 0 ? kLoWeight : 1.f;
-        wait(bar(C::bScFull + g % kScSlots), (g / kScSlots) & 1);
-        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 4 * four;
-        float mx = -INFINITY;
-        const int nvalid = n - j * T - 16 * four;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 o = x_other[32 * k], f = sc[k], lg = sc[T / 4 + k];
-          const float ov[4] = {o.x, o.y, o.z, o.w}, fv[4] = {f.x, f.y, f.z, f.w}, lv[4] = {lg.x, lg.y, lg.z, lg.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = fmaf(fmaf(ov[i], w_other, x[4 * k + i]) * fac, fv[i], lv[i]);
-            x[4 * k + i] = 4 * k + i < nvalid ? v : -INFINITY;
-            mx = fmaxf(mx, x[4 * k + i]);
-          }
-        }
-        if (j == 0) {
-          float all[4];
-          share(mx, all);
-          m_ref = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
-          l_sum = 0.f;
-        } else if (named_bar_or(kBarVote, 32 * kSoftWarps, mx > m_ref + kLag)) {
+        if (j + 1 < nt) load_scores(g + 1);          // (the sum of tile g - 2 is done, then: its weights may go)
+        if (named_bar_or(kBarVote, 32 * kSoftWarps, mx > m_ref + kLag)) {
           float all[4];
           share(mx, all);
           const float mn = fmaxf(m_ref, fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])));
@@ -562,55 +614,59 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_sum *= alpha;
           if (four == 0) bc[hl] = alpha;
           named_bar_sync(kBarAll, 32 * kSoftWarps);
-          wait(bar(C::bPDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
-          tc_fence_after();
-          if (!aborted) {
-            // this warp's 32 dims of blocks 2 th and 2 th + 1, 16 heads at a time
+          if (j > 0) {
+            const uint32_t gp = g - 1;               // its sum is done once its rows are free
+            wait(bar(C::bEmpty + gp % C::kUnits), (gp / C::kUnits) & 1);
+            tc_fence_after();
+            if (!aborted) {
+              // this warp's 32 dims of blocks 2 th and 2 th + 1, 16 heads at a time
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t o[16];
-              const uint32_t ta = tmem + quad + kTmO + 128 * th + 16 * c;
-              tmem_ld16(ta, o);
-              tmem_wait_ld();
-              const float4* al = reinterpret_cast<const float4*>(bc) + 4 * (c & 3);
+              for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                const uint32_t ta = tmem + quad + kTmO + 128 * th + 16 * c;
+                tmem_ld16(ta, o);
+                tmem_wait_ld();
+                const float4* al = reinterpret_cast<const float4*>(bc) + 4 * (c & 3);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 f = al[i];
-                o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f.x);
-                o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f.y);
-                o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f.z);
-                o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f.w);
+                for (int i = 0; i < 4; ++i) {
+                  const float4 f = al[i];
+                  o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f.x);
+                  o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f.y);
+                  o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f.z);
+                  o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f.w);
+                }
+                tmem_st16(ta, o);
               }
-              tmem_st16(ta, o);
+              tmem_wait_st();
             }
-            tmem_wait_st();
           }
         }
         // weights and their parts; 16 rows are one 16-byte chunk of each
+        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 4 * four;
         uint32_t w0[4], w1[4], w2[4], w3[4];
-        const float shift = kTop - m_ref;
+        const float2 shift = f2_pack(kTop - m_ref, kTop - m_ref);
+        float2 l2 = f2_pack(0.f, 0.f), l3 = l2;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float4 iv = sc[2 * T / 4 + k];
           uint32_t c0[2], c1[2], c2[2], c3[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float a = ex2_approx(x[4 * k + 2 * i] + shift), z = ex2_approx(x[4 * k + 2 * i + 1] + shift);
-            l_sum = fmaf(a, i ? iv.z : iv.x, l_sum);
-            l_sum = fmaf(z, i ? iv.w : iv.y, l_sum);
+            const float2 e2 = f2_add(x[2 * k + i], shift);
+            float2 r = f2_pack(ex2_approx(e2.x), ex2_approx(e2.y));
+            if (i == 0) l2 = f2_fma(r, f2_pack(iv.x, iv.y), l2);
+            else l3 = f2_fma(r, f2_pack(iv.z, iv.w), l3);
             if constexpr (kFine) {
-              c0[i] = e4m3x2(a, z);
-              float2 h = e4m3x2_value(c0[i]);
-              float ra = a - h.x, rz = z - h.y;      // (exact, like the next two)
-              c1[i] = e4m3x2(ra, rz);
-              h = e4m3x2_value(c1[i]);
-              ra -= h.x;
-              rz -= h.y;
-              c2[i] = e4m3x2(ra, rz);
-              h = e4m3x2_value(c2[i]);
-              c3[i] = e5m2x2(ra - h.x, rz - h.y);
+              const float2 minus = f2_pack(-1.f, -1.f);
+              c0[i] = e4m3x2(r.x, r.y);
+              r = f2_fma(e4m3x2_value(c0[i]), minus, r);   // (exact, like the next two)
+              c1[i] = e4m3x2(r.x, r.y);
+              r = f2_fma(e4m3x2_value(c1[i]), minus, r);
+              c2[i] = e4m3x2(r.x, r.y);
+              r = f2_fma(e4m3x2_value(c2[i]), minus, r);
+              c3[i] = e5m2x2(r.x, r.y);
             } else {
-              e4m3x2_split(a, z, c0[i], c1[i]);
+              e4m3x2_split(r.x, r.y, c0[i], c1[i]);
             }
           }
           w0[k] = c0[0] | (c0[1] << 16);
@@ -620,7 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             w3[k] = c3[0] | (c3[1] << 16);
           }
         }
-        if (g >= 2) wait(bar(C::bPDone + buf), ((g >> 1) - 1) & 1);
+        l2 = f2_add(l2, l3);
+        l_sum += l2.x + l2.y;
+        if (j + 1 == nt && g >= 2) {                 // no later scores have said so
+          const uint32_t gp = g - 2;
+          wait(bar(C::bEmpty + gp % C::kUnits), (gp / C::kUnits) & 1);
+        }
         if (!aborted) {
           uint8_t* row = smem + C::kOffP + buf * C::kPBuf + hl * 128;
           const int sw = hl & 7;
@@ -638,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(bar(C::bPFull + buf));
           mbar_arrive(bar(C::bScEmpty + g % kScSlots));
         }
+        if (j + 1 < nt) mx = exponents(g + 1, n - (j + 1) * T);
       }
       // ---------------------------------------------------------------- epilogue
       const bool part_ok = dest < p.max_partials;    // a device-only plan naming a partial past the workspace
@@ -685,9 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
-  cluster_sync_all();                                // no CTA leaves while the other may still write or signal to it
+  __syncthreads();
   tc_fence_after();
-  if (warp == kPvWarp) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 template <bool kFine>
@@ -700,15 +762,11 @@ int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodePa
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg<kFine>::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kernel, tm_lat, tm_rope, p, kv_scales) != cudaSuccess) return MLA_ERR_CUDA;
   return cudaPeekAtLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
