@@ -40,18 +40,17 @@
 // TMEM (512 columns): O^T [0, 256), the query [256, 384), two score buffers.
 //
 // Warps:
-//   0-7    softmax and epilogue.  A thread of lane quadrant q reads its part
+//   0-7    softmax.  A thread of lane quadrant q reads its part
 //          (hi: q < 2) of a head's scores for 32 rows, exchanges half of them with
 //          the thread that has the other part, and goes on with 16 rows.
-//   8-15   the next item's query: largest element, parts in registers while the
-//          item before is worked on, then into TMEM and shared memory
-//   16     TMEM allocator, issuer of all products: the scores of tile g + 2, then
-//          the weighted sum of tile g.  They run in that order, so that scores of
-//          g + 1 that are there say that the sum of g - 2 is done.
-//   17-20  gathers of the latents, an atom each: 16 of four rows a tile (a warp
+//   8-15   the next item's query (its largest elements, and half of the parts in
+//          registers, while the item before is worked on; then into TMEM and
+//          shared memory), and the output of the item before
+//   16     issuer of the scores     17  TMEM allocator, issuer of the weighted sums
+//   18-21  gathers of the latents, an atom each: 16 of four rows a tile (a warp
 //          takes some 60 cycles for each of a burst, so they are spread)
-//   21     gathers of the rope keys
-//   22     the numbers made of the rows' scales
+//   22     gathers of the rope keys
+//   23     the numbers made of the rows' scales
 #include "mla_device.cuh"
 #include "mla_launch.h"
 
@@ -60,8 +59,8 @@ namespace rows8 {
 
 constexpr int T = 64;                                // rows of a tile
 constexpr int kSoftWarps = 8, kQueryWarps = 8;
-constexpr int kQueryWarp0 = 8, kMmaWarp = 16, kLatentWarp0 = 17, kRopeWarp = 21, kScaleWarp = 22;
-constexpr int kThreads = 32 * 23;
+constexpr int kQueryWarp0 = 8, kQkWarp = 16, kPvWarp = 17, kLatentWarp0 = 18, kRopeWarp = 22, kScaleWarp = 23;
+constexpr int kThreads = 32 * 24;
 constexpr int kAtom = T * 128;                       // 64 rows x 128 dims
 constexpr int kRopeOff = 4 * kAtom;
 constexpr int kUnit = 4 * kAtom + T * 64;            // a tile: 36 KB
@@ -73,7 +72,7 @@ constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the sca
 constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
 constexpr float kLoWeight = 1.f / 32.f;              // value of a query's lo part
 constexpr float kTop = 5.f, kLag = 3.f;              // weights are 2^(e - m + kTop) with e <= m + kLag
-constexpr int kBarPair0 = 1, kBarAll = 5, kBarVote = 6, kBarGather = 7;   // named barriers
+constexpr int kBarPair0 = 1, kBarAll = 5, kBarVote = 6, kBarGather = 7, kBarQuery = 8;   // named barriers
 constexpr int kTmO = 0, kTmQ = 256, kTmS = 384;
 constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);
 
@@ -89,7 +88,9 @@ struct Cfg {
   static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [2][4][64] maxima, sums
   static constexpr int kOffBc = kOffRed + 2 * 4 * 64 * 4;       // [64] rescaling factors, 1 / l
   static constexpr int kOffFac = kOffBc + 64 * 4;               // [2][64] 2^-a of an item's heads
-  static constexpr int kOffSlots = kOffFac + 2 * 64 * 4;        // [5][64] a tile's slots, for each gathering warp
+  static constexpr int kOffSum = kOffFac + 2 * 64 * 4;          // [2][4][64] an item's sums, for the output
+  static constexpr int kOffRef = kOffSum + 2 * 4 * 64 * 4;      // [2][64] and references
+  static constexpr int kOffSlots = kOffRef + 2 * 64 * 4;        // [5][64] a tile's slots, for each gathering warp
   static constexpr int kOffBar = kOffSlots + 5 * T * 4;
   static constexpr int bFull = 0;                    // [kUnits] a tile's rows have landed
   static constexpr int bEmpty = bFull + kUnits;      // [kUnits]
@@ -102,11 +103,14 @@ struct Cfg {
   static constexpr int bPFull = bSEmpty + 2;         // [2]
   static constexpr int bOFull = bPFull + 2;
   static constexpr int bOEmpty = bOFull + 1;
-  static constexpr int bScFull = bOEmpty + 1;        // [kScSlots]
+  static constexpr int bSumFull = bOEmpty + 1;       // [2]
+  static constexpr int bSumEmpty = bSumFull + 2;     // [2]
+  static constexpr int bScFull = bSumEmpty + 2;      // [kScSlots]
   static constexpr int bScEmpty = bScFull + kScSlots;
   static constexpr int bDrain = bScEmpty + kScSlots;
   static constexpr int kNumBars = bDrain + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffMoved = kOffMisc + 8;     // [2] heads whose reference moved
   static constexpr int kOffLast = kOffMisc + 16;     // [kUnits] last armed use
   static constexpr int kOffItems = (kOffLast + 4 * kUnits + 15) / 16 * 16;
   static constexpr int kSmemBytes = kOffItems + 16 * kItemCache + 1024;
@@ -147,19 +151,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(C::bQFull), kQueryWarps);
     mbar_init(bar(C::bQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::bFacFull + i), 2); mbar_init(bar(C::bFacEmpty + i), kSoftWarps);
+      mbar_init(bar(C::bFacFull + i), kQueryWarps); mbar_init(bar(C::bFacEmpty + i), kSoftWarps);
       mbar_init(bar(C::bSFull + i), 1); mbar_init(bar(C::bSEmpty + i), kSoftWarps);
       mbar_init(bar(C::bPFull + i), kSoftWarps);
+      mbar_init(bar(C::bSumFull + i), kSoftWarps); mbar_init(bar(C::bSumEmpty + i), kQueryWarps);
     }
     mbar_init(bar(C::bOFull), 1);
-    mbar_init(bar(C::bOEmpty), kSoftWarps);
+    mbar_init(bar(C::bOEmpty), kQueryWarps);
     for (int i = 0; i < kScSlots; ++i) { mbar_init(bar(C::bScFull + i), 1); mbar_init(bar(C::bScEmpty + i), kSoftWarps); }
-    mbar_init(bar(C::bDrain), 1);
+    mbar_init(bar(C::bDrain), 2);                   // both issuers' last commits
     for (int i = 0; i < C::kUnits; ++i) last_armed[i] = -1;
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kPvWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -313,97 +318,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u >= 0) drain_wait(bar(C::bFull + lane), u & 1);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kQkWarp) {
     // -------------------------------------------------------------- products
     // The whole warp runs the loop and one elected lane issues, so that
     // descriptors and counters stay in uniform registers.
     const bool lead = elect_one();
-    const int cols = (Hc + 15) & ~15;                // columns that hold heads
-    const uint32_t idesc4 = idesc_e4m3(128, cols, true, false);
-    const uint32_t idesc5 = idesc_f8(kFmtE4M3, kFmtE5M2, 128, cols, true, false);
+    auto D = [](uint64_t d, uint32_t byte_off) -> uint64_t { return d + (byte_off >> 4); };
     const uint64_t dk = sdesc(base, 16, 1024), dv = sdesc(base, kAtom, 1024);
     const uint64_t dr = sdesc(base + kRopeOff, 16, 512, kLayoutSw64);
     const uint64_t dq = sdesc(base + C::kOffQr, 16, 512, kLayoutSw64);
     const uint64_t dp = sdesc(base + C::kOffP, 16, 1024);
-    auto D = [](uint64_t d, uint32_t byte_off) -> uint64_t { return d + (byte_off >> 4); };
-    struct Cursor {                                  // tile j of nt of usable item `count`
-      int it, j, nt;
-      uint32_t count;
-    };
-    auto find = [&](Cursor& c) {
-      for (; c.it < it1; ++c.it) {
-        const int b = item_w(c.it, 0), s = item_w(c.it, 1), e = item_w(c.it, 2);
-        if (!item_ok(p, nnz, b, s, e)) continue;
-        c.nt = (e - s + T - 1) / T;
-        return;
-      }
-    };
-    auto step = [&](Cursor& c) {
-      if (++c.j < c.nt) return;
-      c.j = 0;
-      ++c.it;
-      ++c.count;
-      find(c);
-    };
-    auto scores = [&](uint32_t g, const Cursor& c) -> bool {
-      const uint32_t buf = g & 1, slot = g % C::kUnits;
-      if (c.j == 0 && !mbar_wait(bar(C::bQFull), c.count & 1, wc)) return false;
-      if (g >= 2 && !mbar_wait(bar(C::bSEmpty + buf), ((g >> 1) - 1) & 1, wc)) return false;
-      if (!mbar_wait(bar(C::bFull + slot), (g / C::kUnits) & 1, wc)) return false;
-      tc_fence_after();
-      const uint32_t d_s = tmem + kTmS + buf * T;
-      const uint64_t bk = D(dk, slot * kUnit), br = D(dr, slot * kUnit);
-      if (lead) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k)                 // 512 latent dims, A from TMEM
-          umma_ts_f8(d_s, tmem + kTmQ + 8 * k, D(bk, (k >> 2) * kAtom + (k & 3) * 32), kIdescQK, k != 0 ? 1u : 0u);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) umma_ss_f8(d_s, D(dq, 32 * k), D(br, 32 * k), kIdescQK, 1u);
-        umma_commit(bar(C::bSFull + buf));
-        if (c.j == c.nt - 1) umma_commit(bar(C::bQEmpty));
-      }
-      return true;
-    };
-    auto weighted = [&](uint32_t g, const Cursor& c) -> bool {
-      const uint32_t buf = g & 1, slot = g % C::kUnits;
-      if (!mbar_wait(bar(C::bPFull + buf), (g >> 1) & 1, wc)) return false;
-      if (c.j == 0 && c.count > 0 && !mbar_wait(bar(C::bOEmpty), (c.count - 1) & 1, wc)) return false;
-      tc_fence_after();
-      const uint64_t av = D(dv, slot * kUnit), bp = D(dp, buf * C::kPBuf);
-      if (lead) {
-#pragma unroll
-        for (int mb = 0; mb < 4; ++mb)
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {           // 32 rows
-            const uint64_t a = D(av, mb * kAtom + 4096 * ks);
-            const uint32_t d = tmem + kTmO + 64 * mb;
-            umma_ss_f8(d, a, D(bp, 32 * ks), idesc4, (c.j == 0 && ks == 0) ? 0u : 1u);
-            umma_ss_f8(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
-            if constexpr (kFine) {
-              umma_ss_f8(d, a, D(bp, kPPair + 32 * ks), idesc4, 1u);
-              umma_ss_f8(d, a, D(bp, kPPair + 64 + 32 * ks), idesc5, 1u);
-            }
-          }
-        umma_commit(bar(C::bEmpty + slot));
-        if (c.j == c.nt - 1) umma_commit(bar(C::bOFull));
-      }
-      return true;
-    };
-    Cursor qk{it0, 0, 0, 0}, pv{it0, 0, 0, 0};
-    find(qk);
-    find(pv);
-    uint32_t gq = 0, gp = 0;
+    const int cols = (Hc + 15) & ~15;                // columns that hold heads
+    const uint32_t idesc4 = idesc_e4m3(128, cols, true, false);
+    const uint32_t idesc5 = idesc_f8(kFmtE4M3, kFmtE5M2, 128, cols, true, false);
+    uint32_t g = 0, nitem = 0, slot = 0, lap = 0;
     bool ok = true;
-    while (ok && pv.it < it1) {
-      while (ok && qk.it < it1 && gq <= gp + 2) {
-        ok = scores(gq, qk);
-        ++gq;
-        step(qk);
+    for (int it = it0; it < it1 && ok; ++it) {
+      const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
+      if (!item_ok(p, nnz, b, s, e)) continue;
+      const int nt = (e - s + T - 1) / T;
+      if (warp == kQkWarp) ok = mbar_wait(bar(C::bQFull), nitem & 1, wc);
+      for (int j = 0; j < nt && ok; ++j, ++g) {
+        const uint32_t buf = g & 1;
+        if (warp == kQkWarp) {
+          ok = (g < 2 || mbar_wait(bar(C::bSEmpty + buf), ((g >> 1) - 1) & 1, wc)) && mbar_wait(bar(C::bFull + slot), lap, wc);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d_s = tmem + kTmS + buf * T;
+          const uint64_t bk = D(dk, slot * kUnit), br = D(dr, slot * kUnit);
+          if (lead) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)             // 512 latent dims, A from TMEM
+              umma_ts_f8(d_s, tmem + kTmQ + 8 * k, D(bk, (k >> 2) * kAtom + (k & 3) * 32), kIdescQK, k != 0 ? 1u : 0u);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) umma_ss_f8(d_s, D(dq, 32 * k), D(br, 32 * k), kIdescQK, 1u);
+            umma_commit(bar(C::bSFull + buf));
+            if (j == nt - 1) umma_commit(bar(C::bQEmpty));
+          }
+        } else {
+          ok = mbar_wait(bar(C::bPFull + buf), (g >> 1) & 1, wc) &&
+               (j > 0 || nitem == 0 || mbar_wait(bar(C::bOEmpty), (nitem - 1) & 1, wc));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t av = D(dv, slot * kUnit), bp = D(dp, buf * C::kPBuf);
+          if (lead) {
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+              for (int ks = 0; ks < 2; ++ks) {       // 32 rows
+                const uint64_t a = D(av, mb * kAtom + 4096 * ks);
+                const uint32_t d = tmem + kTmO + 64 * mb;
+                umma_ss_f8(d, a, D(bp, 32 * ks), idesc4, (j == 0 && ks == 0) ? 0u : 1u);
+                umma_ss_f8(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
+                if constexpr (kFine) {
+                  umma_ss_f8(d, a, D(bp, kPPair + 32 * ks), idesc4, 1u);
+                  umma_ss_f8(d, a, D(bp, kPPair + 64 + 32 * ks), idesc5, 1u);
+                }
+              }
+            umma_commit(bar(C::bEmpty + slot));
+            if (j == nt - 1) umma_commit(bar(C::bOFull));
+          }
+        }
+        if (++slot == static_cast<uint32_t>(C::kUnits)) {
+          slot = 0;
+          lap ^= 1;
+        }
       }
-      if (!ok) break;
-      ok = weighted(gp, pv);
-      ++gp;
-      step(pv);
+      ++nitem;
     }
     if (lead) {
       umma_commit(bar(C::bDrain));
@@ -411,53 +392,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= kQueryWarp0) {
-    // ------------------------------------------------------- the items' queries
-    // Row 32 q + lane of A: part q / 2 of head 32 (q % 2) + lane.  Two warps share
-    // a quadrant, each 256 latent and 32 rope dims of its rows.
+    // ------------------------------------------- the items' queries and outputs
+    // Query: row 32 q + lane of A is part q / 2 of head 32 (q % 2) + lane; two
+    // warps share a quadrant, each 256 latent and 32 rope dims of its rows.
+    // Output: dims 32 q + lane of every block of 128, heads 32 half .. of the CTA's.
     const int q = warp & 3, half = (warp >> 2) & 1;
     const int row = 32 * q + lane, hl = row & 63;
     const bool lo = q >= 2, head_ok = hl < Hc;
+    float* facs = reinterpret_cast<float*>(smem + C::kOffFac);
     auto wait = [&](uint32_t bb, uint32_t par) {
-      if (aborted) return;
-      bool r = true;
-      if (lane == 0) r = mbar_wait(bb, par, wc);
-      if (!__shfl_sync(0xffffffffu, r, 0)) aborted = true;
+      if (!aborted && !__all_sync(0xffffffffu, mbar_wait(bb, par, wc))) aborted = true;
     };
-    uint32_t nitem = 0;
-    for (int it = it0; it < it1; ++it) {
-      const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
-      if (!item_ok(p, nnz, b, s, e)) continue;
-      const size_t at = static_cast<size_t>(b) * p.heads + cta * Hc + hl;
-      const uint4* qn = reinterpret_cast<const uint4*>(p.q_nope + at * kLatent);
-      const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + at * kRope);
-      auto absmax8 = [](const uint4& v, float m) {
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    auto query = [&](int b, uint32_t nitem) {
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      // largest elements, coalesced: this warp has heads 8 (warp - 8) .., four rows at a time on their way
+      if (nitem >= 2) wait(bar(C::bFacEmpty + (nitem & 1)), ((nitem >> 1) - 1) & 1);
+#pragma unroll 1
+      for (int r0 = 0; r0 < 8; r0 += 4) {
+        uint4 v[4][3];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
-        return m;
-      };
-      float amax = 0.f;
-      if (head_ok) {
-#pragma unroll 8
-        for (int i = 0; i < 64; ++i) amax = absmax8(__ldg(qn + i), amax);
+        for (int r = 0; r < 4; ++r) {
+          const int h = 8 * (warp - kQueryWarp0) + r0 + r;
+          const size_t at = static_cast<size_t>(b) * p.heads + cta * Hc + h;
+          const bool in = h < Hc;
+          v[r][0] = in ? __ldg(reinterpret_cast<const uint4*>(p.q_nope + at * kLatent) + lane) : zero;
+          v[r][1] = in ? __ldg(reinterpret_cast<const uint4*>(p.q_nope + at * kLatent) + 32 + lane) : zero;
+          v[r][2] = in && lane < 8 ? __ldg(reinterpret_cast<const uint4*>(p.q_rope + at * kRope) + lane) : zero;
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = absmax8(__ldg(qr + i), amax);
+        for (int r = 0; r < 4; ++r) {
+          float amax = 0.f;
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const uint32_t x[4] = {v[r][c].x, v[r][c].y, v[r][c].z, v[r][c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              amax = max3(amax, fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u)));
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          if (lane == 0) {
+            // amax = m 2^e, m in [0.5, 1): a = 8 - e
+            int a = 0;
+            if (amax > 0.f && amax <= 3.0e38f) {
+              int e;
+              frexpf(amax, &e);
+              a = min(126, max(-126, 8 - e));
+            }
+            facs[64 * (nitem & 1) + 8 * (warp - kQueryWarp0) + r0 + r] = ldexpf(1.f, -a);
+          }
+        }
       }
-      int a = 0;
-      if (amax > 0.f && amax <= 3.0e38f) {
-        int ex;
-        frexpf(amax, &ex);
-        a = min(126, max(-126, 8 - ex));
-      }
-      const float up = ldexpf(1.f, a);
-      if (half == 0 && !lo) {
-        // the softmax warps have read what item nitem - 2 left here
-        if (nitem >= 2) wait(bar(C::bFacEmpty + (nitem & 1)), ((nitem >> 1) - 1) & 1);
-        reinterpret_cast<float*>(smem + C::kOffFac)[64 * (nitem & 1) + hl] = ldexpf(1.f, -a);
-        __syncwarp();
-        if (lane == 0 && !aborted) mbar_arrive(bar(C::bFacFull + (nitem & 1)));
-      }
+      __syncwarp();
+      if (lane == 0 && !aborted) mbar_arrive(bar(C::bFacFull + (nitem & 1)));
+      named_bar_sync(kBarQuery, 32 * kQueryWarps);   // the other warps' heads
+      const float up = __frcp_rn(facs[64 * (nitem & 1) + hl]);   // (a power of two)
       // 8 bf16 values to 8 codes of this row's part
       auto part8 = [&](const uint4& v, uint32_t& w0, uint32_t& w1) {
         const uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -474,19 +463,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         w0 = c[0] | (c[1] << 16);
         w1 = c[2] | (c[3] << 16);
       };
-      // half of this warp's dims wait in registers, the other half comes from L1 once they are stored
+      const size_t at = static_cast<size_t>(b) * p.heads + cta * Hc + hl;
+      const uint4* qn = reinterpret_cast<const uint4*>(p.q_nope + at * kLatent);
+      const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + at * kRope);
+      // half of this warp's dims wait in registers, the other half is made once they are stored
       uint32_t code[2][16], rope[8];
-      const uint4 zero = make_uint4(0, 0, 0, 0);
       auto codes = [&](int c0) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          uint4 v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            part8(head_ok ? __ldg(qn + 32 * half + 8 * (c0 + c) + k) : zero, code[c][2 * k], code[c][2 * k + 1]);
+          for (int k = 0; k < 8; ++k) v[k] = head_ok ? __ldg(qn + 32 * half + 8 * (c0 + c) + k) : zero;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) part8(v[k], code[c][2 * k], code[c][2 * k + 1]);
+        }
       };
-      codes(0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) part8(head_ok ? __ldg(qr + 4 * half + k) : zero, rope[2 * k], rope[2 * k + 1]);
+      codes(0);
       if (nitem > 0) wait(bar(C::bQEmpty), (nitem - 1) & 1);
       tc_fence_after();
       const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmQ + 64 * half;
@@ -509,15 +503,80 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0 && !aborted) mbar_arrive(bar(C::bQFull));
+    };
+    auto output = [&](int b, int dest, uint32_t nitem) {
+      const bool part_ok = dest < p.max_partials;    // a device-only plan naming a partial past the workspace
+      if (!part_ok && warp == kQueryWarp0 && lane == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
+      wait(bar(C::bSumFull + (nitem & 1)), (nitem >> 1) & 1);
+      const int h0 = 32 * half;
+      const float* sum = reinterpret_cast<const float*>(smem + C::kOffSum) + 256 * (nitem & 1) + h0 + lane;
+      const float l = (sum[0] + sum[64]) + (sum[128] + sum[192]);
+      const float ref = reinterpret_cast<const float*>(smem + C::kOffRef)[64 * (nitem & 1) + h0 + lane];
+      const float inv = l > 0.f ? 1.f / l : 0.f;     // of head h0 + lane
+      __syncwarp();
+      if (lane == 0 && !aborted) mbar_arrive(bar(C::bSumEmpty + (nitem & 1)));
+      const size_t row0 = static_cast<size_t>(dest < 0 ? b : dest) * p.heads + cta * Hc;
+      if (q == 0 && h0 + lane < Hc && !aborted && part_ok) {
+        const float lse = l > 0.f ? (ref + __log2f(l) - kTop) * 0.69314718055994531f : -INFINITY;
+        if (dest >= 0) p.part_lse[row0 + h0 + lane] = lse;
+        else if (p.lse) p.lse[row0 + h0 + lane] = lse;
+      }
+      wait(bar(C::bOFull), nitem & 1);
+      tc_fence_after();
+      if (!aborted && part_ok) {
+        const size_t first = (row0 + h0) * kLatent + 32 * q + lane;
+        const int n = min(max(Hc - h0, 0), 32);      // heads, a multiple of 8
+        const uint32_t from = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmO + h0;
+        // (a store's 32 lanes are a head's 128 bytes; the type is looked at once, not at every store)
+        auto put = [&](auto* dst, auto as) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {              // block c / 2, 16 heads
+            if (16 * (c & 1) >= n) continue;
+            uint32_t o[16];
+            tmem_ld16(from + 64 * (c >> 1) + 16 * (c & 1), o);
+            tmem_wait_ld();
+            auto* at = dst + 128 * (c >> 1) + 16 * (c & 1) * kLatent;
+            auto eight = [&](int i0) {
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                v[i] = __uint_as_float(o[i0 + i]) * __shfl_sync(0xffffffffu, inv, 16 * (c & 1) + i0 + i);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) at[(i0 + i) * kLatent] = as(v[i]);
+            };
+            eight(0);
+            if (16 * (c & 1) + 8 < n) eight(8);
+          }
+        };
+        if (dest < 0 && p.out_bf16)
+          put(static_cast<__nv_bfloat16*>(p.out) + first, [](float v) { return __float2bfloat16_rn(v); });
+        else
+          put((dest >= 0 ? p.part_o : static_cast<float*>(p.out)) + first, [](float v) { return v; });
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && !aborted) mbar_arrive(bar(C::bOEmpty));
+    };
+    uint32_t nitem = 0;
+    int b_last = 0, dest_last = 0;
+    for (int it = it0; it < it1; ++it) {
+      const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
+      if (!item_ok(p, nnz, b, s, e)) continue;
+      query(b, nitem);
+      if (nitem > 0) output(b_last, dest_last, nitem - 1);
+      b_last = b;
+      dest_last = item_w(it, 3);
       ++nitem;
     }
+    if (nitem > 0) output(b_last, dest_last, nitem - 1);
   } else {
-    // ------------------------------------------------------- softmax, epilogue
+    // ----------------------------------------------------------------- softmax
     const int q = warp & 3, th = warp >> 2, part = q >> 1;
     const int hl = 32 * (q & 1) + lane;              // head of this CTA
     const uint32_t quad = static_cast<uint32_t>(32 * q) << 16;
     float* red = reinterpret_cast<float*>(smem + C::kOffRed);
     float* bc = reinterpret_cast<float*>(smem + C::kOffBc);
+    volatile uint32_t* moved_of = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMoved);   // heads to rescale
     const int four = 2 * th + part;                  // which 16 rows of a tile
     float m_ref = 0.f, l_sum = 0.f, fac = 1.f;
     int rk = 0;
@@ -591,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t g = 0, nitem = 0;
     for (int it = it0; it < it1; ++it) {
-      const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2), dest = item_w(it, 3);
+      const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
       if (!item_ok(p, nnz, b, s, e)) continue;
       const int n = e - s, nt = (n + T - 1) / T;
       wait(bar(C::bFacFull + (nitem & 1)), (nitem >> 1) & 1);
@@ -604,41 +663,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx = exponents(g, n);
       for (int j = 0; j < nt; ++j, ++g) {
         const uint32_t buf = g & 1;
-        if (j + 1 < nt) load_scores(g + 1);          // (the sum of tile g - 2 is done, then: its weights may go)
-        if (named_bar_or(kBarVote, 32 * kSoftWarps, mx > m_ref + kLag)) {
+        if (j + 1 < nt) load_scores(g + 1);
+        const bool moved = named_bar_or(kBarVote, 32 * kSoftWarps, mx > m_ref + kLag);
+        if (moved) {                                 // some head's reference moves
           float all[4];
           share(mx, all);
-          const float mn = fmaxf(m_ref, fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])));
-          const float alpha = ex2_approx(m_ref - mn);
+          const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+          const float mn = mt > m_ref + kLag ? mt : m_ref;
+          const float alpha = mn == m_ref ? 1.f : ex2_approx(m_ref - mn);
           m_ref = mn;
           l_sum *= alpha;
-          if (four == 0) bc[hl] = alpha;
-          named_bar_sync(kBarAll, 32 * kSoftWarps);
-          if (j > 0) {
-            const uint32_t gp = g - 1;               // its sum is done once its rows are free
-            wait(bar(C::bEmpty + gp % C::kUnits), (gp / C::kUnits) & 1);
-            tc_fence_after();
-            if (!aborted) {
-              // this warp's 32 dims of blocks 2 th and 2 th + 1, 16 heads at a time
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t o[16];
-                const uint32_t ta = tmem + quad + kTmO + 128 * th + 16 * c;
-                tmem_ld16(ta, o);
-                tmem_wait_ld();
-                const float4* al = reinterpret_cast<const float4*>(bc) + 4 * (c & 3);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float4 f = al[i];
-                  o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f.x);
-                  o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f.y);
-                  o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f.z);
-                  o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f.w);
-                }
-                tmem_st16(ta, o);
-              }
-              tmem_wait_st();
-            }
+          if (four == 0) {                           // (warps 0 and 1)
+            bc[hl] = alpha;
+            const uint32_t which = __ballot_sync(0xffffffffu, alpha != 1.f);
+            if (lane == 0) moved_of[warp] = which;
           }
         }
         // weights and their parts; 16 rows are one 16-byte chunk of each
@@ -678,10 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l2 = f2_add(l2, l3);
         l_sum += l2.x + l2.y;
-        if (j + 1 == nt && g >= 2) {                 // no later scores have said so
-          const uint32_t gp = g - 2;
-          wait(bar(C::bEmpty + gp % C::kUnits), (gp / C::kUnits) & 1);
-        }
+        if (g >= 2) wait(bar(C::bEmpty + (g - 2) % C::kUnits), ((g - 2) / C::kUnits) & 1);   // these weights' last use
         if (!aborted) {
           uint8_t* row = smem + C::kOffP + buf * C::kPBuf + hl * 128;
           const int sw = hl & 7;
@@ -696,52 +731,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && !aborted) {
-          mbar_arrive(bar(C::bPFull + buf));
+          if (!moved) mbar_arrive(bar(C::bPFull + buf));
           mbar_arrive(bar(C::bScEmpty + g % kScSlots));
         }
         if (j + 1 < nt) mx = exponents(g + 1, n - (j + 1) * T);
-      }
-      // ---------------------------------------------------------------- epilogue
-      const bool part_ok = dest < p.max_partials;    // a device-only plan naming a partial past the workspace
-      if (!part_ok && threadIdx.x == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
-      float all[4];
-      share(l_sum, all);
-      const float l = (all[0] + all[1]) + (all[2] + all[3]);
-      const size_t row0 = static_cast<size_t>(dest < 0 ? b : dest) * p.heads + cta * Hc;
-      if (four == 0) {
-        bc[hl] = l > 0.f ? 1.f / l : 0.f;
-        if (hl < Hc && !aborted && part_ok) {
-          const float lse = l > 0.f ? (m_ref + __log2f(l) - kTop) * 0.69314718055994531f : -INFINITY;
-          if (dest >= 0) p.part_lse[row0 + hl] = lse;
-          else if (p.lse) p.lse[row0 + hl] = lse;
-        }
-      }
-      named_bar_sync(kBarAll, 32 * kSoftWarps);
-      wait(bar(C::bOFull), nitem & 1);
-      tc_fence_after();
-      const bool half_out = dest < 0 && p.out_bf16;
-      float* dst_f = dest >= 0 ? p.part_o + row0 * kLatent : static_cast<float*>(p.out) + row0 * kLatent;
-      __nv_bfloat16* dst_h = static_cast<__nv_bfloat16*>(p.out) + row0 * kLatent;
-      if (!aborted && part_ok) {
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {                // block c / 2, 16 of this warp's 32 heads
-          const int h0 = 32 * th + 16 * (c & 1), d = 128 * (c >> 1) + 32 * q + lane;
-          if (h0 >= Hc) continue;
-          uint32_t o[16];
-          tmem_ld16(tmem + quad + kTmO + 64 * (c >> 1) + h0, o);
-          tmem_wait_ld();
+        if (moved) {
+          // O in the new units, by now that the sum of the tile before is done or nearly so.  A head is a column of
+          // each block; this warp has its 32 dims of blocks 2 th and 2 th + 1.
+          named_bar_sync(kBarAll, 32 * kSoftWarps);  // the factors are there
+          if (j > 0) {
+            wait(bar(C::bEmpty + (g - 1) % C::kUnits), ((g - 1) / C::kUnits) & 1);
+            tc_fence_after();
+            const uint32_t to = tmem + quad + kTmO + 128 * th;
+            if (!aborted) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (h0 + i >= Hc) break;
-            const float v = __uint_as_float(o[i]) * bc[h0 + i];
-            if (half_out) dst_h[static_cast<size_t>(h0 + i) * kLatent + d] = __float2bfloat16_rn(v);
-            else dst_f[static_cast<size_t>(h0 + i) * kLatent + d] = v;
+              for (int w = 0; w < 2; ++w) {
+                for (uint32_t m = moved_of[w]; m; m &= m - 1) {
+                  const int h = 32 * w + __ffs(m) - 1;
+                  const float f = bc[h];
+                  uint32_t a, z;
+                  tmem_ld1(to + h, a);
+                  tmem_ld1(to + 64 + h, z);
+                  tmem_wait_ld();
+                  tmem_st1(to + h, __float_as_uint(__uint_as_float(a) * f));
+                  tmem_st1(to + 64 + h, __float_as_uint(__uint_as_float(z) * f));
+                }
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
           }
+          __syncwarp();
+          if (lane == 0 && !aborted) mbar_arrive(bar(C::bPFull + buf));
         }
       }
-      tc_fence_before();
+      // what the output needs
+      if (nitem >= 2) wait(bar(C::bSumEmpty + (nitem & 1)), ((nitem >> 1) - 1) & 1);
+      reinterpret_cast<float*>(smem + C::kOffSum)[256 * (nitem & 1) + 64 * four + hl] = l_sum;
+      if (four == 0) reinterpret_cast<float*>(smem + C::kOffRef)[64 * (nitem & 1) + hl] = m_ref;
       __syncwarp();
-      if (lane == 0 && !aborted) mbar_arrive(bar(C::bOEmpty));
+      if (lane == 0 && !aborted) mbar_arrive(bar(C::bSumFull + (nitem & 1)));
       ++nitem;
     }
   }
@@ -749,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kPvWarp) tmem_dealloc(tmem, 512);
 }
 
 template <bool kFine>
