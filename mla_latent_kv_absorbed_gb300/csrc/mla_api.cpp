@@ -665,7 +665,7 @@ int decode_fp8(const int32_t* plan_host, const int32_t* plan_dev, const void* q_
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return MLA_ERR_CUDA;
   const int rc = few    ? launch_swab8(H, tm_lat, tm_rope, p, p8, pp, plan_host[kHWorkers], st)
-                 : rows ? launch_rows8(H, tm_lat, tm_rope, p, kv_scales, plan_host[kHWorkers], st)
+                 : rows ? launch_rows8(tm_lat, tm_rope, p, p8, pp, plan_host[kHWorkers], st)
                         : launch_pair8(H, tm_lat, tm_rope, p, kv_scale, plan_host[kHWorkers], st);
   if (rc != MLA_OK) return rc;
   return mla_decode_merge(plan_host, plan_dev, out, out_dtype, lse, workspace, workspace_bytes, stream);

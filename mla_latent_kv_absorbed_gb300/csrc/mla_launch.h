@@ -63,10 +63,11 @@ int launch_swab8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rop
 int launch_pair8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p,
                  float kv_scale, int workers, cudaStream_t stream);
 
-// The same over a cache with a scale for each row, kv_scales [num_slots].
-// tm_rope: box {64, 1}, 64-byte swizzle.
-int launch_rows8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p,
-                 const float* kv_scales, int workers, cudaStream_t stream);
+// The same over a cache with a scale for each row (p8.kv_scales): the query prep
+// kernel, then the decode kernel as its programmatic dependent.  tm_rope: box
+// {64, 1}, 64-byte swizzle.
+int launch_rows8(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p, const Fp8Params& p8,
+                 const Fp8PrepParams& pp, int workers, cudaStream_t stream);
 
 // Bytes of one request's query image for the FP8 decode.
 size_t fp8_image_bytes(int heads);

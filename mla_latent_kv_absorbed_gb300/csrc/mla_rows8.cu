@@ -37,15 +37,20 @@
 // exchanges of 2500 cycles, so its first half, up to the exchange of the parts,
 // is begun before the weights of the tile before are made.
 //
+// A kernel before this one splits each request's query into its parts, once for
+// all items (in here a warp took 20000 cycles an item for it), in the order in
+// which the lanes below read them, and this one is its programmatic dependent:
+// only the warps that need the query wait for it.
+//
 // TMEM (512 columns): O^T [0, 256), the query [256, 384), two score buffers.
 //
 // Warps:
 //   0-7    softmax.  A thread of lane quadrant q reads its part
 //          (hi: q < 2) of a head's scores for 32 rows, exchanges half of them with
 //          the thread that has the other part, and goes on with 16 rows.
-//   8-15   the next item's query (its largest elements, and half of the parts in
-//          registers, while the item before is worked on; then into TMEM and
-//          shared memory), and the output of the item before
+//   8-15   the next item's query (half of its parts in registers while the item
+//          before is worked on; then into TMEM and shared memory), and the output
+//          of the item before
 //   16     issuer of the scores     17  TMEM allocator, issuer of the weighted sums
 //   18-21  gathers of the latents, an atom each: 16 of four rows a tile (a warp
 //          takes some 60 cycles for each of a burst, so they are spread)
@@ -66,13 +71,14 @@ constexpr int kRopeOff = 4 * kAtom;
 constexpr int kUnit = 4 * kAtom + T * 64;            // a tile: 36 KB
 constexpr int kQr = 128 * 64;                        // rope query: [hi; lo] x 64 dims (64-byte swizzle)
 constexpr int kPPair = 64 * 128;                     // two parts of the weights: 64 heads x (64 + 64) rows
+constexpr int kImage = 2 * kRow;                     // bytes of a head's query: hi and lo codes
 constexpr int kXBytes = kSoftWarps * 32 * 64;        // scores on their way to the thread of the other part, of a tile
 constexpr int kScSlots = 3;                          // tiles whose rows' numbers are held
 constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the scales, reciprocals
 constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
 constexpr float kLoWeight = 1.f / 32.f;              // value of a query's lo part
 constexpr float kTop = 5.f, kLag = 3.f;              // weights are 2^(e - m + kTop) with e <= m + kLag
-constexpr int kBarPair0 = 1, kBarAll = 5, kBarVote = 6, kBarGather = 7, kBarQuery = 8;   // named barriers
+constexpr int kBarPair0 = 1, kBarAll = 5, kBarVote = 6, kBarGather = 7;   // named barriers
 constexpr int kTmO = 0, kTmQ = 256, kTmS = 384;
 constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);
 
@@ -87,8 +93,7 @@ struct Cfg {
   static constexpr int kOffSc = kOffX + 2 * kXBytes;
   static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [2][4][64] maxima, sums
   static constexpr int kOffBc = kOffRed + 2 * 4 * 64 * 4;       // [64] rescaling factors, 1 / l
-  static constexpr int kOffFac = kOffBc + 64 * 4;               // [2][64] 2^-a of an item's heads
-  static constexpr int kOffSum = kOffFac + 2 * 64 * 4;          // [2][4][64] an item's sums, for the output
+  static constexpr int kOffSum = kOffBc + 64 * 4;               // [2][4][64] an item's sums, for the output
   static constexpr int kOffRef = kOffSum + 2 * 4 * 64 * 4;      // [2][64] and references
   static constexpr int kOffSlots = kOffRef + 2 * 64 * 4;        // [5][64] a tile's slots, for each gathering warp
   static constexpr int kOffBar = kOffSlots + 5 * T * 4;
@@ -96,9 +101,7 @@ struct Cfg {
   static constexpr int bEmpty = bFull + kUnits;      // [kUnits]
   static constexpr int bQFull = bEmpty + kUnits;
   static constexpr int bQEmpty = bQFull + 1;
-  static constexpr int bFacFull = bQEmpty + 1;       // [2]
-  static constexpr int bFacEmpty = bFacFull + 2;     // [2]
-  static constexpr int bSFull = bFacEmpty + 2;       // [2]
+  static constexpr int bSFull = bQEmpty + 1;         // [2]
   static constexpr int bSEmpty = bSFull + 2;         // [2]
   static constexpr int bPFull = bSEmpty + 2;         // [2]
   static constexpr int bOFull = bPFull + 2;
@@ -127,11 +130,68 @@ __device__ __forceinline__ bool item_in_request(const DecodeParams& p, int b, in
   return lo <= s && e <= hi;
 }
 
+// ------------------------------------------------------------ query parts --
+// One warp a head: lane l has latent dims 16 l .. and, of lanes 0-3, rope dims
+// 16 l ..; q' = q 2^a, hi = e4m3(q'), lo = e4m3(32 (q' - hi)).  A CTA's image is
+// 36 pieces of 16 dims, each with the hi and then the lo codes of its heads.
+// Bound: launch and a round trip, or for large batches HBM.
+constexpr int kPrepThreads = 256;
+__global__ void __launch_bounds__(kPrepThreads) rows8_prep_kernel(const Fp8PrepParams p, int heads) {
+  const int lane = threadIdx.x & 31, warps = gridDim.x * (kPrepThreads / 32), Hc = heads >> 1;
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int i = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5); i < p.rows; i += warps) {
+    const int b = i / heads, h = i - b * heads, c = h >= Hc, hl = c ? h - Hc : h;
+    const uint4* qn = reinterpret_cast<const uint4*>(p.q_nope + static_cast<size_t>(i) * kLatent) + 2 * lane;
+    const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + static_cast<size_t>(i) * kRope) + 2 * lane;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 v[2][2] = {{__ldg(qn), __ldg(qn + 1)}, {lane < 4 ? __ldg(qr) : zero, lane < 4 ? __ldg(qr + 1) : zero}};
+    auto word = [&](int t, int k) -> uint32_t {
+      const uint4& x = v[t][k >> 2];
+      return (k & 3) == 0 ? x.x : (k & 3) == 1 ? x.y : (k & 3) == 2 ? x.z : x.w;
+    };
+    float amax = 0.f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        amax = max3(amax, fabsf(__uint_as_float(word(t, k) << 16)), fabsf(__uint_as_float(word(t, k) & 0xFFFF0000u)));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    int a = 0;                                       // amax = m 2^e, m in [0.5, 1): a = 8 - e
+    if (amax > 0.f && amax <= 3.0e38f) {
+      int e;
+      frexpf(amax, &e);
+      a = min(126, max(-126, 8 - e));
+    }
+    const float up = ldexpf(1.f, a);
+    uint8_t* img = p.img + (static_cast<size_t>(b) * heads + c * Hc) * kImage;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (t == 1 && lane >= 4) break;
+      uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float u0 = __uint_as_float(word(t, k) << 16) * up, u1 = __uint_as_float(word(t, k) & 0xFFFF0000u) * up;
+        const uint32_t h2 = e4m3x2(u0, u1);
+        const float2 hv = e4m3x2_value(h2);
+        hi[k >> 1] |= h2 << (16 * (k & 1));
+        lo[k >> 1] |= e4m3x2((u0 - hv.x) * 32.f, (u1 - hv.y) * 32.f) << (16 * (k & 1));
+      }
+      uint4* dst = reinterpret_cast<uint4*>(img) + (32 * t + lane) * 2 * Hc + hl;
+      dst[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      dst[Hc] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    if (lane == 0) p.fac[i] = ldexpf(1.f, -a);
+  }
+}
+
 template <bool kFine>
 __global__ void __launch_bounds__(kThreads, 1)
     rows8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
-                 const DecodeParams p, const float* __restrict__ kv_scales) {
+                 const DecodeParams p, const Fp8Params p8) {
   using C = Cfg<kFine>;
+  const float* __restrict__ kv_scales = p8.kv_scales;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -151,7 +211,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(C::bQFull), kQueryWarps);
     mbar_init(bar(C::bQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::bFacFull + i), kQueryWarps); mbar_init(bar(C::bFacEmpty + i), kSoftWarps);
       mbar_init(bar(C::bSFull + i), 1); mbar_init(bar(C::bSEmpty + i), kSoftWarps);
       mbar_init(bar(C::bPFull + i), kSoftWarps);
       mbar_init(bar(C::bSumFull + i), kSoftWarps); mbar_init(bar(C::bSumEmpty + i), kQueryWarps);
@@ -174,7 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_wait();
   int it0, it1;
   plan_items(p, w, it0, it1);
   const int32_t* items = p.plan + p.items_off;
@@ -399,105 +457,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, half = (warp >> 2) & 1;
     const int row = 32 * q + lane, hl = row & 63;
     const bool lo = q >= 2, head_ok = hl < Hc;
-    float* facs = reinterpret_cast<float*>(smem + C::kOffFac);
     auto wait = [&](uint32_t bb, uint32_t par) {
       if (!aborted && !__all_sync(0xffffffffu, mbar_wait(bb, par, wc))) aborted = true;
     };
+    griddep_wait();                                  // the queries' parts come from the kernel before
     auto query = [&](int b, uint32_t nitem) {
+      // 16 codes of a row are one 16-byte piece, and the pieces of all rows lie together
+      const uint4* src = reinterpret_cast<const uint4*>(p8.img + (static_cast<size_t>(b) * p.heads + cta * Hc) * kImage) +
+                         (lo ? Hc : 0) + hl;
       const uint4 zero = make_uint4(0, 0, 0, 0);
-      // largest elements, coalesced: this warp has heads 8 (warp - 8) .., four rows at a time on their way
-      if (nitem >= 2) wait(bar(C::bFacEmpty + (nitem & 1)), ((nitem >> 1) - 1) & 1);
-#pragma unroll 1
-      for (int r0 = 0; r0 < 8; r0 += 4) {
-        uint4 v[4][3];
+      uint4 v[8], r[2];
+      auto pieces = [&](int c) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int h = 8 * (warp - kQueryWarp0) + r0 + r;
-          const size_t at = static_cast<size_t>(b) * p.heads + cta * Hc + h;
-          const bool in = h < Hc;
-          v[r][0] = in ? __ldg(reinterpret_cast<const uint4*>(p.q_nope + at * kLatent) + lane) : zero;
-          v[r][1] = in ? __ldg(reinterpret_cast<const uint4*>(p.q_nope + at * kLatent) + 32 + lane) : zero;
-          v[r][2] = in && lane < 8 ? __ldg(reinterpret_cast<const uint4*>(p.q_rope + at * kRope) + lane) : zero;
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float amax = 0.f;
-#pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const uint32_t x[4] = {v[r][c].x, v[r][c].y, v[r][c].z, v[r][c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              amax = max3(amax, fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u)));
-          }
-#pragma unroll
-          for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          if (lane == 0) {
-            // amax = m 2^e, m in [0.5, 1): a = 8 - e
-            int a = 0;
-            if (amax > 0.f && amax <= 3.0e38f) {
-              int e;
-              frexpf(amax, &e);
-              a = min(126, max(-126, 8 - e));
-            }
-            facs[64 * (nitem & 1) + 8 * (warp - kQueryWarp0) + r0 + r] = ldexpf(1.f, -a);
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0 && !aborted) mbar_arrive(bar(C::bFacFull + (nitem & 1)));
-      named_bar_sync(kBarQuery, 32 * kQueryWarps);   // the other warps' heads
-      const float up = __frcp_rn(facs[64 * (nitem & 1) + hl]);   // (a power of two)
-      // 8 bf16 values to 8 codes of this row's part
-      auto part8 = [&](const uint4& v, uint32_t& w0, uint32_t& w1) {
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u0 = __uint_as_float(x[i] << 16) * up, u1 = __uint_as_float(x[i] & 0xFFFF0000u) * up;
-          c[i] = e4m3x2(u0, u1);
-          if (lo) {
-            const float2 hv = e4m3x2_value(c[i]);
-            c[i] = e4m3x2((u0 - hv.x) * 32.f, (u1 - hv.y) * 32.f);
-          }
-        }
-        w0 = c[0] | (c[1] << 16);
-        w1 = c[2] | (c[3] << 16);
+        for (int k = 0; k < 8; ++k) v[k] = head_ok ? src[(16 * half + c + k) * 2 * Hc] : zero;
       };
-      const size_t at = static_cast<size_t>(b) * p.heads + cta * Hc + hl;
-      const uint4* qn = reinterpret_cast<const uint4*>(p.q_nope + at * kLatent);
-      const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + at * kRope);
-      // half of this warp's dims wait in registers, the other half is made once they are stored
-      uint32_t code[2][16], rope[8];
-      auto codes = [&](int c0) {
+      const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmQ + 64 * half;
+      auto store = [&](int c) {
+        if (aborted) return;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint4 v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = head_ok ? __ldg(qn + 32 * half + 8 * (c0 + c) + k) : zero;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) part8(v[k], code[c][2 * k], code[c][2 * k + 1]);
+        for (int k = 0; k < 8; k += 4) {
+          const uint32_t w[16] = {v[k].x,     v[k].y,     v[k].z,     v[k].w,     v[k + 1].x, v[k + 1].y, v[k + 1].z, v[k + 1].w,
+                                  v[k + 2].x, v[k + 2].y, v[k + 2].z, v[k + 2].w, v[k + 3].x, v[k + 3].y, v[k + 3].z, v[k + 3].w};
+          tmem_st16(tq + 4 * (c + k), w);
         }
       };
 #pragma unroll
-      for (int k = 0; k < 4; ++k) part8(head_ok ? __ldg(qr + 4 * half + k) : zero, rope[2 * k], rope[2 * k + 1]);
-      codes(0);
+      for (int k = 0; k < 2; ++k) r[k] = head_ok ? src[(32 + 2 * half + k) * 2 * Hc] : zero;
+      pieces(0);
       if (nitem > 0) wait(bar(C::bQEmpty), (nitem - 1) & 1);
       tc_fence_after();
-      const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmQ + 64 * half;
+      store(0);
+      pieces(8);
+      store(8);
       if (!aborted) {
-        tmem_st16(tq, code[0]);
-        tmem_st16(tq + 16, code[1]);
-      }
-      codes(2);
-      if (!aborted) {
-        tmem_st16(tq + 32, code[0]);
-        tmem_st16(tq + 48, code[1]);
         tmem_wait_st();
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int k = 0; k < 2; ++k)
           *reinterpret_cast<uint4*>(smem + C::kOffQr + (row >> 3) * 512 + (row & 7) * 64 +
-                                    (((2 * half + c) ^ ((row >> 1) & 3)) << 4)) =
-              make_uint4(rope[4 * c], rope[4 * c + 1], rope[4 * c + 2], rope[4 * c + 3]);
+                                    (((2 * half + k) ^ ((row >> 1) & 3)) << 4)) = r[k];
         fence_proxy_async_smem();
       }
       tc_fence_before();
@@ -648,15 +645,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return fmaxf(m0, m1);
     };
+    griddep_wait();                                  // the factors come from the kernel before
+    // 2^-a of this head in the next usable item from `it` on, loaded while the item before is worked on
+    auto factor = [&](int it) -> float {
+      for (; it < it1; ++it) {
+        const int b = item_w(it, 0);
+        if (item_ok(p, nnz, b, item_w(it, 1), item_w(it, 2)))
+          return hl < Hc ? p8.fac[static_cast<size_t>(b) * p.heads + cta * Hc + hl] : 1.f;
+      }
+      return 1.f;
+    };
+    float fac_next = factor(it0);
     uint32_t g = 0, nitem = 0;
     for (int it = it0; it < it1; ++it) {
       const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
       if (!item_ok(p, nnz, b, s, e)) continue;
       const int n = e - s, nt = (n + T - 1) / T;
-      wait(bar(C::bFacFull + (nitem & 1)), (nitem >> 1) & 1);
-      fac = reinterpret_cast<const float*>(smem + C::kOffFac)[64 * (nitem & 1) + hl];
-      __syncwarp();
-      if (lane == 0 && !aborted) mbar_arrive(bar(C::bFacEmpty + (nitem & 1)));
+      fac = fac_next;
+      fac_next = factor(it + 1);
       l_sum = 0.f;
       m_ref = -INFINITY;                             // (the first tile asks for a reference)
       load_scores(g);
@@ -781,32 +787,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kPvWarp) tmem_dealloc(tmem, 512);
 }
 
-template <bool kFine>
-int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p, const float* kv_scales,
-           int workers, cudaStream_t stream) {
-  const auto kernel = &rows8_kernel<kFine>;
-  if (!set_smem_limit(reinterpret_cast<const void*>(kernel), Cfg<kFine>::kSmemBytes)) return MLA_ERR_CUDA;
+template <typename Kernel, typename... Args>
+int launch_after(Kernel* kernel, int grid, int threads, int smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * workers, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<kFine>::kSmemBytes;
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, tm_lat, tm_rope, p, kv_scales) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return MLA_ERR_CUDA;
   return cudaPeekAtLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace rows8
 
-int launch_rows8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p,
-                 const float* kv_scales, int workers, cudaStream_t stream) {
-  if (heads < 48 || heads > 128 || heads % 16 != 0) return MLA_ERR_UNSUPPORTED;
-  return p.out_bf16 ? rows8::launch<false>(tm_lat, tm_rope, p, kv_scales, workers, stream)
-                    : rows8::launch<true>(tm_lat, tm_rope, p, kv_scales, workers, stream);
+int launch_rows8(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p, const Fp8Params& p8,
+                 const Fp8PrepParams& pp, int workers, cudaStream_t stream) {
+  if (p.heads < 48 || p.heads > 128 || p.heads % 16 != 0) return MLA_ERR_UNSUPPORTED;
+  const auto kernel = p.out_bf16 ? &rows8::rows8_kernel<false> : &rows8::rows8_kernel<true>;
+  const int smem = p.out_bf16 ? rows8::Cfg<false>::kSmemBytes : rows8::Cfg<true>::kSmemBytes;
+  if (!set_smem_limit(reinterpret_cast<const void*>(kernel), smem)) return MLA_ERR_CUDA;
+  // few enough blocks that the next kernel's fit beside them (it starts once all have)
+  const int warps = rows8::kPrepThreads / 32, blocks = (pp.rows + warps - 1) / warps, held = 4 * 2 * workers;
+  const int st = rows8::launch_after(&rows8::rows8_prep_kernel, blocks < held ? blocks : held, rows8::kPrepThreads, 0,
+                                     stream, pp, p.heads);
+  if (st != MLA_OK) return st;
+  return rows8::launch_after(kernel, 2 * workers, rows8::kThreads, smem, stream, tm_lat, tm_rope, p, p8);
 }
 
 }  // namespace mla
