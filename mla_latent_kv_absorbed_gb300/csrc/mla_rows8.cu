@@ -45,17 +45,19 @@
 // TMEM (512 columns): O^T [0, 256), the query [256, 384), two score buffers.
 //
 // Warps:
-//   0-7    softmax.  A thread of lane quadrant q reads its part
-//          (hi: q < 2) of a head's scores for 32 rows, exchanges half of them with
-//          the thread that has the other part, and goes on with 16 rows.
-//   8-15   the next item's query (half of its parts in registers while the item
+//   0-15   softmax.  A thread of lane quadrant q reads its part (hi: q < 2) of a
+//          head's scores for 16 rows, exchanges half of them with the thread that
+//          has the other part, and goes on with 8 rows.  (Most of a tile's softmax
+//          is latency, and code that runs once a tile: twice the warps with half
+//          of the rows each take less than half as long.)
+//   16-23  the next item's query (half of its parts in registers while the item
 //          before is worked on; then into TMEM and shared memory), and the output
 //          of the item before
-//   16     issuer of the scores     17  TMEM allocator, issuer of the weighted sums
-//   18-21  gathers of the latents, an atom each: 16 of four rows a tile (a warp
+//   24     issuer of the scores     25  TMEM allocator, issuer of the weighted sums
+//   26-29  gathers of the latents, an atom each: 16 of four rows a tile (a warp
 //          takes some 60 cycles for each of a burst, so they are spread)
-//   22     gathers of the rope keys
-//   23     the numbers made of the rows' scales
+//   30     gathers of the rope keys
+//   31     the numbers made of the rows' scales
 #include "mla_device.cuh"
 #include "mla_launch.h"
 
@@ -63,22 +65,22 @@ namespace mla {
 namespace rows8 {
 
 constexpr int T = 64;                                // rows of a tile
-constexpr int kSoftWarps = 8, kQueryWarps = 8;
-constexpr int kQueryWarp0 = 8, kQkWarp = 16, kPvWarp = 17, kLatentWarp0 = 18, kRopeWarp = 22, kScaleWarp = 23;
-constexpr int kThreads = 32 * 24;
+constexpr int kSoftWarps = 16, kQueryWarps = 8;
+constexpr int kQueryWarp0 = 16, kQkWarp = 24, kPvWarp = 25, kLatentWarp0 = 26, kRopeWarp = 30, kScaleWarp = 31;
+constexpr int kThreads = 32 * 32;
 constexpr int kAtom = T * 128;                       // 64 rows x 128 dims
 constexpr int kRopeOff = 4 * kAtom;
 constexpr int kUnit = 4 * kAtom + T * 64;            // a tile: 36 KB
 constexpr int kQr = 128 * 64;                        // rope query: [hi; lo] x 64 dims (64-byte swizzle)
 constexpr int kPPair = 64 * 128;                     // two parts of the weights: 64 heads x (64 + 64) rows
 constexpr int kImage = 2 * kRow;                     // bytes of a head's query: hi and lo codes
-constexpr int kXBytes = kSoftWarps * 32 * 64;        // scores on their way to the thread of the other part, of a tile
+constexpr int kXBytes = kSoftWarps * 32 * 32;        // scores on their way to the thread of the other part, of a tile
 constexpr int kScSlots = 3;                          // tiles whose rows' numbers are held
 constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the scales, reciprocals
 constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
 constexpr float kLoWeight = 1.f / 32.f;              // value of a query's lo part
 constexpr float kTop = 5.f, kLag = 3.f;              // weights are 2^(e - m + kTop) with e <= m + kLag
-constexpr int kBarPair0 = 1, kBarAll = 5, kBarVote = 6, kBarGather = 7;   // named barriers
+constexpr int kBarPair0 = 1, kBarAll = 9, kBarVote = 10, kBarGather = 11;   // named barriers
 constexpr int kTmO = 0, kTmQ = 256, kTmS = 384;
 constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);
 
@@ -90,11 +92,11 @@ struct Cfg {
   static constexpr int kOffQr = kUnits * kUnit;
   static constexpr int kOffP = kOffQr + kQr;
   static constexpr int kOffX = kOffP + 2 * kPBuf;
-  static constexpr int kOffSc = kOffX + 2 * kXBytes;
-  static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [2][4][64] maxima, sums
-  static constexpr int kOffBc = kOffRed + 2 * 4 * 64 * 4;       // [64] rescaling factors, 1 / l
-  static constexpr int kOffSum = kOffBc + 64 * 4;               // [2][4][64] an item's sums, for the output
-  static constexpr int kOffRef = kOffSum + 2 * 4 * 64 * 4;      // [2][64] and references
+  static constexpr int kOffSc = kOffX + kXBytes;
+  static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [2][8][64] maxima
+  static constexpr int kOffBc = kOffRed + 2 * 8 * 64 * 4;       // [64] rescaling factors
+  static constexpr int kOffSum = kOffBc + 64 * 4;               // [2][8][64] an item's sums, for the output
+  static constexpr int kOffRef = kOffSum + 2 * 8 * 64 * 4;      // [2][64] and references
   static constexpr int kOffSlots = kOffRef + 2 * 64 * 4;        // [5][64] a tile's slots, for each gathering warp
   static constexpr int kOffBar = kOffSlots + 5 * T * 4;
   static constexpr int bFull = 0;                    // [kUnits] a tile's rows have landed
@@ -506,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!part_ok && warp == kQueryWarp0 && lane == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
       wait(bar(C::bSumFull + (nitem & 1)), (nitem >> 1) & 1);
       const int h0 = 32 * half;
-      const float* sum = reinterpret_cast<const float*>(smem + C::kOffSum) + 256 * (nitem & 1) + h0 + lane;
-      const float l = (sum[0] + sum[64]) + (sum[128] + sum[192]);
+      const float* sum = reinterpret_cast<const float*>(smem + C::kOffSum) + 512 * (nitem & 1) + h0 + lane;
+      const float l = ((sum[0] + sum[64]) + (sum[128] + sum[192])) + ((sum[256] + sum[320]) + (sum[384] + sum[448]));
       const float ref = reinterpret_cast<const float*>(smem + C::kOffRef)[64 * (nitem & 1) + h0 + lane];
       const float inv = l > 0.f ? 1.f / l : 0.f;     // of head h0 + lane
       __syncwarp();
@@ -574,76 +576,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* red = reinterpret_cast<float*>(smem + C::kOffRed);
     float* bc = reinterpret_cast<float*>(smem + C::kOffBc);
     volatile uint32_t* moved_of = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMoved);   // heads to rescale
-    const int four = 2 * th + part;                  // which 16 rows of a tile
+    const int eight = 2 * th + part;                 // which 8 rows of a tile
     float m_ref = 0.f, l_sum = 0.f, fac = 1.f;
     int rk = 0;
     auto wait = [&](uint32_t bb, uint32_t par) {     // (every lane for itself: a third of the time of one for all)
       if (!aborted && !__all_sync(0xffffffffu, mbar_wait(bb, par, wc))) aborted = true;
     };
-    // this head's four values, of the four threads that share it
-    auto share = [&](float v, float (&all)[4]) {
-      float* r = red + (rk & 1) * 256;
-      r[four * 64 + hl] = v;
+    // the largest of this head's values, of the eight threads that share it
+    auto largest = [&](float v) -> float {
+      float* r = red + (rk++ & 1) * 512;
+      r[eight * 64 + hl] = v;
       named_bar_sync(kBarAll, 32 * kSoftWarps);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) all[i] = r[i * 64 + hl];
-      ++rk;
+      v = max3(r[hl], r[64 + hl], max3(r[128 + hl], r[192 + hl], r[256 + hl]));
+      return max3(v, r[320 + hl], fmaxf(r[384 + hl], r[448 + hl]));
     };
-    uint32_t kept[16];                               // this part's scores of a tile's 16 rows, on their way
-    float2 x[8];                                     // exponents of a tile's 16 rows
-    // Scores of tile g, from TMEM: the thread of the hi part keeps rows 0-15 of these 32 and sends the others, that
-    // of the lo part the other way round.
+    uint32_t kept[8];                                // this part's scores of a tile's 8 rows, on their way
+    float2 x[4];                                     // exponents of a tile's 8 rows
+    // Scores of tile g, from TMEM: the thread of the hi part keeps rows 0-7 of these 16 and sends the others, that of
+    // the lo part the other way round.  (What was sent last has been read: the other thread has voted since.)
     auto load_scores = [&](uint32_t g) {
       wait(bar(C::bSFull + (g & 1)), (g >> 1) & 1);
-      uint32_t sent[16];
+      uint32_t sent[8];
       if (!aborted) {
         tc_fence_after();
-        const uint32_t ts = tmem + quad + kTmS + T * (g & 1) + 32 * th;
-        tmem_ld16(ts + 16 * (1 - part), sent);
-        tmem_ld16(ts + 16 * part, kept);
+        const uint32_t ts = tmem + quad + kTmS + T * (g & 1) + 16 * th;
+        tmem_ld8(ts + 8 * (1 - part), sent);
+        tmem_ld8(ts + 8 * part, kept);
         tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) kept[i] = sent[i] = 0;
+        for (int i = 0; i < 8; ++i) kept[i] = sent[i] = 0;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0 && !aborted) mbar_arrive(bar(C::bSEmpty + (g & 1)));
-      uint4* xo = reinterpret_cast<uint4*>(smem + C::kOffX + (g & 1) * kXBytes) + warp * 128 + lane;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) xo[32 * k] = make_uint4(sent[4 * k], sent[4 * k + 1], sent[4 * k + 2], sent[4 * k + 3]);
+      uint4* xo = reinterpret_cast<uint4*>(smem + C::kOffX) + warp * 64 + lane;
+      xo[0] = make_uint4(sent[0], sent[1], sent[2], sent[3]);
+      xo[32] = make_uint4(sent[4], sent[5], sent[6], sent[7]);
     };
     // the other part's scores and the exponents; their largest
     const float w_own = part == 0 ? 1.f : kLoWeight, w_other = part == 0 ? kLoWeight : 1.f;
     auto exponents = [&](uint32_t g, int left) -> float {
       wait(bar(C::bScFull + g % kScSlots), (g / kScSlots) & 1);
-      named_bar_sync(kBarPair0 + 2 * (q & 1) + th, 64);
-      const float4* xi = reinterpret_cast<const float4*>(smem + C::kOffX + (g & 1) * kXBytes) + (warp ^ 2) * 128 + lane;
-      const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 4 * four;
+      named_bar_sync(kBarPair0 + 4 * (q & 1) + th, 64);
+      const float4* xi = reinterpret_cast<const float4*>(smem + C::kOffX) + (warp ^ 2) * 64 + lane;
+      const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 2 * eight;
       const float2 f_own = f2_pack(fac * w_own, fac * w_own), f_other = f2_pack(fac * w_other, fac * w_other);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         const float4 o = xi[32 * k], f = sc[k], lg = sc[T / 4 + k];
         float2 t = f2_mul(f2_pack(__uint_as_float(kept[4 * k]), __uint_as_float(kept[4 * k + 1])), f_own);
         x[2 * k] = f2_fma(f2_fma(f2_pack(o.x, o.y), f_other, t), f2_pack(f.x, f.y), f2_pack(lg.x, lg.y));
         t = f2_mul(f2_pack(__uint_as_float(kept[4 * k + 2]), __uint_as_float(kept[4 * k + 3])), f_own);
         x[2 * k + 1] = f2_fma(f2_fma(f2_pack(o.z, o.w), f_other, t), f2_pack(f.z, f.w), f2_pack(lg.z, lg.w));
       }
-      const int nvalid = left - 16 * four;
-      if (nvalid < 16) {
+      const int nvalid = left - 8 * eight;
+      if (nvalid < 8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           if (2 * i >= nvalid) x[i].x = -INFINITY;
           if (2 * i + 1 >= nvalid) x[i].y = -INFINITY;
         }
       }
-      float m0 = fmaxf(x[0].x, x[0].y), m1 = fmaxf(x[1].x, x[1].y);
-#pragma unroll
-      for (int i = 2; i < 8; i += 2) {
-        m0 = max3(m0, x[i].x, x[i].y);
-        m1 = max3(m1, x[i + 1].x, x[i + 1].y);
-      }
-      return fmaxf(m0, m1);
+      return max3(max3(x[0].x, x[0].y, x[1].x), max3(x[1].y, x[2].x, x[2].y), fmaxf(x[3].x, x[3].y));
     };
     griddep_wait();                                  // the factors come from the kernel before
     // 2^-a of this head in the next usable item from `it` on, loaded while the item before is worked on
@@ -669,37 +664,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx = exponents(g, n);
       for (int j = 0; j < nt; ++j, ++g) {
         const uint32_t buf = g & 1;
-        if (j + 1 < nt) load_scores(g + 1);
         const bool moved = named_bar_or(kBarVote, 32 * kSoftWarps, mx > m_ref + kLag);
         if (moved) {                                 // some head's reference moves
-          float all[4];
-          share(mx, all);
-          const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+          const float mt = largest(mx);
           const float mn = mt > m_ref + kLag ? mt : m_ref;
           const float alpha = mn == m_ref ? 1.f : ex2_approx(m_ref - mn);
           m_ref = mn;
           l_sum *= alpha;
-          if (four == 0) {                           // (warps 0 and 1)
+          if (eight == 0) {                          // (warps 0 and 1)
             bc[hl] = alpha;
             const uint32_t which = __ballot_sync(0xffffffffu, alpha != 1.f);
             if (lane == 0) moved_of[warp] = which;
           }
         }
-        // weights and their parts; 16 rows are one 16-byte chunk of each
-        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 4 * four;
-        uint32_t w0[4], w1[4], w2[4], w3[4];
+        if (j + 1 < nt) load_scores(g + 1);
+        // weights and their parts; 8 rows are half a 16-byte chunk of each
+        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 2 * eight;
+        uint32_t w0[2], w1[2], w2[2], w3[2];
         const float2 shift = f2_pack(kTop - m_ref, kTop - m_ref);
-        float2 l2 = f2_pack(0.f, 0.f), l3 = l2;
+        float2 l2 = f2_pack(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
           const float4 iv = sc[2 * T / 4 + k];
           uint32_t c0[2], c1[2], c2[2], c3[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float2 e2 = f2_add(x[2 * k + i], shift);
             float2 r = f2_pack(ex2_approx(e2.x), ex2_approx(e2.y));
-            if (i == 0) l2 = f2_fma(r, f2_pack(iv.x, iv.y), l2);
-            else l3 = f2_fma(r, f2_pack(iv.z, iv.w), l3);
+            l2 = f2_fma(r, i ? f2_pack(iv.z, iv.w) : f2_pack(iv.x, iv.y), l2);
             if constexpr (kFine) {
               const float2 minus = f2_pack(-1.f, -1.f);
               c0[i] = e4m3x2(r.x, r.y);
@@ -720,17 +712,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             w3[k] = c3[0] | (c3[1] << 16);
           }
         }
-        l2 = f2_add(l2, l3);
         l_sum += l2.x + l2.y;
         if (g >= 2) wait(bar(C::bEmpty + (g - 2) % C::kUnits), ((g - 2) / C::kUnits) & 1);   // these weights' last use
         if (!aborted) {
-          uint8_t* row = smem + C::kOffP + buf * C::kPBuf + hl * 128;
-          const int sw = hl & 7;
-          *reinterpret_cast<uint4*>(row + ((four ^ sw) << 4)) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-          *reinterpret_cast<uint4*>(row + (((4 + four) ^ sw) << 4)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          // byte 8 eight of the head's 64 (hi), then the same of the lo part: chunks c at c ^ (head mod 8)
+          uint8_t* row = smem + C::kOffP + buf * C::kPBuf + hl * 128 + 8 * part;
+          const int at = (th ^ (hl & 7)) << 4, at_lo = ((4 + th) ^ (hl & 7)) << 4;
+          *reinterpret_cast<uint2*>(row + at) = make_uint2(w0[0], w0[1]);
+          *reinterpret_cast<uint2*>(row + at_lo) = make_uint2(w1[0], w1[1]);
           if constexpr (kFine) {
-            *reinterpret_cast<uint4*>(row + kPPair + ((four ^ sw) << 4)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-            *reinterpret_cast<uint4*>(row + kPPair + (((4 + four) ^ sw) << 4)) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+            *reinterpret_cast<uint2*>(row + kPPair + at) = make_uint2(w2[0], w2[1]);
+            *reinterpret_cast<uint2*>(row + kPPair + at_lo) = make_uint2(w3[0], w3[1]);
           }
         }
         fence_proxy_async_smem();
@@ -743,24 +735,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j + 1 < nt) mx = exponents(g + 1, n - (j + 1) * T);
         if (moved) {
           // O in the new units, by now that the sum of the tile before is done or nearly so.  A head is a column of
-          // each block; this warp has its 32 dims of blocks 2 th and 2 th + 1.
+          // each block; this warp has its 32 dims of block th.
           named_bar_sync(kBarAll, 32 * kSoftWarps);  // the factors are there
           if (j > 0) {
             wait(bar(C::bEmpty + (g - 1) % C::kUnits), ((g - 1) / C::kUnits) & 1);
             tc_fence_after();
-            const uint32_t to = tmem + quad + kTmO + 128 * th;
+            const uint32_t to = tmem + quad + kTmO + 64 * th;
             if (!aborted) {
 #pragma unroll
               for (int w = 0; w < 2; ++w) {
                 for (uint32_t m = moved_of[w]; m; m &= m - 1) {
                   const int h = 32 * w + __ffs(m) - 1;
                   const float f = bc[h];
-                  uint32_t a, z;
+                  uint32_t a;
                   tmem_ld1(to + h, a);
-                  tmem_ld1(to + 64 + h, z);
                   tmem_wait_ld();
                   tmem_st1(to + h, __float_as_uint(__uint_as_float(a) * f));
-                  tmem_st1(to + 64 + h, __float_as_uint(__uint_as_float(z) * f));
                 }
               }
             }
@@ -773,8 +763,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // what the output needs
       if (nitem >= 2) wait(bar(C::bSumEmpty + (nitem & 1)), ((nitem >> 1) - 1) & 1);
-      reinterpret_cast<float*>(smem + C::kOffSum)[256 * (nitem & 1) + 64 * four + hl] = l_sum;
-      if (four == 0) reinterpret_cast<float*>(smem + C::kOffRef)[64 * (nitem & 1) + hl] = m_ref;
+      reinterpret_cast<float*>(smem + C::kOffSum)[512 * (nitem & 1) + 64 * eight + hl] = l_sum;
+      if (eight == 0) reinterpret_cast<float*>(smem + C::kOffRef)[64 * (nitem & 1) + hl] = m_ref;
       __syncwarp();
       if (lane == 0 && !aborted) mbar_arrive(bar(C::bSumFull + (nitem & 1)));
       ++nitem;
