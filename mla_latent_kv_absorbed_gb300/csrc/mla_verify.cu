@@ -14,11 +14,13 @@
 // second walks the inverse of the node's distribution child by child.)
 //
 // A pick near a border of the running sum is decided by the sum's last bits,
-// so sums are held to about 48 bits: t - q in fp32 with its exact error (t > q
-// >= 0: t - d and the rest are exact), both added to a pair of fp32 numbers with
-// the addition's exact error, pairs joined in 64 bits.  That is 17 fp32
-// operations an element; in 64 bits they would take the SM longer than the
-// element's eight bytes from memory (one two-hundredth of the fp32 rate).
+// so sums are held to about 47 bits, as pairs of fp32 numbers: t - q with its
+// exact error (t > q >= 0: t - d and the rest are exact), added to a pair with
+// the addition's exact error.  That is 17 fp32 operations an element.  64-bit
+// arithmetic, at one two-hundredth of fp32's rate, would take longer than the
+// element's eight bytes from memory; even for the few sums of sums it took a
+// quarter of the kernel's time.  The tests u a < t are exact: the product as a
+// pair by a fused multiply-add.
 //
 // One cluster of CTAs a request, each a stretch of the row: every CTA walks the
 // drafts itself (one warp, a few hundred bytes, the same answer), sums its
@@ -34,7 +36,7 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = kWarps;
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
@@ -43,8 +45,33 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
   return n;
 }
-__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+__device__ __forceinline__ void st_cluster_f2(uint32_t addr, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// A number as the sum x + y of two, |y| at most half a step of x.
+using Pair = float2;
+__device__ __forceinline__ Pair pair_of(float big, float small) {   // |big| >= |small|, or big = 0
+  const float s = __fadd_rn(big, small);
+  return make_float2(s, __fsub_rn(small, __fsub_rn(s, big)));
+}
+// a + b and what rounding left of it
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
+  return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z)));
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.x, b.x);
+  return pair_of(s.x, __fadd_rn(s.y, __fadd_rn(a.y, b.y)));
+}
+__device__ __forceinline__ Pair minus(Pair a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ Pair times(Pair a, float b) {
+  const float p = __fmul_rn(a.x, b);
+  return pair_of(p, __fmaf_rn(a.y, b, __fmaf_rn(a.x, b, -p)));
+}
+__device__ __forceinline__ bool above(Pair a, Pair b) { return a.x > b.x || (a.x == b.x && a.y > b.y); }
+__device__ __forceinline__ Pair shfl_xor(Pair a, int o) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, a.x, o), __shfl_xor_sync(0xffffffffu, a.y, o));
 }
 
 // A probability: NaN and negative values count as 0, values past 1 as 1.
@@ -56,6 +83,13 @@ struct Walk {
   int below;                  // the rejected draft whose q is taken off, or -1
   int excluded;               // tokens whose mass is taken out
 };
+
+// max(t - q, 0), exactly.
+__device__ __forceinline__ Pair rest(float t, float q) {
+  const bool more = t > q;
+  const float d = more ? __fsub_rn(t, q) : 0.f;
+  return make_float2(d, more ? __fsub_rn(__fsub_rn(t, d), q) : 0.f);
+}
 
 // One warp: lane i has drafts i and 32 + i.
 __device__ __forceinline__ Walk walk_drafts(const VerifyParams& p, int b, int lane, bool write, int32_t* gone) {
@@ -98,28 +132,43 @@ __device__ __forceinline__ Walk walk_drafts(const VerifyParams& p, int b, int la
   int path[2] = {lane == 0 ? 0 : -1, -1};
   int node = 0, count = 1;
   unsigned long long rejected = 0;
-  for (bool moved = true; moved;) {                // at most W - 1 children are tried in all
-    unsigned long long kids = both(par[0] == node, par[1] == node);
-    rejected = 0;
-    double left = 1.0;
-    moved = false;
-    while (kids) {
-      const int c = __ffsll(static_cast<long long>(kids)) - 1;
-      kids &= kids - 1;
-      const int x = of(tok, c);
-      const bool again = both((rejected >> lane & 1) && tok[0] == x, (rejected >> (32 + lane) & 1) && tok[1] == x) != 0;
-      const double mass = again ? 0.0 : static_cast<double>(of(t, c));
-      const double against = p.draft ? static_cast<double>(of(q, c)) : left;
-      if (static_cast<double>(fmaxf(of(u, c), 0.f)) * against < mass) {
-        node = c;
-        path[0] = lane == count ? c : path[0];
-        path[1] = lane + 32 == count ? c : path[1];
-        ++count;
-        moved = true;
-        break;
+  // a draft's test against the share `left` of its node's mass, or its own probability
+  auto holds = [&](float u, Pair against, float mass) { return above(make_float2(mass, 0.f), times(against, fmaxf(u, 0.f))); };
+  if (!p.parents) {
+    // a chain: every draft at once; those before the first that fails are accepted
+    const Pair one = make_float2(1.f, 0.f);
+    const bool a0 = holds(u[0], p.draft ? make_float2(q[0], 0.f) : one, t[0]);
+    const bool a1 = holds(u[1], p.draft ? make_float2(q[1], 0.f) : one, t[1]);
+    const unsigned long long fail = ~(both(a0, a1) | 1ull);
+    count = fail ? min(__ffsll(static_cast<long long>(fail)) - 1, W) : W;
+    node = count - 1;
+    if (count < W) rejected = 1ull << count;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) path[k] = lane + 32 * k < count ? lane + 32 * k : -1;
+  } else {
+    for (bool moved = true; moved;) {              // at most W - 1 children are tried in all
+      unsigned long long kids = both(par[0] == node, par[1] == node);
+      rejected = 0;
+      Pair left = make_float2(1.f, 0.f);
+      moved = false;
+      while (kids) {
+        const int c = __ffsll(static_cast<long long>(kids)) - 1;
+        kids &= kids - 1;
+        const int x = of(tok, c);
+        const bool again = both((rejected >> lane & 1) && tok[0] == x, (rejected >> (32 + lane) & 1) && tok[1] == x) != 0;
+        const float mass = again ? 0.f : of(t, c);
+        if (holds(of(u, c), left, mass)) {
+          node = c;
+          path[0] = lane == count ? c : path[0];
+          path[1] = lane + 32 == count ? c : path[1];
+          ++count;
+          moved = true;
+          break;
+        }
+        rejected |= 1ull << c;
+        left = add(left, make_float2(-mass, 0.f));
+        if (!(left.x > 0.f)) left = make_float2(0.f, 0.f);
       }
-      rejected |= 1ull << c;
-      left = fmax(left - mass, 0.0);
     }
   }
   if (write) {
@@ -146,24 +195,24 @@ __device__ __forceinline__ Walk walk_drafts(const VerifyParams& p, int b, int la
 // Which of `n` parts, in their order, the running sum passes `thr` in (the last
 // with any mass where rounding or a number of 1 leaves it short; 0 without mass),
 // and the sum before it.
-__device__ __forceinline__ int pick(const double* sum, int n, double thr, double& before) {
+__device__ __forceinline__ int pick(const Pair* sum, int n, Pair thr, Pair& before) {
   int at = 0;
-  double run = 0.0;
-  before = 0.0;
+  Pair run = make_float2(0.f, 0.f);
+  before = run;
   for (int i = 0; i < n; ++i) {
-    const double s = sum[i];
-    if (s > 0.0) {
+    const Pair s = sum[i], upto = add(run, s);
+    if (s.x > 0.f) {
       at = i;
       before = run;
-      if (run + s > thr) break;
+      if (above(upto, thr)) break;
     }
-    run += s;
+    run = upto;
   }
   return at;
 }
 
 __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) {
-  __shared__ double cta_sum[kMaxCluster], warp_sum[kWarps], part_sum[kWarps];
+  __shared__ Pair cta_sum[kMaxCluster], warp_sum[kWarps], part_sum[kWarps];
   __shared__ int32_t gone[kMaxDrafts];
   __shared__ Walk walk;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -223,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
     }
   };
   // sum of max(t - q, 0) over blocks [k0, k1), by a warp; in every lane
-  auto sum_of = [&](int k0, int k1) {
+  auto sum_of = [&](int k0, int k1) -> Pair {
     float s = 0.f, e = 0.f;
     constexpr int kDeep = 4;
     for (int k = k0 + lane; k < k1; k += 32 * kDeep) {
@@ -237,97 +286,96 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
         clean(k + 32 * j, t[j], q[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool more = t[j][i] > q[j][i];
-          const float d = more ? __fsub_rn(t[j][i], q[j][i]) : 0.f;
-          const float de = more ? __fsub_rn(__fsub_rn(t[j][i], d), q[j][i]) : 0.f;
-          const float n = __fadd_rn(s, d);
-          const float z = __fsub_rn(n, s);
-          const float err = __fadd_rn(__fsub_rn(s, __fsub_rn(n, z)), __fsub_rn(d, z));
-          e += err + de;
-          s = n;
+          const Pair r = rest(t[j][i], q[j][i]), n = two_sum(s, r.x);
+          s = n.x;
+          e += n.y + r.y;
         }
       }
     }
-    double all = static_cast<double>(s) + static_cast<double>(e);
+    Pair all = pair_of(s, e);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    for (int o = 16; o; o >>= 1) all = add(all, shfl_xor(all, o));
     return all;
   };
 
   const int mine = rank * kWarps + warp;
-  const double part = sum_of(first(mine), first(mine + 1));
+  const Pair part = sum_of(first(mine), first(mine + 1));
   if (lane == 0) warp_sum[warp] = part;
   __syncwarp();
   cluster_wait();
   __syncthreads();
-  if (tid < C) {
-    double all = 0.0;
+  if (warp == 0) {
+    Pair all = lane < kWarps ? warp_sum[lane] : make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) all += warp_sum[i];
-    st_cluster_f64(mapa_shared(smem_u32(cta_sum + rank), tid), all);
+    for (int o = kWarps / 2; o; o >>= 1) all = add(all, shfl_xor(all, o));
+    if (lane < C) st_cluster_f2(mapa_shared(smem_u32(cta_sum + rank), lane), all);   // (C <= kWarps: they have it)
   }
   __syncwarp();
   cluster_arrive();
   cluster_wait();
-  double total = 0.0;
-  for (int i = 0; i < C; ++i) total += cta_sum[i];
-  if (!(total > 0.0)) {
+  Pair total = make_float2(0.f, 0.f);
+  for (int i = 0; i < C; ++i) total = add(total, cta_sum[i]);
+  if (!(total.x > 0.f)) {
     if (rank == 0 && tid == 0) p.next[b] = -1;
     return;
   }
-  double thr = static_cast<double>(__ldg(p.uniforms + static_cast<long long>(b) * p.width)) * total;
-  double before;
+  Pair thr = times(total, __ldg(p.uniforms + static_cast<long long>(b) * p.width));
+  Pair before;
   if (pick(cta_sum, C, thr, before) != rank) return;
-  thr -= before;
+  thr = add(thr, minus(before));
   const int w = pick(warp_sum, kWarps, thr, before);
-  thr -= before;
+  thr = add(thr, minus(before));
   // the warp's part in eighths
   const int k0 = first(rank * kWarps + w), k1 = first(rank * kWarps + w + 1);
   const int eighth = (k1 - k0 + kWarps - 1) / kWarps;
   const int e0 = min(k0 + warp * eighth, k1), e1 = min(e0 + eighth, k1);
-  const double sub = sum_of(e0, e1);
+  const Pair sub = sum_of(e0, e1);
   if (lane == 0) part_sum[warp] = sub;
   __syncthreads();
   if (pick(part_sum, kWarps, thr, before) != warp) return;
-  thr -= before;
+  thr = add(thr, minus(before));
   // 32 blocks at a time, a block a lane
-  double run = 0.0;
+  Pair run = make_float2(0.f, 0.f);
   int last = -1;
   for (int k = e0; k < e1; k += 32) {
     float t[4], q[4];
-    double r[4] = {0.0, 0.0, 0.0, 0.0}, s = 0.0;
+    Pair r[4], s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = s;
     if (k + lane < e1) {
       load(k + lane, t, q);
       clean(k + lane, t, q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        r[i] = t[i] > q[i] ? static_cast<double>(t[i]) - static_cast<double>(q[i]) : 0.0;
-        s += r[i];
+        r[i] = rest(t[i], q[i]);
+        s = add(s, r[i]);
       }
     }
-    double upto = s;
+    Pair upto = s, less = make_float2(0.f, 0.f);   // with, and without this lane's own
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
+      const Pair x = make_float2(__shfl_up_sync(0xffffffffu, upto.x, o), __shfl_up_sync(0xffffffffu, upto.y, o));
+      if (lane >= o) upto = add(upto, x);
     }
-    const uint32_t some = __ballot_sync(0xffffffffu, s > 0.0);
-    const uint32_t past = __ballot_sync(0xffffffffu, s > 0.0 && run + upto > thr);
+    less = make_float2(__shfl_up_sync(0xffffffffu, upto.x, 1), __shfl_up_sync(0xffffffffu, upto.y, 1));
+    if (lane == 0) less = make_float2(0.f, 0.f);
+    const uint32_t some = __ballot_sync(0xffffffffu, s.x > 0.f);
+    const uint32_t past = __ballot_sync(0xffffffffu, s.x > 0.f && above(add(run, upto), thr));
     // the first lane past the number, or, to fall back on, the last one with mass
     const int who = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : -1;
     int v = -1;
     if (who == lane) {
-      double x = run + (upto - s);
+      Pair x = add(run, less);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bool over = v >= 0 && past && x > thr;   // passed at an earlier element
-        x += r[i];
-        if (!over && r[i] > 0.0) v = 4 * (k + lane) - lead + i;
+        const bool over = v >= 0 && past && above(x, thr);   // passed at an earlier element
+        x = add(x, r[i]);
+        if (!over && r[i].x > 0.f) v = 4 * (k + lane) - lead + i;
       }
     }
     if (who >= 0) last = __shfl_sync(0xffffffffu, v, who);
     if (past) break;
-    run += __shfl_sync(0xffffffffu, upto, 31);
+    run = add(run, make_float2(__shfl_sync(0xffffffffu, upto.x, 31), __shfl_sync(0xffffffffu, upto.y, 31)));
   }
   if (lane == 0) p.next[b] = last;
 }
@@ -340,7 +388,7 @@ int launch_verify(const VerifyParams& p, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms < 1) return MLA_ERR_CUDA;
   int ctas = 1;
-  while (ctas < 8 && static_cast<long long>(p.batch) * ctas < 8ll * sms && p.vocab / (2 * ctas * kWarps) >= 128) ctas *= 2;
+  while (ctas < kMaxCluster && static_cast<long long>(p.batch) * ctas < 8ll * sms && p.vocab / (2 * ctas * kWarps) >= 128) ctas *= 2;
   const long long grid = static_cast<long long>(p.batch) * ctas;
   if (grid > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg{};
