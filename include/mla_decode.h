@@ -793,7 +793,8 @@ size_t mla_slots_workspace_bytes(int64_t num_slots);
  * passes capacity, or the freed slots freed_capacity (the rest is not written).
  * Pointers are 4-byte aligned (workspace 16); outputs apart from the inputs.
  * Errors: MLA_ERR_INVALID_ARG for bad pointers or sizes, one of a pair without
- * the other; MLA_ERR_UNSUPPORTED for q_len > 64 (with path);
+ * the other; MLA_ERR_UNSUPPORTED for q_len > 64 (with path), or more than 65536
+ * requests with freed;
  * MLA_ERR_WORKSPACE for too small a workspace.  Nothing is launched then. */
 int mla_repack_requests(const int32_t* kv_indptr, const int32_t* kv_indices, int64_t entries, int32_t batch,
                         const int32_t* sources, int32_t new_batch, const int32_t* path, const int32_t* accepted,

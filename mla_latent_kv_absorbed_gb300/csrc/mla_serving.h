@@ -12,6 +12,7 @@
 namespace mla {
 
 constexpr int kMaxDrafts = 64;        // drafts of a request (a 64-bit set of them)
+constexpr int kMaxRequests = 65536;   // requests of a batch whose lists are rewritten with their freed slots
 
 struct VerifyParams {
   const float* target;        // row n of request b at target + b*t_bs + n*t_rs
@@ -66,6 +67,7 @@ struct RepackParams {
   int* status;
   long long entries, capacity, freed_capacity, num_slots;
   int batch, new_batch, width;
+  bool marked;                // (launch_repack: the marking kernel runs before the others)
 };
 
 int launch_repack(const RepackParams& p, cudaStream_t stream);

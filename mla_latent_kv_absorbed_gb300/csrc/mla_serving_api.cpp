@@ -75,7 +75,7 @@ int mla_repack_requests(const int32_t* kv_indptr, const int32_t* kv_indices, int
   if ((path == nullptr) != (accepted == nullptr) || (freed == nullptr) != (freed_count == nullptr))
     return MLA_ERR_INVALID_ARG;
   if (path && q_len < 1) return MLA_ERR_INVALID_ARG;
-  if (path && q_len > kMaxDrafts) return MLA_ERR_UNSUPPORTED;
+  if ((path && q_len > kMaxDrafts) || (freed && batch > kMaxRequests)) return MLA_ERR_UNSUPPORTED;
   if (!ready(workspace)) return MLA_ERR_INVALID_ARG;
   if (workspace_bytes < slots_ws(num_slots).total) return MLA_ERR_WORKSPACE;
   if (!ready(kv_indptr, 4) || !ready(new_indptr, 4) || (new_batch > 0 && !ready(sources, 4)) ||

@@ -45,18 +45,22 @@ __device__ __forceinline__ void set_bit(uint32_t* bits, int slot) { atomicOr(bit
 // The rows of an old request that its successors keep: the first `base`, then
 // the drafts of its path.
 struct Kept {
-  int start, base, count;
+  int start, rows, base, count;
 };
+__device__ __forceinline__ int sat_add(int a, int b) {      // of numbers that are not negative
+  const unsigned s = static_cast<unsigned>(a) + static_cast<unsigned>(b);
+  return s > 0x7FFFFFFFu ? 0x7FFFFFFF : static_cast<int>(s);
+}
 __device__ __forceinline__ Kept kept_of(const RepackParams& p, int src, bool report) {
   if (src < 0 || src >= p.batch) {
     if (report && src != -1) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
-    return {0, 0, 0};
+    return {0, 0, 0, 0};
   }
   const long long lo = __ldg(p.indptr + src), hi = __ldg(p.indptr + src + 1);
   const long long s = min(max(lo, 0ll), p.entries), e = min(max(hi, s), p.entries);
   const int n = static_cast<int>(e - s);
   bool bad = lo != s || hi != e;
-  Kept k{static_cast<int>(s), n, n};
+  Kept k{static_cast<int>(s), n, n, n};
   if (p.path) {
     if (n >= p.width) {
       const int a = __ldg(p.accepted + src);
@@ -72,95 +76,181 @@ __device__ __forceinline__ Kept kept_of(const RepackParams& p, int src, bool rep
   return k;
 }
 
-// Marks the slots that a request gives up: all of them where no new request
+// The kernels below go by entries, not by requests (a long request would keep
+// one block busy alone): a block takes kChunk of them, a thread kDeep in a row,
+// and finds out itself whose they are, from the requests' ends in shared memory,
+// 256 requests at a time.  Bound: the launches and four or five dependent loads
+// each (request, list, entry, set of slots).
+constexpr int kDeep = 8, kChunk = kListThreads * kDeep, kWindow = kListThreads;
+
+// The first of n ascending ends that is past `at` (n: none).
+__device__ __forceinline__ int first_past(const int* ends, int n, long long at) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > at) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Marks the slots that requests give up: all of them where no new request
 // continues it, else those of the drafts off its path.  Another request may hold
 // them too (a shared prefix): the lists' kernel takes those back.
 __global__ void __launch_bounds__(kListThreads) repack_mark_kernel(const RepackParams p) {
+  __shared__ uint32_t goes_on[(kMaxRequests + 31) / 32];
+  __shared__ Kept rows_of[kWindow];
+  __shared__ unsigned long long on_path[kWindow];    // a request's accepted drafts
+  __shared__ int ends[kWindow];
   griddep_wait();
   griddep_launch_dependents();
-  const int o = blockIdx.x, tid = threadIdx.x;
-  const Kept k = kept_of(p, o, false);
-  bool here = false;
-  for (int i = tid; i < p.new_batch; i += kListThreads) here |= __ldg(p.sources + i) == o;
-  const bool goes_on = __syncthreads_or(here) != 0;
-  auto give_up = [&](int j) {
-    const int slot = __ldg(p.indices + j);
-    if (slot >= 0 && slot < p.num_slots) set_bit(p.bits, slot);
-    else record_status(p.status, MLA_ERR_INDEX_OOB);
-  };
-  if (!goes_on) {
-    const long long lo = __ldg(p.indptr + o), hi = __ldg(p.indptr + o + 1);
-    const int s = static_cast<int>(min(max(lo, 0ll), p.entries));
-    const int e = static_cast<int>(min(max(hi, static_cast<long long>(s)), p.entries));
-    for (long long j = s + blockIdx.y * kListThreads + tid; j < e; j += static_cast<long long>(gridDim.y) * kListThreads)
-      give_up(static_cast<int>(j));
-  } else if (p.path && blockIdx.y == 0 && tid < p.width) {
-    const int n = __ldg(p.indptr + o + 1) - __ldg(p.indptr + o);
-    if (n < p.width || k.base != n - p.width) return;
-    bool kept = false;
-    for (int i = 0; i < k.count - k.base; ++i)
-      kept |= min(max(__ldg(p.path + static_cast<long long>(o) * p.width + i), 0), p.width - 1) == tid;
-    if (!kept) give_up(k.start + k.base + tid);
+  const int tid = threadIdx.x;
+  const long long lo = static_cast<long long>(blockIdx.x) * kChunk, hi = min(lo + kChunk, p.entries);
+  const long long mine = lo + kDeep * tid;
+  int slot[kDeep];
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) slot[d] = mine + d < hi ? __ldg(p.indices + mine + d) : 0;
+  for (int i = tid; i < (p.batch + 31) / 32; i += kListThreads) goes_on[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < p.new_batch; i += kListThreads) {
+    const int o = __ldg(p.sources + i);
+    if (o >= 0 && o < p.batch) atomicOr(goes_on + (o >> 5), 1u << (o & 31));
+  }
+  // the window of the block's first entry: lists ascend, so the last that starts at or before it
+  int r0 = 0;
+  if (p.batch > kWindow) {
+    int top = p.batch - 1;
+    while (r0 < top) {
+      const int mid = (r0 + top + 1) >> 1;
+      if (__ldg(p.indptr + mid) <= lo) r0 = mid;
+      else top = mid - 1;
+    }
+  }
+  for (; r0 < p.batch; r0 += kWindow) {
+    const int n = min(kWindow, p.batch - r0);
+    Kept k{0, 0, 0, 0};
+    if (tid < n) k = kept_of(p, r0 + tid, false);
+    unsigned long long path = 0;
+    if (k.base < k.rows && k.start + k.rows > lo && k.start + k.base < hi) {
+      const int32_t* steps = p.path + static_cast<long long>(r0 + tid) * p.width;
+#pragma unroll 8
+      for (int i = 0; i < k.count - k.base; ++i) path |= 1ull << min(max(__ldg(steps + i), 0), p.width - 1);
+    }
+    __syncthreads();                                 // (the window before has been used; goes_on is made)
+    on_path[tid] = path;
+    rows_of[tid] = k;
+    ends[tid] = k.start + k.rows;
+    __syncthreads();
+    if (rows_of[0].start >= hi) break;
+    int a = first_past(ends, n, mine);
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const long long at = mine + d;
+      if (at >= hi) break;
+      while (a < n && ends[a] <= at) ++a;
+      if (a >= n || at < rows_of[a].start) continue; // another window's, or nobody's
+      const Kept& m = rows_of[a];
+      const int o = r0 + a, step = static_cast<int>(at) - m.start - m.base;
+      if ((goes_on[o >> 5] >> (o & 31) & 1) && (step < 0 || (on_path[a] >> step & 1))) continue;
+      if (slot[d] >= 0 && slot[d] < p.num_slots) set_bit(p.bits, slot[d]);
+      else record_status(p.status, MLA_ERR_INDEX_OOB);
+    }
   }
 }
 
-// The new lists: block (r, y) writes its share of request r, whose place it
-// adds up itself from the lengths before it.
+// The new lists.  The lengths of the new requests are added up, a window at a
+// time, until the block's entries are passed.
 __global__ void __launch_bounds__(kListThreads) repack_lists_kernel(const RepackParams p) {
-  __shared__ long long sums[kListThreads / 32];
-  const int r = blockIdx.x, tid = threadIdx.x;
+  __shared__ int ends[kWindow];                      // in the new lists, from the window's first on
+  __shared__ Kept rows_of[kWindow];
+  __shared__ int src_of[kWindow], warp_sums[kWindow / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // behind the marking kernel the inputs are there already: it started after whatever made them
-  if (!p.freed) griddep_wait();
-  long long before = 0;
-  for (int i = tid; i < r; i += kListThreads) before += kept_of(p, __ldg(p.sources + i), false).count;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  if ((tid & 31) == 0) sums[tid >> 5] = before;
-  __syncthreads();
-  before = 0;
-#pragma unroll
-  for (int i = 0; i < kListThreads / 32; ++i) before += sums[i];
-  const int src = r < p.new_batch ? __ldg(p.sources + r) : -1;
-  const bool first = blockIdx.y == 0 && tid == 0;
-  const Kept k = kept_of(p, src, first);
-  if (p.freed) griddep_wait();
+  bool waited = !p.marked;
+  if (waited) griddep_wait();
   griddep_launch_dependents();
-  if (first) {
-    p.new_indptr[r] = static_cast<int>(min(before, p.capacity));
-    if (r == p.new_batch - 1) p.new_indptr[r + 1] = static_cast<int>(min(before + k.count, p.capacity));
-    if (before + k.count > p.capacity) record_status(p.status, MLA_ERR_WORKSPACE);
-  }
-  const int32_t* path = p.path ? p.path + static_cast<long long>(src) * p.width : nullptr;
-  const long long stride = static_cast<long long>(gridDim.y) * kListThreads;
-  constexpr int kDeep = 4;
-  for (long long j0 = blockIdx.y * kListThreads + tid; j0 < k.count; j0 += kDeep * stride) {
-    int slot[kDeep];
+  const long long lo = static_cast<long long>(blockIdx.x) * kChunk, hi = min(lo + kChunk, p.capacity);
+  const long long mine = lo + kDeep * tid;
+  long long before = 0;                              // entries of the windows before
+  for (int r0 = 0; r0 < max(p.new_batch, 1); r0 += kWindow) {
+    const int r = r0 + tid;
+    const int src = r < p.new_batch ? __ldg(p.sources + r) : -1;
+    const Kept k = kept_of(p, src, blockIdx.x == 0 && r < p.new_batch);
+    // (256 forks of 2^31 entries pass 32 bits: past the capacity, sums are only held above it)
+    int upto = k.count;
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      const long long j = j0 + d * stride;
-      if (j >= k.count) continue;
-      int at = static_cast<int>(j);
-      if (at >= k.base) {
-        const int step = __ldg(path + at - k.base), ok = min(max(step, 0), p.width - 1);
-        if (step != ok) record_status(p.status, MLA_ERR_TREE);
-        at = k.base + ok;
-      }
-      slot[d] = __ldg(p.indices + k.start + at);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto = sat_add(upto, y);
     }
+    if (r0 > 0) __syncthreads();                     // the window before has been used
+    if (lane == 31) warp_sums[warp] = upto;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) upto = sat_add(upto, warp_sums[i]);
+    ends[tid] = upto;
+    rows_of[tid] = k;
+    src_of[tid] = src;
+    __syncthreads();
+    if (!waited) {
+      griddep_wait();
+      waited = true;
+    }
+    const long long total = ends[kWindow - 1];
+    if (blockIdx.x == 0) {
+      if (r < p.new_batch) p.new_indptr[r + 1] = static_cast<int>(min(before + upto, p.capacity));
+      if (r == 0) p.new_indptr[0] = 0;
+      if (tid == 0 && before + total > p.capacity) record_status(p.status, MLA_ERR_WORKSPACE);
+    } else if (before >= hi) {
+      break;
+    }
+    if (before + total > lo && before < hi) {
+      int slot[kDeep];
+      int a = first_past(ends, kWindow, mine - before);
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      const long long j = j0 + d * stride;
-      if (j >= k.count) continue;
-      if (before + j < p.capacity) p.new_indices[before + j] = slot[d];
-      if (!p.freed) continue;
-      if (slot[d] < 0 || slot[d] >= p.num_slots) {
-        record_status(p.status, MLA_ERR_INDEX_OOB);
-        continue;
+      for (int d = 0; d < kDeep; ++d) {
+        const long long in = mine + d - before;
+        slot[d] = -1;
+        if (mine + d >= hi || in < 0 || in >= total) continue;
+        while (ends[a] <= in) ++a;
+        const Kept& m = rows_of[a];
+        int at = static_cast<int>(in) - (a ? ends[a - 1] : 0);
+        if (at >= m.base) {
+          const int step = __ldg(p.path + static_cast<long long>(src_of[a]) * p.width + at - m.base);
+          const int ok = min(max(step, 0), p.width - 1);
+          if (step != ok) record_status(p.status, MLA_ERR_TREE);
+          at = m.base + ok;
+        }
+        slot[d] = __ldg(p.indices + m.start + at);
       }
-      // (few are marked: a read that another block's clearing has overtaken clears once more)
-      const uint32_t bit = 1u << (slot[d] & 31);
-      if (p.bits[slot[d] >> 5] & bit) atomicAnd(p.bits + (slot[d] >> 5), ~bit);
+      bool there[kDeep];
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) there[d] = mine + d < hi && mine + d >= before && mine + d - before < total;
+      if (there[0] && there[kDeep - 1] && (reinterpret_cast<uintptr_t>(p.new_indices) & 15) == 0) {
+        int4* out = reinterpret_cast<int4*>(p.new_indices + mine);
+        out[0] = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        out[1] = make_int4(slot[4], slot[5], slot[6], slot[7]);
+      } else {
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d)
+          if (there[d]) p.new_indices[mine + d] = slot[d];
+      }
+      if (p.freed) {
+        // (few are marked: a read that another block's clearing has overtaken clears once more)
+        uint32_t word[kDeep];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+          const bool in = slot[d] >= 0 && slot[d] < p.num_slots;
+          if (there[d] && !in) record_status(p.status, MLA_ERR_INDEX_OOB);
+          word[d] = there[d] && in ? p.bits[slot[d] >> 5] : 0;
+        }
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+          const uint32_t bit = 1u << (slot[d] & 31);
+          if (word[d] & bit) atomicAnd(p.bits + (slot[d] >> 5), ~bit);
+        }
+      }
     }
+    before += total;
   }
 }
 
@@ -204,12 +294,14 @@ __device__ __forceinline__ int cluster_scan(int x, int* warp_sums, int* cta_sums
   return before;
 }
 
-// The words that a thread of the cluster has: a stretch of its own.
+// The words that a thread of the cluster has: its warp's equal share of all, in the lanes' order.
 __device__ __forceinline__ void my_words(long long num_slots, long long& w0, long long& w1) {
-  const long long words = (num_slots + 31) / 32, threads = kScanCtas * kScanThreads;
-  const long long per = (words + threads - 1) / threads;
-  w0 = min((static_cast<long long>(cluster_ctarank()) * kScanThreads + threadIdx.x) * per, words);
-  w1 = min(w0 + per, words);
+  const long long words = (num_slots + 31) / 32, warps = kScanCtas * kScanThreads / 32;
+  const long long share = (words + warps - 1) / warps, per = (share + 31) / 32;
+  const long long first = (static_cast<long long>(cluster_ctarank()) * (kScanThreads / 32) + (threadIdx.x >> 5)) * share;
+  const long long end = min(first + share, words);
+  w0 = min(first + (threadIdx.x & 31) * per, end);
+  w1 = min(w0 + per, end);
 }
 
 // Marked slots to an ascending list; the bitmap is zero again.
@@ -230,7 +322,7 @@ __global__ void __launch_bounds__(kScanThreads) freed_kernel(const RepackParams 
     for (; m; m &= m - 1, ++at)
       if (at < p.freed_capacity) p.freed[at] = static_cast<int>(32 * w) + __ffs(m) - 1;
   }
-  if (w0 == 0 && threadIdx.x == 0 && cluster_ctarank() == 0) {
+  if (threadIdx.x == 0 && cluster_ctarank() == 0) {
     p.freed_count[0] = all;
     if (all > p.freed_capacity) record_status(p.status, MLA_ERR_WORKSPACE);
   }
@@ -268,22 +360,26 @@ __global__ void __launch_bounds__(kScanThreads) compact_scan_kernel(const Compac
   int n;
   int run = cluster_scan(mine, warp_sums, cta_sums, n);
   const long long last_word = n >> 5;
-  for (long long w = w0; w < w1; ++w) {
-    const uint32_t m = c.bits[w];
-    if (m) c.bits[w] = 0;
-    c.live[w] = make_uint2(m, static_cast<uint32_t>(run));
-    // the slots of this word below n
-    const uint32_t low = w < last_word ? 0xffffffffu : w > last_word ? 0u : (1u << (n & 31)) - 1;
-    for (uint32_t f = ~m & low; f; f &= f - 1) {
-      const int bit = __ffs(f) - 1;
-      const int slot = static_cast<int>(32 * w) + bit;
-      c.holes[slot - run - __popc(m & ((1u << bit) - 1))] = slot;
+  // a word's slots by the warp's lanes, a slot a lane
+  const int lane = threadIdx.x & 31;
+  const long long per = __shfl_sync(0xffffffffu, w1 - w0, 0);      // words of a lane (the last ones' may be fewer)
+  for (long long i = 0; i < per; ++i) {
+    const bool mine = w0 + i < w1;
+    const uint32_t m = mine ? c.bits[w0 + i] : 0;
+    if (mine) {
+      if (m) c.bits[w0 + i] = 0;
+      c.live[w0 + i] = make_uint2(m, static_cast<uint32_t>(run));
+      if (w0 + i == last_word) c.counts[1] = n - run - __popc(m & ((1u << (n & 31)) - 1));
     }
-    for (uint32_t a = m & ~low; a; a &= a - 1) {
-      const int bit = __ffs(a) - 1;
-      c.away[n - 1 - run - __popc(m & ((1u << bit) - 1))] = static_cast<int>(32 * w) + bit;
+    for (uint32_t todo = __ballot_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1;
+      const uint32_t word = __shfl_sync(0xffffffffu, m, from);
+      const int before = __shfl_sync(0xffffffffu, run, from) + __popc(word & ((1u << lane) - 1));   // live slots
+      const long long slot = 32 * (__shfl_sync(0xffffffffu, w0, from) + i) + lane;
+      const bool live = word >> lane & 1;
+      if (slot < n && !live) c.holes[slot - before] = static_cast<int>(slot);
+      if (slot >= n && live) c.away[n - 1 - before] = static_cast<int>(slot);
     }
-    if (w == last_word) c.counts[1] = n - run - __popc(m & low);
     run += __popc(m);
   }
   if (threadIdx.x == 0 && cluster_ctarank() == 0) {
@@ -317,16 +413,16 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p, 
   griddep_wait();
   griddep_launch_dependents();
   if constexpr (kLists) rewrite_lists(c);
-  constexpr int kPieces = kRowBytes / 16, kRows = kMoveThreads / kPieces, kDeep = 4;
+  constexpr int kPieces = kRowBytes / 16, kRows = kMoveThreads / kPieces, kUnroll = 4;
   const int row = threadIdx.x / kPieces, piece = threadIdx.x % kPieces;
   const int count = kLists ? __ldcg(p.count_dev) : p.count;
   const long long units = static_cast<long long>(count) * p.layers, step = static_cast<long long>(gridDim.x) * kRows;
-  for (long long u0 = static_cast<long long>(blockIdx.x) * kRows + row; u0 < units; u0 += kDeep * step) {
-    uint4 v[kDeep];
-    float s[kDeep];
-    long long to[kDeep];
+  for (long long u0 = static_cast<long long>(blockIdx.x) * kRows + row; u0 < units; u0 += kUnroll * step) {
+    uint4 v[kUnroll];
+    float s[kUnroll];
+    long long to[kUnroll];
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
+    for (int d = 0; d < kUnroll; ++d) {
       const long long u = u0 + d * step;
       to[d] = -1;
       if (u >= units) continue;
@@ -343,7 +439,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p, 
       if (p.src_scales && piece == 0) s[d] = p.src_scales[from];
     }
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
+    for (int d = 0; d < kUnroll; ++d) {
       if (to[d] < 0) continue;
       *reinterpret_cast<uint4*>(p.dst + to[d] * kRowBytes + 16 * piece) = v[d];
       if (p.src_scales && piece == 0) p.dst_scales[to[d]] = s[d];
@@ -363,26 +459,18 @@ int launch_rows(const MoveParams& m, const CompactParams& c, long long most, lon
                              : launch_after(move_kernel<2 * kRow, kLists>, dim3(grid), kMoveThreads, 1, stream, m, c);
 }
 
-// Blocks that share a request's list: enough for eight an SM, as far as lists reach.
-unsigned stripes(long long entries, int requests, int sms) {
-  const long long mean = entries / (requests > 0 ? requests : 1) / (4 * kListThreads) + 1;
-  const long long want = 8ll * sms / (requests > 0 ? requests : 1) + 1;
-  const long long n = want < 2 * mean ? want : 2 * mean;
-  return static_cast<unsigned>(n < 64 ? n : 64);
-}
-
 }  // namespace
 
-int launch_repack(const RepackParams& p, cudaStream_t stream) {
-  const int sms = device_sm_count();
-  if (sms < 1) return MLA_ERR_CUDA;
-  if (p.freed && p.batch > 0) {
-    const dim3 grid(p.batch, stripes(p.entries, p.batch, sms));
-    const int st = launch_after(repack_mark_kernel, grid, kListThreads, 1, stream, p);
+int launch_repack(const RepackParams& params, cudaStream_t stream) {
+  RepackParams p = params;
+  p.marked = p.freed && p.batch > 0 && p.entries > 0;
+  if (p.marked) {
+    const unsigned blocks = static_cast<unsigned>((p.entries + kChunk - 1) / kChunk);
+    const int st = launch_after(repack_mark_kernel, dim3(blocks), kListThreads, 1, stream, p);
     if (st != MLA_OK) return st;
   }
-  const dim3 grid(p.new_batch > 0 ? p.new_batch : 1, stripes(p.entries, p.new_batch, sms));
-  int st = launch_after(repack_lists_kernel, grid, kListThreads, 1, stream, p);
+  const unsigned blocks = static_cast<unsigned>(p.capacity > 0 ? (p.capacity + kChunk - 1) / kChunk : 1);
+  const int st = launch_after(repack_lists_kernel, dim3(blocks), kListThreads, 1, stream, p);
   if (st != MLA_OK || !p.freed) return st;
   return launch_after(freed_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, stream, p);
 }
