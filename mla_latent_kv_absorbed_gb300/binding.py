@@ -854,19 +854,23 @@ def _layers(w, name, cache, scales):
     """(slots, rows from a layer to the next, layers, bytes of a row) of a cache [N, 576] or [L, N, 576] in bf16 or
     E4M3 codes, and of its scales [N] or [L, N]."""
     import torch
-    if cache.dtype not in (torch.bfloat16, torch.uint8) or cache.dim() not in (2, 3) or cache.shape[-1] != 576:
-        raise ValueError(f"{w}: {name} is {cache.dtype} {tuple(cache.shape)}, bfloat16 or uint8 [.., slots, 576] is wanted")
-    L, N = (1, cache.shape[0]) if cache.dim() == 2 else cache.shape[:2]
-    rows = N if L <= 1 else cache.stride(0) // 576
-    if N and L and (cache.stride(-1) != 1 or (N > 1 and cache.stride(-2) != 576) or (L > 1 and cache.stride(0) % 576)):
-        raise ValueError(f"{w}: {name}'s rows do not lie one after another")
+    dt, shape = cache.dtype, cache.shape
+    codes = dt is torch.uint8
+    if not (codes or dt is torch.bfloat16) or len(shape) not in (2, 3) or shape[-1] != 576:
+        raise ValueError(f"{w}: {name} is {dt} {tuple(shape)}, bfloat16 or uint8 [.., slots, 576] is wanted")
+    L, N = (1, shape[0]) if len(shape) == 2 else shape[:2]
+    rows, dense = N, cache.is_contiguous()
+    if not dense:
+        if N and L and (cache.stride(-1) != 1 or (N > 1 and cache.stride(-2) != 576) or (L > 1 and cache.stride(0) % 576)):
+            raise ValueError(f"{w}: {name}'s rows do not lie one after another")
+        rows = N if L <= 1 else cache.stride(0) // 576
     if scales is not None:
-        if cache.dtype is not torch.uint8:
+        if not codes:
             raise ValueError(f"{w}: {name} has scales, its rows are not 8-bit")
-        _need(w, name + "'s scales", scales, torch.float32, cache.shape[:-1], dense=False)
+        _need(w, name + "'s scales", scales, torch.float32, shape[:-1], dense=False)
         if L > 1 and scales.stride(0) != rows:
             raise ValueError(f"{w}: {name}'s scales lie {scales.stride(0)} apart a layer, its rows {rows}")
-    return N, rows, L, 576 * cache.element_size()
+    return N, rows, L, 576 if codes else 1152
 
 
 def copy_rows(src_cache, src_slots, dst_cache, dst_slots, src_scales=None, dst_scales=None, workspace=None,
@@ -878,11 +882,14 @@ def copy_rows(src_cache, src_slots, dst_cache, dst_slots, src_scales=None, dst_s
     w = "mla_copy_rows"
     _status_word(w, workspace)
     sn, sr, L, nbytes = _layers(w, "src_cache", src_cache, src_scales)
-    dn, dr, dl, dbytes = _layers(w, "dst_cache", dst_cache, dst_scales)
-    if L != dl or nbytes != dbytes:
-        raise ValueError(f"{w}: the caches differ in layers or type")
-    if (src_scales is None) != (dst_scales is None):
-        raise ValueError(f"{w}: src_scales goes with dst_scales")
+    if dst_cache is src_cache and dst_scales is src_scales:
+        dn, dr = sn, sr
+    else:
+        dn, dr, dl, dbytes = _layers(w, "dst_cache", dst_cache, dst_scales)
+        if L != dl or nbytes != dbytes:
+            raise ValueError(f"{w}: the caches differ in layers or type")
+        if (src_scales is None) != (dst_scales is None):
+            raise ValueError(f"{w}: src_scales goes with dst_scales")
     n = _sizes(w, "src_slots", src_slots, 1)[0]
     _need(w, "src_slots", src_slots, torch.int32, (n,))
     _need(w, "dst_slots", dst_slots, torch.int32, (n,))

@@ -18,13 +18,15 @@ namespace {
 
 constexpr int kListThreads = 256;
 constexpr int kScanThreads = 1024, kScanCtas = 8;
+constexpr long long kBulkRows = 16384;             // (row, layer) pairs from which on rows go by bulk copies
 constexpr int kMoveThreads = 288;                  // 4 rows of 72 pieces of 16 bytes, or 8 of 36
 
 template <typename Kernel, typename... Args>
-int launch_after(Kernel* kernel, dim3 grid, int threads, int cluster, cudaStream_t stream, Args... args) {
+int launch_after(Kernel* kernel, dim3 grid, int threads, int cluster, int smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -390,11 +392,12 @@ __global__ void __launch_bounds__(kScanThreads) compact_scan_kernel(const Compac
 }
 
 // The lists, slot by slot: a live slot past the n lowest is the k-th of those.
+template <int kThreads = kMoveThreads>
 __device__ __forceinline__ void rewrite_lists(const CompactParams& c) {
   const long long total = entries_of(c);
   const int n = __ldcg(c.counts), below = n - __ldcg(c.counts + 1);
-  for (long long j = static_cast<long long>(blockIdx.x) * kMoveThreads + threadIdx.x; j < total;
-       j += static_cast<long long>(gridDim.x) * kMoveThreads) {
+  for (long long j = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; j < total;
+       j += static_cast<long long>(gridDim.x) * kThreads) {
     int slot = __ldg(c.indices + j);
     if (slot >= n && slot < c.num_slots) {
       const uint2 m = c.live[slot >> 5];
@@ -406,7 +409,23 @@ __device__ __forceinline__ void rewrite_lists(const CompactParams& c) {
 }
 
 // -------------------------------------------------------------------- rows --
-// A thread has one 16-byte piece of a row, of kDeep (row, layer) pairs at once.
+// (Row, layer) pair u: row u / layers of the lists, layer u % layers.
+struct Pair {
+  long long from, to;                              // rows of the whole caches, or from < 0
+};
+template <bool kLists>
+__device__ __forceinline__ Pair pair_of(const MoveParams& p, long long u, int count, bool report) {
+  const int k = static_cast<int>(u / p.layers), l = static_cast<int>(u - static_cast<long long>(k) * p.layers);
+  const int a = kLists ? __ldcg(p.from + (count - 1 - k)) : __ldg(p.from + k);
+  const int z = kLists ? __ldcg(p.to + k) : __ldg(p.to + k);
+  if (a < 0 || a >= p.src_slots || z < 0 || z >= p.dst_slots) {
+    if (report) record_status(p.status, MLA_ERR_INDEX_OOB);
+    return {-1, -1};
+  }
+  return {l * p.src_rows + a, l * p.dst_rows + z};
+}
+
+// Few rows: a thread has one 16-byte piece of a row, of kUnroll pairs at once.
 // kLists: behind the compaction's scan, with the lists to rewrite as well.
 template <int kRowBytes, bool kLists>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p, const CompactParams c) {
@@ -426,17 +445,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p, 
       const long long u = u0 + d * step;
       to[d] = -1;
       if (u >= units) continue;
-      const int k = static_cast<int>(u / p.layers), l = static_cast<int>(u - static_cast<long long>(k) * p.layers);
-      const int a = kLists ? __ldcg(p.from + (count - 1 - k)) : __ldg(p.from + k);
-      const int z = kLists ? __ldcg(p.to + k) : __ldg(p.to + k);
-      if (a < 0 || a >= p.src_slots || z < 0 || z >= p.dst_slots) {
-        if (piece == 0) record_status(p.status, MLA_ERR_INDEX_OOB);
-        continue;
-      }
-      const long long from = l * p.src_rows + a;
-      to[d] = l * p.dst_rows + z;
-      v[d] = *reinterpret_cast<const uint4*>(p.src + from * kRowBytes + 16 * piece);
-      if (p.src_scales && piece == 0) s[d] = p.src_scales[from];
+      const Pair m = pair_of<kLists>(p, u, count, piece == 0);
+      if (m.from < 0) continue;
+      to[d] = m.to;
+      v[d] = *reinterpret_cast<const uint4*>(p.src + m.from * kRowBytes + 16 * piece);
+      if (p.src_scales && piece == 0) s[d] = p.src_scales[m.from];
     }
 #pragma unroll
     for (int d = 0; d < kUnroll; ++d) {
@@ -447,16 +460,91 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p, 
   }
 }
 
-template <bool kLists>
+// Many rows: whole rows by bulk copies through shared memory.  A warp has two
+// stages of 32 rows: each lane loads its row of one while the rows of the other
+// are on their way out.
+constexpr int kBulkThreads = 96;
+template <int kRowBytes>
+__host__ __device__ constexpr int bulk_smem() { return kBulkThreads / 32 * (2 * 32 * kRowBytes + 16) + 32; }
+template <int kRowBytes, bool kLists>
+__global__ void __launch_bounds__(kBulkThreads) move_bulk_kernel(const MoveParams p, const CompactParams c) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kWarps = kBulkThreads / 32, kStage = 32 * kRowBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem), rows = base + warp * 2 * kStage;
+  const uint32_t bars = base + kWarps * 2 * kStage + 16 * warp;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kWarps * (2 * kStage + 16));
+  const WaitCtx wc{abort_flag, p.status};
+  if (lane == 0) {
+    mbar_init(bars, 1);
+    mbar_init(bars + 8, 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) *abort_flag = 0;
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  if constexpr (kLists) rewrite_lists<kBulkThreads>(c);
+  const int count = kLists ? __ldcg(p.count_dev) : p.count;
+  const long long units = static_cast<long long>(count) * p.layers;
+  const long long step = 32ll * gridDim.x * kWarps, first = 32ll * (static_cast<long long>(blockIdx.x) * kWarps + warp);
+  auto load = [&](long long u0, uint32_t stage) -> long long {
+    const Pair m = u0 + lane < units ? pair_of<kLists>(p, u0 + lane, count, true) : Pair{-1, -1};
+    const int n = __popc(__ballot_sync(0xffffffffu, m.from >= 0));
+    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, n * kRowBytes);
+    __syncwarp();
+    if (m.from >= 0) {
+      bulk_load(rows + stage * kStage + lane * kRowBytes, p.src + m.from * kRowBytes, kRowBytes, bars + 8 * stage);
+      if (p.src_scales) p.dst_scales[m.to] = p.src_scales[m.from];
+    }
+    return m.to;
+  };
+  long long to = first < units ? load(first, 0) : -1;
+  uint32_t i = 0;
+  for (long long u0 = first; u0 < units; u0 += step, ++i) {
+    const uint32_t stage = i & 1;
+    long long next = -1;
+    if (u0 + step < units) {
+      bulk_wait_read();                            // this lane's rows of the other stage have left it
+      __syncwarp();
+      next = load(u0 + step, stage ^ 1);
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, (i >> 1) & 1, wc))) {
+      // no copy outlives the block
+      drain_wait(bars + 8 * stage, (i >> 1) & 1);
+      if (u0 + step < units) drain_wait(bars + 8 * (stage ^ 1), ((i + 1) >> 1) & 1);
+      break;
+    }
+    if (to >= 0) bulk_store(p.dst + to * kRowBytes, rows + stage * kStage + lane * kRowBytes, kRowBytes);
+    bulk_commit();
+    to = next;
+  }
+  bulk_wait_all();
+}
+
+template <int kRowBytes, bool kLists>
 int launch_rows(const MoveParams& m, const CompactParams& c, long long most, long long entries, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms < 1) return MLA_ERR_CUDA;
-  const int rows = kMoveThreads * 16 / m.row_bytes;
-  const long long need = (most * m.layers + rows - 1) / rows, lists = (entries + kMoveThreads - 1) / kMoveThreads;
+  const long long units = most * m.layers;
+  if (units >= kBulkRows) {
+    const int smem = bulk_smem<kRowBytes>(), held = 227 * 1024 / (smem + 1024) * sms;
+    const auto kernel = &move_bulk_kernel<kRowBytes, kLists>;
+    if (!set_smem_limit(reinterpret_cast<const void*>(kernel), smem)) return MLA_ERR_CUDA;
+    const long long need = (units + kBulkThreads - 1) / kBulkThreads;
+    return launch_after(kernel, dim3(static_cast<unsigned>(need < held ? need : held)), kBulkThreads, 1, smem, stream, m, c);
+  }
+  const int rows = kMoveThreads * 16 / kRowBytes;
+  const long long need = (units + rows - 1) / rows, lists = (entries + kMoveThreads - 1) / kMoveThreads;
   const long long want = need > lists ? need : lists, held = 7ll * sms;
   const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want < held ? want : held);
-  return m.row_bytes == kRow ? launch_after(move_kernel<kRow, kLists>, dim3(grid), kMoveThreads, 1, stream, m, c)
-                             : launch_after(move_kernel<2 * kRow, kLists>, dim3(grid), kMoveThreads, 1, stream, m, c);
+  return launch_after(move_kernel<kRowBytes, kLists>, dim3(grid), kMoveThreads, 1, 0, stream, m, c);
+}
+
+template <bool kLists>
+int launch_rows(const MoveParams& m, const CompactParams& c, long long most, long long entries, cudaStream_t stream) {
+  return m.row_bytes == kRow ? launch_rows<kRow, kLists>(m, c, most, entries, stream)
+                             : launch_rows<2 * kRow, kLists>(m, c, most, entries, stream);
 }
 
 }  // namespace
@@ -466,13 +554,13 @@ int launch_repack(const RepackParams& params, cudaStream_t stream) {
   p.marked = p.freed && p.batch > 0 && p.entries > 0;
   if (p.marked) {
     const unsigned blocks = static_cast<unsigned>((p.entries + kChunk - 1) / kChunk);
-    const int st = launch_after(repack_mark_kernel, dim3(blocks), kListThreads, 1, stream, p);
+    const int st = launch_after(repack_mark_kernel, dim3(blocks), kListThreads, 1, 0, stream, p);
     if (st != MLA_OK) return st;
   }
   const unsigned blocks = static_cast<unsigned>(p.capacity > 0 ? (p.capacity + kChunk - 1) / kChunk : 1);
-  const int st = launch_after(repack_lists_kernel, dim3(blocks), kListThreads, 1, stream, p);
+  const int st = launch_after(repack_lists_kernel, dim3(blocks), kListThreads, 1, 0, stream, p);
   if (st != MLA_OK || !p.freed) return st;
-  return launch_after(freed_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, stream, p);
+  return launch_after(freed_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, 0, stream, p);
 }
 
 int launch_move(const MoveParams& m, long long most, cudaStream_t stream) {
@@ -484,9 +572,9 @@ int launch_compact(const CompactParams& c, const MoveParams& m, cudaStream_t str
   if (sms < 1) return MLA_ERR_CUDA;
   const long long blocks = (c.entries + 4 * kListThreads - 1) / (4 * kListThreads), held = 8ll * sms;
   const unsigned grid = static_cast<unsigned>(blocks < 1 ? 1 : blocks < held ? blocks : held);
-  int st = launch_after(compact_mark_kernel, dim3(grid), kListThreads, 1, stream, c);
+  int st = launch_after(compact_mark_kernel, dim3(grid), kListThreads, 1, 0, stream, c);
   if (st != MLA_OK) return st;
-  st = launch_after(compact_scan_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, stream, c);
+  st = launch_after(compact_scan_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, 0, stream, c);
   if (st != MLA_OK) return st;
   const long long half = c.num_slots / 2;
   return launch_rows<true>(m, c, half < c.entries ? half : c.entries, c.entries, stream);

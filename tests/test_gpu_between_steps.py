@@ -335,7 +335,8 @@ def _pool(seed, L, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8", "rows8"])
-@pytest.mark.parametrize("L,N,n", [(1, 2, 1), (3, 41, 20), (2, 5000, 2500), (7, 129, 3), (1, 30000, 9999)])
+@pytest.mark.parametrize("L,N,n", [(1, 2, 1), (3, 41, 20), (2, 5000, 2500), (7, 129, 3), (1, 30000, 9999), (3, 18002, 9001),
+                                   (8, 5000, 2049)])
 def test_copy_rows(L, N, n, dtype):
     torch, B = _t()
     cache, scales = _pool(N, L, N, dtype)
@@ -367,6 +368,24 @@ def test_copy_rows_between_pools_and_out_of_range():
     one, _ = _pool(3, 1, 10, "bf16")                  # a cache of one layer
     B.copy_rows(one[0], _dev([1]), one[0], _dev([9]))
     assert torch.equal(one[0, 1], one[0, 9])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "rows8"])
+def test_copy_many_rows_skips_those_out_of_range(dtype):
+    torch, B = _t()
+    cache, scales = _pool(7, 4, 12000, dtype)
+    ref, ref_s = cache.clone(), None if scales is None else scales.clone()
+    order = np.random.default_rng(7).permutation(12000)
+    src, dst = order[:5000].copy(), order[5000:10000].copy()
+    src[::7], dst[3::11] = 12000, -1
+    ok = (src < 12000) & (dst >= 0)
+    ref[:, _dev(dst[ok]).long()] = cache[:, _dev(src[ok]).long()]
+    if scales is not None:
+        ref_s[:, _dev(dst[ok]).long()] = scales[:, _dev(src[ok]).long()]
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    B.copy_rows(cache, _dev(src), cache, _dev(dst), src_scales=scales, dst_scales=scales, workspace=ws)
+    assert B.check_errors(ws) == 6
+    assert torch.equal(cache, ref) and (scales is None or torch.equal(scales, ref_s))
 
 
 def _compact(idx, N, L=2, dtype="bf16", extra=0, in_place=False, ws=None, seed=0):
@@ -410,6 +429,12 @@ def test_compact_of_patterns(where):
     idx = {"low": np.arange(1000), "high": np.arange(N - 999, N), "every second": np.arange(0, N, 2),
            "one far": np.concatenate((np.arange(63), [N - 1]))}[where]
     _compact(np.random.default_rng(1).permutation(idx), N, L=1, dtype="fp8")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "rows8"])
+@pytest.mark.parametrize("live", [5000, 20000, 39000])
+def test_compact_of_many_rows(live, dtype):
+    _compact(np.random.default_rng(live).permutation(40000)[:live], 40000, L=3, dtype=dtype)
 
 
 def test_compact_of_a_pool_wider_than_one_pass():
