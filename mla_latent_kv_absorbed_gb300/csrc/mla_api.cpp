@@ -654,19 +654,18 @@ int decode_fp8(const int32_t* plan_host, const int32_t* plan_dev, const void* q_
   CUtensorMap tm_lat, tm_rope;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(kRow), static_cast<cuuint64_t>(num_slots)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(kRow)};
-  const bool few = plan_host[kHVariant] == kVariantSwab;
-  const bool wide_rope = rows && !few;          // the whole rope key a box, not a half
-  cuuint32_t box_lat[2] = {128, 1}, box_rope[2] = {wide_rope ? 64u : 32u, 1}, estr[2] = {1, 1};
+  cuuint32_t box_lat[2] = {128, 1}, box_rope[2] = {rows ? 64u : 32u, 1}, estr[2] = {1, 1};
   if (fn(&tm_lat, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(kv_cache), dims, strides, box_lat, estr,
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
       fn(&tm_rope, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(kv_cache), dims, strides, box_rope, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, wide_rope ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, rows ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return MLA_ERR_CUDA;
-  const int rc = few    ? launch_swab8(H, tm_lat, tm_rope, p, p8, pp, plan_host[kHWorkers], st)
-                 : rows ? launch_rows8(tm_lat, tm_rope, p, p8, pp, plan_host[kHWorkers], st)
-                        : launch_pair8(H, tm_lat, tm_rope, p, kv_scale, plan_host[kHWorkers], st);
+  const int rc = rows ? launch_rows8(tm_lat, tm_rope, p, p8, pp, plan_host[kHWorkers], st)
+                 : plan_host[kHVariant] == kVariantSwab
+                     ? launch_swab8(H, tm_lat, tm_rope, p, p8, pp, plan_host[kHWorkers], st)
+                     : launch_pair8(H, tm_lat, tm_rope, p, kv_scale, plan_host[kHWorkers], st);
   if (rc != MLA_OK) return rc;
   return mla_decode_merge(plan_host, plan_dev, out, out_dtype, lse, workspace, workspace_bytes, stream);
 }

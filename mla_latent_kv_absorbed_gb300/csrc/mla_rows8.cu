@@ -75,6 +75,7 @@ constexpr int kQr = 128 * 64;                        // rope query: [hi; lo] x 6
 constexpr int kPPair = 64 * 128;                     // two parts of the weights: 64 heads x (64 + 64) rows
 constexpr int kImage = 2 * kRow;                     // bytes of a head's query: hi and lo codes
 constexpr int kXBytes = kSoftWarps * 32 * 32;        // scores on their way to the thread of the other part, of a tile
+constexpr int kPSlots = 3;                           // tiles whose weights are held
 constexpr int kScSlots = 3;                          // tiles whose rows' numbers are held
 constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the scales, reciprocals
 constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
@@ -91,12 +92,12 @@ struct Cfg {
   static constexpr int kPBuf = kPairs * kPPair;
   static constexpr int kOffQr = kUnits * kUnit;
   static constexpr int kOffP = kOffQr + kQr;
-  static constexpr int kOffX = kOffP + 2 * kPBuf;
+  static constexpr int kOffX = kOffP + kPSlots * kPBuf;
   static constexpr int kOffSc = kOffX + kXBytes;
-  static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [2][8][64] maxima
-  static constexpr int kOffBc = kOffRed + 2 * 8 * 64 * 4;       // [64] rescaling factors
-  static constexpr int kOffSum = kOffBc + 64 * 4;               // [2][8][64] an item's sums, for the output
-  static constexpr int kOffRef = kOffSum + 2 * 8 * 64 * 4;      // [2][64] and references
+  static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [8][64] maxima, or sums
+  static constexpr int kOffBc = kOffRed + 8 * 64 * 4;           // [kUnits][64] a tile's rescaling factors
+  static constexpr int kOffSum = kOffBc + kUnits * 64 * 4;      // [2][64] an item's sums, for the output
+  static constexpr int kOffRef = kOffSum + 2 * 64 * 4;          // [2][64] and references
   static constexpr int kOffSlots = kOffRef + 2 * 64 * 4;        // [5][64] a tile's slots, for each gathering warp
   static constexpr int kOffBar = kOffSlots + 5 * T * 4;
   static constexpr int bFull = 0;                    // [kUnits] a tile's rows have landed
@@ -105,18 +106,19 @@ struct Cfg {
   static constexpr int bQEmpty = bQFull + 1;
   static constexpr int bSFull = bQEmpty + 1;         // [2]
   static constexpr int bSEmpty = bSFull + 2;         // [2]
-  static constexpr int bPFull = bSEmpty + 2;         // [2]
-  static constexpr int bOFull = bPFull + 2;
-  static constexpr int bOEmpty = bOFull + 1;
-  static constexpr int bSumFull = bOEmpty + 1;       // [2]
+  static constexpr int bPFull = bSEmpty + 2;         // [kPSlots]
+  static constexpr int bVoted = bPFull + kPSlots;    // [kUnits] a tile's references are settled
+  static constexpr int bFixed = bVoted + kUnits;     // [kUnits] and what has been added up is in their units
+  static constexpr int bOFull = bFixed + kUnits;
+  static constexpr int bSumFull = bOFull + 1;        // [2]
   static constexpr int bSumEmpty = bSumFull + 2;     // [2]
   static constexpr int bScFull = bSumEmpty + 2;      // [kScSlots]
   static constexpr int bScEmpty = bScFull + kScSlots;
   static constexpr int bDrain = bScEmpty + kScSlots;
   static constexpr int kNumBars = bDrain + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffMoved = kOffMisc + 8;     // [2] heads whose reference moved
-  static constexpr int kOffLast = kOffMisc + 16;     // [kUnits] last armed use
+  static constexpr int kOffMoved = kOffMisc + 8;     // [kUnits][2] heads whose reference a tile moved
+  static constexpr int kOffLast = kOffMoved + kUnits * 8;       // [kUnits] last armed use
   static constexpr int kOffItems = (kOffLast + 4 * kUnits + 15) / 16 * 16;
   static constexpr int kSmemBytes = kOffItems + 16 * kItemCache + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -139,7 +141,7 @@ __device__ __forceinline__ bool item_in_request(const DecodeParams& p, int b, in
 // Bound: launch and a round trip, or for large batches HBM.
 constexpr int kPrepThreads = 256;
 __global__ void __launch_bounds__(kPrepThreads) rows8_prep_kernel(const Fp8PrepParams p, int heads) {
-  const int lane = threadIdx.x & 31, warps = gridDim.x * (kPrepThreads / 32), Hc = heads >> 1;
+  const int lane = threadIdx.x & 31, warps = gridDim.x * (kPrepThreads / 32), Hc = heads > 32 ? heads >> 1 : heads;
   griddep_wait();
   griddep_launch_dependents();
   for (int i = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5); i < p.rows; i += warps) {
@@ -199,14 +201,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = blockIdx.x & 1;                    // which half of the heads
+  const int shift = p.heads > 32 ? 1 : 0;            // a worker's CTAs: two, or one that takes all heads
+  const int cta = blockIdx.x & shift;                // which of them
   auto bar = [&](int i) -> uint32_t { return base + C::kOffBar + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   int* last_armed = reinterpret_cast<int*>(smem + C::kOffLast);
   const WaitCtx wc{abort_flag, p.status};
-  const int w = blockIdx.x >> 1;
-  const int Hc = p.heads >> 1;                       // this CTA's heads: [cta * Hc, (cta + 1) * Hc)
+  const int w = blockIdx.x >> shift;
+  const int Hc = p.heads >> shift;                   // this CTA's heads: [cta * Hc, (cta + 1) * Hc)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bFull + i), 1); mbar_init(bar(C::bEmpty + i), 1); }
@@ -214,11 +217,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(C::bQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::bSFull + i), 1); mbar_init(bar(C::bSEmpty + i), kSoftWarps);
-      mbar_init(bar(C::bPFull + i), kSoftWarps);
       mbar_init(bar(C::bSumFull + i), kSoftWarps); mbar_init(bar(C::bSumEmpty + i), kQueryWarps);
     }
+    for (int i = 0; i < kPSlots; ++i) mbar_init(bar(C::bPFull + i), kSoftWarps);
+    for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bVoted + i), 2); mbar_init(bar(C::bFixed + i), kQueryWarps); }
     mbar_init(bar(C::bOFull), 1);
-    mbar_init(bar(C::bOEmpty), kQueryWarps);
     for (int i = 0; i < kScSlots; ++i) { mbar_init(bar(C::bScFull + i), 1); mbar_init(bar(C::bScEmpty + i), kSoftWarps); }
     mbar_init(bar(C::bDrain), 2);                   // both issuers' last commits
     for (int i = 0; i < C::kUnits; ++i) last_armed[i] = -1;
@@ -416,11 +419,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j == nt - 1) umma_commit(bar(C::bQEmpty));
           }
         } else {
-          ok = mbar_wait(bar(C::bPFull + buf), (g >> 1) & 1, wc) &&
-               (j > 0 || nitem == 0 || mbar_wait(bar(C::bOEmpty), (nitem - 1) & 1, wc));
+          const uint32_t ps = g % kPSlots;
+          ok = mbar_wait(bar(C::bFixed + slot), lap, wc) && mbar_wait(bar(C::bPFull + ps), (g / kPSlots) & 1, wc);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t av = D(dv, slot * kUnit), bp = D(dp, buf * C::kPBuf);
+          const uint64_t av = D(dv, slot * kUnit), bp = D(dp, ps * C::kPBuf);
           if (lead) {
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb)
@@ -508,8 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!part_ok && warp == kQueryWarp0 && lane == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
       wait(bar(C::bSumFull + (nitem & 1)), (nitem >> 1) & 1);
       const int h0 = 32 * half;
-      const float* sum = reinterpret_cast<const float*>(smem + C::kOffSum) + 512 * (nitem & 1) + h0 + lane;
-      const float l = ((sum[0] + sum[64]) + (sum[128] + sum[192])) + ((sum[256] + sum[320]) + (sum[384] + sum[448]));
+      const float l = reinterpret_cast<const float*>(smem + C::kOffSum)[64 * (nitem & 1) + h0 + lane];
       const float ref = reinterpret_cast<const float*>(smem + C::kOffRef)[64 * (nitem & 1) + h0 + lane];
       const float inv = l > 0.f ? 1.f / l : 0.f;     // of head h0 + lane
       __syncwarp();
@@ -552,39 +554,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           put((dest >= 0 ? p.part_o : static_cast<float*>(p.out)) + first, [](float v) { return v; });
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0 && !aborted) mbar_arrive(bar(C::bOEmpty));
+      tc_fence_before();                             // (the next item's first bFixed says that O has been read)
     };
-    uint32_t nitem = 0;
-    int b_last = 0, dest_last = 0;
-    for (int it = it0; it < it1; ++it) {
-      const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
-      if (!item_ok(p, nnz, b, s, e)) continue;
-      query(b, nitem);
-      if (nitem > 0) output(b_last, dest_last, nitem - 1);
-      b_last = b;
-      dest_last = item_w(it, 3);
-      ++nitem;
+    // O in the units of tile g's references, where those moved
+    auto fix = [&](uint32_t g) {
+      const uint32_t at = g % C::kUnits;
+      wait(bar(C::bVoted + at), (g / C::kUnits) & 1);
+      const uint32_t moved = reinterpret_cast<const volatile uint32_t*>(smem + C::kOffMoved)[2 * at + half];
+      if (moved && !aborted) {
+        wait(bar(C::bEmpty + (g - 1) % C::kUnits), ((g - 1) / C::kUnits) & 1);   // the sums of the tiles before are done
+        tc_fence_after();
+        const float4* bc = reinterpret_cast<const float4*>(smem + C::kOffBc) + 16 * at + 8 * half;
+        const uint32_t to = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmO + 32 * half;
+        if (!aborted)
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {              // 8 heads
+            if (((moved >> (8 * c)) & 0xffu) == 0) continue;
+            uint32_t o[4][8];
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb) tmem_ld8(to + 64 * mb + 8 * c, o[mb]);
+            const float4 f0 = bc[2 * c], f1 = bc[2 * c + 1];
+            const float2 f[4] = {f2_pack(f0.x, f0.y), f2_pack(f0.z, f0.w), f2_pack(f1.x, f1.y), f2_pack(f1.z, f1.w)};
+            tmem_wait_ld();
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 v = f2_mul(f2_pack(__uint_as_float(o[mb][2 * i]), __uint_as_float(o[mb][2 * i + 1])), f[i]);
+                o[mb][2 * i] = __float_as_uint(v.x);
+                o[mb][2 * i + 1] = __float_as_uint(v.y);
+              }
+              tmem_st8(to + 64 * mb + 8 * c, o[mb]);
+            }
+          }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0 && !aborted) mbar_arrive(bar(C::bFixed + at));
+    };
+    uint32_t nitem = 0, g = 0;
+    int it = it0;
+    auto usable = [&](int i) { return item_ok(p, nnz, item_w(i, 0), item_w(i, 1), item_w(i, 2)); };
+    while (it < it1 && !usable(it)) ++it;
+    if (it < it1) query(item_w(it, 0), 0);
+    while (it < it1) {
+      const int b = item_w(it, 0), dest = item_w(it, 3);
+      for (int left = (item_w(it, 2) - item_w(it, 1) + T - 1) / T; left > 1; --left) fix(g++);
+      do ++it;
+      while (it < it1 && !usable(it));
+      if (it < it1) query(item_w(it, 0), nitem + 1);
+      fix(g++);
+      output(b, dest, nitem++);
     }
-    if (nitem > 0) output(b_last, dest_last, nitem - 1);
   } else {
     // ----------------------------------------------------------------- softmax
     const int q = warp & 3, th = warp >> 2, part = q >> 1;
     const int hl = 32 * (q & 1) + lane;              // head of this CTA
     const uint32_t quad = static_cast<uint32_t>(32 * q) << 16;
     float* red = reinterpret_cast<float*>(smem + C::kOffRed);
-    float* bc = reinterpret_cast<float*>(smem + C::kOffBc);
     volatile uint32_t* moved_of = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMoved);   // heads to rescale
     const int eight = 2 * th + part;                 // which 8 rows of a tile
     float m_ref = 0.f, l_sum = 0.f, fac = 1.f;
-    int rk = 0;
     auto wait = [&](uint32_t bb, uint32_t par) {     // (every lane for itself: a third of the time of one for all)
       if (!aborted && !__all_sync(0xffffffffu, mbar_wait(bb, par, wc))) aborted = true;
     };
-    // the largest of this head's values, of the eight threads that share it
+    // the largest of this head's values, of the eight threads that share it (who have voted since they read the last)
     auto largest = [&](float v) -> float {
-      float* r = red + (rk++ & 1) * 512;
+      float* r = red;
       r[eight * 64 + hl] = v;
       named_bar_sync(kBarAll, 32 * kSoftWarps);
       v = max3(r[hl], r[64 + hl], max3(r[128 + hl], r[192 + hl], r[256 + hl]));
@@ -663,19 +700,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_scores(g);
       float mx = exponents(g, n);
       for (int j = 0; j < nt; ++j, ++g) {
-        const uint32_t buf = g & 1;
         const bool moved = named_bar_or(kBarVote, 32 * kSoftWarps, mx > m_ref + kLag);
+        uint32_t which = 0;                          // heads whose O has to follow
         if (moved) {                                 // some head's reference moves
           const float mt = largest(mx);
           const float mn = mt > m_ref + kLag ? mt : m_ref;
           const float alpha = mn == m_ref ? 1.f : ex2_approx(m_ref - mn);
           m_ref = mn;
           l_sum *= alpha;
-          if (eight == 0) {                          // (warps 0 and 1)
-            bc[hl] = alpha;
-            const uint32_t which = __ballot_sync(0xffffffffu, alpha != 1.f);
-            if (lane == 0) moved_of[warp] = which;
+          if (eight == 0) {
+            reinterpret_cast<float*>(smem + C::kOffBc)[64 * (g % C::kUnits) + hl] = alpha;
+            which = __ballot_sync(0xffffffffu, alpha != 1.f && hl < Hc);
           }
+        }
+        if (eight == 0) {                            // (warps 0 and 1)
+          if (lane == 0) moved_of[2 * (g % C::kUnits) + warp] = j > 0 ? which : 0;
+          __syncwarp();
+          if (lane == 0 && !aborted) mbar_arrive(bar(C::bVoted + g % C::kUnits));
         }
         if (j + 1 < nt) load_scores(g + 1);
         // weights and their parts; 8 rows are half a 16-byte chunk of each
@@ -713,10 +754,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         l_sum += l2.x + l2.y;
-        if (g >= 2) wait(bar(C::bEmpty + (g - 2) % C::kUnits), ((g - 2) / C::kUnits) & 1);   // these weights' last use
+        // The weights of tile g - 3 lay here.  Scores of tile g + 1 that are there say that its rows are, and these that
+        // the sum of g - 3, whose place they took, is done.
+        static_assert(C::kUnits == kPSlots + 1, "see above");
+        if (j + 1 == nt && g >= kPSlots)
+          wait(bar(C::bEmpty + (g - kPSlots) % C::kUnits), ((g - kPSlots) / C::kUnits) & 1);
         if (!aborted) {
           // byte 8 eight of the head's 64 (hi), then the same of the lo part: chunks c at c ^ (head mod 8)
-          uint8_t* row = smem + C::kOffP + buf * C::kPBuf + hl * 128 + 8 * part;
+          uint8_t* row = smem + C::kOffP + (g % kPSlots) * C::kPBuf + hl * 128 + 8 * part;
           const int at = (th ^ (hl & 7)) << 4, at_lo = ((4 + th) ^ (hl & 7)) << 4;
           *reinterpret_cast<uint2*>(row + at) = make_uint2(w0[0], w0[1]);
           *reinterpret_cast<uint2*>(row + at_lo) = make_uint2(w1[0], w1[1]);
@@ -729,42 +774,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && !aborted) {
-          if (!moved) mbar_arrive(bar(C::bPFull + buf));
+          mbar_arrive(bar(C::bPFull + g % kPSlots));
           mbar_arrive(bar(C::bScEmpty + g % kScSlots));
         }
         if (j + 1 < nt) mx = exponents(g + 1, n - (j + 1) * T);
-        if (moved) {
-          // O in the new units, by now that the sum of the tile before is done or nearly so.  A head is a column of
-          // each block; this warp has its 32 dims of block th.
-          named_bar_sync(kBarAll, 32 * kSoftWarps);  // the factors are there
-          if (j > 0) {
-            wait(bar(C::bEmpty + (g - 1) % C::kUnits), ((g - 1) / C::kUnits) & 1);
-            tc_fence_after();
-            const uint32_t to = tmem + quad + kTmO + 64 * th;
-            if (!aborted) {
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                for (uint32_t m = moved_of[w]; m; m &= m - 1) {
-                  const int h = 32 * w + __ffs(m) - 1;
-                  const float f = bc[h];
-                  uint32_t a;
-                  tmem_ld1(to + h, a);
-                  tmem_wait_ld();
-                  tmem_st1(to + h, __float_as_uint(__uint_as_float(a) * f));
-                }
-              }
-            }
-            tmem_wait_st();
-            tc_fence_before();
-          }
-          __syncwarp();
-          if (lane == 0 && !aborted) mbar_arrive(bar(C::bPFull + buf));
-        }
       }
       // what the output needs
       if (nitem >= 2) wait(bar(C::bSumEmpty + (nitem & 1)), ((nitem >> 1) - 1) & 1);
-      reinterpret_cast<float*>(smem + C::kOffSum)[512 * (nitem & 1) + 64 * eight + hl] = l_sum;
-      if (eight == 0) reinterpret_cast<float*>(smem + C::kOffRef)[64 * (nitem & 1) + hl] = m_ref;
+      float* r = red;
+      named_bar_sync(kBarAll, 32 * kSoftWarps);
+      r[eight * 64 + hl] = l_sum;
+      named_bar_sync(kBarAll, 32 * kSoftWarps);
+      if (eight == 0) {
+        float l = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l += r[i * 64 + hl];
+        reinterpret_cast<float*>(smem + C::kOffSum)[64 * (nitem & 1) + hl] = l;
+        reinterpret_cast<float*>(smem + C::kOffRef)[64 * (nitem & 1) + hl] = m_ref;
+      }
       __syncwarp();
       if (lane == 0 && !aborted) mbar_arrive(bar(C::bSumFull + (nitem & 1)));
       ++nitem;
@@ -797,16 +824,17 @@ int launch_after(Kernel* kernel, int grid, int threads, int smem, cudaStream_t s
 
 int launch_rows8(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p, const Fp8Params& p8,
                  const Fp8PrepParams& pp, int workers, cudaStream_t stream) {
-  if (p.heads < 48 || p.heads > 128 || p.heads % 16 != 0) return MLA_ERR_UNSUPPORTED;
+  if (p.heads < 16 || p.heads > 128 || p.heads % 16 != 0) return MLA_ERR_UNSUPPORTED;
+  const int ctas = p.heads > 32 ? 2 * workers : workers;
   const auto kernel = p.out_bf16 ? &rows8::rows8_kernel<false> : &rows8::rows8_kernel<true>;
   const int smem = p.out_bf16 ? rows8::Cfg<false>::kSmemBytes : rows8::Cfg<true>::kSmemBytes;
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), smem)) return MLA_ERR_CUDA;
   // few enough blocks that the next kernel's fit beside them (it starts once all have)
-  const int warps = rows8::kPrepThreads / 32, blocks = (pp.rows + warps - 1) / warps, held = 4 * 2 * workers;
+  const int warps = rows8::kPrepThreads / 32, blocks = (pp.rows + warps - 1) / warps, held = 4 * ctas;
   const int st = rows8::launch_after(&rows8::rows8_prep_kernel, blocks < held ? blocks : held, rows8::kPrepThreads, 0,
                                      stream, pp, p.heads);
   if (st != MLA_OK) return st;
-  return rows8::launch_after(kernel, 2 * workers, rows8::kThreads, smem, stream, tm_lat, tm_rope, p, p8);
+  return rows8::launch_after(kernel, ctas, rows8::kThreads, smem, stream, tm_lat, tm_rope, p, p8);
 }
 
 }  // namespace mla

@@ -37,20 +37,6 @@
 // atom c+2 follows atom c so one 128-row descriptor covers both halves; R1 is
 // the rope from dim 544 (the h1 rope at K offset 0).
 //
-// kRows: every row has a scale of its own, r_t.  The exponents carry it,
-//   e_t = sm_scale log2(e) r_t (q . code_t) + log2 r_t,
-// so that 2^(e_t - m_ref) is the weight of the row's codes and its product with
-// 1 / r_t (before the weight is rounded) the row's share of the sum.  A softmax thread has one token of a tile
-// for all its heads, so that the scale is a register of its own, loaded a tile
-// ahead and its slot number two tiles ahead.
-//
-// kFine (fp32 output of the row-scaled form): two parts more, so that the
-// weights keep 16 bits.  The third is added to the hi accumulator, the fourth,
-// times 32, to the lo one; a weight's four are the same row's bytes 0-63 and
-// 64-127 of the hi and the lo row.  Weights then are 2^(e - m_ref + 5), at most
-// 256 and the largest at least 32, which puts the parts' smallest step at 2^-14
-// of 32.
-//
 // Warp roles (one CTA per SM, persistent over the plan's work items):
 //   warps 0-3   softmax / epilogue (TMEM lane quadrants 0-3)
 //   warp 4      QK issuer and query-image loader
@@ -64,8 +50,6 @@
 // the first tiles overlap it, and only the QK and softmax warps wait for it.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
-
-#include <type_traits>
 
 #include "mla_device.cuh"
 #include "mla_launch.h"
@@ -293,14 +277,12 @@ __global__ void __launch_bounds__(256) q8_prep_kernel(const Fp8PrepParams p) {
 }
 
 // ------------------------------------------------------------ decode kernel --
-template <int NH, bool kRows, bool kFine>
+template <int NH>
 __global__ void __launch_bounds__(kThreads, 1)
     swab8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const DecodeParams p, const Fp8Params p8) {
   using C = Cfg<NH>;
   constexpr int kHalf = C::kHalf;
-  // a weight is 2^(e - m_ref + kUp), and the reference moves once a score passes it by kLag
-  constexpr float kUp = kFine ? 5.f : 0.f, kLag = kFine ? 3.f : 8.f;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -468,13 +450,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb) {
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-              const uint64_t a = sdesc(ub + atom_pos(mb) * kAtom + 4096 * ks, kAtom, 1024);
-              umma_ss_f8(tmem + C::kTmO + mb * 2 * NH, a, sdesc(pb + 32 * ks, 16, 1024), C::kIdescPV,
-                         (j == 0 && ks == 0) ? 0u : 1u);
-              if constexpr (kFine)
-                umma_ss_f8(tmem + C::kTmO + mb * 2 * NH, a, sdesc(pb + 64 + 32 * ks, 16, 1024), C::kIdescPV, 1u);
-            }
+            for (int ks = 0; ks < 2; ++ks)
+              umma_ss_f8(tmem + C::kTmO + mb * 2 * NH, sdesc(ub + atom_pos(mb) * kAtom + 4096 * ks, kAtom, 1024),
+                         sdesc(pb + 32 * ks, 16, 1024), C::kIdescPV, (j == 0 && ks == 0) ? 0u : 1u);
             if (j == nt - 1 && (mb & 1)) umma_commit(bar(C::bOBlk + (mb >> 1)));
           }
           umma_commit(bar(C::bEmpty + us));
@@ -510,33 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       r = __shfl_sync(0xffffffffu, r, 0);
       if (!r) aborted = true;
     };
-    // kRows: this thread's token of the tiles to come, over all items
-    [[maybe_unused]] int n_it = it0, n_s = 0, n_n = 0, n_t0 = 0;      // the tile whose slot number is loaded next
-    [[maybe_unused]] auto next_slot = [&]() -> int {
-      while (n_t0 >= n_n) {                        // the next usable item
-        if (n_it >= it1) return 0;
-        const int b = items[4 * n_it], s = items[4 * n_it + 1], e = items[4 * n_it + 2];
-        ++n_it;
-        if (!item_ok(p, nnz, b, s, e)) continue;
-        n_s = s;
-        n_n = e - s;
-        n_t0 = 0;
-      }
-      const int slot = __ldg(p.kv_indices + n_s + min(n_t0 + t, n_n - 1));
-      n_t0 += T;
-      return slot;
-    };
-    [[maybe_unused]] auto scale_at = [&](int slot) -> float {
-      return __ldg(p8.kv_scales + (slot >= 0 && static_cast<long long>(slot) < p.num_slots ? slot : 0));
-    };
-    [[maybe_unused]] int slot_next = 0;
-    [[maybe_unused]] float sc_next = 1.f;
-    if constexpr (kRows) {
-      sc_next = scale_at(next_slot());
-      slot_next = next_slot();
-    }
     griddep_wait();   // the per-head factors come from the prep kernel
-    const float kv_scale = kRows ? 1.f : p8.kv_scale;
+    const float kv_scale = p8.kv_scale;
 
     for (int it = it0; it < it1; ++it) {
       const int b = items[4 * it], s = items[4 * it + 1], e = items[4 * it + 2];
@@ -549,14 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = e - s, nt = (n + T - 1) / T;
       for (int j = 0; j < nt; ++j, ++g) {
         const uint32_t buf = g & 1;
-        [[maybe_unused]] float sc = 1.f, sc_log = 0.f, sc_inv = 1.f;
-        if constexpr (kRows) {
-          sc = row_scale(sc_next);
-          sc_log = __log2f(sc);
-          sc_inv = __frcp_rn(sc);
-          sc_next = scale_at(slot_next);
-          slot_next = next_slot();
-        }
         wait(bar(C::bSFull + buf), (g >> 1) & 1);
         tc_fence_after();
         float ps[NH];
@@ -589,9 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sv[kHalf];
 #pragma unroll
         for (int k = 0; k < kHalf; ++k)
-          sv[k] = !valid  ? -INFINITY
-                  : kRows ? fmaf((own[k] + X[((1 - pair) * kHalf + k) * T + t]) * fac[k], sc, sc_log)
-                          : (own[k] + X[((1 - pair) * kHalf + k) * T + t]) * fac[k];
+          sv[k] = valid ? (own[k] + X[((1 - pair) * kHalf + k) * T + t]) * fac[k] : -INFINITY;
         if (j == 0) {
 #pragma unroll
           for (int k = 0; k < kHalf; ++k) { m_ref[k] = sv[k]; l_part[k] = 0.f; }
@@ -600,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           bool need = false;
 #pragma unroll
-          for (int k = 0; k < kHalf; ++k) need |= sv[k] > m_ref[k] + kLag;
+          for (int k = 0; k < kHalf; ++k) need |= sv[k] > m_ref[k] + 8.f;
           need = named_bar_or(kBarVote, 128, need);
           if (need) {
             float mt[kHalf], alpha[kHalf];
@@ -641,31 +584,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // weights: hi + lo / 32 in E4M3, summed as the MMA will see them
         uint32_t phi[kHalf / 2], plo[kHalf / 2];
-        [[maybe_unused]] uint32_t ph3[kFine ? kHalf / 2 : 1], pl4[kFine ? kHalf / 2 : 1];
 #pragma unroll
         for (int k = 0; k < kHalf; k += 2) {
-          const float p0 = ex2_approx(sv[k] - m_ref[k] + kUp), p1 = ex2_approx(sv[k + 1] - m_ref[k + 1] + kUp);
+          const float p0 = ex2_approx(sv[k] - m_ref[k]), p1 = ex2_approx(sv[k + 1] - m_ref[k + 1]);
           const uint32_t h2 = e4m3x2(p0, p1);
           const float2 hv = e4m3x2_value(h2);
           const uint32_t l2 = e4m3x2((p0 - hv.x) * 32.f, (p1 - hv.y) * 32.f);
           const float2 lv = e4m3x2_value(l2);
-          if constexpr (kRows) {
-            // (a soft row's share of the sum can be large where its weight is a few of the smallest steps)
-            l_part[k] = fmaf(p0, sc_inv, l_part[k]);
-            l_part[k + 1] = fmaf(p1, sc_inv, l_part[k + 1]);
-          } else {
-            l_part[k] += fmaf(lv.x, kLoWeight, hv.x);
-            l_part[k + 1] += fmaf(lv.y, kLoWeight, hv.y);
-          }
+          l_part[k] += fmaf(lv.x, kLoWeight, hv.x);
+          l_part[k + 1] += fmaf(lv.y, kLoWeight, hv.y);
           phi[k >> 1] = h2;
           plo[k >> 1] = l2;
-          if constexpr (kFine) {                       // (the differences are exact)
-            const float2 f2 = e4m3x2_value(l2);
-            const float r0 = p0 - hv.x - f2.x * kLoWeight, r1 = p1 - hv.y - f2.y * kLoWeight;
-            ph3[k >> 1] = e4m3x2(r0, r1);
-            const float2 t2 = e4m3x2_value(ph3[k >> 1]);
-            pl4[k >> 1] = e4m3x2((r0 - t2.x) * 32.f, (r1 - t2.y) * 32.f);
-          }
         }
         if (g >= 2) wait(bar(C::bPDone + buf), ((g >> 1) - 1) & 1);
         if (!aborted) {
@@ -678,12 +607,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             pb[sw128_off(h + 1, t)] = static_cast<uint8_t>(phi[k >> 1] >> 8);
             pb[sw128_off(NH + h, t)] = static_cast<uint8_t>(plo[k >> 1]);
             pb[sw128_off(NH + h + 1, t)] = static_cast<uint8_t>(plo[k >> 1] >> 8);
-            if constexpr (kFine) {
-              pb[sw128_off(h, T + t)] = static_cast<uint8_t>(ph3[k >> 1]);
-              pb[sw128_off(h + 1, T + t)] = static_cast<uint8_t>(ph3[k >> 1] >> 8);
-              pb[sw128_off(NH + h, T + t)] = static_cast<uint8_t>(pl4[k >> 1]);
-              pb[sw128_off(NH + h + 1, T + t)] = static_cast<uint8_t>(pl4[k >> 1] >> 8);
-            }
           }
         }
         fence_proxy_async_smem();
@@ -710,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float my_lse = 0.f;
 #pragma unroll
         for (int k = 0; k < kHalf; ++k)
-          if (lane == k) my_lse = (m_ref[k] + __log2f(l_tot[k]) - kUp) * 0.69314718055994531f;
+          if (lane == k) my_lse = (m_ref[k] + __log2f(l_tot[k])) * 0.69314718055994531f;
         if (!aborted && part_ok && wip == 0 && lane < kHalf) {
           const int h = pair * kHalf + lane;
           if (to_out) { if (p.lse) p.lse[static_cast<size_t>(b) * p.heads + h] = my_lse; }
@@ -820,12 +743,11 @@ __global__ void __launch_bounds__(kAppendPieces * kAppendRows) append_fp8_kernel
   *reinterpret_cast<uint4*>(p.kv_cache + slot * kRow + 16 * piece) = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-template <int NH, bool kRows, bool kFine>
+template <int NH>
 int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p, const Fp8Params& p8,
            const Fp8PrepParams& pp, int grid, cudaStream_t stream) {
   using C = Cfg<NH>;
-  const auto kernel = &swab8_kernel<NH, kRows, kFine>;
-  if (!set_smem_limit(reinterpret_cast<const void*>(kernel), C::kSmemBytes)) return MLA_ERR_CUDA;
+  if (!set_smem_limit(reinterpret_cast<const void*>(&swab8_kernel<NH>), C::kSmemBytes)) return MLA_ERR_CUDA;
   const int warps = pp.rows;
   // a plain launch (full stream order): the decode kernel below, its
   // programmatic dependent, starts gathering cache rows before it waits, which
@@ -842,7 +764,7 @@ int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodePa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, tm_lat, tm_rope, p, p8) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, swab8_kernel<NH>, tm_lat, tm_rope, p, p8) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_CUDA;
   }
@@ -853,14 +775,8 @@ int launch(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodePa
 
 int launch_swab8(int heads, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const DecodeParams& p,
                  const Fp8Params& p8, const Fp8PrepParams& pp, int grid, cudaStream_t stream) {
-  auto go = [&](auto nh) {
-    constexpr int NH = decltype(nh)::value;
-    if (!p8.kv_scales) return swab8::launch<NH, false, false>(tm_lat, tm_rope, p, p8, pp, grid, stream);
-    return p.out_bf16 ? swab8::launch<NH, true, false>(tm_lat, tm_rope, p, p8, pp, grid, stream)
-                      : swab8::launch<NH, true, true>(tm_lat, tm_rope, p, p8, pp, grid, stream);
-  };
-  if (heads == 16) return go(std::integral_constant<int, 16>{});
-  if (heads == 32) return go(std::integral_constant<int, 32>{});
+  if (heads == 16) return swab8::launch<16>(tm_lat, tm_rope, p, p8, pp, grid, stream);
+  if (heads == 32) return swab8::launch<32>(tm_lat, tm_rope, p, p8, pp, grid, stream);
   return MLA_ERR_UNSUPPORTED;
 }
 
