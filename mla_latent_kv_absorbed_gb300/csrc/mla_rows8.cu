@@ -76,12 +76,12 @@ constexpr int kPPair = 64 * 128;                     // two parts of the weights
 constexpr int kImage = 2 * kRow;                     // bytes of a head's query: hi and lo codes
 constexpr int kXBytes = kSoftWarps * 32 * 32;        // scores on their way to the thread of the other part, of a tile
 constexpr int kPSlots = 3;                           // tiles whose weights are held
-constexpr int kScSlots = 3;                          // tiles whose rows' numbers are held
+constexpr int kScSlots = 4;                          // tiles whose rows' numbers are held
 constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the scales, reciprocals
 constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
 constexpr float kLoWeight = 1.f / 32.f;              // value of a query's lo part
-constexpr float kTop = 5.f, kLag = 3.f;              // weights are 2^(e - m + kTop) with e <= m + kLag
-constexpr int kBarPair0 = 1, kBarAll = 9, kBarVote = 10, kBarGather = 11;   // named barriers
+constexpr float kTop = 5.f, kLag = 3.75f;            // weights are 2^(e - m + kTop) with e <= m + kLag: to 431 of 448
+constexpr int kBarPair0 = 1, kBarHalf = 9, kBarVote = 11, kBarGather = 13;  // named barriers
 constexpr int kTmO = 0, kTmQ = 256, kTmS = 384;
 constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);
 
@@ -104,7 +104,7 @@ struct Cfg {
   static constexpr int bEmpty = bFull + kUnits;      // [kUnits]
   static constexpr int bQFull = bEmpty + kUnits;
   static constexpr int bQEmpty = bQFull + 1;
-  static constexpr int bSFull = bQEmpty + 1;         // [2]
+  static constexpr int bSFull = bQEmpty + 1;         // [2] a tile's scores, and its rows' numbers
   static constexpr int bSEmpty = bSFull + 2;         // [2]
   static constexpr int bPFull = bSEmpty + 2;         // [kPSlots]
   static constexpr int bVoted = bPFull + kPSlots;    // [kUnits] a tile's references are settled
@@ -112,9 +112,7 @@ struct Cfg {
   static constexpr int bOFull = bFixed + kUnits;
   static constexpr int bSumFull = bOFull + 1;        // [2]
   static constexpr int bSumEmpty = bSumFull + 2;     // [2]
-  static constexpr int bScFull = bSumEmpty + 2;      // [kScSlots]
-  static constexpr int bScEmpty = bScFull + kScSlots;
-  static constexpr int bDrain = bScEmpty + kScSlots;
+  static constexpr int bDrain = bSumEmpty + 2;
   static constexpr int kNumBars = bDrain + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffMoved = kOffMisc + 8;     // [kUnits][2] heads whose reference a tile moved
@@ -213,16 +211,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bFull + i), 1); mbar_init(bar(C::bEmpty + i), 1); }
+    const int soft = Hc > 32 ? kSoftWarps : kSoftWarps / 2;
     mbar_init(bar(C::bQFull), kQueryWarps);
     mbar_init(bar(C::bQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::bSFull + i), 1); mbar_init(bar(C::bSEmpty + i), kSoftWarps);
-      mbar_init(bar(C::bSumFull + i), kSoftWarps); mbar_init(bar(C::bSumEmpty + i), kQueryWarps);
+      mbar_init(bar(C::bSFull + i), 2); mbar_init(bar(C::bSEmpty + i), soft);
+      mbar_init(bar(C::bSumFull + i), soft / 8); mbar_init(bar(C::bSumEmpty + i), kQueryWarps);
     }
-    for (int i = 0; i < kPSlots; ++i) mbar_init(bar(C::bPFull + i), kSoftWarps);
-    for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bVoted + i), 2); mbar_init(bar(C::bFixed + i), kQueryWarps); }
+    for (int i = 0; i < kPSlots; ++i) mbar_init(bar(C::bPFull + i), soft);
+    for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bVoted + i), soft / 8); mbar_init(bar(C::bFixed + i), kQueryWarps); }
     mbar_init(bar(C::bOFull), 1);
-    for (int i = 0; i < kScSlots; ++i) { mbar_init(bar(C::bScFull + i), 1); mbar_init(bar(C::bScEmpty + i), kSoftWarps); }
     mbar_init(bar(C::bDrain), 2);                   // both issuers' last commits
     for (int i = 0; i < C::kUnits; ++i) last_armed[i] = -1;
     *abort_flag = 0;
@@ -296,19 +294,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         load(slot, next);
         ahead = next_slots(slot);
       }
-      const uint32_t sl = g % kScSlots;
+      const float f[2] = {r[0] * p.scale_log2, r[1] * p.scale_log2};
+      const float lg[2] = {__log2f(r[0]), __log2f(r[1])}, iv[2] = {__frcp_rn(r[0]), __frcp_rn(r[1])};
+      // scores of tile g - 2 read: the weights of tile g - 4 have been made
       bool ok = true;
-      if (lane == 0 && g >= kScSlots) ok = mbar_wait(bar(C::bScEmpty + sl), (g / kScSlots - 1) & 1, wc);
+      if (lane == 0 && g >= 2) ok = mbar_wait(bar(C::bSEmpty + (g & 1)), ((g >> 1) - 1) & 1, wc);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      float* out = reinterpret_cast<float*>(smem + C::kOffSc + sl * kScSlot);
+      float* out = reinterpret_cast<float*>(smem + C::kOffSc + (g % kScSlots) * kScSlot);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        out[lane + 32 * i] = r[i] * p.scale_log2;
-        out[T + lane + 32 * i] = __log2f(r[i]);
-        out[2 * T + lane + 32 * i] = __frcp_rn(r[i]);
+        out[lane + 32 * i] = f[i];
+        out[T + lane + 32 * i] = lg[i];
+        out[2 * T + lane + 32 * i] = iv[i];
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::bScFull + sl));
+      if (lane == 0) mbar_arrive(bar(C::bSFull + (g & 1)));
     }
   } else if (warp >= kLatentWarp0) {
     // ------------------------------------------------------------- gathers
@@ -560,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fix = [&](uint32_t g) {
       const uint32_t at = g % C::kUnits;
       wait(bar(C::bVoted + at), (g / C::kUnits) & 1);
-      const uint32_t moved = reinterpret_cast<const volatile uint32_t*>(smem + C::kOffMoved)[2 * at + half];
+      const uint32_t moved =
+          32 * half < Hc ? reinterpret_cast<const volatile uint32_t*>(smem + C::kOffMoved)[2 * at + half] : 0;
       if (moved && !aborted) {
         wait(bar(C::bEmpty + (g - 1) % C::kUnits), ((g - 1) / C::kUnits) & 1);   // the sums of the tiles before are done
         tc_fence_after();
@@ -607,8 +608,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       fix(g++);
       output(b, dest, nitem++);
     }
-  } else {
+  } else if (32 * (warp & 1) < Hc) {
     // ----------------------------------------------------------------- softmax
+    // The warps of heads 0-31 and those of heads 32-63 go on by themselves.
     const int q = warp & 3, th = warp >> 2, part = q >> 1;
     const int hl = 32 * (q & 1) + lane;              // head of this CTA
     const uint32_t quad = static_cast<uint32_t>(32 * q) << 16;
@@ -623,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto largest = [&](float v) -> float {
       float* r = red;
       r[eight * 64 + hl] = v;
-      named_bar_sync(kBarAll, 32 * kSoftWarps);
+      named_bar_sync(kBarHalf + (q & 1), 16 * kSoftWarps);
       v = max3(r[hl], r[64 + hl], max3(r[128 + hl], r[192 + hl], r[256 + hl]));
       return max3(v, r[320 + hl], fmaxf(r[384 + hl], r[448 + hl]));
     };
@@ -654,7 +656,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the other part's scores and the exponents; their largest
     const float w_own = part == 0 ? 1.f : kLoWeight, w_other = part == 0 ? kLoWeight : 1.f;
     auto exponents = [&](uint32_t g, int left) -> float {
-      wait(bar(C::bScFull + g % kScSlots), (g / kScSlots) & 1);
       named_bar_sync(kBarPair0 + 4 * (q & 1) + th, 64);
       const float4* xi = reinterpret_cast<const float4*>(smem + C::kOffX) + (warp ^ 2) * 64 + lane;
       const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 2 * eight;
@@ -700,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_scores(g);
       float mx = exponents(g, n);
       for (int j = 0; j < nt; ++j, ++g) {
-        const bool moved = named_bar_or(kBarVote, 32 * kSoftWarps, mx > m_ref + kLag);
+        const bool moved = named_bar_or(kBarVote + (q & 1), 16 * kSoftWarps, mx > m_ref + kLag);
         uint32_t which = 0;                          // heads whose O has to follow
         if (moved) {                                 // some head's reference moves
           const float mt = largest(mx);
@@ -773,18 +774,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && !aborted) {
-          mbar_arrive(bar(C::bPFull + g % kPSlots));
-          mbar_arrive(bar(C::bScEmpty + g % kScSlots));
-        }
+        if (lane == 0 && !aborted) mbar_arrive(bar(C::bPFull + g % kPSlots));
         if (j + 1 < nt) mx = exponents(g + 1, n - (j + 1) * T);
       }
       // what the output needs
       if (nitem >= 2) wait(bar(C::bSumEmpty + (nitem & 1)), ((nitem >> 1) - 1) & 1);
       float* r = red;
-      named_bar_sync(kBarAll, 32 * kSoftWarps);
+      named_bar_sync(kBarHalf + (q & 1), 16 * kSoftWarps);
       r[eight * 64 + hl] = l_sum;
-      named_bar_sync(kBarAll, 32 * kSoftWarps);
+      named_bar_sync(kBarHalf + (q & 1), 16 * kSoftWarps);
       if (eight == 0) {
         float l = 0.f;
 #pragma unroll
@@ -793,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         reinterpret_cast<float*>(smem + C::kOffRef)[64 * (nitem & 1) + hl] = m_ref;
       }
       __syncwarp();
-      if (lane == 0 && !aborted) mbar_arrive(bar(C::bSumFull + (nitem & 1)));
+      if (eight == 0 && lane == 0 && !aborted) mbar_arrive(bar(C::bSumFull + (nitem & 1)));
       ++nitem;
     }
   }
