@@ -81,7 +81,7 @@ constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the sca
 constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
 constexpr float kLoWeight = 1.f / 32.f;              // value of a query's lo part
 constexpr float kTop = 5.f, kLag = 3.75f;            // weights are 2^(e - m + kTop) with e <= m + kLag: to 431 of 448
-constexpr int kBarPair0 = 1, kBarHalf = 9, kBarVote = 11, kBarGather = 13;  // named barriers
+constexpr int kBarPair0 = 1, kBarTeam = 9, kBarVote = 11, kBarGather = 13;  // named barriers
 constexpr int kTmO = 0, kTmQ = 256, kTmS = 384;
 constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);
 
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kPrepThreads) rows8_prep_kernel(const Fp8PrepP
   }
 }
 
-template <bool kFine>
+// kFew: at most 32 heads a CTA
+template <bool kFine, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1)
     rows8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const DecodeParams p, const Fp8Params p8) {
@@ -211,15 +212,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bFull + i), 1); mbar_init(bar(C::bEmpty + i), 1); }
-    const int soft = Hc > 32 ? kSoftWarps : kSoftWarps / 2;
     mbar_init(bar(C::bQFull), kQueryWarps);
     mbar_init(bar(C::bQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::bSFull + i), 2); mbar_init(bar(C::bSEmpty + i), soft);
-      mbar_init(bar(C::bSumFull + i), soft / 8); mbar_init(bar(C::bSumEmpty + i), kQueryWarps);
+      mbar_init(bar(C::bSFull + i), 2); mbar_init(bar(C::bSEmpty + i), kSoftWarps);
+      mbar_init(bar(C::bSumFull + i), kFew ? 1 : 2); mbar_init(bar(C::bSumEmpty + i), kQueryWarps);
     }
-    for (int i = 0; i < kPSlots; ++i) mbar_init(bar(C::bPFull + i), soft);
-    for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bVoted + i), soft / 8); mbar_init(bar(C::bFixed + i), kQueryWarps); }
+    for (int i = 0; i < kPSlots; ++i) mbar_init(bar(C::bPFull + i), kSoftWarps);
+    for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bVoted + i), kFew ? 1 : 2); mbar_init(bar(C::bFixed + i), kQueryWarps); }
     mbar_init(bar(C::bOFull), 1);
     mbar_init(bar(C::bDrain), 2);                   // both issuers' last commits
     for (int i = 0; i < C::kUnits; ++i) last_armed[i] = -1;
@@ -456,11 +456,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kQueryWarp0) {
     // ------------------------------------------- the items' queries and outputs
-    // Query: row 32 q + lane of A is part q / 2 of head 32 (q % 2) + lane; two
-    // warps share a quadrant, each 256 latent and 32 rope dims of its rows.
-    // Output: dims 32 q + lane of every block of 128, heads 32 half .. of the CTA's.
+    // Query: row 32 q + lane of A is part q / 2 of head 32 (q % 2) + lane (kFew: of
+    // head lane); two warps share a quadrant, each 256 latent and 32 rope dims of
+    // its rows.  Output: dims 32 q + lane of every block of 128, heads 32 half ..
+    // of the CTA's (kFew: of blocks 2 half and 2 half + 1, all heads).
     const int q = warp & 3, half = (warp >> 2) & 1;
-    const int row = 32 * q + lane, hl = row & 63;
+    const int row = 32 * q + lane, hl = kFew ? lane : row & 63;
+    const int h0 = kFew ? 0 : 32 * half;
+    constexpr int kBlocks = kFew ? 2 : 4;            // of the output's 128 dims
+    const int block0 = kFew ? 2 * half : 0;
     const bool lo = q >= 2, head_ok = hl < Hc;
     auto wait = [&](uint32_t bb, uint32_t par) {
       if (!aborted && !__all_sync(0xffffffffu, mbar_wait(bb, par, wc))) aborted = true;
@@ -510,14 +514,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool part_ok = dest < p.max_partials;    // a device-only plan naming a partial past the workspace
       if (!part_ok && warp == kQueryWarp0 && lane == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
       wait(bar(C::bSumFull + (nitem & 1)), (nitem >> 1) & 1);
-      const int h0 = 32 * half;
       const float l = reinterpret_cast<const float*>(smem + C::kOffSum)[64 * (nitem & 1) + h0 + lane];
       const float ref = reinterpret_cast<const float*>(smem + C::kOffRef)[64 * (nitem & 1) + h0 + lane];
       const float inv = l > 0.f ? 1.f / l : 0.f;     // of head h0 + lane
       __syncwarp();
       if (lane == 0 && !aborted) mbar_arrive(bar(C::bSumEmpty + (nitem & 1)));
       const size_t row0 = static_cast<size_t>(dest < 0 ? b : dest) * p.heads + cta * Hc;
-      if (q == 0 && h0 + lane < Hc && !aborted && part_ok) {
+      if (q == 0 && (!kFew || half == 0) && h0 + lane < Hc && !aborted && part_ok) {
         const float lse = l > 0.f ? (ref + __log2f(l) - kTop) * 0.69314718055994531f : -INFINITY;
         if (dest >= 0) p.part_lse[row0 + h0 + lane] = lse;
         else if (p.lse) p.lse[row0 + h0 + lane] = lse;
@@ -525,13 +528,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(bar(C::bOFull), nitem & 1);
       tc_fence_after();
       if (!aborted && part_ok) {
-        const size_t first = (row0 + h0) * kLatent + 32 * q + lane;
+        const size_t first = (row0 + h0) * kLatent + 128 * block0 + 32 * q + lane;
         const int n = min(max(Hc - h0, 0), 32);      // heads, a multiple of 8
-        const uint32_t from = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmO + h0;
+        const uint32_t from = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmO + 64 * block0 + h0;
         // (a store's 32 lanes are a head's 128 bytes; the type is looked at once, not at every store)
         auto put = [&](auto* dst, auto as) {
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {              // block c / 2, 16 heads
+          for (int c = 0; c < 2 * kBlocks; ++c) {    // block c / 2, 16 heads
             if (16 * (c & 1) >= n) continue;
             uint32_t o[16];
             tmem_ld16(from + 64 * (c >> 1) + 16 * (c & 1), o);
@@ -560,25 +563,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fix = [&](uint32_t g) {
       const uint32_t at = g % C::kUnits;
       wait(bar(C::bVoted + at), (g / C::kUnits) & 1);
-      const uint32_t moved =
-          32 * half < Hc ? reinterpret_cast<const volatile uint32_t*>(smem + C::kOffMoved)[2 * at + half] : 0;
+      const uint32_t moved = reinterpret_cast<const volatile uint32_t*>(smem + C::kOffMoved)[2 * at + (kFew ? 0 : half)];
       if (moved && !aborted) {
         wait(bar(C::bEmpty + (g - 1) % C::kUnits), ((g - 1) / C::kUnits) & 1);   // the sums of the tiles before are done
         tc_fence_after();
-        const float4* bc = reinterpret_cast<const float4*>(smem + C::kOffBc) + 16 * at + 8 * half;
-        const uint32_t to = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmO + 32 * half;
+        const float4* bc = reinterpret_cast<const float4*>(smem + C::kOffBc) + 16 * at + h0 / 4;
+        const uint32_t to = tmem + (static_cast<uint32_t>(32 * q) << 16) + kTmO + 64 * block0 + h0;
         if (!aborted)
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {              // 8 heads
             if (((moved >> (8 * c)) & 0xffu) == 0) continue;
-            uint32_t o[4][8];
+            uint32_t o[kBlocks][8];
 #pragma unroll
-            for (int mb = 0; mb < 4; ++mb) tmem_ld8(to + 64 * mb + 8 * c, o[mb]);
+            for (int mb = 0; mb < kBlocks; ++mb) tmem_ld8(to + 64 * mb + 8 * c, o[mb]);
             const float4 f0 = bc[2 * c], f1 = bc[2 * c + 1];
             const float2 f[4] = {f2_pack(f0.x, f0.y), f2_pack(f0.z, f0.w), f2_pack(f1.x, f1.y), f2_pack(f1.z, f1.w)};
             tmem_wait_ld();
 #pragma unroll
-            for (int mb = 0; mb < 4; ++mb) {
+            for (int mb = 0; mb < kBlocks; ++mb) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float2 v = f2_mul(f2_pack(__uint_as_float(o[mb][2 * i]), __uint_as_float(o[mb][2 * i + 1])), f[i]);
@@ -608,75 +610,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       fix(g++);
       output(b, dest, nitem++);
     }
-  } else if (32 * (warp & 1) < Hc) {
+  } else {
     // ----------------------------------------------------------------- softmax
-    // The warps of heads 0-31 and those of heads 32-63 go on by themselves.
+    // The warps of heads 0-31 and those of heads 32-63 go on by themselves.  With
+    // kFew quadrants 1 and 3 hold the heads of 0 and 2 once more, and their warps
+    // take half of the rows.
+    constexpr int kTeams = kFew ? 1 : 2, kRows = kFew ? 4 : 8, kShare = T / kRows;   // threads that share a head
     const int q = warp & 3, th = warp >> 2, part = q >> 1;
-    const int hl = 32 * (q & 1) + lane;              // head of this CTA
+    const int team = kFew ? 0 : q & 1;
+    const int hl = 32 * team + lane;                 // head of this CTA
+    const int eight = kFew ? 4 * th + 2 * (q & 1) + part : 2 * th + part;   // which kRows rows of a tile
     const uint32_t quad = static_cast<uint32_t>(32 * q) << 16;
     float* red = reinterpret_cast<float*>(smem + C::kOffRed);
     volatile uint32_t* moved_of = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMoved);   // heads to rescale
-    const int eight = 2 * th + part;                 // which 8 rows of a tile
     float m_ref = 0.f, l_sum = 0.f, fac = 1.f;
     auto wait = [&](uint32_t bb, uint32_t par) {     // (every lane for itself: a third of the time of one for all)
       if (!aborted && !__all_sync(0xffffffffu, mbar_wait(bb, par, wc))) aborted = true;
     };
-    // the largest of this head's values, of the eight threads that share it (who have voted since they read the last)
+    // the largest of this head's values, of the threads that share it (who have voted since they read the last)
     auto largest = [&](float v) -> float {
       float* r = red;
-      r[eight * 64 + hl] = v;
-      named_bar_sync(kBarHalf + (q & 1), 16 * kSoftWarps);
-      v = max3(r[hl], r[64 + hl], max3(r[128 + hl], r[192 + hl], r[256 + hl]));
-      return max3(v, r[320 + hl], fmaxf(r[384 + hl], r[448 + hl]));
+      r[eight * 32 * kTeams + hl] = v;
+      named_bar_sync(kBarTeam + team, 32 * kSoftWarps / kTeams);
+#pragma unroll
+      for (int i = 0; i < kShare; i += 2) v = max3(v, r[i * 32 * kTeams + hl], r[(i + 1) * 32 * kTeams + hl]);
+      return v;
     };
-    uint32_t kept[8];                                // this part's scores of a tile's 8 rows, on their way
-    float2 x[4];                                     // exponents of a tile's 8 rows
-    // Scores of tile g, from TMEM: the thread of the hi part keeps rows 0-7 of these 16 and sends the others, that of
-    // the lo part the other way round.  (What was sent last has been read: the other thread has voted since.)
+    uint32_t kept[kRows];                            // this part's scores of a tile's kRows rows, on their way
+    float2 x[kRows / 2];                             // exponents of a tile's kRows rows
+    // Scores of tile g, from TMEM: the thread of the hi part keeps the first half of 2 kRows and sends the others, that
+    // of the lo part the other way round.  (What was sent last has been read: the other thread has voted since.)
     auto load_scores = [&](uint32_t g) {
       wait(bar(C::bSFull + (g & 1)), (g >> 1) & 1);
-      uint32_t sent[8];
+      uint32_t sent[kRows];
       if (!aborted) {
         tc_fence_after();
-        const uint32_t ts = tmem + quad + kTmS + T * (g & 1) + 16 * th;
-        tmem_ld8(ts + 8 * (1 - part), sent);
-        tmem_ld8(ts + 8 * part, kept);
+        const uint32_t ts = tmem + quad + kTmS + T * (g & 1) + kRows * eight;
+        if constexpr (kFew) {
+          tmem_ld4(ts + 4 - 8 * part, sent);
+          tmem_ld4(ts, kept);
+        } else {
+          tmem_ld8(ts + 8 - 16 * part, sent);
+          tmem_ld8(ts, kept);
+        }
         tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) kept[i] = sent[i] = 0;
+        for (int i = 0; i < kRows; ++i) kept[i] = sent[i] = 0;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0 && !aborted) mbar_arrive(bar(C::bSEmpty + (g & 1)));
       uint4* xo = reinterpret_cast<uint4*>(smem + C::kOffX) + warp * 64 + lane;
-      xo[0] = make_uint4(sent[0], sent[1], sent[2], sent[3]);
-      xo[32] = make_uint4(sent[4], sent[5], sent[6], sent[7]);
+#pragma unroll
+      for (int k = 0; k < kRows / 4; ++k) xo[32 * k] = make_uint4(sent[4 * k], sent[4 * k + 1], sent[4 * k + 2], sent[4 * k + 3]);
     };
     // the other part's scores and the exponents; their largest
     const float w_own = part == 0 ? 1.f : kLoWeight, w_other = part == 0 ? kLoWeight : 1.f;
     auto exponents = [&](uint32_t g, int left) -> float {
       named_bar_sync(kBarPair0 + 4 * (q & 1) + th, 64);
       const float4* xi = reinterpret_cast<const float4*>(smem + C::kOffX) + (warp ^ 2) * 64 + lane;
-      const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 2 * eight;
+      const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + kRows / 4 * eight;
       const float2 f_own = f2_pack(fac * w_own, fac * w_own), f_other = f2_pack(fac * w_other, fac * w_other);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kRows / 4; ++k) {
         const float4 o = xi[32 * k], f = sc[k], lg = sc[T / 4 + k];
         float2 t = f2_mul(f2_pack(__uint_as_float(kept[4 * k]), __uint_as_float(kept[4 * k + 1])), f_own);
         x[2 * k] = f2_fma(f2_fma(f2_pack(o.x, o.y), f_other, t), f2_pack(f.x, f.y), f2_pack(lg.x, lg.y));
         t = f2_mul(f2_pack(__uint_as_float(kept[4 * k + 2]), __uint_as_float(kept[4 * k + 3])), f_own);
         x[2 * k + 1] = f2_fma(f2_fma(f2_pack(o.z, o.w), f_other, t), f2_pack(f.z, f.w), f2_pack(lg.z, lg.w));
       }
-      const int nvalid = left - 8 * eight;
-      if (nvalid < 8) {
+      const int nvalid = left - kRows * eight;
+      if (nvalid < kRows) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kRows / 2; ++i) {
           if (2 * i >= nvalid) x[i].x = -INFINITY;
           if (2 * i + 1 >= nvalid) x[i].y = -INFINITY;
         }
       }
-      return max3(max3(x[0].x, x[0].y, x[1].x), max3(x[1].y, x[2].x, x[2].y), fmaxf(x[3].x, x[3].y));
+      float m = fmaxf(x[0].x, x[0].y);
+#pragma unroll
+      for (int i = 1; i < kRows / 2; ++i) m = max3(m, x[i].x, x[i].y);
+      return m;
     };
     griddep_wait();                                  // the factors come from the kernel before
     // 2^-a of this head in the next usable item from `it` on, loaded while the item before is worked on
@@ -701,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_scores(g);
       float mx = exponents(g, n);
       for (int j = 0; j < nt; ++j, ++g) {
-        const bool moved = named_bar_or(kBarVote + (q & 1), 16 * kSoftWarps, mx > m_ref + kLag);
+        const bool moved = named_bar_or(kBarVote + team, 32 * kSoftWarps / kTeams, mx > m_ref + kLag);
         uint32_t which = 0;                          // heads whose O has to follow
         if (moved) {                                 // some head's reference moves
           const float mt = largest(mx);
@@ -714,19 +729,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             which = __ballot_sync(0xffffffffu, alpha != 1.f && hl < Hc);
           }
         }
-        if (eight == 0) {                            // (warps 0 and 1)
-          if (lane == 0) moved_of[2 * (g % C::kUnits) + warp] = j > 0 ? which : 0;
+        if (eight == 0) {                            // (a warp of the team)
+          if (lane == 0) moved_of[2 * (g % C::kUnits) + team] = j > 0 ? which : 0;
           __syncwarp();
           if (lane == 0 && !aborted) mbar_arrive(bar(C::bVoted + g % C::kUnits));
         }
         if (j + 1 < nt) load_scores(g + 1);
-        // weights and their parts; 8 rows are half a 16-byte chunk of each
-        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + 2 * eight;
-        uint32_t w0[2], w1[2], w2[2], w3[2];
+        // weights and their parts
+        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + kRows / 4 * eight;
+        uint32_t w0[kRows / 4], w1[kRows / 4], w2[kRows / 4], w3[kRows / 4];
         const float2 shift = f2_pack(kTop - m_ref, kTop - m_ref);
         float2 l2 = f2_pack(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kRows / 4; ++k) {
           const float4 iv = sc[2 * T / 4 + k];
           uint32_t c0[2], c1[2], c2[2], c3[2];
 #pragma unroll
@@ -761,14 +776,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j + 1 == nt && g >= kPSlots)
           wait(bar(C::bEmpty + (g - kPSlots) % C::kUnits), ((g - kPSlots) / C::kUnits) & 1);
         if (!aborted) {
-          // byte 8 eight of the head's 64 (hi), then the same of the lo part: chunks c at c ^ (head mod 8)
-          uint8_t* row = smem + C::kOffP + (g % kPSlots) * C::kPBuf + hl * 128 + 8 * part;
+          // byte kRows eight of the head's 64 (hi), then the same of the lo part: chunks c at c ^ (head mod 8)
+          uint8_t* row = smem + C::kOffP + (g % kPSlots) * C::kPBuf + hl * 128 + (kRows * eight & 15);
           const int at = (th ^ (hl & 7)) << 4, at_lo = ((4 + th) ^ (hl & 7)) << 4;
-          *reinterpret_cast<uint2*>(row + at) = make_uint2(w0[0], w0[1]);
-          *reinterpret_cast<uint2*>(row + at_lo) = make_uint2(w1[0], w1[1]);
+          auto put = [&](int to, const uint32_t (&v)[kRows / 4]) {
+            if constexpr (kFew) *reinterpret_cast<uint32_t*>(row + to) = v[0];
+            else *reinterpret_cast<uint2*>(row + to) = make_uint2(v[0], v[1]);
+          };
+          put(at, w0);
+          put(at_lo, w1);
           if constexpr (kFine) {
-            *reinterpret_cast<uint2*>(row + kPPair + at) = make_uint2(w2[0], w2[1]);
-            *reinterpret_cast<uint2*>(row + kPPair + at_lo) = make_uint2(w3[0], w3[1]);
+            put(kPPair + at, w2);
+            put(kPPair + at_lo, w3);
           }
         }
         fence_proxy_async_smem();
@@ -780,13 +799,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // what the output needs
       if (nitem >= 2) wait(bar(C::bSumEmpty + (nitem & 1)), ((nitem >> 1) - 1) & 1);
       float* r = red;
-      named_bar_sync(kBarHalf + (q & 1), 16 * kSoftWarps);
-      r[eight * 64 + hl] = l_sum;
-      named_bar_sync(kBarHalf + (q & 1), 16 * kSoftWarps);
+      named_bar_sync(kBarTeam + team, 32 * kSoftWarps / kTeams);
+      r[eight * 32 * kTeams + hl] = l_sum;
+      named_bar_sync(kBarTeam + team, 32 * kSoftWarps / kTeams);
       if (eight == 0) {
         float l = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) l += r[i * 64 + hl];
+        for (int i = 0; i < kShare; ++i) l += r[i * 32 * kTeams + hl];
         reinterpret_cast<float*>(smem + C::kOffSum)[64 * (nitem & 1) + hl] = l;
         reinterpret_cast<float*>(smem + C::kOffRef)[64 * (nitem & 1) + hl] = m_ref;
       }
@@ -824,7 +843,9 @@ int launch_rows8(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const De
                  const Fp8PrepParams& pp, int workers, cudaStream_t stream) {
   if (p.heads < 16 || p.heads > 128 || p.heads % 16 != 0) return MLA_ERR_UNSUPPORTED;
   const int ctas = p.heads > 32 ? 2 * workers : workers;
-  const auto kernel = p.out_bf16 ? &rows8::rows8_kernel<false> : &rows8::rows8_kernel<true>;
+  const bool few = p.heads <= 64;                    // heads of a CTA <= 32
+  const auto kernel = p.out_bf16 ? (few ? &rows8::rows8_kernel<false, true> : &rows8::rows8_kernel<false, false>)
+                                 : (few ? &rows8::rows8_kernel<true, true> : &rows8::rows8_kernel<true, false>);
   const int smem = p.out_bf16 ? rows8::Cfg<false>::kSmemBytes : rows8::Cfg<true>::kSmemBytes;
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), smem)) return MLA_ERR_CUDA;
   // few enough blocks that the next kernel's fit beside them (it starts once all have)
