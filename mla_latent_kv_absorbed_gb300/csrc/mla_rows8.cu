@@ -53,11 +53,11 @@
 //   16-23  the next item's query (half of its parts in registers while the item
 //          before is worked on; then into TMEM and shared memory), and the output
 //          of the item before
-//   24     issuer of the scores     25  TMEM allocator, issuer of the weighted sums
-//   26-29  gathers of the latents, an atom each: 16 of four rows a tile (a warp
+//   24     TMEM allocator, issuer of both products
+//   25-28  gathers of the latents, an atom each: 16 of four rows a tile (a warp
 //          takes some 60 cycles for each of a burst, so they are spread)
-//   30     gathers of the rope keys
-//   31     the numbers made of the rows' scales
+//   29     gathers of the rope keys
+//   30     the numbers made of the rows' scales
 #include "mla_device.cuh"
 #include "mla_launch.h"
 
@@ -66,8 +66,8 @@ namespace rows8 {
 
 constexpr int T = 64;                                // rows of a tile
 constexpr int kSoftWarps = 16, kQueryWarps = 8;
-constexpr int kQueryWarp0 = 16, kQkWarp = 24, kPvWarp = 25, kLatentWarp0 = 26, kRopeWarp = 30, kScaleWarp = 31;
-constexpr int kThreads = 32 * 32;
+constexpr int kQueryWarp0 = 16, kMmaWarp = 24, kLatentWarp0 = 25, kRopeWarp = 29, kScaleWarp = 30;
+constexpr int kThreads = 31 * 32;
 constexpr int kAtom = T * 128;                       // 64 rows x 128 dims
 constexpr int kRopeOff = 4 * kAtom;
 constexpr int kUnit = 4 * kAtom + T * 64;            // a tile: 36 KB
@@ -221,12 +221,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kPSlots; ++i) mbar_init(bar(C::bPFull + i), kSoftWarps);
     for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bVoted + i), kFew ? 1 : 2); mbar_init(bar(C::bFixed + i), kQueryWarps); }
     mbar_init(bar(C::bOFull), 1);
-    mbar_init(bar(C::bDrain), 2);                   // both issuers' last commits
+    mbar_init(bar(C::bDrain), 1);
     for (int i = 0; i < C::kUnits; ++i) last_armed[i] = -1;
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kPvWarp) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -381,10 +381,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u >= 0) drain_wait(bar(C::bFull + lane), u & 1);
     }
     __syncwarp();
-  } else if (warp >= kQkWarp) {
+  } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------- products
     // The whole warp runs the loop and one elected lane issues, so that
-    // descriptors and counters stay in uniform registers.
+    // descriptors and counters stay in uniform registers.  Both kinds are one
+    // warp's: the parts of a block's sum share A in the collector buffer, and
+    // nothing may come between them.  It takes whichever is ready, scores first.
     const bool lead = elect_one();
     auto D = [](uint64_t d, uint32_t byte_off) -> uint64_t { return d + (byte_off >> 4); };
     const uint64_t dk = sdesc(base, 16, 1024), dv = sdesc(base, kAtom, 1024);
@@ -394,18 +396,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cols = (Hc + 15) & ~15;                // columns that hold heads
     const uint32_t idesc4 = idesc_e4m3(128, cols, true, false);
     const uint32_t idesc5 = idesc_f8(kFmtE4M3, kFmtE5M2, 128, cols, true, false);
-    uint32_t g = 0, nitem = 0, slot = 0, lap = 0;
-    bool ok = true;
-    for (int it = it0; it < it1 && ok; ++it) {
-      const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
-      if (!item_ok(p, nnz, b, s, e)) continue;
-      const int nt = (e - s + T - 1) / T;
-      if (warp == kQkWarp) ok = mbar_wait(bar(C::bQFull), nitem & 1, wc);
-      for (int j = 0; j < nt && ok; ++j, ++g) {
-        const uint32_t buf = g & 1;
-        if (warp == kQkWarp) {
-          ok = (g < 2 || mbar_wait(bar(C::bSEmpty + buf), ((g >> 1) - 1) & 1, wc)) && mbar_wait(bar(C::bFull + slot), lap, wc);
-          if (!ok) break;
+    struct Cursor {                                  // a tile: the g-th, left tiles of its item with it
+      int it, left;
+      uint32_t g, nitem;
+      bool first;
+    };
+    auto enter = [&](Cursor& c) {                    // the next usable item
+      for (; c.it < it1; ++c.it) {
+        const int b = item_w(c.it, 0), s = item_w(c.it, 1), e = item_w(c.it, 2);
+        if (!item_ok(p, nnz, b, s, e)) continue;
+        c.left = (e - s + T - 1) / T;
+        c.first = true;
+        return;
+      }
+    };
+    auto next = [&](Cursor& c) {
+      ++c.g;
+      c.first = false;
+      if (--c.left == 0) {
+        ++c.it;
+        ++c.nitem;
+        enter(c);
+      }
+    };
+    auto ready = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar(i), parity)); };
+    Cursor qk{it0, 0, 0, 0, false}, pv{it0, 0, 0, 0, false};
+    enter(qk);
+    enter(pv);
+    uint64_t t0 = 0;
+    int idle = 0;
+    while (pv.it < it1) {
+      bool some = false;
+      if (qk.it < it1) {
+        const uint32_t g = qk.g, buf = g & 1, slot = g % C::kUnits;
+        if (ready(C::bFull + slot, (g / C::kUnits) & 1) && (g < 2 || ready(C::bSEmpty + buf, ((g >> 1) - 1) & 1)) &&
+            (!qk.first || ready(C::bQFull, qk.nitem & 1))) {
           tc_fence_after();
           const uint32_t d_s = tmem + kTmS + buf * T;
           const uint64_t bk = D(dk, slot * kUnit), br = D(dr, slot * kUnit);
@@ -416,12 +441,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 2; ++k) umma_ss_f8(d_s, D(dq, 32 * k), D(br, 32 * k), kIdescQK, 1u);
             umma_commit(bar(C::bSFull + buf));
-            if (j == nt - 1) umma_commit(bar(C::bQEmpty));
+            if (qk.left == 1) umma_commit(bar(C::bQEmpty));
           }
-        } else {
-          const uint32_t ps = g % kPSlots;
-          ok = mbar_wait(bar(C::bFixed + slot), lap, wc) && mbar_wait(bar(C::bPFull + ps), (g / kPSlots) & 1, wc);
-          if (!ok) break;
+          next(qk);
+          some = true;
+        }
+      }
+      if (pv.g < qk.g) {
+        const uint32_t g = pv.g, slot = g % C::kUnits, ps = g % kPSlots;
+        if (ready(C::bPFull + ps, (g / kPSlots) & 1) && ready(C::bFixed + slot, (g / C::kUnits) & 1)) {
           tc_fence_after();
           const uint64_t av = D(dv, slot * kUnit), bp = D(dp, ps * C::kPBuf);
           if (lead) {
@@ -431,23 +459,34 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int ks = 0; ks < 2; ++ks) {       // 32 rows
                 const uint64_t a = D(av, mb * kAtom + 4096 * ks);
                 const uint32_t d = tmem + kTmO + 64 * mb;
-                umma_ss_f8(d, a, D(bp, 32 * ks), idesc4, (j == 0 && ks == 0) ? 0u : 1u);
-                umma_ss_f8(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
+                umma_ss_f8_run<ARun::kFirst>(d, a, D(bp, 32 * ks), idesc4, (pv.first && ks == 0) ? 0u : 1u);
                 if constexpr (kFine) {
-                  umma_ss_f8(d, a, D(bp, kPPair + 32 * ks), idesc4, 1u);
+                  umma_ss_f8_run<ARun::kMid>(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
+                  umma_ss_f8_run<ARun::kLast>(d, a, D(bp, kPPair + 32 * ks), idesc4, 1u);
                   umma_ss_f8(d, a, D(bp, kPPair + 64 + 32 * ks), idesc5, 1u);
+                } else {
+                  umma_ss_f8_run<ARun::kLast>(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
                 }
               }
             umma_commit(bar(C::bEmpty + slot));
-            if (j == nt - 1) umma_commit(bar(C::bOFull));
+            if (pv.left == 1) umma_commit(bar(C::bOFull));
           }
-        }
-        if (++slot == static_cast<uint32_t>(C::kUnits)) {
-          slot = 0;
-          lap ^= 1;
+          next(pv);
+          some = true;
         }
       }
-      ++nitem;
+      if (some) {
+        idle = 0;
+      } else if ((++idle & 255) == 0) {              // a bounded wait, as in mbar_wait
+        const uint64_t t = globaltimer();
+        if (idle == 256) t0 = t;
+        if (__any_sync(0xffffffffu, t - t0 > MLA_WAIT_LIMIT_NS)) {
+          *abort_flag = 1;
+          if (lane == 0) record_status(p.status, MLA_ERR_TIMEOUT);
+          break;
+        }
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+      }
     }
     if (lead) {
       umma_commit(bar(C::bDrain));
@@ -818,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kPvWarp) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 template <typename Kernel, typename... Args>
