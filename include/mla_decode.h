@@ -763,7 +763,8 @@ int mla_verify_drafts(const float* target_probs, int64_t target_batch_stride, in
  * num_slots rows (0 for a num_slots outside 1 .. 2^31 - 1).  Zero-filled before
  * its first use; a status word as for mla_decode_run, and a set of slots that is
  * empty between calls, so that calls that share one must not overlap on the GPU.
- * One made for more slots serves a smaller pool as well. */
+ * One made for more slots serves a smaller pool as well, called with all of its
+ * bytes. */
 size_t mla_slots_workspace_bytes(int64_t num_slots);
 
 /* mla_repack_requests -- asynchronous on `stream`.

@@ -31,7 +31,9 @@ struct VerifyParams {
 int launch_verify(const VerifyParams& p, cudaStream_t stream);
 
 // ---- workspace of the calls that keep sets of slots --------------------------
-// A set of slots is a bitmap, 32 to a word; `bits` is all zero between calls.
+// A set of slots is a bitmap, 32 to a word; `bits` is all zero between calls.  It
+// lies at the front and the rest at the end, so that the rest of a small pool's
+// call leaves the words of a larger pool's set alone.
 struct SlotsWs {
   size_t bits;                // uint32 [words]
   size_t live;                // uint2 [words]: a word of the live slots, and how many live ones are in the words before
@@ -40,16 +42,17 @@ struct SlotsWs {
   size_t counts;              // int32 [2]: live slots, and those of them past the lowest n
   size_t total;
 };
-inline SlotsWs slots_ws(int64_t num_slots) {
+inline SlotsWs slots_ws(int64_t num_slots, size_t bytes = 0) {
   const size_t n = static_cast<size_t>(num_slots), words = (n + 31) / 32;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t live = up(8 * words), list = up(4 * (n / 2)), rest = live + 2 * list + 256;
   SlotsWs w{};
   w.bits = kWsHeaderBytes;
-  w.live = up(w.bits + 4 * words);
-  w.holes = up(w.live + 8 * words);
-  w.away = up(w.holes + 4 * (n / 2));
-  w.counts = up(w.away + 4 * (n / 2));
-  w.total = w.counts + 256;
+  w.total = up(w.bits + 4 * words) + rest;
+  w.live = (bytes > w.total ? bytes & ~size_t(255) : w.total) - rest;
+  w.holes = w.live + live;
+  w.away = w.holes + list;
+  w.counts = w.away + list;
   return w;
 }
 

@@ -144,7 +144,7 @@ int mla_compact_cache(void* kv_cache, float* kv_scales, int64_t num_slots, int64
   if (!rows_ok(kv_cache, kv_scales, num_slots, layer_rows, layers, row_bytes) || !ready(kv_indptr, 4) ||
       !ready(live_count, 4) || (entries > 0 && (!ready(kv_indices, 4) || !ready(new_indices, 4))) || !ready(workspace))
     return MLA_ERR_INVALID_ARG;
-  const SlotsWs w = slots_ws(num_slots);
+  const SlotsWs w = slots_ws(num_slots, workspace_bytes);
   if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   CompactParams c{};

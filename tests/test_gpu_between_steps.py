@@ -457,6 +457,23 @@ def test_compact_takes_a_workspace_again_and_records_bad_slots():
 
 # ------------------------------------------------------------------ as they are used
 
+def test_one_workspace_serves_pools_of_two_sizes():
+    torch, B = _t()
+    ws = torch.zeros(B.slots_workspace_bytes(50000), dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(9)
+    for N in (50000, 300, 50000, 7000, 50000):
+        idx = rng.permutation(N)[:2 * N // 3].astype(np.int32)
+        cache = torch.zeros((N, 576), dtype=torch.uint8, device="cuda")
+        new, live, ip = _dev(idx * 0), _dev([0]), _dev([0, len(idx)])
+        B.compact_cache(cache, ip, _dev(idx), new, live, ws)
+        n, to = S.compact(idx)
+        assert int(live) == n and new.cpu().tolist() == [to.get(int(x), int(x)) for x in idx]
+        nip, nidx, freed, count = _dev([0]), _dev([0]), _dev(np.full(N, -1)), _dev([0])
+        B.repack_requests(ip, _dev(idx), _dev([]), nip, nidx, N, ws, freed=freed, freed_count=count)
+        assert int(count) == len(idx) and freed[:len(idx)].cpu().tolist() == sorted(idx.tolist())
+    assert B.check_errors(ws) == 0
+
+
 @pytest.mark.parametrize("H,form", [(16, "tree"), (8, "chain")])
 def test_a_speculative_step(H, form):
     """Drafts appended, attended to in one pass, verified; the lists cut, a request forked and one freed, the pool made
