@@ -353,29 +353,6 @@ __device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t adesc, uint
       : "memory");
 }
 
-// The same in a run of products that share A: the first of them fills the
-// collector buffer with it, the others read it from there and the last lets it
-// go.  Nothing else may be issued in between, and B has one type throughout (a
-// last product with E5M2 after E4M3 ones came out wrong).  (64 columns: 35 cycles each of
-// four instead of 48, 32 columns: 23 instead of 40.)
-enum class ARun { kFirst, kMid, kLast };
-template <ARun kAt>
-__device__ __forceinline__ void umma_ss_f8_run(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-#define MLA_UMMA_RUN(use)                                                       \
-  asm volatile(                                                                 \
-      "{\n\t.reg .pred p;\n\t"                                                  \
-      "setp.ne.b32 p, %4, 0;\n\t"                                               \
-      "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::" use                \
-      " [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),                               \
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)                       \
-      : "memory")
-  if constexpr (kAt == ARun::kFirst) MLA_UMMA_RUN("fill");
-  else if constexpr (kAt == ARun::kMid) MLA_UMMA_RUN("use");
-  else MLA_UMMA_RUN("lastuse");
-#undef MLA_UMMA_RUN
-}
-
 // D[tmem] (+)= A[tmem] * B[smem]^T, kind::f8f6f4 (A: 4 codes per TMEM column, K ascending).
 __device__ __forceinline__ void umma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -478,13 +455,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr)
                : "memory");
 }

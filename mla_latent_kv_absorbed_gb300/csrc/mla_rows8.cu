@@ -1,16 +1,9 @@
 // Absorbed MLA decode over an FP8 (E4M3) latent cache with a scale for every
-// row, for many heads (H = 48..128, step 16) on sm_103a.  ("MLA and
-// torch.compile: v0.3's two sources", section "MLA: starting from a 439-line
-// commit": the FP8 KV cache; "实现差距：MLA 与 DeepSeek V3", section 2.4: the
-// latent and rope dot products summed and scaled, FA2-style online softmax, the
-// latent rows reused as the values.)
-//
-// A worker is two CTAs, and each takes half of the HEADS: all of the scores,
-// the softmax and the output of a head are one CTA's, and nothing passes between
-// the two.  Both gather every row, the second of them from L2.  (As a cluster
-// that gathers half of the rows each and multicasts them, a gather of four rows
-// took the TMA unit 47 cycles, and 40 of them a tile 1900; on its own one takes
-// about 14.)
+// row (H = 16..128, step 16) on sm_103a.  ("MLA and torch.compile: v0.3's two
+// sources", section "MLA: starting from a 439-line commit": the FP8 KV cache;
+// "实现差距：MLA 与 DeepSeek V3", section 2.4: the latent and rope dot products
+// summed and scaled, FA2-style online softmax, the latent rows reused as the
+// values.)
 //
 // Row t has codes x_t and the scale r_t; the exponents carry the scale,
 //   e_t = sm_scale log2(e) r_t (q . x_t) + log2 r_t,
@@ -20,10 +13,11 @@
 //
 // Both products are kind::f8f6f4 and take the codes as they lie in shared
 // memory.  The query is two E4M3 parts, q 2^a = hi + lo / 32 (a puts the head's
-// largest element into [128, 256)), stacked on M: rows 0-63 of A are the hi parts
-// of the CTA's heads, rows 64-127 the lo parts, in tensor memory.
+// largest element into [128, 256)), stacked on M of A, in tensor memory: in each
+// quadrant of 32 rows the hi parts of 16 heads and then their lo parts, so that
+// the two of a head meet by a shuffle.
 //   S[128 x 64 rows] = [hi; lo] X^T          16 K-steps from TMEM, 2 of the rope
-// The weights, at most 256, are parts that add up in one accumulator:
+// The weights, at most 431, are parts that add up in one accumulator:
 //   out bf16   hi + lo, both E4M3: 8 significant bits, or 2^-10 absolute
 //   out fp32   two more, E4M3 and E5M2: 16 bits, or 2^-14 absolute (the largest
 //              weight is 32 or more) - what an fp32 result is asked for
@@ -31,11 +25,31 @@
 //                                            32 rows a part
 // The parts' errors are the weights' own; the sum l takes them unrounded.
 //
-// A tile is 18 and 16 (fp32: 32) products of 48 cycles, the least that one of
-// this width takes: 1650 cycles a tile (fp32 2430) against 580 for its bytes at
-// the measured bandwidth.  The softmax of a tile is a chain of waits and
-// exchanges of 2500 cycles, so its first half, up to the exchange of the parts,
-// is begun before the weights of the tile before are made.
+// A worker of 48 or more heads is two CTAs, and each takes half of the HEADS:
+// all of the scores, the softmax and the output of a head are one CTA's, and
+// nothing passes between the two.  Both gather every row, the second of them
+// from L2.  (As a cluster that gathers half of the rows each and multicasts
+// them, a gather of four rows took the TMA unit 47 cycles, and 40 of them a tile
+// 1900; on its own one takes about 14.)
+//
+// What bounds it: the products of a tile are 18 of 34 cycles and 16 (fp32: 32)
+// of 48 (they read shared memory at its full rate), 1400 cycles (fp32 2150),
+// against 1600 for a tile's bytes at the measured bandwidth where one CTA has
+// them, 800 where two do.  What is measured is 2000 to 2700 cycles a tile: a
+// tile's place in shared memory, of which there are four, is taken for 2500
+// cycles of gathers, 1000 of scores, 2500 (fp32 3800) of softmax and 1500 of
+// sums.  So the softmax's chain is cut where it can be: two crews of warps have
+// every second tile each; rows' numbers arrive with the scores; and O follows a
+// moved reference by other warps' hands.  (Two crews instead of one that begins a
+// tile's scores before the weights of the one before: 27.5 -> 25.6 us of 64
+// requests of 512..4096 rows, 16 heads, bf16 out.  One warp that issues both
+// products can keep A of a block's parts in the collector buffer, 35 cycles a
+// product: 263 -> 256 us of 256 requests of 16..16384 rows, 128 heads, fp32 out,
+// but 24.5 -> 25.6 us of the former, as it has more to wait for at a time.  Five
+// places for tiles where they fit: 25.1 us.)
+//
+// Those two batches take 24.5 us (2.6 TB/s) and 263 us (0.64 PFLOP/s of the
+// formula's operations), kernels before and after included.
 //
 // A kernel before this one splits each request's query into its parts, once for
 // all items (in here a warp took 20000 cycles an item for it), in the order in
@@ -45,19 +59,16 @@
 // TMEM (512 columns): O^T [0, 256), the query [256, 384), two score buffers.
 //
 // Warps:
-//   0-15   softmax.  A thread of lane quadrant q reads its part (hi: q < 2) of a
-//          head's scores for 16 rows, exchanges half of them with the thread that
-//          has the other part, and goes on with 8 rows.  (Most of a tile's softmax
-//          is latency, and code that runs once a tile: twice the warps with half
-//          of the rows each take less than half as long.)
-//   16-23  the next item's query (half of its parts in registers while the item
-//          before is worked on; then into TMEM and shared memory), and the output
-//          of the item before
-//   24     TMEM allocator, issuer of both products
-//   25-28  gathers of the latents, an atom each: 16 of four rows a tile (a warp
+//   0-15   softmax, two crews.  A thread of a head's hi or lo part reads 32 rows'
+//          scores, gives half of them to the thread of the other part and goes
+//          on with 16 rows (at most 32 heads a CTA: quadrants 2 and 3 hold the
+//          heads of 0 and 1 once more, and a thread has half as many)
+//   16-23  the next item's query; O into new references' units; and the output
+//   24     issuer of the scores     25  TMEM allocator, issuer of the weighted sums
+//   26-29  gathers of the latents, an atom each: 16 of four rows a tile (a warp
 //          takes some 60 cycles for each of a burst, so they are spread)
-//   29     gathers of the rope keys
-//   30     the numbers made of the rows' scales
+//   30     gathers of the rope keys
+//   31     the numbers made of the rows' scales
 #include "mla_device.cuh"
 #include "mla_launch.h"
 
@@ -66,39 +77,41 @@ namespace rows8 {
 
 constexpr int T = 64;                                // rows of a tile
 constexpr int kSoftWarps = 16, kQueryWarps = 8;
-constexpr int kQueryWarp0 = 16, kMmaWarp = 24, kLatentWarp0 = 25, kRopeWarp = 29, kScaleWarp = 30;
-constexpr int kThreads = 31 * 32;
+constexpr int kQueryWarp0 = 16, kQkWarp = 24, kPvWarp = 25, kLatentWarp0 = 26, kRopeWarp = 30, kScaleWarp = 31;
+constexpr int kThreads = 32 * 32;
 constexpr int kAtom = T * 128;                       // 64 rows x 128 dims
 constexpr int kRopeOff = 4 * kAtom;
 constexpr int kUnit = 4 * kAtom + T * 64;            // a tile: 36 KB
 constexpr int kQr = 128 * 64;                        // rope query: [hi; lo] x 64 dims (64-byte swizzle)
 constexpr int kPPair = 64 * 128;                     // two parts of the weights: 64 heads x (64 + 64) rows
 constexpr int kImage = 2 * kRow;                     // bytes of a head's query: hi and lo codes
-constexpr int kXBytes = kSoftWarps * 32 * 32;        // scores on their way to the thread of the other part, of a tile
-constexpr int kPSlots = 3;                           // tiles whose weights are held
+constexpr int kCrews = 2, kCrewWarps = kSoftWarps / kCrews;   // a crew has every second tile
 constexpr int kScSlots = 4;                          // tiles whose rows' numbers are held
 constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the scales, reciprocals
 constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
 constexpr float kLoWeight = 1.f / 32.f;              // value of a query's lo part
 constexpr float kTop = 5.f, kLag = 3.75f;            // weights are 2^(e - m + kTop) with e <= m + kLag: to 431 of 448
-constexpr int kBarPair0 = 1, kBarTeam = 9, kBarVote = 11, kBarGather = 13;  // named barriers
+constexpr int kBarCrew0 = 1, kBarGather = 9;   // named barriers
 constexpr int kTmO = 0, kTmQ = 256, kTmS = 384;
 constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);
 
-template <bool kFine>
+template <bool kFine, bool kFew>
 struct Cfg {
   static constexpr int kPairs = kFine ? 2 : 1;       // pairs of weight parts
   static constexpr int kUnits = 4;
+  static constexpr int kPSlots = 3;                  // tiles whose weights are held
+  static constexpr int kGroups = kFew ? 2 : 4;       // of 16 heads
   static constexpr int kPBuf = kPairs * kPPair;
+  static constexpr int kRows = kFew ? 8 : 16;        // rows of a tile that a softmax thread has
   static constexpr int kOffQr = kUnits * kUnit;
   static constexpr int kOffP = kOffQr + kQr;
-  static constexpr int kOffX = kOffP + kPSlots * kPBuf;
-  static constexpr int kOffSc = kOffX + kXBytes;
-  static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [8][64] maxima, or sums
-  static constexpr int kOffBc = kOffRed + 8 * 64 * 4;           // [kUnits][64] a tile's rescaling factors
-  static constexpr int kOffSum = kOffBc + kUnits * 64 * 4;      // [2][64] an item's sums, for the output
-  static constexpr int kOffRef = kOffSum + 2 * 64 * 4;          // [2][64] and references
-  static constexpr int kOffSlots = kOffRef + 2 * 64 * 4;        // [5][64] a tile's slots, for each gathering warp
+  static constexpr int kOffSc = kOffP + kPSlots * kPBuf;
+  static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [kCrews][256] maxima, or sums
+  static constexpr int kOffBc = kOffRed + kCrews * 256 * 4;      // [kUnits][64] a tile's rescaling factors
+  static constexpr int kOffSum = kOffBc + kUnits * 64 * 4;      // [2][kCrews][64] an item's sums, for the output
+  static constexpr int kOffRef = kOffSum + 2 * kCrews * 64 * 4; // [2][kCrews][64] and references
+  static constexpr int kOffNow = kOffRef + 2 * kCrews * 64 * 4; // [64] the references as the last tile left them
+  static constexpr int kOffSlots = kOffNow + 64 * 4;            // [5][64] a tile's slots, for each gathering warp
   static constexpr int kOffBar = kOffSlots + 5 * T * 4;
   static constexpr int bFull = 0;                    // [kUnits] a tile's rows have landed
   static constexpr int bEmpty = bFull + kUnits;      // [kUnits]
@@ -118,9 +131,9 @@ struct Cfg {
   static constexpr int kOffMoved = kOffMisc + 8;     // [kUnits][2] heads whose reference a tile moved
   static constexpr int kOffLast = kOffMoved + kUnits * 8;       // [kUnits] last armed use
   static constexpr int kOffItems = (kOffLast + 4 * kUnits + 15) / 16 * 16;
-  static constexpr int kSmemBytes = kOffItems + 16 * kItemCache + 1024;
+  static constexpr int kSmemBytes = kOffItems + 16 * kItemCache;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
-  static_assert(kUnit % 1024 == 0 && kOffQr % 1024 == 0 && kOffP % 1024 == 0 && kOffX % 16 == 0 && kOffBar % 8 == 0,
+  static_assert(kUnit % 1024 == 0 && kOffQr % 1024 == 0 && kOffP % 1024 == 0 && kOffBar % 8 == 0,
                 "alignment");
 };
 
@@ -193,12 +206,10 @@ template <bool kFine, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1)
     rows8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const DecodeParams p, const Fp8Params p8) {
-  using C = Cfg<kFine>;
+  using C = Cfg<kFine, kFew>;
   const float* __restrict__ kv_scales = p8.kv_scales;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int shift = p.heads > 32 ? 1 : 0;            // a worker's CTAs: two, or one that takes all heads
   const int cta = blockIdx.x & shift;                // which of them
@@ -215,18 +226,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(C::bQFull), kQueryWarps);
     mbar_init(bar(C::bQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::bSFull + i), 2); mbar_init(bar(C::bSEmpty + i), kSoftWarps);
-      mbar_init(bar(C::bSumFull + i), kFew ? 1 : 2); mbar_init(bar(C::bSumEmpty + i), kQueryWarps);
+      mbar_init(bar(C::bSFull + i), 2); mbar_init(bar(C::bSEmpty + i), kCrewWarps);
+      mbar_init(bar(C::bSumFull + i), kCrews * C::kGroups); mbar_init(bar(C::bSumEmpty + i), kQueryWarps);
     }
-    for (int i = 0; i < kPSlots; ++i) mbar_init(bar(C::bPFull + i), kSoftWarps);
-    for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bVoted + i), kFew ? 1 : 2); mbar_init(bar(C::bFixed + i), kQueryWarps); }
+    for (int i = 0; i < C::kPSlots; ++i) mbar_init(bar(C::bPFull + i), kCrewWarps);
+    for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bVoted + i), C::kGroups); mbar_init(bar(C::bFixed + i), kQueryWarps); }
     mbar_init(bar(C::bOFull), 1);
-    mbar_init(bar(C::bDrain), 1);
+    mbar_init(bar(C::bDrain), 2);
     for (int i = 0; i < C::kUnits; ++i) last_armed[i] = -1;
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kPvWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -381,12 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u >= 0) drain_wait(bar(C::bFull + lane), u & 1);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kQkWarp) {
     // -------------------------------------------------------------- products
     // The whole warp runs the loop and one elected lane issues, so that
-    // descriptors and counters stay in uniform registers.  Both kinds are one
-    // warp's: the parts of a block's sum share A in the collector buffer, and
-    // nothing may come between them.  It takes whichever is ready, scores first.
+    // descriptors and counters stay in uniform registers.
     const bool lead = elect_one();
     auto D = [](uint64_t d, uint32_t byte_off) -> uint64_t { return d + (byte_off >> 4); };
     const uint64_t dk = sdesc(base, 16, 1024), dv = sdesc(base, kAtom, 1024);
@@ -396,41 +405,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cols = (Hc + 15) & ~15;                // columns that hold heads
     const uint32_t idesc4 = idesc_e4m3(128, cols, true, false);
     const uint32_t idesc5 = idesc_f8(kFmtE4M3, kFmtE5M2, 128, cols, true, false);
-    struct Cursor {                                  // a tile: the g-th, left tiles of its item with it
-      int it, left;
-      uint32_t g, nitem;
-      bool first;
-    };
-    auto enter = [&](Cursor& c) {                    // the next usable item
-      for (; c.it < it1; ++c.it) {
-        const int b = item_w(c.it, 0), s = item_w(c.it, 1), e = item_w(c.it, 2);
-        if (!item_ok(p, nnz, b, s, e)) continue;
-        c.left = (e - s + T - 1) / T;
-        c.first = true;
-        return;
-      }
-    };
-    auto next = [&](Cursor& c) {
-      ++c.g;
-      c.first = false;
-      if (--c.left == 0) {
-        ++c.it;
-        ++c.nitem;
-        enter(c);
-      }
-    };
-    auto ready = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar(i), parity)); };
-    Cursor qk{it0, 0, 0, 0, false}, pv{it0, 0, 0, 0, false};
-    enter(qk);
-    enter(pv);
-    uint64_t t0 = 0;
-    int idle = 0;
-    while (pv.it < it1) {
-      bool some = false;
-      if (qk.it < it1) {
-        const uint32_t g = qk.g, buf = g & 1, slot = g % C::kUnits;
-        if (ready(C::bFull + slot, (g / C::kUnits) & 1) && (g < 2 || ready(C::bSEmpty + buf, ((g >> 1) - 1) & 1)) &&
-            (!qk.first || ready(C::bQFull, qk.nitem & 1))) {
+    uint32_t g = 0, nitem = 0, slot = 0, lap = 0;
+    bool ok = true;
+    for (int it = it0; it < it1 && ok; ++it) {
+      const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
+      if (!item_ok(p, nnz, b, s, e)) continue;
+      const int nt = (e - s + T - 1) / T;
+      if (warp == kQkWarp) ok = mbar_wait(bar(C::bQFull), nitem & 1, wc);
+      for (int j = 0; j < nt && ok; ++j, ++g) {
+        const uint32_t buf = g & 1;
+        if (warp == kQkWarp) {
+          ok = (g < 2 || mbar_wait(bar(C::bSEmpty + buf), ((g >> 1) - 1) & 1, wc)) && mbar_wait(bar(C::bFull + slot), lap, wc);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t d_s = tmem + kTmS + buf * T;
           const uint64_t bk = D(dk, slot * kUnit), br = D(dr, slot * kUnit);
@@ -441,15 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 2; ++k) umma_ss_f8(d_s, D(dq, 32 * k), D(br, 32 * k), kIdescQK, 1u);
             umma_commit(bar(C::bSFull + buf));
-            if (qk.left == 1) umma_commit(bar(C::bQEmpty));
+            if (j == nt - 1) umma_commit(bar(C::bQEmpty));
           }
-          next(qk);
-          some = true;
-        }
-      }
-      if (pv.g < qk.g) {
-        const uint32_t g = pv.g, slot = g % C::kUnits, ps = g % kPSlots;
-        if (ready(C::bPFull + ps, (g / kPSlots) & 1) && ready(C::bFixed + slot, (g / C::kUnits) & 1)) {
+        } else {
+          const uint32_t ps = g % C::kPSlots;
+          ok = mbar_wait(bar(C::bFixed + slot), lap, wc) && mbar_wait(bar(C::bPFull + ps), (g / C::kPSlots) & 1, wc);
+          if (!ok) break;
           tc_fence_after();
           const uint64_t av = D(dv, slot * kUnit), bp = D(dp, ps * C::kPBuf);
           if (lead) {
@@ -459,34 +442,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int ks = 0; ks < 2; ++ks) {       // 32 rows
                 const uint64_t a = D(av, mb * kAtom + 4096 * ks);
                 const uint32_t d = tmem + kTmO + 64 * mb;
-                umma_ss_f8_run<ARun::kFirst>(d, a, D(bp, 32 * ks), idesc4, (pv.first && ks == 0) ? 0u : 1u);
+                umma_ss_f8(d, a, D(bp, 32 * ks), idesc4, (j == 0 && ks == 0) ? 0u : 1u);
+                umma_ss_f8(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
                 if constexpr (kFine) {
-                  umma_ss_f8_run<ARun::kMid>(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
-                  umma_ss_f8_run<ARun::kLast>(d, a, D(bp, kPPair + 32 * ks), idesc4, 1u);
+                  umma_ss_f8(d, a, D(bp, kPPair + 32 * ks), idesc4, 1u);
                   umma_ss_f8(d, a, D(bp, kPPair + 64 + 32 * ks), idesc5, 1u);
-                } else {
-                  umma_ss_f8_run<ARun::kLast>(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
                 }
               }
             umma_commit(bar(C::bEmpty + slot));
-            if (pv.left == 1) umma_commit(bar(C::bOFull));
+            if (j == nt - 1) umma_commit(bar(C::bOFull));
           }
-          next(pv);
-          some = true;
+        }
+        if (++slot == static_cast<uint32_t>(C::kUnits)) {
+          slot = 0;
+          lap ^= 1;
         }
       }
-      if (some) {
-        idle = 0;
-      } else if ((++idle & 255) == 0) {              // a bounded wait, as in mbar_wait
-        const uint64_t t = globaltimer();
-        if (idle == 256) t0 = t;
-        if (__any_sync(0xffffffffu, t - t0 > MLA_WAIT_LIMIT_NS)) {
-          *abort_flag = 1;
-          if (lane == 0) record_status(p.status, MLA_ERR_TIMEOUT);
-          break;
-        }
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-      }
+      ++nitem;
     }
     if (lead) {
       umma_commit(bar(C::bDrain));
@@ -495,16 +467,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kQueryWarp0) {
     // ------------------------------------------- the items' queries and outputs
-    // Query: row 32 q + lane of A is part q / 2 of head 32 (q % 2) + lane (kFew: of
-    // head lane); two warps share a quadrant, each 256 latent and 32 rope dims of
-    // its rows.  Output: dims 32 q + lane of every block of 128, heads 32 half ..
+    // Query: of quadrant q of A, rows 0-15 are the hi parts of heads 16 q .. and rows
+    // 16-31 their lo parts (kFew: of heads 16 (q % 2) ..); two warps share a
+    // quadrant, each 256 latent and 32 rope dims of its rows.  Output: dims 32 q + lane of every block of 128, heads 32 half ..
     // of the CTA's (kFew: of blocks 2 half and 2 half + 1, all heads).
     const int q = warp & 3, half = (warp >> 2) & 1;
-    const int row = 32 * q + lane, hl = kFew ? lane : row & 63;
+    const int row = 32 * q + lane, hl = 16 * (kFew ? q & 1 : q) + (lane & 15);
     const int h0 = kFew ? 0 : 32 * half;
     constexpr int kBlocks = kFew ? 2 : 4;            // of the output's 128 dims
     const int block0 = kFew ? 2 * half : 0;
-    const bool lo = q >= 2, head_ok = hl < Hc;
+    const bool lo = lane >= 16, head_ok = hl < Hc;
     auto wait = [&](uint32_t bb, uint32_t par) {
       if (!aborted && !__all_sync(0xffffffffu, mbar_wait(bb, par, wc))) aborted = true;
     };
@@ -553,8 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool part_ok = dest < p.max_partials;    // a device-only plan naming a partial past the workspace
       if (!part_ok && warp == kQueryWarp0 && lane == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
       wait(bar(C::bSumFull + (nitem & 1)), (nitem >> 1) & 1);
-      const float l = reinterpret_cast<const float*>(smem + C::kOffSum)[64 * (nitem & 1) + h0 + lane];
-      const float ref = reinterpret_cast<const float*>(smem + C::kOffRef)[64 * (nitem & 1) + h0 + lane];
+      const float* sums = reinterpret_cast<const float*>(smem + C::kOffSum) + 64 * kCrews * (nitem & 1) + h0 + lane;
+      const float* refs = reinterpret_cast<const float*>(smem + C::kOffRef) + 64 * kCrews * (nitem & 1) + h0 + lane;
+      const float ref = fmaxf(refs[0], refs[64]);    // the last tile's
+      const float l = fmaf(sums[0], ex2_approx(refs[0] - ref), sums[64] * ex2_approx(refs[64] - ref));
       const float inv = l > 0.f ? 1.f / l : 0.f;     // of head h0 + lane
       __syncwarp();
       if (lane == 0 && !aborted) mbar_arrive(bar(C::bSumEmpty + (nitem & 1)));
@@ -651,86 +625,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ----------------------------------------------------------------- softmax
-    // The warps of heads 0-31 and those of heads 32-63 go on by themselves.  With
-    // kFew quadrants 1 and 3 hold the heads of 0 and 2 once more, and their warps
-    // take half of the rows.
-    constexpr int kTeams = kFew ? 1 : 2, kRows = kFew ? 4 : 8, kShare = T / kRows;   // threads that share a head
-    const int q = warp & 3, th = warp >> 2, part = q >> 1;
-    const int team = kFew ? 0 : q & 1;
-    const int hl = 32 * team + lane;                 // head of this CTA
-    const int eight = kFew ? 4 * th + 2 * (q & 1) + part : 2 * th + part;   // which kRows rows of a tile
+    // Two crews, a tile each in turn: a tile is a chain of waits and exchanges,
+    // and two of them at once fill each other's.  What passes from a tile to the
+    // next is the heads' references.  A group of 16 heads is a quadrant's, and goes
+    // on by itself; with kFew quadrants 2 and 3 hold the heads of 0 and 1 once more,
+    // and their warps take half of the rows.
+    constexpr int kRows = C::kRows, kShare = T / kRows, kHeads = 16 * C::kGroups;  // kShare threads have a head
+    constexpr int kMeet = 32 * kCrewWarps / C::kGroups;                            // threads of a group
+    const int q = warp & 3, crew = warp >> 3, th = (warp >> 2) & 1, part = lane >> 4;
+    const int group = kFew ? q & 1 : q;
+    const int hl = 16 * group + (lane & 15);         // head of this CTA
+    const int share = kFew ? 4 * th + 2 * (q >> 1) + part : 2 * th + part;         // which kRows rows of a tile
+    const bool first = th == 0 && (!kFew || q < 2);  // the warp that speaks for its group (lanes 0-15: share 0)
+    const int meet = kBarCrew0 + C::kGroups * crew + group;
     const uint32_t quad = static_cast<uint32_t>(32 * q) << 16;
-    float* red = reinterpret_cast<float*>(smem + C::kOffRed);
-    volatile uint32_t* moved_of = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMoved);   // heads to rescale
-    float m_ref = 0.f, l_sum = 0.f, fac = 1.f;
+    float* red = reinterpret_cast<float*>(smem + C::kOffRed) + 256 * crew;
+    volatile float* now = reinterpret_cast<volatile float*>(smem + C::kOffNow);
+    volatile uint16_t* moved_of = reinterpret_cast<volatile uint16_t*>(smem + C::kOffMoved);   // heads to rescale
     auto wait = [&](uint32_t bb, uint32_t par) {     // (every lane for itself: a third of the time of one for all)
       if (!aborted && !__all_sync(0xffffffffu, mbar_wait(bb, par, wc))) aborted = true;
-    };
-    // the largest of this head's values, of the threads that share it (who have voted since they read the last)
-    auto largest = [&](float v) -> float {
-      float* r = red;
-      r[eight * 32 * kTeams + hl] = v;
-      named_bar_sync(kBarTeam + team, 32 * kSoftWarps / kTeams);
-#pragma unroll
-      for (int i = 0; i < kShare; i += 2) v = max3(v, r[i * 32 * kTeams + hl], r[(i + 1) * 32 * kTeams + hl]);
-      return v;
-    };
-    uint32_t kept[kRows];                            // this part's scores of a tile's kRows rows, on their way
-    float2 x[kRows / 2];                             // exponents of a tile's kRows rows
-    // Scores of tile g, from TMEM: the thread of the hi part keeps the first half of 2 kRows and sends the others, that
-    // of the lo part the other way round.  (What was sent last has been read: the other thread has voted since.)
-    auto load_scores = [&](uint32_t g) {
-      wait(bar(C::bSFull + (g & 1)), (g >> 1) & 1);
-      uint32_t sent[kRows];
-      if (!aborted) {
-        tc_fence_after();
-        const uint32_t ts = tmem + quad + kTmS + T * (g & 1) + kRows * eight;
-        if constexpr (kFew) {
-          tmem_ld4(ts + 4 - 8 * part, sent);
-          tmem_ld4(ts, kept);
-        } else {
-          tmem_ld8(ts + 8 - 16 * part, sent);
-          tmem_ld8(ts, kept);
-        }
-        tmem_wait_ld();
-      } else {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) kept[i] = sent[i] = 0;
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0 && !aborted) mbar_arrive(bar(C::bSEmpty + (g & 1)));
-      uint4* xo = reinterpret_cast<uint4*>(smem + C::kOffX) + warp * 64 + lane;
-#pragma unroll
-      for (int k = 0; k < kRows / 4; ++k) xo[32 * k] = make_uint4(sent[4 * k], sent[4 * k + 1], sent[4 * k + 2], sent[4 * k + 3]);
-    };
-    // the other part's scores and the exponents; their largest
-    const float w_own = part == 0 ? 1.f : kLoWeight, w_other = part == 0 ? kLoWeight : 1.f;
-    auto exponents = [&](uint32_t g, int left) -> float {
-      named_bar_sync(kBarPair0 + 4 * (q & 1) + th, 64);
-      const float4* xi = reinterpret_cast<const float4*>(smem + C::kOffX) + (warp ^ 2) * 64 + lane;
-      const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + kRows / 4 * eight;
-      const float2 f_own = f2_pack(fac * w_own, fac * w_own), f_other = f2_pack(fac * w_other, fac * w_other);
-#pragma unroll
-      for (int k = 0; k < kRows / 4; ++k) {
-        const float4 o = xi[32 * k], f = sc[k], lg = sc[T / 4 + k];
-        float2 t = f2_mul(f2_pack(__uint_as_float(kept[4 * k]), __uint_as_float(kept[4 * k + 1])), f_own);
-        x[2 * k] = f2_fma(f2_fma(f2_pack(o.x, o.y), f_other, t), f2_pack(f.x, f.y), f2_pack(lg.x, lg.y));
-        t = f2_mul(f2_pack(__uint_as_float(kept[4 * k + 2]), __uint_as_float(kept[4 * k + 3])), f_own);
-        x[2 * k + 1] = f2_fma(f2_fma(f2_pack(o.z, o.w), f_other, t), f2_pack(f.z, f.w), f2_pack(lg.z, lg.w));
-      }
-      const int nvalid = left - kRows * eight;
-      if (nvalid < kRows) {
-#pragma unroll
-        for (int i = 0; i < kRows / 2; ++i) {
-          if (2 * i >= nvalid) x[i].x = -INFINITY;
-          if (2 * i + 1 >= nvalid) x[i].y = -INFINITY;
-        }
-      }
-      float m = fmaxf(x[0].x, x[0].y);
-#pragma unroll
-      for (int i = 1; i < kRows / 2; ++i) m = max3(m, x[i].x, x[i].y);
-      return m;
     };
     griddep_wait();                                  // the factors come from the kernel before
     // 2^-a of this head in the next usable item from `it` on, loaded while the item before is worked on
@@ -742,40 +655,99 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return 1.f;
     };
+    const float w_own = part == 0 ? 1.f : kLoWeight, w_other = part == 0 ? kLoWeight : 1.f;
     float fac_next = factor(it0);
-    uint32_t g = 0, nitem = 0;
+    uint32_t g0 = 0, nitem = 0;                      // the item's first tile
     for (int it = it0; it < it1; ++it) {
       const int b = item_w(it, 0), s = item_w(it, 1), e = item_w(it, 2);
       if (!item_ok(p, nnz, b, s, e)) continue;
       const int n = e - s, nt = (n + T - 1) / T;
-      fac = fac_next;
+      const float fac = fac_next;
       fac_next = factor(it + 1);
-      l_sum = 0.f;
-      m_ref = -INFINITY;                             // (the first tile asks for a reference)
-      load_scores(g);
-      float mx = exponents(g, n);
-      for (int j = 0; j < nt; ++j, ++g) {
-        const bool moved = named_bar_or(kBarVote + team, 32 * kSoftWarps / kTeams, mx > m_ref + kLag);
-        uint32_t which = 0;                          // heads whose O has to follow
-        if (moved) {                                 // some head's reference moves
-          const float mt = largest(mx);
-          const float mn = mt > m_ref + kLag ? mt : m_ref;
-          const float alpha = mn == m_ref ? 1.f : ex2_approx(m_ref - mn);
-          m_ref = mn;
-          l_sum *= alpha;
-          if (eight == 0) {
-            reinterpret_cast<float*>(smem + C::kOffBc)[64 * (g % C::kUnits) + hl] = alpha;
-            which = __ballot_sync(0xffffffffu, alpha != 1.f && hl < Hc);
+      float l_sum = 0.f, m_own = -INFINITY;          // this thread's sum, in the units of that reference
+      for (int j = (g0 ^ crew) & 1; j < nt; j += kCrews) {
+        const uint32_t g = g0 + j;
+        // Scores, from TMEM: of 2 kRows rows the thread of the hi part goes on with the first half and gives the
+        // second to that of the lo part, 16 lanes on, and gets the lo part's share of its own.
+        uint32_t v0[kRows], v1[kRows];
+        wait(bar(C::bSFull + (g & 1)), (g >> 1) & 1);
+        if (!aborted) {
+          tc_fence_after();
+          const uint32_t ts = tmem + quad + kTmS + T * (g & 1) + kRows * (share - part);
+          if constexpr (kFew) {
+            tmem_ld8(ts, v0);
+            tmem_ld8(ts + 8, v1);
+          } else {
+            tmem_ld16(ts, v0);
+            tmem_ld16(ts + 16, v1);
+          }
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) v0[i] = v1[i] = 0;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && !aborted) mbar_arrive(bar(C::bSEmpty + (g & 1)));
+        // the exponents and their largest
+        float2 x[kRows / 2];
+        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + kRows / 4 * share;
+        const float2 f_own = f2_pack(fac * w_own, fac * w_own), f_other = f2_pack(fac * w_other, fac * w_other);
+        auto score = [&](int i) -> float2 {          // rows i and i + 1
+          auto own = [&](int k) { return __uint_as_float(part ? v1[k] : v0[k]); };
+          auto other = [&](int k) { return __shfl_xor_sync(0xffffffffu, __uint_as_float(part ? v0[k] : v1[k]), 16); };
+          const float a = own(i), b = own(i + 1), c = other(i), d = other(i + 1);
+          return f2_fma(f2_pack(c, d), f_other, f2_mul(f2_pack(a, b), f_own));
+        };
+#pragma unroll
+        for (int k = 0; k < kRows / 4; ++k) {
+          const float4 f = sc[k], lg = sc[T / 4 + k];
+          x[2 * k] = f2_fma(score(4 * k), f2_pack(f.x, f.y), f2_pack(lg.x, lg.y));
+          x[2 * k + 1] = f2_fma(score(4 * k + 2), f2_pack(f.z, f.w), f2_pack(lg.z, lg.w));
+        }
+        const int nvalid = n - j * T - kRows * share;
+        if (nvalid < kRows) {
+#pragma unroll
+          for (int i = 0; i < kRows / 2; ++i) {
+            if (2 * i >= nvalid) x[i].x = -INFINITY;
+            if (2 * i + 1 >= nvalid) x[i].y = -INFINITY;
           }
         }
-        if (eight == 0) {                            // (a warp of the team)
-          if (lane == 0) moved_of[2 * (g % C::kUnits) + team] = j > 0 ? which : 0;
+        float mx = fmaxf(x[0].x, x[0].y);
+#pragma unroll
+        for (int i = 1; i < kRows / 2; ++i) mx = max3(mx, x[i].x, x[i].y);
+        // The references, as the tile before left them.  (This one's are written after its threads have met, and so
+        // after the other crew's have read theirs: its own tile before this one waited for that.)
+        if (g > 0) wait(bar(C::bVoted + (g - 1) % C::kUnits), ((g - 1) / C::kUnits) & 1);
+        const float m_old = j > 0 ? now[hl] : -INFINITY;
+        float m_ref = m_old;
+        uint32_t which = 0;                          // heads whose O has to follow
+        if (named_bar_or(meet, kMeet, j == 0 || mx > m_old + kLag)) {   // some head's reference moves
+          red[share * kHeads + hl] = mx;             // (the last maxima there have been read: all have met since)
+          named_bar_sync(meet, kMeet);
+          float mt = mx;
+#pragma unroll
+          for (int i = 0; i < kShare; i += 2) mt = max3(mt, red[i * kHeads + hl], red[(i + 1) * kHeads + hl]);
+          if (mt > m_old + kLag) m_ref = mt;
+          if (first) {
+            const float alpha = m_ref == m_old ? 1.f : ex2_approx(m_old - m_ref);
+            if (part == 0) {
+              reinterpret_cast<float*>(smem + C::kOffBc)[64 * (g % C::kUnits) + hl] = alpha;
+              now[hl] = m_ref;
+            }
+            which = __ballot_sync(0xffffffffu, part == 0 && alpha != 1.f && hl < Hc);
+          }
+        }
+        if (first) {
+          if (lane == 0) moved_of[4 * (g % C::kUnits) + group] = static_cast<uint16_t>(j > 0 ? which : 0);
           __syncwarp();
           if (lane == 0 && !aborted) mbar_arrive(bar(C::bVoted + g % C::kUnits));
         }
-        if (j + 1 < nt) load_scores(g + 1);
+        if (m_ref != m_own) {
+          l_sum *= ex2_approx(m_own - m_ref);
+          m_own = m_ref;
+        }
         // weights and their parts
-        const float4* sc = reinterpret_cast<const float4*>(smem + C::kOffSc + (g % kScSlots) * kScSlot) + kRows / 4 * eight;
         uint32_t w0[kRows / 4], w1[kRows / 4], w2[kRows / 4], w3[kRows / 4];
         const float2 shift = f2_pack(kTop - m_ref, kTop - m_ref);
         float2 l2 = f2_pack(0.f, 0.f);
@@ -809,18 +781,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         l_sum += l2.x + l2.y;
-        // The weights of tile g - 3 lay here.  Scores of tile g + 1 that are there say that its rows are, and these that
-        // the sum of g - 3, whose place they took, is done.
-        static_assert(C::kUnits == kPSlots + 1, "see above");
-        if (j + 1 == nt && g >= kPSlots)
-          wait(bar(C::bEmpty + (g - kPSlots) % C::kUnits), ((g - kPSlots) / C::kUnits) & 1);
+        const uint32_t ps = g % C::kPSlots;
+        if (g >= C::kPSlots)                         // the sum that used these weights' place
+          wait(bar(C::bEmpty + (g - C::kPSlots) % C::kUnits), ((g - C::kPSlots) / C::kUnits) & 1);
         if (!aborted) {
-          // byte kRows eight of the head's 64 (hi), then the same of the lo part: chunks c at c ^ (head mod 8)
-          uint8_t* row = smem + C::kOffP + (g % kPSlots) * C::kPBuf + hl * 128 + (kRows * eight & 15);
-          const int at = (th ^ (hl & 7)) << 4, at_lo = ((4 + th) ^ (hl & 7)) << 4;
+          // byte kRows share of the head's 64 (hi), then the same of the lo part: chunks c at c ^ (head mod 8)
+          uint8_t* row = smem + C::kOffP + ps * C::kPBuf + hl * 128 + (kRows * share & 15);
+          const int c = kRows * share >> 4, at = (c ^ (hl & 7)) << 4, at_lo = ((4 + c) ^ (hl & 7)) << 4;
           auto put = [&](int to, const uint32_t (&v)[kRows / 4]) {
-            if constexpr (kFew) *reinterpret_cast<uint32_t*>(row + to) = v[0];
-            else *reinterpret_cast<uint2*>(row + to) = make_uint2(v[0], v[1]);
+            if constexpr (kFew) *reinterpret_cast<uint2*>(row + to) = make_uint2(v[0], v[1]);
+            else *reinterpret_cast<uint4*>(row + to) = make_uint4(v[0], v[1], v[2], v[3]);
           };
           put(at, w0);
           put(at_lo, w1);
@@ -832,24 +802,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && !aborted) mbar_arrive(bar(C::bPFull + g % kPSlots));
-        if (j + 1 < nt) mx = exponents(g + 1, n - (j + 1) * T);
+        if (lane == 0 && !aborted) mbar_arrive(bar(C::bPFull + ps));
       }
-      // what the output needs
+      g0 += nt;
+      // what the output needs: each crew's sums, in the units of its last reference
       if (nitem >= 2) wait(bar(C::bSumEmpty + (nitem & 1)), ((nitem >> 1) - 1) & 1);
-      float* r = red;
-      named_bar_sync(kBarTeam + team, 32 * kSoftWarps / kTeams);
-      r[eight * 32 * kTeams + hl] = l_sum;
-      named_bar_sync(kBarTeam + team, 32 * kSoftWarps / kTeams);
-      if (eight == 0) {
+      named_bar_sync(meet, kMeet);
+      red[share * kHeads + hl] = l_sum;
+      named_bar_sync(meet, kMeet);
+      if (first) {
         float l = 0.f;
 #pragma unroll
-        for (int i = 0; i < kShare; ++i) l += r[i * 32 * kTeams + hl];
-        reinterpret_cast<float*>(smem + C::kOffSum)[64 * (nitem & 1) + hl] = l;
-        reinterpret_cast<float*>(smem + C::kOffRef)[64 * (nitem & 1) + hl] = m_ref;
+        for (int i = 0; i < kShare; ++i) l += red[i * kHeads + hl];
+        if (part == 0) {
+          reinterpret_cast<float*>(smem + C::kOffSum)[64 * (kCrews * (nitem & 1) + crew) + hl] = l;
+          reinterpret_cast<float*>(smem + C::kOffRef)[64 * (kCrews * (nitem & 1) + crew) + hl] = m_own;
+        }
+        __syncwarp();
+        if (lane == 0 && !aborted) mbar_arrive(bar(C::bSumFull + (nitem & 1)));
       }
-      __syncwarp();
-      if (eight == 0 && lane == 0 && !aborted) mbar_arrive(bar(C::bSumFull + (nitem & 1)));
       ++nitem;
     }
   }
@@ -857,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kPvWarp) tmem_dealloc(tmem, 512);
 }
 
 template <typename Kernel, typename... Args>
@@ -885,7 +856,8 @@ int launch_rows8(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const De
   const bool few = p.heads <= 64;                    // heads of a CTA <= 32
   const auto kernel = p.out_bf16 ? (few ? &rows8::rows8_kernel<false, true> : &rows8::rows8_kernel<false, false>)
                                  : (few ? &rows8::rows8_kernel<true, true> : &rows8::rows8_kernel<true, false>);
-  const int smem = p.out_bf16 ? rows8::Cfg<false>::kSmemBytes : rows8::Cfg<true>::kSmemBytes;
+  const int smem = p.out_bf16 ? (few ? rows8::Cfg<false, true>::kSmemBytes : rows8::Cfg<false, false>::kSmemBytes)
+                              : (few ? rows8::Cfg<true, true>::kSmemBytes : rows8::Cfg<true, false>::kSmemBytes);
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), smem)) return MLA_ERR_CUDA;
   // few enough blocks that the next kernel's fit beside them (it starts once all have)
   const int warps = rows8::kPrepThreads / 32, blocks = (pp.rows + warps - 1) / warps, held = 4 * ctas;

@@ -244,6 +244,34 @@ def test_decode_few_long_and_many_short(H, lens, half):
     _check(*_decode(codes, scales, lens, H, 6, dtype=torch.bfloat16 if half else torch.float32))
 
 
+@pytest.mark.parametrize("H,half", [(16, True), (64, False), (128, True), (128, False)])
+def test_decode_more_items_than_a_worker_keeps_at_hand(H, half):
+    torch, _ = _t()
+    lens = [3, 0, 130, 1, 64, 65, 2, 5] * 260
+    codes, scales = _cache(H, 90000, 6.0)
+    _check(*_decode(codes, scales, lens, H, 12, dtype=torch.bfloat16 if half else torch.float32))
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_decodes_on_two_streams_at_once(H):
+    torch, B = _t()
+    codes, scales = _cache(H, 30000, 3.0)
+    calls = [_decode(codes, scales, lens, H, 20 + i) for i, lens in enumerate(([700, 9, 4000], [2500, 64], [33] * 90))]
+    first = [(a[9].clone(), a[10].clone()) for a, _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for a, _ in calls:
+            a[9].fill_(float("nan"))
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in calls]
+        for st, (a, _) in zip(streams, calls):
+            B.decode_run_fp8_rows(*a, stream=st)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[9], o) and torch.equal(a[10], z) for (a, _), (o, z) in zip(calls, first))
+    for a, ip in calls:
+        _check(a, ip)
+
+
 @pytest.mark.parametrize("H", [32, 64])
 def test_decode_scales_outside_the_range(H):
     # zero, negative, NaN, infinite and subnormal scales are read as the nearest end; the rest of the batch is exact
