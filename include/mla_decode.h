@@ -492,7 +492,13 @@ int mla_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slots, c
  * mla_decode_run_fp8 over such a cache.
  *   kv_scales  device float32 [num_slots], 4-byte aligned; read at the slots
  *              that kv_indices names (at slot 0 for one outside the cache).
- *   all other arguments, plan, workspace and launches as for mla_decode_run_fp8.
+ *   all other arguments, plan and workspace as for mla_decode_run_fp8.
+ * Launches for every head count a kernel that prepares the queries, the decode
+ * kernel as its programmatic dependent, and the merge of mla_decode_run.  The
+ * weights are held to 8 significant bits for a bf16 out (or 2^-10 of a scale on
+ * which a head's largest is 32 or more), to 16 (or 2^-14) for a float32 out, and
+ * their sum is that of the unrounded ones; with a bf16 out split requests are
+ * merged from float32 states.
  * Errors as for mla_decode_run_fp8, and MLA_ERR_INVALID_ARG for a null or
  * misaligned kv_scales (not looked at when no request has a row). */
 int mla_decode_run_fp8_rows(const int32_t* plan_host, const int32_t* plan_dev, const void* q_nope, const void* q_rope,

