@@ -221,6 +221,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int w = blockIdx.x >> shift;
   const int Hc = p.heads >> shift;                   // this CTA's heads: [cta * Hc, (cta + 1) * Hc)
 
+  // the items' loads, one behind another, while barriers and TMEM are set up
+  const int nnz = __ldg(p.kv_indptr + p.batch);
+  int it0, it1;
+  plan_items(p, w, it0, it1);
+  const int32_t* items = p.plan + p.items_off;
+  int32_t* s_items = reinterpret_cast<int32_t*>(smem + C::kOffItems);
+  if (warp == kQueryWarp0) {
+    const int n_cached = min(max(it1 - it0, 0), kItemCache);
+    for (int i = lane; i < 4 * n_cached; i += 32) s_items[i] = items[4 * it0 + i];
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kUnits; ++i) { mbar_init(bar(C::bFull + i), 1); mbar_init(bar(C::bEmpty + i), 1); }
     mbar_init(bar(C::bQFull), kQueryWarps);
@@ -247,17 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int it0, it1;
-  plan_items(p, w, it0, it1);
-  const int32_t* items = p.plan + p.items_off;
-  int32_t* s_items = reinterpret_cast<int32_t*>(smem + C::kOffItems);
-  const int n_cached = min(max(it1 - it0, 0), kItemCache);
-  for (int i = threadIdx.x; i < 4 * n_cached; i += blockDim.x) s_items[i] = items[4 * it0 + i];
-  __syncthreads();
   auto item_w = [&](int it, int k) -> int {
     return it - it0 < kItemCache ? s_items[4 * (it - it0) + k] : items[4 * it + k];
   };
-  const int nnz = __ldg(p.kv_indptr + p.batch);
   griddep_launch_dependents();
   bool aborted = false;                              // of the softmax and query warps
 
