@@ -351,6 +351,46 @@ def test_decode_on_a_stream_and_replayed(H):
 
 # ---------------------------------------------------------------- as they are used
 
+def test_rows_past_four_gigabytes():
+    """The same rows in a small cache and at the end of one of 4.4 GB: appended, expanded, attended to, copied and
+    compacted, bit for bit."""
+    torch, B = _t()
+    g = _gen(31)
+    T, N, H = 500, 7_600_000, 16
+    rows, pos = _randn(g, T, 576).bfloat16(), torch.arange(T, dtype=torch.int32, device="cuda")
+    fr = B.rope_frequencies()
+    wk, wv = _randn(g, H, 128, 512).bfloat16(), _randn(g, H, 512, 128).bfloat16()
+    qn, qr = _randn(g, 2, H, 512).bfloat16(), _randn(g, 2, H, 64).bfloat16()
+    indptr = np.array([0, 470, T], dtype=np.int32)
+    plan = B.decode_plan(indptr, H)[0]
+    results = []
+    for n in (T, N):
+        slots = n - 1 - (n // T) * torch.arange(T, dtype=torch.int32, device="cuda")
+        codes = torch.zeros((n, 576), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(n, device="cuda")
+        B.rope_append_kv_fp8_rows(codes, scales, slots, rows, pos, fr)
+        k, v = (torch.empty((T, H, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        kr = torch.empty((T, 64), dtype=torch.bfloat16, device="cuda")
+        B.expand_kv_fp8_rows(codes, scales, slots, wk, wv, k, kr, v)
+        ws = torch.zeros(B.decode_fp8_workspace_bytes(plan), dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty((2, H, 512), device="cuda"), torch.empty((2, H), device="cuda")
+        B.decode_run_fp8_rows(plan, torch.from_numpy(plan).cuda(), qn, qr, codes, scales,
+                              torch.from_numpy(indptr).cuda(), slots, SM, out, lse, ws)
+        assert B.check_errors(ws) == 0
+        at = slots.long()
+        results.append((codes[at], scales[at], k, kr, v, out, lse))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    want, want_s = results[0][:2]
+    other = slots - 1                                # free slots among them
+    B.copy_rows(codes, slots, codes, other, src_scales=scales, dst_scales=scales)
+    assert torch.equal(codes[other.long()], want) and torch.equal(scales[other.long()], want_s)
+    ws = torch.zeros(B.slots_workspace_bytes(N), dtype=torch.uint8, device="cuda")
+    new, live = torch.empty_like(other), torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.compact_cache(codes, torch.tensor([0, T], dtype=torch.int32, device="cuda"), other, new, live, ws, kv_scales=scales)
+    assert B.check_errors(ws) == 0 and int(live) == T and int(new.max()) < T
+    assert torch.equal(codes[new.long()], want) and torch.equal(scales[new.long()], want_s)
+
+
 @pytest.mark.parametrize("H", [16, 128])
 def test_a_prompt_and_its_next_step(H):
     """Rows appended, expanded and attended to in both forms: the absorbed decode of the last token and the expanded
