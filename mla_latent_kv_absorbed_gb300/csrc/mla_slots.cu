@@ -373,7 +373,10 @@ __global__ void __launch_bounds__(kScanThreads) compact_scan_kernel(const Compac
       c.live[w0 + i] = make_uint2(m, static_cast<uint32_t>(run));
       if (w0 + i == last_word) c.counts[1] = n - run - __popc(m & ((1u << (n & 31)) - 1));
     }
-    for (uint32_t todo = __ballot_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
+    // (nothing comes of full words below n and of empty ones past it: a pool that is mostly in order)
+    const long long s0 = 32 * (w0 + i);
+    const bool some = mine && (s0 + 32 <= n ? m != 0xFFFFFFFFu : s0 < n || m != 0);
+    for (uint32_t todo = __ballot_sync(0xffffffffu, some); todo; todo &= todo - 1) {
       const int from = __ffs(todo) - 1;
       const uint32_t word = __shfl_sync(0xffffffffu, m, from);
       const int before = __shfl_sync(0xffffffffu, run, from) + __popc(word & ((1u << lane) - 1));   // live slots
