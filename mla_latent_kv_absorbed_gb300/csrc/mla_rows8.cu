@@ -146,31 +146,37 @@ __device__ __forceinline__ bool item_in_request(const DecodeParams& p, int b, in
 }
 
 // ------------------------------------------------------------ query parts --
-// One warp a head: lane l has latent dims 16 l .. and, of lanes 0-3, rope dims
-// 16 l ..; q' = q 2^a, hi = e4m3(q'), lo = e4m3(32 (q' - hi)).  A CTA's image is
-// 36 pieces of 16 dims, each with the hi and then the lo codes of its heads.
-// Bound: launch and a round trip, or for large batches HBM.
-constexpr int kPrepThreads = 256;
+// One warp a head, eight heads a block: lane l has latent dims 16 l .. and rope
+// dims 2 l ..; q' = q 2^a, hi = e4m3(q'), lo = e4m3(32 (q' - hi)).  A CTA's image is 36 pieces of 16 dims, each with the hi and then the lo
+// codes of its heads; the block's eight heads of a piece go out together, 128
+// bytes (one by one, half sectors, the ragged batch's took 20 us).  Bound: launch
+// and a round trip, or for large batches HBM: 32768
+// heads take 14.8 us (5.1 TB/s read and written).
+constexpr int kPrepWarps = 8, kPrepThreads = 32 * kPrepWarps;
 __global__ void __launch_bounds__(kPrepThreads) rows8_prep_kernel(const Fp8PrepParams p, int heads) {
-  const int lane = threadIdx.x & 31, warps = gridDim.x * (kPrepThreads / 32), Hc = heads > 32 ? heads >> 1 : heads;
+  constexpr int kCodes = 2 * kRow / 16, kPitch = kPrepWarps + 1;               // (a piece of padding: bank conflicts)
+  __shared__ uint4 stage[2][kCodes * kPitch];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hc = heads > 32 ? heads >> 1 : heads;
   griddep_wait();
   griddep_launch_dependents();
-  for (int i = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5); i < p.rows; i += warps) {
-    const int b = i / heads, h = i - b * heads, c = h >= Hc, hl = c ? h - Hc : h;
+  uint4 v[2];
+  uint32_t v_rope = 0;
+  auto load = [&](int i) {
     const uint4* qn = reinterpret_cast<const uint4*>(p.q_nope + static_cast<size_t>(i) * kLatent) + 2 * lane;
-    const uint4* qr = reinterpret_cast<const uint4*>(p.q_rope + static_cast<size_t>(i) * kRope) + 2 * lane;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 v[2][2] = {{__ldg(qn), __ldg(qn + 1)}, {lane < 4 ? __ldg(qr) : zero, lane < 4 ? __ldg(qr + 1) : zero}};
-    auto word = [&](int t, int k) -> uint32_t {
-      const uint4& x = v[t][k >> 2];
-      return (k & 3) == 0 ? x.x : (k & 3) == 1 ? x.y : (k & 3) == 2 ? x.z : x.w;
-    };
+    v[0] = __ldg(qn);
+    v[1] = __ldg(qn + 1);
+    v_rope = __ldg(reinterpret_cast<const uint32_t*>(p.q_rope + static_cast<size_t>(i) * kRope) + lane);
+  };
+  const int step = kPrepWarps * gridDim.x;           // (rows: a multiple of eight, of one CTA's image each)
+  int i = blockIdx.x * kPrepWarps + warp, buf = 0;
+  if (i < p.rows) load(i);
+  for (; i < p.rows; i += step, buf ^= 1) {
+    const uint32_t x[9] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w, v_rope};
+    if (i + step < p.rows) load(i + step);
     float amax = 0.f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        amax = max3(amax, fabsf(__uint_as_float(word(t, k) << 16)), fabsf(__uint_as_float(word(t, k) & 0xFFFF0000u)));
+    for (int k = 0; k < 9; ++k)
+      amax = max3(amax, fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u)));
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     int a = 0;                                       // amax = m 2^e, m in [0.5, 1): a = 8 - e
@@ -180,24 +186,32 @@ __global__ void __launch_bounds__(kPrepThreads) rows8_prep_kernel(const Fp8PrepP
       a = min(126, max(-126, 8 - e));
     }
     const float up = ldexpf(1.f, a);
-    uint8_t* img = p.img + (static_cast<size_t>(b) * heads + c * Hc) * kImage;
+    uint32_t hi[9], lo[9];                           // two codes each
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (t == 1 && lane >= 4) break;
-      uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float u0 = __uint_as_float(word(t, k) << 16) * up, u1 = __uint_as_float(word(t, k) & 0xFFFF0000u) * up;
-        const uint32_t h2 = e4m3x2(u0, u1);
-        const float2 hv = e4m3x2_value(h2);
-        hi[k >> 1] |= h2 << (16 * (k & 1));
-        lo[k >> 1] |= e4m3x2((u0 - hv.x) * 32.f, (u1 - hv.y) * 32.f) << (16 * (k & 1));
-      }
-      uint4* dst = reinterpret_cast<uint4*>(img) + (32 * t + lane) * 2 * Hc + hl;
-      dst[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      dst[Hc] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    for (int k = 0; k < 9; ++k) {
+      const float u0 = __uint_as_float(x[k] << 16) * up, u1 = __uint_as_float(x[k] & 0xFFFF0000u) * up;
+      hi[k] = e4m3x2(u0, u1);
+      const float2 hv = e4m3x2_value(hi[k]);
+      lo[k] = e4m3x2((u0 - hv.x) * 32.f, (u1 - hv.y) * 32.f);
     }
+    auto piece = [](const uint32_t (&c)[9]) {
+      return make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
+    };
+    uint4* at = stage[buf] + lane * 2 * kPitch + warp;
+    at[0] = piece(hi);
+    at[kPitch] = piece(lo);
+    uint16_t* at_rope = reinterpret_cast<uint16_t*>(stage[buf] + (32 + (lane >> 3)) * 2 * kPitch + warp) + (lane & 7);
+    at_rope[0] = static_cast<uint16_t>(hi[8]);
+    at_rope[8 * kPitch] = static_cast<uint16_t>(lo[8]);
     if (lane == 0) p.fac[i] = ldexpf(1.f, -a);
+    __syncthreads();                                 // (and the buffer of the round before has been read)
+    const int i0 = i - warp, b = i0 / heads, h = i0 - b * heads, c = h >= Hc, hl = c ? h - Hc : h;
+    uint4* img = reinterpret_cast<uint4*>(p.img + (static_cast<size_t>(b) * heads + c * Hc) * kImage) + hl;
+#pragma unroll
+    for (int j = threadIdx.x; j < kCodes * kPrepWarps; j += kPrepThreads) {
+      const int row = j / kPrepWarps, k = j % kPrepWarps;
+      img[row * Hc + k] = stage[buf][row * kPitch + k];
+    }
   }
 }
 
@@ -861,8 +875,8 @@ int launch_rows8(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const De
   const int smem = p.out_bf16 ? (few ? rows8::Cfg<false, true>::kSmemBytes : rows8::Cfg<false, false>::kSmemBytes)
                               : (few ? rows8::Cfg<true, true>::kSmemBytes : rows8::Cfg<true, false>::kSmemBytes);
   if (!set_smem_limit(reinterpret_cast<const void*>(kernel), smem)) return MLA_ERR_CUDA;
-  // few enough blocks that the next kernel's fit beside them (it starts once all have)
-  const int warps = rows8::kPrepThreads / 32, blocks = (pp.rows + warps - 1) / warps, held = 4 * ctas;
+  // as many blocks as are resident at once (a block for every eight heads: 260.6 us of the ragged batch, not 256.6)
+  const int blocks = (pp.rows + rows8::kPrepWarps - 1) / rows8::kPrepWarps, held = 4 * ctas;
   const int st = rows8::launch_after(&rows8::rows8_prep_kernel, blocks < held ? blocks : held, rows8::kPrepThreads, 0,
                                      stream, pp, p.heads);
   if (st != MLA_OK) return st;
