@@ -48,8 +48,9 @@
 // but 24.5 -> 25.6 us of the former, as it has more to wait for at a time.  Five
 // places for tiles where they fit: 25.1 us.)
 //
-// Those two batches take 24.5 us (2.6 TB/s) and 263 us (0.64 PFLOP/s of the
-// formula's operations), kernels before and after included.
+// With the kernels before and after, the former batch takes 24.2 us (2.7 TB/s) and
+// the latter 253 us (0.67 PFLOP/s of the formula's operations); they have not
+// been timed again with the other forms since the queries' kernel became faster.
 //
 // A kernel before this one splits each request's query into its parts, once for
 // all items (in here a warp took 20000 cycles an item for it), in the order in
