@@ -495,8 +495,8 @@ int mla_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slots, c
  *   all other arguments, plan and workspace as for mla_decode_run_fp8.
  * Launches for every head count a kernel that prepares the queries, the decode
  * kernel as its programmatic dependent, and the merge of mla_decode_run.  The
- * weights are held to 8 significant bits for a bf16 out (or 2^-10 of a scale on
- * which a head's largest is 32 or more), to 16 (or 2^-14) for a float32 out, and
+ * weights are held to 2^-9 of themselves for a bf16 out (or 2^-10 on a scale on
+ * which a head's largest is 32 or more), to 2^-17 of both for a float32 out, and
  * their sum is that of the unrounded ones; with a bf16 out split requests are
  * merged from float32 states.
  * Errors as for mla_decode_run_fp8, and MLA_ERR_INVALID_ARG for a null or

@@ -384,6 +384,12 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t v) {
 constexpr float kRowScaleMin = 0x1p-64f, kRowScaleMax = 0x1p64f;
 __device__ __forceinline__ float row_scale(float s) { return fminf(fmaxf(s, kRowScaleMin), kRowScaleMax); }
 
+// The two values of an E5M2 pair, exactly.
+__device__ __forceinline__ float2 e5m2x2_value(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E5M2);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 // Two values as E4M3 hi + lo parts (low byte = a): hi = e4m3(x), lo =
 // e4m3(f16(x) - hi), the difference taken exactly in f16 (x rounded to f16
 // has 11 significant bits, hi 4); for 0 <= x <= 256 the pair keeps x to

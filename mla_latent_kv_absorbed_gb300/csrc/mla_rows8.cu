@@ -18,9 +18,13 @@
 // the two of a head meet by a shuffle.
 //   S[128 x 64 rows] = [hi; lo] X^T          16 K-steps from TMEM, 2 of the rope
 // The weights, at most 431, are parts that add up in one accumulator:
-//   out bf16   hi + lo, both E4M3: 8 significant bits, or 2^-10 absolute
-//   out fp32   two more, E4M3 and E5M2: 16 bits, or 2^-14 absolute (the largest
-//              weight is 32 or more) - what an fp32 result is asked for
+//   out bf16   hi + lo, both E4M3: off by 2^-9 of the weight, or 2^-10 where E4M3
+//              has no finer steps (the largest weight is 32 or more)
+//   out fp32   two more, both E5M2, whose steps go on down to 2^-16: 2^-17 of the
+//              weight, or 2^-17.  (A part leaves a rest below half its step, in
+//              the binade under that: 2^-4, 2^-9, 2^-13, 2^-17 of w's binade.
+//              With E4M3 as the third the rest was 2^-18, but 2^-14 absolute, and
+//              short lists' results four times as far off.)
 //   O^T[512 dims x heads] += X^T W^T         4 blocks of 128 dims, 2 K-steps of
 //                                            32 rows a part
 // The parts' errors are the weights' own; the sum l takes them unrounded.
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_ss_f8(d, a, D(bp, 32 * ks), idesc4, (j == 0 && ks == 0) ? 0u : 1u);
                 umma_ss_f8(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
                 if constexpr (kFine) {
-                  umma_ss_f8(d, a, D(bp, kPPair + 32 * ks), idesc4, 1u);
+                  umma_ss_f8(d, a, D(bp, kPPair + 32 * ks), idesc5, 1u);
                   umma_ss_f8(d, a, D(bp, kPPair + 64 + 32 * ks), idesc5, 1u);
                 }
               }
@@ -783,8 +787,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               r = f2_fma(e4m3x2_value(c0[i]), minus, r);   // (exact, like the next two)
               c1[i] = e4m3x2(r.x, r.y);
               r = f2_fma(e4m3x2_value(c1[i]), minus, r);
-              c2[i] = e4m3x2(r.x, r.y);
-              r = f2_fma(e4m3x2_value(c2[i]), minus, r);
+              c2[i] = e5m2x2(r.x, r.y);
+              r = f2_fma(e5m2x2_value(c2[i]), minus, r);
               c3[i] = e5m2x2(r.x, r.y);
             } else {
               e4m3x2_split(r.x, r.y, c0[i], c1[i]);
