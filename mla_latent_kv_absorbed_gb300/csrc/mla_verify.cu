@@ -16,7 +16,7 @@
 // A pick near a border of the running sum is decided by the sum's last bits,
 // so sums are held to about 47 bits, as pairs of fp32 numbers: t - q with its
 // exact error (t > q >= 0: t - d and the rest are exact), added to a pair with
-// the addition's exact error.  That is 17 fp32 operations an element.  64-bit
+// the addition's exact error.  That is nine instructions an element.  64-bit
 // arithmetic, at one two-hundredth of fp32's rate, would take longer than the
 // element's eight bytes from memory; even for the few sums of sums it took a
 // quarter of the kernel's time.  The tests u a < t are exact: the product as a
@@ -75,7 +75,7 @@ __device__ __forceinline__ Pair shfl_xor(Pair a, int o) {
 }
 
 // A probability: NaN and negative values count as 0, values past 1 as 1.
-__device__ __forceinline__ float prob(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+__device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 
 // What a request's drafts left: the row that the next token is drawn from.
 struct Walk {
@@ -84,11 +84,10 @@ struct Walk {
   int excluded;               // tokens whose mass is taken out
 };
 
-// max(t - q, 0), exactly.
+// max(t - q, 0), exactly (0 where q >= t).
 __device__ __forceinline__ Pair rest(float t, float q) {
-  const bool more = t > q;
-  const float d = more ? __fsub_rn(t, q) : 0.f;
-  return make_float2(d, more ? __fsub_rn(__fsub_rn(t, d), q) : 0.f);
+  const float less = fminf(q, t), d = __fsub_rn(t, less);
+  return make_float2(d, __fsub_rn(__fsub_rn(t, d), less));
 }
 
 // One warp: lane i has drafts i and 32 + i.
@@ -192,26 +191,42 @@ __device__ __forceinline__ Walk walk_drafts(const VerifyParams& p, int b, int la
   return w;
 }
 
-// Which of `n` parts, in their order, the running sum passes `thr` in (the last
-// with any mass where rounding or a number of 1 leaves it short; 0 without mass),
-// and the sum before it.
-__device__ __forceinline__ int pick(const Pair* sum, int n, Pair thr, Pair& before) {
-  int at = 0;
-  Pair run = make_float2(0.f, 0.f);
-  before = run;
-  for (int i = 0; i < n; ++i) {
-    const Pair s = sum[i], upto = add(run, s);
-    if (s.x > 0.f) {
-      at = i;
-      before = run;
-      if (above(upto, thr)) break;
-    }
-    run = upto;
+// Sums of up to eight parts, a part a lane, and the sums of those up to it.  By a whole warp.
+struct Parts {
+  Pair sum, upto;
+};
+__device__ __forceinline__ Pair shfl(Pair a, int lane) {
+  return make_float2(__shfl_sync(0xffffffffu, a.x, lane), __shfl_sync(0xffffffffu, a.y, lane));
+}
+__device__ __forceinline__ Pair shfl_up(Pair a, int o) {
+  return make_float2(__shfl_up_sync(0xffffffffu, a.x, o), __shfl_up_sync(0xffffffffu, a.y, o));
+}
+__device__ __forceinline__ Parts parts_of(const Pair* sum, int n, int lane) {
+  Parts p;
+  p.sum = lane < n ? sum[lane] : make_float2(0.f, 0.f);
+  p.upto = p.sum;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const Pair x = shfl_up(p.upto, o);
+    if (lane >= o) p.upto = add(p.upto, x);
   }
+  return p;
+}
+// Which part the running sum passes `thr` in (the last with any mass where
+// rounding or a number of 1 leaves it short; 0 without mass), and the sum before
+// it.
+__device__ __forceinline__ int pick(const Parts& p, Pair thr, Pair& before) {
+  const uint32_t some = __ballot_sync(0xffffffffu, p.sum.x > 0.f);
+  const uint32_t past = __ballot_sync(0xffffffffu, p.sum.x > 0.f && above(p.upto, thr));
+  const int at = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
+  before = shfl(p.upto, max(at - 1, 0));
+  if (at == 0) before = make_float2(0.f, 0.f);
   return at;
 }
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) {
+// (Four blocks an SM: 64 requests of eight CTAs are resident at once.  With 77 registers they are not, and the batch
+// of 64 x 8 x 129280 takes 19.4 us instead of 15.0.)
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams p) {
   __shared__ Pair cta_sum[kMaxCluster], warp_sum[kWarps], part_sum[kWarps];
   __shared__ int32_t gone[kMaxDrafts];
   __shared__ Walk walk;
@@ -271,10 +286,13 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
       for (int i = 0; i < 4; ++i) t[i] = at == i ? 0.f : t[i];
     }
   };
-  // sum of max(t - q, 0) over blocks [k0, k1), by a warp; in every lane
+  // Sum of max(t - q, 0) over blocks [k0, k1), by a warp; in every lane.  The even and the odd elements have a running
+  // sum each, and go through packed instructions together.  (Four blocks a lane on their way: 15.8 us of the batch
+  // of 64 x 8 x 129280; two 17.9, three 16.4, six 21.8, and two while two are added up 15.9.)
   auto sum_of = [&](int k0, int k1) -> Pair {
-    float s = 0.f, e = 0.f;
     constexpr int kDeep = 4;
+    const float2 minus1 = make_float2(-1.f, -1.f);
+    float2 s = make_float2(0.f, 0.f), e = s;
     for (int k = k0 + lane; k < k1; k += 32 * kDeep) {
       float t[kDeep][4], q[kDeep][4];
 #pragma unroll
@@ -285,14 +303,18 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
         if (k + 32 * j >= k1) continue;
         clean(k + 32 * j, t[j], q[j]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const Pair r = rest(t[j][i], q[j][i]), n = two_sum(s, r.x);
-          s = n.x;
-          e += n.y + r.y;
+        for (int i = 0; i < 4; i += 2) {
+          const float2 x = make_float2(t[j][i], t[j][i + 1]);
+          const float2 y = make_float2(fminf(q[j][i], x.x), fminf(q[j][i + 1], x.y));
+          const float2 d = f2_fma(y, minus1, x), low = f2_fma(y, minus1, f2_fma(d, minus1, x));   // x - y, exactly
+          const float2 n = f2_add(s, d), z = f2_fma(s, minus1, n);                                // s + d and its error
+          const float2 off = f2_add(f2_fma(f2_fma(z, minus1, n), minus1, s), f2_fma(z, minus1, d));
+          s = n;
+          e = f2_add(e, f2_add(off, low));
         }
       }
     }
-    Pair all = pair_of(s, e);
+    Pair all = add(pair_of(s.x, e.x), pair_of(s.y, e.y));
 #pragma unroll
     for (int o = 16; o; o >>= 1) all = add(all, shfl_xor(all, o));
     return all;
@@ -313,17 +335,17 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
   __syncwarp();
   cluster_arrive();
   cluster_wait();
-  Pair total = make_float2(0.f, 0.f);
-  for (int i = 0; i < C; ++i) total = add(total, cta_sum[i]);
+  const Parts ctas = parts_of(cta_sum, C, lane);
+  const Pair total = shfl(ctas.upto, C - 1);
   if (!(total.x > 0.f)) {
     if (rank == 0 && tid == 0) p.next[b] = -1;
     return;
   }
   Pair thr = times(total, __ldg(p.uniforms + static_cast<long long>(b) * p.width));
   Pair before;
-  if (pick(cta_sum, C, thr, before) != rank) return;
+  if (pick(ctas, thr, before) != rank) return;
   thr = add(thr, minus(before));
-  const int w = pick(warp_sum, kWarps, thr, before);
+  const int w = pick(parts_of(warp_sum, kWarps, lane), thr, before);
   thr = add(thr, minus(before));
   // the warp's part in eighths
   const int k0 = first(rank * kWarps + w), k1 = first(rank * kWarps + w + 1);
@@ -332,7 +354,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
   const Pair sub = sum_of(e0, e1);
   if (lane == 0) part_sum[warp] = sub;
   __syncthreads();
-  if (pick(part_sum, kWarps, thr, before) != warp) return;
+  if (pick(parts_of(part_sum, kWarps, lane), thr, before) != warp) return;
   thr = add(thr, minus(before));
   // 32 blocks at a time, a block a lane
   Pair run = make_float2(0.f, 0.f);
@@ -354,10 +376,10 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
     Pair upto = s, less = make_float2(0.f, 0.f);   // with, and without this lane's own
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const Pair x = make_float2(__shfl_up_sync(0xffffffffu, upto.x, o), __shfl_up_sync(0xffffffffu, upto.y, o));
+      const Pair x = shfl_up(upto, o);
       if (lane >= o) upto = add(upto, x);
     }
-    less = make_float2(__shfl_up_sync(0xffffffffu, upto.x, 1), __shfl_up_sync(0xffffffffu, upto.y, 1));
+    less = shfl_up(upto, 1);
     if (lane == 0) less = make_float2(0.f, 0.f);
     const uint32_t some = __ballot_sync(0xffffffffu, s.x > 0.f);
     const uint32_t past = __ballot_sync(0xffffffffu, s.x > 0.f && above(add(run, upto), thr));
@@ -375,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p) 
     }
     if (who >= 0) last = __shfl_sync(0xffffffffu, v, who);
     if (past) break;
-    run = add(run, make_float2(__shfl_sync(0xffffffffu, upto.x, 31), __shfl_sync(0xffffffffu, upto.y, 31)));
+    run = add(run, shfl(upto, 31));
   }
   if (lane == 0) p.next[b] = last;
 }
