@@ -59,13 +59,13 @@ __device__ __forceinline__ Kept kept_of(const RepackParams& p, int src, bool rep
     return {0, 0, 0, 0};
   }
   const long long lo = __ldg(p.indptr + src), hi = __ldg(p.indptr + src + 1);
+  const int a = p.path ? __ldg(p.accepted + src) : 0;      // (at once with the others)
   const long long s = min(max(lo, 0ll), p.entries), e = min(max(hi, s), p.entries);
   const int n = static_cast<int>(e - s);
   bool bad = lo != s || hi != e;
   Kept k{static_cast<int>(s), n, n, n};
   if (p.path) {
     if (n >= p.width) {
-      const int a = __ldg(p.accepted + src);
       const int take = min(max(a, 0), p.width);
       if (report && a != take) record_status(p.status, MLA_ERR_TREE);
       k.base = n - p.width;
@@ -112,12 +112,7 @@ __global__ void __launch_bounds__(kListThreads) repack_mark_kernel(const RepackP
   int slot[kDeep];
 #pragma unroll
   for (int d = 0; d < kDeep; ++d) slot[d] = mine + d < hi ? __ldg(p.indices + mine + d) : 0;
-  for (int i = tid; i < (p.batch + 31) / 32; i += kListThreads) goes_on[i] = 0;
-  __syncthreads();
-  for (int i = tid; i < p.new_batch; i += kListThreads) {
-    const int o = __ldg(p.sources + i);
-    if (o >= 0 && o < p.batch) atomicOr(goes_on + (o >> 5), 1u << (o & 31));
-  }
+  int source = tid < p.new_batch ? __ldg(p.sources + tid) : -1;
   // the window of the block's first entry: lists ascend, so the last that starts at or before it
   int r0 = 0;
   if (p.batch > kWindow) {
@@ -128,10 +123,18 @@ __global__ void __launch_bounds__(kListThreads) repack_mark_kernel(const RepackP
       else top = mid - 1;
     }
   }
-  for (; r0 < p.batch; r0 += kWindow) {
+  for (bool begun = false; r0 < p.batch; r0 += kWindow, begun = true) {
     const int n = min(kWindow, p.batch - r0);
     Kept k{0, 0, 0, 0};
     if (tid < n) k = kept_of(p, r0 + tid, false);
+    if (!begun) {                                    // (while those loads are on their way)
+      for (int i = tid; i < (p.batch + 31) / 32; i += kListThreads) goes_on[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < p.new_batch; i += kListThreads) {
+        if (i != tid) source = __ldg(p.sources + i);
+        if (source >= 0 && source < p.batch) atomicOr(goes_on + (source >> 5), 1u << (source & 31));
+      }
+    }
     unsigned long long path = 0;
     if (k.base < k.rows && k.start + k.rows > lo && k.start + k.base < hi) {
       const int32_t* steps = p.path + static_cast<long long>(r0 + tid) * p.width;
@@ -306,6 +309,19 @@ __device__ __forceinline__ void my_words(long long num_slots, long long& w0, lon
   w1 = min(w0 + per, end);
 }
 
+// Set bits of words [w0, w1): eight loads at a time.
+__device__ __forceinline__ int count_bits(const uint32_t* bits, long long w0, long long w1) {
+  int n = 0;
+  for (long long w = w0; w < w1; w += 8) {
+    uint32_t m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = w + i < w1 ? bits[w + i] : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n += __popc(m[i]);
+  }
+  return n;
+}
+
 // Marked slots to an ascending list; the bitmap is zero again.
 __global__ void __launch_bounds__(kScanThreads) freed_kernel(const RepackParams p) {
   __shared__ int warp_sums[32], cta_sums[kScanCtas];
@@ -313,8 +329,7 @@ __global__ void __launch_bounds__(kScanThreads) freed_kernel(const RepackParams 
   griddep_launch_dependents();
   long long w0, w1;
   my_words(p.num_slots, w0, w1);
-  int mine = 0;
-  for (long long w = w0; w < w1; ++w) mine += __popc(p.bits[w]);
+  const int mine = count_bits(p.bits, w0, w1);
   int all;
   long long at = cluster_scan(mine, warp_sums, cta_sums, all);
   for (long long w = w0; w < w1 && mine; ++w) {
@@ -357,8 +372,7 @@ __global__ void __launch_bounds__(kScanThreads) compact_scan_kernel(const Compac
   griddep_launch_dependents();
   long long w0, w1;
   my_words(c.num_slots, w0, w1);
-  int mine = 0;
-  for (long long w = w0; w < w1; ++w) mine += __popc(c.bits[w]);
+  const int mine = count_bits(c.bits, w0, w1);
   int n;
   int run = cluster_scan(mine, warp_sums, cta_sums, n);
   const long long last_word = n >> 5;
