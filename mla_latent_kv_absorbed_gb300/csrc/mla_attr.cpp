@@ -1,14 +1,13 @@
 // Per-device launch settings shared by the kernel launchers: the dynamic
-// shared-memory limit of each kernel and the SM count.  Both are looked up
-// once and reused; a process may drive several devices from several host
-// threads, so the caches are keyed on the context (the limit) or the device
-// (the SM count) and safe to use concurrently.
+// shared-memory limit of each kernel, leave for clusters of more than eight, and
+// the SM count.  All are looked up once and reused; a process may drive several
+// devices from several host threads, so the caches are keyed on the context
+// (attributes) or the device (the SM count) and safe to use concurrently.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
 #include <mutex>
-#include <utility>
 #include <vector>
 
 #include "mla_launch.h"
@@ -40,30 +39,43 @@ CUcontext current_context() {
   return ctx;
 }
 
-}  // namespace
-
-bool set_smem_limit(const void* func, int bytes) {
-  // The attribute belongs to the function as loaded in one context: remember
-  // the (function, context) pairs it was set in.  A context made after a
-  // device reset is a new one and gets the attribute again.
+bool set_attribute(const void* func, cudaFuncAttribute attr, int value) {
+  // An attribute belongs to the function as loaded in one context: remember
+  // the (function, attribute, context) triples it was set for.  A context made
+  // after a device reset is a new one and gets the attribute again.
+  struct Done {
+    const void* func;
+    cudaFuncAttribute attr;
+    CUcontext ctx;
+  };
   static std::mutex mu;
-  static std::vector<std::pair<const void*, CUcontext>> done;
+  static std::vector<Done> done;
   CUcontext ctx = current_context();   // null before the device's first runtime call: set it then
   if (ctx) {
     std::lock_guard<std::mutex> lock(mu);
     for (const auto& e : done)
-      if (e.first == func && e.second == ctx) return true;
+      if (e.func == func && e.attr == attr && e.ctx == ctx) return true;
   }
-  if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+  if (cudaFuncSetAttribute(func, attr, value) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
   ctx = current_context();             // the call above made a context current if none was
   if (ctx) {
     std::lock_guard<std::mutex> lock(mu);
-    done.emplace_back(func, ctx);
+    done.push_back({func, attr, ctx});
   }
   return true;
+}
+
+}  // namespace
+
+bool set_smem_limit(const void* func, int bytes) {
+  return set_attribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+bool allow_wide_cluster(const void* func) {
+  return set_attribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 int device_sm_count() {

@@ -13,6 +13,9 @@ namespace mla {
 // the CUDA call failed.
 bool set_smem_limit(const void* func, int bytes);
 
+// Likewise, that a kernel may be launched in clusters of more than eight CTAs.
+bool allow_wide_cluster(const void* func);
+
 // SM count of the current device (cached per device), or 0 on an error.
 int device_sm_count();
 
