@@ -357,9 +357,10 @@ __global__ void __launch_bounds__(kListThreads) compact_mark_kernel(const Compac
   griddep_wait();
   griddep_launch_dependents();
   const long long n = entries_of(c);
-  for (long long j = static_cast<long long>(blockIdx.x) * kListThreads + threadIdx.x; j < n;
+  for (long long j = static_cast<long long>(blockIdx.x) * kListThreads + threadIdx.x; j < c.entries;
        j += static_cast<long long>(gridDim.x) * kListThreads) {
-    const int slot = __ldg(c.indices + j);
+    const int slot = __ldg(c.indices + j);         // (together with their number)
+    if (j >= n) break;
     if (slot >= 0 && slot < c.num_slots) set_bit(c.bits, slot);
     else record_status(c.status, MLA_ERR_INDEX_OOB);
   }
