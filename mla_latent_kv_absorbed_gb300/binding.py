@@ -400,7 +400,7 @@ def decode_run_fp8_rows(plan_host, plan_dev, q_nope, q_rope, kv_cache, kv_scales
     _need(w, "workspace", workspace, torch.uint8, (workspace.numel(),))
     st = _launch_stream(w, stream, plan_dev, q_nope, q_rope, kv_cache, kv_scales, kv_indptr, kv_indices, out, lse,
                         workspace)
-    st = _lib.mla_decode_run_fp8_rows(plan_host.ctypes.data, plan_dev.data_ptr(), q_nope.data_ptr(), q_rope.data_ptr(),
+    st = _lib.mla_decode_run_fp8_rows(_host_ptr(plan_host), plan_dev.data_ptr(), q_nope.data_ptr(), q_rope.data_ptr(),
                                       kv_cache.data_ptr(), N, kv_scales.data_ptr(), kv_indptr.data_ptr(),
                                       _ptr(kv_indices), float(sm_scale), out.data_ptr(), out_dtype, _ptr(lse),
                                       workspace.data_ptr(), workspace.numel(), st)
