@@ -494,11 +494,17 @@ int mla_append_kv_fp8(void* kv_cache, int64_t num_slots, const int32_t* slots, c
  *              that kv_indices names (at slot 0 for one outside the cache).
  *   all other arguments, plan and workspace as for mla_decode_run_fp8.
  * Launches for every head count a kernel that prepares the queries, the decode
- * kernel as its programmatic dependent, and the merge of mla_decode_run.  The
- * weights are held to 2^-9 of themselves for a bf16 out (or 2^-10 on a scale on
- * which a head's largest is 32 or more), to 2^-17 of both for a float32 out, and
- * their sum is that of the unrounded ones; with a bf16 out split requests are
- * merged from float32 states.
+ * kernel as its programmatic dependent, and the merge of mla_decode_run; with a
+ * bf16 out split requests are merged from float32 states.
+ * Accuracy: a weight is held to 2^-8 of itself for a bf16 out, to 2^-16 for a
+ * float32 out, and what the smallest lose beyond that is at most 2^-8 (2^-15) of
+ * all weights together, however many rows there are (one row may outweigh each of
+ * very many others by any factor); their sum is that of the unrounded ones.  The
+ * tensor core cuts its sums to 24 bits, towards zero, two (four) times for every
+ * 32 rows of an uncut request, so over n rows that add up to one side a result
+ * is short of itself by up to n 2^-28 (n 2^-27) in the mean, twice that at most: 1e-3 for
+ * a float32 out over 131072 rows, as with the other caches.  The scales of a
+ * request's rows may be 2^100 apart (a row of zeros has 2^-64).
  * Errors as for mla_decode_run_fp8, and MLA_ERR_INVALID_ARG for a null or
  * misaligned kv_scales (not looked at when no request has a row). */
 int mla_decode_run_fp8_rows(const int32_t* plan_host, const int32_t* plan_dev, const void* q_nope, const void* q_rope,

@@ -402,6 +402,15 @@ __device__ __forceinline__ void e4m3x2_split(float a, float b, uint32_t& hi, uin
       __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&r), __NV_SATFINITE, __NV_E4M3));
 }
 
+// The same with an E5M2 lo, whose steps go on down to 2^-16: 0 <= x <= 448 is kept to 2^-8 of itself, or 2^-14.
+__device__ __forceinline__ void e4m3_e5m2_split(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = e4m3x2(a, b);
+  const __half2_raw hv = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
+  const __half2 r = __hsub2(__floats2half2_rn(a, b), *reinterpret_cast<const __half2*>(&hv));
+  lo = static_cast<uint32_t>(
+      __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&r), __NV_SATFINITE, __NV_E5M2));
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T.
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                         uint32_t idesc, uint32_t accumulate) {

@@ -17,17 +17,27 @@
 // quadrant of 32 rows the hi parts of 16 heads and then their lo parts, so that
 // the two of a head meet by a shuffle.
 //   S[128 x 64 rows] = [hi; lo] X^T          16 K-steps from TMEM, 2 of the rope
-// The weights, at most 431, are parts that add up in one accumulator:
-//   out bf16   hi + lo, both E4M3: off by 2^-9 of the weight, or 2^-10 where E4M3
-//              has no finer steps (the largest weight is 32 or more)
-//   out fp32   two more, both E5M2, whose steps go on down to 2^-16: 2^-17 of the
-//              weight, or 2^-17.  (A part leaves a rest below half its step, in
-//              the binade under that: 2^-4, 2^-9, 2^-13, 2^-17 of w's binade.
-//              With E4M3 as the third the rest was 2^-18, but 2^-14 absolute, and
-//              short lists' results four times as far off.)
+// The weights are parts that add up in one accumulator.  A part leaves a rest
+// below half its step, in the binade under that, and E5M2's steps go on down to
+// 2^-16 where E4M3's end at 2^-9:
+//   out bf16   2^7 for the reference, at most 431: E4M3 + E5M2, off by 2^-8 of the
+//              weight, or 2^-14
+//   out fp32   2^10, at most 3445: E5M2 + E4M3 + two of E5M2, off by 2^-16 of the
+//              weight (rests 2^-3, 2^-8, 2^-12, 2^-16 of its binade), or 2^-17
 //   O^T[512 dims x heads] += X^T W^T         4 blocks of 128 dims, 2 K-steps of
 //                                            32 rows a part
-// The parts' errors are the weights' own; the sum l takes them unrounded.
+// The sum l takes the weights unrounded, so what the second bounds leave out is
+// lost: nothing beside the rows that set the reference, but half of the result
+// where one row outweighs 2^16 others, each by 2^16.  So the reference also
+// goes down: every thread adds up what its rows may have lost at most and the
+// largest weights that it had since the last move, and once the former passes
+// kEps of the latter and of the reference's own row, a tile that lies below the
+// reference takes its place.  (O and l, in fp32, follow a factor of 2^24 upwards
+// as they follow one downwards.)  What is lost is then at most 2 kEps of all
+// weights, at any number of rows.  (With E4M3 + E4M3 at 2^5 and a reference that
+// only went up, 16384 rows of scores N(0, 1) beside one that has 0.8 of the sum
+// were 0.07 off, and 131072 of equal ones 0.5; now 3e-5, and 1e-6 with fp32.
+// Moves are few: 2 to 5 an item of 16384 rows with scores N(0, 1.7) to N(0, 5).)
 //
 // A worker of 48 or more heads is two CTAs, and each takes half of the HEADS:
 // all of the scores, the softmax and the output of a head are one CTA's, and
@@ -52,9 +62,11 @@
 // but 24.5 -> 25.6 us of the former, as it has more to wait for at a time.  Five
 // places for tiles where they fit: 25.1 us.)
 //
-// With the kernels before and after, the former batch takes 24.2 us (2.7 TB/s) and
-// the latter 253 us (0.67 PFLOP/s of the formula's operations); they have not
-// been timed again with the other forms since the queries' kernel became faster.
+// With the kernels before and after, the former batch takes 24.5 us (2.6 TB/s; fp32
+// out 27.9) and the latter 258 us (0.66 PFLOP/s of the formula's operations; bf16
+// out 210; 64 heads 195).  What was tried above was timed before the reference went
+// both ways: with that, and the weights of 2^7 and 2^10, they were 24.0 and 252 us,
+// and 24.6 and 263 with 2^5 and 2^8 and a lag of 3.75.
 //
 // A kernel before this one splits each request's query into its parts, once for
 // all items (in here a warp took 20000 cycles an item for it), in the order in
@@ -95,7 +107,8 @@ constexpr int kScSlots = 4;                          // tiles whose rows' number
 constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the scales, reciprocals
 constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
 constexpr float kLoWeight = 1.f / 32.f;              // value of a query's lo part
-constexpr float kTop = 5.f, kLag = 3.75f;            // weights are 2^(e - m + kTop) with e <= m + kLag: to 431 of 448
+constexpr float kLag = 1.75f;                        // weights are 2^(e - m + kTop) with e <= m + kLag
+constexpr float kDepth = 24.f;                       // the reference's deepest under its highest: less is nothing beside that
 constexpr int kBarCrew0 = 1, kBarGather = 9;   // named barriers
 constexpr int kTmO = 0, kTmQ = 256, kTmS = 384;
 constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);
@@ -108,15 +121,22 @@ struct Cfg {
   static constexpr int kGroups = kFew ? 2 : 4;       // of 16 heads
   static constexpr int kPBuf = kPairs * kPPair;
   static constexpr int kRows = kFew ? 8 : 16;        // rows of a tile that a softmax thread has
+  static constexpr float kTop = kFine ? 10.f : 7.f;  // (the first two parts hold up to 2^11.75, or 2^8.75)
+  static constexpr float kLost = kFine ? 0x1p-17f : 0x1p-14f;   // what a small weight loses at most
+  static constexpr float kEps = kFine ? 0x1p-16f : 0x1p-9f;     // what all weights together may lose of their sum
+  // a thread's share of that of the reference's own row (of weight 2^kTop; kCrews T / kRows threads have a head)
+  static constexpr float kRoom = kEps * (kFine ? 1024.f : 128.f) * kRows / (kCrews * T);
   static constexpr int kOffQr = kUnits * kUnit;
   static constexpr int kOffP = kOffQr + kQr;
   static constexpr int kOffSc = kOffP + kPSlots * kPBuf;
   static constexpr int kOffRed = kOffSc + kScSlots * kScSlot;   // [kCrews][256] maxima, or sums
-  static constexpr int kOffBc = kOffRed + kCrews * 256 * 4;      // [kUnits][64] a tile's rescaling factors
+  static constexpr int kOffOwe = kOffRed + kCrews * 256 * 4;     // [kCrews][256] what may have been lost
+  static constexpr int kOffBc = kOffOwe + kCrews * 256 * 4;      // [kUnits][64] a tile's rescaling factors
   static constexpr int kOffSum = kOffBc + kUnits * 64 * 4;      // [2][kCrews][64] an item's sums, for the output
   static constexpr int kOffRef = kOffSum + 2 * kCrews * 64 * 4; // [2][kCrews][64] and references
   static constexpr int kOffNow = kOffRef + 2 * kCrews * 64 * 4; // [64] the references as the last tile left them
-  static constexpr int kOffSlots = kOffNow + 64 * 4;            // [5][64] a tile's slots, for each gathering warp
+  static constexpr int kOffHigh = kOffNow + 64 * 4;             // [64] the highest references of the item
+  static constexpr int kOffSlots = kOffHigh + 64 * 4;           // [5][64] a tile's slots, for each gathering warp
   static constexpr int kOffBar = kOffSlots + 5 * T * 4;
   static constexpr int bFull = 0;                    // [kUnits] a tile's rows have landed
   static constexpr int bEmpty = bFull + kUnits;      // [kUnits]
@@ -463,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int ks = 0; ks < 2; ++ks) {       // 32 rows
                 const uint64_t a = D(av, mb * kAtom + 4096 * ks);
                 const uint32_t d = tmem + kTmO + 64 * mb;
-                umma_ss_f8(d, a, D(bp, 32 * ks), idesc4, (j == 0 && ks == 0) ? 0u : 1u);
-                umma_ss_f8(d, a, D(bp, 64 + 32 * ks), idesc4, 1u);
+                umma_ss_f8(d, a, D(bp, 32 * ks), kFine ? idesc5 : idesc4, (j == 0 && ks == 0) ? 0u : 1u);
+                umma_ss_f8(d, a, D(bp, 64 + 32 * ks), kFine ? idesc4 : idesc5, 1u);
                 if constexpr (kFine) {
                   umma_ss_f8(d, a, D(bp, kPPair + 32 * ks), idesc5, 1u);
                   umma_ss_f8(d, a, D(bp, kPPair + 64 + 32 * ks), idesc5, 1u);
@@ -542,20 +562,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0 && !aborted) mbar_arrive(bar(C::bQFull));
     };
-    auto output = [&](int b, int dest, uint32_t nitem) {
+    auto output = [&](int b, int dest, uint32_t nitem, uint32_t last) {   // last: the crew of the item's last tile
       const bool part_ok = dest < p.max_partials;    // a device-only plan naming a partial past the workspace
       if (!part_ok && warp == kQueryWarp0 && lane == 0) record_status(p.status, MLA_ERR_PLAN_MISMATCH);
       wait(bar(C::bSumFull + (nitem & 1)), (nitem >> 1) & 1);
       const float* sums = reinterpret_cast<const float*>(smem + C::kOffSum) + 64 * kCrews * (nitem & 1) + h0 + lane;
       const float* refs = reinterpret_cast<const float*>(smem + C::kOffRef) + 64 * kCrews * (nitem & 1) + h0 + lane;
-      const float ref = fmaxf(refs[0], refs[64]);    // the last tile's
-      const float l = fmaf(sums[0], ex2_approx(refs[0] - ref), sums[64] * ex2_approx(refs[64] - ref));
+      const float ref = refs[64 * last];             // O's units (the other crew may have seen a higher one before)
+      const float l = fmaf(sums[64 * (last ^ 1)], ex2_approx(refs[64 * (last ^ 1)] - ref), sums[64 * last]);
       const float inv = l > 0.f ? 1.f / l : 0.f;     // of head h0 + lane
       __syncwarp();
       if (lane == 0 && !aborted) mbar_arrive(bar(C::bSumEmpty + (nitem & 1)));
       const size_t row0 = static_cast<size_t>(dest < 0 ? b : dest) * p.heads + cta * Hc;
       if (q == 0 && (!kFew || half == 0) && h0 + lane < Hc && !aborted && part_ok) {
-        const float lse = l > 0.f ? (ref + __log2f(l) - kTop) * 0.69314718055994531f : -INFINITY;
+        const float lse = l > 0.f ? (ref + __log2f(l) - C::kTop) * 0.69314718055994531f : -INFINITY;
         if (dest >= 0) p.part_lse[row0 + h0 + lane] = lse;
         else if (p.lse) p.lse[row0 + h0 + lane] = lse;
       }
@@ -642,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (it < it1 && !usable(it));
       if (it < it1) query(item_w(it, 0), nitem + 1);
       fix(g++);
-      output(b, dest, nitem++);
+      output(b, dest, nitem++, (g - 1) & 1);
     }
   } else {
     // ----------------------------------------------------------------- softmax
@@ -661,7 +681,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int meet = kBarCrew0 + C::kGroups * crew + group;
     const uint32_t quad = static_cast<uint32_t>(32 * q) << 16;
     float* red = reinterpret_cast<float*>(smem + C::kOffRed) + 256 * crew;
+    float* owe = reinterpret_cast<float*>(smem + C::kOffOwe) + 256 * crew;
     volatile float* now = reinterpret_cast<volatile float*>(smem + C::kOffNow);
+    volatile float* high = reinterpret_cast<volatile float*>(smem + C::kOffHigh);
     volatile uint16_t* moved_of = reinterpret_cast<volatile uint16_t*>(smem + C::kOffMoved);   // heads to rescale
     auto wait = [&](uint32_t bb, uint32_t par) {     // (every lane for itself: a third of the time of one for all)
       if (!aborted && !__all_sync(0xffffffffu, mbar_wait(bb, par, wc))) aborted = true;
@@ -686,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float fac = fac_next;
       fac_next = factor(it + 1);
       float l_sum = 0.f, m_own = -INFINITY;          // this thread's sum, in the units of that reference
+      float over = -C::kRoom;                        // by how much its rows since then may have lost too much
       for (int j = (g0 ^ crew) & 1; j < nt; j += kCrews) {
         const uint32_t g = g0 + j;
         // Scores, from TMEM: of 2 kRows rows the thread of the hi part goes on with the first half and gives the
@@ -743,18 +766,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_old = j > 0 ? now[hl] : -INFINITY;
         float m_ref = m_old;
         uint32_t which = 0;                          // heads whose O has to follow
-        if (named_bar_or(meet, kMeet, j == 0 || mx > m_old + kLag)) {   // some head's reference moves
+        if (named_bar_or(meet, kMeet, j == 0 || mx > m_old + kLag || over > 0.f)) {   // some head's reference may move
           red[share * kHeads + hl] = mx;             // (the last maxima there have been read: all have met since)
+          owe[share * kHeads + hl] = over;
           named_bar_sync(meet, kMeet);
-          float mt = mx;
+          float mt = mx, sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < kShare; i += 2) mt = max3(mt, red[i * kHeads + hl], red[(i + 1) * kHeads + hl]);
-          if (mt > m_old + kLag) m_ref = mt;
+          for (int i = 0; i < kShare; i += 2) {
+            mt = max3(mt, red[i * kHeads + hl], red[(i + 1) * kHeads + hl]);
+            sum += owe[i * kHeads + hl] + owe[(i + 1) * kHeads + hl];
+          }
+          over = sum * (1.f / kShare);               // (the crew's threads of a head go on alike)
+          if (mt > m_old + kLag) {
+            m_ref = mt;
+          } else if (sum > 0.f && mt < m_old - 1.f) {
+            m_ref = fmaxf(mt, high[hl] - kDepth);
+            over = -C::kRoom;
+          }
           if (first) {
             const float alpha = m_ref == m_old ? 1.f : ex2_approx(m_old - m_ref);
             if (part == 0) {
               reinterpret_cast<float*>(smem + C::kOffBc)[64 * (g % C::kUnits) + hl] = alpha;
               now[hl] = m_ref;
+              if (j == 0 || m_ref > m_old) high[hl] = j == 0 ? m_ref : fmaxf(high[hl], m_ref);   // (read above only where it is not written)
             }
             which = __ballot_sync(0xffffffffu, part == 0 && alpha != 1.f && hl < Hc);
           }
@@ -767,10 +801,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (m_ref != m_own) {
           l_sum *= ex2_approx(m_own - m_ref);
           m_own = m_ref;
+          over = -C::kRoom;
         }
+        const float most = ex2_approx(mx - m_ref + C::kTop);         // this thread's largest weight
+        over += fmaf(-C::kEps, most, kRows * fminf(C::kLost, most));
         // weights and their parts
         uint32_t w0[kRows / 4], w1[kRows / 4], w2[kRows / 4], w3[kRows / 4];
-        const float2 shift = f2_pack(kTop - m_ref, kTop - m_ref);
+        const float2 shift = f2_pack(C::kTop - m_ref, C::kTop - m_ref);
         float2 l2 = f2_pack(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kRows / 4; ++k) {
@@ -783,15 +820,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             l2 = f2_fma(r, i ? f2_pack(iv.z, iv.w) : f2_pack(iv.x, iv.y), l2);
             if constexpr (kFine) {
               const float2 minus = f2_pack(-1.f, -1.f);
-              c0[i] = e4m3x2(r.x, r.y);
-              r = f2_fma(e4m3x2_value(c0[i]), minus, r);   // (exact, like the next two)
+              c0[i] = e5m2x2(r.x, r.y);
+              r = f2_fma(e5m2x2_value(c0[i]), minus, r);   // (exact, like the next two)
               c1[i] = e4m3x2(r.x, r.y);
               r = f2_fma(e4m3x2_value(c1[i]), minus, r);
               c2[i] = e5m2x2(r.x, r.y);
               r = f2_fma(e5m2x2_value(c2[i]), minus, r);
               c3[i] = e5m2x2(r.x, r.y);
             } else {
-              e4m3x2_split(r.x, r.y, c0[i], c1[i]);
+              e4m3_e5m2_split(r.x, r.y, c0[i], c1[i]);
             }
           }
           w0[k] = c0[0] | (c0[1] << 16);
