@@ -392,8 +392,8 @@ __device__ __forceinline__ float2 e5m2x2_value(uint32_t v) {
 
 // Two values as E4M3 hi + lo parts (low byte = a): hi = e4m3(x), lo =
 // e4m3(f16(x) - hi), the difference taken exactly in f16 (x rounded to f16
-// has 11 significant bits, hi 4); for 0 <= x <= 256 the pair keeps x to
-// about 8 significant bits.  Five instructions per pair.
+// has 11 significant bits, hi 4); 0 <= x <= 448 is kept to 2^-9 of itself, or
+// 2^-10.  Five instructions per pair.
 __device__ __forceinline__ void e4m3x2_split(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = e4m3x2(a, b);
   const __half2_raw hv = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
@@ -409,6 +409,23 @@ __device__ __forceinline__ void e4m3_e5m2_split(float a, float b, uint32_t& hi, 
   const __half2 r = __hsub2(__floats2half2_rn(a, b), *reinterpret_cast<const __half2*>(&hv));
   lo = static_cast<uint32_t>(
       __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&r), __NV_SATFINITE, __NV_E5M2));
+}
+
+// By how many binades the softmax reference of 8-bit weights goes down after a
+// window of tiles (0: not at all).  `sum` is that of the weights so far, `seen` what
+// it was at the window's start; where the window's is below 2^least, it would have
+// been 2^goal, which bounds its largest weight.  (A window's additions may be off by
+// 2^-19 of the sum, so that much is taken for its own.)  The reference stays within
+// kRefDepth of the highest that it was, now `depth` above it: what lies below counts
+// for nothing, and fp32 holds all sums in its units.
+constexpr float kRefDepth = 24.f;
+__device__ __forceinline__ float ref_drop(float sum, float seen, float least, float goal, float depth) {
+  const float part = fmaxf(sum - seen, 0.f) + 0x1p-18f * sum, mass = __log2f(part);
+  if (!(mass < least && part > 0.f)) return 0.f;
+  return fmaxf(floorf(fminf(goal - mass, kRefDepth - depth)), 0.f);
+}
+__device__ __forceinline__ float exp2_of(float n) {       // n whole, 0 .. 24
+  return __int_as_float((static_cast<int>(n) + 127) << 23);
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T.

@@ -27,13 +27,19 @@
 //     partials are multiplied by 2^-a (the senders' before quantising, the
 //     softmax warps' own before adding the peer's), so the two CTAs' partials
 //     are in the same units;
-//   - P' = 2^(s - m_ref + 5) likewise (a reference that lags the maximum by at
-//     most 3, so P' <= 256 and the maximum's weight is >= 32): hi = e4m3(P'), lo = e4m3(P' - hi),
+//   - P' = 2^(s - m_ref + 7) likewise (a reference that lags the maximum by at
+//     most 1.75, so P' <= 431, and its own row's is 128): hi = e4m3(P'), lo = e4m3(P' - hi),
 //     written side by side in the exchange slot's 128-byte rows (bytes 0-63
 //     hi, 64-127 lo, one byte per token): 2 MMAs per 32-token K-step (the
 //     split takes the difference in f16: five instructions per pair).
-// hi + lo holds P to about 8 significant bits (bf16 has 8), within 2^-10
-// absolute for the small weights.  The epilogue multiplies O by
+// hi + lo holds P' to 2^-9 of itself (bf16 to 2^-9), or 2^-10.  Rows far below the
+// reference would all be dropped (131072 equal ones that have half of the sum
+// beside one row: 0.43 off), so the reference goes down as well, after every 16
+// tiles whose weights sum to less than 2^7, so that they would have been 2^8.  What
+// 1024 rows lose is 1 at most, beside a sum of 2^7 or, once for each reference, its
+// own row's 2^7.  (152 requests of 8192 rows, 128 heads: 648 -> 673 us with scores
+// N(0, 0.5), 688 -> 723 with N(0, 1.7), 704 -> 773 with N(0, 4); an E5M2 lo, off by
+// 2^-14 or 2^-8 of the weight, costs the same.)  The epilogue multiplies O by
 // kv_scale / l; the score decode multiplies by sm_scale * log2(e) * kv_scale.
 //
 // TMEM (512 columns per CTA): O_c [0,256) fp32; the query's hi part [256,320)
@@ -92,8 +98,9 @@ constexpr int kOffQR = kOffRope + kRopeSlots * kRopeAtom;   // rope query hi | l
 constexpr int kOffX = kOffQR + kQRBytes;
 constexpr int kOffXLo = kOffX + kXSlots * kXSlot;       // [kXSlots] low-byte blocks from the peer
 constexpr int kOffXE = kOffXLo + kXSlots * kXLoSlot;    // [kXSlots] exponent blocks from the peer
-constexpr int kOffRed = kOffXE + kXSlots * kXeSlot;     // [2 bufs][2 halves][128] row maxima, [2][128] row sums
-constexpr int kOffBar = kOffRed + (2 * 2 * 128 + 2 * 128) * 4;
+constexpr int kOffRed = kOffXE + kXSlots * kXeSlot;     // [2 bufs][2 halves][128] row maxima, [2][128] row sums,
+                                                        // [2][2][128] sums at the last look, references' depths
+constexpr int kOffBar = kOffRed + (2 * 2 * 128 + 2 * 128 + 2 * 2 * 128) * 4;
 // barriers
 constexpr int bLatFull = 0;
 constexpr int bLatEmpty = bLatFull + kLatBlocks;
@@ -120,6 +127,9 @@ constexpr int kTmO = 0, kTmQHi = 256, kTmQLo = 320, kTmS = 384;
 constexpr uint32_t kIdescQK = idesc_e4m3(128, T, false, false);     // M=128 heads, N=64 tokens
 constexpr uint32_t kIdescQKLo = idesc_f8(kFmtE5M2, kFmtE4M3, 128, T, false, false);   // the query's E5M2 low part
 constexpr uint32_t kIdescPV = idesc_e4m3(128, 256, false, true);    // N=256 dims, B (V) MN-major
+constexpr float kTop = 7.f, kLag = 1.75f;    // P' = 2^(s - m_ref + kTop) with s <= m_ref + kLag
+constexpr int kWindow = 16;                  // tiles after which the softmax reference may go down,
+constexpr float kLeast = 7.f, kGoal = 8.f;   // where their weights sum to less than 2^kLeast, to have 2^kGoal
 static_assert(kProducers == 5, "producers 0-3 gather the latent atoms, producer 4 the rope");
 static_assert(kThreads == 736, "23 warps");
 static_assert(kLead < kLatBlocks && kRopeLead <= kRopeSlots, "a ring slot's phase must not be lapped while waited on");
@@ -447,6 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* red_max = reinterpret_cast<float*>(smem + kOffRed);            // [2][2][128]
     float* red_l = red_max + 2 * 2 * 128;                                 // [2 halves][128]
     float m_ref = 0.f, l_sum = 0.f;
+    // every softmax thread's own: its head's sum at the last look, and how far the reference is below its highest
+    float* seen = red_max + 2 * 2 * 128 + 2 * 128 + th * 128 + h;
+    float* depth = seen + 2 * 128;
     float q_fac = 1.f;                           // 2^-a of this item's head scaling (senders and softmax)
     const float sl_kv = p.scale_log2 * kv_scale; // decoded partials in log2 units of the true scores
     auto wait = [&](uint32_t bb, uint32_t par, bool cluster_scope) {
@@ -534,6 +547,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (threadIdx.x == 32 * kSendWarp0) MLA_TRACE_EVENT(8, g);
     };
 
+    // this warp's half of O (128 columns)
+    auto rescale = [&](float alpha) {
+      if (!aborted) {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[16];
+          const uint32_t ta = tmem + lane_off + kTmO + 128 * th + 16 * c;
+          tmem_ld16(ta, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st16(ta, o);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+    };
+
+    // -- after tile g, the last of a window
+    auto look = [&](uint32_t g) {
+      red_l[th * 128 + h] = l_sum;
+      named_bar_sync(1 + q, 64);
+      const float sum = red_l[h] + red_l[128 + h];
+      const float drop = ref_drop(sum, *seen, kLeast, kGoal, *depth), alpha = exp2_of(drop);
+      *seen = sum * alpha;
+      if (!__any_sync(0xffffffffu, drop > 0.f)) return;
+      *depth += drop;
+      m_ref -= drop;
+      l_sum *= alpha;
+      // (PV(g-1) first: only behind it is the barrier of tile g not a lap behind, see below)
+      wait(bar(bPvDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1, false);
+      wait(bar(bPvDone + (g & 1)), (g >> 1) & 1, false);
+      tc_fence_after();
+      rescale(alpha);
+    };
+
     // -- tile g (j-th of an item of n tokens): add the peer's rows, softmax, P
     auto softmax = [&](uint32_t g, int j, int n) {
       const uint32_t sb = g & 1, xs = g % kXSlots;
@@ -615,49 +664,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         // with a valid score when a causal query row had none before (O and
         // the row sum are still zero then)
         m_ref = mt;
+        *seen = *depth = 0.f;
         if (j == 0) l_sum = 0.f;
       } else {
-        const bool need = mt > m_ref + 3.f;   // P' <= 2^8 (see below)
+        const bool need = mt > m_ref + kLag;
         if (__any_sync(0xffffffffu, need)) {
-          // rescale this warp's half of O (128 columns) after the previous PV has
-          // landed.  PV(g-3) is complete here (the peer sent tile g only after
+          // rescale O after the previous PV has landed.  PV(g-3) is complete here (the peer sent tile g only after
           // this CTA's PV(g - kXSlots) had freed slot g mod kXSlots, and
           // kXSlots <= 3), so the barrier of tile g-1 cannot be a lap behind.
           wait(bar(bPvDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1, false);
           tc_fence_after();
           const float alpha = need ? ex2_approx(m_ref - mt) : 1.f;
           if (need) {
+            *depth = fmaxf(*depth - (mt - m_ref), 0.f);
+            *seen *= alpha;
             m_ref = mt;
             l_sum *= alpha;
           }
-          if (!aborted) {
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t o[16];
-              const uint32_t ta = tmem + lane_off + kTmO + 128 * th + 16 * c;
-              tmem_ld16(ta, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st16(ta, o);
-            }
-            tmem_wait_st();
-          }
-          tc_fence_before();
+          rescale(alpha);
         }
       }
       // P = 2^(s - m_ref) as E4M3 hi and lo, written over the peer's rows
       // (K-major, 128-byte swizzle): token t of the tile is byte t (hi) and
       // byte 64 + t (lo) of row h; this warp's 32 tokens are two 16-byte
       // chunks of each part
-      // P' = 2^(s - m_ref + 5): the reference moves once a tile's maximum is
-      // more than 3 above it, so P' <= 256 and the row maximum's weight is at
-      // least 32; lo (unscaled: it shares the accumulator with hi) is exact
-      // to E4M3's precision down to weights 2^-7 of that and within 2^-10
-      // below, which stays under 2^-9 of the output even over thousands of
-      // such tokens; lse takes the 2^5 out
+      // lo is unscaled (it shares the accumulator with hi): to E4M3's precision
+      // down to P' = 2^-1 and within 2^-10 below; lse takes the 2^kTop out
       const float m_eff = m_ref == -INFINITY ? 0.f : m_ref;   // a row with no valid score yet: P = 0
-      const float2 nm2 = f2_pack(5.f - m_eff, 5.f - m_eff);
+      const float2 nm2 = f2_pack(kTop - m_eff, kTop - m_eff);
       float2 l4[4] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {              // 16 tokens per chunk
@@ -752,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (cta == 0 && th == 0 && head_ok) {
-          const float l = lsum > 0.f ? (m_ref + __log2f(lsum) - 5.f) * 0.69314718055994531f : -INFINITY;
+          const float l = lsum > 0.f ? (m_ref + __log2f(lsum) - kTop) * 0.69314718055994531f : -INFINITY;
           if (part < 0) { if (p.lse) p.lse[static_cast<size_t>(b) * H + h] = l; }
           else p.part_lse[static_cast<size_t>(part) * H + h] = l;
         }
@@ -872,7 +906,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           n_row = max(0, min(n, (hi - lo) - p.q_len + 1 + i - (s - lo)));
         }
         q_fac = ldexpf(1.f, -head_exp(b));
-        for (int j = 0; j < nt; ++j, ++g) softmax(g, j, n_row);
+        for (int j = 0; j < nt;) {
+          const int end = min(j + kWindow, nt);
+          for (; j < end; ++j, ++g) softmax(g, j, n_row);
+          if (j < nt) look(g - 1);
+        }
         epilogue(b, part, nitem);
       }
       ++nitem;

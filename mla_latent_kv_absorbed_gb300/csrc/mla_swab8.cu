@@ -14,10 +14,18 @@
 //     power of two a that puts max |q'| in [128, 256); hi = e4m3(q'),
 //     lo = e4m3((q' - hi) * 32).  hi + lo / 32 holds q' to 8 significant bits
 //     (bf16 has 8), exactly for |q'| >= 2^-7.
-//   weights (per tile, by the softmax warps): P = 2^(s - m_ref) <= 256,
-//     hi = e4m3(P), lo = e4m3((P - hi) * 32); relative error <= 2^-8, the same
-//     bound as rounding P to bf16.  The running sums add hi + lo / 32, so the
-//     normalisation matches the weights the MMA used.
+//   weights (per tile, by the softmax warps): P = 2^(s - m_ref) <= 256, 2^3 for
+//     the row that set the reference; hi = e4m3(P), lo = e4m3((P - hi) * 32);
+//     relative error <= 2^-8, the same bound as rounding P to bf16, or 2^-15 of 1.
+//     The running sums add hi + lo / 32, so the normalisation matches the weights
+//     the MMA used.  Rows far below the reference would all be dropped (131072
+//     equal ones that have half of the sum beside one row: 0.45 off), so the
+//     reference goes down as well, after every 16 tiles whose weights sum to less
+//     than 2^3, so that they would have been 2^5 (or by 12 binades where nothing is
+//     left of them).  What 1024 rows lose is 2^-5 at most, beside a sum of 2^3 or,
+//     once for each reference, its own row's.  (152 requests of 8192 rows: 16 heads
+//     149.5 us before and after, 32 heads 196 -> 202 us with scores N(0, 0.5), 196 ->
+//     207 with N(0, 1.7), 205 -> 240 with N(0, 4).)
 // The two parts ride along N of the same MMA (hi and lo rows of B), so they
 // cost no extra instructions; the sum hi + lo / 32 is taken in fp32 when the
 // accumulators are read.
@@ -66,6 +74,8 @@ constexpr int kRopeAtom = T * 32;          // 2 KB
 constexpr int kUnit = 4 * kAtom + 2 * kRopeAtom;
 constexpr int kRopeOff = 4 * kAtom;
 constexpr float kLoWeight = 1.f / 32.f;    // value of a lo part relative to its hi part
+constexpr float kTop = 3.f;                // weights are 2^(s - m_ref), 2^kTop for the row that set the reference
+constexpr int kWindow = 16;                // tiles after which the reference may go down
 #ifndef MLA_SWAB8_LEAD
 #define MLA_SWAB8_LEAD 3
 #endif
@@ -107,7 +117,8 @@ struct Cfg {
   static constexpr int kOffBar = kOffBc + NH * 4;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffLast = kOffMisc + 32;
-  static constexpr int kSmemBytes = kOffLast + 4 * kUnits + 1024;
+  static constexpr int kOffSeen = kOffLast + 4 * kUnits;  // [2][NH] the sums at the last look, references' depths
+  static constexpr int kSmemBytes = kOffSeen + 4 * 2 * NH + 1024;
   static constexpr int kTmemCols = (NH == 16) ? 256 : 512;
   static constexpr int kTmS = 0;                        // 2 x 4NH
   static constexpr int kTmO = 8 * NH;                   // 4 blocks x 2NH (hi, lo)
@@ -480,6 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int rk = 0;
     uint32_t g = 0, nitem = 0;
     bool aborted = false;
+    float* seen = reinterpret_cast<float*>(smem + C::kOffSeen) + pair * kHalf;
+    float* depth = seen + NH;
     float m_ref[kHalf], l_part[kHalf], fac[kHalf];
     auto wait = [&](uint32_t bb, uint32_t par) {
       if (aborted) return;
@@ -487,6 +500,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) r = mbar_wait(bb, par, wc);
       r = __shfl_sync(0xffffffffu, r, 0);
       if (!r) aborted = true;
+    };
+    // O by the factors in bc, after the sums of tile g
+    auto rescale = [&](uint32_t g) {
+      float alpha_all[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) alpha_all[h] = bc[h];
+      wait(bar(C::bPDone + (g & 1)), (g >> 1) & 1);
+      tc_fence_after();
+      if (!aborted) {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {                // block c >> 1, hi (c even) or lo columns
+          uint32_t o[NH];
+          const uint32_t ta = tmem + lane_off + C::kTmO + c * NH;
+          tmem_ld_cols<NH>(ta, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < NH; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha_all[h]);
+          tmem_st_cols<NH>(ta, o);
+        }
+        tmem_wait_st();
+      }
     };
     griddep_wait();   // the per-head factors come from the prep kernel
     const float kv_scale = p8.kv_scale;
@@ -500,119 +534,156 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < kHalf; ++k)
         fac[k] = p8.fac[static_cast<size_t>(b) * NH + pair * kHalf + k] * p.scale_log2 * kv_scale;
       const int n = e - s, nt = (n + T - 1) / T;
-      for (int j = 0; j < nt; ++j, ++g) {
-        const uint32_t buf = g & 1;
-        wait(bar(C::bSFull + buf), (g >> 1) & 1);
-        tc_fence_after();
-        float ps[NH];
-        if (!aborted) {
-          uint32_t r[NH];
-          const uint32_t ts = tmem + lane_off + C::kTmS + buf * 4 * NH + pair * NH;
-          tmem_ld_cols<NH>(ts, r);
-          tmem_wait_ld();
+      for (int j = 0; j < nt;) {
+        const int end = min(j + kWindow, nt);
+        for (; j < end; ++j, ++g) {
+          const uint32_t buf = g & 1;
+          wait(bar(C::bSFull + buf), (g >> 1) & 1);
+          tc_fence_after();
+          float ps[NH];
+          if (!aborted) {
+            uint32_t r[NH];
+            const uint32_t ts = tmem + lane_off + C::kTmS + buf * 4 * NH + pair * NH;
+            tmem_ld_cols<NH>(ts, r);
+            tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < NH; ++h) ps[h] = __uint_as_float(r[h]);
-          tmem_ld_cols<NH>(ts + 2 * NH, r);
-          tmem_wait_ld();
+            for (int h = 0; h < NH; ++h) ps[h] = __uint_as_float(r[h]);
+            tmem_ld_cols<NH>(ts + 2 * NH, r);
+            tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < NH; ++h) ps[h] = fmaf(__uint_as_float(r[h]), kLoWeight, ps[h]);
-        } else {
+            for (int h = 0; h < NH; ++h) ps[h] = fmaf(__uint_as_float(r[h]), kLoWeight, ps[h]);
+          } else {
 #pragma unroll
-          for (int h = 0; h < NH; ++h) ps[h] = 0.f;
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && !aborted) mbar_arrive(bar(C::bSEmpty + buf));
-        float own[kHalf];
+            for (int h = 0; h < NH; ++h) ps[h] = 0.f;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && !aborted) mbar_arrive(bar(C::bSEmpty + buf));
+          float own[kHalf];
 #pragma unroll
-        for (int k = 0; k < kHalf; ++k) {
-          own[k] = pair ? ps[kHalf + k] : ps[k];
-          X[(pair * kHalf + k) * T + t] = pair ? ps[k] : ps[kHalf + k];
-        }
-        named_bar_sync(kBarSm, 128);
-        const bool valid = t < n - j * T;
-        float sv[kHalf];
+          for (int k = 0; k < kHalf; ++k) {
+            own[k] = pair ? ps[kHalf + k] : ps[k];
+            X[(pair * kHalf + k) * T + t] = pair ? ps[k] : ps[kHalf + k];
+          }
+          named_bar_sync(kBarSm, 128);
+          const bool valid = t < n - j * T;
+          float sv[kHalf];
 #pragma unroll
-        for (int k = 0; k < kHalf; ++k)
-          sv[k] = valid ? (own[k] + X[((1 - pair) * kHalf + k) * T + t]) * fac[k] : -INFINITY;
-        if (j == 0) {
+          for (int k = 0; k < kHalf; ++k)
+            sv[k] = valid ? (own[k] + X[((1 - pair) * kHalf + k) * T + t]) * fac[k] : -INFINITY;
+          if (j == 0) {
 #pragma unroll
-          for (int k = 0; k < kHalf; ++k) { m_ref[k] = sv[k]; l_part[k] = 0.f; }
-          pair_reduce<kHalf, false>(m_ref, red, pair, wip, lane, rk);
-          named_bar_sync(kBarVote, 128);
-        } else {
-          bool need = false;
-#pragma unroll
-          for (int k = 0; k < kHalf; ++k) need |= sv[k] > m_ref[k] + 8.f;
-          need = named_bar_or(kBarVote, 128, need);
-          if (need) {
-            float mt[kHalf], alpha[kHalf];
-#pragma unroll
-            for (int k = 0; k < kHalf; ++k) mt[k] = sv[k];
-            pair_reduce<kHalf, false>(mt, red, pair, wip, lane, rk);
+            for (int k = 0; k < kHalf; ++k) { m_ref[k] = sv[k]; l_part[k] = 0.f; }
+            pair_reduce<kHalf, false>(m_ref, red, pair, wip, lane, rk);
 #pragma unroll
             for (int k = 0; k < kHalf; ++k) {
-              const float mn = fmaxf(m_ref[k], mt[k]);
-              alpha[k] = ex2_approx(m_ref[k] - mn);
-              m_ref[k] = mn;
-              l_part[k] *= alpha[k];
-            }
-            if (wip == 0 && lane == 0) {
-#pragma unroll
-              for (int k = 0; k < kHalf; ++k) bc[pair * kHalf + k] = alpha[k];
-            }
-            named_bar_sync(kBarSm, 128);
-            float alpha_all[NH];
-#pragma unroll
-            for (int h = 0; h < NH; ++h) alpha_all[h] = bc[h];
-            wait(bar(C::bPDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
-            tc_fence_after();
-            if (!aborted) {
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {          // block c >> 1, hi (c even) or lo columns
-                uint32_t o[NH];
-                const uint32_t ta = tmem + lane_off + C::kTmO + c * NH;
-                tmem_ld_cols<NH>(ta, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int h = 0; h < NH; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha_all[h]);
-                tmem_st_cols<NH>(ta, o);
+              m_ref[k] -= kTop;
+              if (wip == 0 && lane == 0) {
+                seen[k] = depth[k] = 0.f;
               }
-              tmem_wait_st();
+            }
+            named_bar_sync(kBarVote, 128);
+          } else {
+            bool need = false;
+#pragma unroll
+            for (int k = 0; k < kHalf; ++k) need |= sv[k] > m_ref[k] + 8.f;
+            need = named_bar_or(kBarVote, 128, need);
+            if (need) {
+              float mt[kHalf], alpha[kHalf];
+#pragma unroll
+              for (int k = 0; k < kHalf; ++k) mt[k] = sv[k];
+              pair_reduce<kHalf, false>(mt, red, pair, wip, lane, rk);
+#pragma unroll
+              for (int k = 0; k < kHalf; ++k) {
+                const float mn = fmaxf(m_ref[k], mt[k] - kTop);
+                alpha[k] = ex2_approx(m_ref[k] - mn);
+                if (wip == 0 && lane == 0) depth[k] = fmaxf(depth[k] - (mn - m_ref[k]), 0.f);
+                m_ref[k] = mn;
+                l_part[k] *= alpha[k];
+              }
+              if (wip == 0 && lane == 0) {
+#pragma unroll
+                for (int k = 0; k < kHalf; ++k) {
+                  bc[pair * kHalf + k] = alpha[k];
+                  seen[k] *= alpha[k];
+                }
+              }
+              named_bar_sync(kBarSm, 128);
+              rescale(g - 1);
             }
           }
-        }
-        // weights: hi + lo / 32 in E4M3, summed as the MMA will see them
-        uint32_t phi[kHalf / 2], plo[kHalf / 2];
-#pragma unroll
-        for (int k = 0; k < kHalf; k += 2) {
-          const float p0 = ex2_approx(sv[k] - m_ref[k]), p1 = ex2_approx(sv[k + 1] - m_ref[k + 1]);
-          const uint32_t h2 = e4m3x2(p0, p1);
-          const float2 hv = e4m3x2_value(h2);
-          const uint32_t l2 = e4m3x2((p0 - hv.x) * 32.f, (p1 - hv.y) * 32.f);
-          const float2 lv = e4m3x2_value(l2);
-          l_part[k] += fmaf(lv.x, kLoWeight, hv.x);
-          l_part[k + 1] += fmaf(lv.y, kLoWeight, hv.y);
-          phi[k >> 1] = h2;
-          plo[k >> 1] = l2;
-        }
-        if (g >= 2) wait(bar(C::bPDone + buf), ((g >> 1) - 1) & 1);
-        if (!aborted) {
-          // [Phi; Plo]^T[buf]: K-major, 128-B swizzle; row = head (hi) or NH + head (lo), byte = token
-          uint8_t* pb = smem + C::kOffP + buf * C::kPBuf;
+          // weights: hi + lo / 32 in E4M3, summed as the MMA will see them
+          uint32_t phi[kHalf / 2], plo[kHalf / 2];
 #pragma unroll
           for (int k = 0; k < kHalf; k += 2) {
-            const int h = pair * kHalf + k;
-            pb[sw128_off(h, t)] = static_cast<uint8_t>(phi[k >> 1]);
-            pb[sw128_off(h + 1, t)] = static_cast<uint8_t>(phi[k >> 1] >> 8);
-            pb[sw128_off(NH + h, t)] = static_cast<uint8_t>(plo[k >> 1]);
-            pb[sw128_off(NH + h + 1, t)] = static_cast<uint8_t>(plo[k >> 1] >> 8);
+            const float p0 = ex2_approx(sv[k] - m_ref[k]), p1 = ex2_approx(sv[k + 1] - m_ref[k + 1]);
+            const uint32_t h2 = e4m3x2(p0, p1);
+            const float2 hv = e4m3x2_value(h2);
+            const uint32_t l2 = e4m3x2((p0 - hv.x) * 32.f, (p1 - hv.y) * 32.f);
+            const float2 lv = e4m3x2_value(l2);
+            l_part[k] += fmaf(lv.x, kLoWeight, hv.x);
+            l_part[k + 1] += fmaf(lv.y, kLoWeight, hv.y);
+            phi[k >> 1] = h2;
+            plo[k >> 1] = l2;
+          }
+          if (g >= 2) wait(bar(C::bPDone + buf), ((g >> 1) - 1) & 1);
+          if (!aborted) {
+            // [Phi; Plo]^T[buf]: K-major, 128-B swizzle; row = head (hi) or NH + head (lo), byte = token
+            uint8_t* pb = smem + C::kOffP + buf * C::kPBuf;
+#pragma unroll
+            for (int k = 0; k < kHalf; k += 2) {
+              const int h = pair * kHalf + k;
+              pb[sw128_off(h, t)] = static_cast<uint8_t>(phi[k >> 1]);
+              pb[sw128_off(h + 1, t)] = static_cast<uint8_t>(phi[k >> 1] >> 8);
+              pb[sw128_off(NH + h, t)] = static_cast<uint8_t>(plo[k >> 1]);
+              pb[sw128_off(NH + h + 1, t)] = static_cast<uint8_t>(plo[k >> 1] >> 8);
+            }
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && !aborted) mbar_arrive(bar(C::bPFull + buf));
+        }
+        if (j >= nt) break;
+        // The window's sums, as the warp's lanes' shares of heads: a lane gives away half of what it has at a time.
+        float v[kHalf];
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k) v[k] = l_part[k];
+#pragma unroll
+        for (int step = 0; step < 5; ++step) {
+          const int o = 16 >> step, n = kHalf >> (step + 1);
+          const bool upper = lane & o;
+          if (n == 0) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            const float give = upper ? v[i] : v[i + n];
+            v[i] = (upper ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, give, o);
           }
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && !aborted) mbar_arrive(bar(C::bPFull + buf));
+        constexpr int kLanes = 32 / kHalf;           // of a head
+        const int hk = lane / kLanes;
+        float* r = red + ((rk & 1) * 2 + pair) * 2 * kHalf;
+        ++rk;
+        if (lane % kLanes == 0) r[wip * kHalf + hk] = v[0];
+        named_bar_sync(kBarPair0 + pair, 64);
+        float drop = 0.f;
+        if (wip == 0 && lane % kLanes == 0) {
+          const float sum = r[hk] + r[kHalf + hk];
+          drop = fminf(ref_drop(sum, seen[hk], kTop, 5.f, depth[hk]), 12.f);
+          bc[pair * kHalf + hk] = exp2_of(drop);
+          seen[hk] = sum * exp2_of(drop);
+          depth[hk] += drop;
+        }
+        if (named_bar_or(kBarVote, 128, drop > 0.f)) {
+#pragma unroll
+          for (int k = 0; k < kHalf; ++k) {
+            const float alpha = bc[pair * kHalf + k];
+            m_ref[k] -= static_cast<float>((__float_as_int(alpha) >> 23) - 127);
+            l_part[k] *= alpha;
+          }
+          rescale(g - 1);
+          tc_fence_before();
+        }
       }
       // ------------------------------------------------------------ epilogue
       const bool tid0 = threadIdx.x == 0;

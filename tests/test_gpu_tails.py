@@ -127,3 +127,32 @@ def test_rows_tail_over_all_sms(H, kind):
     for half in (False, True):
         out, _ = _run(codes, scales, qn, qr, half, 0)
         assert ((out.double() - ref).norm(dim=1, keepdim=True) <= _bound(half, 200000) * size).all()
+
+
+@pytest.mark.parametrize("kind", [k for k in KINDS if k != "loud"])
+@pytest.mark.parametrize("n", [4096, 16384, 131072])
+@pytest.mark.parametrize("H", [16, 32, 48, 128])
+def test_one_scale_tail(n, H, kind):
+    torch, _ = _t()
+    codes, scales, qn, qr = _case(n, H, kind, n + H)
+    ref, size = _reference(codes, scales, qr)
+    x = codes.view(torch.float8_e4m3fn).double()[:, 512:] * SCALE
+    z = torch.logsumexp(qr[0].double() @ x.t() * SM, -1)
+    for half in (False, True):
+        out, lse = _run(codes, SCALE, qn, qr, half, 1 if H <= 32 else 2)
+        err = (out.double() - ref).norm(dim=1, keepdim=True) / size
+        # two parts of the weights whatever the output, off by 2^-8 of themselves at most, and 2^-7 of what a window of
+        # 1024 rows adds up to where all of its weights are small
+        assert err.max() <= _bound(True, n), (half, float(err.max()))
+        # (16 and 32 heads: the sum is that of the rounded weights)
+        assert ((lse.double() - z).abs() <= 2.5 * 2.0 ** -8 + _sums(n)).all()
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_one_scale_tail_over_all_sms(H):
+    for kind in ("equal", "spread", "often", "stairs"):
+        codes, _, qn, qr = _case(200000, H, kind, H)
+        torch, _ = _t()
+        ref, size = _reference(codes, torch.full((200000,), SCALE, device="cuda"), qr)
+        out, _ = _run(codes, SCALE, qn, qr, False, 0)
+        assert ((out.double() - ref).norm(dim=1, keepdim=True) <= _bound(True, 200000) * size).all(), kind
