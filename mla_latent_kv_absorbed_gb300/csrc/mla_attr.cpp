@@ -1,8 +1,8 @@
 // Per-device launch settings shared by the kernel launchers: the dynamic
-// shared-memory limit of each kernel, leave for clusters of more than eight, and
-// the SM count.  All are looked up once and reused; a process may drive several
-// devices from several host threads, so the caches are keyed on the context
-// (attributes) or the device (the SM count) and safe to use concurrently.
+// shared-memory limit of each kernel, the widest cluster that fits, and the SM
+// count.  All are looked up once and reused; a process may drive several devices
+// from several host threads, so the caches are keyed on the context (attributes,
+// clusters) or the device (the SM count) and safe to use concurrently.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -74,8 +74,44 @@ bool set_smem_limit(const void* func, int bytes) {
   return set_attribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-bool allow_wide_cluster(const void* func) {
-  return set_attribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+int widest_cluster(const void* func, int threads, int wide) {
+  struct Found {
+    const void* func;
+    CUcontext ctx;
+    int ctas;
+  };
+  static std::mutex mu;
+  static std::vector<Found> found;
+  // (sets the attribute in every context; a call without a context makes one)
+  const bool allowed = set_attribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const CUcontext ctx = current_context();
+  if (ctx) {
+    std::lock_guard<std::mutex> lock(mu);
+    for (const auto& e : found)
+      if (e.func == func && e.ctx == ctx) return e.ctas;
+  }
+  auto fits = [&](int ctas) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, func, &cfg) == cudaSuccess) return n > 0;
+    cudaGetLastError();
+    return false;
+  };
+  int ctas = allowed ? wide : 8;
+  while (ctas > 0 && !fits(ctas)) ctas /= 2;
+  if (ctx && ctas > 0) {
+    std::lock_guard<std::mutex> lock(mu);
+    found.push_back({func, ctx, ctas});
+  }
+  return ctas;
 }
 
 int device_sm_count() {

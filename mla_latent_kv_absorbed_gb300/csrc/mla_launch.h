@@ -13,8 +13,10 @@ namespace mla {
 // the CUDA call failed.
 bool set_smem_limit(const void* func, int bytes);
 
-// Likewise, that a kernel may be launched in clusters of more than eight CTAs.
-bool allow_wide_cluster(const void* func);
+// The widest cluster, `wide` (a power of two) or a half of it, of which the
+// current device holds one of CTAs of `threads` threads: more than eight need not
+// fit everywhere.  0 where none does.
+int widest_cluster(const void* func, int threads, int wide);
 
 // SM count of the current device (cached per device), or 0 on an error.
 int device_sm_count();

@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kListThreads = 256;
 // 256 requests' lists (freed slots of 2^20) with 4, 8 and 16 CTAs that scan: 25.4, 19.3 and 17.0 us; a pool of 65536
-// slots compacted: 56.8, 55.5 and 54.7.
+// slots compacted: 56.8, 55.5 and 54.7.  (Sixteen are more than fit everywhere: a cluster may be smaller.)
 constexpr int kScanThreads = 1024, kScanCtas = 16;
 constexpr long long kBulkRows = 8192;              // (row, layer) pairs from which on rows go by bulk copies
 constexpr int kMoveThreads = 288;                  // 4 rows of 72 pieces of 16 bytes, or 8 of 36
@@ -39,7 +39,6 @@ int launch_after(Kernel* kernel, dim3 grid, int threads, int cluster, int smem, 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  if (cluster > 8 && !allow_wide_cluster(reinterpret_cast<const void*>(kernel))) return MLA_ERR_CUDA;
   if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return MLA_ERR_CUDA;
   return cudaPeekAtLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(kListThreads) repack_lists_kernel(const Repack
 // the sum of all.
 __device__ __forceinline__ int cluster_scan(int x, int* warp_sums, int* cta_sums, int& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = cluster_ctarank(), ctas = cluster_size();
   int upto = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -286,7 +285,7 @@ __device__ __forceinline__ int cluster_scan(int x, int* warp_sums, int* cta_sums
     }
     warp_sums[lane] = run - mine;
     const int total = __shfl_sync(0xffffffffu, run, 31);
-    if (lane < kScanCtas)
+    if (lane < static_cast<int>(ctas))
       asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(mapa_shared(smem_u32(cta_sums + rank), lane)), "r"(total)
                    : "memory");
     __syncwarp();
@@ -296,15 +295,16 @@ __device__ __forceinline__ int cluster_scan(int x, int* warp_sums, int* cta_sums
   all = 0;
 #pragma unroll
   for (int i = 0; i < kScanCtas; ++i) {
-    if (i < static_cast<int>(rank)) before += cta_sums[i];
-    all += cta_sums[i];
+    const int sum = i < static_cast<int>(ctas) ? cta_sums[i] : 0;
+    if (i < static_cast<int>(rank)) before += sum;
+    all += sum;
   }
   return before;
 }
 
 // The words that a thread of the cluster has: its warp's equal share of all, in the lanes' order.
 __device__ __forceinline__ void my_words(long long num_slots, long long& w0, long long& w1) {
-  const long long words = (num_slots + 31) / 32, warps = kScanCtas * kScanThreads / 32;
+  const long long words = (num_slots + 31) / 32, warps = cluster_size() * (kScanThreads / 32);
   const long long share = (words + warps - 1) / warps, per = (share + 31) / 32;
   const long long first = (static_cast<long long>(cluster_ctarank()) * (kScanThreads / 32) + (threadIdx.x >> 5)) * share;
   const long long end = min(first + share, words);
@@ -577,6 +577,9 @@ int launch_rows(const MoveParams& m, const CompactParams& c, long long most, lon
 int launch_repack(const RepackParams& params, cudaStream_t stream) {
   RepackParams p = params;
   p.marked = p.freed && p.batch > 0 && p.entries > 0;
+  // (asked for before anything is launched: without the last kernel the marks would stay)
+  const int ctas = p.freed ? widest_cluster(reinterpret_cast<const void*>(freed_kernel), kScanThreads, kScanCtas) : 0;
+  if (p.freed && ctas < 1) return MLA_ERR_CUDA;
   if (p.marked) {
     const unsigned blocks = static_cast<unsigned>((p.entries + kChunk - 1) / kChunk);
     const int st = launch_after(repack_mark_kernel, dim3(blocks), kListThreads, 1, 0, stream, p);
@@ -585,7 +588,7 @@ int launch_repack(const RepackParams& params, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>(p.capacity > 0 ? (p.capacity + kChunk - 1) / kChunk : 1);
   const int st = launch_after(repack_lists_kernel, dim3(blocks), kListThreads, 1, 0, stream, p);
   if (st != MLA_OK || !p.freed) return st;
-  return launch_after(freed_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, 0, stream, p);
+  return launch_after(freed_kernel, dim3(ctas), kScanThreads, ctas, 0, stream, p);
 }
 
 int launch_move(const MoveParams& m, long long most, cudaStream_t stream) {
@@ -597,9 +600,11 @@ int launch_compact(const CompactParams& c, const MoveParams& m, cudaStream_t str
   if (sms < 1) return MLA_ERR_CUDA;
   const long long blocks = (c.entries + 4 * kListThreads - 1) / (4 * kListThreads), held = 8ll * sms;
   const unsigned grid = static_cast<unsigned>(blocks < 1 ? 1 : blocks < held ? blocks : held);
+  const int ctas = widest_cluster(reinterpret_cast<const void*>(compact_scan_kernel), kScanThreads, kScanCtas);
+  if (ctas < 1) return MLA_ERR_CUDA;
   int st = launch_after(compact_mark_kernel, dim3(grid), kListThreads, 1, 0, stream, c);
   if (st != MLA_OK) return st;
-  st = launch_after(compact_scan_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, 0, stream, c);
+  st = launch_after(compact_scan_kernel, dim3(ctas), kScanThreads, ctas, 0, stream, c);
   if (st != MLA_OK) return st;
   const long long half = c.num_slots / 2;
   return launch_rows<true>(m, c, half < c.entries ? half : c.entries, c.entries, stream);
