@@ -742,7 +742,7 @@ int mla_prefill_run(const int32_t* plan_host, const int32_t* plan_dev, const voi
  *   r_v = max(t_v - q_v, 0) after a rejected sampled draft, t_v off the rejected
  *         children's tokens for chosen ones, t_v where nothing was rejected,
  * the next token is the lowest v with sum_(w <= v) r_w > u_0 sum_w r_w, or -1
- * when nothing is left.  The comparisons are made in 64 bits and the sums are
+ * when nothing is left.  The drafts' tests are those of 64-bit arithmetic, and the sums are
  * good to about 2^-45 of the whole; entries are probabilities: values outside
  * [0, 1] count as the nearer end, NaN as 0.  With u_0 >= 1 or NaN the token is
  * the last one with r > 0; u_c is taken as 0 when it is negative or NaN.

@@ -19,8 +19,9 @@
 // the addition's exact error.  That is nine instructions an element.  64-bit
 // arithmetic, at one two-hundredth of fp32's rate, would take longer than the
 // element's eight bytes from memory; even for the few sums of sums it took a
-// quarter of the kernel's time.  The tests u a < t are exact: the product as a
-// pair by a fused multiply-add.
+// quarter of the kernel's time.  The tests u a < t are those of 64 bits (a product
+// of two fp32 numbers is exact in them): in fp32 where the two sides are further
+// apart than its roundings, and in 64 bits where they are not.
 //
 // One cluster of CTAs a request, each a stretch of the row: every CTA walks the
 // drafts itself (one warp, a few hundred bytes, the same answer), sums its
@@ -127,19 +128,30 @@ __device__ __forceinline__ Walk walk_drafts(const VerifyParams& p, int b, int la
   int node = 0, count = 1;
   unsigned long long rejected = 0;
   // a draft's test against the share `left` of its node's mass, or its own probability
-  auto holds = [&](float u, Pair against, float mass) { return above(make_float2(mass, 0.f), times(against, fmaxf(u, 0.f))); };
+  constexpr float kNear = 0x1p-20f;                // of `mass`: fp32 has the product, and a pair above 2^-20 its x, to 2^-22
+  auto close = [&](float u, float against, float mass) {
+    const float p = __fmul_rn(u, against), slack = kNear * mass;
+    return mass > 0.f && (mass < 0x1p-100f || !(p < mass - slack || p > mass + slack));
+  };
+  auto less = [&](float u, double against, float mass) { return static_cast<double>(u) * against < static_cast<double>(mass); };
+#pragma unroll
+  for (int k = 0; k < 2; ++k) u[k] = fmaxf(u[k], 0.f);     // (NaN too)
   if (!p.parents) {
     // a chain: every draft at once; those before the first that fails are accepted
-    const Pair one = make_float2(1.f, 0.f);
-    const bool a0 = holds(u[0], p.draft ? make_float2(q[0], 0.f) : one, t[0]);
-    const bool a1 = holds(u[1], p.draft ? make_float2(q[1], 0.f) : one, t[1]);
-    const unsigned long long fail = ~(both(a0, a1) | 1ull);
+    bool a[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float against = p.draft ? q[k] : 1.f;
+      a[k] = close(u[k], against, t[k]) ? less(u[k], static_cast<double>(against), t[k]) : __fmul_rn(u[k], against) < t[k];
+    }
+    const unsigned long long fail = ~(both(a[0], a[1]) | 1ull);
     count = fail ? min(__ffsll(static_cast<long long>(fail)) - 1, W) : W;
     node = count - 1;
     if (count < W) rejected = 1ull << count;
 #pragma unroll
     for (int k = 0; k < 2; ++k) path[k] = lane + 32 * k < count ? lane + 32 * k : -1;
   } else {
+    float counted[2] = {0.f, 0.f};                 // the mass that a rejected draft took (a repeated token's: none)
     for (bool moved = true; moved;) {              // at most W - 1 children are tried in all
       unsigned long long kids = both(par[0] == node, par[1] == node);
       rejected = 0;
@@ -150,8 +162,15 @@ __device__ __forceinline__ Walk walk_drafts(const VerifyParams& p, int b, int la
         kids &= kids - 1;
         const int x = of(tok, c);
         const bool again = both((rejected >> lane & 1) && tok[0] == x, (rejected >> (32 + lane) & 1) && tok[1] == x) != 0;
-        const float mass = again ? 0.f : of(t, c);
-        if (holds(of(u, c), left, mass)) {
+        const float mass = again ? 0.f : of(t, c), uc = of(u, c);
+        bool taken = __fmul_rn(uc, left.x) < mass;
+        if (close(uc, left.x, mass) || left.x < 0x1p-20f) {   // (seldom) what the rejected siblings left, in 64 bits
+          double share = 1.0;
+          for (unsigned long long r = rejected; r; r &= r - 1)
+            share = fmax(share - static_cast<double>(of(counted, __ffsll(static_cast<long long>(r)) - 1)), 0.0);
+          taken = less(uc, share, mass);
+        }
+        if (taken) {
           node = c;
           path[0] = lane == count ? c : path[0];
           path[1] = lane + 32 == count ? c : path[1];
@@ -160,6 +179,8 @@ __device__ __forceinline__ Walk walk_drafts(const VerifyParams& p, int b, int la
           break;
         }
         rejected |= 1ull << c;
+        counted[0] = lane == c ? mass : counted[0];
+        counted[1] = lane + 32 == c ? mass : counted[1];
         left = add(left, make_float2(-mass, 0.f));
         if (!(left.x > 0.f)) left = make_float2(0.f, 0.f);
       }
