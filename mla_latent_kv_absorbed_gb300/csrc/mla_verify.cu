@@ -357,7 +357,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     if (rank == 0 && tid == 0) p.next[b] = -1;
     return;
   }
-  Pair thr = times(total, __ldg(p.uniforms + static_cast<long long>(b) * p.width));
+  const float u0 = __ldg(p.uniforms + static_cast<long long>(b) * p.width);
+  Pair thr = times(total, u0);
+  if (!(u0 < 1.f)) thr.x = __int_as_float(0x7FFFFFFF);   // (NaN: nothing is past it, whatever the parts' roundings)
   Pair before;
   if (pick(ctas, thr, before) != rank) return;
   thr = add(thr, minus(before));

@@ -70,3 +70,21 @@ def test_what_siblings_left_where_it_is_nearly_nothing():
     u[:, 0] = rng.random(B)
     u[:, 8] = rng.random(B)
     _same(_verify(_dev(target, np.float32), tokens, u, parents=parents), S.verify(target, tokens, u, parents=parents))
+
+
+@pytest.mark.parametrize("V", [37, 4099, 32001, 129280])
+@pytest.mark.parametrize("u0", [1.0, 1.5, float("inf"), float("nan")])
+def test_a_number_of_one_draws_the_last_token(V, u0):
+    # however little mass the last tokens have beside the sums' last bits
+    rng = np.random.default_rng(V)
+    B = 48
+    target = rng.random((B, 1, V)).astype(np.float32)
+    target /= target.sum(-1, keepdims=True)
+    last = V - 1 - rng.integers(0, 30, B)
+    for b in range(B):
+        target[b, 0, last[b] - 5:] = 0
+        target[b, 0, last[b]] = np.float32(2.0 ** -rng.integers(30, 120))
+    u = np.full((B, 1), u0, dtype=np.float32)
+    got = _verify(_dev(target, np.float32), np.zeros((B, 1), int), u)
+    assert got[2].tolist() == last.tolist()
+    _same(got, S.verify(target, np.zeros((B, 1), int), u))
