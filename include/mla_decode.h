@@ -767,7 +767,8 @@ int mla_prefill_run(const int32_t* plan_host, const int32_t* plan_dev, const voi
  *   workspace      NULL, or a workspace (its status word).
  * Pointers are 4-byte aligned (workspace 16); outputs apart from the inputs.
  * Errors: MLA_ERR_INVALID_ARG for bad pointers, sizes or strides;
- * MLA_ERR_UNSUPPORTED for q_len > 64 and for draft_probs with tree_parents.
+ * MLA_ERR_UNSUPPORTED for q_len > 64, a vocab past 2^30, and draft_probs with
+ * tree_parents.
  * Nothing is launched then, nor for batch == 0. */
 int mla_verify_drafts(const float* target_probs, int64_t target_batch_stride, int64_t target_row_stride,
                       const float* draft_probs, int64_t draft_batch_stride, int64_t draft_row_stride,
@@ -810,8 +811,8 @@ size_t mla_slots_workspace_bytes(int64_t num_slots);
  * passes capacity, or the freed slots freed_capacity (the rest is not written).
  * Pointers are 4-byte aligned (workspace 16); outputs apart from the inputs.
  * Errors: MLA_ERR_INVALID_ARG for bad pointers or sizes, one of a pair without
- * the other; MLA_ERR_UNSUPPORTED for q_len > 64 (with path), or more than 65536
- * requests with freed;
+ * the other, a capacity past 2^31 - 2; MLA_ERR_UNSUPPORTED for q_len > 64 (with
+ * path), more than 65536 requests with freed, or more than 2^20 new ones;
  * MLA_ERR_WORKSPACE for too small a workspace.  Nothing is launched then. */
 int mla_repack_requests(const int32_t* kv_indptr, const int32_t* kv_indices, int64_t entries, int32_t batch,
                         const int32_t* sources, int32_t new_batch, const int32_t* path, const int32_t* accepted,

@@ -12,7 +12,10 @@
 namespace mla {
 
 constexpr int kMaxDrafts = 64;        // drafts of a request (a 64-bit set of them)
+constexpr int kMaxVocab = 1 << 30;    // (four elements to a block, and those of the last one are counted in 32 bits)
 constexpr int kMaxRequests = 65536;   // requests of a batch whose lists are rewritten with their freed slots
+constexpr int kMaxNew = 1 << 20;      // new requests: every block adds up the lengths of all before its own
+constexpr long long kMaxCapacity = 0x7FFFFFFEll;   // entries of the new lists: a sum of lengths ends at 2^31 - 1, and is past it
 
 struct VerifyParams {
   const float* target;        // row n of request b at target + b*t_bs + n*t_rs

@@ -35,7 +35,7 @@ int mla_verify_drafts(const float* target_probs, int64_t target_batch_stride, in
                       int32_t q_len, int32_t vocab, int32_t* path, int32_t* accepted, int32_t* next_token,
                       void* workspace, void* stream) {
   if (batch < 0 || q_len < 1 || vocab < 1) return MLA_ERR_INVALID_ARG;
-  if (q_len > kMaxDrafts || (draft_probs && tree_parents)) return MLA_ERR_UNSUPPORTED;
+  if (q_len > kMaxDrafts || vocab > kMaxVocab || (draft_probs && tree_parents)) return MLA_ERR_UNSUPPORTED;
   if (!stride_ok(target_batch_stride) || !stride_ok(target_row_stride)) return MLA_ERR_INVALID_ARG;
   if (draft_probs && (!stride_ok(draft_batch_stride) || !stride_ok(draft_row_stride))) return MLA_ERR_INVALID_ARG;
   if (batch == 0) return MLA_OK;
@@ -69,13 +69,13 @@ int mla_repack_requests(const int32_t* kv_indptr, const int32_t* kv_indices, int
                         int32_t q_len, int32_t* new_indptr, int32_t* new_indices, int64_t capacity, int64_t num_slots,
                         int32_t* freed, int64_t freed_capacity, int32_t* freed_count, void* workspace,
                         size_t workspace_bytes, void* stream) {
-  if (batch < 0 || new_batch < 0 || entries < 0 || entries > 0x7FFFFFFFll || capacity < 0 || capacity > 0x7FFFFFFFll ||
+  if (batch < 0 || new_batch < 0 || entries < 0 || entries > 0x7FFFFFFFll || capacity < 0 || capacity > kMaxCapacity ||
       freed_capacity < 0 || !slots_ok(num_slots))
     return MLA_ERR_INVALID_ARG;
   if ((path == nullptr) != (accepted == nullptr) || (freed == nullptr) != (freed_count == nullptr))
     return MLA_ERR_INVALID_ARG;
   if (path && q_len < 1) return MLA_ERR_INVALID_ARG;
-  if ((path && q_len > kMaxDrafts) || (freed && batch > kMaxRequests)) return MLA_ERR_UNSUPPORTED;
+  if ((path && q_len > kMaxDrafts) || (freed && batch > kMaxRequests) || new_batch > kMaxNew) return MLA_ERR_UNSUPPORTED;
   if (!ready(workspace)) return MLA_ERR_INVALID_ARG;
   if (workspace_bytes < slots_ws(num_slots).total) return MLA_ERR_WORKSPACE;
   if (!ready(kv_indptr, 4) || !ready(new_indptr, 4) || (new_batch > 0 && !ready(sources, 4)) ||

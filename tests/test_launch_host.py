@@ -112,6 +112,34 @@ def test_nothing_is_marked_where_no_cluster_fits(stand_in):
     assert _calls(stand_in, 0)[1:] == [[4, []], [4, []]]
 
 
+LIMITS = r"""
+import ctypes, json, sys
+lib, shim = ctypes.CDLL(sys.argv[1]), ctypes.CDLL(sys.argv[2])
+p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+at, big = p(1 << 20), sz(1 << 28)
+def verify(vocab):
+    return lib.mla_verify_drafts(at, i64(0), i64(0), None, i64(0), i64(0), at, None, at, i32(1), i32(1), i32(vocab), at, at, at,
+                                 None, None)
+def repack(new, room):
+    return lib.mla_repack_requests(at, at, i64(500), i32(3), at, i32(new), None, None, i32(0), at, at, i64(room), i64(1000),
+                                   None, i64(0), None, at, big, None)
+top = 2**31 - 1
+st = [verify(2**30), verify(2**30 + 1), verify(top), repack(2**20, 500), repack(2**20 + 1, 500), repack(top, 500),
+      repack(2, top - 1), repack(2, top)]
+print(json.dumps([st, shim.launches((ctypes.c_int * 64)())]))
+"""
+
+
+def test_sizes_that_32_bits_do_not_count_are_refused(stand_in):
+    # the last block of a row, the windows of new requests and the sum of their lengths: one more would wrap around
+    from mla_latent_kv_absorbed_gb300 import build
+    r = subprocess.run([sys.executable, "-c", LIMITS, build.LIB, stand_in], capture_output=True, text=True,
+                       env=dict(os.environ, LD_PRELOAD=stand_in, MOST="16", CUDA_VISIBLE_DEVICES=""))
+    assert r.returncode == 0, r.stderr
+    st, launched = json.loads(r.stdout)
+    assert st == [0, 2, 2, 0, 2, 2, 0, 1] and launched == 3
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("most", [8, 1])
 def test_scans_of_smaller_clusters_give_the_same(tmp_path, most):
