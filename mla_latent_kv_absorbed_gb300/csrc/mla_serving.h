@@ -41,7 +41,8 @@ struct SlotsWs {
   size_t bits;                // uint32 [words]
   size_t live;                // uint2 [words]: a word of the live slots, and how many live ones are in the words before
   size_t holes;               // int32 [slots / 2]: free slots among the lowest n, ascending
-  size_t away;                // int32 [slots / 2]: live slots past them, ascending
+  size_t away;                // int32 [slots / 2]: live slots past them, descending (the k-th of them in ascending
+                              // order, which goes to holes[k], is entry count - 1 - k)
   size_t counts;              // int32 [2]: live slots, and those of them past the lowest n
   size_t total;
 };
@@ -100,7 +101,7 @@ struct CompactParams {
   int32_t* live_count;        // [1]
   uint32_t* bits;             // [words], zero
   uint2* live;                // [words]
-  int32_t *holes, *away;      // [num_slots / 2]
+  int32_t *holes, *away;      // [num_slots / 2], as in SlotsWs
   int32_t* counts;            // [2]
   int* status;
   long long entries, num_slots;
