@@ -16,8 +16,10 @@
 // A pick near a border of the running sum is decided by the sum's last bits,
 // so sums are held to about 47 bits, as pairs of fp32 numbers: t - q with its
 // exact error (t > q >= 0: t - d and the rest are exact), added to a pair with
-// the addition's exact error.  That is nine instructions an element.  64-bit
-// arithmetic, at one two-hundredth of fp32's rate, would take longer than the
+// the addition's exact error (the published error-free transformations: Knuth's
+// sum of two numbers, Dekker's of a larger and a smaller one, a product's error by
+// a fused multiply-add).  Two elements go through eleven packed instructions, beside
+// the clamping and the minimum.  64-bit arithmetic, at one two-hundredth of fp32's rate, would take longer than the
 // element's eight bytes from memory; even for the few sums of sums it took a
 // quarter of the kernel's time.  The tests u a < t are those of 64 bits (a product
 // of two fp32 numbers is exact in them): in fp32 where the two sides are further
@@ -241,7 +243,7 @@ __device__ __forceinline__ int pick(const Parts& p, Pair thr, Pair& before) {
 }
 
 // (Four blocks an SM: 64 requests of eight CTAs are resident at once.  With 77 registers they are not, and the batch
-// of 64 x 8 x 129280 takes 19.4 us instead of 15.0.)
+// of 64 x 8 x 129280 takes 4 us more.)
 __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams p) {
   __shared__ Pair cta_sum[kMaxCluster], warp_sum[kWarps], part_sum[kWarps];
   __shared__ int32_t gone[kMaxDrafts];
@@ -304,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
   };
   // Sum of max(t - q, 0) over blocks [k0, k1), by a warp; in every lane.  The even and the odd elements have a running
   // sum each, and go through packed instructions together.  (Four blocks a lane on their way: 15.8 us of the batch
-  // of 64 x 8 x 129280; two 17.9, three 16.4, six 21.8, and two while two are added up 15.9.)
+  // of 64 x 8 x 129280; two 17.9, three 16.4, six 21.8, and two while two are added up 15.9, all before the parts'
+  // sums were scanned by lanes; with that, and the drafts' tests as in 64 bits, 15.2.)
   auto sum_of = [&](int k0, int k1) -> Pair {
     constexpr int kDeep = 4;
     const float2 minus1 = make_float2(-1.f, -1.f);
