@@ -455,9 +455,10 @@ int mla_decode_fp8_workspace_bytes(const int32_t* plan_host, size_t* workspace_b
  *              calls sharing a workspace must not overlap on the GPU).
  *   all other arguments as for mla_decode_run.
  * Accuracy: a weight is held to 2^-8 of itself (H >= 48: 2^-9), and what the
- * smallest lose beyond that is at most 2^-7 of all weights together, however many
- * rows there are and by whatever factor one of them outweighs the others; the
- * tensor core's sums as for mla_decode_run_fp8_rows with a bf16 out.
+ * smallest lose beyond that is at most 2^-5 of all weights together in the worst
+ * order of them (measured: below 2^-7), however many rows there are and by
+ * whatever factor one of them outweighs the others; the tensor core's sums as for
+ * mla_decode_run_fp8_rows with a bf16 out.
  * Launches (H 16 / 32) a query-prep kernel (each request's query split into
  * two E4M3 parts after a per-head power-of-two scaling) and the decode kernel
  * as its programmatic dependent, or (H 48..128) the two-CTA kernel, which

@@ -36,8 +36,10 @@
 // as they follow one downwards.)  What is lost is then at most 2 kEps of all
 // weights, at any number of rows.  (With E4M3 + E4M3 at 2^5 and a reference that
 // only went up, 16384 rows of scores N(0, 1) beside one that has 0.8 of the sum
-// were 0.07 off, and 131072 of equal ones 0.5; now 3e-5, and 1e-6 with fp32.
-// Moves are few: 2 to 5 an item of 16384 rows with scores N(0, 1.7) to N(0, 5).)
+// gave 0.07 off, and 65536 equal ones 0.4, by an emulation; what is measured now is
+// a bf16 out's rounding, and 4e-5 for an fp32 out, which is the tensor core's cut
+// of its sums.  Moves are few: 2 to 5 an item of 16384 rows with scores N(0, 1.7) to
+// N(0, 5).)
 //
 // A worker of 48 or more heads is two CTAs, and each takes half of the HEADS:
 // all of the scores, the softmax and the output of a head are one CTA's, and
