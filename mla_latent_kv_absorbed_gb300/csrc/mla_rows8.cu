@@ -39,7 +39,9 @@
 // gave 0.07 off, and 65536 equal ones 0.4, by an emulation; what is measured now is
 // a bf16 out's rounding, and 4e-5 for an fp32 out, which is the tensor core's cut
 // of its sums.  Moves are few: 2 to 5 an item of 16384 rows with scores N(0, 1.7) to
-// N(0, 5).)
+// N(0, 5), and fewer since an item's first reference stands 3 above its first tile's
+// maximum: 152 requests of 8192 rows, 128 heads, fp32 out, scores N(0, 1.7): 398 ->
+// 384 us, and 390 with a reference that only went up.)
 //
 // A worker of 48 or more heads is two CTAs, and each takes half of the HEADS:
 // all of the scores, the softmax and the output of a head are one CTA's, and
@@ -110,6 +112,7 @@ constexpr int kScSlot = 3 * T * 4;                   // factors, log2 of the sca
 constexpr int kItemCache = 16;                       // this worker's first items, copied to shared memory
 constexpr float kLoWeight = 1.f / 32.f;              // value of a query's lo part
 constexpr float kLag = 1.75f;                        // weights are 2^(e - m + kTop) with e <= m + kLag
+constexpr float kHead = 3.f, kHeadRoom = 0.125f;     // an item's first reference is that far above its first tile's maximum
 constexpr float kDepth = 24.f;                       // the reference's deepest under its highest: less is nothing beside that
 constexpr int kBarCrew0 = 1, kBarGather = 9;   // named barriers
 constexpr int kTmO = 0, kTmQ = 256, kTmS = 384;
@@ -710,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float fac = fac_next;
       fac_next = factor(it + 1);
       float l_sum = 0.f, m_own = -INFINITY;          // this thread's sum, in the units of that reference
-      float over = -C::kRoom;                        // by how much its rows since then may have lost too much
+      float over = 0.f;                              // by how much its rows since then may have lost too much
       for (int j = (g0 ^ crew) & 1; j < nt; j += kCrews) {
         const uint32_t g = g0 + j;
         // Scores, from TMEM: of 2 kRows rows the thread of the hi part goes on with the first half and gives the
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           over = sum * (1.f / kShare);               // (the crew's threads of a head go on alike)
           if (mt > m_old + kLag) {
-            m_ref = mt;
+            m_ref = j == 0 ? mt + kHead : mt;
           } else if (sum > 0.f && mt < m_old - 1.f) {
             m_ref = fmaxf(mt, high[hl] - kDepth);
             over = -C::kRoom;
@@ -803,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (m_ref != m_own) {
           l_sum *= ex2_approx(m_own - m_ref);
           m_own = m_ref;
-          over = -C::kRoom;
+          over = j < kCrews ? -C::kRoom * kHeadRoom : -C::kRoom;
         }
         const float most = ex2_approx(mx - m_ref + C::kTop);         // this thread's largest weight
         over += fmaf(-C::kEps, most, kRows * fminf(C::kLost, most));
